@@ -267,6 +267,100 @@ int sfa_backward_int(const sfa_desc* d, const void* q, const void* k, const void
 int sfa_decode_int(const sfa_desc* d, const void* q, const void* k_cache, const void* v_cache,
                    const int32_t* pos, void* o, float* lse, void* stream);
 
+/* ---- serving: a paged key/value cache held in 4 bits ------------------
+ *
+ * A cache is [n_pages][Hkv] blocks of 72 * page bytes (sfa_kv4_cache_bytes),
+ * each block, in this order:
+ *   key codes    [page][32]  e2m1, dim 2i in the low, 2i + 1 in the high half of byte i
+ *   value codes  [page][32]
+ *   scales       [page][8]   e4m3: keys' dims 0-15, 16-31, 32-47, 48-63, then the values'
+ * A stored number is code * scale * (kscale for keys, vscale for values).
+ * Keys are stored rotated at their own position.  Row p of request r lies in
+ * page block_table[r][p / page], at row p mod page of it; its slot is
+ * page id * page + p mod page.
+ *
+ * Numbers kept by the caller for a step: n_new and seq_lens [R], block_table
+ * [R][max_pages], free_pages [n_pages] of which the first n_free[0] are a
+ * stack of unused page ids (its top last).  Index errors found on the device
+ * (a page id outside the pool, a length outside the block table, a position
+ * outside the RoPE table) are recorded as SFA_ERR_DEVICE_BOUNDS; the row in
+ * question is then skipped, or the key in question left out, never read or
+ * written out of range.  All entry points only enqueue work, keep no state
+ * between calls, and may be captured into a graph. */
+typedef struct {
+  int32_t n_pages, page, Hkv, D; /* the pool; page: 16, 32, 64 or 128 rows; D = 64; n_pages * page < 2^31 */
+  int32_t R, max_pages;          /* requests (1..8192 for sfa_kv4_plan); width of the block table,
+                                  * max_pages * page <= 2^24 */
+  int32_t N;                     /* rows: N >= 0 (0: nothing to do); N * Hkv <= 2^27 */
+  int32_t Hq, dtype;             /* attend: query heads (G = Hq / Hkv a power of two <= 32); sfa_dtype
+                                  * of q and o, of k and v */
+  int64_t q_stride, k_stride, v_stride; /* elements between rows of q (>= Hq * 64), of append's k and v
+                                  * (>= Hkv * 64); multiples of 16 bytes */
+  float kscale, vscale;          /* positive and finite */
+  const float* rope;             /* sfa_rope_table for rope_T positions, or NULL for no rotation */
+  int32_t rope_T;
+  const int32_t* dist;           /* attend: host key distances as for sfa_decode_int; NULL: every key
+                                  * up to the query's own position */
+  int32_t n_dist;
+} sfa_kv4_desc;
+
+int sfa_kv4_cache_bytes(int32_t n_pages, int32_t page, int32_t Hkv, size_t* bytes);
+
+/* Block tables and slot maps of one step, from request lengths (d: n_pages,
+ * page, R, max_pages, N).  seq_lens[r] rows of request r are stored; n_new[r]
+ * >= 0 more come, -1 ends the request and gives its pages back.  First the
+ * pages of ended requests are pushed on the stack, in (request, page) order,
+ * then the pages that the new rows need are popped, in (request, page) order,
+ * and entered in block_table (other entries are left as they are, those of
+ * ended requests too; free_pages is written only at places
+ * n_free .. n_free_out - 1).
+ *   cu_q       [R + 1]  prefix sums of the new rows: request r's are rows cu_q[r] .. cu_q[r + 1] - 1
+ *   slots, pos [N]      slot and position of every new row; -1 behind the last one
+ *   lens_out   [R]      stored rows after the step, 0 for ended requests (may be seq_lens itself)
+ *   n_free_out [1]      (may be n_free itself)
+ * A step that does not fit changes nothing: lens_out = seq_lens, n_free_out =
+ * n_free, cu_q 0, slots and pos -1, and the device status SFA_ERR_CAPACITY
+ * (too few free pages, more than N new rows) or SFA_ERR_DEVICE_BOUNDS (n_new
+ * below -1, a length below 0 or above max_pages * page, a stack outside
+ * free_pages). */
+int sfa_kv4_plan(const sfa_kv4_desc* d, const int32_t* n_new, const int32_t* seq_lens,
+                 int32_t* block_table, int32_t* free_pages, const int32_t* n_free, int32_t* cu_q,
+                 int32_t* slots, int32_t* pos, int32_t* lens_out, int32_t* n_free_out, void* stream);
+
+/* Write rows into the cache (d: n_pages, page, Hkv, D, N, dtype, k_stride,
+ * v_stride, kscale, vscale, rope).  k, v: N rows of [Hkv, 64].  Row n goes to
+ * slots[n] (all distinct; a negative slot is skipped), its key rotated at
+ * pos[n] in fp32 (each product and sum rounded once).  Per 16 dims: x divided by
+ * kscale or vscale, scale = e4m3(max |x| / 6), 448 at most, code =
+ * e2m1(x / scale), 6 at most; all to nearest, ties to even, quotients in fp32.
+ * A zero scale has zero codes; a block with a NaN is stored as NaN. */
+int sfa_kv4_append(const sfa_kv4_desc* d, const void* k, const void* v, void* cache,
+                   const int32_t* slots, const int32_t* pos, void* stream);
+
+/* Rows of the cache as numbers (d: n_pages, page, Hkv, D, N, dtype, kscale,
+ * vscale): k, v [N, Hkv, 64], the (rotated) keys and the values at slots[n];
+ * zeros for a negative slot. */
+int sfa_kv4_read(const sfa_kv4_desc* d, const void* cache, const int32_t* slots, void* k, void* v,
+                 void* stream);
+
+/* Attention of N query rows over their requests' cached rows.
+ *   q        N rows of [Hq, 64], unrotated
+ *   seq_lens [R]      stored rows of each request, the queries' own included
+ *   cu_q     [R + 1]  request r's queries are rows cu_q[r] .. cu_q[r + 1] - 1 and stand at its
+ *                     last positions, in order; rows from cu_q[R] on are left untouched.  NULL
+ *                     (N = R): row r is request r's last position; a request of length 0 gives
+ *                     a zero row and lse = -inf
+ *   o        [N, Hq, 64]  d->dtype
+ *   lse      fp32 [N, Hq], natural log of the softmax denominator, or NULL
+ * A query at position p attends the rows j <= p (d->dist NULL), or p - s for
+ * every s <= p of d->dist (which holds 0 and nothing negative); logits are
+ * q . k / 8 after the rotation of q at p by d->rope.  ws: sfa_kv4_workspace_size
+ * bytes (NULL when that is 0), scratch of this call alone. */
+int sfa_kv4_workspace_size(const sfa_kv4_desc* d, size_t* bytes);
+int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
+                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* o,
+                   float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Allocation-free variant of sfa_forward (no counterpart on the pages; it
  * exists for callers that cannot allocate device memory: programs whose
  * allocator owns all device memory and bars raw cudaMalloc from libraries,
@@ -302,7 +396,11 @@ typedef enum {
   SFA_KERNEL_ROPE = 4,
   SFA_KERNEL_PREP = 5, /* RoPE-rotated bf16 copy of K for the tensor-core kernels */
   SFA_KERNEL_DECODE = 6,
-  SFA_KERNEL_KINDS = 7
+  SFA_KERNEL_KV4_PLAN = 7,
+  SFA_KERNEL_KV4_APPEND = 8,
+  SFA_KERNEL_KV4_READ = 9,
+  SFA_KERNEL_KV4_ATTEND = 10,
+  SFA_KERNEL_KINDS = 11
 } sfa_kernel_kind;
 int sfa_timing_enable(int on);
 int sfa_timing_read(double* ms, int64_t* launches, int n);

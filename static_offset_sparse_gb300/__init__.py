@@ -10,10 +10,12 @@ from .api import (alpha_schedule, backward, backward_int, band_plan, decode_int,
                   offsets_christoffel, offsets_fib, offsets_pow2, offsets_powerlaw, reach,
                   residue_classes, rope_keys, rope_table, rung_table, status_string, timing_enable,
                   timing_read, workspace_size)
+from .kv4 import kv4_append, kv4_attend, kv4_cache, kv4_plan, kv4_read, kv4_workspace_size
 
 __all__ = [
     "LIB_PATH", "MAX_RUNGS", "SCHED_COPRIME", "SCHED_FIXED", "SCHED_LINEAR", "SFA_BF16",
     "SFA_F32", "SfaError", "alpha_schedule", "backward", "backward_int", "band_plan",
+    "kv4_append", "kv4_attend", "kv4_cache", "kv4_plan", "kv4_read", "kv4_workspace_size",
     "decode_int", "forward", "forward_int", "get_device_status", "int_distances", "make_desc", "offsets_christoffel",
     "offset_histogram", "offsets_fib", "offsets_pow2", "offsets_powerlaw", "reach",
     "residue_classes", "rope_keys", "rope_table", "rung_table", "status_string",

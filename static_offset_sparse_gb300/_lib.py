@@ -37,6 +37,18 @@ class Desc(C.Structure):
     ]
 
 
+class Kv4Desc(C.Structure):
+    _fields_ = [
+        ("n_pages", C.c_int32), ("page", C.c_int32), ("Hkv", C.c_int32), ("D", C.c_int32),
+        ("R", C.c_int32), ("max_pages", C.c_int32), ("N", C.c_int32),
+        ("Hq", C.c_int32), ("dtype", C.c_int32),
+        ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+        ("kscale", C.c_float), ("vscale", C.c_float),
+        ("rope", C.c_void_p), ("rope_T", C.c_int32),
+        ("dist", C.c_void_p), ("n_dist", C.c_int32),
+    ]
+
+
 _LIB = None
 _LOCK = threading.Lock()
 _P = C.c_void_p
@@ -65,6 +77,12 @@ SIGNATURES = {
     "sfa_get_device_status": [_P, _I32P],
     "sfa_forward_noalloc": [C.POINTER(Desc), _P, _P, _P, _P, _P, _P],
     "sfa_decode_int": [C.POINTER(Desc), _P, _P, _P, _P, _P, _P, _P],
+    "sfa_kv4_cache_bytes": [C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)],
+    "sfa_kv4_plan": [C.POINTER(Kv4Desc)] + [_P] * 11,
+    "sfa_kv4_append": [C.POINTER(Kv4Desc)] + [_P] * 6,
+    "sfa_kv4_read": [C.POINTER(Kv4Desc)] + [_P] * 5,
+    "sfa_kv4_workspace_size": [C.POINTER(Kv4Desc), C.POINTER(C.c_size_t)],
+    "sfa_kv4_attend": [C.POINTER(Kv4Desc)] + [_P] * 8 + [C.c_size_t, _P],
     "sfa_rope_keys": [C.POINTER(Desc), _P, _P, _P],
     "sfa_reach": [_I32P, _I32P, C.c_int32, C.c_int32, _I32P, C.POINTER(C.c_int64)],
     "sfa_residue_classes": [_I32P, C.c_int32, C.c_int32, C.POINTER(C.c_int64)],

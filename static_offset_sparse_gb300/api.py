@@ -312,7 +312,8 @@ def get_device_status() -> int:
     return out.value
 
 
-KERNEL_KINDS = ("fwd", "bwd_q", "bwd_kv", "dalpha_reduce", "rope_table", "prep", "decode")
+KERNEL_KINDS = ("fwd", "bwd_q", "bwd_kv", "dalpha_reduce", "rope_table", "prep", "decode",
+                "kv4_plan", "kv4_append", "kv4_read", "kv4_attend")
 
 
 def timing_enable(on: bool = True) -> None:

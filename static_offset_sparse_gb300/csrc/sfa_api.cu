@@ -118,6 +118,8 @@ static int status_ptr(int** out) {
   return SFA_OK;
 }
 
+int device_status(int** out) { return status_ptr(out); }
+
 // ---- launch timing --------------------------------------------------------
 struct TimingRec {
   int kind;

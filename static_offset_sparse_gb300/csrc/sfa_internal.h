@@ -108,6 +108,8 @@ int launch_band_backward(const AttnArgs& a, const BandPlan& p, const void* kr, v
 // Optional launch timing (sfa_api.cu): returns a record id or -1 when off.
 // The CUDA context current on the calling thread, nullptr if none (sfa_api.cu).
 ::CUctx_st* current_context();
+// Device address of the status word of the current device (sfa_api.cu).
+int device_status(int** out);
 int timing_start(int kind, void* stream);
 void timing_stop(int id, void* stream);
 
