@@ -429,7 +429,9 @@ int sfa_set_option(int32_t option, int32_t value);
  * loads in flight and leaves.  skip_group >= 0 makes CTA (0, 0) of the rung
  * tensor-core forward and query-side backward issue neither the expect_tx
  * nor the loads of that staged group (window chunks first, then rung pairs),
- * so its consumers' wait runs out with nothing in flight; -1 turns this off.
+ * so its consumers' wait runs out with nothing in flight, and the first warp
+ * that streams sfa_kv4_attend's first keys start no copies for that tile of its
+ * ring; -1 turns this off.
  * The setting is process-wide and read by every later call until changed;
  * the outputs of a call that timed out are undefined.  Returns
  * SFA_ERR_INVALID_ARG for wait_cycles < 0 or skip_group < -1. */

@@ -155,6 +155,12 @@ static int g_dbg_skip = -1;
 // sfa_set_option values
 static int g_opt_band_tc05 = 0;
 
+void wait_injection(long long* cycles, int32_t* skip) {
+  std::lock_guard<std::mutex> lock(g_dbg_mu);
+  *cycles = g_dbg_wait > 0 ? g_dbg_wait : kDefaultWaitCycles;
+  *skip = g_dbg_skip;
+}
+
 static int fill_args(const sfa_desc* d, AttnArgs* a) {
   *a = AttnArgs{};
   a->B = d->B;

@@ -110,6 +110,9 @@ int launch_band_backward(const AttnArgs& a, const BandPlan& p, const void* kr, v
 ::CUctx_st* current_context();
 // Device address of the status word of the current device (sfa_api.cu).
 int device_status(int** out);
+// Limit of a bounded wait in SM clock cycles, and the staged group whose loads
+// are left out or -1 (sfa_debug_inject).
+void wait_injection(long long* cycles, int32_t* skip);
 int timing_start(int kind, void* stream);
 void timing_stop(int id, void* stream);
 

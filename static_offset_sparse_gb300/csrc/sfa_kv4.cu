@@ -327,9 +327,12 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const ReadArgs a) {
     const uint2 c = *reinterpret_cast<const uint2*>(block + (value ? 32 * S : 0) + 32 * at + 8 * (part & 3));
     const float s = unpack_f16(e4m3x2_f16x2(block[64 * S + 8 * at + part])).x;
     const float sc = value ? a.vscale : a.kscale;
+    uint32_t y[8];
+    e2m1x8_f16(c.x, y);
+    e2m1x8_f16(c.y, y + 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float2 f = unpack_f16(e2m1x2_f16x2(((e < 4 ? c.x : c.y) >> (8 * (e & 3))) & 255u));
+      const float2 f = unpack_f16(y[e]);
       x[2 * e] = (f.x * s) * sc;
       x[2 * e + 1] = (f.y * s) * sc;
     }
@@ -514,6 +517,7 @@ int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
   a.cu_q = cu_q;
   a.o = o;
   a.lse = lse;
+  wait_injection(&a.wait_cycles, &a.debug_skip);
   if ((rc = device_status(&a.status)) != SFA_OK) return rc;
   return launch_kv4_attend(a, p, d->dtype, ws, stream);
 }

@@ -20,37 +20,43 @@
 
 namespace sfa {
 
-// Probabilities are kept times 2^kPShift: f16's smallest steps then lie 2^-36
-// below the largest probability of a column.
-constexpr float kPShift = 12.0f;
+// Probabilities are kept times 2^kPShift, relative to a maximum that may lag
+// the true one by 2^kLag (the statistics move only when a logit passes it by
+// more): at most 2^15 in f16, whose smallest steps then lie 2^-35 below the
+// largest probability of a column.
+constexpr float kPShift = 11.0f, kLag = 4.0f;
 
-// The group's queries of one row as B fragments: lane (g, t) holds dims
-// 16t .. 16t + 15 of head 8 nt + g, in the order the keys' codes come in.
+// Queries as B fragments: column c is head c mod G of row c / G; lane (g, t)
+// holds dims 16t .. 16t + 15 of column 8 nt + g, in the order the keys' codes
+// come in.
 template <int NT>
 struct QFrag {
   uint32_t hi[NT][8], lo[NT][8];
   float c[NT][2];  // logit of accumulator (heads 2t, 2t + 1), log2 units
 
-  // row: q + the group's first head; heads from G on are zero columns.
+  // base: the first head of the first row, which stands at pos; columns from
+  // ncol on, and rows before position 0, are zero.
   template <typename TIO>
-  __device__ __forceinline__ void load(const TIO* row, int G, const float2* rope, int pos, float scale, int lane) {
+  __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, int ncol, const float2* rope, int pos, float scale,
+                                       int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int head = 8 * nt + g;
+      const int col = 8 * nt + g, p = pos + (col >> lgG);
+      const TIO* row = base + (col >> lgG) * stride + (col & ((1 << lgG) - 1)) * kD;
       float x[16], y[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-      if (head < G) {
-        load8(row + head * kD + 16 * t, x);
-        load8(row + head * kD + 16 * t + 8, x + 8);
+      if (col < ncol && p >= 0) {
+        load8(row + 16 * t, x);
+        load8(row + 16 * t + 8, x + 8);
         if (rope) {  // the pair of dim j is j +- 32
-          load8(row + head * kD + 16 * (t ^ 2), y);
-          load8(row + head * kD + 16 * (t ^ 2) + 8, y + 8);
+          load8(row + 16 * (t ^ 2), y);
+          load8(row + 16 * (t ^ 2) + 8, y + 8);
 #pragma unroll
           for (int c8 = 0; c8 < 16; c8 += 8) {
             float cs[8], sn[8];
-            load_rope8(rope, pos, 16 * (t & 1) + c8, cs, sn);
+            load_rope8(rope, p, 16 * (t & 1) + c8, cs, sn);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[c8 + e] = x[c8 + e] * cs[e] + (t < 2 ? -y[c8 + e] : y[c8 + e]) * sn[e];
           }
@@ -84,13 +90,16 @@ struct QFrag {
 template <int NT>
 __device__ __forceinline__ void key_products(const QFrag<NT>& q, uint2 ka, uint2 kb, uint32_t sa, uint32_t sb, float (*s)[4]) {
   const uint32_t fa = e4m3x2_f16x2(sa * 0x101u), fb = e4m3x2_f16x2(sb * 0x101u);
+  uint32_t xa[8], xb[8];
+  e2m1x8_f16(ka.x, xa);
+  e2m1x8_f16(ka.y, xa + 4);
+  e2m1x8_f16(kb.x, xb);
+  e2m1x8_f16(kb.y, xb + 4);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    const uint32_t wa = (ks < 2 ? ka.x : ka.y) >> (16 * (ks & 1)), wb = (ks < 2 ? kb.x : kb.y) >> (16 * (ks & 1));
-    const uint32_t a[4] = {hmul2(e2m1x2_f16x2(wa & 255u), fa), hmul2(e2m1x2_f16x2(wb & 255u), fb),
-                           hmul2(e2m1x2_f16x2((wa >> 8) & 255u), fa), hmul2(e2m1x2_f16x2((wb >> 8) & 255u), fb)};
+    const uint32_t a[4] = {hmul2(xa[2 * ks], fa), hmul2(xb[2 * ks], fb), hmul2(xa[2 * ks + 1], fa), hmul2(xb[2 * ks + 1], fb)};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       mma_f16(s[nt], a, q.hi[nt][2 * ks], q.hi[nt][2 * ks + 1]);
@@ -119,12 +128,14 @@ __device__ __forceinline__ void value_products(const uint32_t* w, uint32_t scale
   const uint32_t fab = e4m3x2_f16x2(scales & 0xffffu), fcd = e4m3x2_f16x2(scales >> 16);
   // bytes that hold one dim of two keys: even dims, then odd dims
   const uint32_t lo4 = 0x0f0f0f0fu;
-  const uint32_t eab = (w[0] & lo4) | ((w[1] << 4) & ~lo4), oab = ((w[0] >> 4) & lo4) | (w[1] & ~lo4);
-  const uint32_t ecd = (w[2] & lo4) | ((w[3] << 4) & ~lo4), ocd = ((w[2] >> 4) & lo4) | (w[3] & ~lo4);
+  uint32_t x[4][4];
+  e2m1x8_f16((w[0] & lo4) | ((w[1] << 4) & ~lo4), x[0]);
+  e2m1x8_f16(((w[0] >> 4) & lo4) | (w[1] & ~lo4), x[1]);
+  e2m1x8_f16((w[2] & lo4) | ((w[3] << 4) & ~lo4), x[2]);
+  e2m1x8_f16(((w[2] >> 4) & lo4) | (w[3] & ~lo4), x[3]);
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
-    const uint32_t a[4] = {hmul2(e2m1x2_f16x2((eab >> (8 * mt)) & 255u), fab), hmul2(e2m1x2_f16x2((oab >> (8 * mt)) & 255u), fab),
-                           hmul2(e2m1x2_f16x2((ecd >> (8 * mt)) & 255u), fcd), hmul2(e2m1x2_f16x2((ocd >> (8 * mt)) & 255u), fcd)};
+    const uint32_t a[4] = {hmul2(x[0][mt], fab), hmul2(x[1][mt], fab), hmul2(x[2][mt], fcd), hmul2(x[3][mt], fcd)};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       mma_f16(o[nt][mt], a, b0[nt], b1[nt]);
@@ -237,7 +248,8 @@ __global__ void __launch_bounds__(32 * kGatherWarps)
   acc.clear();
   if (live && pos >= 0) {
     QFrag<NT> q;
-    q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, G, a.rope, pos, 0.125f * kLog2e * a.kscale, lane);
+    q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, G, a.rope, pos, 0.125f * kLog2e * a.kscale,
+           lane);
     const int32_t* trow = a.table + (int64_t)r * a.max_pages;
     const int Wt = min(P.W, pos);
     int nr = 0;
@@ -343,16 +355,576 @@ static cudaError_t gather(const Kv4Args& a, const Plan& p, int warps, cudaStream
   return launch_pdl(kv4_gather_kernel<TIO, NT>, dim3((unsigned)((units + per - 1) / per)), dim3(32 * kGatherWarps), smem, s, a, p, warps);
 }
 
-size_t kv4_attend_workspace(const Kv4Args&, const Plan&, int) { return 0; }
+// ---------------------------------------------------------------- stream
 
-int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void*, void* stream) {
-  if (a.N == 0) return SFA_OK;
-  const int tiles = (int)std::min<int64_t>(((int64_t)p.W + 1 + p.n + 15) / 16, ((int64_t)a.max_pages << a.lgS) / 16);
-  const int warps = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;
+// The whole prefix, or a wide window: a request's pages stream through shared
+// memory.  A warp owns a ring of kStages tiles of 64 keys, filled by
+// asynchronous bulk copies (three a page: key codes, value codes, scales) that
+// one lane each issues; the page ids are read kStages tiles earlier still.
+//
+// Work: an item is up to rows_per query rows of one request (a decode step: one
+// row), its columns rows x heads of one KV head; its keys are cut into chunks
+// of chunk_tiles tiles at absolute places, so what is added to what depends on
+// the call's shapes and the row's own length, not on other requests.  All
+// chunks, in order, are shared out evenly over one wave of CTAs: each CTA adds
+// up the items' chunk counts (from the lengths, in one block-wide scan), takes
+// its part and walks it, the copies running on across chunks and items.  The
+// four warps take every fourth tile of a chunk and meet in shared memory at its
+// end.  Chunks of a longer item go to the workspace, joined by a second kernel.
+constexpr int kStreamWarps = 4, kStages = 3, kTile = 64, kTileBytes = kTile * kKv4Row;
+constexpr int kSMs = 152;
+
+struct StreamArgs {
+  int32_t items, lg_rows, chunk_tiles, max_chunks, W;
+  float* part_o;   // [item][KV head][chunk][column][64]
+  float2* part_ml; // [item][KV head][chunk][column] (m, l)
+};
+
+struct Item {
+  int r, row0, nrows, pfirst, c0, nch;  // nch = 0: no rows
+  __device__ __forceinline__ int plast() const { return pfirst + nrows - 1; }
+};
+
+// Item x.  Requests start at item cu_q[r] / rows + r: room for each one's last,
+// shorter item without a scan over the requests.  A request whose positions
+// leave the tables counts as empty: zero rows, and the status says so.
+__device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, int x) {
+  Item it;
+  int len;
+  if (!a.cu_q) {
+    it.r = it.row0 = x;
+    it.nrows = 1;
+    len = a.seq_lens[x];
+    it.pfirst = len - 1;
+  } else {
+    int lo = 0, n = a.R;  // largest r with cu_q[r] / rows + r <= x
+    while (n > 1) {
+      const int half = n >> 1;
+      const bool le = (a.cu_q[lo + half] >> s.lg_rows) + lo + half <= x;
+      lo += le ? half : 0;
+      n = le ? n - half : half;
+    }
+    const int c = a.cu_q[lo], end = min(a.cu_q[lo + 1], a.N);
+    it.r = lo;
+    it.row0 = c + ((x - lo - (c >> s.lg_rows)) << s.lg_rows);
+    it.nrows = min(1 << s.lg_rows, end - it.row0);
+    if (c < 0 || it.row0 < c || it.nrows <= 0) {
+      it.nrows = it.nch = it.pfirst = it.c0 = 0;
+      return it;
+    }
+    len = a.seq_lens[lo];
+    it.pfirst = len - (end - it.row0);
+  }
+  const bool empty = !a.cu_q && len == 0;
+  if (empty || it.pfirst < 0 || it.pfirst > (a.max_pages << a.lgS) - it.nrows || (a.rope && it.pfirst > a.rope_T - it.nrows)) {
+    if (!empty) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+    it.pfirst = -it.nrows;
+    it.c0 = 0;
+    it.nch = 1;
+    return it;
+  }
+  const int ck = s.chunk_tiles * kTile;
+  it.c0 = max(0, it.pfirst - s.W) / ck;
+  it.nch = it.plast() / ck - it.c0 + 1;
+  return it;
+}
+
+// A place in the CTA's run of chunks, and the tiles of the chunk there.
+struct Cursor {
+  Item it;
+  int x, h, c, left;  // left: chunks of the run from here on
+  int tb, te;
+  __device__ __forceinline__ void tiles(const StreamArgs& s) {
+    tb = max(c * s.chunk_tiles, max(0, it.pfirst - s.W) / kTile);
+    te = it.plast() < 0 ? tb : min((c + 1) * s.chunk_tiles, it.plast() / kTile + 1);
+  }
+  // the next chunk; false at the end of the run
+  __device__ __forceinline__ bool next(const Kv4Args& a, const StreamArgs& s) {
+    if (--left <= 0) return false;
+    if (++c == it.c0 + it.nch) {
+      if (++h == a.Hkv) {
+        h = 0;
+        do
+          it = item_at(a, s, ++x);
+        while (it.nch == 0 && x + 1 < s.items);
+      }
+      c = it.c0;
+    }
+    tiles(s);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// The warp's ring of tiles: its copies run ahead of the tiles it consumes.
+struct Ring {
+  uint32_t data, bar;        // shared addresses of the slots and of their barriers
+  volatile int* pages;       // per slot: which of the tile's pages are there
+  Cursor at;                 // the tile whose page ids are read next
+  int ti;
+  bool more;
+  int pid[kStages], meta[kStages];  // tiles whose ids have been read, nearest first; meta < 0: none
+  int issued, used, skip;
+
+  __device__ __forceinline__ void skip_empty(const Kv4Args& a, const StreamArgs& s, int warp) {
+    while (more && ti >= at.te) {
+      more = at.next(a, s);
+      ti = at.tb + warp;
+    }
+  }
+  // read the page ids of the next tile: lanes 3p .. 3p + 2 for page p of it
+  __device__ __forceinline__ void read_ids(const Kv4Args& a, const StreamArgs& s, int warp, int lane) {
+#pragma unroll
+    for (int k = 0; k + 1 < kStages; ++k) {
+      pid[k] = pid[k + 1];
+      meta[k] = meta[k + 1];
+    }
+    meta[kStages - 1] = -1;
+    if (!more) return;
+    const int j = ti * kTile, last = at.it.plast();
+    const int rows = min(1 << a.lgS, kTile);
+    const int n = min(kTile / rows, (last - j) / rows + 1);
+    pid[kStages - 1] = lane < 3 * n ? a.table[(int64_t)at.it.r * a.max_pages + ((j + lane / 3 * rows) >> a.lgS)] : -1;
+    meta[kStages - 1] = n | ((j >> a.lgS << a.lgS) == j ? 0 : 8) | at.h << 4;
+    ti += kStreamWarps;
+    skip_empty(a, s, warp);
+  }
+  // start the copies of the nearest tile whose ids have been read
+  __device__ __forceinline__ void issue(const Kv4Args& a, int lane) {
+    if (meta[0] < 0) return;
+    const int slot = issued % kStages, n = meta[0] & 7, h = meta[0] >> 4;
+    ++issued;
+    const bool mine = lane < 3 * n, ok = mine && pid[0] >= 0 && pid[0] < a.n_pages;
+    if (mine && !ok) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+    const uint32_t there = __ballot_sync(0xffffffffu, ok) & 0x249u;  // bit 3p: page p
+    const int S = 1 << a.lgS, rows = min(S, kTile);
+    const uint32_t b = bar + 8 * slot, d = data + slot * kTileBytes;
+    if (issued - 1 == skip) return;
+    if (lane == 0) {
+      pages[slot] = (int)((there & 1) | (there >> 2 & 2) | (there >> 4 & 4) | (there >> 6 & 8));
+      mbar_expect_tx(b, __popc(there) * rows * kKv4Row);
+    }
+    __syncwarp();
+    if (ok) {
+      const int p = lane / 3, part = lane - 3 * p, row = meta[0] & 8 ? kTile : 0;
+      const uint8_t* src = a.cache + ((int64_t)pid[0] * a.Hkv + h) * (kKv4Row * S);
+      if (part == 2)
+        bulk_load(d + 64 * kTile + 8 * p * rows, src + 64 * S + 8 * row, 8 * rows, b);
+      else
+        bulk_load(d + 32 * kTile * part + 32 * p * rows, src + 32 * S * part + 32 * row, 32 * rows, b);
+    }
+  }
+};
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8u(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// Row r of a 16-key tile is key r ^ (r >> 2 & 1): the rows that lanes of one
+// shared-memory pass read then lie in different banks, for keys (rows g) and
+// values (rows 2t, 2t + 1) alike.
+__device__ __forceinline__ int key_of(int r) { return r ^ ((r >> 2) & 1); }
+
+// One tile of 64 keys from key j0 on, in shared memory at T.
+template <int NT, bool EXACT>
+__device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& sa, const Item& it, const QFrag<NT>& q, Acc<NT>& acc,
+                                            uint32_t T, int j0, int pages, int lane) {
+  constexpr int GB = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // 16-key groups whose logits are held at once
+  const int g = lane >> 2, t = lane & 3;
+  const int rows = min(1 << a.lgS, kTile), lgr = min(a.lgS, 6);
+  const bool full = pages == (1 << (kTile / rows)) - 1 && j0 + kTile - 1 <= it.pfirst && j0 >= it.plast() - sa.W;
+  // does column 8 nt + 2 t + e attend key k of the tile?
+  auto attends = [&](int nt, int e, int k) {
+    const int p = it.pfirst + ((8 * nt + 2 * t + e) >> a.lgG), j = j0 + k;
+    return j <= p && j >= p - sa.W && (pages >> (k >> lgr) & 1);
+  };
+#pragma unroll
+  for (int gb = 0; gb < 4; gb += GB) {
+    float s[GB][NT][4];
+#pragma unroll
+    for (int i = 0; i < GB; ++i) {
+      const int ka = 16 * (gb + i) + key_of(g), kb = ka + 8;
+      key_products(q, lds64(T + 32 * ka + 8 * t), lds64(T + 32 * kb + 8 * t), lds8u(T + 64 * kTile + 8 * ka + t),
+                   lds8u(T + 64 * kTile + 8 * kb + t), s[i]);
+      if (!full)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (!attends(nt, e, ka)) s[i][nt][e] = -INFINITY;
+            if (!attends(nt, e, kb)) s[i][nt][2 + e] = -INFINITY;
+          }
+    }
+    // the statistics move only when a logit passes them by more than kLag
+    float top[NT][2];
+    bool passes = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+        for (int i = 1; i < GB; ++i) x = fmaxf(x, fmaxf(s[i][nt][e], s[i][nt][2 + e]));
+        top[nt][e] = x * q.c[nt][e];
+        passes |= top[nt][e] > acc.m[nt][e] + kLag;
+      }
+    if (__any_sync(0xffffffffu, passes))
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = top[nt][e];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          if (x > acc.m[nt][e]) {
+            const float corr = ex2(acc.m[nt][e] - x);  // 0 on the first keys
+            acc.m[nt][e] = x;
+            acc.l[nt][e] *= corr;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              acc.o[nt][mt][e] *= corr;
+              acc.o[nt][mt][2 + e] *= corr;
+            }
+          }
+        }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float off = acc.m[nt][e] == -INFINITY ? 0.0f : kPShift - acc.m[nt][e];
+#pragma unroll
+        for (int i = 0; i < GB; ++i) {
+          s[i][nt][e] = ex2(fmaf(s[i][nt][e], q.c[nt][e], off));
+          s[i][nt][2 + e] = ex2(fmaf(s[i][nt][2 + e], q.c[nt][e], off));
+          acc.l[nt][e] += s[i][nt][e] + s[i][nt][2 + e];
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < GB; ++i) {
+      uint32_t w[4], vs[4];
+      bool nan = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 16 * (gb + i) + key_of(2 * t + (e & 1)) + 8 * (e >> 1);
+        w[e] = lds32(T + 32 * kTile + 32 * k + 4 * g);
+        vs[e] = lds8u(T + 64 * kTile + 8 * k + 4 + (g >> 1));
+        if (!full) {  // rows that are not stored hold anything, a NaN scale perhaps; 0 * NaN must not reach the sums
+          if (j0 + k > it.plast() || !(pages >> (k >> lgr) & 1)) vs[e] = 0;
+          nan |= (vs[e] & 127u) == 127u;
+        }
+      }
+      if (!full && __any_sync(0xffffffffu, nan)) {
+        // a stored NaN reaches the columns that attend it, and no others
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((vs[e] & 127u) == 127u) vs[e] = 0;
+        for (int k = 16 * (gb + i); k < 16 * (gb + i) + 16; ++k)
+          if ((lds8u(T + 64 * kTile + 8 * k + 4 + (g >> 1)) & 127u) == 127u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (attends(nt, e, k))
+#pragma unroll
+                  for (int mt = 0; mt < 4; ++mt) acc.o[nt][mt][e] = acc.o[nt][mt][2 + e] = __int_as_float(0x7fffffff);
+      }
+      value_products<NT, EXACT>(w, vs[0] | vs[1] << 8 | vs[2] << 16 | vs[3] << 24, s[i], acc.o);
+    }
+  }
+}
+
+template <typename TIO, int NT>
+__global__ void __launch_bounds__(32 * kStreamWarps, NT == 1 ? 3 : 2) kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
+  constexpr bool kExact = sizeof(TIO) == 4;
+  constexpr int NC = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* const po = reinterpret_cast<float*>(smem + kStreamWarps * kStages * kTileBytes);  // [warp][NC][66]
+  float2* const ml = reinterpret_cast<float2*>(po + kStreamWarps * NC * 66);               // [warp][NC]
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(ml + kStreamWarps * NC);
+  int* const pages = reinterpret_cast<int*>(bars + kStreamWarps * kStages);
+  int* const where = pages + kStreamWarps * kStages;  // warp sums, then the CTA's first chunk
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  pdl_launch_dependents();
+  Ring ring;
+  ring.data = smem_u32(smem) + warp * kStages * kTileBytes;
+  ring.bar = smem_u32(bars + warp * kStages);
+  ring.pages = pages + warp * kStages;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(ring.bar + 8 * i, 1);
+    mbar_fence_init();
+  }
+  pdl_wait();
+
+  // this CTA's run of chunks
+  const int per = (sa.items + 32 * kStreamWarps - 1) / (32 * kStreamWarps);
+  const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
+  int mine = 0;
+  for (int x = x0; x < x1; ++x) mine += item_at(a, sa, x).nch * a.Hkv;
+  int inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += y;
+  }
+  if (lane == 31) where[warp] = inc;
+  __syncthreads();
+  int before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kStreamWarps; ++w) {
+    if (w < warp) before += where[w];
+    total += where[w];
+  }
+  const int first = (int)((int64_t)total * blockIdx.x / gridDim.x), last = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  if (first == last) return;
+  if (first >= before && first < before + mine) {
+    int at = before;
+    for (int x = x0; x < x1; ++x) {
+      const Item it = item_at(a, sa, x);
+      if (first < at + it.nch * a.Hkv) {
+        where[4] = x;
+        where[5] = (first - at) / it.nch;
+        where[6] = it.c0 + (first - at) % it.nch;
+        break;
+      }
+      at += it.nch * a.Hkv;
+    }
+  }
+  __syncthreads();
+  Cursor cur;
+  cur.x = where[4];
+  cur.h = where[5];
+  cur.c = where[6];
+  cur.it = item_at(a, sa, cur.x);
+  cur.left = last - first;
+  cur.tiles(sa);
+
+  ring.at = cur;
+  ring.ti = cur.tb + warp;
+  ring.more = true;
+  ring.issued = ring.used = 0;
+  ring.skip = first == 0 && warp == 0 ? a.debug_skip : -1;
+  ring.skip_empty(a, sa, warp);
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) ring.read_ids(a, sa, warp, lane);
+#pragma unroll
+  for (int k = 0; k < kStages; ++k) {
+    ring.issue(a, lane);
+    ring.read_ids(a, sa, warp, lane);
+  }
+
   const int G = 1 << a.lgG;
-  cudaStream_t s = (cudaStream_t)stream;
-  LaunchTimer tm(SFA_KERNEL_KV4_ATTEND, stream);
+  QFrag<NT> q;
+  Acc<NT> acc;
+  int qx = -1, qh = -1;
+  bool dead = false;  // a wait ran out: no more copies, no more work
+  do {
+    const int ncol = cur.it.nrows << a.lgG;
+    if (cur.x != qx || cur.h != qh) {
+      q.load(static_cast<const TIO*>(a.q) + (int64_t)cur.it.row0 * a.q_stride + cur.h * G * kD, a.q_stride, a.lgG, ncol, a.rope,
+             cur.it.pfirst, 0.125f * kLog2e * a.kscale, lane);
+      qx = cur.x;
+      qh = cur.h;
+    }
+    acc.clear();
+    for (int ti = cur.tb + warp; ti < cur.te; ti += kStreamWarps) {
+      const int slot = ring.used % kStages, phase = ring.used / kStages & 1;
+      if (!dead && !mbar_wait_bounded(ring.bar + 8 * slot, phase, a.wait_cycles)) {
+        record_status(a.status, SFA_ERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead) continue;
+      ++ring.used;
+      stream_tile<NT, kExact>(a, sa, cur.it, q, acc, ring.data + slot * kTileBytes, ti * kTile, ring.pages[slot], lane);
+      __syncwarp();
+      ring.issue(a, lane);
+      ring.read_ids(a, sa, warp, lane);
+    }
+    acc.close();
+    if (g == 0)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ml[warp * NC + 8 * nt + 2 * t + e] = make_float2(acc.m[nt][e], acc.l[nt][e]);
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 8 * nt + 2 * t + e;
+        if (col >= ncol) continue;
+        float M = ml[col].x;
+#pragma unroll
+        for (int w = 1; w < kStreamWarps; ++w) M = fmaxf(M, ml[w * NC + col].x);
+        const float f = acc.m[nt][e] == -INFINITY ? 0.0f : ex2(acc.m[nt][e] - M);
+        float* out = po + (warp * NC + col) * 66 + 8 * g;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+          *reinterpret_cast<float2*>(out + 2 * mt) = make_float2(acc.o[nt][mt][e] * f, acc.o[nt][mt][2 + e] * f);
+      }
+    __syncthreads();
+    for (int i = tid; i < 8 * ncol; i += 32 * kStreamWarps) {
+      const int col = i >> 3, d = i & 7;
+      float M = ml[col].x, l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int w = 1; w < kStreamWarps; ++w) M = fmaxf(M, ml[w * NC + col].x);
+#pragma unroll
+      for (int w = 0; w < kStreamWarps; ++w) {
+        const float2 v = ml[w * NC + col];
+        l += v.y * (v.x == -INFINITY ? 0.0f : ex2(v.x - M));
+        const float* y = po + (w * NC + col) * 66 + 8 * d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += y[e];
+      }
+      if (cur.it.nch == 1) {
+        write_head<TIO>(a, cur.it.row0 + (col >> a.lgG), cur.h * G + (col & (G - 1)), d, x, M, l);
+      } else {
+        const int64_t at = (((int64_t)cur.x * a.Hkv + cur.h) * sa.max_chunks + cur.c - cur.it.c0) * (G << sa.lg_rows) + col;
+        store8(sa.part_o + at * kD + 8 * d, x);
+        if (d == 0) sa.part_ml[at] = make_float2(M, l);
+      }
+    }
+    __syncthreads();  // ml and po are filled again by the next chunk
+  } while (cur.next(a, sa));
+  // after a timeout: the copies still in flight end before the CTA does
+  if (dead)
+    for (; ring.used < ring.issued; ++ring.used)
+      mbar_wait_bounded(ring.bar + 8 * (ring.used % kStages), ring.used / kStages & 1, a.wait_cycles);
+}
+
+// The chunks of one (item, KV head) joined: `cols` columns a CTA, 8 lanes a
+// column, the chunks dealt out over the remaining threads.
+constexpr int kJoinThreads = 128;
+
+template <typename TIO>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, const StreamArgs sa, int cols) {
+  __shared__ float red[kJoinThreads][9];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int x = blockIdx.x / a.Hkv, h = blockIdx.x - x * a.Hkv;
+  const Item it = item_at(a, sa, x);
+  const int ncol = it.nrows << a.lgG, G = 1 << a.lgG, width = G << sa.lg_rows;
+  if (it.nch <= 1 || (int)blockIdx.y * cols >= ncol) return;
+  const int lanes = 8 * cols, groups = kJoinThreads / lanes;
+  const int i = threadIdx.x % lanes, grp = threadIdx.x / lanes, d = i & 7;
+  const int col = min((int)blockIdx.y * cols + (i >> 3), ncol - 1);
+  const int64_t at = ((int64_t)blockIdx.x * sa.max_chunks) * width + col;
+  float M = -INFINITY;
+  for (int c = grp; c < it.nch; c += groups) M = fmaxf(M, sa.part_ml[at + (int64_t)c * width].x);
+  red[threadIdx.x][8] = M;
+  __syncthreads();
+  for (int k = 0; k < groups; ++k) M = fmaxf(M, red[k * lanes + i][8]);
+  __syncthreads();
+  float l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int c = grp; c < it.nch; c += groups) {
+    const float2 v = sa.part_ml[at + (int64_t)c * width];
+    const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - M);
+    float z[8];
+    load8(sa.part_o + (at + (int64_t)c * width) * kD + 8 * d, z);
+    l += v.y * f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], f, y[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = y[e];
+  red[threadIdx.x][8] = l;
+  __syncthreads();
+  if (grp != 0 || (int)blockIdx.y * cols + (i >> 3) >= ncol) return;
+  for (int k = 1; k < groups; ++k) {
+    l += red[k * lanes + i][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] += red[k * lanes + i][e];
+  }
+  write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M, l);
+}
+
+// The stream kernel's shape for a call; items = 0: the gather kernel takes it.
+struct StreamShape {
+  StreamArgs s;
+  int nt, grid;
+  int64_t slots;  // chunks the workspace has room for
+};
+
+static StreamShape stream_shape(const Kv4Args& a, const Plan& p) {
+  StreamShape z = {};
+  const int64_t cap = (int64_t)a.max_pages << a.lgS;
+  if (p.n > 0 || std::min<int64_t>(cap, (int64_t)p.W + 1) <= 64) return z;
+  const int G = 1 << a.lgG;
+  // columns a warp holds: as many rows as a request brings on average, 32 at most
+  const int avg = a.cu_q ? (a.N + a.R - 1) / a.R : 1;
+  z.nt = G * avg > 16 ? 4 : G * avg > 8 ? 2 : 1;
+  z.nt = std::max(z.nt, G > 16 ? 4 : G > 8 ? 2 : 1);
+  z.s.lg_rows = a.cu_q ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
+  z.s.items = a.cu_q ? (a.N >> z.s.lg_rows) + a.R : a.R;
+  z.s.W = p.W;
+  z.grid = kSMs * (z.nt == 1 ? 3 : 2);
+  // chunks: at least 512 keys, and so that the whole block table's worth of
+  // them stays within 16 a CTA (the workspace's size; 16 parts a CTA balance to
+  // a few percent)
+  const int64_t units = (int64_t)z.s.items * a.Hkv;
+  int64_t ck = 512;
+  while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.grid) ck *= 2;
+  z.s.chunk_tiles = (int)(ck / kTile);
+  z.s.max_chunks = (int)((cap + ck - 1) / ck);
+  z.slots = z.s.max_chunks > 1 ? units * z.s.max_chunks : 0;
+  return z;
+}
+
+template <typename TIO, int NT>
+static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
+  constexpr int NC = 8 * NT;
+  constexpr size_t smem = kStreamWarps * (kStages * (kTileBytes + 8 + 4) + NC * (66 * 4 + 8)) + 64;
+  static_assert(smem <= 227 * 1024 / (NT == 1 ? 3 : 2), "CTAs an SM");
+  cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = launch_pdl(kv4_stream_kernel<TIO, NT>, dim3((unsigned)z.grid), dim3(32 * kStreamWarps), smem, s, a, z.s);
+  if (e != cudaSuccess || z.slots == 0) return e;
+  const int width = 1 << (a.lgG + z.s.lg_rows);
+  const int cols = z.s.max_chunks > 32 ? 1 : std::min(width, kJoinThreads / 8);
+  return launch_pdl(kv4_join_kernel<TIO>, dim3((unsigned)(z.s.items * a.Hkv), (unsigned)((width + cols - 1) / cols)), dim3(kJoinThreads), 0,
+                    s, a, z.s, cols);
+}
+
+size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, int) {
+  const StreamShape z = stream_shape(a, p);
+  return (size_t)z.slots * ((size_t)66 * 4 << (a.lgG + z.s.lg_rows));
+}
+
+int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void* stream_) {
+  const int G = 1 << a.lgG;
+  cudaStream_t s = (cudaStream_t)stream_;
+  LaunchTimer tm(SFA_KERNEL_KV4_ATTEND, stream_);
   cudaError_t e;
+  StreamShape z = stream_shape(a, p);
+  if (z.s.items > 0) {
+    z.s.part_o = static_cast<float*>(ws);
+    z.s.part_ml = reinterpret_cast<float2*>(z.s.part_o + ((size_t)z.slots * kD << (a.lgG + z.s.lg_rows)));
+    if (dtype == SFA_BF16)
+      e = z.nt == 1 ? stream<bf16, 1>(a, z, s) : z.nt == 2 ? stream<bf16, 2>(a, z, s) : stream<bf16, 4>(a, z, s);
+    else
+      e = z.nt == 1 ? stream<float, 1>(a, z, s) : z.nt == 2 ? stream<float, 2>(a, z, s) : stream<float, 4>(a, z, s);
+    return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+  }
+  const int tiles = (int)((std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS) + 15) / 16);
+  const int warps = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;
   if (dtype == SFA_BF16)
     e = G <= 8 ? gather<bf16, 1>(a, p, warps, s) : G == 16 ? gather<bf16, 2>(a, p, warps, s) : gather<bf16, 4>(a, p, warps, s);
   else

@@ -530,3 +530,26 @@ def test_captured_decode_steps(sfa, dist):
             assert torch.equal(a[n], b[n]), n
     assert sfa.get_device_status() == 0
     assert a["lens"].tolist() == [n + 20 for n in start]
+
+
+def test_attend_wait_that_runs_out(sfa, sfa_lib):
+    """A tile whose copies are never started: its wait runs out, the status says so, the call ends, and
+    the next call is right."""
+    import torch
+
+    rng = np.random.default_rng(14)
+    lens, page = [3000, 700], 16
+    cache, table = make_cache(rng, lens, page, 2)
+    q = torch.from_numpy(rng.standard_normal((2, 8, 64))).float().cuda()
+    args = (q, _cuda(cache), _cuda(table), _i32(lens))
+    good = sfa.kv4_attend(*args)
+    torch.cuda.synchronize()
+    try:
+        for tile in (0, 1):
+            assert sfa_lib.sfa_debug_inject(2000000, tile) == 0
+            sfa.kv4_attend(*args)
+            assert sfa.get_device_status() == 5  # SFA_ERR_TIMEOUT (the warp has two tiles)
+    finally:
+        sfa_lib.sfa_debug_inject(0, -1)
+    again = sfa.kv4_attend(*args)
+    assert sfa.get_device_status() == 0 and torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
