@@ -1,6 +1,8 @@
 // The paged 4-bit cache's bookkeeping, its write and its read-back: block
 // tables and slot maps from request lengths, rotate + quantise + store, and
 // rows as numbers.
+#include <algorithm>
+
 #include "sfa_kv4.cuh"
 #include "sfa_launch.cuh"
 
@@ -490,8 +492,11 @@ int sfa_kv4_workspace_size(const sfa_kv4_desc* d, size_t* bytes) {
   Kv4Args a;
   if (!bytes) return SFA_ERR_INVALID_ARG;
   const int rc = check_attend(d, &p, &a);
-  if (rc == SFA_OK) *bytes = kv4_attend_workspace(a, p, d->dtype);
-  return rc;
+  if (rc != SFA_OK) return rc;
+  // without cu_q N = R; with N = R the call may be of either kind
+  *bytes = kv4_attend_workspace(a, p, true);
+  if (d->N == d->R) *bytes = std::max(*bytes, kv4_attend_workspace(a, p, false));
+  return SFA_OK;
 }
 
 int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
@@ -507,7 +512,7 @@ int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
   if (!at16(q) || !at16(cache) || !at16(o) || !at4(block_table) || !at4(seq_lens) || !at4(cu_q) || !at4(lse))
     return SFA_ERR_INVALID_ARG;
   if (!stride_ok(d->q_stride, d->Hq, d->dtype)) return SFA_ERR_INVALID_ARG;
-  const size_t need = kv4_attend_workspace(a, p, d->dtype);
+  const size_t need = kv4_attend_workspace(a, p, cu_q != nullptr);
   if (need && (!ws || !at16(ws))) return SFA_ERR_INVALID_ARG;
   if (ws_bytes < need) return SFA_ERR_CAPACITY;
   a.q = q;

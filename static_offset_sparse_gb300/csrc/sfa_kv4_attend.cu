@@ -864,17 +864,17 @@ struct StreamShape {
   int64_t slots;  // chunks the workspace has room for
 };
 
-static StreamShape stream_shape(const Kv4Args& a, const Plan& p) {
+static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   StreamShape z = {};
   const int64_t cap = (int64_t)a.max_pages << a.lgS;
   if (p.n > 0 || std::min<int64_t>(cap, (int64_t)p.W + 1) <= 64) return z;
   const int G = 1 << a.lgG;
   // columns a warp holds: as many rows as a request brings on average, 32 at most
-  const int avg = a.cu_q ? (a.N + a.R - 1) / a.R : 1;
+  const int avg = ragged ? (a.N + a.R - 1) / a.R : 1;
   z.nt = G * avg > 16 ? 4 : G * avg > 8 ? 2 : 1;
   z.nt = std::max(z.nt, G > 16 ? 4 : G > 8 ? 2 : 1);
-  z.s.lg_rows = a.cu_q ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
-  z.s.items = a.cu_q ? (a.N >> z.s.lg_rows) + a.R : a.R;
+  z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
+  z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
   z.s.W = p.W;
   z.grid = kSMs * (z.nt == 1 ? 3 : 2);
   // chunks: at least 512 keys, and so that the whole block table's worth of
@@ -903,8 +903,8 @@ static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s
                     s, a, z.s, cols);
 }
 
-size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, int) {
-  const StreamShape z = stream_shape(a, p);
+size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, bool ragged) {
+  const StreamShape z = stream_shape(a, p, ragged);
   return (size_t)z.slots * ((size_t)66 * 4 << (a.lgG + z.s.lg_rows));
 }
 
@@ -913,7 +913,7 @@ int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void
   cudaStream_t s = (cudaStream_t)stream_;
   LaunchTimer tm(SFA_KERNEL_KV4_ATTEND, stream_);
   cudaError_t e;
-  StreamShape z = stream_shape(a, p);
+  StreamShape z = stream_shape(a, p, a.cu_q != nullptr);
   if (z.s.items > 0) {
     z.s.part_o = static_cast<float*>(ws);
     z.s.part_ml = reinterpret_cast<float2*>(z.s.part_o + ((size_t)z.slots * kD << (a.lgG + z.s.lg_rows)));

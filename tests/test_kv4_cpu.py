@@ -129,3 +129,22 @@ def test_plain_pool():
     pool = ref.Pool(np.full((2, 4), -1), [0, 1, 2, 3], [0, 0], 16)
     assert pool.step([17, 1], 20) == ([0, 17, 18], [3 * 16 + i for i in range(16)] + [2 * 16, 16] + [-1] * 2, list(range(17)) + [0] + [-1] * 2)
     assert pool.step([-1, 0], 1) == ([0, 0, 0], [-1], [-1]) and pool.free == [0, 3, 2] and pool.lens == [0, 1]
+
+
+def _workspace(lib, **kw):
+    n = C.c_size_t(0)
+    assert lib.sfa_kv4_workspace_size(_desc(**kw), C.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("R,N", [(8, 4000), (3, 64), (16, 17), (5, 5), (1, 1), (300, 300)])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 1), (32, 1), (4, 4)])
+@pytest.mark.parametrize("page,max_pages", [(64, 256), (16, 33), (128, 8192)])
+def test_workspace_holds_the_split_rows(sfa_lib, R, N, Hq, Hkv, page, max_pages):
+    """If any scratch is wanted there is room for two parts (m, l and 64 sums) of every row and head, with
+    ragged rows and with one row a request; its size stays within bounds however wide the block table."""
+    kw = dict(n_pages=1 << 14, R=R, N=N, Hq=Hq, Hkv=Hkv, page=page, max_pages=max_pages, q_stride=Hq * 64)
+    n = _workspace(sfa_lib, **kw)
+    assert n >= 2 * N * Hq * 66 * 4 or (n == 0 and N > 2000)  # enough rows: none is split
+    assert n <= max(16 * 456 * 8 * 66 * 4, 16 * 304 * 32 * 66 * 4)
+    assert _workspace(sfa_lib, **{**kw, "max_pages": 512 // page}) == 0
