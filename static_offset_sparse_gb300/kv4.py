@@ -16,100 +16,129 @@ from ._lib import SFA_BF16, SFA_F32, Kv4Desc, _lib, check, i32_array
 from .api import _ROPE_CACHE, _torch, rope_table
 
 ROW_BYTES = 72  # one (row, head): 32 + 32 bytes of codes, 8 of scales
+PAGES = {ROW_BYTES * page: page for page in (16, 32, 64, 128)}
+
+# A decode step of a small batch takes the GPU a few microseconds, so the checks
+# below are single expressions over cheap attributes; what says what is wrong is
+# only run when one of them fails.
 
 
-def _need(t, name, dtype, dim, device=None):
+def _refuse(name, t, dtype, dim, device=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libsfa has no CPU path)")
     if t.dtype != dtype or t.dim() != dim:
         raise ValueError(f"{name} must be {dtype} with {dim} dimension(s), got {t.dtype} {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache's device is {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _ints(device, **tensors):
+def _ints(index, n, t, name):
+    """t is int32 [n] on device `index`."""
     i32 = _torch().int32
-    for name, t in tensors.items():
-        _need(t, name, i32, 1, device)
+    if not (t.dtype is i32 and t.get_device() == index and t.dim() == 1 and t.is_contiguous()):
+        _refuse(name, t, i32, 1, index)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} element(s), got {t.shape[0]}")
+    return t.data_ptr()
 
 
-def _page(cache) -> int:
-    _need(cache, "cache", _torch().uint8, 3)
-    page, rest = divmod(cache.shape[2], ROW_BYTES)
-    if rest or page not in (16, 32, 64, 128):
+def _dense(index, shape, dtype, t, name):
+    """t is a contiguous tensor of this shape and type on device `index`."""
+    if not (t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.shape == shape):
+        if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        _refuse(name, t, dtype, len(shape), index)
+    return t.data_ptr()
+
+
+def _pool(cache):
+    """Device index, pages, KV heads and rows a page of a cache."""
+    u8 = _torch().uint8
+    if not (cache.dtype is u8 and cache.is_cuda and cache.dim() == 3 and cache.is_contiguous()):
+        _refuse("cache", cache, u8, 3)
+    P, H, width = cache.shape
+    page = PAGES.get(width)
+    if page is None:
         raise ValueError(f"cache must be [pages, Hkv, {ROW_BYTES} * page] with page 16, 32, 64 or 128, "
                          f"got {tuple(cache.shape)}")
-    return page
+    return cache.get_device(), P, H, page
 
 
 def _code(dtype) -> int:
     torch = _torch()
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return SFA_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return SFA_F32
     raise TypeError(f"unsupported dtype {dtype}")
 
 
-def _rows(t, name, heads, device, dtype=None):
-    """Stride between the rows of t [N, heads, 64], whose rows are dense."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (libsfa has no CPU path)")
-    if t.dim() != 3 or t.shape[2] != 64 or (heads and t.shape[1] != heads):
+def _rows(t, name, heads, index):
+    """Rows, heads and the stride between the rows of t [N, heads, 64], whose rows are dense."""
+    if t.get_device() != index or t.dim() != 3:
+        _refuse(name, t, t.dtype, 3, index)
+    n, h, d = t.shape
+    if d != 64 or (heads and h != heads):
         raise ValueError(f"{name} must be [rows, {heads or 'Hq'}, 64], got {tuple(t.shape)}")
-    if t.device != device or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or t.dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return n, h, 64 * h
     s = t.stride()
-    width = t.shape[1] * 64
-    if s[2] != 1 or (s[1] != 64 and t.shape[1] > 1):
+    if s[2] != 1 or (s[1] != 64 and h > 1):
         raise ValueError(f"{name}: the [heads, 64] part of a row must be contiguous")
-    if t.shape[0] <= 1:
-        return width
-    if s[0] < width or s[0] * t.element_size() % 16:
+    if n <= 1:
+        return n, h, 64 * h
+    if s[0] < 64 * h or s[0] * t.element_size() % 16:
         raise ValueError(f"{name}: rows must not overlap and must start at multiples of 16 bytes")
-    return s[0]
+    return n, h, s[0]
 
 
 def _scales(kscale, vscale):
-    for name, x in (("kscale", kscale), ("vscale", vscale)):
-        if not (0.0 < x < math.inf):
-            raise ValueError(f"{name} must be positive and finite")
+    if not (0.0 < kscale < math.inf and 0.0 < vscale < math.inf):
+        raise ValueError("kscale and vscale must be positive and finite")
 
 
-def _rope(rope, rope_theta, T, device):
-    """The table's (pointer, positions, tensor): the caller's, or the cached one of rope_theta."""
+def _rope(rope, rope_theta, T, index):
+    """Pointer and positions of the RoPE table: the caller's, or the cached one of rope_theta."""
     torch = _torch()
     if rope is None:
         if not rope_theta or rope_theta <= 0:
-            return None, 0, None
-        key = (int(T), float(rope_theta), device.index)
-        if key not in _ROPE_CACHE:
+            return None, 0
+        key = (int(T), float(rope_theta), index)
+        rope = _ROPE_CACHE.get(key)
+        if rope is None:
             if torch.cuda.is_current_stream_capturing():
                 raise ValueError("make the RoPE table before the capture: rope_table(T, rope_theta), passed as rope=")
-            rope_table(T, rope_theta, device)
+            rope = rope_table(T, rope_theta, torch.device("cuda", index))
             # the table is shared by later calls on any stream
-            torch.cuda.current_stream(device).synchronize()
-        rope = _ROPE_CACHE[key]
-    _need(rope, "rope", torch.float32, 3, device)
-    if rope.shape[1:] != (32, 2):
-        raise ValueError(f"rope must be [positions, 32, 2], got {tuple(rope.shape)}")
-    return rope.data_ptr(), rope.shape[0], rope
+            torch.cuda.current_stream(index).synchronize()
+    n = rope.shape[0]
+    return _dense(index, (n, 32, 2), torch.float32, rope, "rope"), n
 
 
 @functools.lru_cache(maxsize=64)
 def _offsets(dist: tuple):
-    return i32_array(dist)
+    arr, n = i32_array(dist)
+    return C.cast(arr, C.c_void_p), n, arr
 
 
-def _call(fn, name, device, desc, *args):
+def _stream_of(index):
+    """The current stream's handle on device `index` (the direct getter takes 0.1 us, the Stream object 2)."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
-        check(fn(desc, *args, torch.cuda.current_stream(device).cuda_stream), name)
-        return
-    with torch.cuda.device(device):
-        check(fn(desc, *args, torch.cuda.current_stream(device).cuda_stream), name)
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(fn, name, index, *args):
+    """fn(*args, the device's current stream), with that device current."""
+    cuda = _torch().cuda
+    if index == cuda.current_device():
+        rc = fn(*args, _stream_of(index))
+    else:
+        with cuda.device(index):
+            rc = fn(*args, _stream_of(index))
+    if rc:
+        check(rc, name)
 
 
 def kv4_cache(n_pages: int, Hkv: int, page: int = 64, device=None):
@@ -132,25 +161,26 @@ def kv4_plan(n_new, seq_lens, block_table, free_pages, n_free, *, page: int, row
     update those in place, as a captured step wants).  A step that does not fit
     changes nothing and sets the device status."""
     torch = _torch()
-    dev = block_table.device
-    _need(block_table, "block_table", torch.int32, 2)
-    _ints(dev, n_new=n_new, seq_lens=seq_lens, free_pages=free_pages, n_free=n_free)
-    R = block_table.shape[0]
-    if n_new.shape[0] != R or seq_lens.shape[0] != R or n_free.shape[0] != 1:
-        raise ValueError("kv4_plan: n_new and seq_lens [R], block_table [R, max_pages], n_free [1]")
+    i32 = torch.int32
+    if not (block_table.dtype is i32 and block_table.is_cuda and block_table.dim() == 2 and block_table.is_contiguous()):
+        _refuse("block_table", block_table, i32, 2)
     if rows < 0:
         raise ValueError("rows must not be negative")
-    for name, t, n in (("seq_lens_out", seq_lens_out, R), ("n_free_out", n_free_out, 1)):
-        if t is not None:
-            _ints(dev, **{name: t})
-            if t.shape[0] != n:
-                raise ValueError(f"{name} must have {n} element(s)")
-    own = torch.empty((2 * R + 2 + 2 * rows,), dtype=torch.int32, device=dev).split([R + 1, rows, rows, R, 1])
-    out = (*own[:3], own[3] if seq_lens_out is None else seq_lens_out, own[4] if n_free_out is None else n_free_out)
-    d = Kv4Desc(n_pages=free_pages.shape[0], page=page, R=R, max_pages=block_table.shape[1], N=rows)
-    _call(_lib().sfa_kv4_plan, "sfa_kv4_plan", dev, d, n_new.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-          free_pages.data_ptr(), n_free.data_ptr(), *[t.data_ptr() for t in out])
-    return out
+    at = block_table.get_device()
+    R, width = block_table.shape
+    P = free_pages.shape[0]
+    own = torch.empty((2 * R + 2 + 2 * rows,), dtype=i32, device=block_table.device)
+    cu_q, slots, pos, lens, left = own.split([R + 1, rows, rows, R, 1])
+    if seq_lens_out is not None:
+        lens = seq_lens_out
+    if n_free_out is not None:
+        left = n_free_out
+    d = Kv4Desc(P, page, 0, 0, R, width, rows)
+    p = own.data_ptr()
+    _call(_lib().sfa_kv4_plan, "sfa_kv4_plan", at, d, _ints(at, R, n_new, "n_new"), _ints(at, R, seq_lens, "seq_lens"),
+          block_table.data_ptr(), _ints(at, P, free_pages, "free_pages"), _ints(at, 1, n_free, "n_free"), p, p + 4 * (R + 1),
+          p + 4 * (R + 1 + rows), _ints(at, R, lens, "seq_lens_out"), _ints(at, 1, left, "n_free_out"))
+    return cu_q, slots, pos, lens, left
 
 
 def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, kscale: float = 1.0,
@@ -159,62 +189,56 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
     (bf16 or fp32; rows may be slices of wider ones) at slots [N] (distinct;
     negative: skipped) and positions pos [N].  rope: a table of rope_table; else
     the one of rope_theta for the pool's rows (0: no rotation)."""
-    page = _page(cache)
-    dev, H = cache.device, cache.shape[1]
-    ks, vs = _rows(k, "k", H, dev), _rows(v, "v", H, dev, k.dtype)
-    _ints(dev, slots=slots, pos=pos)
-    N = k.shape[0]
-    if v.shape[0] != N or slots.shape[0] != N or pos.shape[0] != N:
-        raise ValueError("kv4_append: k and v [N, Hkv, 64], slots and pos [N]")
+    at, P, H, page = _pool(cache)
+    N, _, ks = _rows(k, "k", H, at)
+    n, _, vs = _rows(v, "v", H, at)
+    if n != N or v.dtype is not k.dtype:
+        raise ValueError(f"k and v must have the same rows and type, got {tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
     _scales(kscale, vscale)
-    rp, rT, keep = _rope(rope, rope_theta, min(cache.shape[0] * page, 1 << 24), dev)
-    d = Kv4Desc(cache.shape[0], page, H, 64, 0, 0, N, 0, _code(k.dtype), 0, ks, vs, kscale, vscale, rp, rT)
-    _call(_lib().sfa_kv4_append, "sfa_kv4_append", dev, d, k.data_ptr(), v.data_ptr(), cache.data_ptr(), slots.data_ptr(),
-          pos.data_ptr())
+    rp, rT = _rope(rope, rope_theta, min(P * page, 1 << 24), at)
+    d = Kv4Desc(P, page, H, 64, 0, 0, N, 0, _code(k.dtype), 0, ks, vs, kscale, vscale, rp, rT)
+    _call(_lib().sfa_kv4_append, "sfa_kv4_append", at, d, k.data_ptr(), v.data_ptr(), cache.data_ptr(),
+          _ints(at, N, slots, "slots"), _ints(at, N, pos, "pos"))
 
 
 def kv4_read(cache, slots, *, dtype=None, kscale: float = 1.0, vscale: float = 1.0, k=None, v=None):
     """Rows of the cache as numbers (sfa_kv4_read): k, v [N, Hkv, 64], the
     rotated keys and the values stored at slots [N] (negative: zeros)."""
     torch = _torch()
-    page = _page(cache)
-    dev, H = cache.device, cache.shape[1]
-    _ints(dev, slots=slots)
-    dtype = dtype or (k.dtype if k is not None else torch.bfloat16)
+    at, P, H, page = _pool(cache)
+    if dtype is None:
+        dtype = k.dtype if k is not None else torch.bfloat16
     code = _code(dtype)
     N = slots.shape[0]
     _scales(kscale, vscale)
+    shape = (N, H, 64)
     if k is None:
-        k = torch.empty((N, H, 64), dtype=dtype, device=dev)
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
     if v is None:
-        v = torch.empty((N, H, 64), dtype=dtype, device=dev)
-    for name, t in (("k", k), ("v", v)):
-        _need(t, name, dtype, 3, dev)
-        if t.shape != (N, H, 64):
-            raise ValueError(f"{name} must be {(N, H, 64)}, got {tuple(t.shape)}")
-    d = Kv4Desc(cache.shape[0], page, H, 64, 0, 0, N, 0, code, 0, 0, 0, kscale, vscale)
-    _call(_lib().sfa_kv4_read, "sfa_kv4_read", dev, d, cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr())
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
+    d = Kv4Desc(P, page, H, 64, 0, 0, N, 0, code, 0, 0, 0, kscale, vscale)
+    _call(_lib().sfa_kv4_read, "sfa_kv4_read", at, d, cache.data_ptr(), _ints(at, N, slots, "slots"),
+          _dense(at, shape, dtype, k, "k"), _dense(at, shape, dtype, v, "v"))
     return k, v
 
 
 def _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale):
-    page = _page(cache)
-    dev, H = cache.device, cache.shape[1]
-    qs = _rows(q, "q", 0, dev)
-    _need(block_table, "block_table", _torch().int32, 2, dev)
+    at, P, H, page = _pool(cache)
+    N, Hq, qs = _rows(q, "q", 0, at)
+    i32 = _torch().int32
+    if not (block_table.dtype is i32 and block_table.get_device() == at and block_table.dim() == 2 and block_table.is_contiguous()):
+        _refuse("block_table", block_table, i32, 2, at)
+    R, width = block_table.shape
     _scales(kscale, vscale)
-    rp, rT, keep = _rope(rope, rope_theta, min(block_table.shape[1] * page, 1 << 24), dev)
-    arr, nd = _offsets(tuple(dist)) if dist is not None else (None, 0)
-    d = Kv4Desc(cache.shape[0], page, H, 64, block_table.shape[0], block_table.shape[1], q.shape[0], q.shape[1],
-                _code(q.dtype), qs, 0, 0, kscale, vscale, rp, rT, C.cast(arr, C.c_void_p) if arr is not None else None, nd)
-    d._keep = (arr, keep)
-    return d
+    rp, rT = _rope(rope, rope_theta, min(width * page, 1 << 24), at)
+    arr, nd, _ = _offsets(tuple(dist)) if dist is not None else (None, 0, None)
+    return at, R, N, Hq, Kv4Desc(P, page, H, 64, R, width, N, Hq, _code(q.dtype), qs, 0, 0, kscale, vscale, rp, rT, arr, nd)
 
 
 def kv4_workspace_size(q, cache, block_table, *, dist=None) -> int:
     """Scratch bytes of kv4_attend for these shapes."""
     n = C.c_size_t(0)
-    d = _attend_desc(q, cache, block_table, dist, 0, None, 1.0, 1.0)
+    d = _attend_desc(q, cache, block_table, dist, 0, None, 1.0, 1.0)[-1]
     check(_lib().sfa_kv4_workspace_size(d, C.byref(n)), "sfa_kv4_workspace_size")
     return n.value
 
@@ -228,35 +252,29 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
     dist: offsets as for decode_int (0 required), None for every earlier row.
     Returns o [N, Hq, 64] and lse fp32 [N, Hq]."""
     torch = _torch()
-    d = _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale)
-    dev, (N, Hq, _) = cache.device, q.shape
-    _ints(dev, seq_lens=seq_lens)
-    R = block_table.shape[0]
-    if seq_lens.shape[0] != R:
-        raise ValueError("kv4_attend: seq_lens [R], block_table [R, max_pages]")
-    if cu_q is None:
-        if N != R:
-            raise ValueError(f"kv4_attend: without cu_q, q has a row for each of the {R} requests, got {N}")
-    else:
-        _ints(dev, cu_q=cu_q)
-        if cu_q.shape[0] != R + 1:
-            raise ValueError("kv4_attend: cu_q [R + 1]")
+    at, R, N, Hq, d = _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale)
+    if cu_q is None and N != R:
+        raise ValueError(f"without cu_q, q has one row for each of the {R} requests, got {N}")
+    shape = (N, Hq, 64)
     if o is None:
-        o = torch.empty((N, Hq, 64), dtype=q.dtype, device=dev)
-    else:
-        _need(o, "o", q.dtype, 3, dev)
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", torch.float32, 2, dev)
-    if o.shape != (N, Hq, 64) or lse.shape != (N, Hq):
-        raise ValueError(f"kv4_attend: o {(N, Hq, 64)} and lse {(N, Hq)}")
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
     L = _lib()
     n = C.c_size_t(0)
-    check(L.sfa_kv4_workspace_size(d, C.byref(n)), "sfa_kv4_workspace_size")
-    if n.value and (ws is None or ws.numel() < n.value):
-        ws = torch.empty((n.value,), dtype=torch.uint8, device=dev)
-    _call(L.sfa_kv4_attend, "sfa_kv4_attend", dev, d, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
-          seq_lens.data_ptr(), cu_q.data_ptr() if cu_q is not None else None, o.data_ptr(), lse.data_ptr(),
-          ws.data_ptr() if n.value else None, n.value)
+    rc = L.sfa_kv4_workspace_size(d, C.byref(n))
+    if rc:
+        check(rc, "sfa_kv4_workspace_size")
+    n = n.value
+    if n == 0:
+        w = None
+    else:
+        if ws is None or ws.numel() * ws.element_size() < n:
+            ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
+        elif ws.get_device() != at or not ws.is_contiguous():
+            _refuse("ws", ws, ws.dtype, ws.dim(), at)
+        w = ws.data_ptr()
+    _call(L.sfa_kv4_attend, "sfa_kv4_attend", at, d, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+          _ints(at, R, seq_lens, "seq_lens"), None if cu_q is None else _ints(at, R + 1, cu_q, "cu_q"),
+          _dense(at, shape, q.dtype, o, "o"), _dense(at, (N, Hq), torch.float32, lse, "lse"), w, n)
     return o, lse
