@@ -109,10 +109,10 @@ __device__ __forceinline__ void key_products(const QFrag<NT>& q, uint2 ka, uint2
 }
 
 // Values of keys 2t, 2t + 1, 2t + 8, 2t + 9: codes of dims 8g .. 8g + 7 and the
-// scales of their block (bytes, first key first).  o[nt][mt] = accumulators of
+// scales of their block (bytes of two keys each, the first in the low one).  o[nt][mt] = accumulators of
 // dims (8g + 2 mt, 8g + 2 mt + 1) x heads (2t, 2t + 1).
 template <int NT, bool EXACT>
-__device__ __forceinline__ void value_products(const uint32_t* w, uint32_t scales, const float (*p)[4], float (*o)[4][4]) {
+__device__ __forceinline__ void value_products(const uint32_t* w, uint32_t sab, uint32_t scd, const float (*p)[4], float (*o)[4][4]) {
   uint32_t b0[NT], b1[NT], l0[NT], l1[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -125,7 +125,7 @@ __device__ __forceinline__ void value_products(const uint32_t* w, uint32_t scale
       l1[nt] = movmatrix_t(pack_f16(p[nt][2] - r1.x, p[nt][3] - r1.y));
     }
   }
-  const uint32_t fab = e4m3x2_f16x2(scales & 0xffffu), fcd = e4m3x2_f16x2(scales >> 16);
+  const uint32_t fab = e4m3x2_f16x2(sab), fcd = e4m3x2_f16x2(scd);
   // bytes that hold one dim of two keys: even dims, then odd dims
   const uint32_t lo4 = 0x0f0f0f0fu;
   uint32_t x[4][4];
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps)
       float s[NT][4];
       key_products(q, ka, kb, sa, sb, s);
       softmax_step(q, s, ia >= 0, ib >= 0, acc.m, acc.l, acc.o);
-      value_products<NT, kExact>(w, vs, s, acc.o);
+      value_products<NT, kExact>(w, vs & 0xffffu, vs >> 16, s, acc.o);
     }
   }
   acc.close();
@@ -462,6 +462,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // The warp's ring of tiles: its copies run ahead of the tiles it consumes.
+// Lanes 3p .. 3p + 2 look after page p of a tile: key codes, value codes, scales.
 struct Ring {
   uint32_t data, bar;        // shared addresses of the slots and of their barriers
   volatile int* pages;       // per slot: which of the tile's pages are there
@@ -469,16 +470,27 @@ struct Ring {
   int ti;
   bool more;
   int pid[kStages], meta[kStages];  // tiles whose ids have been read, nearest first; meta < 0: none
-  int issued, used, skip;
+  int slot_in, issued, used, skip;
+  int rows, page0, dst, bytes;      // rows of a page in a tile; this lane's page (its first key), place and size of its copy
+  int64_t src, block;               // its place in a (page, head) block; a block's size
 
+  __device__ __forceinline__ void lanes(const Kv4Args& a, int lane) {
+    const int S = 1 << a.lgS, p = lane / 3, part = lane - 3 * p;
+    rows = min(S, kTile);
+    page0 = p * rows;
+    bytes = part == 2 ? 8 * rows : 32 * rows;
+    src = part == 2 ? 64 * S : 32 * S * part;
+    dst = (part == 2 ? 64 * kTile : 32 * kTile * part) + p * bytes;
+    block = kKv4Row * S;
+  }
   __device__ __forceinline__ void skip_empty(const Kv4Args& a, const StreamArgs& s, int warp) {
     while (more && ti >= at.te) {
       more = at.next(a, s);
       ti = at.tb + warp;
     }
   }
-  // read the page ids of the next tile: lanes 3p .. 3p + 2 for page p of it
-  __device__ __forceinline__ void read_ids(const Kv4Args& a, const StreamArgs& s, int warp, int lane) {
+  // read the page ids of the next tile
+  __device__ __forceinline__ void read_ids(const Kv4Args& a, const StreamArgs& s, int warp) {
 #pragma unroll
     for (int k = 0; k + 1 < kStages; ++k) {
       pid[k] = pid[k + 1];
@@ -486,158 +498,141 @@ struct Ring {
     }
     meta[kStages - 1] = -1;
     if (!more) return;
-    const int j = ti * kTile, last = at.it.plast();
-    const int rows = min(1 << a.lgS, kTile);
-    const int n = min(kTile / rows, (last - j) / rows + 1);
-    pid[kStages - 1] = lane < 3 * n ? a.table[(int64_t)at.it.r * a.max_pages + ((j + lane / 3 * rows) >> a.lgS)] : -1;
-    meta[kStages - 1] = n | ((j >> a.lgS << a.lgS) == j ? 0 : 8) | at.h << 4;
+    const int j = ti * kTile + page0;
+    const bool mine = page0 < kTile && j <= at.it.plast();
+    pid[kStages - 1] = mine ? a.table[(int64_t)at.it.r * a.max_pages + (j >> a.lgS)] : -2;  // -2: no page of the tile
+    meta[kStages - 1] = at.h << 1 | (a.lgS == 7 ? ti & 1 : 0);  // the KV head, which half of a long page
     ti += kStreamWarps;
-    skip_empty(a, s, warp);
+    if (ti >= at.te) skip_empty(a, s, warp);
   }
   // start the copies of the nearest tile whose ids have been read
   __device__ __forceinline__ void issue(const Kv4Args& a, int lane) {
     if (meta[0] < 0) return;
-    const int slot = issued % kStages, n = meta[0] & 7, h = meta[0] >> 4;
-    ++issued;
-    const bool mine = lane < 3 * n, ok = mine && pid[0] >= 0 && pid[0] < a.n_pages;
-    if (mine && !ok) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+    const int slot = slot_in;
+    slot_in = slot + 1 == kStages ? 0 : slot + 1;
+    const bool ok = pid[0] >= 0 && pid[0] < a.n_pages;
+    if (!ok && pid[0] != -2) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
     const uint32_t there = __ballot_sync(0xffffffffu, ok) & 0x249u;  // bit 3p: page p
-    const int S = 1 << a.lgS, rows = min(S, kTile);
-    const uint32_t b = bar + 8 * slot, d = data + slot * kTileBytes;
-    if (issued - 1 == skip) return;
+    const uint32_t b = bar + 8 * slot;
+    if (issued++ == skip) return;
     if (lane == 0) {
       pages[slot] = (int)((there & 1) | (there >> 2 & 2) | (there >> 4 & 4) | (there >> 6 & 8));
       mbar_expect_tx(b, __popc(there) * rows * kKv4Row);
     }
     __syncwarp();
-    if (ok) {
-      const int p = lane / 3, part = lane - 3 * p, row = meta[0] & 8 ? kTile : 0;
-      const uint8_t* src = a.cache + ((int64_t)pid[0] * a.Hkv + h) * (kKv4Row * S);
-      if (part == 2)
-        bulk_load(d + 64 * kTile + 8 * p * rows, src + 64 * S + 8 * row, 8 * rows, b);
-      else
-        bulk_load(d + 32 * kTile * part + 32 * p * rows, src + 32 * S * part + 32 * row, 32 * rows, b);
-    }
+    if (ok)  // bytes / rows of a row, times 64 rows, into the second half of a long page
+      bulk_load(data + slot * kTileBytes + dst, a.cache + ((int64_t)pid[0] * a.Hkv + (meta[0] >> 1)) * block + src + (meta[0] & 1 ? bytes : 0),
+                bytes, b);
   }
 };
-
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8u(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(addr));
-  return v;
-}
 
 // Row r of a 16-key tile is key r ^ (r >> 2 & 1): the rows that lanes of one
 // shared-memory pass read then lie in different banks, for keys (rows g) and
 // values (rows 2t, 2t + 1) alike.
 __device__ __forceinline__ int key_of(int r) { return r ^ ((r >> 2) & 1); }
 
-// One tile of 64 keys from key j0 on, in shared memory at T.
-template <int NT, bool EXACT>
-__device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& sa, const Item& it, const QFrag<NT>& q, Acc<NT>& acc,
-                                            uint32_t T, int j0, int pages, int lane) {
-  constexpr int GB = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // 16-key groups whose logits are held at once
+// 16 GB keys (from key k0 of a tile that starts at key j0, its data at T) added
+// to the columns' sums.  MASKED: some column may not attend some key.
+template <int NT, int GB, bool EXACT, bool MASKED>
+__device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& sa, const Item& it, const QFrag<NT>& q, Acc<NT>& acc,
+                                            const uint8_t* T, int j0, int k0, int pages, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int rows = min(1 << a.lgS, kTile), lgr = min(a.lgS, 6);
-  const bool full = pages == (1 << (kTile / rows)) - 1 && j0 + kTile - 1 <= it.pfirst && j0 >= it.plast() - sa.W;
+  const int lgr = min(a.lgS, 6);
+  const uint8_t* const kt = T + 32 * (k0 + key_of(g)) + 8 * t;
+  const uint8_t* const st = T + 64 * kTile + 8 * (k0 + key_of(g)) + t;
   // does column 8 nt + 2 t + e attend key k of the tile?
   auto attends = [&](int nt, int e, int k) {
     const int p = it.pfirst + ((8 * nt + 2 * t + e) >> a.lgG), j = j0 + k;
     return j <= p && j >= p - sa.W && (pages >> (k >> lgr) & 1);
   };
+  float s[GB][NT][4];
 #pragma unroll
-  for (int gb = 0; gb < 4; gb += GB) {
-    float s[GB][NT][4];
-#pragma unroll
-    for (int i = 0; i < GB; ++i) {
-      const int ka = 16 * (gb + i) + key_of(g), kb = ka + 8;
-      key_products(q, lds64(T + 32 * ka + 8 * t), lds64(T + 32 * kb + 8 * t), lds8u(T + 64 * kTile + 8 * ka + t),
-                   lds8u(T + 64 * kTile + 8 * kb + t), s[i]);
-      if (!full)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (!attends(nt, e, ka)) s[i][nt][e] = -INFINITY;
-            if (!attends(nt, e, kb)) s[i][nt][2 + e] = -INFINITY;
-          }
-    }
-    // the statistics move only when a logit passes them by more than kLag
-    float top[NT][2];
-    bool passes = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
-#pragma unroll
-        for (int i = 1; i < GB; ++i) x = fmaxf(x, fmaxf(s[i][nt][e], s[i][nt][2 + e]));
-        top[nt][e] = x * q.c[nt][e];
-        passes |= top[nt][e] > acc.m[nt][e] + kLag;
-      }
-    if (__any_sync(0xffffffffu, passes))
+  for (int i = 0; i < GB; ++i) {
+    key_products(q, *reinterpret_cast<const uint2*>(kt + 512 * i), *reinterpret_cast<const uint2*>(kt + 512 * i + 256),
+                 (uint32_t)st[128 * i], (uint32_t)st[128 * i + 64], s[i]);
+    if (MASKED) {
+      const int ka = k0 + 16 * i + key_of(g);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = top[nt][e];
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          if (x > acc.m[nt][e]) {
-            const float corr = ex2(acc.m[nt][e] - x);  // 0 on the first keys
-            acc.m[nt][e] = x;
-            acc.l[nt][e] *= corr;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-              acc.o[nt][mt][e] *= corr;
-              acc.o[nt][mt][2 + e] *= corr;
-            }
-          }
+          if (!attends(nt, e, ka)) s[i][nt][e] = -INFINITY;
+          if (!attends(nt, e, ka + 8)) s[i][nt][2 + e] = -INFINITY;
         }
+    }
+  }
+  // the statistics move only when a logit passes them by more than kLag
+  float top[NT][2];
+  bool passes = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+      for (int i = 1; i < GB; ++i) x = fmaxf(x, fmaxf(s[i][nt][e], s[i][nt][2 + e]));
+      top[nt][e] = x * q.c[nt][e];
+      passes |= top[nt][e] > acc.m[nt][e] + kLag;
+    }
+  if (__any_sync(0xffffffffu, passes))
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float off = acc.m[nt][e] == -INFINITY ? 0.0f : kPShift - acc.m[nt][e];
+        float x = top[nt][e];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        if (x > acc.m[nt][e]) {
+          const float corr = ex2(acc.m[nt][e] - x);  // 0 on the first keys
+          acc.m[nt][e] = x;
+          acc.l[nt][e] *= corr;
 #pragma unroll
-        for (int i = 0; i < GB; ++i) {
-          s[i][nt][e] = ex2(fmaf(s[i][nt][e], q.c[nt][e], off));
-          s[i][nt][2 + e] = ex2(fmaf(s[i][nt][2 + e], q.c[nt][e], off));
-          acc.l[nt][e] += s[i][nt][e] + s[i][nt][2 + e];
+          for (int mt = 0; mt < 4; ++mt) {
+            acc.o[nt][mt][e] *= corr;
+            acc.o[nt][mt][2 + e] *= corr;
+          }
         }
       }
 #pragma unroll
-    for (int i = 0; i < GB; ++i) {
-      uint32_t w[4], vs[4];
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float off = acc.m[nt][e] == -INFINITY ? 0.0f : kPShift - acc.m[nt][e];
+#pragma unroll
+      for (int i = 0; i < GB; ++i) {
+        s[i][nt][e] = ex2(fmaf(s[i][nt][e], q.c[nt][e], off));
+        s[i][nt][2 + e] = ex2(fmaf(s[i][nt][2 + e], q.c[nt][e], off));
+        acc.l[nt][e] += s[i][nt][e] + s[i][nt][2 + e];
+      }
+    }
+  // rows 2t and 2t + 1 of a 16-key tile are keys kv and kv ^ 1
+  const int kv = key_of(2 * t), kw = kv ^ 1;
+  const uint8_t* const va = T + 32 * kTile + 32 * (k0 + kv) + 4 * g;
+  const uint8_t* const vb = T + 32 * kTile + 32 * (k0 + kw) + 4 * g;
+  const uint8_t* const sv = T + 64 * kTile + 8 * (k0 + kv) + 4 + (g >> 1);
+  const uint8_t* const sw = T + 64 * kTile + 8 * (k0 + kw) + 4 + (g >> 1);
+#pragma unroll
+  for (int i = 0; i < GB; ++i) {
+    const uint32_t w[4] = {*reinterpret_cast<const uint32_t*>(va + 512 * i), *reinterpret_cast<const uint32_t*>(vb + 512 * i),
+                           *reinterpret_cast<const uint32_t*>(va + 512 * i + 256), *reinterpret_cast<const uint32_t*>(vb + 512 * i + 256)};
+    uint32_t vs[4] = {sv[128 * i], sw[128 * i], sv[128 * i + 64], sw[128 * i + 64]};
+    if (MASKED) {
       bool nan = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = 16 * (gb + i) + key_of(2 * t + (e & 1)) + 8 * (e >> 1);
-        w[e] = lds32(T + 32 * kTile + 32 * k + 4 * g);
-        vs[e] = lds8u(T + 64 * kTile + 8 * k + 4 + (g >> 1));
-        if (!full) {  // rows that are not stored hold anything, a NaN scale perhaps; 0 * NaN must not reach the sums
-          if (j0 + k > it.plast() || !(pages >> (k >> lgr) & 1)) vs[e] = 0;
-          nan |= (vs[e] & 127u) == 127u;
-        }
+      for (int e = 0; e < 4; ++e) {  // rows that are not stored hold anything, a NaN scale perhaps; 0 * NaN must not reach the sums
+        const int k = k0 + 16 * i + (e & 1 ? kw : kv) + 8 * (e >> 1);
+        if (j0 + k > it.plast() || !(pages >> (k >> lgr) & 1)) vs[e] = 0;
+        nan |= (vs[e] & 127u) == 127u;
       }
-      if (!full && __any_sync(0xffffffffu, nan)) {
+      if (__any_sync(0xffffffffu, nan)) {
         // a stored NaN reaches the columns that attend it, and no others
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if ((vs[e] & 127u) == 127u) vs[e] = 0;
-        for (int k = 16 * (gb + i); k < 16 * (gb + i) + 16; ++k)
-          if ((lds8u(T + 64 * kTile + 8 * k + 4 + (g >> 1)) & 127u) == 127u)
+#pragma unroll 1
+        for (int k = k0 + 16 * i; k < k0 + 16 * i + 16; ++k)
+          if ((T[64 * kTile + 8 * k + 4 + (g >> 1)] & 127u) == 127u)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -646,8 +641,25 @@ __device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& 
 #pragma unroll
                   for (int mt = 0; mt < 4; ++mt) acc.o[nt][mt][e] = acc.o[nt][mt][2 + e] = __int_as_float(0x7fffffff);
       }
-      value_products<NT, EXACT>(w, vs[0] | vs[1] << 8 | vs[2] << 16 | vs[3] << 24, s[i], acc.o);
     }
+    value_products<NT, EXACT>(w, vs[0] | vs[1] << 8, vs[2] | vs[3] << 8, s[i], acc.o);
+  }
+}
+
+// One tile.  The loop over its keys stays a loop: unrolled, the code of the
+// twelve warps of an SM no longer fits the instruction cache (ncu: 1.9 of 6.7
+// stalled warps an issue waited for instructions).
+template <int NT, bool EXACT>
+__device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& sa, const Item& it, const QFrag<NT>& q, Acc<NT>& acc,
+                                            const uint8_t* T, int j0, int pages, int all_pages, int lane) {
+  constexpr int GB = NT == 1 ? 2 : 1;  // 16-key groups whose logits are held at once
+  const bool full = pages == all_pages && j0 + kTile - 1 <= it.pfirst && j0 >= it.plast() - sa.W;
+  if (full) {
+#pragma unroll 1
+    for (int k = 0; k < kTile; k += 16 * GB) stream_keys<NT, GB, EXACT, false>(a, sa, it, q, acc, T, j0, k, pages, lane);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < kTile; k += 16) stream_keys<NT, 1, EXACT, true>(a, sa, it, q, acc, T, j0, k, pages, lane);
   }
 }
 
@@ -719,21 +731,23 @@ __global__ void __launch_bounds__(32 * kStreamWarps, NT == 1 ? 3 : 2) kv4_stream
   ring.at = cur;
   ring.ti = cur.tb + warp;
   ring.more = true;
-  ring.issued = ring.used = 0;
+  ring.slot_in = ring.issued = ring.used = 0;
+  ring.lanes(a, lane);
   ring.skip = first == 0 && warp == 0 ? a.debug_skip : -1;
   ring.skip_empty(a, sa, warp);
 #pragma unroll
-  for (int k = 0; k < kStages; ++k) ring.read_ids(a, sa, warp, lane);
+  for (int k = 0; k < kStages; ++k) ring.read_ids(a, sa, warp);
 #pragma unroll
   for (int k = 0; k < kStages; ++k) {
     ring.issue(a, lane);
-    ring.read_ids(a, sa, warp, lane);
+    ring.read_ids(a, sa, warp);
   }
 
   const int G = 1 << a.lgG;
   QFrag<NT> q;
   Acc<NT> acc;
-  int qx = -1, qh = -1;
+  int qx = -1, qh = -1, slot = 0, phase = 0;
+  const int all_pages = (1 << (kTile / ring.rows)) - 1;
   bool dead = false;  // a wait ran out: no more copies, no more work
   do {
     const int ncol = cur.it.nrows << a.lgG;
@@ -745,18 +759,22 @@ __global__ void __launch_bounds__(32 * kStreamWarps, NT == 1 ? 3 : 2) kv4_stream
     }
     acc.clear();
     for (int ti = cur.tb + warp; ti < cur.te; ti += kStreamWarps) {
-      const int slot = ring.used % kStages, phase = ring.used / kStages & 1;
       if (!dead && !mbar_wait_bounded(ring.bar + 8 * slot, phase, a.wait_cycles)) {
         record_status(a.status, SFA_ERR_TIMEOUT);
         dead = true;
       }
       dead = __any_sync(0xffffffffu, dead);
       if (dead) continue;
+      stream_tile<NT, kExact>(a, sa, cur.it, q, acc, smem + (warp * kStages + slot) * kTileBytes, ti * kTile, ring.pages[slot], all_pages,
+                              lane);
       ++ring.used;
-      stream_tile<NT, kExact>(a, sa, cur.it, q, acc, ring.data + slot * kTileBytes, ti * kTile, ring.pages[slot], lane);
+      if (++slot == kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
       __syncwarp();
       ring.issue(a, lane);
-      ring.read_ids(a, sa, warp, lane);
+      ring.read_ids(a, sa, warp);
     }
     acc.close();
     if (g == 0)
