@@ -354,7 +354,8 @@ int sfa_kv4_read(const sfa_kv4_desc* d, const void* cache, const int32_t* slots,
  *   lse      fp32 [N, Hq], natural log of the softmax denominator, or NULL
  * A query at position p attends the rows j <= p (d->dist NULL), or p - s for
  * every s <= p of d->dist (which holds 0 and nothing negative); logits are
- * q . k / 8 after the rotation of q at p by d->rope.  ws: sfa_kv4_workspace_size
+ * q . k / 8 after the rotation of q at p by d->rope.  (N + R) * Hkv * max_pages
+ * * page beyond 2^37 may be refused (SFA_ERR_UNSUPPORTED).  ws: sfa_kv4_workspace_size
  * bytes (NULL when that is 0), scratch of this call alone. */
 int sfa_kv4_workspace_size(const sfa_kv4_desc* d, size_t* bytes);
 int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,

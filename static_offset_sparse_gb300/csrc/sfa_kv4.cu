@@ -407,7 +407,7 @@ static int check_attend(const sfa_kv4_desc* d, Plan* p, Kv4Args* a) {
   a->kscale = d->kscale;
   a->vscale = d->vscale;
   a->q_stride = d->q_stride;
-  return SFA_OK;
+  return kv4_attend_fits(*a, *p, true) && (d->N != d->R || kv4_attend_fits(*a, *p, false)) ? SFA_OK : SFA_ERR_UNSUPPORTED;
 }
 
 }  // namespace sfa

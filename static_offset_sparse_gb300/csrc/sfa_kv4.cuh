@@ -108,7 +108,9 @@ __device__ __forceinline__ bool kv4_row(const Kv4Args& a, int n, int lane, int& 
   return n < end;
 }
 
-// sfa_kv4_attend.cu: scratch bytes of an attend call (ragged: with cu_q), and the call.
+// sfa_kv4_attend.cu: whether the tiles of an attend call (ragged: with cu_q)
+// can be counted in 31 bits, its scratch bytes, and the call.
+bool kv4_attend_fits(const Kv4Args& a, const Plan& p, bool ragged);
 size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, bool ragged);
 int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void* stream);
 

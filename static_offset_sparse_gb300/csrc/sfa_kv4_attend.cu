@@ -358,24 +358,26 @@ static cudaError_t gather(const Kv4Args& a, const Plan& p, int warps, cudaStream
 // ---------------------------------------------------------------- stream
 
 // The whole prefix, or a wide window: a request's pages stream through shared
-// memory.  A warp owns a ring of kStages tiles of 64 keys, filled by
-// asynchronous bulk copies (three a page: key codes, value codes, scales) that
-// one lane each issues; the page ids are read kStages tiles earlier still.
+// memory.  A CTA is four warps that compute and one that copies: it reads a
+// chunk's page ids, waits for a free slot of the ring (tiles of 64 keys) and
+// starts one asynchronous bulk copy a page (64-row pages, whose block is a tile
+// as it stands) or three (key codes, value codes, scales).
 //
 // Work: an item is up to rows_per query rows of one request (a decode step: one
 // row), its columns rows x heads of one KV head; its keys are cut into chunks
 // of chunk_tiles tiles at absolute places, so what is added to what depends on
-// the call's shapes and the row's own length, not on other requests.  All
-// chunks, in order, are shared out evenly over one wave of CTAs: each CTA adds
-// up the items' chunk counts (from the lengths, in one block-wide scan), takes
-// its part and walks it, the copies running on across chunks and items.  The
-// four warps take every fourth tile of a chunk and meet in shared memory at its
-// end.  Chunks of a longer item go to the workspace, joined by a second kernel.
-constexpr int kStreamWarps = 4, kStages = 3, kTile = 64, kTileBytes = kTile * kKv4Row;
+// the call's shapes and the row's own length, not on other requests.  The tiles
+// of all chunks, in order, are shared out evenly over one wave of CTAs, whole
+// chunks at a time: each CTA adds up the items' tiles (from the lengths, in one
+// block-wide scan), takes its part and walks it, the copies running on across
+// chunks and items.  The four warps take every fourth tile of a chunk and meet
+// in shared memory at its end.  Chunks of a longer item go to the workspace,
+// joined by a second kernel.
+constexpr int kStreamWarps = 4, kSlots = 8, kTile = 64, kTileBytes = kTile * kKv4Row;
 constexpr int kSMs = 152;
 
 struct StreamArgs {
-  int32_t items, lg_rows, chunk_tiles, max_chunks, W;
+  int32_t items, lg_rows, chunk_tiles, lg_chunk, max_chunks, W;
   float* part_o;   // [item][KV head][chunk][column][64]
   float2* part_ml; // [item][KV head][chunk][column] (m, l)
 };
@@ -423,30 +425,33 @@ __device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, i
     it.nch = 1;
     return it;
   }
-  const int ck = s.chunk_tiles * kTile;
-  it.c0 = max(0, it.pfirst - s.W) / ck;
-  it.nch = it.plast() / ck - it.c0 + 1;
+  const int lg = s.lg_chunk + 6;  // 64 keys a tile
+  it.c0 = max(0, it.pfirst - s.W) >> lg;
+  it.nch = (it.plast() >> lg) - it.c0 + 1;
   return it;
 }
 
-// A place in the CTA's run of chunks, and the tiles of the chunk there.
+// A place in the CTA's run of chunks: chunk c of (item x, KV head h), its tiles
+// tb .. te - 1, and the run's weight (tiles; 1 for a chunk of none) up to here.
 struct Cursor {
   Item it;
-  int x, h, c, left;  // left: chunks of the run from here on
-  int tb, te;
+  int x, h, c, tb, te;
+  int at, end;
   __device__ __forceinline__ void tiles(const StreamArgs& s) {
     tb = max(c * s.chunk_tiles, max(0, it.pfirst - s.W) / kTile);
     te = it.plast() < 0 ? tb : min((c + 1) * s.chunk_tiles, it.plast() / kTile + 1);
   }
   // the next chunk; false at the end of the run
   __device__ __forceinline__ bool next(const Kv4Args& a, const StreamArgs& s) {
-    if (--left <= 0) return false;
+    at += max(1, te - tb);
+    if (at >= end) return false;
     if (++c == it.c0 + it.nch) {
       if (++h == a.Hkv) {
         h = 0;
-        do
+        do {
+          if (x + 1 >= s.items) return false;
           it = item_at(a, s, ++x);
-        while (it.nch == 0 && x + 1 < s.items);
+        } while (it.nch == 0);
       }
       c = it.c0;
     }
@@ -455,76 +460,76 @@ struct Cursor {
   }
 };
 
+// Tiles of one KV head of an item (1 for an empty one, 0 for none).
+__device__ __forceinline__ int item_tiles(const StreamArgs& s, const Item& it) {
+  return it.nch == 0 ? 0 : it.plast() < 0 ? 1 : it.plast() / kTile + 1 - max(0, it.pfirst - s.W) / kTile;
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
                : "memory");
 }
 
-// The warp's ring of tiles: its copies run ahead of the tiles it consumes.
-// Lanes 3p .. 3p + 2 look after page p of a tile: key codes, value codes, scales.
-struct Ring {
-  uint32_t data, bar;        // shared addresses of the slots and of their barriers
-  volatile int* pages;       // per slot: which of the tile's pages are there
-  Cursor at;                 // the tile whose page ids are read next
-  int ti;
-  bool more;
-  int pid[kStages], meta[kStages];  // tiles whose ids have been read, nearest first; meta < 0: none
-  int slot_in, issued, used, skip;
-  int rows, page0, dst, bytes;      // rows of a page in a tile; this lane's page (its first key), place and size of its copy
-  int64_t src, block;               // its place in a (page, head) block; a block's size
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
 
-  __device__ __forceinline__ void lanes(const Kv4Args& a, int lane) {
-    const int S = 1 << a.lgS, p = lane / 3, part = lane - 3 * p;
-    rows = min(S, kTile);
-    page0 = p * rows;
-    bytes = part == 2 ? 8 * rows : 32 * rows;
-    src = part == 2 ? 64 * S : 32 * S * part;
-    dst = (part == 2 ? 64 * kTile : 32 * kTile * part) + p * bytes;
-    block = kKv4Row * S;
-  }
-  __device__ __forceinline__ void skip_empty(const Kv4Args& a, const StreamArgs& s, int warp) {
-    while (more && ti >= at.te) {
-      more = at.next(a, s);
-      ti = at.tb + warp;
+// The copying warp: every tile of the CTA's run, in order, into slot n mod
+// kSlots as soon as tile n - kSlots has been read.
+__device__ __forceinline__ void copy_run(const Kv4Args& a, const StreamArgs& sa, Cursor cur, uint32_t ring, uint32_t full, uint32_t empty,
+                                         volatile int* pages, int skip, int lane) {
+  const int S = 1 << a.lgS, rows = min(S, kTile), np = kTile / rows, lgnp = __ffs(np) - 1, batch = 32 >> lgnp;
+  const int64_t block = kKv4Row * S;
+  int n = 0;
+  bool dead = false;
+  do {
+    const int32_t* trow = a.table + (int64_t)cur.it.r * a.max_pages;
+    const uint8_t* head = a.cache + cur.h * block;
+    const int last = cur.it.plast();
+    for (int t0 = cur.tb; t0 < cur.te && !dead; t0 += batch) {
+      // lane: page `lane mod np` of tile t0 + lane / np
+      const int j = (t0 + (lane >> lgnp)) * kTile + (lane & (np - 1)) * rows;
+      const bool mine = t0 + (lane >> lgnp) < cur.te && j <= last;
+      const int pid = mine ? trow[j >> a.lgS] : 0;
+      const bool ok = mine && pid >= 0 && pid < a.n_pages;
+      if (mine && !ok) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+      const uint32_t there = __ballot_sync(0xffffffffu, ok);
+      const uint8_t* src = head + pid * (block * a.Hkv);
+      const int k1 = min(batch, cur.te - t0);
+      for (int k = 0; k < k1; ++k, ++n) {
+        const int slot = n % kSlots;
+        if (n >= kSlots && !mbar_wait_bounded(empty + 8 * slot, (n / kSlots - 1) & 1, a.wait_cycles)) {
+          record_status(a.status, SFA_ERR_TIMEOUT);
+          dead = true;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+        if (n == skip) continue;
+        const uint32_t b = full + 8 * slot, d = ring + slot * kTileBytes;
+        const uint32_t here = (there >> (k << lgnp)) & ((1u << np) - 1);
+        if (lane == 0) {
+          pages[slot] = (int)here;
+          mbar_expect_tx(b, __popc(here) * rows * kKv4Row);
+        }
+        __syncwarp();
+        if (ok && lane >> lgnp == k) {
+          const int p = lane & (np - 1), row = j & (S - 1);
+          if (S == kTile) {
+            bulk_load(d, src, kTileBytes, b);
+          } else {
+            bulk_load(d + 32 * p * rows, src + 32 * row, 32 * rows, b);
+            bulk_load(d + 32 * kTile + 32 * p * rows, src + 32 * S + 32 * row, 32 * rows, b);
+            bulk_load(d + 64 * kTile + 8 * p * rows, src + 64 * S + 8 * row, 8 * rows, b);
+          }
+        }
+      }
     }
-  }
-  // read the page ids of the next tile
-  __device__ __forceinline__ void read_ids(const Kv4Args& a, const StreamArgs& s, int warp) {
-#pragma unroll
-    for (int k = 0; k + 1 < kStages; ++k) {
-      pid[k] = pid[k + 1];
-      meta[k] = meta[k + 1];
-    }
-    meta[kStages - 1] = -1;
-    if (!more) return;
-    const int j = ti * kTile + page0;
-    const bool mine = page0 < kTile && j <= at.it.plast();
-    pid[kStages - 1] = mine ? a.table[(int64_t)at.it.r * a.max_pages + (j >> a.lgS)] : -2;  // -2: no page of the tile
-    meta[kStages - 1] = at.h << 1 | (a.lgS == 7 ? ti & 1 : 0);  // the KV head, which half of a long page
-    ti += kStreamWarps;
-    if (ti >= at.te) skip_empty(a, s, warp);
-  }
-  // start the copies of the nearest tile whose ids have been read
-  __device__ __forceinline__ void issue(const Kv4Args& a, int lane) {
-    if (meta[0] < 0) return;
-    const int slot = slot_in;
-    slot_in = slot + 1 == kStages ? 0 : slot + 1;
-    const bool ok = pid[0] >= 0 && pid[0] < a.n_pages;
-    if (!ok && pid[0] != -2) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
-    const uint32_t there = __ballot_sync(0xffffffffu, ok) & 0x249u;  // bit 3p: page p
-    const uint32_t b = bar + 8 * slot;
-    if (issued++ == skip) return;
-    if (lane == 0) {
-      pages[slot] = (int)((there & 1) | (there >> 2 & 2) | (there >> 4 & 4) | (there >> 6 & 8));
-      mbar_expect_tx(b, __popc(there) * rows * kKv4Row);
-    }
-    __syncwarp();
-    if (ok)  // bytes / rows of a row, times 64 rows, into the second half of a long page
-      bulk_load(data + slot * kTileBytes + dst, a.cache + ((int64_t)pid[0] * a.Hkv + (meta[0] >> 1)) * block + src + (meta[0] & 1 ? bytes : 0),
-                bytes, b);
-  }
-};
+  } while (!dead && cur.next(a, sa));
+  // the copies end before the CTA does, whatever became of their readers
+  for (int i = max(0, n - kSlots); i < n; ++i)
+    if (i != skip && !mbar_wait_bounded(full + 8 * (i % kSlots), i / kSlots & 1, a.wait_cycles)) record_status(a.status, SFA_ERR_TIMEOUT);
+}
 
 // Row r of a 16-key tile is key r ^ (r >> 2 & 1): the rows that lanes of one
 // shared-memory pass read then lie in different banks, for keys (rows g) and
@@ -646,9 +651,10 @@ __device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& 
   }
 }
 
-// One tile.  The loop over its keys stays a loop: unrolled, the code of the
-// twelve warps of an SM no longer fits the instruction cache (ncu: 1.9 of 6.7
-// stalled warps an issue waited for instructions).
+// One tile.  With one column tile 32 keys' logits are held at once: 204 clocks
+// an SM a tile with its data at hand (197 is what the memory takes to bring
+// one); 64 at once take 183, but then 16 warps' registers do not hold the rest.
+// Masked tiles, and wider ones, take 16 keys at a time.
 template <int NT, bool EXACT>
 __device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& sa, const Item& it, const QFrag<NT>& q, Acc<NT>& acc,
                                             const uint8_t* T, int j0, int pages, int all_pages, int lane) {
@@ -663,92 +669,103 @@ __device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& 
   }
 }
 
+// CTAs an SM of the variant with NT column tiles.
+constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : NT == 2 ? 2 : 1; }
+
 template <typename TIO, int NT>
-__global__ void __launch_bounds__(32 * kStreamWarps, NT == 1 ? 3 : 2) kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
+__global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
   constexpr bool kExact = sizeof(TIO) == 4;
-  constexpr int NC = 8 * NT;
+  constexpr int NC = 8 * NT, kThr = 32 * (kStreamWarps + 1);
   extern __shared__ __align__(128) uint8_t smem[];
-  float* const po = reinterpret_cast<float*>(smem + kStreamWarps * kStages * kTileBytes);  // [warp][NC][66]
-  float2* const ml = reinterpret_cast<float2*>(po + kStreamWarps * NC * 66);               // [warp][NC]
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(ml + kStreamWarps * NC);
-  int* const pages = reinterpret_cast<int*>(bars + kStreamWarps * kStages);
-  int* const where = pages + kStreamWarps * kStages;  // warp sums, then the CTA's first chunk
+  float* const po = reinterpret_cast<float*>(smem + kSlots * kTileBytes);         // [2][warp][NC][66]
+  float2* const ml = reinterpret_cast<float2*>(po + 2 * kStreamWarps * NC * 66);  // [2][warp][NC]
+  // the slots' full and empty barriers, the buffers' (filled by four warps, joined by one)
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(ml + 2 * kStreamWarps * NC);
+  int* const pages = reinterpret_cast<int*>(bars + 2 * kSlots + 4);
+  int* const sums = pages + kSlots;                                               // [warps]
+  int* const where = sums + kStreamWarps + 1;                                     // first item, head, chunk, weight
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kSlots;
   pdl_launch_dependents();
-  Ring ring;
-  ring.data = smem_u32(smem) + warp * kStages * kTileBytes;
-  ring.bar = smem_u32(bars + warp * kStages);
-  ring.pages = pages + warp * kStages;
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(ring.bar + 8 * i, 1);
+  if (tid == 0) {
+    for (int i = 0; i < 2 * kSlots + 4; ++i) mbar_init(full + 8 * i, i == 2 * kSlots || i == 2 * kSlots + 1 ? kStreamWarps : 1);
     mbar_fence_init();
+    where[0] = -1;
   }
   pdl_wait();
 
-  // this CTA's run of chunks
-  const int per = (sa.items + 32 * kStreamWarps - 1) / (32 * kStreamWarps);
+  // this CTA's run of chunks: those that begin in its share of the tiles
+  const int per = (sa.items + kThr - 1) / kThr;
   const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
   int mine = 0;
-  for (int x = x0; x < x1; ++x) mine += item_at(a, sa, x).nch * a.Hkv;
+  for (int x = x0; x < x1; ++x) mine += item_tiles(sa, item_at(a, sa, x)) * a.Hkv;
   int inc = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, inc, off);
     if (lane >= off) inc += y;
   }
-  if (lane == 31) where[warp] = inc;
+  if (lane == 31) sums[warp] = inc;
   __syncthreads();
   int before = inc - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kStreamWarps; ++w) {
-    if (w < warp) before += where[w];
-    total += where[w];
+  for (int w = 0; w <= kStreamWarps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
   }
-  const int first = (int)((int64_t)total * blockIdx.x / gridDim.x), last = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-  if (first == last) return;
-  if (first >= before && first < before + mine) {
+  const int share = total / (int)gridDim.x, rest = total - share * (int)gridDim.x, b = blockIdx.x;
+  const int first = share * b + min(b, rest), last = first + share + (b < rest);
+  if (first < last && first >= before && first < before + mine) {
     int at = before;
     for (int x = x0; x < x1; ++x) {
       const Item it = item_at(a, sa, x);
-      if (first < at + it.nch * a.Hkv) {
-        where[4] = x;
-        where[5] = (first - at) / it.nch;
-        where[6] = it.c0 + (first - at) % it.nch;
+      const int nt = item_tiles(sa, it);
+      if (first < at + nt * a.Hkv) {
+        // the first chunk that begins at `first` or later; its head's end is a chunk's beginning too
+        const int h = (first - at) / nt, in = first - at - h * nt;
+        const int t0 = max(0, it.pfirst - sa.W) / kTile;
+        const int c = in == 0 ? it.c0 : (in + t0 + sa.chunk_tiles - 1) >> sa.lg_chunk;
+        where[0] = x;
+        where[1] = h;
+        where[2] = c;
+        where[3] = at + h * nt + (c == it.c0 ? 0 : min(c * sa.chunk_tiles - t0, nt));
         break;
       }
-      at += it.nch * a.Hkv;
+      at += nt * a.Hkv;
     }
   }
   __syncthreads();
+  if (where[0] < 0) return;
   Cursor cur;
-  cur.x = where[4];
-  cur.h = where[5];
-  cur.c = where[6];
+  cur.x = where[0];
+  cur.h = where[1];
+  cur.c = where[2];
+  cur.at = where[3];
+  cur.end = last;
+  if (cur.at >= cur.end) return;
   cur.it = item_at(a, sa, cur.x);
-  cur.left = last - first;
-  cur.tiles(sa);
-
-  ring.at = cur;
-  ring.ti = cur.tb + warp;
-  ring.more = true;
-  ring.slot_in = ring.issued = ring.used = 0;
-  ring.lanes(a, lane);
-  ring.skip = first == 0 && warp == 0 ? a.debug_skip : -1;
-  ring.skip_empty(a, sa, warp);
-#pragma unroll
-  for (int k = 0; k < kStages; ++k) ring.read_ids(a, sa, warp);
-#pragma unroll
-  for (int k = 0; k < kStages; ++k) {
-    ring.issue(a, lane);
-    ring.read_ids(a, sa, warp);
+  if (cur.c >= cur.it.c0 + cur.it.nch) {  // the share begins inside a head's last chunk: step to the next head
+    cur.c = cur.it.c0 + cur.it.nch - 1;
+    cur.te = cur.tb = 0;
+    cur.at -= 1;
+    if (!cur.next(a, sa)) return;
+  } else {
+    cur.tiles(sa);
   }
 
+  if (warp == kStreamWarps) {
+    copy_run(a, sa, cur, smem_u32(smem), full, empty, pages, cur.at == 0 ? a.debug_skip : -1, lane);
+    return;
+  }
   const int G = 1 << a.lgG;
+  const int all_pages = (1 << (kTile >> min(a.lgS, 6))) - 1;
   QFrag<NT> q;
   Acc<NT> acc;
-  int qx = -1, qh = -1, slot = 0, phase = 0;
-  const int all_pages = (1 << (kTile / ring.rows)) - 1;
-  bool dead = false;  // a wait ran out: no more copies, no more work
+  int qx = -1, qh = -1, n0 = 0, nchunk = 0;  // n0, nchunk: tiles and chunks of the run before this one
+  bool dead = false;                         // a wait ran out: no more waits, no more work
+  auto wait = [&](uint32_t bar, int phase) {
+    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait_bounded(bar, phase, a.wait_cycles));
+  };
   do {
     const int ncol = cur.it.nrows << a.lgG;
     if (cur.x != qx || cur.h != qh) {
@@ -758,59 +775,55 @@ __global__ void __launch_bounds__(32 * kStreamWarps, NT == 1 ? 3 : 2) kv4_stream
       qh = cur.h;
     }
     acc.clear();
-    for (int ti = cur.tb + warp; ti < cur.te; ti += kStreamWarps) {
-      if (!dead && !mbar_wait_bounded(ring.bar + 8 * slot, phase, a.wait_cycles)) {
-        record_status(a.status, SFA_ERR_TIMEOUT);
-        dead = true;
-      }
-      dead = __any_sync(0xffffffffu, dead);
-      if (dead) continue;
-      stream_tile<NT, kExact>(a, sa, cur.it, q, acc, smem + (warp * kStages + slot) * kTileBytes, ti * kTile, ring.pages[slot], all_pages,
-                              lane);
-      ++ring.used;
-      if (++slot == kStages) {
-        slot = 0;
-        phase ^= 1;
-      }
+    for (int k = warp; k < cur.te - cur.tb; k += kStreamWarps) {
+      const int n = n0 + k, slot = n % kSlots;
+      wait(full + 8 * slot, n / kSlots & 1);
+      if (dead) break;
+      stream_tile<NT, kExact>(a, sa, cur.it, q, acc, smem + slot * kTileBytes, (cur.tb + k) * kTile, pages[slot], all_pages, lane);
       __syncwarp();
-      ring.issue(a, lane);
-      ring.read_ids(a, sa, warp);
+      if (lane == 0) mbar_arrive(empty + 8 * slot);
     }
+    n0 += cur.te - cur.tb;
+    // The four warps' sums meet in one of two buffers.  No warp waits for the others here: the
+    // warps take turns at joining a chunk's sums, and a buffer is waited for when it is filled again.
     acc.close();
-    if (g == 0)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) ml[warp * NC + 8 * nt + 2 * t + e] = make_float2(acc.m[nt][e], acc.l[nt][e]);
-    __syncthreads();
+    const int buf = nchunk & 1, round = nchunk >> 1;
+    const uint32_t in = full + 8 * (2 * kSlots + buf), out_ = in + 16;
+    if (round > 0) wait(out_, (round - 1) & 1);
+    float* const pb = po + buf * kStreamWarps * NC * 66;
+    float2* const mb = ml + buf * kStreamWarps * NC;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int col = 8 * nt + 2 * t + e;
         if (col >= ncol) continue;
-        float M = ml[col].x;
+        if (g == 0) mb[warp * NC + col] = make_float2(acc.m[nt][e], acc.l[nt][e]);
+        float* out = pb + (warp * NC + col) * 66 + 8 * g;
 #pragma unroll
-        for (int w = 1; w < kStreamWarps; ++w) M = fmaxf(M, ml[w * NC + col].x);
-        const float f = acc.m[nt][e] == -INFINITY ? 0.0f : ex2(acc.m[nt][e] - M);
-        float* out = po + (warp * NC + col) * 66 + 8 * g;
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-          *reinterpret_cast<float2*>(out + 2 * mt) = make_float2(acc.o[nt][mt][e] * f, acc.o[nt][mt][2 + e] * f);
+        for (int mt = 0; mt < 4; ++mt) *reinterpret_cast<float2*>(out + 2 * mt) = make_float2(acc.o[nt][mt][e], acc.o[nt][mt][2 + e]);
       }
-    __syncthreads();
-    for (int i = tid; i < 8 * ncol; i += 32 * kStreamWarps) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(in);
+    if (warp != (nchunk++ & 3)) continue;
+    wait(in, round & 1);
+    for (int i = lane; i < 8 * ncol; i += 32) {  // eight lanes a column
       const int col = i >> 3, d = i & 7;
-      float M = ml[col].x, l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      float M = -INFINITY, l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int w = 1; w < kStreamWarps; ++w) M = fmaxf(M, ml[w * NC + col].x);
+      for (int w = 0; w < kStreamWarps; ++w) M = fmaxf(M, mb[w * NC + col].x);
 #pragma unroll
       for (int w = 0; w < kStreamWarps; ++w) {
-        const float2 v = ml[w * NC + col];
-        l += v.y * (v.x == -INFINITY ? 0.0f : ex2(v.x - M));
-        const float* y = po + (w * NC + col) * 66 + 8 * d;
+        const float2 v = mb[w * NC + col];
+        const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - M);
+        l = fmaf(v.y, f, l);
+        const float* y = pb + (w * NC + col) * 66 + 8 * d;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += y[e];
+        for (int e = 0; e < 8; e += 2) {
+          const float2 z = *reinterpret_cast<const float2*>(y + e);
+          x[e] = fmaf(z.x, f, x[e]);
+          x[e + 1] = fmaf(z.y, f, x[e + 1]);
+        }
       }
       if (cur.it.nch == 1) {
         write_head<TIO>(a, cur.it.row0 + (col >> a.lgG), cur.h * G + (col & (G - 1)), d, x, M, l);
@@ -820,17 +833,16 @@ __global__ void __launch_bounds__(32 * kStreamWarps, NT == 1 ? 3 : 2) kv4_stream
         if (d == 0) sa.part_ml[at] = make_float2(M, l);
       }
     }
-    __syncthreads();  // ml and po are filled again by the next chunk
+    __syncwarp();
+    if (lane == 0) mbar_arrive(out_);
   } while (cur.next(a, sa));
-  // after a timeout: the copies still in flight end before the CTA does
-  if (dead)
-    for (; ring.used < ring.issued; ++ring.used)
-      mbar_wait_bounded(ring.bar + 8 * (ring.used % kStages), ring.used / kStages & 1, a.wait_cycles);
+  if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
 }
 
 // The chunks of one (item, KV head) joined: `cols` columns a CTA, 8 lanes a
-// column, the chunks dealt out over the remaining threads.
-constexpr int kJoinThreads = 128;
+// column, the chunks dealt out over the remaining threads (their partial sums
+// are read once, 264 bytes each: what counts is how many are in flight).
+constexpr int kJoinThreads = 512;
 
 template <typename TIO>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, const StreamArgs sa, int cols) {
@@ -841,7 +853,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
   const Item it = item_at(a, sa, x);
   const int ncol = it.nrows << a.lgG, G = 1 << a.lgG, width = G << sa.lg_rows;
   if (it.nch <= 1 || (int)blockIdx.y * cols >= ncol) return;
-  const int lanes = 8 * cols, groups = kJoinThreads / lanes;
+  const int lanes = 8 * cols, groups = blockDim.x / lanes;
   const int i = threadIdx.x % lanes, grp = threadIdx.x / lanes, d = i & 7;
   const int col = min((int)blockIdx.y * cols + (i >> 3), ncol - 1);
   const int64_t at = ((int64_t)blockIdx.x * sa.max_chunks) * width + col;
@@ -894,14 +906,15 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
   z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
   z.s.W = p.W;
-  z.grid = kSMs * (z.nt == 1 ? 3 : 2);
-  // chunks: at least 512 keys, and so that the whole block table's worth of
-  // them stays within 16 a CTA (the workspace's size; 16 parts a CTA balance to
-  // a few percent)
+  z.grid = kSMs * stream_ctas(z.nt);
+  // chunks: 512 keys (two tiles a warp), 256 where that would leave CTAs without
+  // one; more where the whole block table's worth of them would pass 16 a CTA
+  // (which bounds the workspace; the CTAs' shares differ by a chunk at most)
   const int64_t units = (int64_t)z.s.items * a.Hkv;
-  int64_t ck = 512;
+  int64_t ck = (cap + 511) / 512 * units <= z.grid ? 256 : 512;
   while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.grid) ck *= 2;
   z.s.chunk_tiles = (int)(ck / kTile);
+  z.s.lg_chunk = __builtin_ctz((unsigned)z.s.chunk_tiles);
   z.s.max_chunks = (int)((cap + ck - 1) / ck);
   z.slots = z.s.max_chunks > 1 ? units * z.s.max_chunks : 0;
   return z;
@@ -910,15 +923,24 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
 template <typename TIO, int NT>
 static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
   constexpr int NC = 8 * NT;
-  constexpr size_t smem = kStreamWarps * (kStages * (kTileBytes + 8 + 4) + NC * (66 * 4 + 8)) + 64;
-  static_assert(smem <= 227 * 1024 / (NT == 1 ? 3 : 2), "CTAs an SM");
+  constexpr size_t smem = kSlots * (kTileBytes + 16 + 4) + 2 * kStreamWarps * NC * (66 * 4 + 8) + 32 + 64;
+  static_assert(smem + 1024 <= 228 * 1024 / stream_ctas(NT), "CTAs an SM");
   cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = launch_pdl(kv4_stream_kernel<TIO, NT>, dim3((unsigned)z.grid), dim3(32 * kStreamWarps), smem, s, a, z.s);
+  if (e == cudaSuccess) e = launch_pdl(kv4_stream_kernel<TIO, NT>, dim3((unsigned)z.grid), dim3(32 * (kStreamWarps + 1)), smem, s, a, z.s);
   if (e != cudaSuccess || z.slots == 0) return e;
   const int width = 1 << (a.lgG + z.s.lg_rows);
-  const int cols = z.s.max_chunks > 32 ? 1 : std::min(width, kJoinThreads / 8);
-  return launch_pdl(kv4_join_kernel<TIO>, dim3((unsigned)(z.s.items * a.Hkv), (unsigned)((width + cols - 1) / cols)), dim3(kJoinThreads), 0,
-                    s, a, z.s, cols);
+  // enough columns to fill the card: four lanes' groups a column (a warp), four
+  // columns a CTA; else as many groups as a column may have chunks, up to 64
+  const int64_t columns = (int64_t)z.s.items * a.Hkv * width;
+  const int deep = columns >= 4 * kSMs ? 4 : std::min(64, 1 << (32 - __builtin_clz((unsigned)z.s.max_chunks - 1)));
+  const int cols = std::min(width, deep == 4 ? 4 : 1);
+  return launch_pdl(kv4_join_kernel<TIO>, dim3((unsigned)(z.s.items * a.Hkv), (unsigned)((width + cols - 1) / cols)), dim3(8 * deep * cols),
+                    0, s, a, z.s, cols);
+}
+
+bool kv4_attend_fits(const Kv4Args& a, const Plan& p, bool ragged) {
+  const StreamShape z = stream_shape(a, p, ragged);
+  return (int64_t)z.s.items * a.Hkv * (((int64_t)a.max_pages << a.lgS) / kTile + 1) < (1LL << 31);
 }
 
 size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, bool ragged) {

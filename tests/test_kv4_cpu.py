@@ -56,7 +56,7 @@ def test_row_refusals(sfa_lib, kw, rc):
 
 
 @pytest.mark.parametrize("kw,rc", [(dict(Hq=6), 2), (dict(Hq=7), 2), (dict(Hq=128), 2), (dict(Hq=0), 1), (dict(R=0), 1), (dict(R=4), 1),
-                                   (dict(max_pages=0), 1), (dict(max_pages=1 << 21), 2), (dict(q_stride=504), 1), (dict(q_stride=513), 1)])
+                                   (dict(max_pages=0), 1), (dict(max_pages=1 << 21), 2), (dict(q_stride=504), 1), (dict(q_stride=513), 1), (dict(R=1 << 20, N=1 << 20, Hkv=8, max_pages=1 << 20), 2)])
 def test_attend_refusals(sfa_lib, kw, rc):
     assert sfa_lib.sfa_kv4_attend(_desc(**kw), P, P, P, P, None, P, P, P, 1 << 30, None) == rc
 
@@ -147,4 +147,4 @@ def test_workspace_holds_the_split_rows(sfa_lib, R, N, Hq, Hkv, page, max_pages)
     n = _workspace(sfa_lib, **kw)
     assert n >= 2 * N * Hq * 66 * 4 or (n == 0 and N > 2000)  # enough rows: none is split
     assert n <= max(16 * 456 * 8 * 66 * 4, 16 * 304 * 32 * 66 * 4)
-    assert _workspace(sfa_lib, **{**kw, "max_pages": 512 // page}) == 0
+    assert _workspace(sfa_lib, **{**kw, "max_pages": 256 // page}) == 0
