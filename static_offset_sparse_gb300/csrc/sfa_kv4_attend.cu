@@ -713,7 +713,9 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
     if (w < warp) before += sums[w];
     total += sums[w];
   }
-  const int share = total / (int)gridDim.x, rest = total - share * (int)gridDim.x, b = blockIdx.x;
+  // CTAs kSMs apart come to lie on one SM: neighbouring shares, whose roundings to whole chunks cancel
+  const int share = total / (int)gridDim.x, rest = total - share * (int)gridDim.x, perSM = gridDim.x / kSMs;
+  const int b = blockIdx.x % kSMs * perSM + blockIdx.x / kSMs;
   const int first = share * b + min(b, rest), last = first + share + (b < rest);
   if (first < last && first >= before && first < before + mine) {
     int at = before;

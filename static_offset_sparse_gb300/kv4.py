@@ -170,16 +170,17 @@ def kv4_plan(n_new, seq_lens, block_table, free_pages, n_free, *, page: int, row
     R, width = block_table.shape
     P = free_pages.shape[0]
     own = torch.empty((2 * R + 2 + 2 * rows,), dtype=i32, device=block_table.device)
-    cu_q, slots, pos, lens, left = own.split([R + 1, rows, rows, R, 1])
-    if seq_lens_out is not None:
-        lens = seq_lens_out
-    if n_free_out is not None:
-        left = n_free_out
-    d = Kv4Desc(P, page, 0, 0, R, width, rows)
+    cu_q, slots, pos, lens, left = own.split_with_sizes((R + 1, rows, rows, R, 1))
     p = own.data_ptr()
-    _call(_lib().sfa_kv4_plan, "sfa_kv4_plan", at, d, _ints(at, R, n_new, "n_new"), _ints(at, R, seq_lens, "seq_lens"),
-          block_table.data_ptr(), _ints(at, P, free_pages, "free_pages"), _ints(at, 1, n_free, "n_free"), p, p + 4 * (R + 1),
-          p + 4 * (R + 1 + rows), _ints(at, R, lens, "seq_lens_out"), _ints(at, 1, left, "n_free_out"))
+    p_lens = p + 4 * (R + 1 + 2 * rows)
+    p_left = p_lens + 4 * R
+    if seq_lens_out is not None:
+        lens, p_lens = seq_lens_out, _ints(at, R, seq_lens_out, "seq_lens_out")
+    if n_free_out is not None:
+        left, p_left = n_free_out, _ints(at, 1, n_free_out, "n_free_out")
+    _call(_lib().sfa_kv4_plan, "sfa_kv4_plan", at, Kv4Desc(P, page, 0, 0, R, width, rows), _ints(at, R, n_new, "n_new"),
+          _ints(at, R, seq_lens, "seq_lens"), block_table.data_ptr(), _ints(at, P, free_pages, "free_pages"),
+          _ints(at, 1, n_free, "n_free"), p, p + 4 * (R + 1), p + 4 * (R + 1 + rows), p_lens, p_left)
     return cu_q, slots, pos, lens, left
 
 
@@ -214,11 +215,16 @@ def kv4_read(cache, slots, *, dtype=None, kscale: float = 1.0, vscale: float = 1
     shape = (N, H, 64)
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
+        kp = k.data_ptr()
+    else:
+        kp = _dense(at, shape, dtype, k, "k")
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
-    d = Kv4Desc(P, page, H, 64, 0, 0, N, 0, code, 0, 0, 0, kscale, vscale)
-    _call(_lib().sfa_kv4_read, "sfa_kv4_read", at, d, cache.data_ptr(), _ints(at, N, slots, "slots"),
-          _dense(at, shape, dtype, k, "k"), _dense(at, shape, dtype, v, "v"))
+        v = torch.empty_like(k)
+        vp = v.data_ptr()
+    else:
+        vp = _dense(at, shape, dtype, v, "v")
+    _call(_lib().sfa_kv4_read, "sfa_kv4_read", at, Kv4Desc(P, page, H, 64, 0, 0, N, 0, code, 0, 0, 0, kscale, vscale),
+          cache.data_ptr(), _ints(at, N, slots, "slots"), kp, vp)
     return k, v
 
 
@@ -255,11 +261,16 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
     at, R, N, Hq, d = _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale)
     if cu_q is None and N != R:
         raise ValueError(f"without cu_q, q has one row for each of the {R} requests, got {N}")
-    shape = (N, Hq, 64)
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op = o.data_ptr()
+    else:
+        op = _dense(at, (N, Hq, 64), q.dtype, o, "o")
     if lse is None:
         lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        lp = lse.data_ptr()
+    else:
+        lp = _dense(at, (N, Hq), torch.float32, lse, "lse")
     L = _lib()
     n = C.c_size_t(0)
     rc = L.sfa_kv4_workspace_size(d, C.byref(n))
@@ -276,5 +287,5 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
         w = ws.data_ptr()
     _call(L.sfa_kv4_attend, "sfa_kv4_attend", at, d, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
           _ints(at, R, seq_lens, "seq_lens"), None if cu_q is None else _ints(at, R + 1, cu_q, "cu_q"),
-          _dense(at, shape, q.dtype, o, "o"), _dense(at, (N, Hq), torch.float32, lse, "lse"), w, n)
+          op, lp, w, n)
     return o, lse
