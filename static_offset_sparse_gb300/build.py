@@ -22,7 +22,7 @@ DEBUG_LIB = os.path.join(PKG, "libsfa_debug.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["sfa_host.cpp", "sfa_api.cu", "sfa_fwd.cu", "sfa_bwd.cu", "sfa_fwd_tc.cu", "sfa_bwd_tc.cu",
-           "sfa_noalloc.cu", "sfa_decode.cu", "sfa_schedule.cpp", "sfa_band.cu", "sfa_kv4.cu", "sfa_kv4_attend.cu"]
+           "sfa_noalloc.cu", "sfa_decode.cu", "sfa_schedule.cpp", "sfa_band.cu", "sfa_kv4.cu", "sfa_kv4_attend.cu", "sfa_kv4_prompt.cu"]
 # The bounds-checked build (libsfa_debug.so) recompiles the SIMT kernels with
 # SFA_DEBUG_BOUNDS: every row index they form is range-checked, a bad one is
 # recorded as SFA_ERR_DEVICE_BOUNDS and its access skipped.

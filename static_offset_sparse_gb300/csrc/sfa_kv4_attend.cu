@@ -15,16 +15,10 @@
 
 #include <algorithm>
 
-#include "sfa_kv4.cuh"
+#include "sfa_kv4_stream.cuh"
 #include "sfa_launch.cuh"
 
 namespace sfa {
-
-// Probabilities are kept times 2^kPShift, relative to a maximum that may lag
-// the true one by 2^kLag (the statistics move only when a logit passes it by
-// more): at most 2^15 in f16, whose smallest steps then lie 2^-35 below the
-// largest probability of a column.
-constexpr float kPShift = 11.0f, kLag = 4.0f;
 
 // Queries as B fragments: column c is head c mod G of row c / G; lane (g, t)
 // holds dims 16t .. 16t + 15 of column 8 nt + g, in the order the keys' codes
@@ -205,18 +199,6 @@ struct Acc {
   }
 };
 
-// One head's output row (dims 8g .. 8g + 7 of lane (g, t)) and log-sum-exp.
-// l = 0: no keys, a zero row and -inf.
-template <typename TIO>
-__device__ __forceinline__ void write_head(const Kv4Args& a, int64_t n, int head, int g, const float* x, float m, float l) {
-  float y[8];
-  const float inv = l == 0.0f ? 0.0f : a.vscale / l;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = l == 0.0f ? 0.0f : x[e] * inv;
-  store8(static_cast<TIO*>(a.o) + (n * a.Hq + head) * kD + 8 * g, y);
-  if (a.lse && g == 0) a.lse[n * a.Hq + head] = l == 0.0f ? -INFINITY : (m - kPShift) * kLn2 + logf(l);
-}
-
 // ---------------------------------------------------------------- gather
 
 // Any offset list, one (row, KV head) a group of `warps` warps: lanes look up
@@ -373,163 +355,7 @@ static cudaError_t gather(const Kv4Args& a, const Plan& p, int warps, cudaStream
 // chunks and items.  The four warps take every fourth tile of a chunk and meet
 // in shared memory at its end.  Chunks of a longer item go to the workspace,
 // joined by a second kernel.
-constexpr int kStreamWarps = 4, kSlots = 8, kTile = 64, kTileBytes = kTile * kKv4Row;
-constexpr int kSMs = 152;
-
-struct StreamArgs {
-  int32_t items, lg_rows, chunk_tiles, lg_chunk, max_chunks, W;
-  float* part_o;   // [item][KV head][chunk][column][64]
-  float2* part_ml; // [item][KV head][chunk][column] (m, l)
-};
-
-struct Item {
-  int r, row0, nrows, pfirst, c0, nch;  // nch = 0: no rows
-  __device__ __forceinline__ int plast() const { return pfirst + nrows - 1; }
-};
-
-// Item x.  Requests start at item cu_q[r] / rows + r: room for each one's last,
-// shorter item without a scan over the requests.  A request whose positions
-// leave the tables counts as empty: zero rows, and the status says so.
-__device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, int x) {
-  Item it;
-  int len;
-  if (!a.cu_q) {
-    it.r = it.row0 = x;
-    it.nrows = 1;
-    len = a.seq_lens[x];
-    it.pfirst = len - 1;
-  } else {
-    int lo = 0, n = a.R;  // largest r with cu_q[r] / rows + r <= x
-    while (n > 1) {
-      const int half = n >> 1;
-      const bool le = (a.cu_q[lo + half] >> s.lg_rows) + lo + half <= x;
-      lo += le ? half : 0;
-      n = le ? n - half : half;
-    }
-    const int c = a.cu_q[lo], end = min(a.cu_q[lo + 1], a.N);
-    it.r = lo;
-    it.row0 = c + ((x - lo - (c >> s.lg_rows)) << s.lg_rows);
-    it.nrows = min(1 << s.lg_rows, end - it.row0);
-    if (c < 0 || it.row0 < c || it.nrows <= 0) {
-      it.nrows = it.nch = it.pfirst = it.c0 = 0;
-      return it;
-    }
-    len = a.seq_lens[lo];
-    it.pfirst = len - (end - it.row0);
-  }
-  const bool empty = !a.cu_q && len == 0;
-  if (empty || it.pfirst < 0 || it.pfirst > (a.max_pages << a.lgS) - it.nrows || (a.rope && it.pfirst > a.rope_T - it.nrows)) {
-    if (!empty) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
-    it.pfirst = -it.nrows;
-    it.c0 = 0;
-    it.nch = 1;
-    return it;
-  }
-  const int lg = s.lg_chunk + 6;  // 64 keys a tile
-  it.c0 = max(0, it.pfirst - s.W) >> lg;
-  it.nch = (it.plast() >> lg) - it.c0 + 1;
-  return it;
-}
-
-// A place in the CTA's run of chunks: chunk c of (item x, KV head h), its tiles
-// tb .. te - 1, and the run's weight (tiles; 1 for a chunk of none) up to here.
-struct Cursor {
-  Item it;
-  int x, h, c, tb, te;
-  int at, end;
-  __device__ __forceinline__ void tiles(const StreamArgs& s) {
-    tb = max(c * s.chunk_tiles, max(0, it.pfirst - s.W) / kTile);
-    te = it.plast() < 0 ? tb : min((c + 1) * s.chunk_tiles, it.plast() / kTile + 1);
-  }
-  // the next chunk; false at the end of the run
-  __device__ __forceinline__ bool next(const Kv4Args& a, const StreamArgs& s) {
-    at += max(1, te - tb);
-    if (at >= end) return false;
-    if (++c == it.c0 + it.nch) {
-      if (++h == a.Hkv) {
-        h = 0;
-        do {
-          if (x + 1 >= s.items) return false;
-          it = item_at(a, s, ++x);
-        } while (it.nch == 0);
-      }
-      c = it.c0;
-    }
-    tiles(s);
-    return true;
-  }
-};
-
-// Tiles of one KV head of an item (1 for an empty one, 0 for none).
-__device__ __forceinline__ int item_tiles(const StreamArgs& s, const Item& it) {
-  return it.nch == 0 ? 0 : it.plast() < 0 ? 1 : it.plast() / kTile + 1 - max(0, it.pfirst - s.W) / kTile;
-}
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(bar)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-
-// The copying warp: every tile of the CTA's run, in order, into slot n mod
-// kSlots as soon as tile n - kSlots has been read.
-__device__ __forceinline__ void copy_run(const Kv4Args& a, const StreamArgs& sa, Cursor cur, uint32_t ring, uint32_t full, uint32_t empty,
-                                         volatile int* pages, int skip, int lane) {
-  const int S = 1 << a.lgS, rows = min(S, kTile), np = kTile / rows, lgnp = __ffs(np) - 1, batch = 32 >> lgnp;
-  const int64_t block = kKv4Row * S;
-  int n = 0;
-  bool dead = false;
-  do {
-    const int32_t* trow = a.table + (int64_t)cur.it.r * a.max_pages;
-    const uint8_t* head = a.cache + cur.h * block;
-    const int last = cur.it.plast();
-    for (int t0 = cur.tb; t0 < cur.te && !dead; t0 += batch) {
-      // lane: page `lane mod np` of tile t0 + lane / np
-      const int j = (t0 + (lane >> lgnp)) * kTile + (lane & (np - 1)) * rows;
-      const bool mine = t0 + (lane >> lgnp) < cur.te && j <= last;
-      const int pid = mine ? trow[j >> a.lgS] : 0;
-      const bool ok = mine && pid >= 0 && pid < a.n_pages;
-      if (mine && !ok) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
-      const uint32_t there = __ballot_sync(0xffffffffu, ok);
-      const uint8_t* src = head + pid * (block * a.Hkv);
-      const int k1 = min(batch, cur.te - t0);
-      for (int k = 0; k < k1; ++k, ++n) {
-        const int slot = n % kSlots;
-        if (n >= kSlots && !mbar_wait_bounded(empty + 8 * slot, (n / kSlots - 1) & 1, a.wait_cycles)) {
-          record_status(a.status, SFA_ERR_TIMEOUT);
-          dead = true;
-        }
-        dead = __any_sync(0xffffffffu, dead);
-        if (dead) break;
-        if (n == skip) continue;
-        const uint32_t b = full + 8 * slot, d = ring + slot * kTileBytes;
-        const uint32_t here = (there >> (k << lgnp)) & ((1u << np) - 1);
-        if (lane == 0) {
-          pages[slot] = (int)here;
-          mbar_expect_tx(b, __popc(here) * rows * kKv4Row);
-        }
-        __syncwarp();
-        if (ok && lane >> lgnp == k) {
-          const int p = lane & (np - 1), row = j & (S - 1);
-          if (S == kTile) {
-            bulk_load(d, src, kTileBytes, b);
-          } else {
-            bulk_load(d + 32 * p * rows, src + 32 * row, 32 * rows, b);
-            bulk_load(d + 32 * kTile + 32 * p * rows, src + 32 * S + 32 * row, 32 * rows, b);
-            bulk_load(d + 64 * kTile + 8 * p * rows, src + 64 * S + 8 * row, 8 * rows, b);
-          }
-        }
-      }
-    }
-  } while (!dead && cur.next(a, sa));
-  // the copies end before the CTA does, whatever became of their readers
-  for (int i = max(0, n - kSlots); i < n; ++i)
-    if (i != skip && !mbar_wait_bounded(full + 8 * (i % kSlots), i / kSlots & 1, a.wait_cycles)) record_status(a.status, SFA_ERR_TIMEOUT);
-}
+constexpr int kStreamWarps = 4, kSlots = 8;
 
 // Row r of a 16-key tile is key r ^ (r >> 2 & 1): the rows that lanes of one
 // shared-memory pass read then lie in different banks, for keys (rows g) and
@@ -670,7 +496,8 @@ __device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& 
 }
 
 // CTAs an SM of the variant with NT column tiles.
-constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : NT == 2 ? 2 : 1; }
+constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : NT == 4 ? 1 : 2; }
+static_assert(stream_ctas(kPromptColumns / 8) == kPromptCtas, "the tensor memory kernel's grid");
 
 template <typename TIO, int NT>
 __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
@@ -690,73 +517,14 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
   if (tid == 0) {
     for (int i = 0; i < 2 * kSlots + 4; ++i) mbar_init(full + 8 * i, i == 2 * kSlots || i == 2 * kSlots + 1 ? kStreamWarps : 1);
     mbar_fence_init();
-    where[0] = -1;
   }
   pdl_wait();
 
-  // this CTA's run of chunks: those that begin in its share of the tiles
-  const int per = (sa.items + kThr - 1) / kThr;
-  const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
-  int mine = 0;
-  for (int x = x0; x < x1; ++x) mine += item_tiles(sa, item_at(a, sa, x)) * a.Hkv;
-  int inc = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += y;
-  }
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  int before = inc - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w <= kStreamWarps; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
-  }
-  // CTAs kSMs apart come to lie on one SM: neighbouring shares, whose roundings to whole chunks cancel
-  const int share = total / (int)gridDim.x, rest = total - share * (int)gridDim.x, perSM = gridDim.x / kSMs;
-  const int b = blockIdx.x % kSMs * perSM + blockIdx.x / kSMs;
-  const int first = share * b + min(b, rest), last = first + share + (b < rest);
-  if (first < last && first >= before && first < before + mine) {
-    int at = before;
-    for (int x = x0; x < x1; ++x) {
-      const Item it = item_at(a, sa, x);
-      const int nt = item_tiles(sa, it);
-      if (first < at + nt * a.Hkv) {
-        // the first chunk that begins at `first` or later; its head's end is a chunk's beginning too
-        const int h = (first - at) / nt, in = first - at - h * nt;
-        const int t0 = max(0, it.pfirst - sa.W) / kTile;
-        const int c = in == 0 ? it.c0 : (in + t0 + sa.chunk_tiles - 1) >> sa.lg_chunk;
-        where[0] = x;
-        where[1] = h;
-        where[2] = c;
-        where[3] = at + h * nt + (c == it.c0 ? 0 : min(c * sa.chunk_tiles - t0, nt));
-        break;
-      }
-      at += nt * a.Hkv;
-    }
-  }
-  __syncthreads();
-  if (where[0] < 0) return;
   Cursor cur;
-  cur.x = where[0];
-  cur.h = where[1];
-  cur.c = where[2];
-  cur.at = where[3];
-  cur.end = last;
-  if (cur.at >= cur.end) return;
-  cur.it = item_at(a, sa, cur.x);
-  if (cur.c >= cur.it.c0 + cur.it.nch) {  // the share begins inside a head's last chunk: step to the next head
-    cur.c = cur.it.c0 + cur.it.nch - 1;
-    cur.te = cur.tb = 0;
-    cur.at -= 1;
-    if (!cur.next(a, sa)) return;
-  } else {
-    cur.tiles(sa);
-  }
+  if (!find_run<kThr>(a, sa, sums, where, cur)) return;
 
   if (warp == kStreamWarps) {
-    copy_run(a, sa, cur, smem_u32(smem), full, empty, pages, cur.at == 0 ? a.debug_skip : -1, lane);
+    copy_run<kSlots>(a, sa, cur, smem_u32(smem), full, empty, pages, cur.at == 0 ? a.debug_skip : -1, lane);
     return;
   }
   const int G = 1 << a.lgG;
@@ -905,16 +673,19 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   const int avg = ragged ? (a.N + a.R - 1) / a.R : 1;
   z.nt = G * avg > 16 ? 4 : G * avg > 8 ? 2 : 1;
   z.nt = std::max(z.nt, G > 16 ? 4 : G > 8 ? 2 : 1);
+  // from half of 128 columns on: the tensor memory kernel (nt = 16)
+  if (G * avg >= 64) z.nt = kPromptColumns / 8;
   z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
   z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
   z.s.W = p.W;
   z.grid = kSMs * stream_ctas(z.nt);
   // chunks: 512 keys (two tiles a warp), 256 where that would leave CTAs without
-  // one; more where the whole block table's worth of them would pass 16 a CTA
-  // (which bounds the workspace; the CTAs' shares differ by a chunk at most)
+  // one; more where the whole block table's worth of them would pass 16 a CTA (8
+  // of the wider items): that bounds the workspace, and the CTAs' shares differ
+  // by a chunk at most
   const int64_t units = (int64_t)z.s.items * a.Hkv;
   int64_t ck = (cap + 511) / 512 * units <= z.grid ? 256 : 512;
-  while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.grid) ck *= 2;
+  while (ck < cap && (cap + ck - 1) / ck * units > (z.nt == kPromptColumns / 8 ? 8 : 16) * z.grid) ck *= 2;
   z.s.chunk_tiles = (int)(ck / kTile);
   z.s.lg_chunk = __builtin_ctz((unsigned)z.s.chunk_tiles);
   z.s.max_chunks = (int)((cap + ck - 1) / ck);
@@ -922,14 +693,9 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   return z;
 }
 
-template <typename TIO, int NT>
-static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
-  constexpr int NC = 8 * NT;
-  constexpr size_t smem = kSlots * (kTileBytes + 16 + 4) + 2 * kStreamWarps * NC * (66 * 4 + 8) + 32 + 64;
-  static_assert(smem + 1024 <= 228 * 1024 / stream_ctas(NT), "CTAs an SM");
-  cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = launch_pdl(kv4_stream_kernel<TIO, NT>, dim3((unsigned)z.grid), dim3(32 * (kStreamWarps + 1)), smem, s, a, z.s);
-  if (e != cudaSuccess || z.slots == 0) return e;
+template <typename TIO>
+static cudaError_t join(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
+  if (z.slots == 0) return cudaSuccess;
   const int width = 1 << (a.lgG + z.s.lg_rows);
   // enough columns to fill the card: four lanes' groups a column (a warp), four
   // columns a CTA; else as many groups as a column may have chunks, up to 64
@@ -938,6 +704,24 @@ static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s
   const int cols = std::min(width, deep == 4 ? 4 : 1);
   return launch_pdl(kv4_join_kernel<TIO>, dim3((unsigned)(z.s.items * a.Hkv), (unsigned)((width + cols - 1) / cols)), dim3(8 * deep * cols),
                     0, s, a, z.s, cols);
+}
+
+template <typename TIO, int NT>
+static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
+  constexpr int NC = 8 * NT;
+  constexpr size_t smem = kSlots * (kTileBytes + 16 + 4) + 2 * kStreamWarps * NC * (66 * 4 + 8) + 32 + 64;
+  static_assert(smem + 1024 <= 228 * 1024 / stream_ctas(NT), "CTAs an SM");
+  const cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return e != cudaSuccess ? e : launch_pdl(kv4_stream_kernel<TIO, NT>, dim3((unsigned)z.grid), dim3(32 * (kStreamWarps + 1)), smem, s, a, z.s);
+}
+
+template <typename TIO>
+static cudaError_t stream_and_join(const Kv4Args& a, const StreamShape& z, int dtype, cudaStream_t s) {
+  const cudaError_t e = z.nt == 1   ? stream<TIO, 1>(a, z, s)
+                        : z.nt == 2 ? stream<TIO, 2>(a, z, s)
+                        : z.nt == 4 ? stream<TIO, 4>(a, z, s)
+                                    : launch_kv4_prompt(a, z.s, dtype, s);
+  return e == cudaSuccess ? join<TIO>(a, z, s) : e;
 }
 
 bool kv4_attend_fits(const Kv4Args& a, const Plan& p, bool ragged) {
@@ -959,10 +743,7 @@ int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void
   if (z.s.items > 0) {
     z.s.part_o = static_cast<float*>(ws);
     z.s.part_ml = reinterpret_cast<float2*>(z.s.part_o + ((size_t)z.slots * kD << (a.lgG + z.s.lg_rows)));
-    if (dtype == SFA_BF16)
-      e = z.nt == 1 ? stream<bf16, 1>(a, z, s) : z.nt == 2 ? stream<bf16, 2>(a, z, s) : stream<bf16, 4>(a, z, s);
-    else
-      e = z.nt == 1 ? stream<float, 1>(a, z, s) : z.nt == 2 ? stream<float, 2>(a, z, s) : stream<float, 4>(a, z, s);
+    e = dtype == SFA_BF16 ? stream_and_join<bf16>(a, z, dtype, s) : stream_and_join<float>(a, z, dtype, s);
     return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
   }
   const int tiles = (int)((std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS) + 15) / 16);

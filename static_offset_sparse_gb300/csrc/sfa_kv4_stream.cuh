@@ -1,0 +1,259 @@
+// What the streaming attention kernels over the paged 4-bit cache share: how
+// the work is cut and shared out, the warp that copies, the outputs.
+#pragma once
+
+#include <math.h>
+
+#include "sfa_kv4.cuh"
+
+namespace sfa {
+
+// Probabilities are kept times 2^kPShift, relative to a maximum that may lag
+// the true one by 2^kLag (the statistics move only when a logit passes it by
+// more): at most 2^15 in f16, whose smallest steps then lie 2^-35 below the
+// largest probability of a column.
+constexpr float kPShift = 11.0f, kLag = 4.0f;
+
+// One head's output row (dims 8g .. 8g + 7 of lane (g, t)) and log-sum-exp.
+// l = 0: no keys, a zero row and -inf.
+template <typename TIO>
+__device__ __forceinline__ void write_head(const Kv4Args& a, int64_t n, int head, int g, const float* x, float m, float l) {
+  float y[8];
+  const float inv = l == 0.0f ? 0.0f : a.vscale / l;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = l == 0.0f ? 0.0f : x[e] * inv;
+  store8(static_cast<TIO*>(a.o) + (n * a.Hq + head) * kD + 8 * g, y);
+  if (a.lse && g == 0) a.lse[n * a.Hq + head] = l == 0.0f ? -INFINITY : (m - kPShift) * kLn2 + logf(l);
+}
+
+constexpr int kTile = 64, kTileBytes = kTile * kKv4Row;
+constexpr int kSMs = 152;
+
+struct StreamArgs {
+  int32_t items, lg_rows, chunk_tiles, lg_chunk, max_chunks, W;
+  float* part_o;   // [item][KV head][chunk][column][64]
+  float2* part_ml; // [item][KV head][chunk][column] (m, l)
+};
+
+struct Item {
+  int r, row0, nrows, pfirst, c0, nch;  // nch = 0: no rows
+  __device__ __forceinline__ int plast() const { return pfirst + nrows - 1; }
+};
+
+// Item x.  Requests start at item cu_q[r] / rows + r: room for each one's last,
+// shorter item without a scan over the requests.  A request whose positions
+// leave the tables counts as empty: zero rows, and the status says so.
+__device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, int x) {
+  Item it;
+  int len;
+  if (!a.cu_q) {
+    it.r = it.row0 = x;
+    it.nrows = 1;
+    len = a.seq_lens[x];
+    it.pfirst = len - 1;
+  } else {
+    int lo = 0, n = a.R;  // largest r with cu_q[r] / rows + r <= x
+    while (n > 1) {
+      const int half = n >> 1;
+      const bool le = (a.cu_q[lo + half] >> s.lg_rows) + lo + half <= x;
+      lo += le ? half : 0;
+      n = le ? n - half : half;
+    }
+    const int c = a.cu_q[lo], end = min(a.cu_q[lo + 1], a.N);
+    it.r = lo;
+    it.row0 = c + ((x - lo - (c >> s.lg_rows)) << s.lg_rows);
+    it.nrows = min(1 << s.lg_rows, end - it.row0);
+    if (c < 0 || it.row0 < c || it.nrows <= 0) {
+      it.nrows = it.nch = it.pfirst = it.c0 = 0;
+      return it;
+    }
+    len = a.seq_lens[lo];
+    it.pfirst = len - (end - it.row0);
+  }
+  const bool empty = !a.cu_q && len == 0;
+  if (empty || it.pfirst < 0 || it.pfirst > (a.max_pages << a.lgS) - it.nrows || (a.rope && it.pfirst > a.rope_T - it.nrows)) {
+    if (!empty) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+    it.pfirst = -it.nrows;
+    it.c0 = 0;
+    it.nch = 1;
+    return it;
+  }
+  const int lg = s.lg_chunk + 6;  // 64 keys a tile
+  it.c0 = max(0, it.pfirst - s.W) >> lg;
+  it.nch = (it.plast() >> lg) - it.c0 + 1;
+  return it;
+}
+
+// A place in the CTA's run of chunks: chunk c of (item x, KV head h), its tiles
+// tb .. te - 1, and the run's weight (tiles; 1 for a chunk of none) up to here.
+struct Cursor {
+  Item it;
+  int x, h, c, tb, te;
+  int at, end;
+  __device__ __forceinline__ void tiles(const StreamArgs& s) {
+    tb = max(c * s.chunk_tiles, max(0, it.pfirst - s.W) / kTile);
+    te = it.plast() < 0 ? tb : min((c + 1) * s.chunk_tiles, it.plast() / kTile + 1);
+  }
+  // the next chunk; false at the end of the run
+  __device__ __forceinline__ bool next(const Kv4Args& a, const StreamArgs& s) {
+    at += max(1, te - tb);
+    if (at >= end) return false;
+    if (++c == it.c0 + it.nch) {
+      if (++h == a.Hkv) {
+        h = 0;
+        do {
+          if (x + 1 >= s.items) return false;
+          it = item_at(a, s, ++x);
+        } while (it.nch == 0);
+      }
+      c = it.c0;
+    }
+    tiles(s);
+    return true;
+  }
+};
+
+// Tiles of one KV head of an item (1 for an empty one, 0 for none).
+__device__ __forceinline__ int item_tiles(const StreamArgs& s, const Item& it) {
+  return it.nch == 0 ? 0 : it.plast() < 0 ? 1 : it.plast() / kTile + 1 - max(0, it.pfirst - s.W) / kTile;
+}
+
+// This CTA's run of chunks: those that begin in its share of the tiles; false
+// if there are none.  All THREADS threads call it, with shared memory for
+// THREADS / 32 sums and the 4 numbers of `where`.
+template <int THREADS>
+__device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa, int* sums, int* where, Cursor& cur) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (sa.items + THREADS - 1) / THREADS;
+  const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
+  if (tid == 0) where[0] = -1;
+  int mine = 0;
+  for (int x = x0; x < x1; ++x) mine += item_tiles(sa, item_at(a, sa, x)) * a.Hkv;
+  int inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += y;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  // CTAs kSMs apart come to lie on one SM: neighbouring shares, whose roundings to whole chunks cancel
+  const int share = total / (int)gridDim.x, rest = total - share * (int)gridDim.x, perSM = gridDim.x / kSMs;
+  const int b = blockIdx.x % kSMs * perSM + blockIdx.x / kSMs;
+  const int first = share * b + min(b, rest), last = first + share + (b < rest);
+  if (first < last && first >= before && first < before + mine) {
+    int at = before;
+    for (int x = x0; x < x1; ++x) {
+      const Item it = item_at(a, sa, x);
+      const int nt = item_tiles(sa, it);
+      if (first < at + nt * a.Hkv) {
+        // the first chunk that begins at `first` or later; its head's end is a chunk's beginning too
+        const int h = (first - at) / nt, in = first - at - h * nt;
+        const int t0 = max(0, it.pfirst - sa.W) / kTile;
+        const int c = in == 0 ? it.c0 : (in + t0 + sa.chunk_tiles - 1) >> sa.lg_chunk;
+        where[0] = x;
+        where[1] = h;
+        where[2] = c;
+        where[3] = at + h * nt + (c == it.c0 ? 0 : min(c * sa.chunk_tiles - t0, nt));
+        break;
+      }
+      at += nt * a.Hkv;
+    }
+  }
+  __syncthreads();
+  if (where[0] < 0) return false;
+  cur.x = where[0];
+  cur.h = where[1];
+  cur.c = where[2];
+  cur.at = where[3];
+  cur.end = last;
+  if (cur.at >= cur.end) return false;
+  cur.it = item_at(a, sa, cur.x);
+  if (cur.c >= cur.it.c0 + cur.it.nch) {  // the share begins inside a head's last chunk: step to the next head
+    cur.c = cur.it.c0 + cur.it.nch - 1;
+    cur.te = cur.tb = 0;
+    cur.at -= 1;
+    return cur.next(a, sa);
+  }
+  cur.tiles(sa);
+  return true;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+
+// The copying warp: every tile of the CTA's run, in order, into slot n mod
+// SLOTS as soon as tile n - SLOTS has been read.
+template <int SLOTS>
+__device__ __forceinline__ void copy_run(const Kv4Args& a, const StreamArgs& sa, Cursor cur, uint32_t ring, uint32_t full, uint32_t empty,
+                                         volatile int* pages, int skip, int lane) {
+  const int S = 1 << a.lgS, rows = min(S, kTile), np = kTile / rows, lgnp = __ffs(np) - 1, batch = 32 >> lgnp;
+  const int64_t block = kKv4Row * S;
+  int n = 0;
+  bool dead = false;
+  do {
+    const int32_t* trow = a.table + (int64_t)cur.it.r * a.max_pages;
+    const uint8_t* head = a.cache + cur.h * block;
+    const int last = cur.it.plast();
+    for (int t0 = cur.tb; t0 < cur.te && !dead; t0 += batch) {
+      // lane: page `lane mod np` of tile t0 + lane / np
+      const int j = (t0 + (lane >> lgnp)) * kTile + (lane & (np - 1)) * rows;
+      const bool mine = t0 + (lane >> lgnp) < cur.te && j <= last;
+      const int pid = mine ? trow[j >> a.lgS] : 0;
+      const bool ok = mine && pid >= 0 && pid < a.n_pages;
+      if (mine && !ok) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+      const uint32_t there = __ballot_sync(0xffffffffu, ok);
+      const uint8_t* src = head + pid * (block * a.Hkv);
+      const int k1 = min(batch, cur.te - t0);
+      for (int k = 0; k < k1; ++k, ++n) {
+        const int slot = n % SLOTS;
+        if (n >= SLOTS && !mbar_wait_bounded(empty + 8 * slot, (n / SLOTS - 1) & 1, a.wait_cycles)) {
+          record_status(a.status, SFA_ERR_TIMEOUT);
+          dead = true;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+        if (n == skip) continue;
+        const uint32_t b = full + 8 * slot, d = ring + slot * kTileBytes;
+        const uint32_t here = (there >> (k << lgnp)) & ((1u << np) - 1);
+        if (lane == 0) {
+          pages[slot] = (int)here;
+          mbar_expect_tx(b, __popc(here) * rows * kKv4Row);
+        }
+        __syncwarp();
+        if (ok && lane >> lgnp == k) {
+          const int p = lane & (np - 1), row = j & (S - 1);
+          if (S == kTile) {
+            bulk_load(d, src, kTileBytes, b);
+          } else {
+            bulk_load(d + 32 * p * rows, src + 32 * row, 32 * rows, b);
+            bulk_load(d + 32 * kTile + 32 * p * rows, src + 32 * S + 32 * row, 32 * rows, b);
+            bulk_load(d + 64 * kTile + 8 * p * rows, src + 64 * S + 8 * row, 8 * rows, b);
+          }
+        }
+      }
+    }
+  } while (!dead && cur.next(a, sa));
+  // the copies end before the CTA does, whatever became of their readers
+  for (int i = max(0, n - SLOTS); i < n; ++i)
+    if (i != skip && !mbar_wait_bounded(full + 8 * (i % SLOTS), i / SLOTS & 1, a.wait_cycles)) record_status(a.status, SFA_ERR_TIMEOUT);
+}
+
+// sfa_kv4_prompt.cu: the stream of many rows a request, 128 columns an item.
+constexpr int kPromptColumns = 128, kPromptCtas = 2;
+cudaError_t launch_kv4_prompt(const Kv4Args& a, const StreamArgs& s, int dtype, cudaStream_t stream);
+
+}  // namespace sfa

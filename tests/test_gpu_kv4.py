@@ -384,8 +384,13 @@ def test_attend_padded_rows_and_strides(sfa, dist):
     o = torch.full((64, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((64, 8), 7.0, device="cuda")
     sfa.kv4_attend(q, _cuda(cache), _cuda(table), _i32(lens), cu_q=cu, dist=dist, o=o, lse=lse)
-    o2, l2 = sfa.kv4_attend(q[:37].contiguous(), _cuda(cache), _cuda(table), _i32(lens), cu_q=cu, dist=dist)
-    assert torch.equal(o[:37], o2) and torch.equal(lse[:37], l2)
+    # the same capacity: the variant is chosen by the rows that a request brings on average
+    o2, l2 = sfa.kv4_attend(q.contiguous(), _cuda(cache), _cuda(table), _i32(lens), cu_q=cu, dist=dist)
+    assert torch.equal(o[:37], o2[:37]) and torch.equal(lse[:37], l2[:37])
+    o3, l3 = sfa.kv4_attend(q[:37], _cuda(cache), _cuda(table), _i32(lens), cu_q=cu, dist=dist)
+    cs = ref.rope(table.shape[1] * page)
+    for got in ((o[:37], lse[:37]), (o3, l3)):
+        check_rows(*got, q[:37], cache, table, lens, [0, 30, 30, 37], page, dist, cs, 1.0, 1.0, True)
     assert (o[37:] == 7).all() and (lse[37:] == 7).all()
     assert sfa.get_device_status() == 0
 
@@ -532,24 +537,81 @@ def test_captured_decode_steps(sfa, dist):
     assert a["lens"].tolist() == [n + 20 for n in start]
 
 
-def test_attend_wait_that_runs_out(sfa, sfa_lib):
+@pytest.mark.parametrize("rows", [1, 40])
+def test_attend_wait_that_runs_out(sfa, sfa_lib, rows):
     """A tile whose copies are never started: its wait runs out, the status says so, the call ends, and
-    the next call is right."""
+    the next call is right (one row a request, and prompts)."""
     import torch
 
     rng = np.random.default_rng(14)
     lens, page = [3000, 700], 16
     cache, table = make_cache(rng, lens, page, 2)
-    q = torch.from_numpy(rng.standard_normal((2, 8, 64))).float().cuda()
+    q = torch.from_numpy(rng.standard_normal((2 * rows, 8, 64))).float().cuda()
     args = (q, _cuda(cache), _cuda(table), _i32(lens))
-    good = sfa.kv4_attend(*args)
+    cu = _i32([0, rows, 2 * rows])
+    good = sfa.kv4_attend(*args, cu_q=cu)
     torch.cuda.synchronize()
     try:
         for tile in (0, 1):
             assert sfa_lib.sfa_debug_inject(2000000, tile) == 0
-            sfa.kv4_attend(*args)
+            sfa.kv4_attend(*args, cu_q=cu)
             assert sfa.get_device_status() == 5  # SFA_ERR_TIMEOUT (the warp has two tiles)
     finally:
         sfa_lib.sfa_debug_inject(0, -1)
-    again = sfa.kv4_attend(*args)
+    again = sfa.kv4_attend(*args, cu_q=cu)
     assert sfa.get_device_status() == 0 and torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,new,Hq,Hkv,page,dist", [
+    ([700, 300, 64], [200, 129, 64], 8, 2, 64, None),
+    ([1000, 31, 500, 77], [33, 31, 500, 1], 16, 1, 16, None),
+    ([2500, 900], [300, 64], 4, 4, 128, None),
+    ([900, 70], [40, 70], 32, 1, 32, None),
+    ([1500, 130, 600], [100, 130, 64], 8, 2, 32, list(range(200))),
+    ([1, 300, 128], [1, 300, 128], 8, 1, 16, list(range(65))),
+])
+def test_attend_prompts(sfa, dtype, lens, new, Hq, Hkv, page, dist):
+    """Pieces of prompts, long enough for the tensor memory kernel: columns that fill their items and
+    do not, prefixes that are split and are not, windows."""
+    import torch
+
+    rng = np.random.default_rng(len(lens) + page)
+    cache, table = make_cache(rng, lens, page, Hkv)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = torch.from_numpy(2 * rng.standard_normal((cu[-1], Hq, 64))).to(_dt(dtype))
+    cs = ref.rope(table.shape[1] * page)
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), cu_q=_i32(cu), dist=dist, rope=_cuda(cs), kscale=0.7)
+    assert sfa.get_device_status() == 0
+    check_rows(o, lse, q, cache, table, lens, cu, page, dist, cs, 0.7, 1.0, dtype == "bf16")
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+@pytest.mark.parametrize("dist", [None, list(range(90))])
+def test_attend_nan_value_among_rows(sfa, rows, dist):
+    """A stored NaN in a value block reaches those rows that attend its key, in that block's dims, and
+    no others, whatever shares a tile with it."""
+    import torch
+
+    rng = np.random.default_rng(15)
+    n, page = 200, 16
+    cache, table = make_cache(rng, [n], page, 2, garbage=False)
+    q = torch.from_numpy(rng.standard_normal((rows, 8, 64))).float().cuda()
+    args = (_cuda(table), _i32([n]))
+    cu = _i32([0, rows])
+    clean, lse = sfa.kv4_attend(q, _cuda(cache), *args, cu_q=cu, dist=dist)
+    key = n - 2 if rows == 3 else n - 35
+    for old in (key, n - rows - 60):
+        cache[table[0, old // page], 1, 64 * page + 8 * (old % page) + 4 + 2] = 127  # KV head 1, dims 32 .. 47
+    o, lse2 = sfa.kv4_attend(q, _cuda(cache), *args, cu_q=cu, dist=dist)
+    pos = np.arange(n - rows, n)
+    W = n if dist is None else len(dist) - 1
+    hit = np.zeros(rows, bool)
+    for old in (key, n - rows - 60):
+        hit |= (old <= pos) & (old >= pos - W)
+    assert hit.any() and (rows == 3 or dist is None or not hit.all())
+    want = torch.zeros((rows, 8, 64), dtype=torch.bool)
+    want[torch.from_numpy(hit), 4:, 32:48] = True
+    assert torch.equal(o.isnan().cpu(), want)
+    assert torch.equal(o[~want.cuda()], clean[~want.cuda()]) and torch.equal(lse, lse2)
+    assert sfa.get_device_status() == 0

@@ -146,5 +146,5 @@ def test_workspace_holds_the_split_rows(sfa_lib, R, N, Hq, Hkv, page, max_pages)
     kw = dict(n_pages=1 << 14, R=R, N=N, Hq=Hq, Hkv=Hkv, page=page, max_pages=max_pages, q_stride=Hq * 64)
     n = _workspace(sfa_lib, **kw)
     assert n >= 2 * N * Hq * 66 * 4 or (n == 0 and N > 2000)  # enough rows: none is split
-    assert n <= max(16 * 456 * 8 * 66 * 4, 16 * 304 * 32 * 66 * 4)
+    assert n <= 8 * 304 * 128 * 66 * 4  # 82 MB
     assert _workspace(sfa_lib, **{**kw, "max_pages": 256 // page}) == 0
