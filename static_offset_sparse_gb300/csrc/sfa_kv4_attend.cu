@@ -496,8 +496,7 @@ __device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& 
 }
 
 // CTAs an SM of the variant with NT column tiles.
-constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : NT == 4 ? 1 : 2; }
-static_assert(stream_ctas(kPromptColumns / 8) == kPromptCtas, "the tensor memory kernel's grid");
+constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : NT == 2 ? 2 : 1; }
 
 template <typename TIO, int NT>
 __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
@@ -662,6 +661,7 @@ struct StreamShape {
   StreamArgs s;
   int nt, grid;
   int64_t slots;  // chunks the workspace has room for
+  size_t bytes;   // the workspace
 };
 
 static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
@@ -673,23 +673,30 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   const int avg = ragged ? (a.N + a.R - 1) / a.R : 1;
   z.nt = G * avg > 16 ? 4 : G * avg > 8 ? 2 : 1;
   z.nt = std::max(z.nt, G > 16 ? 4 : G > 8 ? 2 : 1);
-  // from half of 128 columns on: the tensor memory kernel (nt = 16)
+  // from half a tile of 128 columns on: the tensor memory kernel (nt = 32)
   if (G * avg >= 64) z.nt = kPromptColumns / 8;
   z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
   z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
   z.s.W = p.W;
   z.grid = kSMs * stream_ctas(z.nt);
-  // chunks: 512 keys (two tiles a warp), 256 where that would leave CTAs without
-  // one; more where the whole block table's worth of them would pass 16 a CTA (8
-  // of the wider items): that bounds the workspace, and the CTAs' shares differ
-  // by a chunk at most
   const int64_t units = (int64_t)z.s.items * a.Hkv;
+  if (z.nt == kPromptColumns / 8) {  // cuts its work otherwise
+    z.s.chunk_tiles = 1 << 18;
+    z.s.lg_chunk = 18;
+    z.s.max_chunks = 1;
+    z.bytes = prompt_workspace(units);
+    return z;
+  }
+  // chunks: 512 keys (two tiles a warp), 256 where that would leave CTAs without
+  // one; more where the whole block table's worth of them would pass 16 a CTA
+  // (which bounds the workspace; the CTAs' shares differ by a chunk at most)
   int64_t ck = (cap + 511) / 512 * units <= z.grid ? 256 : 512;
-  while (ck < cap && (cap + ck - 1) / ck * units > (z.nt == kPromptColumns / 8 ? 8 : 16) * z.grid) ck *= 2;
+  while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.grid) ck *= 2;
   z.s.chunk_tiles = (int)(ck / kTile);
   z.s.lg_chunk = __builtin_ctz((unsigned)z.s.chunk_tiles);
   z.s.max_chunks = (int)((cap + ck - 1) / ck);
   z.slots = z.s.max_chunks > 1 ? units * z.s.max_chunks : 0;
+  z.bytes = (size_t)z.slots * ((size_t)66 * 4 << (a.lgG + z.s.lg_rows));
   return z;
 }
 
@@ -716,11 +723,8 @@ static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s
 }
 
 template <typename TIO>
-static cudaError_t stream_and_join(const Kv4Args& a, const StreamShape& z, int dtype, cudaStream_t s) {
-  const cudaError_t e = z.nt == 1   ? stream<TIO, 1>(a, z, s)
-                        : z.nt == 2 ? stream<TIO, 2>(a, z, s)
-                        : z.nt == 4 ? stream<TIO, 4>(a, z, s)
-                                    : launch_kv4_prompt(a, z.s, dtype, s);
+static cudaError_t stream_and_join(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
+  const cudaError_t e = z.nt == 1 ? stream<TIO, 1>(a, z, s) : z.nt == 2 ? stream<TIO, 2>(a, z, s) : stream<TIO, 4>(a, z, s);
   return e == cudaSuccess ? join<TIO>(a, z, s) : e;
 }
 
@@ -730,8 +734,7 @@ bool kv4_attend_fits(const Kv4Args& a, const Plan& p, bool ragged) {
 }
 
 size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, bool ragged) {
-  const StreamShape z = stream_shape(a, p, ragged);
-  return (size_t)z.slots * ((size_t)66 * 4 << (a.lgG + z.s.lg_rows));
+  return stream_shape(a, p, ragged).bytes;
 }
 
 int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void* stream_) {
@@ -743,7 +746,9 @@ int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void
   if (z.s.items > 0) {
     z.s.part_o = static_cast<float*>(ws);
     z.s.part_ml = reinterpret_cast<float2*>(z.s.part_o + ((size_t)z.slots * kD << (a.lgG + z.s.lg_rows)));
-    e = dtype == SFA_BF16 ? stream_and_join<bf16>(a, z, dtype, s) : stream_and_join<float>(a, z, dtype, s);
+    e = z.nt == kPromptColumns / 8 ? launch_kv4_prompt(a, z.s, dtype, ws, s)
+        : dtype == SFA_BF16        ? stream_and_join<bf16>(a, z, s)
+                                   : stream_and_join<float>(a, z, s);
     return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
   }
   const int tiles = (int)((std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS) + 15) / 16);

@@ -1,52 +1,151 @@
 // Prompts over the paged 4-bit cache: many query rows a request, on the
 // fifth-generation tensor cores.
 //
-// An item is 128 columns (128 / G rows x the G heads of a KV head) of one
-// request, a step 128 keys.  Per step
+// An item is two tiles of 128 columns (256 / G rows x the G heads of a KV head)
+// of one request, a step 128 keys.  Per step
 //   four warps turn the raw codes and scales (as the copying warp brings them)
 //     into f16 keys and values in shared memory, a thread a key: code * scale
 //     is a whole f16 number;
-//   one thread issues S = Q K^T, twice (the query's two f16 parts: logits good
-//     to fp32's last bits), 128 x 128 sums in tensor memory;
-//   four warps, a thread a column of the item (a lane of tensor memory), take
-//     the maximum, exponentiate, and put P in f16 back into tensor memory, where
-//     the same issuing thread takes it as the left operand of O += P V.
-// fp32 outputs add a second product with what rounding P to f16 dropped (it
-// takes the place of the logits already read).
-// Two CTAs an SM: one's exponentials run under the other's products.  What
-// bounds it is the softmax: 128 x 128 exponentials, scalings and packings a
-// step against 384 clocks of products.
+//   one thread issues S = Q K^T for each tile, twice (the query's two f16
+//     parts: logits good to fp32's last bits), 128 x 128 sums in tensor memory;
+//   four warps a tile, a thread a column (a lane of tensor memory), take the
+//     maximum, exponentiate, and put P in f16 back into tensor memory, where
+//     the issuing thread takes it as the left operand of O += P V.
+// One tile's exponentials run under the other's products, and both use the same
+// keys and values.  fp32 outputs add a second product with what rounding P to
+// f16 dropped (it takes the place of logits already read).  What bounds it is
+// the softmax: 2 x 128 x 128 exponentials, scalings, sums and packings a step
+// against 768 clocks of products.
 //
-// Work is cut and shared out as for single rows (sfa_kv4_stream.cuh), chunks
-// joined by the same kernel.
+// The steps of all (item, KV head) units, in order, are shared out evenly over
+// one CTA an SM, to the step: units are long and few, and whole chunks of them
+// left a quarter of the SMs' time idle.  A unit that spans CTAs leaves a part
+// from each in the workspace (two a CTA at most), joined by a second kernel; so
+// the last bits of a split row depend on the batch it is in.
 #include "sfa_kv4_stream.cuh"
 #include "sfa_launch.cuh"
 #include "sfa_umma.cuh"
 
 namespace sfa {
 
-constexpr int kPSlots = 6, kStep = 128;
-constexpr int kPWarps = 10, kPThreads = 32 * kPWarps;  // softmax 0-3, dequantise 4-7, copy 8, products 9
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 192, kPCols = 256;
-// shared memory: Q hi, Q lo, K, V (128 rows of 128 bytes each, 128-byte
-// swizzle), the raw ring, then what is small
+constexpr int kPSlots = 8, kStep = 128;
+constexpr int kPWarps = 14, kPThreads = 32 * kPWarps;  // softmax 0-3 and 4-7, dequantise 8-11, copy 12, products 13
+// tensor memory of a tile: logits, probabilities, outputs
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 192, kColTile = 256, kPCols = 512;
+// shared memory: Q [tile][part], K [2], V [2] (128 rows of 128 bytes each,
+// 128-byte swizzle), the raw ring, then what is small
 constexpr int kPTile = 128 * 128;
-constexpr int kPromptSmem = 4 * kPTile + kPSlots * kTileBytes + 1024;
+constexpr int kPromptSmem = 8 * kPTile + kPSlots * kTileBytes + 1024;
 
 struct PromptShared {
   uint64_t raw_full[kPSlots], raw_empty[kPSlots];
-  uint64_t k_full, v_full, s_full, p_full, pv_done, q_full;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by step parity
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full[2];   // by tile
   int pages[kPSlots];
-  int step_pages[2];    // pages there of a step's two tiles: bits 0-3 and 4-7
-  int step_nan[2][4];   // whether a warp's values of the step hold a NaN
+  int step_pages[2];      // pages there of a step's two 64-key tiles: bits 0-3 and 4-7
+  int step_nan[2][4];     // whether a warp's values of the step hold a NaN
   uint8_t nan[2][kStep];  // per key: the scale blocks of its value that are NaN
-  int sums[kPWarps], where[4];
+  int sums[kPWarps], where[3];
   uint32_t tmem;
 };
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  tmem_ld16(taddr, v);
-  tmem_ld16(taddr + 16, v + 16);
+// Parts of split units: two a CTA, [column][64] and (m, l); which parts a unit has.
+struct PromptParts {
+  float* o;     // [2 kSMs][256][64]
+  float2* ml;   // [2 kSMs][256]
+  int2* units;  // [unit]: first part, their number
+};
+
+__device__ __forceinline__ int first_tile(const StreamArgs& s, const Item& it) { return max(0, it.pfirst - s.W) / kTile; }
+// Steps of an (item, KV head): 1 for an empty one, 0 for none.
+__device__ __forceinline__ int item_steps(const StreamArgs& s, const Item& it) {
+  return it.nch == 0 ? 0 : it.plast() < 0 ? 1 : (it.plast() / kTile - first_tile(s, it)) / 2 + 1;
+}
+
+// A CTA's piece of a unit: its steps s0 .. s1 - 1, tiles tb .. te - 1.
+struct Piece {
+  Item it;
+  int x, h, s0, s1, steps, tb, te;
+  int at, end;  // steps before this piece's first; the CTA's end
+  __device__ __forceinline__ void set(const StreamArgs& s, int from) {
+    steps = item_steps(s, it);
+    s0 = from;
+    s1 = min(steps, s0 + end - at);
+    const int t0 = first_tile(s, it);
+    tb = t0 + 2 * s0;
+    te = it.plast() < 0 ? tb : min(t0 + 2 * s1, it.plast() / kTile + 1);
+  }
+  __device__ __forceinline__ bool next(const Kv4Args& a, const StreamArgs& s) {
+    at += s1 - s0;
+    if (at >= end) return false;
+    if (++h == a.Hkv) {
+      h = 0;
+      do {
+        if (x + 1 >= s.items) return false;
+        it = item_at(a, s, ++x);
+      } while (it.nch == 0);
+    }
+    set(s, 0);
+    return true;
+  }
+};
+
+// The steps' shares: CTA b begins at share * b + min(b, rest).
+struct Shares {
+  int share, rest;
+  __device__ __forceinline__ int begin(int b) const { return share * b + min(b, rest); }
+  __device__ __forceinline__ int owner(int step) const {
+    const int big = (share + 1) * rest;
+    return step < big ? step / (share + 1) : rest + (step - big) / share;
+  }
+};
+
+// This CTA's first piece; false if it has none.  Called by all threads.
+__device__ __forceinline__ bool find_piece(const Kv4Args& a, const StreamArgs& sa, int* sums, int* where, Shares& sh, Piece& cur) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (sa.items + kPThreads - 1) / kPThreads;
+  const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
+  int mine = 0;
+  for (int x = x0; x < x1; ++x) mine += item_steps(sa, item_at(a, sa, x)) * a.Hkv;
+  int inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += y;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPWarps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  sh.share = total / (int)gridDim.x;
+  sh.rest = total - sh.share * (int)gridDim.x;
+  const int first = sh.begin(blockIdx.x), last = sh.begin(blockIdx.x + 1);
+  if (first < last && first >= before && first < before + mine) {
+    int at = before;
+    for (int x = x0; x < x1; ++x) {
+      const int n = item_steps(sa, item_at(a, sa, x));
+      if (first < at + n * a.Hkv) {
+        where[0] = x;
+        where[1] = (first - at) / n;
+        where[2] = (first - at) % n;
+        break;
+      }
+      at += n * a.Hkv;
+    }
+  }
+  __syncthreads();
+  if (first == last) return false;
+  cur.x = where[0];
+  cur.h = where[1];
+  cur.at = first;
+  cur.end = last;
+  cur.it = item_at(a, sa, cur.x);
+  cur.set(sa, where[2]);
+  return true;
 }
 
 // 64 codes and 4 scales -> a row of f16 at row r of a swizzled tile; zero: zeros.
@@ -66,15 +165,103 @@ __device__ __forceinline__ void dequantise_row(const uint8_t* codes, uint32_t sc
   }
 }
 
+// Two fp32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// The keys of a step that a column attends.
+struct Keys {
+  int lo, hi, pages, lgr;
+  __device__ __forceinline__ bool attended(int k) const {
+    return k >= lo && k <= hi && (pages >> ((k >> 6) * 4 + ((k & 63) >> lgr)) & 1);
+  }
+};
+
+// Logits of 32 keys from c on, at v; the next 32 are asked for before they are used.
+template <bool MASKED>
+__device__ __forceinline__ void column_take(uint32_t s, int c, const Keys& keys, float* v, float* next, bool more) {
+  tmem_wait_ld32(v);
+  if (more) tmem_ld32(s + c + 32, next);
+  if (MASKED)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!keys.attended(c + e)) v[e] = -INFINITY;
+}
+
+// The largest of a column's 128 logits (its own lane of tensor memory).  Both
+// walks are loops over 64 keys: unrolled over 128, with the masked form beside
+// it, the eight softmax warps waited for instructions longer than they ran.
+template <bool MASKED>
+__device__ __forceinline__ float column_top(uint32_t s, const Keys& keys) {
+  float top = -INFINITY, v[2][32];
+  tmem_ld32(s, v[0]);
+#pragma unroll 1
+  for (int c = 0; c < kStep; c += 64)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      column_take<MASKED>(s, c + 32 * h, keys, v[h], v[h ^ 1], h == 0 || c == 0);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(v[h][e], v[h][e + 1]));
+    }
+  return top;
+}
+
+// P = 2^(s cs + off) of a column, into tensor memory; returns their sum.
+template <bool EXACT, bool MASKED>
+__device__ __forceinline__ float column_exp(uint32_t tl, const Keys& keys, float cs, float off) {
+  const float2 cs2 = make_float2(cs, cs), off2 = make_float2(off, off);
+  float2 sum = make_float2(0.0f, 0.0f);
+  float v[2][32];
+  tmem_ld32(tl + kColS, v[0]);
+#pragma unroll 1
+  for (int c = 0; c < kStep; c += 64)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      column_take<MASKED>(tl + kColS, c + 32 * h, keys, v[h], v[h ^ 1], h == 0 || c == 0);
+      float w[16];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const float2 y = fma2(make_float2(v[h][e], v[h][e + 1]), cs2, off2);
+        v[h][e] = ex2(y.x);
+        v[h][e + 1] = ex2(y.y);
+        sum = add2(sum, make_float2(v[h][e], v[h][e + 1]));
+        w[e >> 1] = __uint_as_float(pack_f16(v[h][e], v[h][e + 1]));
+      }
+      tmem_st16(tl + kColP + c / 2 + 16 * h, w);
+      if (EXACT) {  // the rest of P goes over logits that have been read (those asked for lie behind)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 r = unpack_f16(__float_as_uint(w[e]));
+          w[e] = __uint_as_float(pack_f16(v[h][2 * e] - r.x, v[h][2 * e + 1] - r.y));
+        }
+        tmem_st16(tl + kColS + c / 2 + 16 * h, w);
+      }
+    }
+  return sum.x + sum.y;
+}
+
 template <typename TIO>
-__global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(const Kv4Args a, const StreamArgs sa) {
+__global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args a, const StreamArgs sa, const PromptParts parts) {
   constexpr bool kExact = sizeof(TIO) == 4;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PromptShared sh;
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* const kt = smem + 2 * kPTile;
-  uint8_t* const vt = smem + 3 * kPTile;
-  uint8_t* const raw = smem + 4 * kPTile;
+  uint8_t* const kt = smem + 4 * kPTile;
+  uint8_t* const vt = smem + 6 * kPTile;
+  uint8_t* const raw = smem + 8 * kPTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   if (tid == 0) {
@@ -82,12 +269,16 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
       mbar_init(smem_u32(&sh.raw_full[i]), 1);
       mbar_init(smem_u32(&sh.raw_empty[i]), 4);
     }
-    mbar_init(smem_u32(&sh.k_full), 4);
-    mbar_init(smem_u32(&sh.v_full), 4);
-    mbar_init(smem_u32(&sh.s_full), 2);  // the products' end, and the issuing thread: what it has seen of the step, its readers see
-    mbar_init(smem_u32(&sh.p_full), 4);
-    mbar_init(smem_u32(&sh.pv_done), 1);
-    mbar_init(smem_u32(&sh.q_full), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.k_full[i]), 4);
+      mbar_init(smem_u32(&sh.k_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_full[i]), 4);
+      mbar_init(smem_u32(&sh.v_empty[i]), 1);
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.p_full[i]), 4);
+      mbar_init(smem_u32(&sh.pv_done[i]), 1);
+      mbar_init(smem_u32(&sh.q_full[i]), 4);
+    }
     mbar_fence_init();
   }
   if (warp == kPWarps - 1) {
@@ -95,93 +286,123 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
     tmem_relinquish();
   }
   pdl_wait();
-  Cursor cur;
+  Piece cur;
+  Shares shares;
   tc05_fence_before();
-  const bool work = find_run<kPThreads>(a, sa, sh.sums, sh.where, cur);  // (two barriers of the CTA inside)
+  const bool work = find_piece(a, sa, sh.sums, sh.where, shares, cur);  // (two barriers of the CTA inside)
   tc05_fence_after();
   const uint32_t tm = sh.tmem;
   const int G = 1 << a.lgG;
-  bool dead = false;
+  bool dead = false;  // a wait ran out: no more waits, no more work
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
-    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait_bounded(smem_u32(bar), phase, a.wait_cycles));
+    if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait_bounded(smem_u32(bar), phase & 1, a.wait_cycles));
   };
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(bar));
   };
-  int j = 0, n = 0, nq = 0;  // steps, raw tiles and query loads before the current one
-  int qx = -1, qh = -1;
   if (!work) {
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     copy_run<kPSlots>(a, sa, cur, smem_u32(raw), smem_u32(sh.raw_full), smem_u32(sh.raw_empty), sh.pages,
                       cur.at == 0 ? a.debug_skip : -1, lane);
-  } else if (warp == 9) {
+  } else if (warp == 13) {
     // ---- the products
     constexpr uint32_t idS = idesc_f16(128, kStep, false, false), idO = idesc_f16(128, 64, false, true);
     const uint32_t q0 = smem_u32(smem), k0 = smem_u32(kt), v0 = smem_u32(vt);
-    int last = 0;  // steps whose S product was issued
-    do {
-      if (cur.te > cur.tb && (cur.x != qx || cur.h != qh)) {
-        qx = cur.x;
-        qh = cur.h;
-        wait(&sh.q_full, nq++ & 1);
-      }
-      for (int t = cur.tb; t < cur.te && !dead; t += 2, ++j) {
-        wait(&sh.k_full, j & 1);
-        if (dead) break;
-        if (lane == 0) {
-          tc05_fence_after();
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16(tm + kColS, smem_desc_sw128(q0 + part * kPTile + 32 * k, 16, 1024), smem_desc_sw128(k0 + 32 * k, 16, 1024), idS,
-                        part + k > 0);
-          umma_commit(smem_u32(&sh.s_full));
-          mbar_arrive(smem_u32(&sh.s_full));
-        }
-        last = j + 1;
-        wait(&sh.v_full, j & 1);
-        wait(&sh.p_full, j & 1);  // (with a chunk's first step: the last chunk's O has been read)
-        if (dead) break;
-        if (lane == 0) {
-          tc05_fence_after();
-#pragma unroll
-          for (int part = 0; part < (kExact ? 2 : 1); ++part)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_ts(tm + kColO, tm + (part ? kColS : kColP) + 8 * k, smem_desc_sw128(v0 + 2048 * k, 8192, 1024), idO,
-                      t > cur.tb || part + k > 0);
-          umma_commit(smem_u32(&sh.pv_done));
-        }
-        if (kExact) wait(&sh.pv_done, j & 1);  // the logits' columns hold the rest of P until then
-      }
-    } while (!dead && cur.next(a, sa));
-    if (dead) {  // products still under way end before their memory goes
+    int nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};  // query loads, logit and value products of each tile
+    // S = Q K^T of tile T in step j; last: the step's last one
+    auto logits = [&](int T, int j, bool fresh, bool last) {
+      if (fresh) wait(&sh.q_full[T], nq[T]++);
+      wait(&sh.k_full[j & 1], j >> 1);
+      if (kExact && ns[T] > 0) wait(&sh.pv_done[T], ns[T] - 1);  // the logits' columns hold the rest of P until then
+      if (dead) return;
       if (lane == 0) {
-        record_status(a.status, SFA_ERR_TIMEOUT);
-        if (last > 0) mbar_wait_bounded(smem_u32(&sh.s_full), (last - 1) & 1, a.wait_cycles);
-        if (last > 1) mbar_wait_bounded(smem_u32(&sh.pv_done), (last - 2) & 1, a.wait_cycles);
+        tc05_fence_after();
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tm + kColTile * T + kColS, smem_desc_sw128(q0 + (2 * T + part) * kPTile + 32 * k, 16, 1024),
+                      smem_desc_sw128(k0 + (j & 1) * kPTile + 32 * k, 16, 1024), idS, part + k > 0);
+        umma_commit(smem_u32(&sh.s_full[T]));
+        if (last) umma_commit(smem_u32(&sh.k_empty[j & 1]));
+      }
+      ++ns[T];
+    };
+    // O (+)= P V
+    auto outputs = [&](int T, int j, bool begin, bool last) {
+      wait(&sh.v_full[j & 1], j >> 1);
+      wait(&sh.p_full[T], np[T]);  // (with a piece's first step: the last piece's O has been read)
+      if (dead) return;
+      if (lane == 0) {
+        tc05_fence_after();
+#pragma unroll
+        for (int part = 0; part < (kExact ? 2 : 1); ++part)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_ts(tm + kColTile * T + kColO, tm + kColTile * T + (part ? kColS : kColP) + 8 * k,
+                    smem_desc_sw128(v0 + (j & 1) * kPTile + 2048 * k, 8192, 1024), idO, !begin || part + k > 0);
+        umma_commit(smem_u32(&sh.pv_done[T]));
+        if (last) umma_commit(smem_u32(&sh.v_empty[j & 1]));
+      }
+      ++np[T];
+    };
+    bool more = true;
+    while (more && cur.te == cur.tb) more = cur.next(a, sa);
+    int t = cur.tb, j = 0;
+    bool two = (cur.it.nrows << a.lgG) > 128;
+    if (more) {
+      logits(0, 0, true, !two);
+      if (two) logits(1, 0, true, true);
+    }
+    while (more && !dead) {
+      const bool begin = t == cur.tb, was_two = two;
+      bool fresh = false;
+      t += 2;
+      if (t >= cur.te) {
+        do more = cur.next(a, sa);
+        while (more && cur.te == cur.tb);
+        fresh = true;
+        t = cur.tb;
+        two = (cur.it.nrows << a.lgG) > 128;
+      }
+      outputs(0, j, begin, !was_two);
+      if (more && !fresh) logits(0, j + 1, false, !two);
+      if (was_two) outputs(1, j, begin, true);
+      if (more && !fresh && two) logits(1, j + 1, false, true);
+      if (more && fresh) {
+        logits(0, j + 1, true, !two);
+        if (two) logits(1, j + 1, true, true);
+      }
+      ++j;
+    }
+    if (dead && lane == 0) {  // products still under way end before their memory goes
+      record_status(a.status, SFA_ERR_TIMEOUT);
+      for (int T = 0; T < 2; ++T) {
+        if (ns[T] > 0) mbar_wait_bounded(smem_u32(&sh.s_full[T]), (ns[T] - 1) & 1, a.wait_cycles);
+        if (np[T] > 0) mbar_wait_bounded(smem_u32(&sh.pv_done[T]), (np[T] - 1) & 1, a.wait_cycles);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ---- codes to f16, a thread a key of the step
-    const int key = tid - 128, half = key >> 6, k64 = key & 63;
+    const int key = tid - 256, half = key >> 6, k64 = key & 63;
     const int lgr = min(a.lgS, 6);
+    int j = 0, n = 0;  // steps and raw tiles before the current one
     do {
       for (int t = cur.tb; t < cur.te && !dead; t += 2, ++j) {
         const bool two = t + 1 < cur.te;
-        const int s0 = n % kPSlots, s1 = (n + 1) % kPSlots;
-        wait(&sh.raw_full[s0], n / kPSlots & 1);
-        if (two) wait(&sh.raw_full[s1], (n + 1) / kPSlots & 1);
-        const int slot = half ? s1 : s0;
+        const int s0 = n % kPSlots, s1 = (n + 1) % kPSlots, buf = j & 1;
+        wait(&sh.raw_full[s0], n / kPSlots);
+        if (two) wait(&sh.raw_full[s1], (n + 1) / kPSlots);
         const int pg0 = sh.pages[s0], pg1 = two ? sh.pages[s1] : 0;
-        const uint8_t* T = raw + slot * kTileBytes;
+        const uint8_t* T = raw + (half ? s1 : s0) * kTileBytes;
         const bool zero = (half && !two) || t * kTile + key > cur.it.plast() || !((half ? pg1 : pg0) >> (k64 >> lgr) & 1);
         const uint2 sc = zero ? make_uint2(0, 0) : *reinterpret_cast<const uint2*>(T + 64 * kTile + 8 * k64);
-        if (j > 0) wait(&sh.s_full, (j - 1) & 1);  // the last step's keys have been read
+        if (j > 1) wait(&sh.k_empty[buf], (j >> 1) - 1);
         if (dead) break;
-        dequantise_row(T + 32 * k64, sc.x, zero, kt, key);
+        dequantise_row(T + 32 * k64, sc.x, zero, kt + buf * kPTile, key);
+        fence_async_smem();
+        arrive(&sh.k_full[buf]);
         // a NaN value block is stored as zeros: the columns that attend its key are told (0 * NaN would reach all)
         uint32_t nan = 0, vs = sc.y;
 #pragma unroll
@@ -190,20 +411,17 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
             nan |= 1u << b;
             vs &= ~(255u << (8 * b));
           }
-        const int buf = j & 1;
-        sh.nan[buf][key] = (uint8_t)nan;
         const bool any = __any_sync(0xffffffffu, nan != 0);
-        if (lane == 0) {
-          sh.step_nan[buf][warp - 4] = any;
-          if (warp == 4) sh.step_pages[buf] = pg0 | pg1 << 4;
-        }
-        fence_async_smem();
-        arrive(&sh.k_full);
-        if (j > 0) wait(&sh.pv_done, (j - 1) & 1);  // and its values
+        if (j > 1) wait(&sh.v_empty[buf], (j >> 1) - 1);  // (both tiles have done with that step)
         if (dead) break;
-        dequantise_row(T + 32 * kTile + 32 * k64, vs, zero, vt, key);
+        sh.nan[buf][key] = (uint8_t)nan;
+        if (lane == 0) {
+          sh.step_nan[buf][warp - 8] = any;
+          if (warp == 8) sh.step_pages[buf] = pg0 | pg1 << 4;
+        }
+        dequantise_row(T + 32 * kTile + 32 * k64, vs, zero, vt + buf * kPTile, key);
         fence_async_smem();
-        arrive(&sh.v_full);
+        arrive(&sh.v_full[buf]);
         if (lane == 0) {
           mbar_arrive(smem_u32(&sh.raw_empty[s0]));
           if (two) mbar_arrive(smem_u32(&sh.raw_empty[s1]));
@@ -214,19 +432,34 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
     if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
   } else {
     // ---- softmax, a thread a column
-    const uint32_t tl = tm + ((uint32_t)(32 * warp) << 16);  // this warp's lanes of tensor memory
+    const int T = warp >> 2, lane_row = tid & 127;
+    const uint32_t tl = tm + kColTile * T + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes of tensor memory
+    uint8_t* const qt = smem + 2 * T * kPTile;
     const int row = tid >> a.lgG, lgr = min(a.lgS, 6);
     const int all_pages = (1 << (kTile >> lgr)) - 1;
     const int full_pages = all_pages | all_pages << 4;
+    // Steps before the current one, and those in which this tile had columns.  A barrier's phase is
+    // known by its parity alone, and a tile may sit steps out: once its own logits are there, the
+    // step's other barriers are at that step's phase.
+    int j = 0, jt = 0;
     float cs = 0.0f;
+    bool first = true;  // the CTA's first piece
     do {
       const int ncol = cur.it.nrows << a.lgG;
+      if (tid == 0 && cur.s0 == 0) {  // the unit begins here: which parts it leaves
+        const int b = blockIdx.x, count = shares.owner(cur.at + cur.steps - 1) - b + 1;
+        parts.units[(int64_t)cur.x * a.Hkv + cur.h] = make_int2(2 * b + (first ? 0 : 1), count);
+      }
+      const bool whole = cur.s0 == 0 && cur.s1 == cur.steps;
+      if (ncol <= 128 * T) {  // no column of this tile
+        j += (cur.te - cur.tb + 1) >> 1;
+        first = false;
+        continue;
+      }
       const bool mine = tid < ncol;
       const int p = cur.it.pfirst + row, head = cur.h * G + (tid & (G - 1));
       const int64_t out_row = cur.it.row0 + row;
-      if (cur.te > cur.tb && (cur.x != qx || cur.h != qh)) {
-        qx = cur.x;
-        qh = cur.h;
+      if (cur.te > cur.tb) {
         // the column's query: rotated, scaled by a power of two to its own size, in two f16 parts.  The
         // products that read the last one have ended: this thread has seen their sums
         const TIO* src = static_cast<const TIO*>(a.q) + out_row * a.q_stride + head * kD;
@@ -258,40 +491,29 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
               const float2 r = unpack_f16(h[e]);
               l[e] = pack_f16(u - r.x, v - r.y);
             }
-            *reinterpret_cast<uint4*>(smem + swz(tid, c + 4 * i)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(smem + kPTile + swz(tid, c + 4 * i)) = make_uint4(l[0], l[1], l[2], l[3]);
+            *reinterpret_cast<uint4*>(qt + swz(lane_row, c + 4 * i)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(qt + kPTile + swz(lane_row, c + 4 * i)) = make_uint4(l[0], l[1], l[2], l[3]);
           }
         }
         fence_async_smem();
-        arrive(&sh.q_full);
+        arrive(&sh.q_full[T]);
       }
       float m = -INFINITY, l = 0.0f;
       uint32_t nans = 0;  // scale blocks of the output that an attended NaN reaches
-      for (int t = cur.tb; t < cur.te && !dead; t += 2, ++j) {
+      for (int t = cur.tb; t < cur.te && !dead; t += 2, ++j, ++jt) {
         const int buf = j & 1, j0 = t * kTile;
-        wait(&sh.s_full, j & 1);
+        wait(&sh.s_full[T], jt);
+        wait(&sh.v_full[buf], j >> 1);  // (what is said about the step's keys; in this order, see below)
         if (dead) break;
         tc05_fence_after();
         const int pg = sh.step_pages[buf];
         const bool full = pg == full_pages && j0 + kStep - 1 <= cur.it.pfirst && j0 >= cur.it.plast() - sa.W;
         const int k_lo = max(p - sa.W - j0, 0), k_hi = mine ? min(p - j0, kStep - 1) : -1;
-        auto attends = [&](int k) { return k >= k_lo && k <= k_hi && (pg >> ((k >> 6) * 4 + ((k & 63) >> lgr)) & 1); };
+        const Keys keys = {k_lo, k_hi, pg, lgr};
         if (sh.step_nan[buf][0] | sh.step_nan[buf][1] | sh.step_nan[buf][2] | sh.step_nan[buf][3])
           for (int k = 0; k < kStep; ++k)
-            if (sh.nan[buf][k] && attends(k)) nans |= sh.nan[buf][k];
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kStep; c += 32) {
-          float s[32];
-          tmem_ld32(tl + kColS + c, s);
-          tmem_wait_ld();
-          if (!full)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!attends(c + e)) s[e] = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, s[e]);
-        }
+            if (sh.nan[buf][k] && keys.attended(k)) nans |= sh.nan[buf][k];
+        float top = full ? column_top<false>(tl + kColS, keys) : column_top<true>(tl + kColS, keys);
         top *= cs;
         // the maximum moves only when a logit passes it by more than kLag
         const bool move = top > m + kLag;
@@ -301,7 +523,7 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
           m = top;
           l *= corr;
         }
-        if (j > 0) wait(&sh.pv_done, (j - 1) & 1);  // P's columns are free, O stands still
+        if (jt > 0) wait(&sh.pv_done[T], jt - 1);  // P's columns are free, O stands still
         if (dead) break;
         tc05_fence_after();
         if (t > cur.tb && __any_sync(0xffffffffu, move)) {
@@ -316,44 +538,17 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
           }
         }
         const float off = m == -INFINITY ? 0.0f : kPShift - m;
-        float part[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < kStep; c += 32) {
-          float s[32], w[16];
-          tmem_ld32(tl + kColS + c, s);
-          tmem_wait_ld();
-          if (!full)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!attends(c + e)) s[e] = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            s[e] = ex2(fmaf(s[e], cs, off));
-            part[e & 1] += s[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = __uint_as_float(pack_f16(s[2 * e], s[2 * e + 1]));
-          tmem_st16(tl + kColP + c / 2, w);
-          if (kExact) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 r = unpack_f16(__float_as_uint(w[e]));
-              w[e] = __uint_as_float(pack_f16(s[2 * e] - r.x, s[2 * e + 1] - r.y));
-            }
-            tmem_st16(tl + kColS + c / 2, w);  // over logits that have been read
-          }
-        }
-        l += part[0] + part[1];
+        l += full ? column_exp<kExact, false>(tl, keys, cs, off) : column_exp<kExact, true>(tl, keys, cs, off);
         tmem_wait_st();
         tc05_fence_before();
-        arrive(&sh.p_full);
+        arrive(&sh.p_full[T]);
       }
       const bool any = cur.te > cur.tb;  // (an empty item has no step)
       if (any) {
-        wait(&sh.pv_done, (j - 1) & 1);
+        wait(&sh.pv_done[T], jt - 1);
         tc05_fence_after();
       }
-      const int64_t at = (((int64_t)cur.x * a.Hkv + cur.h) * sa.max_chunks + cur.c - cur.it.c0) * kPromptColumns + tid;
+      const int64_t at = (int64_t)(2 * blockIdx.x + (first ? 0 : 1)) * kPromptColumns + tid;
 #pragma unroll
       for (int c = 0; c < 64; c += 16) {
         float o[16];
@@ -368,16 +563,17 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = __int_as_float(0x7fffffff);
         if (!mine) {
-        } else if (cur.it.nch == 1) {
+        } else if (whole) {
           write_head<TIO>(a, out_row, head, c / 8, o, m, l);
           write_head<TIO>(a, out_row, head, c / 8 + 1, o + 8, m, l);
         } else {
-          store8(sa.part_o + at * kD + c, o);
-          store8(sa.part_o + at * kD + c + 8, o + 8);
-          if (c == 0) sa.part_ml[at] = make_float2(m, l);
+          store8(parts.o + at * kD + c, o);
+          store8(parts.o + at * kD + c + 8, o + 8);
+          if (c == 0) parts.ml[at] = make_float2(m, l);
         }
       }
       tc05_fence_before();
+      first = false;
     } while (!dead && cur.next(a, sa));
     if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
   }
@@ -387,12 +583,50 @@ __global__ void __launch_bounds__(kPThreads, kPromptCtas) kv4_prompt_kernel(cons
   if (warp == kPWarps - 1) tmem_dealloc(tm, kPCols);
 }
 
-cudaError_t launch_kv4_prompt(const Kv4Args& a, const StreamArgs& s, int dtype, cudaStream_t stream) {
-  static_assert((kPromptSmem + (int)sizeof(PromptShared) + 1024) * kPromptCtas <= 228 * 1024, "CTAs an SM");
+// The parts of one unit joined, in the order of their keys: 32 columns a CTA, 8
+// lanes a column.
+template <typename TIO>
+__global__ void __launch_bounds__(256) kv4_prompt_join_kernel(const Kv4Args a, const StreamArgs sa, const PromptParts parts) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int x = blockIdx.x / a.Hkv, h = blockIdx.x - x * a.Hkv, G = 1 << a.lgG;
+  const Item it = item_at(a, sa, x);
+  const int col = 32 * blockIdx.y + (threadIdx.x >> 3), d = threadIdx.x & 7;
+  if (it.nch == 0 || col >= it.nrows << a.lgG) return;
+  const int2 u = parts.units[blockIdx.x];
+  if (u.y <= 1) return;
+  // its first part is the last of CTA u.x / 2 or all of it; the others are their CTAs' first
+  auto place = [&](int i) { return (int64_t)(i == 0 ? u.x : 2 * (u.x / 2 + i)) * kPromptColumns + col; };
+  float M = -INFINITY, l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int i = 0; i < u.y; ++i) M = fmaxf(M, parts.ml[place(i)].x);
+  for (int i = 0; i < u.y; ++i) {
+    const float2 v = parts.ml[place(i)];
+    const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - M);
+    float z[8];
+    load8(parts.o + place(i) * kD + 8 * d, z);
+    l = fmaf(v.y, f, l);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], f, y[e]);
+  }
+  write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M, l);
+}
+
+static constexpr size_t kPartBytes = (size_t)2 * kSMs * kPromptColumns * (kD + 2) * sizeof(float);
+
+size_t prompt_workspace(int64_t units) { return kPartBytes + (size_t)units * sizeof(int2); }
+
+cudaError_t launch_kv4_prompt(const Kv4Args& a, StreamArgs s, int dtype, void* ws, cudaStream_t stream) {
+  static_assert(kPromptSmem + (int)sizeof(PromptShared) + 1024 <= 228 * 1024, "shared memory of an SM");
+  PromptParts parts;
+  parts.o = static_cast<float*>(ws);
+  parts.ml = reinterpret_cast<float2*>(parts.o + (size_t)2 * kSMs * kPromptColumns * kD);
+  parts.units = reinterpret_cast<int2*>(parts.ml + (size_t)2 * kSMs * kPromptColumns);
   auto kern = dtype == SFA_BF16 ? kv4_prompt_kernel<bf16> : kv4_prompt_kernel<float>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmem);
+  auto join = dtype == SFA_BF16 ? kv4_prompt_join_kernel<bf16> : kv4_prompt_join_kernel<float>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmem);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(kSMs), dim3(kPThreads), kPromptSmem, stream, a, s, parts);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(kSMs * kPromptCtas), dim3(kPThreads), kPromptSmem, stream, a, s);
+  return launch_pdl(join, dim3((unsigned)(s.items * a.Hkv), kPromptColumns / 32), dim3(256), 0, stream, a, s, parts);
 }
 
 }  // namespace sfa

@@ -197,8 +197,8 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 
 // The copying warp: every tile of the CTA's run, in order, into slot n mod
 // SLOTS as soon as tile n - SLOTS has been read.
-template <int SLOTS>
-__device__ __forceinline__ void copy_run(const Kv4Args& a, const StreamArgs& sa, Cursor cur, uint32_t ring, uint32_t full, uint32_t empty,
+template <int SLOTS, typename CURSOR>
+__device__ __forceinline__ void copy_run(const Kv4Args& a, const StreamArgs& sa, CURSOR cur, uint32_t ring, uint32_t full, uint32_t empty,
                                          volatile int* pages, int skip, int lane) {
   const int S = 1 << a.lgS, rows = min(S, kTile), np = kTile / rows, lgnp = __ffs(np) - 1, batch = 32 >> lgnp;
   const int64_t block = kKv4Row * S;
@@ -252,8 +252,10 @@ __device__ __forceinline__ void copy_run(const Kv4Args& a, const StreamArgs& sa,
     if (i != skip && !mbar_wait_bounded(full + 8 * (i % SLOTS), i / SLOTS & 1, a.wait_cycles)) record_status(a.status, SFA_ERR_TIMEOUT);
 }
 
-// sfa_kv4_prompt.cu: the stream of many rows a request, 128 columns an item.
-constexpr int kPromptColumns = 128, kPromptCtas = 2;
-cudaError_t launch_kv4_prompt(const Kv4Args& a, const StreamArgs& s, int dtype, cudaStream_t stream);
+// sfa_kv4_prompt.cu: the stream of many rows a request, 256 columns an item,
+// with its join; ws: prompt_workspace(units) bytes.
+constexpr int kPromptColumns = 256;
+size_t prompt_workspace(int64_t units);
+cudaError_t launch_kv4_prompt(const Kv4Args& a, StreamArgs s, int dtype, void* ws, cudaStream_t stream);
 
 }  // namespace sfa

@@ -141,10 +141,16 @@ def _workspace(lib, **kw):
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 1), (32, 1), (4, 4)])
 @pytest.mark.parametrize("page,max_pages", [(64, 256), (16, 33), (128, 8192)])
 def test_workspace_holds_the_split_rows(sfa_lib, R, N, Hq, Hkv, page, max_pages):
-    """If any scratch is wanted there is room for two parts (m, l and 64 sums) of every row and head, with
-    ragged rows and with one row a request; its size stays within bounds however wide the block table."""
+    """Room for what the kernels leave there.  Prompts (64 columns and more a request on average): two
+    parts for each of 152 CTAs, 256 columns of m, l and 64 sums.  Other rows: two parts at least of every
+    row and head if any scratch is wanted, within a bound that the block table's width does not move, and
+    none for prefixes of one chunk."""
     kw = dict(n_pages=1 << 14, R=R, N=N, Hq=Hq, Hkv=Hkv, page=page, max_pages=max_pages, q_stride=Hq * 64)
     n = _workspace(sfa_lib, **kw)
+    prompts = 2 * 152 * 256 * 66 * 4
+    if Hq // Hkv * -(-N // R) >= 64:
+        assert prompts < n <= prompts + 8 * (N + R) * Hkv
+        return
     assert n >= 2 * N * Hq * 66 * 4 or (n == 0 and N > 2000)  # enough rows: none is split
-    assert n <= 8 * 304 * 128 * 66 * 4  # 82 MB
+    assert n <= 16 * 608 * 8 * 66 * 4 + 16 * 304 * 16 * 66 * 4
     assert _workspace(sfa_lib, **{**kw, "max_pages": 256 // page}) == 0
