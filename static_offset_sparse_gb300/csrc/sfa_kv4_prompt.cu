@@ -29,6 +29,13 @@
 namespace sfa {
 
 constexpr int kPSlots = 8, kStep = 128;
+// Probabilities times 2^8, relative to a maximum that lags the true one: the
+// 128 of a step then sum up to 2^15 at most while the maximum stands, and a sum
+// below 65000 says that none has left f16's range.  (fp32 outputs know the
+// maximum in every step and keep kPShift.)
+template <bool EXACT>
+constexpr float kPromptShift = EXACT ? kPShift : 8.0f;
+constexpr float kSumLimit = 65000.0f;
 constexpr int kPWarps = 14, kPThreads = 32 * kPWarps;  // softmax 0-3 and 4-7, dequantise 8-11, copy 12, products 13
 // tensor memory of a tile: logits, probabilities, outputs
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 192, kColTile = 256, kPCols = 512;
@@ -308,7 +315,9 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
   } else if (warp == 13) {
     // ---- the products
     constexpr uint32_t idS = idesc_f16(128, kStep, false, false), idO = idesc_f16(128, 64, false, true);
-    const uint32_t q0 = smem_u32(smem), k0 = smem_u32(kt), v0 = smem_u32(vt);
+    // descriptors' low words of the bases; a row is 128 bytes, a tile kPTile: in 16-byte units
+    constexpr uint32_t kHi = smem_desc_hi(1024), kTileU = kPTile / 16;
+    const uint32_t q0 = smem_desc_lo(smem_u32(smem), 16), k0 = smem_desc_lo(smem_u32(kt), 16), v0 = smem_desc_lo(smem_u32(vt), 8192);
     int nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};  // query loads, logit and value products of each tile
     // S = Q K^T of tile T in step j; last: the step's last one
     auto logits = [&](int T, int j, bool fresh, bool last) {
@@ -316,35 +325,31 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
       wait(&sh.k_full[j & 1], j >> 1);
       if (kExact && ns[T] > 0) wait(&sh.pv_done[T], ns[T] - 1);  // the logits' columns hold the rest of P until then
       if (dead) return;
-      if (lane == 0) {
+      if (elect_one()) {
         tc05_fence_after();
+        const uint32_t d = tm + kColTile * T + kColS, q = q0 + 2 * T * kTileU, k = k0 + (j & 1) * kTileU;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_bf16(tm + kColTile * T + kColS, smem_desc_sw128(q0 + (2 * T + part) * kPTile + 32 * k, 16, 1024),
-                      smem_desc_sw128(k0 + (j & 1) * kPTile + 32 * k, 16, 1024), idS, part + k > 0);
+        for (int i = 0; i < 8; ++i) umma_ss_lo(d, q + (i >> 2) * kTileU + 2 * (i & 3), k + 2 * (i & 3), kHi, idS, i > 0);
         umma_commit(smem_u32(&sh.s_full[T]));
         if (last) umma_commit(smem_u32(&sh.k_empty[j & 1]));
       }
+      __syncwarp();
       ++ns[T];
     };
     // O (+)= P V
     auto outputs = [&](int T, int j, bool begin, bool last) {
       wait(&sh.v_full[j & 1], j >> 1);
-      wait(&sh.p_full[T], np[T]);  // (with a piece's first step: the last piece's O has been read)
       if (dead) return;
-      if (lane == 0) {
+      if (elect_one()) {
         tc05_fence_after();
+        const uint32_t d = tm + kColTile * T, v = v0 + (j & 1) * kTileU;
 #pragma unroll
-        for (int part = 0; part < (kExact ? 2 : 1); ++part)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_ts(tm + kColTile * T + kColO, tm + kColTile * T + (part ? kColS : kColP) + 8 * k,
-                    smem_desc_sw128(v0 + (j & 1) * kPTile + 2048 * k, 8192, 1024), idO, !begin || part + k > 0);
+        for (int i = 0; i < (kExact ? 16 : 8); ++i)  // 16 keys: two groups of 8 rows
+          umma_ts_lo(d + kColO, d + (i >= 8 ? kColS : kColP) + 8 * (i & 7), v + 128 * (i & 7), kHi, idO, !begin || i > 0);
         umma_commit(smem_u32(&sh.pv_done[T]));
         if (last) umma_commit(smem_u32(&sh.v_empty[j & 1]));
       }
+      __syncwarp();
       ++np[T];
     };
     bool more = true;
@@ -366,10 +371,15 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         t = cur.tb;
         two = (cur.it.nrows << a.lgG) > 128;
       }
-      outputs(0, j, begin, !was_two);
-      if (more && !fresh) logits(0, j + 1, false, !two);
-      if (was_two) outputs(1, j, begin, true);
-      if (more && !fresh && two) logits(1, j + 1, false, true);
+      // the next logits first, where the queries stay: their readers wait longest (fp32 outputs: the rest
+      // of P lies there)
+      for (int T = 0; T < (was_two ? 2 : 1); ++T) {
+        const bool last = T == was_two;
+        wait(&sh.p_full[T], np[T]);  // the logits have been read (with a piece's first step: the last piece's O too)
+        if (more && !fresh && !kExact) logits(T, j + 1, false, last);
+        outputs(T, j, begin, last);
+        if (more && !fresh && kExact) logits(T, j + 1, false, last);
+      }
       if (more && fresh) {
         logits(0, j + 1, true, !two);
         if (two) logits(1, j + 1, true, true);
@@ -513,32 +523,38 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         if (sh.step_nan[buf][0] | sh.step_nan[buf][1] | sh.step_nan[buf][2] | sh.step_nan[buf][3])
           for (int k = 0; k < kStep; ++k)
             if (sh.nan[buf][k] && keys.attended(k)) nans |= sh.nan[buf][k];
-        float top = full ? column_top<false>(tl + kColS, keys) : column_top<true>(tl + kColS, keys);
-        top *= cs;
-        // the maximum moves only when a logit passes it by more than kLag
-        const bool move = top > m + kLag;
-        float corr = 1.0f;
-        if (move) {
-          corr = ex2(m - top);  // 0 on the first keys
-          m = top;
-          l *= corr;
-        }
         if (jt > 0) wait(&sh.pv_done[T], jt - 1);  // P's columns are free, O stands still
         if (dead) break;
         tc05_fence_after();
-        if (t > cur.tb && __any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            float o[16];
-            tmem_ld16(tl + kColO + c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= corr;
-            tmem_st16(tl + kColO + c, o);
+        // After a piece's first step P is taken with the maximum so far: only if a sum passes the limit are
+        // the logits looked at again, the maximum moved and P taken anew.  (fp32 outputs look first: their P
+        // takes the logits' place.)
+        const bool look = kExact || t == cur.tb;
+        float sum = 0.0f, off = m == -INFINITY ? 0.0f : kPromptShift<kExact> - m;
+        if (!look) sum = full ? column_exp<kExact, false>(tl, keys, cs, off) : column_exp<kExact, true>(tl, keys, cs, off);
+        const bool again = look || __any_sync(0xffffffffu, sum > kSumLimit || (m == -INFINITY && sum > 0.0f));
+        if (again) {
+          const float top = cs * (full ? column_top<false>(tl + kColS, keys) : column_top<true>(tl + kColS, keys));
+          float corr = 1.0f;
+          if (top > m + kLag) {
+            corr = ex2(m - top);  // 0 on the first keys
+            m = top;
+            l *= corr;
           }
+          if (t > cur.tb)
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+              float o[16];
+              tmem_ld16(tl + kColO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= corr;
+              tmem_st16(tl + kColO + c, o);
+            }
+          off = m == -INFINITY ? 0.0f : kPromptShift<kExact> - m;
+          sum = full ? column_exp<kExact, false>(tl, keys, cs, off) : column_exp<kExact, true>(tl, keys, cs, off);
         }
-        const float off = m == -INFINITY ? 0.0f : kPShift - m;
-        l += full ? column_exp<kExact, false>(tl, keys, cs, off) : column_exp<kExact, true>(tl, keys, cs, off);
+        l += sum;
         tmem_wait_st();
         tc05_fence_before();
         arrive(&sh.p_full[T]);
@@ -564,8 +580,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
           for (int e = 0; e < 16; ++e) o[e] = __int_as_float(0x7fffffff);
         if (!mine) {
         } else if (whole) {
-          write_head<TIO>(a, out_row, head, c / 8, o, m, l);
-          write_head<TIO>(a, out_row, head, c / 8 + 1, o + 8, m, l);
+          write_head<TIO>(a, out_row, head, c / 8, o, m + (kPShift - kPromptShift<sizeof(TIO) == 4>), l);
+          write_head<TIO>(a, out_row, head, c / 8 + 1, o + 8, m + (kPShift - kPromptShift<sizeof(TIO) == 4>), l);
         } else {
           store8(parts.o + at * kD + c, o);
           store8(parts.o + at * kD + c + 8, o + 8);
@@ -608,7 +624,7 @@ __global__ void __launch_bounds__(256) kv4_prompt_join_kernel(const Kv4Args a, c
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], f, y[e]);
   }
-  write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M, l);
+  write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M + (kPShift - kPromptShift<sizeof(TIO) == 4>), l);
 }
 
 static constexpr size_t kPartBytes = (size_t)2 * kSMs * kPromptColumns * (kD + 2) * sizeof(float);
