@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
     // S = Q K^T of tile T in step j; last: the step's last one
     auto logits = [&](int T, int j, bool fresh, bool last) {
       if (fresh) wait(&sh.q_full[T], nq[T]++);
-      wait(&sh.k_full[j & 1], j >> 1);
+      if (T == 0) wait(&sh.k_full[j & 1], j >> 1);  // (the first tile has columns in every step)
       if (kExact && ns[T] > 0) wait(&sh.pv_done[T], ns[T] - 1);  // the logits' columns hold the rest of P until then
       if (dead) return;
       if (elect_one()) {
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
     };
     // O (+)= P V
     auto outputs = [&](int T, int j, bool begin, bool last) {
-      wait(&sh.v_full[j & 1], j >> 1);
+      if (T == 0) wait(&sh.v_full[j & 1], j >> 1);
       if (dead) return;
       if (elect_one()) {
         tc05_fence_after();
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         const TIO* src = static_cast<const TIO*>(a.q) + out_row * a.q_stride + head * kD;
         const bool there = mine && p >= 0;
         float big = 0.0f;
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; c < 4; ++c) {
           float lo[8], hi[8];
           if (there) {
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         const int ex = min(max((int)(__float_as_uint(big) >> 23), 9), 253);
         const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f;
         cs = __uint_as_float((uint32_t)ex << 23) * (0.125f * kLog2e * a.kscale * 0.00390625f);
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; c < 4; ++c) {
           float x[2][8] = {{0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0, 0, 0}};
           if (there) load_pair_chunk(src, c, a.rope, p, x[0], x[1]);
