@@ -626,11 +626,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
   const int i = threadIdx.x % lanes, grp = threadIdx.x / lanes, d = i & 7;
   const int col = min((int)blockIdx.y * cols + (i >> 3), ncol - 1);
   const int64_t at = ((int64_t)blockIdx.x * sa.max_chunks) * width + col;
+  // groups that share a warp are joined by shuffles, warps through shared memory
+  const int wide = min(lanes, 32), step = max(lanes, 32);
   float M = -INFINITY;
+#pragma unroll 4
   for (int c = grp; c < it.nch; c += groups) M = fmaxf(M, sa.part_ml[at + (int64_t)c * width].x);
+  for (int o = wide; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   red[threadIdx.x][8] = M;
   __syncthreads();
-  for (int k = 0; k < groups; ++k) M = fmaxf(M, red[k * lanes + i][8]);
+  for (int k = threadIdx.x % step; k < (int)blockDim.x; k += step) M = fmaxf(M, red[k][8]);
   __syncthreads();
   float l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
@@ -643,15 +647,20 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], f, y[e]);
   }
+  for (int o = wide; o < 32; o <<= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] += __shfl_xor_sync(0xffffffffu, y[e], o);
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = y[e];
   red[threadIdx.x][8] = l;
   __syncthreads();
-  if (grp != 0 || (int)blockIdx.y * cols + (i >> 3) >= ncol) return;
-  for (int k = 1; k < groups; ++k) {
-    l += red[k * lanes + i][8];
+  if (threadIdx.x >= lanes || (int)blockIdx.y * cols + (i >> 3) >= ncol) return;
+  for (int k = step + i; k < (int)blockDim.x; k += step) {
+    l += red[k][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += red[k * lanes + i][e];
+    for (int e = 0; e < 8; ++e) y[e] += red[k][e];
   }
   write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M, l);
 }
@@ -707,7 +716,7 @@ static cudaError_t join(const Kv4Args& a, const StreamShape& z, cudaStream_t s) 
   // enough columns to fill the card: four lanes' groups a column (a warp), four
   // columns a CTA; else as many groups as a column may have chunks, up to 64
   const int64_t columns = (int64_t)z.s.items * a.Hkv * width;
-  const int deep = columns >= 4 * kSMs ? 4 : std::min(64, 1 << (32 - __builtin_clz((unsigned)z.s.max_chunks - 1)));
+  const int deep = columns >= 4 * kSMs ? 4 : std::max(4, std::min(64, 1 << (32 - __builtin_clz((unsigned)z.s.max_chunks - 1))));
   const int cols = std::min(width, deep == 4 ? 4 : 1);
   return launch_pdl(kv4_join_kernel<TIO>, dim3((unsigned)(z.s.items * a.Hkv), (unsigned)((width + cols - 1) / cols)), dim3(8 * deep * cols),
                     0, s, a, z.s, cols);
