@@ -10,7 +10,6 @@ from .api import (alpha_schedule, backward, backward_int, band_plan, decode_int,
                   offsets_christoffel, offsets_fib, offsets_pow2, offsets_powerlaw, reach,
                   residue_classes, rope_keys, rope_table, rung_table, status_string, timing_enable,
                   timing_read, workspace_size)
-from .kv4 import kv4_append, kv4_attend, kv4_cache, kv4_plan, kv4_read, kv4_workspace_size
 
 __all__ = [
     "LIB_PATH", "MAX_RUNGS", "SCHED_COPRIME", "SCHED_FIXED", "SCHED_LINEAR", "SFA_BF16",
@@ -21,3 +20,16 @@ __all__ = [
     "residue_classes", "rope_keys", "rope_table", "rung_table", "status_string",
     "workspace_size", "timing_enable", "timing_read",
 ]
+
+_KV4 = ("kv4_append", "kv4_attend", "kv4_cache", "kv4_plan", "kv4_read", "kv4_workspace_size")
+
+
+def __getattr__(name):
+    """The serving names, whose module imports torch (the others do when called)."""
+    if name in _KV4:
+        from . import kv4
+
+        for n in _KV4:
+            globals()[n] = getattr(kv4, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

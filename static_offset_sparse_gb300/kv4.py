@@ -5,6 +5,11 @@ kv4_attend.  The cache is a uint8 CUDA tensor [pages, Hkv, 72 * page] whose
 layout include/sfa.h gives; everything else is an int32 tensor on the same
 device.  Calls take the current stream of that device, only enqueue work, and
 may be captured into a CUDA graph.
+
+A decode step of a small batch takes the GPU a few microseconds, less than
+Python takes to look its arguments over.  So the checks are single expressions
+over cheap attributes, written out where they are made; what says what is wrong
+is run only when one of them fails.
 """
 from __future__ import annotations
 
@@ -12,51 +17,52 @@ import ctypes as C
 import functools
 import math
 
+import torch
+
 from ._lib import SFA_BF16, SFA_F32, Kv4Desc, _lib, check, i32_array
-from .api import _ROPE_CACHE, _torch, rope_table
+from .api import _ROPE_CACHE, rope_table
 
 ROW_BYTES = 72  # one (row, head): 32 + 32 bytes of codes, 8 of scales
 PAGES = {ROW_BYTES * page: page for page in (16, 32, 64, 128)}
+CODES = {torch.bfloat16: SFA_BF16, torch.float32: SFA_F32}
 
-# A decode step of a small batch takes the GPU a few microseconds, so the checks
-# below are single expressions over cheap attributes; what says what is wrong is
-# only run when one of them fails.
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
+_INF = math.inf
+_current_device = torch.cuda.current_device
+# the current stream's handle: the direct getter takes 0.1 us, the Stream object 2
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _refuse(name, t, dtype, dim, device=None):
+def _refuse(name, t, dtype, shape, index=None):
+    """Say why t is not a contiguous CUDA tensor of this type and shape (None: any size) on device `index`."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libsfa has no CPU path)")
-    if t.dtype != dtype or t.dim() != dim:
-        raise ValueError(f"{name} must be {dtype} with {dim} dimension(s), got {t.dtype} {tuple(t.shape)}")
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        want = ", ".join("any" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name} must be {dtype} [{want}], got {t.dtype} {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on device {t.get_device()}, expected {index}")
 
 
 def _ints(index, n, t, name):
-    """t is int32 [n] on device `index`."""
-    i32 = _torch().int32
-    if not (t.dtype is i32 and t.get_device() == index and t.dim() == 1 and t.is_contiguous()):
-        _refuse(name, t, i32, 1, index)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} element(s), got {t.shape[0]}")
+    """Address of t, int32 [n] on device `index`."""
+    if not (t.dtype is _I32 and t.get_device() == index and t.shape == (n,) and t.is_contiguous()):
+        _refuse(name, t, _I32, (n,), index)
     return t.data_ptr()
 
 
 def _dense(index, shape, dtype, t, name):
-    """t is a contiguous tensor of this shape and type on device `index`."""
-    if not (t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.shape == shape):
-        if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
-            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-        _refuse(name, t, dtype, len(shape), index)
+    """Address of t, contiguous, of this shape and type, on device `index`."""
+    if not (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        _refuse(name, t, dtype, shape, index)
     return t.data_ptr()
 
 
 def _pool(cache):
     """Device index, pages, KV heads and rows a page of a cache."""
-    u8 = _torch().uint8
-    if not (cache.dtype is u8 and cache.is_cuda and cache.dim() == 3 and cache.is_contiguous()):
-        _refuse("cache", cache, u8, 3)
+    if not (cache.dtype is _U8 and cache.is_cuda and cache.dim() == 3 and cache.is_contiguous()):
+        _refuse("cache", cache, _U8, (None, None, None))
     P, H, width = cache.shape
     page = PAGES.get(width)
     if page is None:
@@ -66,18 +72,16 @@ def _pool(cache):
 
 
 def _code(dtype) -> int:
-    torch = _torch()
-    if dtype is torch.bfloat16:
-        return SFA_BF16
-    if dtype is torch.float32:
-        return SFA_F32
-    raise TypeError(f"unsupported dtype {dtype}")
+    code = CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def _rows(t, name, heads, index):
     """Rows, heads and the stride between the rows of t [N, heads, 64], whose rows are dense."""
     if t.get_device() != index or t.dim() != 3:
-        _refuse(name, t, t.dtype, 3, index)
+        _refuse(name, t, t.dtype, (None, heads or None, 64), index)
     n, h, d = t.shape
     if d != 64 or (heads and h != heads):
         raise ValueError(f"{name} must be [rows, {heads or 'Hq'}, 64], got {tuple(t.shape)}")
@@ -94,18 +98,15 @@ def _rows(t, name, heads, index):
 
 
 def _scales(kscale, vscale):
-    if not (0.0 < kscale < math.inf and 0.0 < vscale < math.inf):
-        raise ValueError("kscale and vscale must be positive and finite")
+    raise ValueError(f"kscale and vscale must be positive and finite, got {kscale}, {vscale}")
 
 
 def _rope(rope, rope_theta, T, index):
     """Pointer and positions of the RoPE table: the caller's, or the cached one of rope_theta."""
-    torch = _torch()
     if rope is None:
         if not rope_theta or rope_theta <= 0:
             return None, 0
-        key = (int(T), float(rope_theta), index)
-        rope = _ROPE_CACHE.get(key)
+        rope = _ROPE_CACHE.get((int(T), float(rope_theta), index))
         if rope is None:
             if torch.cuda.is_current_stream_capturing():
                 raise ValueError("make the RoPE table before the capture: rope_table(T, rope_theta), passed as rope=")
@@ -113,7 +114,9 @@ def _rope(rope, rope_theta, T, index):
             # the table is shared by later calls on any stream
             torch.cuda.current_stream(index).synchronize()
     n = rope.shape[0]
-    return _dense(index, (n, 32, 2), torch.float32, rope, "rope"), n
+    if not (rope.dtype is _F32 and rope.get_device() == index and rope.shape == (n, 32, 2) and rope.is_contiguous()):
+        _refuse("rope", rope, _F32, (None, 32, 2), index)
+    return rope.data_ptr(), n
 
 
 @functools.lru_cache(maxsize=64)
@@ -122,20 +125,12 @@ def _offsets(dist: tuple):
     return C.cast(arr, C.c_void_p), n, arr
 
 
-def _stream_of(index):
-    """The current stream's handle on device `index` (the direct getter takes 0.1 us, the Stream object 2)."""
-    torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
-
-
 def _call(fn, name, index, *args):
     """fn(*args, the device's current stream), with that device current."""
-    cuda = _torch().cuda
-    if index == cuda.current_device():
+    if index == _current_device():
         rc = fn(*args, _stream_of(index))
     else:
-        with cuda.device(index):
+        with torch.cuda.device(index):
             rc = fn(*args, _stream_of(index))
     if rc:
         check(rc, name)
@@ -145,8 +140,7 @@ def kv4_cache(n_pages: int, Hkv: int, page: int = 64, device=None):
     """A pool of n_pages pages, every row zero."""
     n = C.c_size_t(0)
     check(_lib().sfa_kv4_cache_bytes(n_pages, page, Hkv, C.byref(n)), "sfa_kv4_cache_bytes")
-    torch = _torch()
-    return torch.zeros((n_pages, Hkv, ROW_BYTES * page), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros((n_pages, Hkv, ROW_BYTES * page), dtype=_U8, device=device or "cuda")
 
 
 def kv4_plan(n_new, seq_lens, block_table, free_pages, n_free, *, page: int, rows: int,
@@ -160,16 +154,14 @@ def kv4_plan(n_new, seq_lens, block_table, free_pages, n_free, *, page: int, row
     free pages after the step (seq_lens_out=seq_lens and n_free_out=n_free
     update those in place, as a captured step wants).  A step that does not fit
     changes nothing and sets the device status."""
-    torch = _torch()
-    i32 = torch.int32
-    if not (block_table.dtype is i32 and block_table.is_cuda and block_table.dim() == 2 and block_table.is_contiguous()):
-        _refuse("block_table", block_table, i32, 2)
+    if not (block_table.dtype is _I32 and block_table.is_cuda and block_table.dim() == 2 and block_table.is_contiguous()):
+        _refuse("block_table", block_table, _I32, (None, None))
     if rows < 0:
         raise ValueError("rows must not be negative")
     at = block_table.get_device()
     R, width = block_table.shape
     P = free_pages.shape[0]
-    own = torch.empty((2 * R + 2 + 2 * rows,), dtype=i32, device=block_table.device)
+    own = torch.empty((2 * R + 2 + 2 * rows,), dtype=_I32, device=block_table.device)
     cu_q, slots, pos, lens, left = own.split_with_sizes((R + 1, rows, rows, R, 1))
     p = own.data_ptr()
     p_lens = p + 4 * (R + 1 + 2 * rows)
@@ -193,25 +185,27 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
     at, P, H, page = _pool(cache)
     N, _, ks = _rows(k, "k", H, at)
     n, _, vs = _rows(v, "v", H, at)
-    if n != N or v.dtype is not k.dtype:
-        raise ValueError(f"k and v must have the same rows and type, got {tuple(k.shape)} {k.dtype}, {tuple(v.shape)} {v.dtype}")
-    _scales(kscale, vscale)
+    dtype = k.dtype
+    if n != N or v.dtype is not dtype:
+        raise ValueError(f"k and v must have the same rows and type, got {tuple(k.shape)} {dtype}, {tuple(v.shape)} {v.dtype}")
+    if not (0.0 < kscale < _INF and 0.0 < vscale < _INF):
+        _scales(kscale, vscale)
     rp, rT = _rope(rope, rope_theta, min(P * page, 1 << 24), at)
-    d = Kv4Desc(P, page, H, 64, 0, 0, N, 0, _code(k.dtype), 0, ks, vs, kscale, vscale, rp, rT)
-    _call(_lib().sfa_kv4_append, "sfa_kv4_append", at, d, k.data_ptr(), v.data_ptr(), cache.data_ptr(),
-          _ints(at, N, slots, "slots"), _ints(at, N, pos, "pos"))
+    _call(_lib().sfa_kv4_append, "sfa_kv4_append", at,
+          Kv4Desc(P, page, H, 64, 0, 0, N, 0, _code(dtype), 0, ks, vs, kscale, vscale, rp, rT), k.data_ptr(), v.data_ptr(),
+          cache.data_ptr(), _ints(at, N, slots, "slots"), _ints(at, N, pos, "pos"))
 
 
 def kv4_read(cache, slots, *, dtype=None, kscale: float = 1.0, vscale: float = 1.0, k=None, v=None):
     """Rows of the cache as numbers (sfa_kv4_read): k, v [N, Hkv, 64], the
     rotated keys and the values stored at slots [N] (negative: zeros)."""
-    torch = _torch()
     at, P, H, page = _pool(cache)
     if dtype is None:
         dtype = k.dtype if k is not None else torch.bfloat16
     code = _code(dtype)
     N = slots.shape[0]
-    _scales(kscale, vscale)
+    if not (0.0 < kscale < _INF and 0.0 < vscale < _INF):
+        _scales(kscale, vscale)
     shape = (N, H, 64)
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
@@ -231,11 +225,11 @@ def kv4_read(cache, slots, *, dtype=None, kscale: float = 1.0, vscale: float = 1
 def _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale):
     at, P, H, page = _pool(cache)
     N, Hq, qs = _rows(q, "q", 0, at)
-    i32 = _torch().int32
-    if not (block_table.dtype is i32 and block_table.get_device() == at and block_table.dim() == 2 and block_table.is_contiguous()):
-        _refuse("block_table", block_table, i32, 2, at)
+    if not (block_table.dtype is _I32 and block_table.get_device() == at and block_table.dim() == 2 and block_table.is_contiguous()):
+        _refuse("block_table", block_table, _I32, (None, None), at)
     R, width = block_table.shape
-    _scales(kscale, vscale)
+    if not (0.0 < kscale < _INF and 0.0 < vscale < _INF):
+        _scales(kscale, vscale)
     rp, rT = _rope(rope, rope_theta, min(width * page, 1 << 24), at)
     arr, nd, _ = _offsets(tuple(dist)) if dist is not None else (None, 0, None)
     return at, R, N, Hq, Kv4Desc(P, page, H, 64, R, width, N, Hq, _code(q.dtype), qs, 0, 0, kscale, vscale, rp, rT, arr, nd)
@@ -257,7 +251,6 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
     positions of request r, and rows behind cu_q[R] are left as they were.
     dist: offsets as for decode_int (0 required), None for every earlier row.
     Returns o [N, Hq, 64] and lse fp32 [N, Hq]."""
-    torch = _torch()
     at, R, N, Hq, d = _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale)
     if cu_q is None and N != R:
         raise ValueError(f"without cu_q, q has one row for each of the {R} requests, got {N}")
@@ -267,10 +260,10 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
     else:
         op = _dense(at, (N, Hq, 64), q.dtype, o, "o")
     if lse is None:
-        lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((N, Hq), dtype=_F32, device=q.device)
         lp = lse.data_ptr()
     else:
-        lp = _dense(at, (N, Hq), torch.float32, lse, "lse")
+        lp = _dense(at, (N, Hq), _F32, lse, "lse")
     L = _lib()
     n = C.c_size_t(0)
     rc = L.sfa_kv4_workspace_size(d, C.byref(n))
@@ -281,11 +274,10 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
         w = None
     else:
         if ws is None or ws.numel() * ws.element_size() < n:
-            ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
+            ws = torch.empty((n,), dtype=_U8, device=q.device)
         elif ws.get_device() != at or not ws.is_contiguous():
-            _refuse("ws", ws, ws.dtype, ws.dim(), at)
+            _refuse("ws", ws, ws.dtype, tuple(ws.shape), at)
         w = ws.data_ptr()
     _call(L.sfa_kv4_attend, "sfa_kv4_attend", at, d, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
-          _ints(at, R, seq_lens, "seq_lens"), None if cu_q is None else _ints(at, R + 1, cu_q, "cu_q"),
-          op, lp, w, n)
+          _ints(at, R, seq_lens, "seq_lens"), None if cu_q is None else _ints(at, R + 1, cu_q, "cu_q"), op, lp, w, n)
     return o, lse
