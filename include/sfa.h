@@ -288,7 +288,8 @@ int sfa_decode_int(const sfa_desc* d, const void* q, const void* k_cache, const 
  * written out of range.  All entry points only enqueue work, keep no state
  * between calls, and may be captured into a graph. */
 typedef struct {
-  int32_t n_pages, page, Hkv, D; /* the pool; page: 16, 32, 64 or 128 rows; D = 64; n_pages * page < 2^31 */
+  int32_t n_pages, page, Hkv, D; /* the pool; page: 16, 32, 64 or 128 rows; D = 64; n_pages * page < 2^31,
+                                  * the cache below 128 GiB */
   int32_t R, max_pages;          /* requests (1..8192 for sfa_kv4_plan); width of the block table,
                                   * max_pages * page <= 2^24 */
   int32_t N;                     /* rows: N >= 0 (0: nothing to do); N * Hkv <= 2^27 */
@@ -333,7 +334,8 @@ int sfa_kv4_plan(const sfa_kv4_desc* d, const int32_t* n_new, const int32_t* seq
  * pos[n] in fp32 (each product and sum rounded once).  Per 16 dims: x divided by
  * kscale or vscale, scale = e4m3(max |x| / 6), 448 at most, code =
  * e2m1(x / scale), 6 at most; all to nearest, ties to even, quotients in fp32.
- * A zero scale has zero codes; a block with a NaN is stored as NaN. */
+ * A zero scale has zero codes; a block with a NaN is stored as NaN; a zero may
+ * come back with either sign. */
 int sfa_kv4_append(const sfa_kv4_desc* d, const void* k, const void* v, void* cache,
                    const int32_t* slots, const int32_t* pos, void* stream);
 

@@ -196,7 +196,7 @@ struct AppendArgs {
   const int32_t* pos;
   const float2* rope;
   int32_t N, Hkv, lgS, n_pages, rope_T;
-  float kscale, vscale;
+  float kscale, vscale, inv_kscale, inv_vscale;
   int* status;
 };
 
@@ -206,20 +206,40 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
   return r;
 }
 
-// 16 numbers -> 8 bytes of codes and their scale.  scale = e4m3(amax / 6) to
-// nearest even, 448 at most; code = e2m1(x / scale) to nearest even.  Both
-// quotients are IEEE divisions, so the bytes are a function of the numbers
-// alone.  A NaN among them gives a NaN scale; a zero scale has zero codes.
-__device__ __forceinline__ uint2 quantise16(const float* x, uint32_t& scale) {
+// a / b from r = 1 / b, both quotients rounded to nearest: Markstein's theorem
+// ("Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990): with r the rounded reciprocal, one correction of a r by its exact
+// remainder rounds correctly while nothing leaves the range of normal numbers.
+// 3 operations where a division takes about ten.
+__device__ __forceinline__ float divide(float a, float b, float r) {
+  const float q = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
+}
+
+// 16 numbers -> 8 bytes of codes and their scale.  The numbers are first divided
+// by `by` (its rounded reciprocal inv); scale = e4m3(amax / 6) to nearest even,
+// 448 at most; code = e2m1(x / scale) to nearest even.  All quotients are the
+// correctly rounded ones, so the bytes are a function of the numbers alone.  A
+// NaN among them gives a NaN scale; a zero scale has zero codes.
+__device__ __forceinline__ uint2 quantise16(float* x, float by, float inv, uint32_t& scale) {
   float m = 0.0f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) m = fmax_nan(m, fabsf(x[e]));
+  // where remainders are exact (a sum below 2^-60 of the largest rounds to code 0 either way)
+  const bool plain = m >= 0x1p-40f && m <= 0x1p60f && by >= 0x1p-40f && by <= 0x1p40f;
+  if (by != 1.0f) {
+    m = __fdiv_rn(m, by);  // rounding is monotone: the largest stays the largest
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = plain ? divide(x[e], by, inv) : __fdiv_rn(x[e], by);
+  }
   scale = __nv_cvt_float_to_fp8(__fdiv_rn(m, 6.0f), __NV_SATFINITE, __NV_E4M3);
   const float s = unpack_f16(e4m3x2_f16x2(scale)).x;
   uint32_t w[2] = {0, 0};
+  if (s == 0.0f) return make_uint2(0, 0);
+  const float r = __fdiv_rn(1.0f, s);
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
-    const float lo = s == 0.0f ? 0.0f : __fdiv_rn(x[e], s), hi = s == 0.0f ? 0.0f : __fdiv_rn(x[e + 1], s);
+    const float lo = plain ? divide(x[e], s, r) : __fdiv_rn(x[e], s), hi = plain ? divide(x[e + 1], s, r) : __fdiv_rn(x[e + 1], s);
     uint32_t b;
     asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(b) : "f"(hi), "f"(lo));
     w[e >> 3] |= b << (4 * (e & 7));
@@ -280,14 +300,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
         }
       }
     }
-    const float sc = value ? a.vscale : a.kscale;
-    if (sc != 1.0f)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        lo[e] = __fdiv_rn(lo[e], sc);
-        hi[e] = __fdiv_rn(hi[e], sc);
-      }
-    const uint2 c0 = quantise16(lo, s0), c1 = quantise16(hi, s1);
+    const float sc = value ? a.vscale : a.kscale, inv = value ? a.inv_vscale : a.inv_kscale;
+    const uint2 c0 = quantise16(lo, sc, inv, s0), c1 = quantise16(hi, sc, inv, s1);
     uint8_t* codes = block + (value ? 32 * S : 0) + 32 * at;
     *reinterpret_cast<uint2*>(codes + 8 * u) = c0;
     *reinterpret_cast<uint2*>(codes + 16 + 8 * u) = c1;
@@ -367,6 +381,7 @@ static int check_rows(const sfa_kv4_desc* d) {
   if (d->Hkv <= 0 || (d->dtype != SFA_F32 && d->dtype != SFA_BF16)) return SFA_ERR_INVALID_ARG;
   if (!(d->kscale > 0.0f && d->kscale <= 3.4e38f && d->vscale > 0.0f && d->vscale <= 3.4e38f)) return SFA_ERR_INVALID_ARG;
   if (d->D != kD || (int64_t)d->N * d->Hkv > (1 << 27)) return SFA_ERR_UNSUPPORTED;
+  if ((int64_t)d->n_pages * d->page > ((1LL << 37) - 1) / kKv4Row / d->Hkv) return SFA_ERR_UNSUPPORTED;  // rows of 32 bytes in 32 bits
   if (d->rope && (d->rope_T <= 0 || !at16(d->rope))) return SFA_ERR_INVALID_ARG;
   return SFA_OK;
 }
@@ -461,7 +476,7 @@ int sfa_kv4_append(const sfa_kv4_desc* d, const void* k, const void* v, void* ca
   if (!stride_ok(d->k_stride, d->Hkv, d->dtype) || !stride_ok(d->v_stride, d->Hkv, d->dtype)) return SFA_ERR_INVALID_ARG;
   AppendArgs a = {k, v, d->k_stride, d->v_stride, static_cast<uint8_t*>(cache), slots, pos,
                   reinterpret_cast<const float2*>(d->rope), d->N, d->Hkv, __builtin_ctz((unsigned)d->page),
-                  d->n_pages, d->rope_T, d->kscale, d->vscale, nullptr};
+                  d->n_pages, d->rope_T, d->kscale, d->vscale, 1.0f / d->kscale, 1.0f / d->vscale, nullptr};
   if ((rc = device_status(&a.status)) != SFA_OK) return rc;
   const dim3 grid((unsigned)(((int64_t)d->N * d->Hkv * 4 + 255) / 256));
   LaunchTimer tm(SFA_KERNEL_KV4_APPEND, stream);

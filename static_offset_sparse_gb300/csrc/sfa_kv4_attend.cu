@@ -204,128 +204,133 @@ struct Acc {
 // Any offset list, one (row, KV head) a group of `warps` warps: lanes look up
 // their keys' pages, tiles of 16 keys go round the group's warps, and the
 // group's partial results meet in shared memory.  Bounded by latency (row map,
-// block table, cache row: three dependent loads) at decode sizes and by the
-// gathered sectors (32 + 32 + 32 bytes a key) at prompt sizes.
+// block table, cache row: three dependent loads) at decode sizes and by its
+// instructions at prompt sizes (the query's rotation and split cost a row as
+// much as 16 keys do).  The offsets beyond the window are taken to shared memory
+// once a CTA, which walks over units: read where they come in, by as many
+// addresses as lanes, they were replayed for every tile.
 constexpr int kGatherWarps = 4;
+constexpr uint32_t kNone = 0xffffffffu;
 
 template <typename TIO, int NT>
 __global__ void __launch_bounds__(32 * kGatherWarps)
     kv4_gather_kernel(const Kv4Args a, const __grid_constant__ Plan P, int warps) {
   constexpr bool kExact = sizeof(TIO) == 4;
+  __shared__ int rung[kMaxRungs];
   extern __shared__ float part[];  // [kGatherWarps][8 NT][66]
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int mine = warp % warps;
-  const int64_t unit = (int64_t)blockIdx.x * (kGatherWarps / warps) + warp / warps;
-  const int64_t n = unit / a.Hkv;
-  const int h = (int)(unit - n * a.Hkv), G = 1 << a.lgG, S = 1 << a.lgS;
+  const int mine = warp % warps, G = 1 << a.lgG, S = 1 << a.lgS;
+  for (int i = threadIdx.x; i < P.n; i += 32 * kGatherWarps) rung[i] = P.c[i];
   pdl_wait();
-  int r = 0, pos = -1;
-  const bool live = n < a.N && kv4_row(a, (int)n, lane, r, pos);
-  if (live && (pos < -1 || (pos < 0 && a.cu_q) || pos >= (a.max_pages << a.lgS) || (a.rope && pos >= a.rope_T))) {
-    if (lane == 0) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
-    pos = -1;
-  }
-  Acc<NT> acc;
-  acc.clear();
-  if (live && pos >= 0) {
-    QFrag<NT> q;
-    q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, G, a.rope, pos, 0.125f * kLog2e * a.kscale,
-           lane);
-    const int32_t* trow = a.table + (int64_t)r * a.max_pages;
-    const int Wt = min(P.W, pos);
-    int nr = 0;
-    while (nr < P.n && P.c[nr] <= pos) ++nr;
-    const int nk = Wt + 1 + nr;
-    for (int j0 = 16 * mine; j0 < nk; j0 += 16 * warps) {
-      const int j = j0 + (lane & 15);
-      int slot = -1;
-      if (j < nk) {
-        const int p = pos - (j <= Wt ? j : P.c[j - Wt - 1]);
-        const int page = trow[p >> a.lgS];
-        if (page >= 0 && page < a.n_pages)
-          slot = (page << a.lgS) + (p & (S - 1));
-        else
-          record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
-      }
-      auto block = [&](int sl) { return a.cache + ((int64_t)(sl >> a.lgS) * a.Hkv + h) * (kKv4Row * S); };
-      const int ia = __shfl_sync(0xffffffffu, slot, g), ib = __shfl_sync(0xffffffffu, slot, g + 8);
-      uint2 ka = make_uint2(0, 0), kb = ka;
-      uint32_t sa = 0, sb = 0, w[4] = {0, 0, 0, 0}, vs = 0;
-      if (ia >= 0) {
-        const uint8_t* b = block(ia);
-        ka = *reinterpret_cast<const uint2*>(b + 32 * (ia & (S - 1)) + 8 * t);
-        sa = b[64 * S + 8 * (ia & (S - 1)) + t];
-      }
-      if (ib >= 0) {
-        const uint8_t* b = block(ib);
-        kb = *reinterpret_cast<const uint2*>(b + 32 * (ib & (S - 1)) + 8 * t);
-        sb = b[64 * S + 8 * (ib & (S - 1)) + t];
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int iv = __shfl_sync(0xffffffffu, slot, 2 * t + (e & 1) + 8 * (e >> 1));
-        if (iv >= 0) {
-          const uint8_t* b = block(iv);
-          w[e] = *reinterpret_cast<const uint32_t*>(b + 32 * S + 32 * (iv & (S - 1)) + 4 * g);
-          vs |= (uint32_t)b[64 * S + 8 * (iv & (S - 1)) + 4 + (g >> 1)] << (8 * e);
-        }
-      }
-      float s[NT][4];
-      key_products(q, ka, kb, sa, sb, s);
-      softmax_step(q, s, ia >= 0, ib >= 0, acc.m, acc.l, acc.o);
-      value_products<NT, kExact>(w, vs & 0xffffu, vs >> 16, s, acc.o);
-    }
-  }
-  acc.close();
-  if (warps == 1) {
-    if (live)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int head = 8 * nt + 2 * t + e;
-          float x[8];
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            x[2 * mt] = acc.o[nt][mt][e];
-            x[2 * mt + 1] = acc.o[nt][mt][2 + e];
-          }
-          if (head < G) write_head<TIO>(a, n, h * G + head, g, x, acc.m[nt][e], acc.l[nt][e]);
-        }
-    return;
-  }
-  // [warp][head][m, l, 64 dims]
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float* w = part + (warp * 8 * NT + 8 * nt + 2 * t + e) * 66;
-      if (g == 0) {
-        w[0] = acc.m[nt][e];
-        w[1] = acc.l[nt][e];
-      }
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-        *reinterpret_cast<float2*>(w + 2 + 8 * g + 2 * mt) = make_float2(acc.o[nt][mt][e], acc.o[nt][mt][2 + e]);
-    }
   __syncthreads();
-  if (!live) return;
-  // lanes 8 i .. 8 i + 7 of the group's warp w join head 4 w + i, and so on
-  for (int head = 4 * mine + (lane >> 3); head < G; head += 4 * warps) {
-    const float* w = part + ((warp - mine) * 8 * NT + head) * 66;
-    const int d = lane & 7;
-    float m = -INFINITY, l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int i = 0; i < warps; ++i) m = fmaxf(m, w[i * 8 * NT * 66]);
-    for (int i = 0; i < warps; ++i) {
-      const float* wi = w + i * 8 * NT * 66;
-      if (wi[1] == 0.0f) continue;
-      const float f = ex2(wi[0] - m);
-      l += wi[1] * f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] += wi[2 + 8 * d + e] * f;
+  const int64_t units = (int64_t)a.N * a.Hkv;
+  const int per = kGatherWarps / warps;
+  for (int64_t first = (int64_t)blockIdx.x * per; first < units; first += (int64_t)gridDim.x * per) {
+    const int64_t unit = first + warp / warps, n = unit / a.Hkv;
+    const int h = (int)(unit - n * a.Hkv);
+    int r = 0, pos = -1;
+    const bool live = n < a.N && kv4_row(a, (int)n, lane, r, pos);
+    if (live && (pos < -1 || (pos < 0 && a.cu_q) || pos >= (a.max_pages << a.lgS) || (a.rope && pos >= a.rope_T))) {
+      if (lane == 0) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+      pos = -1;
     }
-    write_head<TIO>(a, n, h * G + head, d, x, m, l);
+    Acc<NT> acc;
+    acc.clear();
+    if (live && pos >= 0) {
+      QFrag<NT> q;
+      q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, G, a.rope, pos, 0.125f * kLog2e * a.kscale,
+             lane);
+      const int32_t* trow = a.table + (int64_t)r * a.max_pages;
+      const int Wt = min(P.W, pos);
+      int nr = 0;  // rungs that reach a row
+      for (int i = 0; i < P.n; i += 32) nr += __popc(__ballot_sync(0xffffffffu, i + lane < P.n && rung[i + lane] <= pos));
+      const int nk = Wt + 1 + nr;
+      for (int j0 = 16 * mine; j0 < nk; j0 += 16 * warps) {
+        // lane i: key i mod 16 of the tile, its code row (in 32 bytes from the cache's begin) and its scales
+        const int j = j0 + (lane & 15);
+        uint32_t row = kNone;
+        uint2 sc = make_uint2(0, 0);
+        if (j < nk) {
+          const int p = pos - (j <= Wt ? j : rung[j - Wt - 1]);
+          const int page = trow[p >> a.lgS], at = p & (S - 1);
+          if (page >= 0 && page < a.n_pages) {
+            const uint32_t first_row = ((uint32_t)page * a.Hkv + h) * (uint32_t)(9 * S / 4);
+            row = first_row + at;
+            sc = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)first_row * 32 + 64 * S + 8 * at));
+          } else {
+            record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+          }
+        }
+        const uint32_t ra = __shfl_sync(0xffffffffu, row, g), rb = __shfl_sync(0xffffffffu, row, g + 8);
+        const uint32_t sa = __shfl_sync(0xffffffffu, sc.x, g) >> (8 * t) & 255u, sb = __shfl_sync(0xffffffffu, sc.x, g + 8) >> (8 * t) & 255u;
+        uint2 ka = make_uint2(0, 0), kb = ka;
+        if (ra != kNone) ka = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)ra * 32 + 8 * t));
+        if (rb != kNone) kb = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)rb * 32 + 8 * t));
+        uint32_t w[4], vs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int from = 2 * t + (e & 1) + 8 * (e >> 1);
+          const uint32_t rv = __shfl_sync(0xffffffffu, row, from);
+          vs[e] = __shfl_sync(0xffffffffu, sc.y, from) >> (8 * (g >> 1)) & 255u;
+          w[e] = rv == kNone ? 0u : __ldg(reinterpret_cast<const uint32_t*>(a.cache + (uint64_t)rv * 32 + 32 * S + 4 * g));
+        }
+        float s[NT][4];
+        key_products(q, ka, kb, sa, sb, s);
+        softmax_step(q, s, ra != kNone, rb != kNone, acc.m, acc.l, acc.o);
+        value_products<NT, kExact>(w, vs[0] | vs[1] << 8, vs[2] | vs[3] << 8, s, acc.o);
+      }
+    }
+    acc.close();
+    if (warps == 1) {
+      if (live)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int head = 8 * nt + 2 * t + e;
+            float x[8];
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              x[2 * mt] = acc.o[nt][mt][e];
+              x[2 * mt + 1] = acc.o[nt][mt][2 + e];
+            }
+            if (head < G) write_head<TIO>(a, n, h * G + head, g, x, acc.m[nt][e], acc.l[nt][e]);
+          }
+      continue;
+    }
+    // [warp][head][m, l, 64 dims]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* w = part + (warp * 8 * NT + 8 * nt + 2 * t + e) * 66;
+        if (g == 0) {
+          w[0] = acc.m[nt][e];
+          w[1] = acc.l[nt][e];
+        }
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+          *reinterpret_cast<float2*>(w + 2 + 8 * g + 2 * mt) = make_float2(acc.o[nt][mt][e], acc.o[nt][mt][2 + e]);
+      }
+    __syncthreads();
+    // lanes 8 i .. 8 i + 7 of the group's warp w join head 4 w + i, and so on
+    for (int head = 4 * mine + (lane >> 3); live && head < G; head += 4 * warps) {
+      const float* w = part + ((warp - mine) * 8 * NT + head) * 66;
+      const int d = lane & 7;
+      float m = -INFINITY, l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int i = 0; i < warps; ++i) m = fmaxf(m, w[i * 8 * NT * 66]);
+      for (int i = 0; i < warps; ++i) {
+        const float* wi = w + i * 8 * NT * 66;
+        if (wi[1] == 0.0f) continue;
+        const float f = ex2(wi[0] - m);
+        l += wi[1] * f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += wi[2 + 8 * d + e] * f;
+      }
+      write_head<TIO>(a, n, h * G + head, d, x, m, l);
+    }
+    __syncthreads();  // the buffer is filled again by the next unit
   }
 }
 
@@ -334,7 +339,8 @@ static cudaError_t gather(const Kv4Args& a, const Plan& p, int warps, cudaStream
   const int64_t units = (int64_t)a.N * a.Hkv;
   const int per = kGatherWarps / warps;
   const size_t smem = warps > 1 ? (size_t)kGatherWarps * 8 * NT * 66 * sizeof(float) : 0;
-  return launch_pdl(kv4_gather_kernel<TIO, NT>, dim3((unsigned)((units + per - 1) / per)), dim3(32 * kGatherWarps), smem, s, a, p, warps);
+  const int64_t ctas = std::min<int64_t>((units + per - 1) / per, kSMs * 16);  // 16 CTAs of 4 warps fill an SM
+  return launch_pdl(kv4_gather_kernel<TIO, NT>, dim3((unsigned)ctas), dim3(32 * kGatherWarps), smem, s, a, p, warps);
 }
 
 // ---------------------------------------------------------------- stream
@@ -676,7 +682,9 @@ struct StreamShape {
 static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   StreamShape z = {};
   const int64_t cap = (int64_t)a.max_pages << a.lgS;
-  if (p.n > 0 || std::min<int64_t>(cap, (int64_t)p.W + 1) <= 64) return z;
+  // few keys, or a wave of rows with few: one launch and no workspace win
+  const int64_t keys = std::min<int64_t>(cap, (int64_t)p.W + 1);
+  if (p.n > 0 || keys <= 64 || (keys <= 512 && (int64_t)a.N * a.Hkv <= 4 * kSMs)) return z;
   const int G = 1 << a.lgG;
   // columns a warp holds: as many rows as a request brings on average, 32 at most
   const int avg = ragged ? (a.N + a.R - 1) / a.R : 1;

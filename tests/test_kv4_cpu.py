@@ -45,7 +45,7 @@ def test_plan_pointer_refusals(sfa_lib):
 
 @pytest.mark.parametrize("kw,rc", [(dict(D=128), 2), (dict(dtype=2), 1), (dict(Hkv=0), 1), (dict(kscale=0.0), 1), (dict(vscale=-1.0), 1),
                                    (dict(kscale=float("nan")), 1), (dict(vscale=float("inf")), 1), (dict(rope=P, rope_T=0), 1),
-                                   (dict(rope=ODD, rope_T=4), 1), (dict(N=1 << 27), 2), (dict(page=8), 2)])
+                                   (dict(rope=ODD, rope_T=4), 1), (dict(N=1 << 27), 2), (dict(page=8), 2), (dict(n_pages=1 << 26, Hkv=2), 2)])
 def test_row_refusals(sfa_lib, kw, rc):
     d = _desc(**kw)
     assert sfa_lib.sfa_kv4_append(d, P, P, P, P, P, None) == rc
