@@ -221,30 +221,50 @@ __device__ __forceinline__ float divide(float a, float b, float r) {
 // 448 at most; code = e2m1(x / scale) to nearest even.  All quotients are the
 // correctly rounded ones, so the bytes are a function of the numbers alone.  A
 // NaN among them gives a NaN scale; a zero scale has zero codes.
-__device__ __forceinline__ uint2 quantise16(float* x, float by, float inv, uint32_t& scale) {
-  float m = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) m = fmax_nan(m, fabsf(x[e]));
-  // where remainders are exact (a sum below 2^-60 of the largest rounds to code 0 either way)
-  const bool plain = m >= 0x1p-40f && m <= 0x1p60f && by >= 0x1p-40f && by <= 0x1p40f;
+template <typename DIV>
+__device__ __forceinline__ uint2 quantise16_by(float* x, float m, float by, float inv, uint32_t& scale, DIV div) {
   if (by != 1.0f) {
     m = __fdiv_rn(m, by);  // rounding is monotone: the largest stays the largest
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = plain ? divide(x[e], by, inv) : __fdiv_rn(x[e], by);
+    for (int e = 0; e < 16; ++e) x[e] = div(x[e], by, inv);
   }
   scale = __nv_cvt_float_to_fp8(__fdiv_rn(m, 6.0f), __NV_SATFINITE, __NV_E4M3);
   const float s = unpack_f16(e4m3x2_f16x2(scale)).x;
-  uint32_t w[2] = {0, 0};
   if (s == 0.0f) return make_uint2(0, 0);
   const float r = __fdiv_rn(1.0f, s);
+  uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 16; e += 2) {
-    const float lo = plain ? divide(x[e], s, r) : __fdiv_rn(x[e], s), hi = plain ? divide(x[e + 1], s, r) : __fdiv_rn(x[e + 1], s);
+    const float lo = div(x[e], s, r), hi = div(x[e + 1], s, r);
     uint32_t b;
     asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(b) : "f"(hi), "f"(lo));
     w[e >> 3] |= b << (4 * (e & 7));
   }
   return make_uint2(w[0], w[1]);
+}
+
+// The rare blocks (all but zero, huge, infinite, NaN) apart: their divisions
+// would fill the instruction cache of the others.
+__device__ __noinline__ uint2 quantise16_rare(const float* x, float m, float by, uint32_t* scale) {
+  float y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = x[e];
+  return quantise16_by(y, m, by, 0.0f, *scale, [](float a, float b, float) { return __fdiv_rn(a, b); });
+}
+
+__device__ __forceinline__ uint2 quantise16(float* x, float by, float inv, uint32_t& scale) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = fmax_nan(m, fabsf(x[e]));
+  // where remainders are exact (what lies 2^-60 below the largest has code 0 either way)
+  if (m >= 0x1p-40f && m <= 0x1p60f && by >= 0x1p-40f && by <= 0x1p40f) return quantise16_by(x, m, by, inv, scale, divide);
+  float y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = x[e];
+  uint32_t s;
+  const uint2 c = quantise16_rare(y, m, by, &s);
+  scale = s;
+  return c;
 }
 
 template <typename TIO>
@@ -260,12 +280,10 @@ template <typename TIO>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t unit = i >> 2;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x, unit = i >> 2;  // (N * Hkv <= 2^27)
   const int part = (int)(i & 3), u = part & 1;
   const bool value = part >= 2;
-  const int64_t n = unit / a.Hkv;
-  const int h = (int)(unit - n * a.Hkv);
+  const int n = (int)(unit / (uint32_t)a.Hkv), h = (int)unit - n * a.Hkv;
   int slot = -1, p = 0;
   if (n < a.N) {
     slot = a.slots[n];
@@ -330,10 +348,10 @@ template <typename TIO>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const ReadArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t unit = i >> 3, n = unit / a.Hkv;
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x, unit = i >> 3;  // (N * Hkv <= 2^27)
+  const int n = (int)(unit / (uint32_t)a.Hkv);
   if (n >= a.N) return;
-  const int part = (int)(i & 7), h = (int)(unit - n * a.Hkv), S = 1 << a.lgS;
+  const int part = (int)(i & 7), h = (int)unit - n * a.Hkv, S = 1 << a.lgS;
   const bool value = part >= 4;
   const int slot = a.slots[n];
   float x[16];
@@ -357,7 +375,7 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const ReadArgs a) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] = 0.0f;
   }
-  TIO* out = static_cast<TIO*>(value ? a.v : a.k) + unit * kD + 16 * (part & 3);
+  TIO* out = static_cast<TIO*>(value ? a.v : a.k) + (int64_t)unit * kD + 16 * (part & 3);
   store8(out, x);
   store8(out + 8, x + 8);
 }

@@ -14,6 +14,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sfa_kv4_stream.cuh"
 #include "sfa_launch.cuh"
@@ -23,66 +24,93 @@ namespace sfa {
 // Queries as B fragments: column c is head c mod G of row c / G; lane (g, t)
 // holds dims 16t .. 16t + 15 of column 8 nt + g, in the order the keys' codes
 // come in.
+// One column tile: 8 B registers of high and 8 of low parts; returns the factor
+// that takes the accumulator of column g to its logit (log2 units, `scale`
+// included).  base: the first head of the first row, which stands at pos;
+// columns from ncol on, and rows before position 0, are zero.
+template <typename TIO>
+__device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, int lgG, int ncol, const float2* rope, int pos, float scale,
+                                              int nt, int lane, uint32_t* hi, uint32_t* lo) {
+  const int g = lane >> 2, t = lane & 3;
+  const int col = 8 * nt + g, p = pos + (col >> lgG);
+  const TIO* row = base + (col >> lgG) * stride + (col & ((1 << lgG) - 1)) * kD;
+  float x[16], y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+  if (col < ncol && p >= 0) {
+    load8(row + 16 * t, x);
+    load8(row + 16 * t + 8, x + 8);
+    if (rope) {  // the pair of dim j is j +- 32
+      load8(row + 16 * (t ^ 2), y);
+      load8(row + 16 * (t ^ 2) + 8, y + 8);
+#pragma unroll
+      for (int c8 = 0; c8 < 16; c8 += 8) {
+        float cs[8], sn[8];
+        load_rope8(rope, p, 16 * (t & 1) + c8, cs, sn);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[c8 + e] = x[c8 + e] * cs[e] + (t < 2 ? -y[c8 + e] : y[c8 + e]) * sn[e];
+      }
+    }
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  // 2^(8 - exponent of the largest): its parts then reach f16's 2^-24 steps
+  // 2^-33 below it
+  const int ex = min(max((int)(__float_as_uint(m) >> 23), 9), 253);
+  const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a = x[2 * e] * f, b = x[2 * e + 1] * f;
+    hi[e] = pack_f16(a, b);
+    const float2 r = unpack_f16(hi[e]);
+    lo[e] = pack_f16(a - r.x, b - r.y);
+  }
+  return __uint_as_float((uint32_t)ex << 23) * (scale * 0.00390625f);
+}
+
+// All of them in registers, 16 a column tile.
 template <int NT>
 struct QFrag {
   uint32_t hi[NT][8], lo[NT][8];
   float c[NT][2];  // logit of accumulator (heads 2t, 2t + 1), log2 units
 
-  // base: the first head of the first row, which stands at pos; columns from
-  // ncol on, and rows before position 0, are zero.
   template <typename TIO>
   __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, int ncol, const float2* rope, int pos, float scale,
                                        int lane) {
-    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int col = 8 * nt + g, p = pos + (col >> lgG);
-      const TIO* row = base + (col >> lgG) * stride + (col & ((1 << lgG) - 1)) * kD;
-      float x[16], y[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-      if (col < ncol && p >= 0) {
-        load8(row + 16 * t, x);
-        load8(row + 16 * t + 8, x + 8);
-        if (rope) {  // the pair of dim j is j +- 32
-          load8(row + 16 * (t ^ 2), y);
-          load8(row + 16 * (t ^ 2) + 8, y + 8);
-#pragma unroll
-          for (int c8 = 0; c8 < 16; c8 += 8) {
-            float cs[8], sn[8];
-            load_rope8(rope, p, 16 * (t & 1) + c8, cs, sn);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[c8 + e] = x[c8 + e] * cs[e] + (t < 2 ? -y[c8 + e] : y[c8 + e]) * sn[e];
-          }
-        }
-      }
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      // 2^(8 - exponent of the largest): its parts then reach f16's 2^-24 steps
-      // 2^-33 below it
-      const int ex = min(max((int)(__float_as_uint(m) >> 23), 9), 253);
-      const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f;
-      const float back = __uint_as_float((uint32_t)ex << 23) * (scale * 0.00390625f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = x[2 * e] * f, b = x[2 * e + 1] * f;
-        hi[nt][e] = pack_f16(a, b);
-        const float2 r = unpack_f16(hi[nt][e]);
-        lo[nt][e] = pack_f16(a - r.x, b - r.y);
-      }
-      c[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-      c[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      const float back = load_queries(base, stride, lgG, ncol, rope, pos, scale, nt, lane, hi[nt], lo[nt]);
+      c[nt][0] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3));
+      c[nt][1] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3) + 4);
     }
+  }
+  // the B registers of step ks, columns nt: two of high parts, two of low ones
+  __device__ __forceinline__ uint4 b(int ks, int nt) const {
+    return make_uint4(hi[nt][2 * ks], hi[nt][2 * ks + 1], lo[nt][2 * ks], lo[nt][2 * ks + 1]);
+  }
+};
+
+// The same in shared memory, for all of a CTA's warps: 64 registers a lane less
+// with four column tiles, which is what lets two CTAs share an SM.
+template <int NT>
+struct QShared {
+  uint32_t frag;  // shared address of this lane's: [step][column tile][lane]
+  float c[NT][2];
+  // (volatile: read where it is used, not kept in the registers that it is here to save)
+  __device__ __forceinline__ uint4 b(int ks, int nt) const {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(frag + (ks * NT + nt) * 512));
+    return v;
   }
 };
 
 // Keys g and g + 8 of a tile: 16 codes and the scale of dims 16t .. 16t + 15
 // each.  s[nt] = accumulators of keys (g, g, g + 8, g + 8) x heads (2t, 2t + 1).
-template <int NT>
-__device__ __forceinline__ void key_products(const QFrag<NT>& q, uint2 ka, uint2 kb, uint32_t sa, uint32_t sb, float (*s)[4]) {
+template <int NT, typename Q>
+__device__ __forceinline__ void key_products(const Q& q, uint2 ka, uint2 kb, uint32_t sa, uint32_t sb, float (*s)[4]) {
   const uint32_t fa = e4m3x2_f16x2(sa * 0x101u), fb = e4m3x2_f16x2(sb * 0x101u);
   uint32_t xa[8], xb[8];
   e2m1x8_f16(ka.x, xa);
@@ -96,8 +124,9 @@ __device__ __forceinline__ void key_products(const QFrag<NT>& q, uint2 ka, uint2
     const uint32_t a[4] = {hmul2(xa[2 * ks], fa), hmul2(xb[2 * ks], fb), hmul2(xa[2 * ks + 1], fa), hmul2(xb[2 * ks + 1], fb)};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      mma_f16(s[nt], a, q.hi[nt][2 * ks], q.hi[nt][2 * ks + 1]);
-      mma_f16(s[nt], a, q.lo[nt][2 * ks], q.lo[nt][2 * ks + 1]);
+      const uint4 b = q.b(ks, nt);
+      mma_f16(s[nt], a, b.x, b.y);
+      mma_f16(s[nt], a, b.z, b.w);
     }
   }
 }
@@ -213,7 +242,7 @@ constexpr int kGatherWarps = 4;
 constexpr uint32_t kNone = 0xffffffffu;
 
 template <typename TIO, int NT>
-__global__ void __launch_bounds__(32 * kGatherWarps)
+__global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 6 : 1)
     kv4_gather_kernel(const Kv4Args a, const __grid_constant__ Plan P, int warps) {
   constexpr bool kExact = sizeof(TIO) == 4;
   __shared__ int rung[kMaxRungs];
@@ -224,13 +253,11 @@ __global__ void __launch_bounds__(32 * kGatherWarps)
   for (int i = threadIdx.x; i < P.n; i += 32 * kGatherWarps) rung[i] = P.c[i];
   pdl_wait();
   __syncthreads();
-  const int64_t units = (int64_t)a.N * a.Hkv;
-  const int per = kGatherWarps / warps;
-  for (int64_t first = (int64_t)blockIdx.x * per; first < units; first += (int64_t)gridDim.x * per) {
-    const int64_t unit = first + warp / warps, n = unit / a.Hkv;
-    const int h = (int)(unit - n * a.Hkv);
+  const int units = a.N * a.Hkv, per = kGatherWarps / warps;  // (N * Hkv <= 2^27)
+  for (int first = blockIdx.x * per; first < units; first += gridDim.x * per) {
+    const int unit = first + warp / warps, n = (int)((uint32_t)unit / (uint32_t)a.Hkv), h = unit - n * a.Hkv;
     int r = 0, pos = -1;
-    const bool live = n < a.N && kv4_row(a, (int)n, lane, r, pos);
+    const bool live = n < a.N && kv4_row(a, n, lane, r, pos);
     if (live && (pos < -1 || (pos < 0 && a.cu_q) || pos >= (a.max_pages << a.lgS) || (a.rope && pos >= a.rope_T))) {
       if (lane == 0) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
       pos = -1;
@@ -276,7 +303,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps)
           w[e] = rv == kNone ? 0u : __ldg(reinterpret_cast<const uint32_t*>(a.cache + (uint64_t)rv * 32 + 32 * S + 4 * g));
         }
         float s[NT][4];
-        key_products(q, ka, kb, sa, sb, s);
+        key_products<NT>(q, ka, kb, sa, sb, s);
         softmax_step(q, s, ra != kNone, rb != kNone, acc.m, acc.l, acc.o);
         value_products<NT, kExact>(w, vs[0] | vs[1] << 8, vs[2] | vs[3] << 8, s, acc.o);
       }
@@ -370,8 +397,8 @@ __device__ __forceinline__ int key_of(int r) { return r ^ ((r >> 2) & 1); }
 
 // 16 GB keys (from key k0 of a tile that starts at key j0, its data at T) added
 // to the columns' sums.  MASKED: some column may not attend some key.
-template <int NT, int GB, bool EXACT, bool MASKED>
-__device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& sa, const Item& it, const QFrag<NT>& q, Acc<NT>& acc,
+template <int NT, int GB, bool EXACT, bool MASKED, typename Q>
+__device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& sa, const Item& it, const Q& q, Acc<NT>& acc,
                                             const uint8_t* T, int j0, int k0, int pages, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const int lgr = min(a.lgS, 6);
@@ -385,7 +412,7 @@ __device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& 
   float s[GB][NT][4];
 #pragma unroll
   for (int i = 0; i < GB; ++i) {
-    key_products(q, *reinterpret_cast<const uint2*>(kt + 512 * i), *reinterpret_cast<const uint2*>(kt + 512 * i + 256),
+    key_products<NT>(q, *reinterpret_cast<const uint2*>(kt + 512 * i), *reinterpret_cast<const uint2*>(kt + 512 * i + 256),
                  (uint32_t)st[128 * i], (uint32_t)st[128 * i + 64], s[i]);
     if (MASKED) {
       const int ka = k0 + 16 * i + key_of(g);
@@ -487,8 +514,8 @@ __device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& 
 // an SM a tile with its data at hand (197 is what the memory takes to bring
 // one); 64 at once take 183, but then 16 warps' registers do not hold the rest.
 // Masked tiles, and wider ones, take 16 keys at a time.
-template <int NT, bool EXACT>
-__device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& sa, const Item& it, const QFrag<NT>& q, Acc<NT>& acc,
+template <int NT, bool EXACT, typename Q>
+__device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& sa, const Item& it, const Q& q, Acc<NT>& acc,
                                             const uint8_t* T, int j0, int pages, int all_pages, int lane) {
   constexpr int GB = NT == 1 ? 2 : 1;  // 16-key groups whose logits are held at once
   const bool full = pages == all_pages && j0 + kTile - 1 <= it.pfirst && j0 >= it.plast() - sa.W;
@@ -501,8 +528,12 @@ __device__ __forceinline__ void stream_tile(const Kv4Args& a, const StreamArgs& 
   }
 }
 
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
 // CTAs an SM of the variant with NT column tiles.
-constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : NT == 2 ? 2 : 1; }
+constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : 2; }
 
 template <typename TIO, int NT>
 __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
@@ -511,8 +542,10 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
   extern __shared__ __align__(128) uint8_t smem[];
   float* const po = reinterpret_cast<float*>(smem + kSlots * kTileBytes);         // [2][warp][NC][66]
   float2* const ml = reinterpret_cast<float2*>(po + 2 * kStreamWarps * NC * 66);  // [2][warp][NC]
+  uint4* const qs = reinterpret_cast<uint4*>(ml + 2 * kStreamWarps * NC);          // NT = 4: [step][column tile][lane]
+  float* const qc = reinterpret_cast<float*>(qs + 4 * NT * 32);                   //         [NC]
   // the slots' full and empty barriers, the buffers' (filled by four warps, joined by one)
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(ml + 2 * kStreamWarps * NC);
+  uint64_t* const bars = NT == 4 ? reinterpret_cast<uint64_t*>(qc + NC) : reinterpret_cast<uint64_t*>(ml + 2 * kStreamWarps * NC);
   int* const pages = reinterpret_cast<int*>(bars + 2 * kSlots + 4);
   int* const sums = pages + kSlots;                                               // [warps]
   int* const where = sums + kStreamWarps + 1;                                     // first item, head, chunk, weight
@@ -534,7 +567,7 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
   }
   const int G = 1 << a.lgG;
   const int all_pages = (1 << (kTile >> min(a.lgS, 6))) - 1;
-  QFrag<NT> q;
+  std::conditional_t<NT == 4, QShared<NT>, QFrag<NT>> q;
   Acc<NT> acc;
   int qx = -1, qh = -1, n0 = 0, nchunk = 0;  // n0, nchunk: tiles and chunks of the run before this one
   bool dead = false;                         // a wait ran out: no more waits, no more work
@@ -544,8 +577,25 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
   do {
     const int ncol = cur.it.nrows << a.lgG;
     if (cur.x != qx || cur.h != qh) {
-      q.load(static_cast<const TIO*>(a.q) + (int64_t)cur.it.row0 * a.q_stride + cur.h * G * kD, a.q_stride, a.lgG, ncol, a.rope,
-             cur.it.pfirst, 0.125f * kLog2e * a.kscale, lane);
+      const TIO* base = static_cast<const TIO*>(a.q) + (int64_t)cur.it.row0 * a.q_stride + cur.h * G * kD;
+      const float scale = 0.125f * kLog2e * a.kscale;
+      if constexpr (NT == 4) {  // a column tile a warp
+        static_assert(NT == kStreamWarps || NT != 4, "a column tile a warp");
+        uint32_t hi[8], lo[8];
+        const float back = load_queries(base, a.q_stride, a.lgG, ncol, a.rope, cur.it.pfirst, scale, warp, lane, hi, lo);
+        bar_sync(1, 32 * kStreamWarps);  // the last item's queries have been used
+        if (t == 0) qc[8 * warp + g] = back;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) qs[(ks * NT + warp) * 32 + lane] = make_uint4(hi[2 * ks], hi[2 * ks + 1], lo[2 * ks], lo[2 * ks + 1]);
+        bar_sync(1, 32 * kStreamWarps);
+        q.frag = smem_u32(qs + lane);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) q.c[nt][e] = qc[8 * nt + 2 * t + e];
+      } else {
+        q.load(base, a.q_stride, a.lgG, ncol, a.rope, cur.it.pfirst, scale, lane);
+      }
       qx = cur.x;
       qh = cur.h;
     }
@@ -690,8 +740,9 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   const int avg = ragged ? (a.N + a.R - 1) / a.R : 1;
   z.nt = G * avg > 16 ? 4 : G * avg > 8 ? 2 : 1;
   z.nt = std::max(z.nt, G > 16 ? 4 : G > 8 ? 2 : 1);
-  // from half a tile of 128 columns on: the tensor memory kernel (nt = 32)
-  if (G * avg >= 64) z.nt = kPromptColumns / 8;
+  // more than 32 columns: the tensor memory kernel (nt = 32; 64 requests of up to 20000 rows, 8 / 2 heads,
+  // 12 rows each: 113 us, and 150 us in items of 32 columns; 6 rows each: 113 and 85)
+  if (ragged && G * avg > 32) z.nt = kPromptColumns / 8;
   z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
   z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
   z.s.W = p.W;
@@ -733,7 +784,7 @@ static cudaError_t join(const Kv4Args& a, const StreamShape& z, cudaStream_t s) 
 template <typename TIO, int NT>
 static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
   constexpr int NC = 8 * NT;
-  constexpr size_t smem = kSlots * (kTileBytes + 16 + 4) + 2 * kStreamWarps * NC * (66 * 4 + 8) + 32 + 64;
+  constexpr size_t smem = kSlots * (kTileBytes + 16 + 4) + 2 * kStreamWarps * NC * (66 * 4 + 8) + 32 + 64 + (NT == 4 ? 4 * NT * 512 + NC * 4 : 0);
   static_assert(smem + 1024 <= 228 * 1024 / stream_ctas(NT), "CTAs an SM");
   const cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   return e != cudaSuccess ? e : launch_pdl(kv4_stream_kernel<TIO, NT>, dim3((unsigned)z.grid), dim3(32 * (kStreamWarps + 1)), smem, s, a, z.s);

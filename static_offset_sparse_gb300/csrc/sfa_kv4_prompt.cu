@@ -189,11 +189,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// The keys of a step that a column attends.
+// The keys of a step that a column attends: lo .. hi, where their pages are there.
 struct Keys {
   int lo, hi, pages, lgr;
   __device__ __forceinline__ bool attended(int k) const {
     return k >= lo && k <= hi && (pages >> ((k >> 6) * 4 + ((k & 63) >> lgr)) & 1);
+  }
+  // keys c .. c + 31 as bits
+  __device__ __forceinline__ uint32_t bits(int c) const {
+    const int a = max(lo - c, 0), b = min(hi - c, 31);
+    if (a > b) return 0;
+    uint32_t m = (0xffffffffu << a) & (0xffffffffu >> (31 - b));
+    const int pg = pages >> ((c >> 6) * 4);
+    if (lgr >= 5) return pg >> ((c & 63) >> lgr) & 1 ? m : 0;
+    if (!(pg >> ((c & 63) >> 4) & 1)) m &= 0xffff0000u;
+    if (!(pg >> (((c & 63) >> 4) + 1) & 1)) m &= 0x0000ffffu;
+    return m;
   }
 };
 
@@ -202,10 +213,12 @@ template <bool MASKED>
 __device__ __forceinline__ void column_take(uint32_t s, int c, const Keys& keys, float* v, float* next, bool more) {
   tmem_wait_ld32(v);
   if (more) tmem_ld32(s + c + 32, next);
-  if (MASKED)
+  if (MASKED) {
+    const uint32_t m = keys.bits(c);
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-      if (!keys.attended(c + e)) v[e] = -INFINITY;
+      if (!(m >> e & 1)) v[e] = -INFINITY;
+  }
 }
 
 // The largest of a column's 128 logits (its own lane of tensor memory).  Both
