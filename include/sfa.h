@@ -290,7 +290,7 @@ int sfa_decode_int(const sfa_desc* d, const void* q, const void* k_cache, const 
 typedef struct {
   int32_t n_pages, page, Hkv, D; /* the pool; page: 16, 32, 64 or 128 rows; D = 64; n_pages * page < 2^31,
                                   * the cache below 128 GiB */
-  int32_t R, max_pages;          /* requests (1..8192 for sfa_kv4_plan); width of the block table,
+  int32_t R, max_pages;          /* requests (plan: 1..8192); width of the block table,
                                   * max_pages * page <= 2^24 */
   int32_t N;                     /* rows: N >= 0 (0: nothing to do); N * Hkv <= 2^27 */
   int32_t Hq, dtype;             /* attend: query heads (G = Hq / Hkv a power of two <= 32); sfa_dtype
@@ -356,7 +356,12 @@ int sfa_kv4_read(const sfa_kv4_desc* d, const void* cache, const int32_t* slots,
  *   lse      fp32 [N, Hq], natural log of the softmax denominator, or NULL
  * A query at position p attends the rows j <= p (d->dist NULL), or p - s for
  * every s <= p of d->dist (which holds 0 and nothing negative); logits are
- * q . k / 8 after the rotation of q at p by d->rope.  (N + R) * Hkv * max_pages
+ * q . k / 8 after the rotation of q at p by d->rope.  A NaN that is stored
+ * reaches the rows that attend it and no others; rows of a page behind
+ * seq_lens may hold anything.  o and lse overlap no input.  What is added in
+ * which order depends on the shapes and the row's own request; from 33 query
+ * columns (rows a request on average x G) on, a long prefix is also split by
+ * what else is in the batch, so the last bits of a row may depend on it.  (N + R) * Hkv * max_pages
  * * page beyond 2^37 may be refused (SFA_ERR_UNSUPPORTED).  ws: sfa_kv4_workspace_size
  * bytes (NULL when that is 0), scratch of this call alone. */
 int sfa_kv4_workspace_size(const sfa_kv4_desc* d, size_t* bytes);

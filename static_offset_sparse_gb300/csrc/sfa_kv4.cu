@@ -411,7 +411,7 @@ static bool stride_ok(int64_t stride, int heads, int dtype) {
 static int check_attend(const sfa_kv4_desc* d, Plan* p, Kv4Args* a) {
   int rc = check_rows(d);
   if (rc != SFA_OK) return rc;
-  if (d->R <= 0 || d->max_pages <= 0 || d->Hq <= 0) return SFA_ERR_INVALID_ARG;
+  if (d->R < 0 || (d->R == 0 && d->N > 0) || d->max_pages <= 0 || d->Hq <= 0) return SFA_ERR_INVALID_ARG;
   if ((int64_t)d->max_pages * d->page > (1 << 24) || d->Hq % d->Hkv) return SFA_ERR_UNSUPPORTED;
   const int G = d->Hq / d->Hkv;
   if (G > 32 || (G & (G - 1)) || (int64_t)d->N * d->Hq > (1LL << 31) - 1) return SFA_ERR_UNSUPPORTED;
@@ -440,6 +440,7 @@ static int check_attend(const sfa_kv4_desc* d, Plan* p, Kv4Args* a) {
   a->kscale = d->kscale;
   a->vscale = d->vscale;
   a->q_stride = d->q_stride;
+  if (d->N == 0) return SFA_OK;
   return kv4_attend_fits(*a, *p, true) && (d->N != d->R || kv4_attend_fits(*a, *p, false)) ? SFA_OK : SFA_ERR_UNSUPPORTED;
 }
 
@@ -527,6 +528,8 @@ int sfa_kv4_workspace_size(const sfa_kv4_desc* d, size_t* bytes) {
   const int rc = check_attend(d, &p, &a);
   if (rc != SFA_OK) return rc;
   // without cu_q N = R; with N = R the call may be of either kind
+  *bytes = 0;
+  if (d->N == 0) return SFA_OK;
   *bytes = kv4_attend_workspace(a, p, true);
   if (d->N == d->R) *bytes = std::max(*bytes, kv4_attend_workspace(a, p, false));
   return SFA_OK;

@@ -539,13 +539,13 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         if (jt > 0) wait(&sh.pv_done[T], jt - 1);  // P's columns are free, O stands still
         if (dead) break;
         tc05_fence_after();
-        // After a piece's first step P is taken with the maximum so far: only if a sum passes the limit are
-        // the logits looked at again, the maximum moved and P taken anew.  (fp32 outputs look first: their P
-        // takes the logits' place.)
+        // After a piece's first step P is taken with the maximum so far: only if a sum passes the limit, or
+        // a column that had no key so far has some, are the logits looked at, the maximum moved and P taken
+        // anew.  (fp32 outputs look first: their P takes the logits' place.)
         const bool look = kExact || t == cur.tb;
         float sum = 0.0f, off = m == -INFINITY ? 0.0f : kPromptShift<kExact> - m;
         if (!look) sum = full ? column_exp<kExact, false>(tl, keys, cs, off) : column_exp<kExact, true>(tl, keys, cs, off);
-        const bool again = look || __any_sync(0xffffffffu, sum > kSumLimit || (m == -INFINITY && sum > 0.0f));
+        const bool again = look || __any_sync(0xffffffffu, sum > kSumLimit || (m == -INFINITY && k_lo <= k_hi));
         if (again) {
           const float top = cs * (full ? column_top<false>(tl + kColS, keys) : column_top<true>(tl + kColS, keys));
           float corr = 1.0f;

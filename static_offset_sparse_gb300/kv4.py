@@ -24,6 +24,7 @@ from .api import _ROPE_CACHE, rope_table
 
 ROW_BYTES = 72  # one (row, head): 32 + 32 bytes of codes, 8 of scales
 PAGES = {ROW_BYTES * page: page for page in (16, 32, 64, 128)}
+MAX_OWN_POSITIONS = 1 << 20  # longest RoPE table (256 bytes a position) that a call makes by itself
 CODES = {torch.bfloat16: SFA_BF16, torch.float32: SFA_F32}
 
 _U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
@@ -102,10 +103,12 @@ def _scales(kscale, vscale):
 
 
 def _rope(rope, rope_theta, T, index):
-    """Pointer and positions of the RoPE table: the caller's, or the cached one of rope_theta."""
+    """Pointer and positions of the RoPE table: the caller's, or the cached one of rope_theta for T positions."""
     if rope is None:
         if not rope_theta or rope_theta <= 0:
             return None, 0
+        if T > MAX_OWN_POSITIONS:
+            raise ValueError(f"a RoPE table for {T} positions is not made on the side: pass rope=rope_table(positions)")
         rope = _ROPE_CACHE.get((int(T), float(rope_theta), index))
         if rope is None:
             if torch.cuda.is_current_stream_capturing():
@@ -180,8 +183,9 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
                vscale: float = 1.0):
     """Rotate, quantise and store new rows (sfa_kv4_append): k, v [N, Hkv, 64]
     (bf16 or fp32; rows may be slices of wider ones) at slots [N] (distinct;
-    negative: skipped) and positions pos [N].  rope: a table of rope_table; else
-    the one of rope_theta for the pool's rows (0: no rotation)."""
+    negative: skipped) and positions pos [N].  rope: a table of rope_table that
+    covers the positions; else one of rope_theta for as many positions as the
+    pool has rows is made once and kept, up to 2^20 (0: no rotation)."""
     at, P, H, page = _pool(cache)
     N, _, ks = _rows(k, "k", H, at)
     n, _, vs = _rows(v, "v", H, at)
@@ -190,7 +194,7 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
         raise ValueError(f"k and v must have the same rows and type, got {tuple(k.shape)} {dtype}, {tuple(v.shape)} {v.dtype}")
     if not (0.0 < kscale < _INF and 0.0 < vscale < _INF):
         _scales(kscale, vscale)
-    rp, rT = _rope(rope, rope_theta, min(P * page, 1 << 24), at)
+    rp, rT = _rope(rope, rope_theta, P * page, at)
     _call(_lib().sfa_kv4_append, "sfa_kv4_append", at,
           Kv4Desc(P, page, H, 64, 0, 0, N, 0, _code(dtype), 0, ks, vs, kscale, vscale, rp, rT), k.data_ptr(), v.data_ptr(),
           cache.data_ptr(), _ints(at, N, slots, "slots"), _ints(at, N, pos, "pos"))
@@ -230,7 +234,7 @@ def _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale):
     R, width = block_table.shape
     if not (0.0 < kscale < _INF and 0.0 < vscale < _INF):
         _scales(kscale, vscale)
-    rp, rT = _rope(rope, rope_theta, min(width * page, 1 << 24), at)
+    rp, rT = _rope(rope, rope_theta, width * page, at)
     arr, nd, _ = _offsets(tuple(dist)) if dist is not None else (None, 0, None)
     return at, R, N, Hq, Kv4Desc(P, page, H, 64, R, width, N, Hq, _code(q.dtype), qs, 0, 0, kscale, vscale, rp, rT, arr, nd)
 
@@ -250,7 +254,8 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
     position (seq_lens - 1); else rows cu_q[r] .. cu_q[r + 1] - 1 are the last
     positions of request r, and rows behind cu_q[R] are left as they were.
     dist: offsets as for decode_int (0 required), None for every earlier row.
-    Returns o [N, Hq, 64] and lse fp32 [N, Hq]."""
+    rope: as in kv4_append (without it, for the block table's width).  o and lse
+    overlap none of the inputs.  Returns o [N, Hq, 64] and lse fp32 [N, Hq]."""
     at, R, N, Hq, d = _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale)
     if cu_q is None and N != R:
         raise ValueError(f"without cu_q, q has one row for each of the {R} requests, got {N}")

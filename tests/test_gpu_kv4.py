@@ -431,7 +431,9 @@ def test_offsets_past_32_bits(sfa):
     k = torch.randn((2, H, 64), device="cuda")
     v = torch.randn((2, H, 64), device="cuda")
     slots = _i32([(P - 1) * page + 5, (P - 1) * page + 6])
-    sfa.kv4_append(k, v, cache, slots, _i32([5, 6]))
+    with pytest.raises(ValueError, match="rope_table"):
+        sfa.kv4_append(k, v, cache, slots, _i32([5, 6]))
+    sfa.kv4_append(k, v, cache, slots, _i32([5, 6]), rope=sfa.rope_table(64))
     gk, gv = sfa.kv4_read(cache, slots, dtype=torch.float32)
     assert (gv - v).abs().max() <= v.abs().max() / 6 * 1.0625 + 1e-6  # half of the widest step, and the scale's rounding
     small = sfa.kv4_cache(2, H, page)
@@ -614,4 +616,137 @@ def test_attend_nan_value_among_rows(sfa, rows, dist):
     want[torch.from_numpy(hit), 4:, 32:48] = True
     assert torch.equal(o.isnan().cpu(), want)
     assert torch.equal(o[~want.cuda()], clean[~want.cuda()]) and torch.equal(lse, lse2)
+    assert sfa.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,Hq,dist", [(1, 8, None), (1, 8, [0, 3, 60]), (3, 8, list(range(70))), (6, 8, list(range(200))),
+                                         (80, 8, list(range(200))), (80, 8, None), (33, 8, [0, 1, 5])])
+def test_attend_far_below_zero(sfa, dtype, new, Hq, dist):
+    """All logits equal and far below zero (-800), rows of a tile reaching their first key in different steps: the
+    mean of the values, as with any other logit."""
+    import torch
+
+    rng = np.random.default_rng(16)
+    n, page, Hkv = 900, 64, 2
+    cache, table = make_cache(rng, [n], page, Hkv)
+    code, s8 = ref.quantise(np.full((n, Hkv, 64), -2.0, np.float32))
+    for p in range(n):
+        cache[table[0, p // page], :, 32 * (p % page):][:, :32] = code[p, :, 0::2] | (code[p, :, 1::2] << 4)
+        cache[table[0, p // page], :, 64 * page + 8 * (p % page):][:, :4] = s8[p]
+    k, v = stored(cache, table, 0, n, page)
+    assert (k == k[0, 0, 0]).all()
+    q = torch.full((new, Hq, 64), 50.0, dtype=_dt(dtype))
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32([n]), cu_q=_i32([0, new]), dist=dist, rope_theta=0)
+    assert sfa.get_device_status() == 0
+    check_rows(o, lse, q, cache, table, [n], [0, new], page, dist, None, 1.0, 1.0, dtype == "bf16")
+    assert (lse < -700).all()
+
+
+@pytest.mark.parametrize("new", [1, 5, 90])
+def test_attend_captured(sfa, new):
+    """A captured call (one that splits its rows, with its workspace from the graph's own memory), replayed
+    with other queries and lengths, gives the eager call's bits; two graphs replayed at once on two streams
+    do not disturb each other."""
+    import torch
+
+    rng = np.random.default_rng(17)
+    lens, page, R = [2000, 900, 130], 32, 3
+    cache, table = make_cache(rng, lens, page, 2)
+    c, t, rope = _cuda(cache), _cuda(table), sfa.rope_table(table.shape[1] * page)
+    cu = _i32(np.arange(R + 1) * new) if new > 1 else None
+    made = []
+    for i in range(2):
+        q = torch.zeros((R * new, 8, 64), dtype=torch.bfloat16, device="cuda")
+        n = _i32(lens)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                got = sfa.kv4_attend(q, c, t, n, cu_q=cu, rope=rope)
+        made.append((q, n, side, graph, got))
+    for step in range(4):
+        want = []
+        for i, (q, n, side, graph, got) in enumerate(made):
+            q.copy_(torch.from_numpy(rng.standard_normal(tuple(q.shape))))
+            n.copy_(_i32([x - 7 * step - i for x in lens]))
+            want.append(sfa.kv4_attend(q, c, t, n, cu_q=cu, rope=rope))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for q, n, side, graph, got in made:
+                with torch.cuda.stream(side):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for w, (q, n, side, graph, got) in zip(want, made):
+            assert torch.equal(w[0], got[0]) and torch.equal(w[1], got[1])
+    assert sfa.get_device_status() == 0
+    # a table that a call would have to make first is refused inside a capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="before the capture"):
+            sfa.kv4_attend(q, c, t, n, cu_q=cu, rope_theta=12345.0)
+        q.add_(0)
+
+
+def test_attend_on_another_stream(sfa):
+    """Inputs made on one stream and used on another that waits for it; the default stream's table is shared."""
+    import torch
+
+    rng = np.random.default_rng(18)
+    lens, page = [700, 40], 16
+    cache, table = make_cache(rng, lens, page, 2)
+    q = torch.from_numpy(rng.standard_normal((2, 8, 64))).float().cuda()
+    args = (_cuda(cache), _cuda(table), _i32(lens))
+    want = sfa.kv4_attend(q, *args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q2 = q * 2
+        got = sfa.kv4_attend(q2 / 2, *args)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_python_refusals(sfa):
+    """Wrong types, shapes, strides and devices are refused before anything is launched."""
+    import torch
+
+    cache, table = sfa.kv4_cache(4, 2, 16), torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    lens = _i32([1, 1, 1])
+    q = torch.zeros((3, 8, 64), device="cuda")
+    ok = lambda **kw: sfa.kv4_attend(kw.pop("q", q), kw.pop("cache", cache), kw.pop("table", table), kw.pop("lens", lens), **kw)  # noqa: E731
+    ok()
+    with pytest.raises(TypeError):
+        ok(q=q.half())
+    for kw in (dict(q=q[:, :, :32]), dict(q=q[0]), dict(q=q.transpose(0, 1)), dict(q=torch.zeros((3, 8, 128), device="cuda")[:, :, ::2]),
+               dict(q=torch.zeros((3, 8 * 64 + 1), device="cuda")[:, :512].unflatten(1, (8, 64))), dict(q=q.cpu()), dict(cache=cache[:, :, :100]),
+               dict(cache=cache.int()), dict(table=table.long()), dict(table=table.t()), dict(table=table.cpu()), dict(lens=lens[:2]),
+               dict(lens=lens.float()), dict(cu_q=lens), dict(cu_q=_i32([0, 1, 2, 3]).long()), dict(kscale=0.0), dict(vscale=float("nan")),
+               dict(o=torch.zeros((3, 8, 64), dtype=torch.bfloat16, device="cuda")), dict(lse=torch.zeros((3, 7), device="cuda")),
+               dict(rope=torch.zeros((5, 32), device="cuda")), dict(rope=torch.zeros((5, 32, 2), dtype=torch.float64, device="cuda")), dict(q=q[:2])):
+        with pytest.raises(ValueError):
+            ok(**kw)
+    for kw in (dict(dist=[1, 2]), dict(dist=[0, -1]), dict(dist=list(range(0, 1000, 2))), dict(q=torch.zeros((3, 7, 64), device="cuda"))):
+        with pytest.raises(sfa.SfaError):
+            ok(**kw)
+    k = torch.zeros((3, 2, 64), device="cuda")
+    for a in ((k, k.bfloat16(), cache, lens, lens), (k, k[:2], cache, lens, lens), (k, k, cache, lens[:2], lens), (k, k, cache, lens, lens.float()),
+              (k[:, :1], k[:, :1], cache, lens, lens)):
+        with pytest.raises(ValueError):
+            sfa.kv4_append(*a)
+    with pytest.raises(ValueError):
+        sfa.kv4_read(cache, lens, k=k, v=k[:2])
+    free = _i32([0, 1, 2, 3])
+    for a in ((lens[:2], lens, table, free, lens[:1]), (lens, lens, table, free, lens), (lens, lens, table.long(), free, lens[:1])):
+        with pytest.raises(ValueError):
+            sfa.kv4_plan(*a, page=16, rows=4)
+    with pytest.raises(ValueError):
+        sfa.kv4_plan(lens, lens, table, free, lens[:1], page=16, rows=-1)
+    with pytest.raises(sfa.SfaError):
+        sfa.kv4_plan(lens, lens, table, free, lens[:1], page=17, rows=4)
+    # nothing to do is no error
+    assert sfa.kv4_attend(q[:0], cache, table[:0], lens[:0])[0].shape == (0, 8, 64)
+    sfa.kv4_append(k[:0], k[:0], cache, lens[:0], lens[:0])
+    assert sfa.kv4_read(cache, lens[:0])[0].shape == (0, 2, 64)
     assert sfa.get_device_status() == 0

@@ -90,6 +90,9 @@ def test_nothing_to_do(sfa_lib):
     assert sfa_lib.sfa_kv4_append(_desc(N=0), None, None, None, None, None, None) == 0
     assert sfa_lib.sfa_kv4_read(_desc(N=0), None, None, None, None, None) == 0
     assert sfa_lib.sfa_kv4_attend(_desc(N=0), P, P, P, P, P, P, P, None, 0, None) == 0
+    assert sfa_lib.sfa_kv4_attend(_desc(N=0, R=0), P, P, P, P, None, P, P, None, 0, None) == 0
+    n = C.c_size_t(1)
+    assert sfa_lib.sfa_kv4_workspace_size(_desc(N=0, R=0), C.byref(n)) == 0 and n.value == 0
 
 
 def test_python_refuses_cpu_tensors(sfa_lib):
