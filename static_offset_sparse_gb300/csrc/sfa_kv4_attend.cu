@@ -167,17 +167,21 @@ __device__ __forceinline__ void value_products(const uint32_t* w, uint32_t sab, 
   }
 }
 
-// One online-softmax step over a tile's logits (log2 units times c, -inf for
-// absent keys): p = 2^(s - m + kPShift), o and l rescaled when m grows.
+// One online-softmax step over two tiles' logits (log2 units times c, -inf for
+// absent keys: bits 0, 1 of `there` say whether this lane's keys g and g + 8 of
+// the first tile are there, bits 2, 3 of the second): p = 2^(s - m + kPShift), o
+// and l rescaled when m grows.
 template <int NT>
-__device__ __forceinline__ void softmax_step(const QFrag<NT>& q, float (*s)[4], bool va, bool vb, float (*m)[2], float (*l)[2],
+__device__ __forceinline__ void softmax_step(const QFrag<NT>& q, float (*s)[NT][4], int there, float (*m)[2], float (*l)[2],
                                              float (*o)[4][4]) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float x = va ? s[nt][e] * q.c[nt][e] : -INFINITY, y = vb ? s[nt][2 + e] * q.c[nt][e] : -INFINITY;
-      float mx = fmaxf(x, y);
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = there >> i & 1 ? s[i >> 1][nt][2 * (i & 1) + e] * q.c[nt][e] : -INFINITY;
+      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -192,11 +196,12 @@ __device__ __forceinline__ void softmax_step(const QFrag<NT>& q, float (*s)[4], 
         }
       }
       const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e] - kPShift;  // no key yet: 2^-inf = 0
-      x = ex2(x - ref);
-      y = ex2(y - ref);
-      l[nt][e] += x + y;
-      s[nt][e] = x;
-      s[nt][2 + e] = y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = ex2(x[i] - ref);
+        s[i >> 1][nt][2 * (i & 1) + e] = x[i];
+      }
+      l[nt][e] += (x[0] + x[1]) + (x[2] + x[3]);
     }
 }
 
@@ -231,7 +236,7 @@ struct Acc {
 // ---------------------------------------------------------------- gather
 
 // Any offset list, one (row, KV head) a group of `warps` warps: lanes look up
-// their keys' pages, tiles of 16 keys go round the group's warps, and the
+// their keys' pages, pairs of 16-key tiles go round the group's warps, and the
 // group's partial results meet in shared memory.  Bounded by latency (row map,
 // block table, cache row: three dependent loads) at decode sizes and by its
 // instructions at prompt sizes (the query's rotation and split cost a row as
@@ -242,7 +247,7 @@ constexpr int kGatherWarps = 4;
 constexpr uint32_t kNone = 0xffffffffu;
 
 template <typename TIO, int NT>
-__global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 6 : 1)
+__global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
     kv4_gather_kernel(const Kv4Args a, const __grid_constant__ Plan P, int warps) {
   constexpr bool kExact = sizeof(TIO) == 4;
   __shared__ int rung[kMaxRungs];
@@ -273,9 +278,9 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 6 : 1)
       int nr = 0;  // rungs that reach a row
       for (int i = 0; i < P.n; i += 32) nr += __popc(__ballot_sync(0xffffffffu, i + lane < P.n && rung[i + lane] <= pos));
       const int nk = Wt + 1 + nr;
-      for (int j0 = 16 * mine; j0 < nk; j0 += 16 * warps) {
-        // lane i: key i mod 16 of the tile, its code row (in 32 bytes from the cache's begin) and its scales
-        const int j = j0 + (lane & 15);
+      for (int j0 = 32 * mine; j0 < nk; j0 += 32 * warps) {
+        // lane i: key i of two tiles, its code row (in 32 bytes from the cache's begin) and its scales
+        const int j = j0 + lane;
         uint32_t row = kNone;
         uint2 sc = make_uint2(0, 0);
         if (j < nk) {
@@ -289,23 +294,34 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 6 : 1)
             record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
           }
         }
-        const uint32_t ra = __shfl_sync(0xffffffffu, row, g), rb = __shfl_sync(0xffffffffu, row, g + 8);
-        const uint32_t sa = __shfl_sync(0xffffffffu, sc.x, g) >> (8 * t) & 255u, sb = __shfl_sync(0xffffffffu, sc.x, g + 8) >> (8 * t) & 255u;
-        uint2 ka = make_uint2(0, 0), kb = ka;
-        if (ra != kNone) ka = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)ra * 32 + 8 * t));
-        if (rb != kNone) kb = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)rb * 32 + 8 * t));
-        uint32_t w[4], vs[4];
+        const bool two = nk - j0 > 16;  // (uniform) the second tile has keys
+        float s[2][NT][4];
+        uint32_t w[2][4], vs[2][4];
+        int there = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int from = 2 * t + (e & 1) + 8 * (e >> 1);
-          const uint32_t rv = __shfl_sync(0xffffffffu, row, from);
-          vs[e] = __shfl_sync(0xffffffffu, sc.y, from) >> (8 * (g >> 1)) & 255u;
-          w[e] = rv == kNone ? 0u : __ldg(reinterpret_cast<const uint32_t*>(a.cache + (uint64_t)rv * 32 + 32 * S + 4 * g));
+        for (int i = 0; i < 2; ++i) {
+          if (i == 1 && !two) break;
+          const int g0 = 16 * i + g;
+          const uint32_t ra = __shfl_sync(0xffffffffu, row, g0), rb = __shfl_sync(0xffffffffu, row, g0 + 8);
+          const uint32_t sa = __shfl_sync(0xffffffffu, sc.x, g0) >> (8 * t) & 255u;
+          const uint32_t sb = __shfl_sync(0xffffffffu, sc.x, g0 + 8) >> (8 * t) & 255u;
+          uint2 ka = make_uint2(0, 0), kb = ka;
+          if (ra != kNone) ka = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)ra * 32 + 8 * t));
+          if (rb != kNone) kb = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)rb * 32 + 8 * t));
+          there |= (ra != kNone) << (2 * i) | (rb != kNone) << (2 * i + 1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int from = 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
+            const uint32_t rv = __shfl_sync(0xffffffffu, row, from);
+            vs[i][e] = __shfl_sync(0xffffffffu, sc.y, from) >> (8 * (g >> 1)) & 255u;
+            w[i][e] = rv == kNone ? 0u : __ldg(reinterpret_cast<const uint32_t*>(a.cache + (uint64_t)rv * 32 + 32 * S + 4 * g));
+          }
+          key_products<NT>(q, ka, kb, sa, sb, s[i]);
         }
-        float s[NT][4];
-        key_products<NT>(q, ka, kb, sa, sb, s);
-        softmax_step(q, s, ra != kNone, rb != kNone, acc.m, acc.l, acc.o);
-        value_products<NT, kExact>(w, vs[0] | vs[1] << 8, vs[2] | vs[3] << 8, s, acc.o);
+        softmax_step(q, s, there, acc.m, acc.l, acc.o);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (i == 0 || two) value_products<NT, kExact>(w[i], vs[i][0] | vs[i][1] << 8, vs[i][2] | vs[i][3] << 8, s[i], acc.o);
       }
     }
     acc.close();
@@ -684,25 +700,32 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
   const int64_t at = ((int64_t)blockIdx.x * sa.max_chunks) * width + col;
   // groups that share a warp are joined by shuffles, warps through shared memory
   const int wide = min(lanes, 32), step = max(lanes, 32);
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int c = grp; c < it.nch; c += groups) M = fmaxf(M, sa.part_ml[at + (int64_t)c * width].x);
-  for (int o = wide; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  red[threadIdx.x][8] = M;
-  __syncthreads();
-  for (int k = threadIdx.x % step; k < (int)blockDim.x; k += step) M = fmaxf(M, red[k][8]);
-  __syncthreads();
-  float l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  // (m, l, o) of the thread's chunks, one pass, the sums moved along with their maximum
+  float M = -INFINITY, l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
   for (int c = grp; c < it.nch; c += groups) {
     const float2 v = sa.part_ml[at + (int64_t)c * width];
-    const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - M);
     float z[8];
     load8(sa.part_o + (at + (int64_t)c * width) * kD + 8 * d, z);
-    l += v.y * f;
+    const float top = fmaxf(M, v.x);
+    const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top), back = M == -INFINITY ? 0.0f : ex2(M - top);
+    M = top;
+    l = fmaf(l, back, v.y * f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], f, y[e]);
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], back, z[e] * f);
   }
+  // all of them against the column's maximum
+  float top = M;
+  for (int o = wide; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  red[threadIdx.x][8] = top;
+  __syncthreads();
+  for (int k = threadIdx.x % step; k < (int)blockDim.x; k += step) top = fmaxf(top, red[k][8]);
+  __syncthreads();
+  const float f = M == -INFINITY ? 0.0f : ex2(M - top);
+  M = top;
+  l *= f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] *= f;
   for (int o = wide; o < 32; o <<= 1) {
     l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
@@ -820,7 +843,7 @@ int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void
     return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
   }
   const int tiles = (int)((std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS) + 15) / 16);
-  const int warps = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;
+  const int warps = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;  // two tiles a step
   if (dtype == SFA_BF16)
     e = G <= 8 ? gather<bf16, 1>(a, p, warps, s) : G == 16 ? gather<bf16, 2>(a, p, warps, s) : gather<bf16, 4>(a, p, warps, s);
   else
