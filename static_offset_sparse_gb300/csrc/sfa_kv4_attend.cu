@@ -26,18 +26,17 @@ namespace sfa {
 // come in.
 // One column tile: 8 B registers of high and 8 of low parts; returns the factor
 // that takes the accumulator of column g to its logit (log2 units, `scale`
-// included).  base: the first head of the first row, which stands at pos;
-// columns from ncol on, and rows before position 0, are zero.
+// included).  base: the first head of the first row; p: the position of this
+// lane's column, below 0 for a zero column.
 template <typename TIO>
-__device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, int lgG, int ncol, const float2* rope, int pos, float scale,
-                                              int nt, int lane, uint32_t* hi, uint32_t* lo) {
-  const int g = lane >> 2, t = lane & 3;
-  const int col = 8 * nt + g, p = pos + (col >> lgG);
+__device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, int lgG, int p, const float2* rope, float scale, int nt,
+                                              int lane, uint32_t* hi, uint32_t* lo) {
+  const int g = lane >> 2, t = lane & 3, col = 8 * nt + g;
   const TIO* row = base + (col >> lgG) * stride + (col & ((1 << lgG) - 1)) * kD;
   float x[16], y[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-  if (col < ncol && p >= 0) {
+  if (p >= 0) {
     load8(row + 16 * t, x);
     load8(row + 16 * t + 8, x + 8);
     if (rope) {  // the pair of dim j is j +- 32
@@ -77,12 +76,12 @@ struct QFrag {
   uint32_t hi[NT][8], lo[NT][8];
   float c[NT][2];  // logit of accumulator (heads 2t, 2t + 1), log2 units
 
-  template <typename TIO>
-  __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, int ncol, const float2* rope, int pos, float scale,
-                                       int lane) {
+  // at: position of column 8 nt + lane / 4
+  template <typename TIO, typename AT>
+  __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, AT at, const float2* rope, float scale, int lane) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float back = load_queries(base, stride, lgG, ncol, rope, pos, scale, nt, lane, hi[nt], lo[nt]);
+      const float back = load_queries(base, stride, lgG, at(8 * nt + (lane >> 2)), rope, scale, nt, lane, hi[nt], lo[nt]);
       c[nt][0] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3));
       c[nt][1] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3) + 4);
     }
@@ -168,11 +167,11 @@ __device__ __forceinline__ void value_products(const uint32_t* w, uint32_t sab, 
 }
 
 // One online-softmax step over two tiles' logits (log2 units times c, -inf for
-// absent keys: bits 0, 1 of `there` say whether this lane's keys g and g + 8 of
-// the first tile are there, bits 2, 3 of the second): p = 2^(s - m + kPShift), o
-// and l rescaled when m grows.
-template <int NT>
-__device__ __forceinline__ void softmax_step(const QFrag<NT>& q, float (*s)[NT][4], int there, float (*m)[2], float (*l)[2],
+// absent keys: there(nt, e, i) says whether column 8 nt + 2 t + e attends key g
+// of the first tile (i = 0), g + 8 (1), g and g + 8 of the second (2, 3)):
+// p = 2^(s - m + kPShift), o and l rescaled when m grows.
+template <int NT, typename THERE>
+__device__ __forceinline__ void softmax_step(const QFrag<NT>& q, float (*s)[NT][4], THERE there, float (*m)[2], float (*l)[2],
                                              float (*o)[4][4]) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -180,7 +179,7 @@ __device__ __forceinline__ void softmax_step(const QFrag<NT>& q, float (*s)[NT][
     for (int e = 0; e < 2; ++e) {
       float x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = there >> i & 1 ? s[i >> 1][nt][2 * (i & 1) + e] * q.c[nt][e] : -INFINITY;
+      for (int i = 0; i < 4; ++i) x[i] = there(nt, e, i) ? s[i >> 1][nt][2 * (i & 1) + e] * q.c[nt][e] : -INFINITY;
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -246,9 +245,19 @@ struct Acc {
 constexpr int kGatherWarps = 4;
 constexpr uint32_t kNone = 0xffffffffu;
 
-template <typename TIO, int NT>
+// PACK: 8 / G consecutive rows share a warp's columns.  Their keys follow one
+// another in the tiles, and a key of another row counts as absent: what a row
+// costs besides its keys (its query, its outputs) is paid once for all of them,
+// and tiles fill up (7807 rows of 19 keys, 8 / 2 heads: 29 us a row a warp).
+struct GatherRows {
+  int rows;        // 8 / G with PACK, else 1
+  int keys;        // most keys of a row
+  uint32_t magic;  // 2^32 / keys, rounded up: a key's row without a division
+};
+
+template <typename TIO, int NT, bool PACK>
 __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
-    kv4_gather_kernel(const Kv4Args a, const __grid_constant__ Plan P, int warps) {
+    kv4_gather_kernel(const Kv4Args a, const __grid_constant__ Plan P, int warps, const GatherRows gr) {
   constexpr bool kExact = sizeof(TIO) == 4;
   __shared__ int rung[kMaxRungs];
   extern __shared__ float part[];  // [kGatherWarps][8 NT][66]
@@ -258,46 +267,105 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
   for (int i = threadIdx.x; i < P.n; i += 32 * kGatherWarps) rung[i] = P.c[i];
   pdl_wait();
   __syncthreads();
-  const int units = a.N * a.Hkv, per = kGatherWarps / warps;  // (N * Hkv <= 2^27)
+  const int nrow = PACK ? gr.rows : 1;
+  const int units = (PACK ? (a.N + nrow - 1) / nrow : a.N) * a.Hkv, per = kGatherWarps / warps;  // (N * Hkv <= 2^27)
   for (int first = blockIdx.x * per; first < units; first += gridDim.x * per) {
-    const int unit = first + warp / warps, n = (int)((uint32_t)unit / (uint32_t)a.Hkv), h = unit - n * a.Hkv;
-    int r = 0, pos = -1;
-    const bool live = n < a.N && kv4_row(a, n, lane, r, pos);
+    const int unit = first + warp / warps, nu = (int)((uint32_t)unit / (uint32_t)a.Hkv), h = unit - nu * a.Hkv;
+    const int n = nu * nrow;
+    // lane i: row n + i, its request, position (-1: no keys) and keys
+    int r = 0, pos = -1, nk = 0;
+    bool live = false;
+    if (!PACK) {
+      live = n < a.N && kv4_row(a, n, lane, r, pos);
+    } else {
+      int r1 = 0, p1 = -1, end = 0;
+      for (int i = 0; i < nrow; ++i) {  // rows of one request stand side by side
+        bool l1 = n + i < a.N;
+        if (l1 && a.cu_q && i > 0 && n + i < end) {
+          ++p1;
+        } else {
+          l1 = l1 && kv4_row(a, n + i, lane, r1, p1);
+          end = l1 && a.cu_q ? a.cu_q[r1 + 1] : 0;
+        }
+        if (lane == i) {
+          r = r1;
+          pos = p1;
+          live = l1;
+        }
+      }
+    }
     if (live && (pos < -1 || (pos < 0 && a.cu_q) || pos >= (a.max_pages << a.lgS) || (a.rope && pos >= a.rope_T))) {
-      if (lane == 0) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+      if (PACK || lane == 0) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
       pos = -1;
     }
+    if (!live) pos = -1;
+    for (int i = 0; i < nrow; ++i) {
+      const int p = PACK ? __shfl_sync(0xffffffffu, pos, i) : pos;
+      int nr = 0;  // rungs that reach a row
+      for (int k = 0; k < P.n; k += 32) nr += __popc(__ballot_sync(0xffffffffu, k + lane < P.n && rung[k + lane] <= p));
+      if (!PACK || lane == i) nk = p < 0 ? 0 : min(P.W, p) + 1 + nr;
+    }
+    const uint32_t alive = PACK ? __ballot_sync(0xffffffffu, live) : live ? 1u : 0u;
+    // this lane's columns (two a column tile) belong to row (8 nt + 2 t + e) / G
     Acc<NT> acc;
     acc.clear();
-    if (live && pos >= 0) {
+    const int most = PACK ? gr.keys * nrow : nk;
+    if (PACK ? __any_sync(0xffffffffu, nk > 0) : nk > 0) {
       QFrag<NT> q;
-      q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, G, a.rope, pos, 0.125f * kLog2e * a.kscale,
-             lane);
-      const int32_t* trow = a.table + (int64_t)r * a.max_pages;
-      const int Wt = min(P.W, pos);
-      int nr = 0;  // rungs that reach a row
-      for (int i = 0; i < P.n; i += 32) nr += __popc(__ballot_sync(0xffffffffu, i + lane < P.n && rung[i + lane] <= pos));
-      const int nk = Wt + 1 + nr;
-      for (int j0 = 32 * mine; j0 < nk; j0 += 32 * warps) {
+      auto at = [&](int col) {
+        const int p = PACK ? __shfl_sync(0xffffffffu, pos, col >> a.lgG) : pos;
+        return PACK || col < G ? p : -1;
+      };
+      q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, at, a.rope, 0.125f * kLog2e * a.kscale, lane);
+      for (int j0 = 32 * mine; j0 < most; j0 += 32 * warps) {
         // lane i: key i of two tiles, its code row (in 32 bytes from the cache's begin) and its scales
-        const int j = j0 + lane;
+        int j = j0 + lane, kr = 0;
+        if (PACK) {
+          kr = (int)__umulhi((uint32_t)j, gr.magic);
+          j -= kr * gr.keys;
+        }
+        const int kpos = PACK ? __shfl_sync(0xffffffffu, pos, kr & 7) : pos;
+        const int knk = PACK ? __shfl_sync(0xffffffffu, nk, kr & 7) : nk;
+        const int kreq = PACK ? __shfl_sync(0xffffffffu, r, kr & 7) : r;
         uint32_t row = kNone;
         uint2 sc = make_uint2(0, 0);
-        if (j < nk) {
-          const int p = pos - (j <= Wt ? j : rung[j - Wt - 1]);
-          const int page = trow[p >> a.lgS], at = p & (S - 1);
+        if (kr < nrow && j < knk) {
+          const int Wt = min(P.W, kpos), p = kpos - (j <= Wt ? j : rung[j - Wt - 1]);
+          const int page = a.table[(int64_t)kreq * a.max_pages + (p >> a.lgS)], in = p & (S - 1);
           if (page >= 0 && page < a.n_pages) {
             const uint32_t first_row = ((uint32_t)page * a.Hkv + h) * (uint32_t)(9 * S / 4);
-            row = first_row + at;
-            sc = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)first_row * 32 + 64 * S + 8 * at));
+            row = first_row + in;
+            sc = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)first_row * 32 + 64 * S + 8 * in));
           } else {
             record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
           }
         }
-        const bool two = nk - j0 > 16;  // (uniform) the second tile has keys
+        if (PACK) {  // a NaN value block reaches its own row's columns, and no others (0 * NaN would)
+          uint32_t nan = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if ((sc.y >> (8 * b) & 127u) == 127u) nan |= 1u << b;
+          uint32_t with = __ballot_sync(0xffffffffu, nan != 0);
+          if (with) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if (nan >> b & 1) sc.y &= ~(255u << (8 * b));
+            for (; with; with &= with - 1) {
+              const int k = __ffs(with) - 1;
+              const uint32_t kn = __shfl_sync(0xffffffffu, nan, k);
+              const int of = __shfl_sync(0xffffffffu, kr, k);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (kn >> (g >> 1) & 1 && of == (2 * t + e) >> a.lgG)
+#pragma unroll
+                  for (int mt = 0; mt < 4; ++mt) acc.o[0][mt][e] = acc.o[0][mt][2 + e] = __int_as_float(0x7fffffff);
+            }
+          }
+        }
+        const bool two = most - j0 > 16;  // (uniform) the second tile has keys
         float s[2][NT][4];
         uint32_t w[2][4], vs[2][4];
-        int there = 0;
+        int there = 0, of[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (i == 1 && !two) break;
@@ -309,6 +377,10 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
           if (ra != kNone) ka = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)ra * 32 + 8 * t));
           if (rb != kNone) kb = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)rb * 32 + 8 * t));
           there |= (ra != kNone) << (2 * i) | (rb != kNone) << (2 * i + 1);
+          if (PACK) {
+            of[2 * i] = (int)__umulhi((uint32_t)(j0 + g0), gr.magic);
+            of[2 * i + 1] = (int)__umulhi((uint32_t)(j0 + g0 + 8), gr.magic);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int from = 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
@@ -318,7 +390,8 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
           }
           key_products<NT>(q, ka, kb, sa, sb, s[i]);
         }
-        softmax_step(q, s, there, acc.m, acc.l, acc.o);
+        softmax_step(
+            q, s, [&](int, int e, int i) { return (there >> i & 1) && (!PACK || of[i] == (2 * t + e) >> a.lgG); }, acc.m, acc.l, acc.o);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (i == 0 || two) value_products<NT, kExact>(w[i], vs[i][0] | vs[i][1] << 8, vs[i][2] | vs[i][3] << 8, s[i], acc.o);
@@ -326,7 +399,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
     }
     acc.close();
     if (warps == 1) {
-      if (live)
+      if (alive)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -338,7 +411,9 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
               x[2 * mt] = acc.o[nt][mt][e];
               x[2 * mt + 1] = acc.o[nt][mt][2 + e];
             }
-            if (head < G) write_head<TIO>(a, n, h * G + head, g, x, acc.m[nt][e], acc.l[nt][e]);
+            const int of = PACK ? head >> a.lgG : 0;
+            if (PACK ? alive >> of & 1 : head < G)
+              write_head<TIO>(a, n + of, h * G + (PACK ? head & (G - 1) : head), g, x, acc.m[nt][e], acc.l[nt][e]);
           }
       continue;
     }
@@ -377,13 +452,31 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
   }
 }
 
-template <typename TIO, int NT>
-static cudaError_t gather(const Kv4Args& a, const Plan& p, int warps, cudaStream_t s) {
-  const int64_t units = (int64_t)a.N * a.Hkv;
+template <typename TIO, int NT, bool PACK>
+static cudaError_t gather(const Kv4Args& a, const Plan& p, int warps, const GatherRows& gr, cudaStream_t s) {
+  const int64_t units = (int64_t)((a.N + gr.rows - 1) / gr.rows) * a.Hkv;
   const int per = kGatherWarps / warps;
   const size_t smem = warps > 1 ? (size_t)kGatherWarps * 8 * NT * 66 * sizeof(float) : 0;
-  const int64_t ctas = std::min<int64_t>((units + per - 1) / per, kSMs * 16);  // 16 CTAs of 4 warps fill an SM
-  return launch_pdl(kv4_gather_kernel<TIO, NT>, dim3((unsigned)ctas), dim3(32 * kGatherWarps), smem, s, a, p, warps);
+  const int64_t ctas = std::min<int64_t>((units + per - 1) / per, kSMs * 16);
+  return launch_pdl(kv4_gather_kernel<TIO, NT, PACK>, dim3((unsigned)ctas), dim3(32 * kGatherWarps), smem, s, a, p, warps, gr);
+}
+
+template <typename TIO>
+static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
+  const int64_t keys = std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS);
+  const int tiles = (int)((keys + 15) / 16), G = 1 << a.lgG;
+  const int warps = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;  // two tiles a step
+  GatherRows gr = {1, (int)keys, 0};
+  if (G > 16) return gather<TIO, 4, false>(a, p, warps, gr, s);
+  if (G > 8) return gather<TIO, 2, false>(a, p, warps, gr, s);
+  // more than a wave of rows with few keys: what counts is work, not latency
+  if (G < 8 && warps == 1 && (int64_t)a.N * a.Hkv > kSMs * 5 * kGatherWarps) {
+    gr.rows = 8 / G;
+    gr.keys = std::max(2, gr.keys);  // (2^32 / 1 would not fit)
+    gr.magic = (uint32_t)(((1ull << 32) + gr.keys - 1) / gr.keys);
+    return gather<TIO, 1, true>(a, p, 1, gr, s);
+  }
+  return gather<TIO, 1, false>(a, p, warps, gr, s);
 }
 
 // ---------------------------------------------------------------- stream
@@ -595,10 +688,11 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
     if (cur.x != qx || cur.h != qh) {
       const TIO* base = static_cast<const TIO*>(a.q) + (int64_t)cur.it.row0 * a.q_stride + cur.h * G * kD;
       const float scale = 0.125f * kLog2e * a.kscale;
+      auto at = [&](int col) { return col < ncol ? cur.it.pfirst + (col >> a.lgG) : -1; };
       if constexpr (NT == 4) {  // a column tile a warp
         static_assert(NT == kStreamWarps || NT != 4, "a column tile a warp");
         uint32_t hi[8], lo[8];
-        const float back = load_queries(base, a.q_stride, a.lgG, ncol, a.rope, cur.it.pfirst, scale, warp, lane, hi, lo);
+        const float back = load_queries(base, a.q_stride, a.lgG, at(8 * warp + g), a.rope, scale, warp, lane, hi, lo);
         bar_sync(1, 32 * kStreamWarps);  // the last item's queries have been used
         if (t == 0) qc[8 * warp + g] = back;
 #pragma unroll
@@ -610,7 +704,7 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
 #pragma unroll
           for (int e = 0; e < 2; ++e) q.c[nt][e] = qc[8 * nt + 2 * t + e];
       } else {
-        q.load(base, a.q_stride, a.lgG, ncol, a.rope, cur.it.pfirst, scale, lane);
+        q.load(base, a.q_stride, a.lgG, at, a.rope, scale, lane);
       }
       qx = cur.x;
       qh = cur.h;
@@ -829,7 +923,6 @@ size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, bool ragged) {
 }
 
 int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void* stream_) {
-  const int G = 1 << a.lgG;
   cudaStream_t s = (cudaStream_t)stream_;
   LaunchTimer tm(SFA_KERNEL_KV4_ATTEND, stream_);
   cudaError_t e;
@@ -842,12 +935,7 @@ int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void
                                    : stream_and_join<float>(a, z, s);
     return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
   }
-  const int tiles = (int)((std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS) + 15) / 16);
-  const int warps = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;  // two tiles a step
-  if (dtype == SFA_BF16)
-    e = G <= 8 ? gather<bf16, 1>(a, p, warps, s) : G == 16 ? gather<bf16, 2>(a, p, warps, s) : gather<bf16, 4>(a, p, warps, s);
-  else
-    e = G <= 8 ? gather<float, 1>(a, p, warps, s) : G == 16 ? gather<float, 2>(a, p, warps, s) : gather<float, 4>(a, p, warps, s);
+  e = dtype == SFA_BF16 ? gather_any<bf16>(a, p, s) : gather_any<float>(a, p, s);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 

@@ -750,3 +750,65 @@ def test_python_refusals(sfa):
     sfa.kv4_append(k[:0], k[:0], cache, lens[:0], lens[:0])
     assert sfa.kv4_read(cache, lens[:0])[0].shape == (0, 2, 64)
     assert sfa.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,dist", [(8, 2, FIB), (4, 4, [0, 1, 2, 5, 40]), (4, 2, [0]), (2, 2, list(range(32))), (8, 2, [0, 300])])
+def test_attend_many_rows_of_few_keys(sfa, dtype, Hq, Hkv, dist):
+    """Enough rows that several share a warp's columns: rows of one request and of neighbours, requests
+    without rows, rows without all their keys, a stored NaN value among them, an odd number of rows and
+    rows behind the last."""
+    import torch
+
+    rng = np.random.default_rng(19)
+    page = 16
+    lens = [1700 // Hkv, 5, 0, 900, 40, 2400 // Hkv]
+    new = [1650 // Hkv, 5, 0, 33, 1, 1500 // Hkv]
+    cache, table = make_cache(rng, lens, page, Hkv, garbage=True)
+    nan_at = lens[0] - 100  # request 0, KV head 0, dims 16 .. 31
+    cache[table[0, nan_at // page], 0, 64 * page + 8 * (nan_at % page) + 5] = 127
+    cu = np.concatenate([[0], np.cumsum(new)])
+    N = int(cu[-1]) + 60
+    q = torch.from_numpy(rng.standard_normal((N, Hq, 64))).to(_dt(dtype))
+    cs = ref.rope(table.shape[1] * page)
+    o = torch.full((N, Hq, 64), 3.0, dtype=_dt(dtype), device="cuda")
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), cu_q=_i32(cu), dist=dist, rope=_cuda(cs), o=o)
+    assert sfa.get_device_status() == 0
+    assert N * Hkv > 3040 and (o[cu[-1]:] == 3).all()
+    G = Hq // Hkv
+    pos = np.arange(lens[0] - new[0], lens[0])
+    hit = np.isin(pos - nan_at, dist)
+    assert hit.any()
+    want = torch.zeros((N, Hq, 64), dtype=torch.bool)
+    want[torch.from_numpy(np.flatnonzero(hit)), :G, 16:32] = True
+    assert torch.equal(o.isnan().cpu(), want)
+    clean = cache.copy()
+    clean[table[0, nan_at // page], 0, 64 * page + 8 * (nan_at % page) + 5] = 0  # what the other dims see of it
+    o = torch.where(want.cuda(), torch.zeros_like(o), o)
+    on, qn = o.double().cpu().numpy(), q.double().numpy()
+    for r, n in enumerate(lens):
+        a, b = cu[r], cu[r + 1]
+        if a == b:
+            continue
+        k, v = stored(clean, table, r, n, page)
+        wo, wl, av, sz = ref.attend(qn[a:b], k, v, np.arange(n - (b - a), n), dist, 1.0, 1.0, cs)
+        bo, bl = ref.bounds(wo, wl, av, sz, dtype == "bf16")
+        wo[want[a:b].numpy()] = 0
+        assert (np.abs(on[a:b] - wo) <= bo).all() and (np.abs(lse[a:b].double().cpu().numpy() - wl) <= bl).all(), r
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (2, 2)])
+def test_attend_many_tokens_of_few_keys(sfa, Hq, Hkv):
+    """One row a request, more requests than a wave: the same rows as a call for a few of them, bit for bit or within
+    the bound (other rows in a tile do not change a row's sums, only their order)."""
+    import torch
+
+    rng = np.random.default_rng(20)
+    R, page = 1601 if Hkv == 2 else 1700, 16
+    lens = [int(x) for x in rng.integers(0, 60, R)]
+    cache, table = make_cache(rng, lens, page, Hkv)
+    q = torch.from_numpy(rng.standard_normal((R, Hq, 64))).float()
+    cs = ref.rope(table.shape[1] * page)
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), dist=[0, 1, 2, 3, 8, 33], rope=_cuda(cs))
+    assert sfa.get_device_status() == 0
+    check_rows(o, lse, q, cache, table, lens, list(range(R + 1)), page, [0, 1, 2, 3, 8, 33], cs, 1.0, 1.0, False)
