@@ -465,15 +465,16 @@ template <typename TIO>
 static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
   const int64_t keys = std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS);
   const int tiles = (int)((keys + 15) / 16), G = 1 << a.lgG;
-  const int warps = tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;  // two tiles a step
+  // up to a wave of warps: a row's keys go round several, for its latency; beyond, what counts is work
+  const bool many = (int64_t)a.N * a.Hkv > kSMs * 5 * kGatherWarps;
+  const int warps = many || tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;  // two tiles a step
   GatherRows gr = {1, (int)keys, 0};
   if (G > 16) return gather<TIO, 4, false>(a, p, warps, gr, s);
   if (G > 8) return gather<TIO, 2, false>(a, p, warps, gr, s);
-  // more than a wave of rows with few keys: what counts is work, not latency
-  if (G < 8 && warps == 1 && (int64_t)a.N * a.Hkv > kSMs * 5 * kGatherWarps) {
+  if (G < 8 && many && keys <= 4096) {
     gr.rows = 8 / G;
     gr.keys = std::max(2, gr.keys);  // (2^32 / 1 would not fit)
-    gr.magic = (uint32_t)(((1ull << 32) + gr.keys - 1) / gr.keys);
+    gr.magic = (uint32_t)(((1ull << 32) + gr.keys - 1) / gr.keys);  // exact up to 8 * 4096 keys
     return gather<TIO, 1, true>(a, p, 1, gr, s);
   }
   return gather<TIO, 1, false>(a, p, warps, gr, s);
@@ -915,7 +916,7 @@ static cudaError_t stream_and_join(const Kv4Args& a, const StreamShape& z, cudaS
 
 bool kv4_attend_fits(const Kv4Args& a, const Plan& p, bool ragged) {
   const StreamShape z = stream_shape(a, p, ragged);
-  return (int64_t)z.s.items * a.Hkv * (((int64_t)a.max_pages << a.lgS) / kTile + 1) < (1LL << 31);
+  return (int64_t)z.s.items * a.Hkv * (((int64_t)a.max_pages << a.lgS) / kTile + 4) < (1LL << 31);
 }
 
 size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, bool ragged) {

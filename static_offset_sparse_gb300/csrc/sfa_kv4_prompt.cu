@@ -18,8 +18,8 @@
 // against 768 clocks of products.
 //
 // The steps of all (item, KV head) units, in order, are shared out evenly over
-// one CTA an SM, to the step: units are long and few, and whole chunks of them
-// left a quarter of the SMs' time idle.  A unit that spans CTAs leaves a part
+// one CTA an SM, to the step (and what a unit costs besides): units are long and
+// few, and whole chunks of them left a quarter of the SMs' time idle.  A unit that spans CTAs leaves a part
 // from each in the workspace (two a CTA at most), joined by a second kernel; so
 // the last bits of a split row depend on the batch it is in.
 #include "sfa_kv4_stream.cuh"
@@ -69,22 +69,34 @@ __device__ __forceinline__ int item_steps(const StreamArgs& s, const Item& it) {
   return it.nch == 0 ? 0 : it.plast() < 0 ? 1 : (it.plast() / kTile - first_tile(s, it)) / 2 + 1;
 }
 
+// What a piece costs besides its steps (its queries, its first logits, its
+// outputs), in steps: the CTA where a unit begins has it in its share.  Without
+// it the CTAs with more pieces ran a quarter longer than the average (8 prompts
+// over 2048 to 16384 rows: 110 us with 0, 98 with 3, 95 with 6).
+constexpr int kUnitCost = 6;
+__device__ __forceinline__ int item_weight(const StreamArgs& s, const Item& it) {
+  const int n = item_steps(s, it);
+  return n == 0 ? 0 : n + kUnitCost;
+}
+
 // A CTA's piece of a unit: its steps s0 .. s1 - 1, tiles tb .. te - 1.
 struct Piece {
   Item it;
   int x, h, s0, s1, steps, tb, te;
-  int at, end;  // steps before this piece's first; the CTA's end
-  __device__ __forceinline__ void set(const StreamArgs& s, int from) {
+  int begin, end;  // the weight before this unit, and where the CTA's share ends
+  // the unit from weight `off` of it on; false if no step of it lies in the share
+  __device__ __forceinline__ bool set(const StreamArgs& s, int off) {
     steps = item_steps(s, it);
-    s0 = from;
-    s1 = min(steps, s0 + end - at);
+    s0 = max(0, off - kUnitCost);
+    s1 = max(s0, min(steps, end - begin - kUnitCost));
     const int t0 = first_tile(s, it);
     tb = t0 + 2 * s0;
     te = it.plast() < 0 ? tb : min(t0 + 2 * s1, it.plast() / kTile + 1);
+    return s0 < s1;
   }
   __device__ __forceinline__ bool next(const Kv4Args& a, const StreamArgs& s) {
-    at += s1 - s0;
-    if (at >= end) return false;
+    begin += steps + kUnitCost;
+    if (begin >= end) return false;
     if (++h == a.Hkv) {
       h = 0;
       do {
@@ -92,18 +104,17 @@ struct Piece {
         it = item_at(a, s, ++x);
       } while (it.nch == 0);
     }
-    set(s, 0);
-    return true;
+    return set(s, 0);  // (without a step it is the share's last unit)
   }
 };
 
-// The steps' shares: CTA b begins at share * b + min(b, rest).
+// The shares of the weight: CTA b's begins at share * b + min(b, rest).
 struct Shares {
   int share, rest;
   __device__ __forceinline__ int begin(int b) const { return share * b + min(b, rest); }
-  __device__ __forceinline__ int owner(int step) const {
+  __device__ __forceinline__ int owner(int w) const {
     const int big = (share + 1) * rest;
-    return step < big ? step / (share + 1) : rest + (step - big) / share;
+    return w < big ? w / (share + 1) : rest + (w - big) / share;
   }
 };
 
@@ -113,7 +124,7 @@ __device__ __forceinline__ bool find_piece(const Kv4Args& a, const StreamArgs& s
   const int per = (sa.items + kPThreads - 1) / kPThreads;
   const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
   int mine = 0;
-  for (int x = x0; x < x1; ++x) mine += item_steps(sa, item_at(a, sa, x)) * a.Hkv;
+  for (int x = x0; x < x1; ++x) mine += item_weight(sa, item_at(a, sa, x)) * a.Hkv;
   int inc = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -134,7 +145,7 @@ __device__ __forceinline__ bool find_piece(const Kv4Args& a, const StreamArgs& s
   if (first < last && first >= before && first < before + mine) {
     int at = before;
     for (int x = x0; x < x1; ++x) {
-      const int n = item_steps(sa, item_at(a, sa, x));
+      const int n = item_weight(sa, item_at(a, sa, x));
       if (first < at + n * a.Hkv) {
         where[0] = x;
         where[1] = (first - at) / n;
@@ -148,11 +159,10 @@ __device__ __forceinline__ bool find_piece(const Kv4Args& a, const StreamArgs& s
   if (first == last) return false;
   cur.x = where[0];
   cur.h = where[1];
-  cur.at = first;
+  cur.begin = first - where[2];
   cur.end = last;
   cur.it = item_at(a, sa, cur.x);
-  cur.set(sa, where[2]);
-  return true;
+  return cur.set(sa, where[2]) || cur.next(a, sa);
 }
 
 // 64 codes and 4 scales -> a row of f16 at row r of a swizzled tile; zero: zeros.
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
   if (!work) {
   } else if (warp == 12) {
     copy_run<kPSlots>(a, sa, cur, smem_u32(raw), smem_u32(sh.raw_full), smem_u32(sh.raw_empty), sh.pages,
-                      cur.at == 0 ? a.debug_skip : -1, lane);
+                      cur.begin == 0 && cur.s0 == 0 ? a.debug_skip : -1, lane);
   } else if (warp == 13) {
     // ---- the products
     constexpr uint32_t idS = idesc_f16(128, kStep, false, false), idO = idesc_f16(128, 64, false, true);
@@ -470,7 +480,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
     do {
       const int ncol = cur.it.nrows << a.lgG;
       if (tid == 0 && cur.s0 == 0) {  // the unit begins here: which parts it leaves
-        const int b = blockIdx.x, count = shares.owner(cur.at + cur.steps - 1) - b + 1;
+        const int b = blockIdx.x, count = shares.owner(cur.begin + kUnitCost + cur.steps - 1) - b + 1;
         parts.units[(int64_t)cur.x * a.Hkv + cur.h] = make_int2(2 * b + (first ? 0 : 1), count);
       }
       const bool whole = cur.s0 == 0 && cur.s1 == cur.steps;
