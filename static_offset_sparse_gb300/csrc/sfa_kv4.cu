@@ -16,7 +16,8 @@ namespace sfa {
 // popped in (request, page) order.  The work is a few hundred bytes a request
 // and bounded by latency, so one CTA does all of it between barriers (no
 // atomics: the same inputs give the same pages); the row maps of more than
-// kPlanRows rows are left to a second kernel over the whole card.
+// kPlanRows rows are left to a second kernel over the whole card (47458 rows:
+// 9.6 us, and 15 in the one CTA; 256 requests of a row each: 5.0 us).
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 4 * kPlanThreads;
 
@@ -275,7 +276,9 @@ __device__ __forceinline__ void load16(const TIO* p, float* x) {
 
 // Four threads a (row, head): two on the keys, each with 16 rotation pairs
 // (dims 16u.. and 32 + 16u..: two whole scale blocks), two on the values.
-// Bounded by memory: 2 * 64 elements in, 72 bytes out.
+// 2 * 64 elements in, 72 bytes out, but bounded by instructions and the loads'
+// latency: 32741 rows of 2 heads in bf16 (17.6 MB in) take 13.8 us with cold
+// caches, 670 warp instructions for a warp's eight (row, head)s at 1.8 a clock.
 template <typename TIO>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
   pdl_launch_dependents();
@@ -344,6 +347,8 @@ struct ReadArgs {
 };
 
 // Eight threads a (row, head), one for each scale block of its key and value.
+// Bounded by memory once there is enough to do: 65536 rows of 2 heads in bf16
+// (43 MB moved) take 9.3 us, 4.65 TB/s; a few hundred rows 2.1 us, latency alone.
 template <typename TIO>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const ReadArgs a) {
   pdl_launch_dependents();

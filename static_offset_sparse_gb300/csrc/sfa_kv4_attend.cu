@@ -237,40 +237,79 @@ struct Acc {
 // Any offset list, one (row, KV head) a group of `warps` warps: lanes look up
 // their keys' pages, pairs of 16-key tiles go round the group's warps, and the
 // group's partial results meet in shared memory.  Bounded by latency (row map,
-// block table, cache row: three dependent loads) at decode sizes and by its
-// instructions at prompt sizes (the query's rotation and split cost a row as
-// much as 16 keys do).  The offsets beyond the window are taken to shared memory
-// once a CTA, which walks over units: read where they come in, by as many
-// addresses as lanes, they were replayed for every tile.
+// block table, cache row: three dependent loads) at decode sizes (32 rows of 23
+// keys, 8 / 2 heads: 4.3 us) and by its instructions at prompt sizes (7807 rows
+// of 19 keys, 8 / 2 heads: 25 us, 1040 warp instructions a row pair and head at
+// 2 a clock; the query's rotation and split are 250 of them).  The offsets
+// beyond the window are taken to shared memory once a CTA, which walks over
+// units: read where they come in, by as many addresses as lanes, they were
+// replayed for every tile.
 constexpr int kGatherWarps = 4;
 constexpr uint32_t kNone = 0xffffffffu;
 
 // PACK: 8 / G consecutive rows share a warp's columns.  Their keys follow one
 // another in the tiles, and a key of another row counts as absent: what a row
 // costs besides its keys (its query, its outputs) is paid once for all of them,
-// and tiles fill up (7807 rows of 19 keys, 8 / 2 heads: 29 us a row a warp).
+// and tiles fill up (7807 rows of 19 keys, 8 / 2 heads: 29 us a row a warp, 25
+// so; 12800 rows, 4 / 4 heads: 82 and 43).
+//
+// CLUSTER: a (row, KV head) is a cluster of 8 CTAs, 32 warps, whose results meet
+// through distributed shared memory: a few rows over some thousands of keys in
+// one launch without a workspace.
+enum GatherKind { kOne, kPack, kCluster };
+constexpr int kClusterCtas = 8;
+
+// A cluster a (row, KV head), where all of them fit the card at once: 1 row of
+// 1000 keys, 8 / 2 heads 8.4 -> 6.4 us against the streaming kernel and its join,
+// 38 rows 11.3 -> 9.1, 4 requests of 6 to 9 rows 14.3 -> 9.2.  Up to 512 keys four
+// warps are no slower (7.0 and 6.4 us, 8.7 and 9.0); in two waves it loses
+// (64 rows: 12.5 and 15.5 us).
+static bool clustered(const Kv4Args& a, int64_t keys) {
+  return keys > 512 && (int64_t)a.N * a.Hkv * kClusterCtas <= 4 * kSMs;
+}
+
 struct GatherRows {
   int rows;        // 8 / G with PACK, else 1
   int keys;        // most keys of a row
   uint32_t magic;  // 2^32 / keys, rounded up: a key's row without a division
 };
 
-template <typename TIO, int NT, bool PACK>
+// A float of another CTA of the cluster, at the place that `mine` has in this one.
+__device__ __forceinline__ float cluster_read(const float* mine, int rank) {
+  uint32_t addr;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+template <typename TIO, int NT, GatherKind KIND>
 __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
     kv4_gather_kernel(const Kv4Args a, const __grid_constant__ Plan P, int warps, const GatherRows gr) {
-  constexpr bool kExact = sizeof(TIO) == 4;
+  constexpr bool kExact = sizeof(TIO) == 4, PACK = KIND == kPack;
   __shared__ int rung[kMaxRungs];
   extern __shared__ float part[];  // [kGatherWarps][8 NT][66]
+  __shared__ float joined[KIND == kCluster ? 8 * NT : 1][66];  // the CTA's (m, l, 64 sums) of a head
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int mine = warp % warps, G = 1 << a.lgG, S = 1 << a.lgS;
+  // this warp among those of its (row, KV head)
+  const int rank = KIND == kCluster ? blockIdx.x % kClusterCtas : 0;
+  const int mine = KIND == kCluster ? rank * kGatherWarps + warp : warp % warps;
+  const int G = 1 << a.lgG, S = 1 << a.lgS;
   for (int i = threadIdx.x; i < P.n; i += 32 * kGatherWarps) rung[i] = P.c[i];
   pdl_wait();
   __syncthreads();
   const int nrow = PACK ? gr.rows : 1;
-  const int units = (PACK ? (a.N + nrow - 1) / nrow : a.N) * a.Hkv, per = kGatherWarps / warps;  // (N * Hkv <= 2^27)
-  for (int first = blockIdx.x * per; first < units; first += gridDim.x * per) {
-    const int unit = first + warp / warps, nu = (int)((uint32_t)unit / (uint32_t)a.Hkv), h = unit - nu * a.Hkv;
+  const int units = (PACK ? (a.N + nrow - 1) / nrow : a.N) * a.Hkv;  // (N * Hkv <= 2^27)
+  const int per = KIND == kCluster ? 1 : kGatherWarps / warps;
+  const int begin = KIND == kCluster ? blockIdx.x / kClusterCtas : blockIdx.x * per;
+  const int stride = KIND == kCluster ? gridDim.x / kClusterCtas : gridDim.x * per;
+  for (int first = begin; first < units; first += stride) {
+    const int unit = KIND == kCluster ? first : first + warp / warps;
+    const int nu = (int)((uint32_t)unit / (uint32_t)a.Hkv), h = unit - nu * a.Hkv;
     const int n = nu * nrow;
     // lane i: row n + i, its request, position (-1: no keys) and keys
     int r = 0, pos = -1, nk = 0;
@@ -317,7 +356,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
         return PACK || col < G ? p : -1;
       };
       q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, at, a.rope, 0.125f * kLog2e * a.kscale, lane);
-      for (int j0 = 32 * mine; j0 < most; j0 += 32 * warps) {
+      for (int j0 = 32 * mine; j0 < most; j0 += 32 * (KIND == kCluster ? kClusterCtas * kGatherWarps : warps)) {
         // lane i: key i of two tiles, its code row (in 32 bytes from the cache's begin) and its scales
         int j = j0 + lane, kr = 0;
         if (PACK) {
@@ -398,7 +437,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
       }
     }
     acc.close();
-    if (warps == 1) {
+    if (KIND != kCluster && warps == 1) {
       if (alive)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -433,51 +472,92 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
       }
     __syncthreads();
     // lanes 8 i .. 8 i + 7 of the group's warp w join head 4 w + i, and so on
-    for (int head = 4 * mine + (lane >> 3); live && head < G; head += 4 * warps) {
-      const float* w = part + ((warp - mine) * 8 * NT + head) * 66;
-      const int d = lane & 7;
+    const int team = KIND == kCluster ? kGatherWarps : warps, member = KIND == kCluster ? warp : mine, d = lane & 7;
+    for (int head = 4 * member + (lane >> 3); live && head < G; head += 4 * team) {
+      const float* w = part + ((warp - member) * 8 * NT + head) * 66;
       float m = -INFINITY, l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      for (int i = 0; i < warps; ++i) m = fmaxf(m, w[i * 8 * NT * 66]);
-      for (int i = 0; i < warps; ++i) {
+      for (int i = 0; i < team; ++i) m = fmaxf(m, w[i * 8 * NT * 66]);
+      for (int i = 0; i < team; ++i) {
         const float* wi = w + i * 8 * NT * 66;
         if (wi[1] == 0.0f) continue;
-        const float f = ex2(wi[0] - m);
+        const float f = wi[0] == -INFINITY ? 0.0f : ex2(wi[0] - m);
         l += wi[1] * f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += wi[2 + 8 * d + e] * f;
       }
-      write_head<TIO>(a, n, h * G + head, d, x, m, l);
+      if (KIND != kCluster) {
+        write_head<TIO>(a, n, h * G + head, d, x, m, l);
+        continue;
+      }
+      if (d == 0) {
+        joined[head][0] = m;
+        joined[head][1] = l;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) joined[head][2 + 8 * d + e] = x[e];
     }
-    __syncthreads();  // the buffer is filled again by the next unit
+    if (KIND != kCluster) {
+      __syncthreads();  // the buffer is filled again by the next unit
+      continue;
+    }
+    cluster_sync();
+    // CTA `rank` joins heads rank, rank + 8, ..: a warp a head, eight dims a lane
+    for (int head = rank + kClusterCtas * warp; live && head < G; head += kClusterCtas * kGatherWarps) {
+      float m[kClusterCtas], M = -INFINITY, l = 0.0f, x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < kClusterCtas; ++c) {
+        m[c] = cluster_read(&joined[head][0], c);
+        M = fmaxf(M, m[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < kClusterCtas; ++c) {
+        const float f = m[c] == -INFINITY ? 0.0f : ex2(m[c] - M);
+        l = fmaf(cluster_read(&joined[head][1], c), f, l);
+        if (lane < 8)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = fmaf(cluster_read(&joined[head][2 + 8 * lane + e], c), f, x[e]);
+      }
+      if (lane < 8) write_head<TIO>(a, n, h * G + head, lane, x, M, l);
+    }
+    cluster_sync();  // until all have read, before the next unit or the end
   }
 }
 
-template <typename TIO, int NT, bool PACK>
+template <typename TIO, int NT, GatherKind KIND>
 static cudaError_t gather(const Kv4Args& a, const Plan& p, int warps, const GatherRows& gr, cudaStream_t s) {
   const int64_t units = (int64_t)((a.N + gr.rows - 1) / gr.rows) * a.Hkv;
   const int per = kGatherWarps / warps;
-  const size_t smem = warps > 1 ? (size_t)kGatherWarps * 8 * NT * 66 * sizeof(float) : 0;
+  const size_t smem = KIND == kCluster || warps > 1 ? (size_t)kGatherWarps * 8 * NT * 66 * sizeof(float) : 0;
+  if (KIND == kCluster)
+    return launch_pdl_cluster(kv4_gather_kernel<TIO, NT, KIND>, dim3((unsigned)(units * kClusterCtas)), dim3(32 * kGatherWarps),
+                              kClusterCtas, smem, s, a, p, warps, gr);
   const int64_t ctas = std::min<int64_t>((units + per - 1) / per, kSMs * 16);
-  return launch_pdl(kv4_gather_kernel<TIO, NT, PACK>, dim3((unsigned)ctas), dim3(32 * kGatherWarps), smem, s, a, p, warps, gr);
+  return launch_pdl(kv4_gather_kernel<TIO, NT, KIND>, dim3((unsigned)ctas), dim3(32 * kGatherWarps), smem, s, a, p, warps, gr);
+}
+
+template <typename TIO, GatherKind KIND>
+static cudaError_t gather_nt(const Kv4Args& a, const Plan& p, int warps, const GatherRows& gr, cudaStream_t s) {
+  const int G = 1 << a.lgG;
+  return G > 16  ? gather<TIO, 4, KIND>(a, p, warps, gr, s)
+         : G > 8 ? gather<TIO, 2, KIND>(a, p, warps, gr, s)
+                 : gather<TIO, 1, KIND>(a, p, warps, gr, s);
 }
 
 template <typename TIO>
 static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
-  const int64_t keys = std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS);
+  const int64_t keys = std::min<int64_t>((int64_t)p.W + 1 + p.n, (int64_t)a.max_pages << a.lgS), units = (int64_t)a.N * a.Hkv;
   const int tiles = (int)((keys + 15) / 16), G = 1 << a.lgG;
-  // up to a wave of warps: a row's keys go round several, for its latency; beyond, what counts is work
-  const bool many = (int64_t)a.N * a.Hkv > kSMs * 5 * kGatherWarps;
-  const int warps = many || tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4;  // two tiles a step
   GatherRows gr = {1, (int)keys, 0};
-  if (G > 16) return gather<TIO, 4, false>(a, p, warps, gr, s);
-  if (G > 8) return gather<TIO, 2, false>(a, p, warps, gr, s);
+  if (clustered(a, keys)) return gather_nt<TIO, kCluster>(a, p, kGatherWarps, gr, s);
+  // up to a wave of warps: a row's keys go round several, for its latency; beyond, what counts is work
+  const bool many = units > kSMs * 5 * kGatherWarps;
   if (G < 8 && many && keys <= 4096) {
     gr.rows = 8 / G;
     gr.keys = std::max(2, gr.keys);  // (2^32 / 1 would not fit)
     gr.magic = (uint32_t)(((1ull << 32) + gr.keys - 1) / gr.keys);  // exact up to 8 * 4096 keys
-    return gather<TIO, 1, true>(a, p, 1, gr, s);
+    return gather<TIO, 1, kPack>(a, p, 1, gr, s);
   }
-  return gather<TIO, 1, false>(a, p, warps, gr, s);
+  return gather_nt<TIO, kOne>(a, p, many || tiles <= 2 ? 1 : tiles <= 4 ? 2 : 4, gr, s);  // two tiles a step
 }
 
 // ---------------------------------------------------------------- stream
@@ -498,6 +578,11 @@ static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
 // chunks and items.  The four warps take every fourth tile of a chunk and meet
 // in shared memory at its end.  Chunks of a longer item go to the workspace,
 // joined by a second kernel.
+//
+// Bounded by its instructions, next to the memory: 128 requests of 1024 to 32768
+// rows, 8 / 2 heads (167 MB) take 54 us, 3.1 TB/s (the tiles' instructions 28 us
+// of it, the memory would take 25; the rest is the start, the chunks' ends and
+// an uneven end), one of 400001 rows, 16 / 2 heads (58 MB) 23.
 constexpr int kStreamWarps = 4, kSlots = 8;
 
 // Row r of a 16-key tile is key r ^ (r >> 2 & 1): the rows that lanes of one
@@ -778,6 +863,7 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
 // The chunks of one (item, KV head) joined: `cols` columns a CTA, 8 lanes a
 // column, the chunks dealt out over the remaining threads (their partial sums
 // are read once, 264 bytes each: what counts is how many are in flight).
+// Bounded by latency: 8 to 9 us after either of the calls above.
 constexpr int kJoinThreads = 512;
 
 template <typename TIO>
@@ -850,9 +936,13 @@ struct StreamShape {
 static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   StreamShape z = {};
   const int64_t cap = (int64_t)a.max_pages << a.lgS;
-  // few keys, or a wave of rows with few: one launch and no workspace win
-  const int64_t keys = std::min<int64_t>(cap, (int64_t)p.W + 1);
-  if (p.n > 0 || keys <= 64 || (keys <= 512 && (int64_t)a.N * a.Hkv <= 4 * kSMs)) return z;
+  // few keys, or a wave of rows with few, or of clusters with some: one launch and
+  // no workspace win.  (A cluster's keys: 16 units of 3000, 9.7 us streamed and
+  // 10.0; 76 units of 4000, 17.5 and 15.0; 2 units of 2000 and 4000, 8.4 and 8.5
+  // streamed, 7.9 and 9.4.)
+  const int64_t keys = std::min<int64_t>(cap, (int64_t)p.W + 1), units_n = (int64_t)a.N * a.Hkv;
+  if (p.n > 0 || keys <= 64 || (keys <= 512 && units_n <= 4 * kSMs)) return z;
+  if (keys <= (units_n >= 16 ? 4096 : 2048) && clustered(a, keys)) return z;
   const int G = 1 << a.lgG;
   // columns a warp holds: as many rows as a request brings on average, 32 at most
   const int avg = ragged ? (a.N + a.R - 1) / a.R : 1;

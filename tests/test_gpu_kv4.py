@@ -325,6 +325,30 @@ def test_attend_long(sfa, dtype, dist):
     check_rows(o, lse, q, cache, table, lens, list(range(6)), page, dist, cs, 1.0, 1.0, dtype == "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 1), (32, 1), (4, 4)])
+@pytest.mark.parametrize("new", [None, [3, 0, 4, 1, 2], [9, 0, 6, 1, 2]])
+@pytest.mark.parametrize("dist", [None, list(range(700)), list(range(520)) + [530, 600, 1200]])
+def test_attend_block_tables(sfa, dtype, Hq, Hkv, new, dist):
+    """Few rows of up to 1400 keys under block tables of 1500, 3500 and 6500 rows, whose width and not the
+    requests' lengths chooses how a row's keys are shared out."""
+    import torch
+
+    rng = np.random.default_rng(21)
+    lens, page = [1400, 0, 513, 1, 90], 32
+    cache, table = make_cache(rng, lens, page, Hkv)
+    cu = np.concatenate([[0], np.cumsum(new if new else [1] * len(lens))])
+    q = torch.from_numpy(1.5 * rng.standard_normal((cu[-1], Hq, 64))).to(_dt(dtype))
+    c, cs = _cuda(cache), ref.rope(table.shape[1] * page)
+    for rows in (1500, 3500, 6500):
+        t = np.full((len(lens), rows // page), -1, np.int32)
+        t[:, :table.shape[1]] = table
+        o, lse = sfa.kv4_attend(q.cuda(), c, _cuda(t), _i32(lens), cu_q=_i32(cu) if new else None, dist=dist,
+                                rope=_cuda(cs), rope_theta=0, vscale=1.3)
+        assert sfa.get_device_status() == 0
+        check_rows(o, lse, q, cache, table, lens, cu, page, dist, cs, 1.0, 1.3, dtype == "bf16")
+
+
 def test_attend_sizes_of_queries(sfa):
     """Queries from the smallest to the largest: scaled by powers of two the result of a scaled
     kscale, bit for bit; zero queries average the values."""
@@ -637,10 +661,12 @@ def test_attend_far_below_zero(sfa, dtype, new, Hq, dist):
     k, v = stored(cache, table, 0, n, page)
     assert (k == k[0, 0, 0]).all()
     q = torch.full((new, Hq, 64), 50.0, dtype=_dt(dtype))
-    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32([n]), cu_q=_i32([0, new]), dist=dist, rope_theta=0)
-    assert sfa.get_device_status() == 0
-    check_rows(o, lse, q, cache, table, [n], [0, new], page, dist, None, 1.0, 1.0, dtype == "bf16")
-    assert (lse < -700).all()
+    for spare in (0, 100):  # columns of the block table
+        t = np.pad(table, ((0, 0), (0, spare)), constant_values=-1)
+        o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(t), _i32([n]), cu_q=_i32([0, new]), dist=dist, rope_theta=0)
+        assert sfa.get_device_status() == 0
+        check_rows(o, lse, q, cache, table, [n], [0, new], page, dist, None, 1.0, 1.0, dtype == "bf16")
+        assert (lse < -700).all()
 
 
 @pytest.mark.parametrize("new", [1, 5, 90])
