@@ -176,8 +176,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
 __global__ void __launch_bounds__(256) kv4_plan_rows_kernel(const PlanArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.N) return;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= a.N) return;
+  const int i = (int)at;
   if (i >= a.cu[a.R]) {
     a.slots[i] = a.pos[i] = -1;
     return;
@@ -486,7 +487,7 @@ int sfa_kv4_plan(const sfa_kv4_desc* d, const int32_t* n_new, const int32_t* seq
   LaunchTimer tm(SFA_KERNEL_KV4_PLAN, stream);
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = launch_pdl(kv4_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, a, here);
-  if (e == cudaSuccess && !here) e = launch_pdl(kv4_plan_rows_kernel, dim3((unsigned)((d->N + 255) / 256)), dim3(256), 0, s, a);
+  if (e == cudaSuccess && !here) e = launch_pdl(kv4_plan_rows_kernel, dim3((unsigned)(((int64_t)d->N + 255) / 256)), dim3(256), 0, s, a);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 

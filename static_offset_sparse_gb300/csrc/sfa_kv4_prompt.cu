@@ -486,6 +486,10 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         const int b = blockIdx.x, count = shares.owner(cur.begin + kUnitCost + cur.steps - 1) - b + 1;
         parts.units[(int64_t)cur.x * a.Hkv + cur.h] = make_int2(2 * b + (first ? 0 : 1), count);
       }
+      if (dead) {  // (the join reads every unit's parts, whatever is in them)
+        first = false;
+        continue;
+      }
       const bool whole = cur.s0 == 0 && cur.s1 == cur.steps;
       if (ncol <= 128 * T) {  // no column of this tile
         j += (cur.te - cur.tb + 1) >> 1;
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
       }
       tc05_fence_before();
       first = false;
-    } while (!dead && cur.next(a, sa));
+    } while (cur.next(a, sa));
     if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
   }
   tc05_fence_before();

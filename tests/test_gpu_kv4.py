@@ -588,6 +588,30 @@ def test_attend_wait_that_runs_out(sfa, sfa_lib, rows):
     assert sfa.get_device_status() == 0 and torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
 
 
+def test_attend_wait_that_runs_out_before_other_units(sfa, sfa_lib):
+    """A wait that runs out in the first of a CTA's pieces of prompts: those behind it are still told to the
+    join, in a workspace that holds anything before."""
+    import torch
+
+    rng = np.random.default_rng(22)
+    lens, new, page = [400] * 200, 70, 16
+    cache, table = make_cache(rng, [400], page, 2)
+    q = torch.from_numpy(rng.standard_normal((200 * new, 8, 64))).float().cuda()
+    args = (q, _cuda(cache), _cuda(np.repeat(table, 200, 0)), _i32(lens))
+    cu = _i32(np.arange(201) * new)
+    n = sfa.kv4_workspace_size(*args[:3])
+    good = sfa.kv4_attend(*args, cu_q=cu)
+    torch.cuda.synchronize()
+    try:
+        assert sfa_lib.sfa_debug_inject(2000000, 0) == 0
+        sfa.kv4_attend(*args, cu_q=cu, ws=torch.full((n,), 1, dtype=torch.uint8, device="cuda"))
+        assert sfa.get_device_status() == 5  # SFA_ERR_TIMEOUT
+    finally:
+        sfa_lib.sfa_debug_inject(0, -1)
+    again = sfa.kv4_attend(*args, cu_q=cu, ws=torch.full((n,), 1, dtype=torch.uint8, device="cuda"))
+    assert sfa.get_device_status() == 0 and torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("lens,new,Hq,Hkv,page,dist", [
     ([700, 300, 64], [200, 129, 64], 8, 2, 64, None),
