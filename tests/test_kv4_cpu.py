@@ -160,3 +160,13 @@ def test_workspace_holds_the_split_rows(sfa_lib, R, N, Hq, Hkv, page, max_pages)
     assert n >= 2 * N * Hq * 66 * 4 or (n == 0 and N > 2000)  # enough rows: none is split
     assert n <= 16 * 608 * 8 * 66 * 4 + 16 * 304 * 16 * 66 * 4
     assert _workspace(sfa_lib, **{**kw, "max_pages": 256 // page}) == 0
+
+
+def test_descriptor_bytes():
+    """The Python calls' descriptor, packed by hand, is the C structure."""
+    pytest.importorskip("torch")
+    from static_offset_sparse_gb300 import kv4
+    from static_offset_sparse_gb300._lib import Kv4Desc
+
+    values = [*range(101, 110), 2 ** 40, 2 ** 41, 2 ** 42, 0.75, 1.5, 2 ** 47 - 16, 7, 2 ** 46, 9]
+    assert bytes(Kv4Desc(*values)) == kv4._desc(*values) and len(values) == len(Kv4Desc._fields_)
