@@ -563,7 +563,7 @@ static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
 // ---------------------------------------------------------------- stream
 
 // The whole prefix, or a wide window: a request's pages stream through shared
-// memory.  A CTA is four warps that compute and one that copies: it reads a
+// memory.  A team is four warps that compute and one that copies: it reads a
 // chunk's page ids, waits for a free slot of the ring (tiles of 64 keys) and
 // starts one asynchronous bulk copy a page (64-row pages, whose block is a tile
 // as it stands) or three (key codes, value codes, scales).
@@ -572,15 +572,22 @@ static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
 // row), its columns rows x heads of one KV head; its keys are cut into chunks
 // of chunk_tiles tiles at absolute places, so what is added to what depends on
 // the call's shapes and the row's own length, not on other requests.  The tiles
-// of all chunks, in order, are shared out evenly over one wave of CTAs, whole
-// chunks at a time: each CTA adds up the items' tiles (from the lengths, in one
-// block-wide scan), takes its part and walks it, the copies running on across
-// chunks and items.  The four warps take every fourth tile of a chunk and meet
-// in shared memory at its end.  Chunks of a longer item go to the workspace,
-// joined by a second kernel.
+// of all chunks, in order, are shared out evenly over one wave of teams, whole
+// chunks at a time: each CTA adds up the items' tiles (from the lengths, in
+// one block-wide scan), and each team takes its part and walks it, the copies
+// running on across chunks and items.  The four warps take every fourth tile of a
+// chunk and meet in shared memory at its end.  Chunks of a longer item go to the
+// workspace, joined by a second kernel.
+//
+// One column tile: one CTA an SM with four teams, not a CTA a team.  A quarter of
+// an SM's registers holds five warps of 96, and four CTAs of five warps fit only
+// if each puts its fifth in another quarter; where they did not, three ran, and
+// the fourth when all else was done (the batch below: 67 us with the join, and
+// 55).  More columns: two CTAs of a team an SM, for their registers (a CTA of two
+// teams may have 168 a thread: 64 requests of 4 to 8 rows, 32 columns, 75 us and 71).
 //
 // Bounded by its instructions, next to the memory: 128 requests of 1024 to 32768
-// rows, 8 / 2 heads (167 MB) take 54 us, 3.1 TB/s (the tiles' instructions 28 us
+// rows, 8 / 2 heads (167 MB) take 46 us, 3.6 TB/s (the tiles' instructions 28 us
 // of it, the memory would take 25; the rest is the start, the chunks' ends and
 // an uneven end), one of 400001 rows, 16 / 2 heads (58 MB) 23.
 constexpr int kStreamWarps = 4, kSlots = 8;
@@ -727,14 +734,28 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
-// CTAs an SM of the variant with NT column tiles.
-constexpr int stream_ctas(int NT) { return NT == 1 ? 4 : 2; }
+// The variant with NT column tiles: teams a CTA, CTAs an SM, shared memory of a team.
+template <int NT>
+constexpr int kStreamTeams = NT == 1 ? 4 : 1;
+template <int NT>
+constexpr int kStreamCtas = NT == 1 ? 1 : 2;
+template <int NT>
+constexpr int kTeamSmem = (kSlots * kTileBytes + 2 * kStreamWarps * 8 * NT * (66 * 4 + 8) + (NT == 4 ? 4 * NT * 512 + 8 * NT * 4 : 0) +
+                           8 * (2 * kSlots + 4) + 4 * kSlots + 127) / 128 * 128;
 
 template <typename TIO, int NT>
-__global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
+__global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kStreamCtas<NT>)
+    kv4_stream_kernel(const Kv4Args a, const StreamArgs sa) {
   constexpr bool kExact = sizeof(TIO) == 4;
-  constexpr int NC = 8 * NT, kThr = 32 * (kStreamWarps + 1);
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int NC = 8 * NT, TEAMS = kStreamTeams<NT>, kThr = 32 * (kStreamWarps + 1) * TEAMS;
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  __shared__ int sums[kThr / 32], where[4 * TEAMS];  // where: first item, head, chunk, weight of a team
+  const int tid = threadIdx.x, lane = tid & 31, cta_warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  // the teams' computing warps, then their copying ones
+  const bool copies = cta_warp >= kStreamWarps * TEAMS;
+  const int team = TEAMS == 1 ? 0 : copies ? cta_warp - kStreamWarps * TEAMS : cta_warp / kStreamWarps;
+  const int warp = TEAMS == 1 ? cta_warp : cta_warp % kStreamWarps;
+  uint8_t* const smem = smem_all + team * kTeamSmem<NT>;
   float* const po = reinterpret_cast<float*>(smem + kSlots * kTileBytes);         // [2][warp][NC][66]
   float2* const ml = reinterpret_cast<float2*>(po + 2 * kStreamWarps * NC * 66);  // [2][warp][NC]
   uint4* const qs = reinterpret_cast<uint4*>(ml + 2 * kStreamWarps * NC);          // NT = 4: [step][column tile][lane]
@@ -742,21 +763,18 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
   // the slots' full and empty barriers, the buffers' (filled by four warps, joined by one)
   uint64_t* const bars = NT == 4 ? reinterpret_cast<uint64_t*>(qc + NC) : reinterpret_cast<uint64_t*>(ml + 2 * kStreamWarps * NC);
   int* const pages = reinterpret_cast<int*>(bars + 2 * kSlots + 4);
-  int* const sums = pages + kSlots;                                               // [warps]
-  int* const where = sums + kStreamWarps + 1;                                     // first item, head, chunk, weight
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kSlots;
   pdl_launch_dependents();
-  if (tid == 0) {
+  if (copies && lane == 0) {
     for (int i = 0; i < 2 * kSlots + 4; ++i) mbar_init(full + 8 * i, i == 2 * kSlots || i == 2 * kSlots + 1 ? kStreamWarps : 1);
     mbar_fence_init();
   }
   pdl_wait();
 
   Cursor cur;
-  if (!find_run<kThr>(a, sa, sums, where, cur)) return;
+  if (!find_run<kThr, TEAMS>(a, sa, sums, where, team, cur)) return;
 
-  if (warp == kStreamWarps) {
+  if (copies) {
     copy_run<kSlots>(a, sa, cur, smem_u32(smem), full, empty, pages, cur.at == 0 ? a.debug_skip : -1, lane);
     return;
   }
@@ -776,7 +794,7 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1), stream_ctas(NT)) kv4_
       const float scale = 0.125f * kLog2e * a.kscale;
       auto at = [&](int col) { return col < ncol ? cur.it.pfirst + (col >> a.lgG) : -1; };
       if constexpr (NT == 4) {  // a column tile a warp
-        static_assert(NT == kStreamWarps || NT != 4, "a column tile a warp");
+        static_assert(NT == kStreamWarps && TEAMS == 1, "a column tile a warp; one team at the barrier");
         uint32_t hi[8], lo[8];
         const float back = load_queries(base, a.q_stride, a.lgG, at(8 * warp + g), a.rope, scale, warp, lane, hi, lo);
         bar_sync(1, 32 * kStreamWarps);  // the last item's queries have been used
@@ -928,7 +946,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
 // The stream kernel's shape for a call; items = 0: the gather kernel takes it.
 struct StreamShape {
   StreamArgs s;
-  int nt, grid;
+  int nt, teams;
   int64_t slots;  // chunks the workspace has room for
   size_t bytes;   // the workspace
 };
@@ -954,7 +972,7 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
   z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
   z.s.W = p.W;
-  z.grid = kSMs * stream_ctas(z.nt);
+  z.teams = kSMs * (z.nt == 1 ? kStreamTeams<1> * kStreamCtas<1> : kStreamTeams<4> * kStreamCtas<4>);
   const int64_t units = (int64_t)z.s.items * a.Hkv;
   if (z.nt == kPromptColumns / 8) {  // cuts its work otherwise
     z.s.chunk_tiles = 1 << 18;
@@ -963,11 +981,11 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
     z.bytes = prompt_workspace(units);
     return z;
   }
-  // chunks: 512 keys (two tiles a warp), 256 where that would leave CTAs without
-  // one; more where the whole block table's worth of them would pass 16 a CTA
-  // (which bounds the workspace; the CTAs' shares differ by a chunk at most)
-  int64_t ck = (cap + 511) / 512 * units <= z.grid ? 256 : 512;
-  while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.grid) ck *= 2;
+  // chunks: 512 keys (two tiles a warp), 256 where that would leave teams without
+  // one; more where the whole block table's worth of them would pass 16 a team
+  // (which bounds the workspace; the teams' shares differ by a chunk at most)
+  int64_t ck = (cap + 511) / 512 * units <= z.teams ? 256 : 512;
+  while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.teams) ck *= 2;
   z.s.chunk_tiles = (int)(ck / kTile);
   z.s.lg_chunk = __builtin_ctz((unsigned)z.s.chunk_tiles);
   z.s.max_chunks = (int)((cap + ck - 1) / ck);
@@ -991,11 +1009,12 @@ static cudaError_t join(const Kv4Args& a, const StreamShape& z, cudaStream_t s) 
 
 template <typename TIO, int NT>
 static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
-  constexpr int NC = 8 * NT;
-  constexpr size_t smem = kSlots * (kTileBytes + 16 + 4) + 2 * kStreamWarps * NC * (66 * 4 + 8) + 32 + 64 + (NT == 4 ? 4 * NT * 512 + NC * 4 : 0);
-  static_assert(smem + 1024 <= 228 * 1024 / stream_ctas(NT), "CTAs an SM");
-  const cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  return e != cudaSuccess ? e : launch_pdl(kv4_stream_kernel<TIO, NT>, dim3((unsigned)z.grid), dim3(32 * (kStreamWarps + 1)), smem, s, a, z.s);
+  constexpr int smem = kStreamTeams<NT> * kTeamSmem<NT>;
+  static_assert((smem + 512 + 1024) * kStreamCtas<NT> <= 228 * 1024, "CTAs an SM");
+  const cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e != cudaSuccess ? e
+                          : launch_pdl(kv4_stream_kernel<TIO, NT>, dim3(kSMs * kStreamCtas<NT>), dim3(32 * (kStreamWarps + 1) * kStreamTeams<NT>), (size_t)smem,
+                                       s, a, z.s);
 }
 
 template <typename TIO>

@@ -84,7 +84,7 @@ __device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, i
   return it;
 }
 
-// A place in the CTA's run of chunks: chunk c of (item x, KV head h), its tiles
+// A place in a team's run of chunks: chunk c of (item x, KV head h), its tiles
 // tb .. te - 1, and the run's weight (tiles; 1 for a chunk of none) up to here.
 struct Cursor {
   Item it;
@@ -118,15 +118,15 @@ __device__ __forceinline__ int item_tiles(const StreamArgs& s, const Item& it) {
   return it.nch == 0 ? 0 : it.plast() < 0 ? 1 : it.plast() / kTile + 1 - max(0, it.pfirst - s.W) / kTile;
 }
 
-// This CTA's run of chunks: those that begin in its share of the tiles; false
-// if there are none.  All THREADS threads call it, with shared memory for
-// THREADS / 32 sums and the 4 numbers of `where`.
-template <int THREADS>
-__device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa, int* sums, int* where, Cursor& cur) {
+// A team's run of chunks: those that begin in its share of the tiles; false if
+// there are none.  All THREADS threads of the CTA's TEAMS teams call it, with
+// shared memory for THREADS / 32 sums and 4 numbers a team (`where`).
+template <int THREADS, int TEAMS>
+__device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa, int* sums, int* where, int team, Cursor& cur) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (sa.items + THREADS - 1) / THREADS;
   const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
-  if (tid == 0) where[0] = -1;
+  if (tid < TEAMS) where[4 * tid] = -1;
   int mine = 0;
   for (int x = x0; x < x1; ++x) mine += item_tiles(sa, item_at(a, sa, x)) * a.Hkv;
   int inc = mine;
@@ -143,11 +143,16 @@ __device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa,
     if (w < warp) before += sums[w];
     total += sums[w];
   }
-  // CTAs kSMs apart come to lie on one SM: neighbouring shares, whose roundings to whole chunks cancel
-  const int share = total / (int)gridDim.x, rest = total - share * (int)gridDim.x, perSM = gridDim.x / kSMs;
-  const int b = blockIdx.x % kSMs * perSM + blockIdx.x / kSMs;
-  const int first = share * b + min(b, rest), last = first + share + (b < rest);
-  if (first < last && first >= before && first < before + mine) {
+  // the teams of an SM (CTAs kSMs apart come to lie on one) have neighbouring shares, whose roundings to
+  // whole chunks cancel
+  const int share = total / (int)(gridDim.x * TEAMS), rest = total - share * (int)(gridDim.x * TEAMS);
+  const int b0 = (blockIdx.x % kSMs * (gridDim.x / kSMs) + blockIdx.x / kSMs) * TEAMS;
+  auto begin = [&](int b) { return share * b + min(b, rest); };
+#pragma unroll 1
+  for (int i = 0; i < TEAMS; ++i) {
+    const int first = begin(b0 + i);
+    if (first == begin(b0 + i + 1) || first < before || first >= before + mine) continue;
+    int* const w = where + 4 * i;
     int at = before;
     for (int x = x0; x < x1; ++x) {
       const Item it = item_at(a, sa, x);
@@ -157,22 +162,23 @@ __device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa,
         const int h = (first - at) / nt, in = first - at - h * nt;
         const int t0 = max(0, it.pfirst - sa.W) / kTile;
         const int c = in == 0 ? it.c0 : (in + t0 + sa.chunk_tiles - 1) >> sa.lg_chunk;
-        where[0] = x;
-        where[1] = h;
-        where[2] = c;
-        where[3] = at + h * nt + (c == it.c0 ? 0 : min(c * sa.chunk_tiles - t0, nt));
+        w[0] = x;
+        w[1] = h;
+        w[2] = c;
+        w[3] = at + h * nt + (c == it.c0 ? 0 : min(c * sa.chunk_tiles - t0, nt));
         break;
       }
       at += nt * a.Hkv;
     }
   }
   __syncthreads();
+  where += 4 * team;
   if (where[0] < 0) return false;
   cur.x = where[0];
   cur.h = where[1];
   cur.c = where[2];
   cur.at = where[3];
-  cur.end = last;
+  cur.end = begin(b0 + team + 1);
   if (cur.at >= cur.end) return false;
   cur.it = item_at(a, sa, cur.x);
   if (cur.c >= cur.it.c0 + cur.it.nch) {  // the share begins inside a head's last chunk: step to the next head
@@ -195,7 +201,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
-// The copying warp: every tile of the CTA's run, in order, into slot n mod
+// The copying warp: every tile of the team's run, in order, into slot n mod
 // SLOTS as soon as tile n - SLOTS has been read.
 template <int SLOTS, typename CURSOR>
 __device__ __forceinline__ void copy_run(const Kv4Args& a, const StreamArgs& sa, CURSOR cur, uint32_t ring, uint32_t full, uint32_t empty,
