@@ -878,69 +878,74 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kS
   if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
 }
 
-// The chunks of one (item, KV head) joined: `cols` columns a CTA, 8 lanes a
-// column, the chunks dealt out over the remaining threads (their partial sums
-// are read once, 264 bytes each: what counts is how many are in flight).
-// Bounded by latency: 8 to 9 us after either of the calls above.
+// (m, l, 8 sums) of some keys of a column; what other keys gave is added.
+struct Part {
+  float m = -INFINITY, l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  __device__ __forceinline__ void add(float m2, float l2, const float* z) {
+    const float top = fmaxf(m, m2);
+    const float f = m2 == -INFINITY ? 0.0f : ex2(m2 - top), back = m == -INFINITY ? 0.0f : ex2(m - top);
+    m = top;
+    l = fmaf(l, back, l2 * f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], back, z[e] * f);
+  }
+  // lanes `step`, 2 step, .. apart
+  __device__ __forceinline__ void add_lanes(int step) {
+    for (int o = step; o < 32; o <<= 1) {
+      float z[8];
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = __shfl_xor_sync(0xffffffffu, y[e], o);
+      add(m2, l2, z);
+    }
+  }
+};
+
+// The chunks of one (item, KV head) joined: `lanes` lanes a CTA, each 8 dims of a
+// column (8 or all 32 of four columns, or 2 of one, where columns are few), the
+// chunks dealt out over the groups of lanes (their partial sums are read once,
+// 264 bytes each: what counts is how many are in flight).  Bounded by latency:
+// 3 us after 2 in which the grid before it ends.
 constexpr int kJoinThreads = 512;
 
 template <typename TIO>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, const StreamArgs sa, int cols) {
-  __shared__ float red[kJoinThreads][9];
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, const StreamArgs sa, int lanes) {
+  __shared__ float red[kJoinThreads / 32][10][32];
   pdl_launch_dependents();
   pdl_wait();
   const int x = blockIdx.x / a.Hkv, h = blockIdx.x - x * a.Hkv;
   const Item it = item_at(a, sa, x);
   const int ncol = it.nrows << a.lgG, G = 1 << a.lgG, width = G << sa.lg_rows;
-  if (it.nch <= 1 || (int)blockIdx.y * cols >= ncol) return;
-  const int lanes = 8 * cols, groups = blockDim.x / lanes;
-  const int i = threadIdx.x % lanes, grp = threadIdx.x / lanes, d = i & 7;
-  const int col = min((int)blockIdx.y * cols + (i >> 3), ncol - 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int i = threadIdx.x & (lanes - 1), at8 = blockIdx.y * lanes + i, d = at8 & 7;  // the lane among all columns' lanes
+  if (it.nch <= 1 || blockIdx.y * lanes >= 8 * ncol) return;
+  const int col = min(at8 >> 3, ncol - 1);
   const int64_t at = ((int64_t)blockIdx.x * sa.max_chunks) * width + col;
-  // groups that share a warp are joined by shuffles, warps through shared memory
-  const int wide = min(lanes, 32), step = max(lanes, 32);
-  // (m, l, o) of the thread's chunks, one pass, the sums moved along with their maximum
-  float M = -INFINITY, l = 0.0f, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  Part p;
 #pragma unroll 4
-  for (int c = grp; c < it.nch; c += groups) {
+  for (int c = threadIdx.x / lanes; c < it.nch; c += blockDim.x / lanes) {
     const float2 v = sa.part_ml[at + (int64_t)c * width];
     float z[8];
     load8(sa.part_o + (at + (int64_t)c * width) * kD + 8 * d, z);
-    const float top = fmaxf(M, v.x);
-    const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top), back = M == -INFINITY ? 0.0f : ex2(M - top);
-    M = top;
-    l = fmaf(l, back, v.y * f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e], back, z[e] * f);
+    p.add(v.x, v.y, z);
   }
-  // all of them against the column's maximum
-  float top = M;
-  for (int o = wide; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  red[threadIdx.x][8] = top;
-  __syncthreads();
-  for (int k = threadIdx.x % step; k < (int)blockDim.x; k += step) top = fmaxf(top, red[k][8]);
-  __syncthreads();
-  const float f = M == -INFINITY ? 0.0f : ex2(M - top);
-  M = top;
-  l *= f;
+  p.add_lanes(lanes);
+  red[warp][8][lane] = p.m;
+  red[warp][9][lane] = p.l;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] *= f;
-  for (int o = wide; o < 32; o <<= 1) {
-    l += __shfl_xor_sync(0xffffffffu, l, o);
+  for (int e = 0; e < 8; ++e) red[warp][e][lane] = p.y[e];
+  __syncthreads();
+  if (warp > 0) return;
+  // 32 / lanes warps' sums at a time
+  Part q;
+  for (int w = lane / lanes; w < warps; w += 32 / lanes) {
+    float z[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += __shfl_xor_sync(0xffffffffu, y[e], o);
+    for (int e = 0; e < 8; ++e) z[e] = red[w][e][i];
+    q.add(red[w][8][i], red[w][9][i], z);
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = y[e];
-  red[threadIdx.x][8] = l;
-  __syncthreads();
-  if (threadIdx.x >= lanes || (int)blockIdx.y * cols + (i >> 3) >= ncol) return;
-  for (int k = step + i; k < (int)blockDim.x; k += step) {
-    l += red[k][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] += red[k][e];
-  }
-  write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M, l);
+  q.add_lanes(lanes);
+  if (lane < lanes && at8 < 8 * ncol) write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, q.y, q.m, q.l);
 }
 
 // The stream kernel's shape for a call; items = 0: the gather kernel takes it.
@@ -998,13 +1003,16 @@ template <typename TIO>
 static cudaError_t join(const Kv4Args& a, const StreamShape& z, cudaStream_t s) {
   if (z.slots == 0) return cudaSuccess;
   const int width = 1 << (a.lgG + z.s.lg_rows);
-  // enough columns to fill the card: four lanes' groups a column (a warp), four
-  // columns a CTA; else as many groups as a column may have chunks, up to 64
+  // enough columns to fill the card: up to four a CTA, eight groups (four beyond a wave of CTAs of eight);
+  // else a quarter column a CTA (400001 keys of 16 columns: 10.5 us with whole ones, 16 CTAs, and 8), and
+  // groups for two chunks each
   const int64_t columns = (int64_t)z.s.items * a.Hkv * width;
-  const int deep = columns >= 4 * kSMs ? 4 : std::max(4, std::min(64, 1 << (32 - __builtin_clz((unsigned)z.s.max_chunks - 1))));
-  const int cols = std::min(width, deep == 4 ? 4 : 1);
-  return launch_pdl(kv4_join_kernel<TIO>, dim3((unsigned)(z.s.items * a.Hkv), (unsigned)((width + cols - 1) / cols)), dim3(8 * deep * cols),
-                    0, s, a, z.s, cols);
+  const bool fills = columns >= 4 * kSMs;
+  const int lanes = fills ? std::min(32, 8 * width) : 2;
+  int groups = !fills ? 32 : 8 * columns / lanes > 4 * kSMs ? 4 : 8;
+  while (!fills && groups < kJoinThreads / 2 && 2 * groups < z.s.max_chunks) groups *= 2;
+  return launch_pdl(kv4_join_kernel<TIO>, dim3((unsigned)(z.s.items * a.Hkv), (unsigned)(8 * width / lanes)), dim3(lanes * groups), 0, s, a,
+                    z.s, lanes);
 }
 
 template <typename TIO, int NT>
