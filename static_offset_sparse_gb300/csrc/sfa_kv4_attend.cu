@@ -991,6 +991,10 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   // (which bounds the workspace; the teams' shares differ by a chunk at most)
   int64_t ck = (cap + 511) / 512 * units <= z.teams ? 256 : 512;
   while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.teams) ck *= 2;
+  // up to 2048 keys one chunk, without workspace and join (128 requests of 300 to 1900, 8 / 4 heads: 25.0 and
+  // 21.0 us, 80 of 8 / 2 heads 14.8 and 14.4); with 32 columns only if there is one for each team (100
+  // requests 27.6 and 30.1, 300 47.0 and 45.4)
+  if (cap <= 2048 && (z.nt < 4 || units >= z.teams)) ck = 2048;
   z.s.chunk_tiles = (int)(ck / kTile);
   z.s.lg_chunk = __builtin_ctz((unsigned)z.s.chunk_tiles);
   z.s.max_chunks = (int)((cap + ck - 1) / ck);
