@@ -749,7 +749,8 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kS
   constexpr bool kExact = sizeof(TIO) == 4;
   constexpr int NC = 8 * NT, TEAMS = kStreamTeams<NT>, kThr = 32 * (kStreamWarps + 1) * TEAMS;
   extern __shared__ __align__(128) uint8_t smem_all[];
-  __shared__ int sums[kThr / 32], where[4 * TEAMS];  // where: first item, head, chunk, weight of a team
+  __shared__ int sums[kThr / 32];
+  __shared__ RunStart where[TEAMS];
   const int tid = threadIdx.x, lane = tid & 31, cta_warp = tid >> 5, g = lane >> 2, t = lane & 3;
   // the teams' computing warps, then their copying ones
   const bool copies = cta_warp >= kStreamWarps * TEAMS;

@@ -47,6 +47,12 @@ constexpr uint32_t kColS = 0, kColP = 128, kColO = 192, kColTile = 256, kPCols =
 constexpr int kPTile = 128 * 128;
 constexpr int kPromptSmem = 8 * kPTile + kPSlots * kTileBytes + 1024;
 
+// Where a CTA's share begins: the unit, and how far into its weight.
+struct PieceStart {
+  Item it;
+  int x, h, in;
+};
+
 struct PromptShared {
   uint64_t raw_full[kPSlots], raw_empty[kPSlots];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by step parity
@@ -55,7 +61,8 @@ struct PromptShared {
   int step_pages[2];      // pages there of a step's two 64-key tiles: bits 0-3 and 4-7
   int step_nan[2][4];     // whether a warp's values of the step hold a NaN
   uint8_t nan[2][kStep];  // per key: the scale blocks of its value that are NaN
-  int sums[kPWarps], where[3];
+  int sums[kPWarps];
+  PieceStart where;
   uint32_t tmem;
 };
 
@@ -121,51 +128,40 @@ struct Shares {
   }
 };
 
-// This CTA's first piece; false if it has none.  Called by all threads.
-__device__ __forceinline__ bool find_piece(const Kv4Args& a, const StreamArgs& sa, int* sums, int* where, Shares& sh, Piece& cur) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// This CTA's first piece; false if it has none.  Called by all threads.  (One
+// loop run twice, as in find_run.)
+__device__ __forceinline__ bool find_piece(const Kv4Args& a, const StreamArgs& sa, int* sums, PieceStart* where, Shares& sh, Piece& cur) {
+  const int tid = threadIdx.x;
   const int per = (sa.items + kPThreads - 1) / kPThreads;
   const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
-  int mine = 0;
-  for (int x = x0; x < x1; ++x) mine += item_weight(sa, item_at(a, sa, x)) * a.Hkv;
-  int inc = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += y;
-  }
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  int before = inc - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kPWarps; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
-  }
-  sh.share = total / (int)gridDim.x;
-  sh.rest = total - sh.share * (int)gridDim.x;
-  const int first = sh.begin(blockIdx.x), last = sh.begin(blockIdx.x + 1);
-  if (first < last && first >= before && first < before + mine) {
+  int before = 0, first = 0, last = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
     int at = before;
+#pragma unroll 1
     for (int x = x0; x < x1; ++x) {
-      const int n = item_weight(sa, item_at(a, sa, x));
-      if (first < at + n * a.Hkv) {
-        where[0] = x;
-        where[1] = (first - at) / n;
-        where[2] = (first - at) % n;
-        break;
-      }
-      at += n * a.Hkv;
+      const Item it = item_at(a, sa, x);
+      const int n = item_weight(sa, it), end = at + n * a.Hkv;
+      if (pass > 0 && first < last && first >= at && first < end) *where = {it, x, (first - at) / n, (first - at) % n};
+      at = end;
+    }
+    if (pass == 0) {
+      int total;
+      cta_sums<kPThreads>(at, sums, before, total);
+      sh.share = total / (int)gridDim.x;
+      sh.rest = total - sh.share * (int)gridDim.x;
+      first = sh.begin(blockIdx.x);
+      last = sh.begin(blockIdx.x + 1);
     }
   }
   __syncthreads();
   if (first == last) return false;
-  cur.x = where[0];
-  cur.h = where[1];
-  cur.begin = first - where[2];
+  cur.it = where->it;
+  cur.x = where->x;
+  cur.h = where->h;
+  cur.begin = first - where->in;
   cur.end = last;
-  cur.it = item_at(a, sa, cur.x);
-  return cur.set(sa, where[2]) || cur.next(a, sa);
+  return cur.set(sa, where->in) || cur.next(a, sa);
 }
 
 // 64 codes and 4 scales -> a row of f16 at row r of a swizzled tile; zero: zeros.
@@ -322,7 +318,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
   Piece cur;
   Shares shares;
   tc05_fence_before();
-  const bool work = find_piece(a, sa, sh.sums, sh.where, shares, cur);  // (two barriers of the CTA inside)
+  const bool work = find_piece(a, sa, sh.sums, &sh.where, shares, cur);  // (two barriers of the CTA inside)
   tc05_fence_after();
   const uint32_t tm = sh.tmem;
   const int G = 1 << a.lgG;

@@ -118,17 +118,10 @@ __device__ __forceinline__ int item_tiles(const StreamArgs& s, const Item& it) {
   return it.nch == 0 ? 0 : it.plast() < 0 ? 1 : it.plast() / kTile + 1 - max(0, it.pfirst - s.W) / kTile;
 }
 
-// A team's run of chunks: those that begin in its share of the tiles; false if
-// there are none.  All THREADS threads of the CTA's TEAMS teams call it, with
-// shared memory for THREADS / 32 sums and 4 numbers a team (`where`).
-template <int THREADS, int TEAMS>
-__device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa, int* sums, int* where, int team, Cursor& cur) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (sa.items + THREADS - 1) / THREADS;
-  const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
-  if (tid < TEAMS) where[4 * tid] = -1;
-  int mine = 0;
-  for (int x = x0; x < x1; ++x) mine += item_tiles(sa, item_at(a, sa, x)) * a.Hkv;
+// Sums of the warps' `mine` before a thread's own and over the CTA; one barrier.
+template <int THREADS>
+__device__ __forceinline__ void cta_sums(int mine, int* sums, int& before, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -137,50 +130,72 @@ __device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa,
   }
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  int before = inc - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
-  }
+  static_assert(THREADS <= 1024, "a lane a warp");
+  const int v = lane < THREADS / 32 ? sums[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, v);
+  before = inc - mine + __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+}
+
+// Where a team's run begins: the first item, its head and chunk, the weight there.
+struct RunStart {
+  Item it;
+  int x, h, c, at;
+};
+
+// A team's run of chunks: those that begin in its share of the tiles; false if
+// there are none.  All THREADS threads of the CTA's TEAMS teams call it, with
+// shared memory for THREADS / 32 sums and a RunStart a team (`where`).  Its one
+// loop over the items runs twice, to count and to find: the code is cold when a
+// kernel starts, and a second copy of item_at cost 2300 clocks.
+template <int THREADS, int TEAMS>
+__device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa, int* sums, RunStart* where, int team, Cursor& cur) {
+  const int tid = threadIdx.x;
+  const int per = (sa.items + THREADS - 1) / THREADS;
+  const int x0 = min(sa.items, tid * per), x1 = min(sa.items, x0 + per);
+  if (tid < TEAMS) where[tid].x = -1;
   // the teams of an SM (CTAs kSMs apart come to lie on one) have neighbouring shares, whose roundings to
   // whole chunks cancel
-  const int share = total / (int)(gridDim.x * TEAMS), rest = total - share * (int)(gridDim.x * TEAMS);
-  const int b0 = (blockIdx.x % kSMs * (gridDim.x / kSMs) + blockIdx.x / kSMs) * TEAMS;
+  const int teams = gridDim.x * TEAMS, b0 = (blockIdx.x % kSMs * (gridDim.x / kSMs) + blockIdx.x / kSMs) * TEAMS;
+  int share = 0, rest = 0, before = 0;
   auto begin = [&](int b) { return share * b + min(b, rest); };
 #pragma unroll 1
-  for (int i = 0; i < TEAMS; ++i) {
-    const int first = begin(b0 + i);
-    if (first == begin(b0 + i + 1) || first < before || first >= before + mine) continue;
-    int* const w = where + 4 * i;
+  for (int pass = 0; pass < 2; ++pass) {
     int at = before;
+#pragma unroll 1
     for (int x = x0; x < x1; ++x) {
       const Item it = item_at(a, sa, x);
-      const int nt = item_tiles(sa, it);
-      if (first < at + nt * a.Hkv) {
-        // the first chunk that begins at `first` or later; its head's end is a chunk's beginning too
-        const int h = (first - at) / nt, in = first - at - h * nt;
-        const int t0 = max(0, it.pfirst - sa.W) / kTile;
-        const int c = in == 0 ? it.c0 : (in + t0 + sa.chunk_tiles - 1) >> sa.lg_chunk;
-        w[0] = x;
-        w[1] = h;
-        w[2] = c;
-        w[3] = at + h * nt + (c == it.c0 ? 0 : min(c * sa.chunk_tiles - t0, nt));
-        break;
+      const int nt = item_tiles(sa, it), end = at + nt * a.Hkv;
+      if (pass > 0 && end > begin(b0) && at < begin(b0 + TEAMS)) {
+#pragma unroll 1
+        for (int i = 0; i < TEAMS; ++i) {
+          const int first = begin(b0 + i);
+          if (first == begin(b0 + i + 1) || first < at || first >= end) continue;
+          // the first chunk that begins at `first` or later; its head's end is a chunk's beginning too
+          const int h = (first - at) / nt, in = first - at - h * nt;
+          const int t0 = max(0, it.pfirst - sa.W) / kTile;
+          const int c = in == 0 ? it.c0 : (in + t0 + sa.chunk_tiles - 1) >> sa.lg_chunk;
+          where[i] = {it, x, h, c, at + h * nt + (c == it.c0 ? 0 : min(c * sa.chunk_tiles - t0, nt))};
+        }
       }
-      at += nt * a.Hkv;
+      at = end;
+    }
+    if (pass == 0) {
+      int total;
+      cta_sums<THREADS>(at, sums, before, total);
+      share = total / teams;
+      rest = total - share * teams;
     }
   }
   __syncthreads();
-  where += 4 * team;
-  if (where[0] < 0) return false;
-  cur.x = where[0];
-  cur.h = where[1];
-  cur.c = where[2];
-  cur.at = where[3];
+  const RunStart& w = where[team];
+  if (w.x < 0) return false;
+  cur.it = w.it;
+  cur.x = w.x;
+  cur.h = w.h;
+  cur.c = w.c;
+  cur.at = w.at;
   cur.end = begin(b0 + team + 1);
   if (cur.at >= cur.end) return false;
-  cur.it = item_at(a, sa, cur.x);
   if (cur.c >= cur.it.c0 + cur.it.nch) {  // the share begins inside a head's last chunk: step to the next head
     cur.c = cur.it.c0 + cur.it.nch - 1;
     cur.te = cur.tb = 0;
