@@ -15,9 +15,13 @@
 // keys and values.  fp32 outputs add a second product with what rounding P to
 // f16 dropped (it takes the place of logits already read).  What bounds it is
 // the chain from a step's logits over its softmax (1300 clocks of exponentials,
-// scalings, sums and packings) to the next step's logits: about 3000 clocks a
-// step, of them 1536 of products.  8 prompts of 300 to 700 rows over 2048 to
-// 16384, 8 / 2 heads: 95 us with the join, 39% of the tensor cores' cycles.
+// scalings, sums and packings) to the next step's logits, about 3000 clocks a
+// step, of them 1536 of products, and next to it shared memory, which the logits'
+// products read at its full rate (8 KB in 64 clocks) for 1024 clocks and all else
+// uses for some 700.  (P in shared memory in odd steps, so that exponentials need
+// not wait for the last step's outputs, took 109 us where this takes 94.)  8
+// prompts of 300 to 700 rows over 2048 to 16384, 8 / 2 heads: 94 us with the
+// join, 39% of the tensor cores' cycles.
 //
 // The steps of all (item, KV head) units, in order, are shared out evenly over
 // one CTA an SM, to the step (and what a unit costs besides): units are long and
