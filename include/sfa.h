@@ -361,9 +361,9 @@ int sfa_kv4_read(const sfa_kv4_desc* d, const void* cache, const int32_t* slots,
  * seq_lens may hold anything.  o and lse overlap no input.  What is added in
  * which order depends on the shapes and the row's own request; from 33 query
  * columns (rows a request on average x G) on, a long prefix is also split by
- * what else is in the batch, so the last bits of a row may depend on it.  (N + R) * Hkv * max_pages
- * * page beyond 2^37 may be refused (SFA_ERR_UNSUPPORTED).  ws: sfa_kv4_workspace_size
- * bytes (NULL when that is 0), scratch of this call alone. */
+ * what else is in the batch, so the last bits of a row may depend on it.  (N + R) * Hkv beyond
+ * 2^24, or that times max_pages * page beyond 2^34, may be refused (SFA_ERR_UNSUPPORTED).
+ * ws: sfa_kv4_workspace_size bytes (NULL when that is 0), scratch of this call alone. */
 int sfa_kv4_workspace_size(const sfa_kv4_desc* d, size_t* bytes);
 int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
                    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* o,

@@ -1038,7 +1038,8 @@ static cudaError_t stream_and_join(const Kv4Args& a, const StreamShape& z, cudaS
 
 bool kv4_attend_fits(const Kv4Args& a, const Plan& p, bool ragged) {
   const StreamShape z = stream_shape(a, p, ragged);
-  return (int64_t)z.s.items * a.Hkv * (((int64_t)a.max_pages << a.lgS) / kTile + 4) < (1LL << 31);
+  const int64_t tiles = ((int64_t)a.max_pages << a.lgS) / kTile + 1;
+  return (int64_t)z.s.items * a.Hkv * (tiles + (z.s.max_chunks + 1LL) * kChunkCost) < (1LL << 31);
 }
 
 size_t kv4_attend_workspace(const Kv4Args& a, const Plan& p, bool ragged) {
