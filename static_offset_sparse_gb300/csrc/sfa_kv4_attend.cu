@@ -263,9 +263,10 @@ constexpr int kClusterCtas = 8;
 // 1000 keys, 8 / 2 heads 8.4 -> 6.4 us against the streaming kernel and its join,
 // 38 rows 11.3 -> 9.1, 4 requests of 6 to 9 rows 14.3 -> 9.2.  Up to 512 keys four
 // warps are no slower (7.0 and 6.4 us, 8.7 and 9.0); in two waves it loses
-// (64 rows: 12.5 and 15.5 us).
+// (64 rows: 12.5 and 15.5 us; four CTAs an SM, two with more than 8 heads a KV
+// head: 64 rows of 16 / 1 heads 14.1 and 20.2).
 static bool clustered(const Kv4Args& a, int64_t keys) {
-  return keys > 512 && (int64_t)a.N * a.Hkv * kClusterCtas <= 4 * kSMs;
+  return keys > 512 && (int64_t)a.N * a.Hkv * kClusterCtas <= (a.lgG > 3 ? 2 : 4) * kSMs;
 }
 
 struct GatherRows {
@@ -993,9 +994,9 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   int64_t ck = (cap + 511) / 512 * units <= z.teams ? 256 : 512;
   while (ck < cap && (cap + ck - 1) / ck * units > 16 * z.teams) ck *= 2;
   // up to 2048 keys one chunk, without workspace and join (128 requests of 300 to 1900, 8 / 4 heads: 25.0 and
-  // 21.0 us, 80 of 8 / 2 heads 14.8 and 14.4); with 32 columns only if there is one for each team (100
+  // 21.0 us, 80 of 8 / 2 heads 14.8 and 14.4); with more columns only if there is one for each team (32: 100
   // requests 27.6 and 30.1, 300 47.0 and 45.4)
-  if (cap <= 2048 && (z.nt < 4 || units >= z.teams)) ck = 2048;
+  if (cap <= 2048 && (z.nt == 1 || units >= z.teams)) ck = 2048;
   z.s.chunk_tiles = (int)(ck / kTile);
   z.s.lg_chunk = __builtin_ctz((unsigned)z.s.chunk_tiles);
   z.s.max_chunks = (int)((cap + ck - 1) / ck);

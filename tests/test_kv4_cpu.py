@@ -147,11 +147,11 @@ def test_workspace_holds_the_split_rows(sfa_lib, R, N, Hq, Hkv, page, max_pages)
     """Room for what the kernels leave there.  Prompts (64 columns and more a request on average): two
     parts for each of 152 CTAs, 256 columns of m, l and 64 sums.  Other rows: two parts at least of every
     row and head if any scratch is wanted, within a bound that the block table's width does not move, and
-    none for prefixes of one chunk (2048 keys; 256 for 32 columns and many rows of them)."""
+    none for prefixes of one chunk (2048 keys; 256 for more than 8 columns of a few requests)."""
     kw = dict(n_pages=1 << 14, R=R, N=N, Hq=Hq, Hkv=Hkv, page=page, max_pages=max_pages, q_stride=Hq * 64)
     n = _workspace(sfa_lib, **kw)
     prompts = 2 * 152 * 256 * 66 * 4
-    if page * max_pages <= 2048 and (8 * N * Hkv <= 608 or Hq // Hkv * -(-N // R) <= 16):
+    if page * max_pages <= 2048 and (8 * N * Hkv <= (608 if Hq // Hkv <= 8 else 304) or Hq // Hkv * -(-N // R) <= 8):
         assert n == 0
         return
     if Hq // Hkv * -(-N // R) >= 64:
