@@ -7,9 +7,10 @@ device.  Calls take the current stream of that device, only enqueue work, and
 may be captured into a CUDA graph.
 
 A decode step of a small batch takes the GPU a few microseconds, less than
-Python takes to look its arguments over.  So the checks are single expressions
-over cheap attributes, written out where they are made; what says what is wrong
-is run only when one of them fails.
+Python takes to look its arguments over.  So a call whose arguments are in order
+is made by csrc/kv4_py.cpp.  What that does not take (arguments to be refused,
+another device than the current one, a RoPE table by its theta, a workspace of
+the caller's), or all if it could not be built, is done here.
 """
 from __future__ import annotations
 
@@ -150,6 +151,18 @@ def _call(name, index, *args):
         check(rc, name)
 
 
+@functools.cache
+def _native():
+    """The native calls, or None where they could not be built."""
+    try:
+        from . import _kv4
+    except ImportError:
+        return None
+    L = _lib()
+    _kv4.bind(*(C.cast(L["sfa_kv4_" + name], C.c_void_p).value for name in ("plan", "append", "read", "workspace_size", "attend")))
+    return _kv4
+
+
 def kv4_cache(n_pages: int, Hkv: int, page: int = 64, device=None):
     """A pool of n_pages pages, every row zero."""
     n = C.c_size_t(0)
@@ -168,6 +181,13 @@ def kv4_plan(n_new, seq_lens, block_table, free_pages, n_free, *, page: int, row
     free pages after the step (seq_lens_out=seq_lens and n_free_out=n_free
     update those in place, as a captured step wants).  A step that does not fit
     changes nothing and sets the device status."""
+    fast = _native()
+    if fast is not None:
+        r = fast.plan(n_new, seq_lens, block_table, free_pages, n_free, page, rows, seq_lens_out, n_free_out)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            check(r, "sfa_kv4_plan")
     if not (block_table.dtype is _I32 and block_table.is_cuda and block_table.dim() == 2 and block_table.is_contiguous()):
         _refuse("block_table", block_table, _I32, (None, None))
     if rows < 0:
@@ -197,6 +217,11 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
     negative: skipped) and positions pos [N].  rope: a table of rope_table that
     covers the positions; else one of rope_theta for as many positions as the
     pool has rows is made once and kept, up to 2^20 (0: no rotation)."""
+    fast = _native()
+    if fast is not None and (rope is not None or not rope_theta):
+        r = fast.append(k, v, cache, slots, pos, rope, kscale, vscale)
+        if r is not None:
+            return check(r, "sfa_kv4_append") if r else None
     at, P, H, page = _pool(cache)
     N, _, ks = _rows(k, "k", H, at)
     n, _, vs = _rows(v, "v", H, at)
@@ -213,6 +238,13 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
 def kv4_read(cache, slots, *, dtype=None, kscale: float = 1.0, vscale: float = 1.0, k=None, v=None):
     """Rows of the cache as numbers (sfa_kv4_read): k, v [N, Hkv, 64], the
     rotated keys and the values stored at slots [N] (negative: zeros)."""
+    fast = _native()
+    if fast is not None and k is None and v is None and (dtype is None or dtype in CODES):
+        r = fast.read(cache, slots, kscale, vscale, dtype is not _F32)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            check(r, "sfa_kv4_read")
     at, P, H, page = _pool(cache)
     if dtype is None:
         dtype = k.dtype if k is not None else torch.bfloat16
@@ -266,6 +298,14 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
     dist: offsets as for decode_int (0 required), None for every earlier row.
     rope: as in kv4_append (without it, for the block table's width).  o and lse
     overlap none of the inputs.  Returns o [N, Hq, 64] and lse fp32 [N, Hq]."""
+    fast = _native()
+    if fast is not None and (rope is not None or not rope_theta):
+        r = fast.attend(q, cache, block_table, seq_lens, cu_q, None if dist is None else _offsets(tuple(dist)), rope, kscale, vscale,
+                        o, lse, ws)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            check(r, "sfa_kv4_attend")
     at, R, N, Hq, keep, d = _attend_desc(q, cache, block_table, dist, rope_theta, rope, kscale, vscale)
     if cu_q is None and N != R:
         raise ValueError(f"without cu_q, q has one row for each of the {R} requests, got {N}")

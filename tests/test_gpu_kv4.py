@@ -862,3 +862,75 @@ def test_attend_many_tokens_of_few_keys(sfa, Hq, Hkv):
     o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), dist=[0, 1, 2, 3, 8, 33], rope=_cuda(cs))
     assert sfa.get_device_status() == 0
     check_rows(o, lse, q, cache, table, lens, list(range(R + 1)), page, [0, 1, 2, 3, 8, 33], cs, 1.0, 1.0, False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_native_calls_and_ctypes_calls(sfa, dtype, monkeypatch):
+    """A step's four calls through the native binding and without it: the same bits, the same tensors handed
+    through, on the caller's stream, slices of wider rows, outputs given or made."""
+    import torch
+    from static_offset_sparse_gb300 import kv4
+
+    native = kv4._native()
+    assert native is not None
+    rng = np.random.default_rng(23)
+    page, R, P = 16, 3, 40
+    rope = sfa.rope_table(160)
+    wide = torch.from_numpy(rng.standard_normal((2, 61, 14, 64))).to(_dt(dtype)).cuda()
+    out = []
+    for use in (native, None):
+        calls = []
+        if use is not None:
+            class Counted:
+                def __getattr__(self, name):
+                    def call(*a):
+                        r = getattr(native, name)(*a)
+                        calls.append((name, r is not None))
+                        return r
+                    return call
+            monkeypatch.setattr(kv4, "_native", lambda: counted)
+            counted = Counted()
+        else:
+            monkeypatch.setattr(kv4, "_native", lambda: None)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = []
+        with torch.cuda.stream(side):
+            cache = sfa.kv4_cache(P, 2, page)
+            table, free = _i32(np.full((R, 10), -1)), _i32(np.arange(P))
+            lens, nf = _i32([0] * R), _i32([P])
+            for step, new in enumerate(([60, 0, 1], [2, 30, 17])):
+                qkv = wide[step]
+                given = dict(seq_lens_out=lens, n_free_out=nf) if step else {}
+                cu, slots, pos, l2, n2 = sfa.kv4_plan(_i32(new), lens, table, free, nf, page=page, rows=61, **given)
+                if step:
+                    assert l2 is lens and n2 is nf
+                lens, nf = l2, n2
+                sfa.kv4_append(qkv[:, 8:10], qkv[:, 11:13], cache, slots, pos, rope=rope, kscale=0.5)
+                k, v = sfa.kv4_read(cache, slots, dtype=_dt(dtype), kscale=0.5)
+                o, lse = torch.zeros((61, 8, 64), dtype=_dt(dtype), device="cuda"), torch.zeros((61, 8), device="cuda")
+                a = (qkv[:, :8], cache, table, lens)
+                r = sfa.kv4_attend(*a, cu_q=cu, rope=rope, kscale=0.5, o=o, lse=lse)
+                assert r[0] is o and r[1] is lse
+                o2, l2 = sfa.kv4_attend(*a, cu_q=cu, rope=rope, kscale=0.5, dist=[0, 1, 2, 5, 40])
+                last = (cu[1:].long() - 1).clamp(min=0)
+                o3, l3 = sfa.kv4_attend(qkv[last, :8], cache, table, lens, rope_theta=0)
+                n = sum(new)
+                got += [t.clone() for t in (cu, slots, pos, lens, nf, table, free[:int(nf)], cache, k, v, o[:n], lse[:n], o2[:n], l2[:n], o3, l3)]
+        side.synchronize()
+        out.append(got)
+        if use is not None:
+            assert len(calls) == 12 and all(took for _, took in calls), calls
+    for a, b in zip(*out):
+        assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a, b)
+    # what is not in order goes the long way, with its reasons
+    monkeypatch.setattr(kv4, "_native", lambda: native)
+    q = wide[0][:3, :8]
+    assert native.attend(q, cache, table, lens, None, None, None, 1, 1.0, None, None, None) is None
+    assert native.attend(q.cpu(), cache, table, lens, None, None, None, 1.0, 1.0, None, None, None) is None
+    assert native.attend(q, cache, table, lens[:2], None, None, None, 1.0, 1.0, None, None, None) is None
+    for bad in (dict(kscale=0.0), dict(vscale=float("nan")), dict(rope=rope[:, :16]), dict(lse=lse.double())):
+        with pytest.raises(ValueError):
+            sfa.kv4_attend(q, cache, table, lens, **{"rope": rope, **bad})
+    with pytest.raises((ValueError, RuntimeError)):
+        sfa.kv4_attend(q[:, :6], cache, table, lens, rope=rope)  # 3 heads a KV head
