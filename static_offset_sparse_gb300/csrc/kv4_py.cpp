@@ -83,7 +83,8 @@ bool rows(const Tensor* t, int64_t* stride) {
 bool rope_table(PyObject* o, int index, sfa_kv4_desc* d) {
   if (o == Py_None) return true;
   const Tensor* t = tensor(o, index);
-  if (!t || t->scalar_type() != at::kFloat || t->dim() != 3 || t->size(1) != 32 || t->size(2) != 2 || !t->is_contiguous() || !fits(t->size(0)))
+  if (!t || t->scalar_type() != at::kFloat || t->dim() != 3 || t->size(1) != 32 || t->size(2) != 2 || !t->is_contiguous() ||
+      !fits(t->size(0)))
     return false;
   d->rope = static_cast<const float*>(t->data_ptr());
   d->rope_T = (int32_t)t->size(0);
@@ -124,7 +125,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   uint8_t* const cache = q ? pool(a[1], index, &d) : nullptr;
   const Tensor* const table = cache ? tensor(a[2], index) : nullptr;
   if (!table || table->scalar_type() != at::kInt || table->dim() != 2 || !table->is_contiguous() || !fits(table->size(0)) ||
-      !fits(table->size(1)) || !rows(q, &d.q_stride) || !code(q->scalar_type(), &d.dtype) || !scales(a[7], a[8], &d) || !rope_table(a[6], index, &d))
+      !fits(table->size(1)) || !rows(q, &d.q_stride) || !code(q->scalar_type(), &d.dtype) || !scales(a[7], a[8], &d) ||
+      !rope_table(a[6], index, &d))
     SLOW;
   d.R = (int32_t)table->size(0);
   d.max_pages = (int32_t)table->size(1);
@@ -238,7 +240,8 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   int32_t *const cp = static_cast<int32_t*>(cu.data_ptr()), *const sp = static_cast<int32_t*>(slots.data_ptr());
   int32_t *const pp = static_cast<int32_t*>(pos.data_ptr()), *const tp = static_cast<int32_t*>(table->data_ptr());
-  const int rc = enqueue([&](void* s) { return plan_entry(&d, fresh, lens, tp, free_pages, n_free, cp, sp, pp, lens_out, left, s); }, index);
+  const int rc =
+      enqueue([&](void* s) { return plan_entry(&d, fresh, lens, tp, free_pages, n_free, cp, sp, pp, lens_out, left, s); }, index);
   if (rc) return PyLong_FromLong(rc);
   PyObject* const r = PyTuple_New(5);
   if (!r) return nullptr;

@@ -101,7 +101,9 @@ struct QShared {
   // (volatile: read where it is used, not kept in the registers that it is here to save)
   __device__ __forceinline__ uint4 b(int ks, int nt) const {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(frag + (ks * NT + nt) * 512));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(frag + (ks * NT + nt) * 512));
     return v;
   }
 };
@@ -588,9 +590,9 @@ static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
 // teams may have 168 a thread: 64 requests of 4 to 8 rows, 32 columns, 75 us and 71).
 //
 // Bounded by its instructions, next to the memory: 128 requests of 1024 to 32768
-// rows, 8 / 2 heads (167 MB) take 46 us, 3.6 TB/s (the tiles' instructions 28 us
+// rows, 8 / 2 heads (167 MB) take 44 us, 3.8 TB/s (the tiles' instructions 28 us
 // of it, the memory would take 25; the rest is the start, the chunks' ends and
-// an uneven end), one of 400001 rows, 16 / 2 heads (58 MB) 23.
+// an uneven end), one of 400001 rows, 16 / 2 heads (58 MB) 20.
 constexpr int kStreamWarps = 4, kSlots = 8;
 
 // Row r of a 16-key tile is key r ^ (r >> 2 & 1): the rows that lanes of one
@@ -802,7 +804,8 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kS
         bar_sync(1, 32 * kStreamWarps);  // the last item's queries have been used
         if (t == 0) qc[8 * warp + g] = back;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) qs[(ks * NT + warp) * 32 + lane] = make_uint4(hi[2 * ks], hi[2 * ks + 1], lo[2 * ks], lo[2 * ks + 1]);
+        for (int ks = 0; ks < 4; ++ks)
+          qs[(ks * NT + warp) * 32 + lane] = make_uint4(hi[2 * ks], hi[2 * ks + 1], lo[2 * ks], lo[2 * ks + 1]);
         bar_sync(1, 32 * kStreamWarps);
         q.frag = smem_u32(qs + lane);
 #pragma unroll
@@ -974,7 +977,7 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   z.nt = G * avg > 16 ? 4 : G * avg > 8 ? 2 : 1;
   z.nt = std::max(z.nt, G > 16 ? 4 : G > 8 ? 2 : 1);
   // more than 32 columns: the tensor memory kernel (nt = 32; 64 requests of up to 20000 rows, 8 / 2 heads,
-  // 12 rows each: 113 us, and 150 us in items of 32 columns; 6 rows each: 113 and 85)
+  // 12 rows each: 113 us, and 150 us in items of 32 columns; 6 rows each: 113 and 85; both a quarter less since)
   if (ragged && G * avg > 32) z.nt = kPromptColumns / 8;
   z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
   z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
@@ -1026,9 +1029,9 @@ static cudaError_t stream(const Kv4Args& a, const StreamShape& z, cudaStream_t s
   constexpr int smem = kStreamTeams<NT> * kTeamSmem<NT>;
   static_assert((smem + 512 + 1024) * kStreamCtas<NT> <= 228 * 1024, "CTAs an SM");
   const cudaError_t e = cudaFuncSetAttribute(kv4_stream_kernel<TIO, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return e != cudaSuccess ? e
-                          : launch_pdl(kv4_stream_kernel<TIO, NT>, dim3(kSMs * kStreamCtas<NT>), dim3(32 * (kStreamWarps + 1) * kStreamTeams<NT>), (size_t)smem,
-                                       s, a, z.s);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv4_stream_kernel<TIO, NT>, dim3(kSMs * kStreamCtas<NT>), dim3(32 * (kStreamWarps + 1) * kStreamTeams<NT>), (size_t)smem, s,
+                    a, z.s);
 }
 
 template <typename TIO>

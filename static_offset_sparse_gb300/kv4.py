@@ -231,7 +231,8 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
     if not (0.0 < kscale <= _MAX and 0.0 < vscale <= _MAX):
         _scales(kscale, vscale)
     rp, rT = _rope(rope, rope_theta, P * page, at)
-    _call("sfa_kv4_append", at, _desc(P, page, H, 64, 0, 0, N, 0, _code(dtype), 0, ks, vs, kscale, vscale, rp, rT, 0, 0), k.data_ptr(), v.data_ptr(),
+    _call("sfa_kv4_append", at, _desc(P, page, H, 64, 0, 0, N, 0, _code(dtype), 0, ks, vs, kscale, vscale, rp, rT, 0, 0),
+          k.data_ptr(), v.data_ptr(),
           cache.data_ptr(), _ints(at, N, slots, "slots"), _ints(at, N, pos, "pos"))
 
 
