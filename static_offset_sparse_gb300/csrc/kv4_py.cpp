@@ -2,7 +2,7 @@
 // outputs allocated and the entry point called without the interpreter, whose
 // share of a call is three times what the GPU takes for a small one (attention
 // of 32 rows of 23 keys: 17.5 us a call through ctypes, 5.7 so, 4.3 on the GPU;
-// a plan 22 and 7, a write and a read of 32 rows 20 and 7).  Only what is in
+// a plan 22 and 5.2, a write and a read of 32 rows 20 and 7).  Only what is in
 // order is done here.  Anything else (wrong types or shapes, another device than
 // the current one, a RoPE table by its theta) comes back as None, and kv4.py
 // says what is wrong or does it; an entry point's error comes back as its number.
@@ -101,6 +101,14 @@ bool scales(PyObject* k, PyObject* v, sfa_kv4_desc* d) {
 
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, int index) {
   return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)index), c10::nullopt);
+}
+
+// n int32 from `offset` on of a buffer that several outputs share.
+Tensor part(const Tensor& buffer, int64_t offset, int64_t n) {
+  auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
+  impl->set_sizes_contiguous({n});
+  impl->set_storage_offset(offset);
+  return Tensor(std::move(impl));
 }
 
 // The call itself, without the interpreter's lock: a full queue waits in there.
@@ -228,28 +236,22 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int32_t* const n_free = ints(a[4], index, 1);
   int32_t *lens_out = a[7] == Py_None ? nullptr : ints(a[7], index, d.R), *left = a[8] == Py_None ? nullptr : ints(a[8], index, 1);
   if (!fresh || !lens || !free_pages || !n_free || (a[7] != Py_None && !lens_out) || (a[8] != Py_None && !left)) SLOW;
-  const Tensor cu = empty({d.R + 1LL}, at::kInt, index), slots = empty({N}, at::kInt, index), pos = empty({N}, at::kInt, index);
-  Tensor own_lens, own_left;
-  if (!lens_out) {
-    own_lens = empty({d.R}, at::kInt, index);
-    lens_out = static_cast<int32_t*>(own_lens.data_ptr());
-  }
-  if (!left) {
-    own_left = empty({1}, at::kInt, index);
-    left = static_cast<int32_t*>(own_left.data_ptr());
-  }
-  int32_t *const cp = static_cast<int32_t*>(cu.data_ptr()), *const sp = static_cast<int32_t*>(slots.data_ptr());
-  int32_t *const pp = static_cast<int32_t*>(pos.data_ptr()), *const tp = static_cast<int32_t*>(table->data_ptr());
+  const int64_t R = d.R;
+  const Tensor own = empty({2 * R + 2 + 2 * N}, at::kInt, index);  // boundaries, slots, positions, lengths, pages left
+  int32_t *const cp = static_cast<int32_t*>(own.data_ptr()), *const sp = cp + R + 1, *const pp = sp + N;
+  int32_t* const tp = static_cast<int32_t*>(table->data_ptr());
+  if (!lens_out) lens_out = pp + N;
+  if (!left) left = pp + N + R;
   const int rc =
       enqueue([&](void* s) { return plan_entry(&d, fresh, lens, tp, free_pages, n_free, cp, sp, pp, lens_out, left, s); }, index);
   if (rc) return PyLong_FromLong(rc);
   PyObject* const r = PyTuple_New(5);
   if (!r) return nullptr;
-  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(cu));
-  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(slots));
-  PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(pos));
-  PyTuple_SET_ITEM(r, 3, a[7] == Py_None ? THPVariable_Wrap(own_lens) : Py_NewRef(a[7]));
-  PyTuple_SET_ITEM(r, 4, a[8] == Py_None ? THPVariable_Wrap(own_left) : Py_NewRef(a[8]));
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(part(own, 0, R + 1)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(part(own, R + 1, N)));
+  PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(part(own, R + 1 + N, N)));
+  PyTuple_SET_ITEM(r, 3, a[7] == Py_None ? THPVariable_Wrap(part(own, R + 1 + 2 * N, R)) : Py_NewRef(a[7]));
+  PyTuple_SET_ITEM(r, 4, a[8] == Py_None ? THPVariable_Wrap(part(own, 2 * R + 1 + 2 * N, 1)) : Py_NewRef(a[8]));
   return r;
   END_HANDLE_TH_ERRORS
 }
