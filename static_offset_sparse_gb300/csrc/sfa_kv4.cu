@@ -172,19 +172,45 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
   }
 }
 
-// The row maps of a large step, one thread a row.
+// The row maps of a large step, a warp 32 rows: the first one's request by a
+// search of 32 boundaries at a time, the others' among the 32 after it, and the
+// next, held by the lanes.
 __global__ void __launch_bounds__(256) kv4_plan_rows_kernel(const PlanArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= a.N) return;
-  const int i = (int)at;
-  if (i >= a.cu[a.R]) {
-    a.slots[i] = a.pos[i] = -1;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, i0 = i - lane;
+  if (i0 >= a.N) return;
+  const int last = a.cu[a.R];
+  if (i0 >= last) {
+    if (i < a.N) a.slots[i] = a.pos[i] = -1;
     return;
   }
-  const int r = upper(a.cu + 1, a.R, i);
-  put_row(a, i, a.lens_out[r] - (a.cu[r + 1] - i), a.table + (int64_t)r * a.max_pages);
+  // the first request whose end lies beyond i0
+  int lo = 0, len = a.R;
+  while (len > 1) {
+    const int step = (len + 31) >> 5, at = lane * step;
+    const bool le = at < len && a.cu[lo + at] <= i0;
+    const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;  // cu does not decrease: the first k + 1 of them
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  int r = -1, end = 0;
+  for (; __any_sync(0xffffffffu, r < 0 && i < last); lo += 32) {
+    const int mine = lo + lane < a.R ? a.cu[lo + lane + 1] : 0x7fffffff;
+    int k = 0;  // ends among the 32 that are not beyond i
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) k += __shfl_sync(0xffffffffu, mine, k + s - 1) <= i ? s : 0;
+    const int e = __shfl_sync(0xffffffffu, mine, k);
+    if (r < 0 && i < last && e > i) {
+      r = lo + k;
+      end = e;
+    }
+  }
+  if (r >= 0)
+    put_row(a, (int)i, a.lens_out[r] - (end - (int)i), a.table + (int64_t)r * a.max_pages);
+  else if (i < a.N)
+    a.slots[i] = a.pos[i] = -1;
 }
 
 // ---------------------------------------------------------------- append
