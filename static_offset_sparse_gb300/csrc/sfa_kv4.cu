@@ -17,7 +17,7 @@ namespace sfa {
 // and bounded by latency, so one CTA does all of it between barriers (no
 // atomics: the same inputs give the same pages); the row maps of more than
 // kPlanRows rows are left to a second kernel over the whole card (47458 rows:
-// 9.6 us, and 15 in the one CTA; 256 requests of a row each: 5.0 us).
+// 8.7 us, and 15 in the one CTA; 256 requests of a row each: 5.0 us).
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 4 * kPlanThreads;
 
