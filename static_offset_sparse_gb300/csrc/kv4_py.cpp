@@ -4,7 +4,7 @@
 // of 32 rows of 23 keys: 17.5 us a call through ctypes, 5.7 so, 4.3 on the GPU;
 // a plan 22 and 5.2, a write and a read of 32 rows 20 and 7).  Only what is in
 // order is done here.  Anything else (wrong types or shapes, another device than
-// the current one, a RoPE table by its theta) comes back as None, and kv4.py
+// the current one, a workspace of the caller's) comes back as None, and kv4.py
 // says what is wrong or does it; an entry point's error comes back as its number.
 #include <Python.h>
 

@@ -9,7 +9,7 @@ may be captured into a CUDA graph.
 A decode step of a small batch takes the GPU a few microseconds, less than
 Python takes to look its arguments over.  So a call whose arguments are in order
 is made by csrc/kv4_py.cpp.  What that does not take (arguments to be refused,
-another device than the current one, a RoPE table by its theta, a workspace of
+another device than the current one, a RoPE table yet to be made, a workspace of
 the caller's), or all if it could not be built, is done here.
 """
 from __future__ import annotations
@@ -125,6 +125,12 @@ def _rope(rope, rope_theta, T, index):
     return rope.data_ptr(), n
 
 
+def _made_rope(rope_theta, cache, t, axis):
+    """The RoPE table that an earlier call made for as many pages as t has along axis, if one did."""
+    page = PAGES.get(cache.shape[-1]) if cache.dim() and t.dim() else None
+    return page and _ROPE_CACHE.get((t.shape[axis] * page, float(rope_theta), cache.get_device()))
+
+
 @functools.lru_cache(maxsize=64)
 def _offsets(dist: tuple):
     arr, n = i32_array(dist)
@@ -218,8 +224,9 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
     covers the positions; else one of rope_theta for as many positions as the
     pool has rows is made once and kept, up to 2^20 (0: no rotation)."""
     fast = _native()
-    if fast is not None and (rope is not None or not rope_theta):
-        r = fast.append(k, v, cache, slots, pos, rope, kscale, vscale)
+    made = rope if rope is not None or not rope_theta else _made_rope(rope_theta, cache, cache, 0)
+    if fast is not None and (made is not None or not rope_theta):
+        r = fast.append(k, v, cache, slots, pos, made, kscale, vscale)
         if r is not None:
             return check(r, "sfa_kv4_append") if r else None
     at, P, H, page = _pool(cache)
@@ -300,8 +307,9 @@ def kv4_attend(q, cache, block_table, seq_lens, *, cu_q=None, dist=None, rope_th
     rope: as in kv4_append (without it, for the block table's width).  o and lse
     overlap none of the inputs.  Returns o [N, Hq, 64] and lse fp32 [N, Hq]."""
     fast = _native()
-    if fast is not None and (rope is not None or not rope_theta):
-        r = fast.attend(q, cache, block_table, seq_lens, cu_q, None if dist is None else _offsets(tuple(dist)), rope, kscale, vscale,
+    made = rope if rope is not None or not rope_theta else _made_rope(rope_theta, cache, block_table, -1)
+    if fast is not None and (made is not None or not rope_theta):
+        r = fast.attend(q, cache, block_table, seq_lens, cu_q, None if dist is None else _offsets(tuple(dist)), made, kscale, vscale,
                         o, lse, ws)
         if type(r) is tuple:
             return r

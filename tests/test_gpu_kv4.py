@@ -915,6 +915,14 @@ def test_native_calls_and_ctypes_calls(sfa, dtype, monkeypatch):
                 o2, l2 = sfa.kv4_attend(*a, cu_q=cu, rope=rope, kscale=0.5, dist=[0, 1, 2, 5, 40])
                 last = (cu[1:].long() - 1).clamp(min=0)
                 o3, l3 = sfa.kv4_attend(qkv[last, :8], cache, table, lens, rope_theta=0)
+                if step and use is not None:  # a table by its theta: made by the first call, found by the second
+                    a3, before = (qkv[last, :8], cache, table, lens), len(calls)
+                    theta = 777.0 if dtype == "f32" else 555.0
+                    sfa.kv4_attend(*a3, rope_theta=theta)
+                    o4, l4 = sfa.kv4_attend(*a3, rope_theta=theta)
+                    o5, l5 = sfa.kv4_attend(*a3, rope=sfa.rope_table(160, theta))
+                    assert calls[before:] == [("attend", True)] * 2 and torch.equal(o4, o5) and torch.equal(l4, l5)
+                    del calls[before:]
                 n = sum(new)
                 got += [t.clone() for t in (cu, slots, pos, lens, nf, table, free[:int(nf)], cache, k, v, o[:n], lse[:n], o2[:n], l2[:n], o3, l3)]
         side.synchronize()
