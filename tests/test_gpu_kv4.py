@@ -349,6 +349,71 @@ def test_attend_block_tables(sfa, dtype, Hq, Hkv, new, dist):
         check_rows(o, lse, q, cache, table, lens, cu, page, dist, cs, 1.0, 1.3, dtype == "bf16")
 
 
+@pytest.mark.parametrize("width", [60, 500])
+@pytest.mark.parametrize("dist", [None, list(range(600)) + [640]])
+def test_attend_few_rows_padded_nan_bad_pages(sfa, width, dist):
+    """A few rows over more keys than a step sees: rows behind the last request stay as they were, NaN reaches
+    its own rows only, pages outside the pool are reported and left out."""
+    import torch
+
+    rng = np.random.default_rng(24)
+    lens, new, page = [900, 20, 7], [10, 0, 7], 16
+    cache, table = make_cache(rng, lens, page, 2, garbage=False)
+    t = np.full((3, width), -1, np.int32)
+    t[:, :table.shape[1]] = table
+    cu = _i32([0, 10, 10, 17])
+    q = torch.from_numpy(rng.standard_normal((24, 8, 64))).float().cuda()
+    o, lse = torch.full((24, 8, 64), 7.0, device="cuda"), torch.full((24, 8), 7.0, device="cuda")
+    sfa.kv4_attend(q, _cuda(cache), _cuda(t), _i32(lens), cu_q=cu, dist=dist, rope_theta=0, o=o, lse=lse)
+    assert sfa.get_device_status() == 0
+    check_rows(o[:17], lse[:17], q[:17], cache, table, lens, [0, 10, 10, 17], page, dist, None, 1.0, 1.0, False)
+    assert (o[17:] == 7).all() and (lse[17:] == 7).all()
+    # a NaN in a value of the first request's key 895 (KV head 1, dims 16 .. 31): rows at 895 and later
+    bad = cache.copy()
+    bad[table[0, 895 // page], 1, 64 * page + 8 * (895 % page) + 4 + 1] = 127
+    q2 = q.clone()
+    q2[12, 3, 0] = float("nan")  # and in a query
+    o2, l2 = sfa.kv4_attend(q2, _cuda(bad), _cuda(t), _i32(lens), cu_q=cu, dist=dist, rope_theta=0)
+    want = torch.zeros((17, 8, 64), dtype=torch.bool)
+    want[5:10, 4:, 16:32] = True
+    want[12, 3] = True
+    assert torch.equal(o2[:17].isnan().cpu(), want) and torch.equal(o2[:17][~want.cuda()], o[:17][~want.cuda()])
+    # the first request's page of rows 320 .. 335 is nowhere: its rows without those keys
+    t2 = t.copy()
+    t2[0, 20] = cache.shape[0]
+    o3, l3 = sfa.kv4_attend(q, _cuda(cache), _cuda(t2), _i32(lens), cu_q=cu, dist=dist, rope_theta=0)
+    assert sfa.get_device_status() == 6 and torch.equal(o3[10:17], o[10:17]) and torch.equal(l3[10:17], lse[10:17])
+    k, v = stored(cache, table, 0, 900, page)
+    for row in (0, 9):
+        p = 890 + row
+        j = np.array([x for x in (range(p + 1) if dist is None else p - np.array(dist)) if x >= 0 and x // page != 20])
+        wo, wl, av, sz = ref.attend(q[row:row + 1].double().cpu().numpy(), k, v, np.array([p]), sorted((p - j).tolist()), 1.0, 1.0, None)
+        bo, bl = ref.bounds(wo, wl, av, sz, False)
+        assert (np.abs(o3[row:row + 1].double().cpu().numpy() - wo) <= bo).all()
+        assert (np.abs(l3[row:row + 1].double().cpu().numpy() - wl) <= bl).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,dtype", [(8, 2, "f32"), (16, 1, "bf16"), (32, 1, "bf16")])
+def test_attend_rows_do_not_depend_on_their_batch(sfa, Hq, Hkv, dtype):
+    """One row a request: its bits are its own, whatever the other requests' lengths, block table of some
+    chunks."""
+    import torch
+
+    rng = np.random.default_rng(25)
+    lens, page = [5000, 6900, 2100, 300], 64
+    cache, table = make_cache(rng, lens, page, Hkv)
+    q = torch.from_numpy(rng.standard_normal((4, Hq, 64))).to(_dt(dtype)).cuda()
+    args = (_cuda(cache), _cuda(table))
+    rope = _cuda(ref.rope(table.shape[1] * page))
+    o, lse = sfa.kv4_attend(q, *args, _i32(lens), rope=rope)
+    for other in ([5000, 1, 0, 0], [5000, 6900, 2099, 299], [5000, 64, 2100, 17]):
+        o2, l2 = sfa.kv4_attend(q, *args, _i32(other), rope=rope)
+        for r in range(4):
+            if other[r] == lens[r]:
+                assert torch.equal(o[r], o2[r]) and torch.equal(lse[r], l2[r])
+    assert sfa.get_device_status() == 0
+
+
 def test_attend_sizes_of_queries(sfa):
     """Queries from the smallest to the largest: scaled by powers of two the result of a scaled
     kscale, bit for bit; zero queries average the values."""
