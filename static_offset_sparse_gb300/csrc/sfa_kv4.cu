@@ -310,8 +310,9 @@ __device__ __forceinline__ void load16(const TIO* p, float* x) {
   load8(p + 8, x + 8);
 }
 
-// Four threads a (row, head): two on the keys, each with 16 rotation pairs
-// (dims 16u.. and 32 + 16u..: two whole scale blocks), two on the values.
+// Four threads a (row, head): two on the key, each with 16 rotation pairs (dims
+// 16u.. and 32 + 16u..: two whole scale blocks), two on the value, in another
+// warp, which has no rotation to go through.
 // 2 * 64 elements in, 72 bytes out, but bounded by instructions and the loads'
 // latency: 32741 rows of 2 heads in bf16 (22 MB, and 8 of the RoPE table) take
 // 7.9 us, 13.8 with cold caches (8.2 with one number divided at a time).
@@ -319,21 +320,20 @@ template <typename TIO>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x, unit = i >> 2;  // (N * Hkv <= 2^27)
-  const int part = (int)(i & 3), u = part & 1;
-  const bool value = part >= 2;
+  const uint32_t unit = blockIdx.x * 64u + (threadIdx.x >> 6) * 16u + ((threadIdx.x & 31) >> 1);  // (N * Hkv <= 2^27)
+  const int u = threadIdx.x & 1;
+  const bool value = threadIdx.x & 32;
   const int n = (int)(unit / (uint32_t)a.Hkv), h = (int)unit - n * a.Hkv;
   int slot = -1, p = 0;
   if (n < a.N) {
     slot = a.slots[n];
     p = a.pos[n];
-    if (slot >= 0 && ((slot >> a.lgS) >= a.n_pages || (!value && a.rope && (p < 0 || p >= a.rope_T)))) {
+    // (a row is written whole or not at all)
+    if (slot >= 0 && ((slot >> a.lgS) >= a.n_pages || (a.rope && (p < 0 || p >= a.rope_T)))) {
       record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
       slot = -1;
     }
   }
-  // a row is written whole or not at all: the keys' threads know whether
-  slot = __shfl_sync(0xffffffffu, slot, (threadIdx.x & 31) & ~3);
   uint32_t s0 = 0, s1 = 0;
   uint8_t* block = nullptr;
   const int S = 1 << a.lgS, at = slot & (S - 1);
@@ -363,11 +363,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
     *reinterpret_cast<uint2*>(codes + 8 * u) = c0;
     *reinterpret_cast<uint2*>(codes + 16 + 8 * u) = c1;
   }
-  // the row's 8 scales leave in one store
+  // the four scales leave in one store
   uint32_t w = (s0 << (8 * u)) | (s1 << (16 + 8 * u));
   w |= __shfl_xor_sync(0xffffffffu, w, 1);
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 2);
-  if (block && part == 0) *reinterpret_cast<uint2*>(block + 64 * S + 8 * at) = make_uint2(w, other);
+  if (block && u == 0) *reinterpret_cast<uint32_t*>(block + 64 * S + 8 * at + (value ? 4 : 0)) = w;
 }
 
 // ---------------------------------------------------------------- read
