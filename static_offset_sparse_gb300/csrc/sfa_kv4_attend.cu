@@ -241,7 +241,7 @@ struct Acc {
 // group's partial results meet in shared memory.  Bounded by latency (row map,
 // block table, cache row: three dependent loads) at decode sizes (32 rows of 23
 // keys, 8 / 2 heads: 4.3 us) and by its instructions at prompt sizes (7807 rows
-// of 19 keys, 8 / 2 heads: 25 us, 1040 warp instructions a row pair and head at
+// of 19 keys, 8 / 2 heads: 25 us, 2070 warp instructions a row pair and KV head at
 // 2 a clock; the query's rotation and split are 250 of them).  The offsets
 // beyond the window are taken to shared memory once a CTA, which walks over
 // units: read where they come in, by as many addresses as lanes, they were
