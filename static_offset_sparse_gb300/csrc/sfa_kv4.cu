@@ -17,9 +17,10 @@ namespace sfa {
 // and bounded by latency, so one CTA does all of it between barriers (no
 // atomics: the same inputs give the same pages); the row maps of more than
 // kPlanRows rows are left to a second kernel over the whole card (47458 rows:
-// 8.7 us, and 15 in the one CTA; 256 requests of a row each: 5.0 us).
+// 8.7 us, and 15 in the one CTA; 4096 rows 5.1 and 5.9; 2048 in the one CTA 4.5;
+// 256 requests of a row each, with pages to move, 5.0).
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanRows = 4 * kPlanThreads;
+constexpr int kPlanRows = 2 * kPlanThreads;
 
 struct PlanArgs {
   const int32_t* n_new;
@@ -59,6 +60,10 @@ __device__ __forceinline__ void put_row(const PlanArgs& a, int row, int p, const
   a.pos[row] = p;
 }
 
+// MANY: more than a request a thread, whose numbers go through shared memory, so
+// that neighbouring threads read neighbouring requests (8192 requests 24 us, and
+// 17 so; with one a thread the detour costs 0.2 of 5).
+template <bool MANY>
 __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a, int rows_here) {
   extern __shared__ int sm[];
   int* const back = sm;            // inclusive prefix of released pages
@@ -78,7 +83,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
   const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
   const int nf = *a.n_free;
   long long s[3] = {0, 0, 0};
-  for (int r = r0; r < r1; ++r) {
+  for (int r = MANY ? tid : r0; r < (MANY ? a.R : r1); r += MANY ? kPlanThreads : 1) {
     const int nn = a.n_new[r], len = a.lens[r];
     if (nn < -1 || len < 0 || len > cap || len + (long long)max(nn, 0) > cap) bad = 1;
     const int held = (len + S1) >> a.lgS;
@@ -86,13 +91,23 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
     const int keep = nn < 0 ? 0 : len;
     const int add = max(nn, 0);
     const int nd = (int)(((long long)keep + add + S1) >> a.lgS) - (held - b);
-    s[0] += b;
-    s[1] += nd;
-    s[2] += add;
+    if (!MANY) {
+      s[0] += b;
+      s[1] += nd;
+      s[2] += add;
+    }
     kept[r] = keep;
     back[r] = b;
     need[r] = nd;
     rows[r] = add;
+  }
+  if (MANY) {
+    __syncthreads();
+    for (int r = r0; r < r1; ++r) {
+      s[0] += back[r];
+      s[1] += need[r];
+      s[2] += rows[r];
+    }
   }
   long long mine[3] = {s[0], s[1], s[2]};
 #pragma unroll
@@ -139,14 +154,21 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
     back[r] = (int)ex[0];
     need[r] = (int)ex[1];
     rows[r] = (int)ex[2];
-    a.cu[r + 1] = (int)ex[2];
-    a.lens_out[r] = kept[r] + add;
+    if (!MANY) {
+      a.cu[r + 1] = (int)ex[2];
+      a.lens_out[r] = kept[r] + add;
+    }
   }
   if (tid == 0) {
     a.cu[0] = 0;
     *a.n_free_out = left;
   }
   __syncthreads();
+  if (MANY)
+    for (int r = tid; r < a.R; r += kPlanThreads) {
+      a.cu[r + 1] = rows[r];
+      a.lens_out[r] = kept[r] + rows[r] - (r ? rows[r - 1] : 0);
+    }
   // the page at place x of the stack: the old free pages, then the released ones
   auto stacked = [&](int x) {
     if (x < nf) return a.free_pages[x];
@@ -546,12 +568,13 @@ int sfa_kv4_plan(const sfa_kv4_desc* d, const int32_t* n_new, const int32_t* seq
                 d->R, d->N, d->max_pages, d->n_pages, __builtin_ctz((unsigned)d->page), nullptr};
   if ((rc = device_status(&a.status)) != SFA_OK) return rc;
   const size_t smem = (size_t)d->R * 16;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024) != cudaSuccess)
+  auto kern = d->R > kPlanThreads ? kv4_plan_kernel<true> : kv4_plan_kernel<false>;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024) != cudaSuccess)
     return SFA_ERR_CUDA;
   const int here = d->N <= kPlanRows;
   LaunchTimer tm(SFA_KERNEL_KV4_PLAN, stream);
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = launch_pdl(kv4_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, a, here);
+  cudaError_t e = launch_pdl(kern, dim3(1), dim3(kPlanThreads), smem, s, a, here);
   if (e == cudaSuccess && !here) e = launch_pdl(kv4_plan_rows_kernel, dim3((unsigned)(((int64_t)d->N + 255) / 256)), dim3(256), 0, s, a);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }

@@ -60,7 +60,8 @@ def _pool(rng, lens, page, spare, width):
 
 
 @pytest.mark.parametrize("R,page,rows,most", [(1, 16, 1, 1), (3, 32, 40, 20), (257, 64, 300, 1), (1000, 16, 4096, 9),
-                                              (1025, 128, 4097, 4), (2500, 16, 9000, 6), (5000, 64, 5000, 1)])
+                                              (1025, 128, 4097, 4), (2500, 16, 9000, 6), (5000, 64, 5000, 1),
+                                              (400, 16, 2048, 9), (400, 16, 2049, 9), (8192, 32, 8192, 1)])
 def test_plan_steps(sfa, R, page, rows, most):
     """Several steps in a row: some requests grow, some idle, some end and start again."""
     import torch
