@@ -7,6 +7,7 @@ are not given, take the current torch stream, and call the library.
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 from ._lib import (SFA_BF16, SFA_F32, Desc, MAX_RUNGS, _lib, check, i32_array)
 
@@ -125,7 +126,8 @@ def status_string(code: int) -> str:
 
 # ------------------------------------------------------------ device calls
 
-_ROPE_CACHE: dict = {}
+_ROPE_CACHE: dict = {}  # (positions, theta, device index) -> table; complete ones only
+_ROPE_LOCK = threading.Lock()
 
 
 def _torch():
@@ -139,19 +141,35 @@ def _stream():
 
 
 def rope_table(T: int, theta: float = 1e4, device=None):
-    """fp32 [T, 32, 2] (cos, sin) table written by sfa_rope_table (cached)."""
+    """fp32 [T, 32, 2] (cos, sin) table written by sfa_rope_table.
+
+    The first call of a length waits for the table before it is kept: any stream
+    and thread that finds it afterwards may read it without waiting for another.
+    Inside a graph capture, where nothing can be waited for, a table that is not
+    there yet belongs to the capture, which fills it at each replay."""
     torch = _torch()
     dev = torch.device(device if device is not None else "cuda")
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     key = (int(T), float(theta), dev.index)
     tab = _ROPE_CACHE.get(key)
-    if tab is None:
-        tab = torch.empty((T, 32, 2), dtype=torch.float32, device=dev)
-        with torch.cuda.device(dev):
-            check(_lib().sfa_rope_table(T, float(theta), C.c_void_p(tab.data_ptr()), _stream()),
-                  "sfa_rope_table")
-        _ROPE_CACHE[key] = tab
+    if tab is not None:
+        return tab
+    with torch.cuda.device(dev):
+        if torch.cuda.is_current_stream_capturing():
+            return _new_rope_table(T, theta, dev)
+        with _ROPE_LOCK:
+            if key not in _ROPE_CACHE:
+                tab = _new_rope_table(T, theta, dev)
+                torch.cuda.current_stream().synchronize()
+                _ROPE_CACHE[key] = tab
+            return _ROPE_CACHE[key]
+
+
+def _new_rope_table(T, theta, dev):
+    """A table of the current stream's, which is dev's."""
+    tab = _torch().empty((T, 32, 2), dtype=_torch().float32, device=dev)
+    check(_lib().sfa_rope_table(T, float(theta), C.c_void_p(tab.data_ptr()), _stream()), "sfa_rope_table")
     return tab
 
 

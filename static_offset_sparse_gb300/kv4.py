@@ -114,11 +114,11 @@ def _rope(rope, rope_theta, T, index):
             raise ValueError(f"a RoPE table for {T} positions is not made on the side: pass rope=rope_table(positions)")
         rope = _ROPE_CACHE.get((int(T), float(rope_theta), index))
         if rope is None:
-            if torch.cuda.is_current_stream_capturing():
+            with torch.cuda.device(index):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if capturing:  # (only the cache keeps a table alive behind its address)
                 raise ValueError("make the RoPE table before the capture: rope_table(T, rope_theta), passed as rope=")
             rope = rope_table(T, rope_theta, torch.device("cuda", index))
-            # the table is shared by later calls on any stream
-            torch.cuda.current_stream(index).synchronize()
     n = rope.shape[0]
     if not (rope.dtype is _F32 and rope.get_device() == index and rope.shape == (n, 32, 2) and rope.is_contiguous()):
         _refuse("rope", rope, _F32, (None, 32, 2), index)

@@ -1,0 +1,104 @@
+"""The paged 4-bit cache's calls as programs make them: tables made elsewhere, calls back to back, rows out of
+range among rows in range, batches that keep every team busy for several chunks."""
+import threading
+
+import numpy as np
+import pytest
+
+import kv4_ref as ref
+from test_gpu_kv4 import FIB, _cuda, _dt, _i32, check_rows, make_cache, sfa, stored  # noqa: F401 (sfa: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ the RoPE table that a call finds
+
+
+def _small(sfa, seed, width=None):
+    import torch
+
+    rng = np.random.default_rng(seed)
+    lens, page = [300, 77], 16
+    cache, table = make_cache(rng, lens, page, 2)
+    if width:
+        table = np.pad(table, ((0, 0), (0, width - table.shape[1])), constant_values=-1)
+    q = torch.from_numpy(rng.standard_normal((2, 8, 64))).float()
+    return (q.cuda(), _cuda(cache), _cuda(table), _i32(lens)), (q, cache, table, lens, [0, 1, 2], page)
+
+
+def _right(sfa, got, plain, theta):
+    q, cache, table, lens, cu, page = plain
+    check_rows(*got, q, cache, table, lens, cu, page, None, ref.rope(table.shape[1] * page, theta), 1.0, 1.0, False)
+
+
+def test_table_made_on_a_busy_stream(sfa):
+    """rope_table on a stream with work ahead of it, then a call without rope= on one that waits for nothing."""
+    import torch
+
+    args, plain = _small(sfa, 31)
+    T, theta = plain[2].shape[1] * plain[5], 4321.0
+    sfa.rope_table(T, 1e3)
+    sfa.kv4_attend(*args, rope_theta=1e3)  # kernels are loaded, which waits for the device
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(a):
+        spoiled = torch.full((T, 32, 2), float("nan"), device="cuda")  # what the table's memory held before
+        del spoiled
+        torch.cuda._sleep(200_000_000)
+        sfa.rope_table(T, theta)
+    with torch.cuda.stream(b):
+        got = sfa.kv4_attend(*args, rope_theta=theta)
+    torch.cuda.synchronize()
+    _right(sfa, got, plain, theta)
+
+
+def test_table_of_a_capture(sfa):
+    """forward in a capture makes a table that only replays fill: an eager call of its length makes its own,
+    and the graph's replays are right whatever was captured beside it."""
+    import torch
+
+    args, plain = _small(sfa, 32)
+    T, theta = plain[2].shape[1] * plain[5], 8765.0
+    rng = np.random.default_rng(5)
+    q, k, v = (torch.from_numpy(rng.standard_normal((1, h, T, 64))).to(torch.bfloat16).cuda() for h in (8, 2, 2))
+    sfa.forward_int(q, k, v, dist=FIB)  # first use outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = sfa.forward_int(q, k, v, dist=FIB, rope_theta=theta)
+        o2, _ = sfa.forward_int(o, k, v, dist=FIB, rope_theta=theta)
+    got = sfa.kv4_attend(*args, rope_theta=theta)
+    torch.cuda.synchronize()
+    _right(sfa, got, plain, theta)
+    graph.replay()
+    torch.cuda.synchronize()
+    wo, wl = sfa.forward_int(q, k, v, dist=FIB, rope_theta=theta)
+    assert torch.equal(o, wo) and torch.equal(lse, wl)
+    assert torch.equal(o2, sfa.forward_int(wo, k, v, dist=FIB, rope_theta=theta)[0])
+    assert sfa.get_device_status() == 0
+
+
+def test_first_calls_of_two_threads(sfa):
+    """Two threads with a stream each, both first to want a table."""
+    import torch
+
+    args, plain = _small(sfa, 33)
+    torch.cuda.synchronize()
+    for theta in (1234.5, 2345.5, 3456.5, 4567.5):
+        got, gate = [None, None], threading.Barrier(2)
+
+        def call(i):
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(2_000_000)
+                gate.wait()
+                got[i] = sfa.kv4_attend(*args, rope_theta=theta)
+                stream.synchronize()
+
+        threads = [threading.Thread(target=call, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        for g in got:
+            _right(sfa, g, plain, theta)
