@@ -126,7 +126,9 @@ def status_string(code: int) -> str:
 
 # ------------------------------------------------------------ device calls
 
-_ROPE_CACHE: dict = {}  # (positions, theta, device index) -> table; complete ones only
+_ROPE_CACHE: dict = {}  # (positions, theta, device index) -> table, the first rows of a _ROPE_WHOLE; complete ones only
+_ROPE_WHOLE: dict = {}  # (theta, device index) -> the longest table so far
+_ROPE_LEAST = 1024  # positions of the shortest
 _ROPE_LOCK = threading.Lock()
 
 
@@ -143,27 +145,44 @@ def _stream():
 def rope_table(T: int, theta: float = 1e4, device=None):
     """fp32 [T, 32, 2] (cos, sin) table written by sfa_rope_table.
 
-    The first call of a length waits for the table before it is kept: any stream
-    and thread that finds it afterwards may read it without waiting for another.
-    Inside a graph capture, where nothing can be waited for, a table that is not
-    there yet belongs to the capture, which fills it at each replay."""
+    Tables are kept for the process's life, 256 bytes a position.  A theta's
+    tables on a device are the first rows of one whose length is a power of two,
+    made anew, twice as long at least, when a call wants more positions: all of
+    them together hold less than four times the longest that was asked for.
+
+    The call that makes one waits for it before it is kept: any stream and thread
+    that finds it afterwards may read it without waiting for another.  Inside a
+    graph capture, where nothing can be waited for, a table that is not there yet
+    belongs to the capture, which fills it at each replay."""
     torch = _torch()
     dev = torch.device(device if device is not None else "cuda")
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    key = (int(T), float(theta), dev.index)
-    tab = _ROPE_CACHE.get(key)
+    tab = _kept_rope_table(T, theta, dev.index)
     if tab is not None:
         return tab
     with torch.cuda.device(dev):
-        if torch.cuda.is_current_stream_capturing():
+        if T < 1 or torch.cuda.is_current_stream_capturing():
             return _new_rope_table(T, theta, dev)
         with _ROPE_LOCK:
-            if key not in _ROPE_CACHE:
-                tab = _new_rope_table(T, theta, dev)
+            tab = _kept_rope_table(T, theta, dev.index)
+            if tab is None:
+                whole = _new_rope_table(max(_ROPE_LEAST, 1 << (int(T) - 1).bit_length()), theta, dev)
                 torch.cuda.current_stream().synchronize()
-                _ROPE_CACHE[key] = tab
-            return _ROPE_CACHE[key]
+                _ROPE_WHOLE[float(theta), dev.index] = whole
+                tab = _kept_rope_table(T, theta, dev.index)
+            return tab
+
+
+def _kept_rope_table(T, theta, index):
+    """The table of T positions if an earlier call made one of as many or more, else None."""
+    key = (int(T), float(theta), index)
+    tab = _ROPE_CACHE.get(key)
+    if tab is None:
+        whole = _ROPE_WHOLE.get(key[1:])
+        if whole is not None and 0 < T <= whole.shape[0]:
+            tab = _ROPE_CACHE.setdefault(key, whole[:int(T)])
+    return tab
 
 
 def _new_rope_table(T, theta, dev):

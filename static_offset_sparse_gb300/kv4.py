@@ -21,7 +21,7 @@ import struct
 import torch
 
 from ._lib import SFA_BF16, SFA_F32, SIGNATURES, _lib, check, i32_array
-from .api import _ROPE_CACHE, rope_table
+from .api import _ROPE_CACHE, _kept_rope_table, rope_table
 
 ROW_BYTES = 72  # one (row, head): 32 + 32 bytes of codes, 8 of scales
 PAGES = {ROW_BYTES * page: page for page in (16, 32, 64, 128)}
@@ -112,7 +112,7 @@ def _rope(rope, rope_theta, T, index):
             return 0, 0
         if T > MAX_OWN_POSITIONS:
             raise ValueError(f"a RoPE table for {T} positions is not made on the side: pass rope=rope_table(positions)")
-        rope = _ROPE_CACHE.get((int(T), float(rope_theta), index))
+        rope = _kept_rope_table(T, rope_theta, index)
         if rope is None:
             with torch.cuda.device(index):
                 capturing = torch.cuda.is_current_stream_capturing()
@@ -222,7 +222,8 @@ def kv4_append(k, v, cache, slots, pos, *, rope_theta: float = 1e4, rope=None, k
     (bf16 or fp32; rows may be slices of wider ones) at slots [N] (distinct;
     negative: skipped) and positions pos [N].  rope: a table of rope_table that
     covers the positions; else one of rope_theta for as many positions as the
-    pool has rows is made once and kept, up to 2^20 (0: no rotation)."""
+    pool has rows, up to 2^20 (0: no rotation).  The first call that wants a
+    longer one than is there makes it, and waits for it, as rope_table does."""
     fast = _native()
     made = rope if rope is not None or not rope_theta else _made_rope(rope_theta, cache, cache, 0)
     if fast is not None and (made is not None or not rope_theta):

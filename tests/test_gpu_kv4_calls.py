@@ -42,7 +42,7 @@ def test_table_made_on_a_busy_stream(sfa):
     torch.cuda.synchronize()
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
     with torch.cuda.stream(a):
-        spoiled = torch.full((T, 32, 2), float("nan"), device="cuda")  # what the table's memory held before
+        spoiled = torch.full((1024, 32, 2), float("nan"), device="cuda")  # what the table's memory held before
         del spoiled
         torch.cuda._sleep(200_000_000)
         sfa.rope_table(T, theta)
@@ -102,3 +102,27 @@ def test_first_calls_of_two_threads(sfa):
             t.join()
         for g in got:
             _right(sfa, g, plain, theta)
+
+
+def test_tables_of_growing_block_tables(sfa):
+    """Block tables of many widths: the same rotations, a table shared by all of them, the cache's memory within
+    a few times the longest."""
+    import torch
+    from static_offset_sparse_gb300 import api
+
+    theta = 6543.0
+    args, plain = _small(sfa, 34)
+    want = sfa.kv4_attend(*args, rope=_cuda(ref.rope(3000, theta)))
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for width in range(args[2].shape[1], 400):
+        t = torch.nn.functional.pad(args[2], (0, width - args[2].shape[1]), value=-1)
+        got = sfa.kv4_attend(args[0], args[1], t, args[3], rope_theta=theta)
+    del t
+    _right(sfa, got, plain, theta)
+    assert torch.cuda.memory_allocated() - before < 4 * 6400 * 256
+    tab = sfa.rope_table(6390, theta)
+    assert tab.is_contiguous() and torch.equal(sfa.rope_table(100, theta), tab[:100])
+    assert np.abs(tab.double().cpu().numpy() - ref.rope(6390, theta)).max() <= 2.0 ** -23
+    assert len({x.untyped_storage().data_ptr() for (n, th, i), x in api._ROPE_CACHE.items() if th == theta}) <= 4
+    assert torch.equal(want[1].isfinite(), got[1].isfinite())

@@ -51,6 +51,8 @@ def fake(monkeypatch):
     monkeypatch.setattr(api, "_torch", lambda: t)
     monkeypatch.setattr(api, "_lib", lambda: types.SimpleNamespace(sfa_rope_table=lambda *a: 0))
     monkeypatch.setattr(api, "_ROPE_CACHE", {})
+    if hasattr(api, "_ROPE_WHOLE"):
+        monkeypatch.setattr(api, "_ROPE_WHOLE", {})
     return t
 
 
@@ -99,3 +101,20 @@ def test_a_second_thread_waits_for_the_table(fake):
     assert _written(fake.api.rope_table(100, 1e4))
     other.join()
     assert got == [True] and len(fake.tables) == 1
+
+
+def test_widths_share_a_table(fake):
+    """A table for every width of a block table that grows by pages is a few tables, not one a width."""
+    for pages in range(1, 1001):
+        tab = fake.api.rope_table(64 * pages, 1e4)
+        assert tab.shape == (64 * pages, 32, 2) and _written(tab)
+    sizes = [t.shape[0] for t in fake.tables]
+    assert len(sizes) <= 11 and sum(sizes) < 4 * 64000 and fake.waits == len(sizes)
+    assert fake.api.rope_table(64, 1e4) is fake.api.rope_table(64, 1e4)
+    fake.api.rope_table(64, 500.0)  # another theta has its own
+    assert fake.waits == len(sizes) + 1
+    fake.capturing = True  # a new width that a kept table covers, inside a capture
+    before = len(fake.tables)
+    assert fake.api.rope_table(63000, 1e4).shape == (63000, 32, 2) and len(fake.tables) == before
+    fake.api.rope_table(1 << 17, 1e4)  # one that none covers
+    assert fake.tables[-1].shape == (1 << 17, 32, 2) and fake.waits == len(sizes) + 1
