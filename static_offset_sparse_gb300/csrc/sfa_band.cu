@@ -118,9 +118,9 @@ __device__ __forceinline__ void band_rope_pairs(const float2* rope, const int* p
   for (int x = 0; x < 2; ++x)
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      const float2* tab = rope + (int64_t)pos[x] * 32 + 16 * kk + 2 * tig;
-      rp[x][2 * kk] = __ldg(reinterpret_cast<const float4*>(tab));
-      rp[x][2 * kk + 1] = __ldg(reinterpret_cast<const float4*>(tab + 8));
+      const float2* rope_at = rope + (int64_t)pos[x] * 32 + 16 * kk + 2 * tig;
+      rp[x][2 * kk] = __ldg(reinterpret_cast<const float4*>(rope_at));
+      rp[x][2 * kk + 1] = __ldg(reinterpret_cast<const float4*>(rope_at + 8));
     }
 }
 
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kBThreads, 3)
                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mq,
                       const __grid_constant__ CUtensorMap mdo, const __grid_constant__ CUtensorMap mo,
                       const __grid_constant__ CUtensorMap mqt,
-                      const __grid_constant__ CUtensorMap mdq, float2* __restrict__ stat,
+                      const __grid_constant__ CUtensorMap mdq, float2* stat,
                       const __grid_constant__ BandPlan P) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[kBStages + 1];
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kBThreads, 3)
     band_bwd_kv_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mqt,
                        const __grid_constant__ CUtensorMap mdo, const __grid_constant__ CUtensorMap mdk,
-                       const __grid_constant__ CUtensorMap mdv, const float2* __restrict__ stat,
+                       const __grid_constant__ CUtensorMap mdv, const float2* stat,
                        const __grid_constant__ BandPlan P) {
   constexpr int BU = kBR / G;
   extern __shared__ unsigned char smem_raw[];
@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(kBThreads, 3)
           const int n = 32 * hq + 8 * nt + 2 * tig + c;
           const int u = cw.us + n % BU;
           uq[nt][c] = u < Uc ? u : -(1 << 30);
-          sd[nt][c] = __ldg(stat + (int64_t)(qplane + n / BU) * T + cw.r + delta * min(u, Uc - 1));
+          sd[nt][c] = stat[(int64_t)(qplane + n / BU) * T + cw.r + delta * min(u, Uc - 1)];
         }
       float st[4][4], dpt[4][4];
       {

@@ -415,8 +415,8 @@ __device__ __forceinline__ void kv_group(uint32_t qst, uint32_t dst, const uint3
       if (FOLD) {  // words dS hi, dS lo, P hi, P lo
         const uint4 r4 = *reinterpret_cast<const uint4*>(csm + rec + m1 * STEP);
         const int qi = qw + m1 + (tig >> 1);
-        const float c0 = __ldg(corr + (int64_t)(tig & 1) * T + qi);
-        const float c1 = __ldg(corr + (int64_t)((tig & 1) + 2) * T + qi);
+        const float c0 = corr[(int64_t)(tig & 1) * T + qi];
+        const float c1 = corr[(int64_t)((tig & 1) + 2) * T + qi];
         const float2 lo = unpack_bf16(r4.y), pw = unpack_bf16(r4.z);
         one = make_uint4(r4.x, pack_bf16(fmaf(pw.x, c0, lo.x), fmaf(pw.y, c1, lo.y)), r4.z, r4.w);
       } else {  // words dS, P
@@ -437,8 +437,8 @@ __device__ __forceinline__ void kv_group(uint32_t qst, uint32_t dst, const uint3
         const int m = 4 * ks + 2 * hb;
         const bool on = (mask >> m) & 1u;
         const int qi = on ? qw + m + (tig >> 1) : 0;
-        cf[ks][hb][0] = on ? __ldg(corr + (int64_t)(tig & 1) * T + qi) : 0.0f;
-        cf[ks][hb][1] = on ? __ldg(corr + (int64_t)((tig & 1) + 2) * T + qi) : 0.0f;
+        cf[ks][hb][0] = on ? corr[(int64_t)(tig & 1) * T + qi] : 0.0f;
+        cf[ks][hb][1] = on ? corr[(int64_t)((tig & 1) + 2) * T + qi] : 0.0f;
       }
   }
 #pragma unroll

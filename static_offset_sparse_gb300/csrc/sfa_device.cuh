@@ -30,16 +30,18 @@ __device__ __forceinline__ bool dbg_in(int64_t i, int64_t n, int* status) {
 __device__ __forceinline__ bool dbg_in(int64_t, int64_t, int*) { return true; }
 #endif
 
-// Eight consecutive elements -> fp32.  p must be 16-byte aligned.
+// Eight consecutive elements -> fp32.  p must be 16-byte aligned.  Ordinary
+// loads: a kernel that was launched early lives while the one before it writes
+// what it will read, so only RoPE tables may be read as read-only data (__ldg).
 __device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = reinterpret_cast<const float4*>(p)[0];
+  const float4 b = reinterpret_cast<const float4*>(p)[1];
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 
 __device__ __forceinline__ void load8(const bf16* p, float* x) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
   const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -82,10 +84,10 @@ __device__ __forceinline__ void store8(bf16* p, const float* x) {
 // [T][32] float2 (cos, sin).
 __device__ __forceinline__ void load_rope8(const float2* tab, int64_t pos, int j0, float* cs,
                                            float* sn) {
-  const float4* p = reinterpret_cast<const float4*>(tab + pos * 32 + j0);
+  const float4* rope = reinterpret_cast<const float4*>(tab + pos * 32 + j0);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float4 v = __ldg(p + e);
+    const float4 v = __ldg(rope + e);
     cs[2 * e] = v.x;
     sn[2 * e] = v.y;
     cs[2 * e + 1] = v.z;

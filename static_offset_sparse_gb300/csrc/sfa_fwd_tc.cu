@@ -37,9 +37,8 @@ namespace sfa {
 
 constexpr int kPrepPlanes = 1;
 
-__global__ void __launch_bounds__(256) rope_prep_kernel(const bf16* __restrict__ k,
-                                                        const float2* __restrict__ rope,
-                                                        bf16* __restrict__ kr, int64_t planes, int T) {
+__global__ void __launch_bounds__(256) rope_prep_kernel(const bf16* k, const float2* __restrict__ rope,
+                                                        bf16* kr, int64_t planes, int T) {
   pdl_launch_dependents();
   pdl_wait();  // K may be the previous kernel's output
   const int64_t it = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;

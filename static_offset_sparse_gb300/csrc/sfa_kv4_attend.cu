@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
           if (page >= 0 && page < a.n_pages) {
             const uint32_t first_row = ((uint32_t)page * a.Hkv + h) * (uint32_t)(9 * S / 4);
             row = first_row + in;
-            sc = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)first_row * 32 + 64 * S + 8 * in));
+            sc = *reinterpret_cast<const uint2*>(a.cache + (uint64_t)first_row * 32 + 64 * S + 8 * in);
           } else {
             record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
           }
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
           const uint32_t sa = __shfl_sync(0xffffffffu, sc.x, g0) >> (8 * t) & 255u;
           const uint32_t sb = __shfl_sync(0xffffffffu, sc.x, g0 + 8) >> (8 * t) & 255u;
           uint2 ka = make_uint2(0, 0), kb = ka;
-          if (ra != kNone) ka = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)ra * 32 + 8 * t));
-          if (rb != kNone) kb = __ldg(reinterpret_cast<const uint2*>(a.cache + (uint64_t)rb * 32 + 8 * t));
+          if (ra != kNone) ka = *reinterpret_cast<const uint2*>(a.cache + (uint64_t)ra * 32 + 8 * t);
+          if (rb != kNone) kb = *reinterpret_cast<const uint2*>(a.cache + (uint64_t)rb * 32 + 8 * t);
           there |= (ra != kNone) << (2 * i) | (rb != kNone) << (2 * i + 1);
           if (PACK) {
             of[2 * i] = (int)__umulhi((uint32_t)(j0 + g0), gr.magic);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
             const int from = 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
             const uint32_t rv = __shfl_sync(0xffffffffu, row, from);
             vs[i][e] = __shfl_sync(0xffffffffu, sc.y, from) >> (8 * (g >> 1)) & 255u;
-            w[i][e] = rv == kNone ? 0u : __ldg(reinterpret_cast<const uint32_t*>(a.cache + (uint64_t)rv * 32 + 32 * S + 4 * g));
+            w[i][e] = rv == kNone ? 0u : *reinterpret_cast<const uint32_t*>(a.cache + (uint64_t)rv * 32 + 32 * S + 4 * g);
           }
           key_products<NT>(q, ka, kb, sa, sb, s[i]);
         }

@@ -126,3 +126,78 @@ def test_tables_of_growing_block_tables(sfa):
     assert np.abs(tab.double().cpu().numpy() - ref.rope(6390, theta)).max() <= 2.0 ** -23
     assert len({x.untyped_storage().data_ptr() for (n, th, i), x in api._ROPE_CACHE.items() if th == theta}) <= 4
     assert torch.equal(want[1].isfinite(), got[1].isfinite())
+
+
+# ------------------------------------------------------------------ calls back to back
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,width,Hq", [(1, 700, 8), (3, 700, 16), (40, 300, 8)])
+def test_calls_with_other_inputs_in_turn(sfa, dtype, new, width, Hq):
+    """Calls that split their rows, two inputs in turn over one workspace, nothing between them: each gives its
+    own result again.  (A kernel starts while the one before it writes what it will read.)"""
+    import torch
+
+    rng = np.random.default_rng(41)
+    page, R = 64, 3
+    inputs = []
+    for lens in ([9000, 5000, 700], [8000, 9100, 41]):
+        cache, table = make_cache(rng, lens, page, 2)
+        table = np.pad(table, ((0, 0), (0, width - table.shape[1])), constant_values=-1)
+        q = torch.from_numpy(rng.standard_normal((R * new, Hq, 64))).to(_dt(dtype)).cuda()
+        inputs.append((q, _cuda(cache), _cuda(table), _i32(lens)))
+    cu = _i32(np.arange(R + 1) * new) if new > 1 else None
+    n = max(sfa.kv4_workspace_size(*x[:3]) for x in inputs)
+    assert n > 0
+    ws = torch.zeros((n,), dtype=torch.uint8, device="cuda")
+    want = [sfa.kv4_attend(*x, cu_q=cu, rope_theta=0) for x in inputs]
+    out = [[(torch.zeros_like(w[0]), torch.zeros_like(w[1])) for w in want] for _ in range(10)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for turn in out:
+            for x, (o, lse) in zip(inputs, turn):
+                sfa.kv4_attend(*x, cu_q=cu, rope_theta=0, ws=ws, o=o, lse=lse)
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        for turn in out:
+            for w, got in zip(want, turn):
+                assert torch.equal(w[0], got[0]) and torch.equal(w[1], got[1])
+                got[0].zero_()
+    assert sfa.get_device_status() == 0
+
+
+@pytest.mark.parametrize("R,dist", [(5, None), (5, FIB), (60, FIB), (900, [0, 1, 2, 5])])
+def test_rows_written_by_the_call_before(sfa, R, dist):
+    """append and attend in turn over the same slots, two contents in turn: attention reads what the call just
+    before it wrote."""
+    import torch
+
+    rng = np.random.default_rng(42)
+    page, lens = 16, [20] * R
+    cache, table = make_cache(rng, lens, page, 2)
+    c, t, n = _cuda(cache), _cuda(table), _i32(lens)
+    q = torch.from_numpy(rng.standard_normal((R, 8, 64))).to(torch.bfloat16).cuda()
+    slots = _i32([int(table[r, p // page]) * page + p % page for r in range(R) for p in range(20)])
+    pos = _i32([p for r in range(R) for p in range(20)])
+    kv = [torch.from_numpy(rng.standard_normal((2, R * 20, 2, 64))).to(torch.bfloat16).cuda() for _ in range(2)]
+    want = []
+    for x in kv:
+        sfa.kv4_append(x[0], x[1], c, slots, pos, rope_theta=0)
+        torch.cuda.synchronize()
+        want.append(sfa.kv4_attend(q, c, t, n, dist=dist, rope_theta=0))
+        torch.cuda.synchronize()
+    out = []
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(10):
+            for x in kv:
+                sfa.kv4_append(x[0], x[1], c, slots, pos, rope_theta=0)
+                out.append(sfa.kv4_attend(q, c, t, n, dist=dist, rope_theta=0))
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, got in enumerate(out):
+            assert torch.equal(want[i % 2][0], got[0]) and torch.equal(want[i % 2][1], got[1]), i
+    assert not torch.equal(want[0][0], want[1][0]) and sfa.get_device_status() == 0

@@ -170,3 +170,23 @@ def test_descriptor_bytes():
 
     values = [*range(101, 110), 2 ** 40, 2 ** 41, 2 ** 42, 0.75, 1.5, 2 ** 47 - 16, 7, 2 ** 46, 9]
     assert bytes(Kv4Desc(*values)) == kv4._desc(*values) and len(values) == len(Kv4Desc._fields_)
+
+
+def test_only_rope_tables_are_read_as_read_only_data():
+    """Kernels are launched early: they live while the one before them writes what they will read, and only
+    ordinary loads are ordered by their wait for it.  So __ldg, and __restrict__ on what is read (which makes the
+    compiler use the same loads), are for RoPE tables alone."""
+    import os
+    import re
+
+    import static_offset_sparse_gb300 as pkg
+
+    csrc = os.path.join(os.path.dirname(pkg.__file__), "csrc")
+    reads = []
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        reads += [(name, m.group(0)) for m in re.finditer(r"__ldg\([^;]*;|[^,(]*__restrict__[^,)]*|ld\.global\.nc", text)]
+    assert len(reads) >= 5
+    for name, text in reads:
+        assert "rope" in text, (name, text)
