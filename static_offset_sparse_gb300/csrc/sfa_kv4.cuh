@@ -75,6 +75,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+// What takes an accumulator (of a query whose largest number has exponent bits
+// ex, scaled to 2^8) to its logit in log2 units.  Everything before the last
+// product is a power of two.  It is a normal number whatever kscale is: a masked
+// logit is -inf times it, and for a factor raised to 2^-126 no logit reaches 2^-99.
+__device__ __forceinline__ float logit_factor(int ex, float kscale) {
+  return fmaxf(__uint_as_float((uint32_t)ex << 23) * 0.00390625f * kscale * (0.125f * kLog2e), 0x1p-126f);
+}
+
 // Arguments of an attend call, passed by value.
 struct Kv4Args {
   const void* q;

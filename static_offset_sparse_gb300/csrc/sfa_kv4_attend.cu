@@ -25,11 +25,11 @@ namespace sfa {
 // holds dims 16t .. 16t + 15 of column 8 nt + g, in the order the keys' codes
 // come in.
 // One column tile: 8 B registers of high and 8 of low parts; returns the factor
-// that takes the accumulator of column g to its logit (log2 units, `scale`
+// that takes the accumulator of column g to its logit (log2 units, kscale
 // included).  base: the first head of the first row; p: the position of this
 // lane's column, below 0 for a zero column.
 template <typename TIO>
-__device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, int lgG, int p, const float2* rope, float scale, int nt,
+__device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, int lgG, int p, const float2* rope, float kscale, int nt,
                                               int lane, uint32_t* hi, uint32_t* lo) {
   const int g = lane >> 2, t = lane & 3, col = 8 * nt + g;
   const TIO* row = base + (col >> lgG) * stride + (col & ((1 << lgG) - 1)) * kD;
@@ -67,7 +67,7 @@ __device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, i
     const float2 r = unpack_f16(hi[e]);
     lo[e] = pack_f16(a - r.x, b - r.y);
   }
-  return __uint_as_float((uint32_t)ex << 23) * (scale * 0.00390625f);
+  return logit_factor(ex, kscale);
 }
 
 // All of them in registers, 16 a column tile.
@@ -78,10 +78,10 @@ struct QFrag {
 
   // at: position of column 8 nt + lane / 4
   template <typename TIO, typename AT>
-  __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, AT at, const float2* rope, float scale, int lane) {
+  __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, AT at, const float2* rope, float kscale, int lane) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float back = load_queries(base, stride, lgG, at(8 * nt + (lane >> 2)), rope, scale, nt, lane, hi[nt], lo[nt]);
+      const float back = load_queries(base, stride, lgG, at(8 * nt + (lane >> 2)), rope, kscale, nt, lane, hi[nt], lo[nt]);
       c[nt][0] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3));
       c[nt][1] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3) + 4);
     }
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
         const int p = PACK ? __shfl_sync(0xffffffffu, pos, col >> a.lgG) : pos;
         return PACK || col < G ? p : -1;
       };
-      q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, at, a.rope, 0.125f * kLog2e * a.kscale, lane);
+      q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, at, a.rope, a.kscale, lane);
       for (int j0 = 32 * mine; j0 < most; j0 += 32 * (KIND == kCluster ? kClusterCtas * kGatherWarps : warps)) {
         // lane i: key i of two tiles, its code row (in 32 bytes from the cache's begin) and its scales
         int j = j0 + lane, kr = 0;
@@ -795,12 +795,11 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kS
     const int ncol = cur.it.nrows << a.lgG;
     if (cur.x != qx || cur.h != qh) {
       const TIO* base = static_cast<const TIO*>(a.q) + (int64_t)cur.it.row0 * a.q_stride + cur.h * G * kD;
-      const float scale = 0.125f * kLog2e * a.kscale;
       auto at = [&](int col) { return col < ncol ? cur.it.pfirst + (col >> a.lgG) : -1; };
       if constexpr (NT == 4) {  // a column tile a warp
         static_assert(NT == kStreamWarps && TEAMS == 1, "a column tile a warp; one team at the barrier");
         uint32_t hi[8], lo[8];
-        const float back = load_queries(base, a.q_stride, a.lgG, at(8 * warp + g), a.rope, scale, warp, lane, hi, lo);
+        const float back = load_queries(base, a.q_stride, a.lgG, at(8 * warp + g), a.rope, a.kscale, warp, lane, hi, lo);
         bar_sync(1, 32 * kStreamWarps);  // the last item's queries have been used
         if (t == 0) qc[8 * warp + g] = back;
 #pragma unroll
@@ -813,7 +812,7 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kS
 #pragma unroll
           for (int e = 0; e < 2; ++e) q.c[nt][e] = qc[8 * nt + 2 * t + e];
       } else {
-        q.load(base, a.q_stride, a.lgG, at, a.rope, scale, lane);
+        q.load(base, a.q_stride, a.lgG, at, a.rope, a.kscale, lane);
       }
       qx = cur.x;
       qh = cur.h;

@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         }
         const int ex = min(max((int)(__float_as_uint(big) >> 23), 9), 253);
         const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f;
-        cs = __uint_as_float((uint32_t)ex << 23) * (0.125f * kLog2e * a.kscale * 0.00390625f);
+        cs = logit_factor(ex, a.kscale);
 #pragma unroll 2
         for (int c = 0; c < 4; ++c) {
           float x[2][8] = {{0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0, 0, 0}};

@@ -201,3 +201,30 @@ def test_rows_written_by_the_call_before(sfa, R, dist):
         for i, got in enumerate(out):
             assert torch.equal(want[i % 2][0], got[0]) and torch.equal(want[i % 2][1], got[1]), i
     assert not torch.equal(want[0][0], want[1][0]) and sfa.get_device_status() == 0
+
+
+# ------------------------------------------------------------------ numbers at the ends of their range
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,width,dist", [(1, 30, [0, 1, 7, 200]), (1, 80, None), (1, 200, None), (3, 200, None), (6, 200, None),
+                                            (40, 60, None), (40, 60, list(range(70)))])
+@pytest.mark.parametrize("kscale", [1e-7, 1e-20, 2.0 ** -126, 2.0 ** -140])
+def test_attend_small_kscale(sfa, dtype, new, width, dist, kscale):
+    """Zero and tiny queries times a small kscale: a masked key stays masked, whichever kernel the
+    call goes to (gather, cluster, stream with one to four column tiles, prompts)."""
+    import torch
+
+    rng = np.random.default_rng(51)
+    lens, page, Hq = [500, 130, 41], 32, 8
+    cache, table = make_cache(rng, lens, page, 2)
+    table = np.pad(table, ((0, 0), (0, width - table.shape[1])), constant_values=-1)
+    cu = np.arange(len(lens) + 1) * new
+    q = torch.from_numpy(rng.standard_normal((cu[-1], Hq, 64)))
+    q[::2] *= 0
+    q[:, 1] *= 2.0 ** -110
+    q = q.to(_dt(dtype))
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), cu_q=_i32(cu) if new > 1 else None, dist=dist, rope_theta=0,
+                            kscale=kscale)
+    assert sfa.get_device_status() == 0
+    check_rows(o, lse, q, cache, table, lens, cu, page, dist, None, float(np.float32(kscale)), 1.0, dtype == "bf16")
