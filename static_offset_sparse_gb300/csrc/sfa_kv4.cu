@@ -1,6 +1,8 @@
 // The paged 4-bit cache's bookkeeping, its write and its read-back: block
 // tables and slot maps from request lengths, rotate + quantise + store, and
 // rows as numbers.
+#include <math.h>
+
 #include <algorithm>
 
 #include "sfa_kv4.cuh"
@@ -530,7 +532,8 @@ static int check_attend(const sfa_kv4_desc* d, Plan* p, Kv4Args* a) {
   a->lgS = __builtin_ctz((unsigned)d->page);
   a->rope = reinterpret_cast<const float2*>(d->rope);
   a->rope_T = d->rope_T;
-  a->kscale = d->kscale;
+  a->qmul = (float)(2.0 * frexp(0.125 * M_LOG2E * d->kscale, &a->qexp));
+  a->qexp -= 1;
   a->vscale = d->vscale;
   a->q_stride = d->q_stride;
   if (d->N == 0) return SFA_OK;

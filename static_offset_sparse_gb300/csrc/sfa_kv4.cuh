@@ -76,11 +76,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 // What takes an accumulator (of a query whose largest number has exponent bits
-// ex, scaled to 2^8) to its logit in log2 units.  Everything before the last
-// product is a power of two.  It is a normal number whatever kscale is: a masked
-// logit is -inf times it, and for a factor raised to 2^-126 no logit reaches 2^-99.
-__device__ __forceinline__ float logit_factor(int ex, float kscale) {
-  return fmaxf(__uint_as_float((uint32_t)ex << 23) * 0.00390625f * kscale * (0.125f * kLog2e), 0x1p-126f);
+// ex, scaled to 2^8 and times Kv4Args::qmul) to its logit in log2 units: a power
+// of two, so that the product is exact and 2^(s c - m) cannot pass 1 by what
+// rounding a large maximum m leaves out.  It is a normal number whatever kscale
+// is: a masked logit is -inf times it, and for a factor raised to 2^-126 no logit
+// reaches 2^-98.
+__device__ __forceinline__ float logit_factor(int ex, int qexp) {
+  return __uint_as_float((uint32_t)min(max(ex - 8 + qexp, 1), 254) << 23);
 }
 
 // Arguments of an attend call, passed by value.
@@ -95,7 +97,8 @@ struct Kv4Args {
   const float2* rope;       // [rope_T][32] or nullptr
   int64_t q_stride;         // elements between query rows
   int32_t R, N, Hq, Hkv, lgG, max_pages, n_pages, lgS, rope_T;
-  float kscale, vscale;
+  float qmul, vscale;       // kscale log2(e) / 8 = qmul 2^qexp, qmul in [1, 2]
+  int32_t qexp;
   int* status;
   long long wait_cycles;    // limit of every bounded wait
   int32_t debug_skip;       // test injection: tile whose copies the first warp of the first chunk's CTA never starts, or -1

@@ -6,8 +6,11 @@
 // dequantised once for the whole group.  What keeps it exact:
 //  * keys and values are whole f16 numbers (code * scale);
 //  * the query, rotated in fp32, is scaled by a power of two to its own row's
-//    size and split into two f16 parts (22 bits), whose products go to one
-//    fp32 accumulator: logits are good to fp32's last bits;
+//    size (and by the mantissa of kscale log2(e) / 8) and split into two f16
+//    parts (22 bits), whose products go to one fp32 accumulator: logits, a power
+//    of two times that, are good to fp32's last bits;
+//  * what is added to a logit before 2^x is rounded so that the result cannot
+//    pass the largest that the kernel reckons with, however large logits are;
 //  * probabilities are rounded to f16 (2^-12 of each) for the values' product;
 //    fp32 outputs add a second product with what that rounding dropped;
 //  * the softmax sum is taken in fp32 from the unrounded probabilities.
@@ -25,11 +28,10 @@ namespace sfa {
 // holds dims 16t .. 16t + 15 of column 8 nt + g, in the order the keys' codes
 // come in.
 // One column tile: 8 B registers of high and 8 of low parts; returns the factor
-// that takes the accumulator of column g to its logit (log2 units, kscale
-// included).  base: the first head of the first row; p: the position of this
+// that takes the accumulator of column g to its logit (log2 units).  base: the first head of the first row; p: the position of this
 // lane's column, below 0 for a zero column.
 template <typename TIO>
-__device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, int lgG, int p, const float2* rope, float kscale, int nt,
+__device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, int lgG, int p, const float2* rope, float qmul, int qexp, int nt,
                                               int lane, uint32_t* hi, uint32_t* lo) {
   const int g = lane >> 2, t = lane & 3, col = 8 * nt + g;
   const TIO* row = base + (col >> lgG) * stride + (col & ((1 << lgG) - 1)) * kD;
@@ -59,7 +61,7 @@ __device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, i
   // 2^(8 - exponent of the largest): its parts then reach f16's 2^-24 steps
   // 2^-33 below it
   const int ex = min(max((int)(__float_as_uint(m) >> 23), 9), 253);
-  const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f;
+  const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f * qmul;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float a = x[2 * e] * f, b = x[2 * e + 1] * f;
@@ -67,7 +69,7 @@ __device__ __forceinline__ float load_queries(const TIO* base, int64_t stride, i
     const float2 r = unpack_f16(hi[e]);
     lo[e] = pack_f16(a - r.x, b - r.y);
   }
-  return logit_factor(ex, kscale);
+  return logit_factor(ex, qexp);
 }
 
 // All of them in registers, 16 a column tile.
@@ -78,10 +80,10 @@ struct QFrag {
 
   // at: position of column 8 nt + lane / 4
   template <typename TIO, typename AT>
-  __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, AT at, const float2* rope, float kscale, int lane) {
+  __device__ __forceinline__ void load(const TIO* base, int64_t stride, int lgG, AT at, const float2* rope, float qmul, int qexp, int lane) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float back = load_queries(base, stride, lgG, at(8 * nt + (lane >> 2)), rope, kscale, nt, lane, hi[nt], lo[nt]);
+      const float back = load_queries(base, stride, lgG, at(8 * nt + (lane >> 2)), rope, qmul, qexp, nt, lane, hi[nt], lo[nt]);
       c[nt][0] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3));
       c[nt][1] = __shfl_sync(0xffffffffu, back, 8 * (lane & 3) + 4);
     }
@@ -196,7 +198,7 @@ __device__ __forceinline__ void softmax_step(const QFrag<NT>& q, float (*s)[NT][
           o[nt][mt][2 + e] *= corr;
         }
       }
-      const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e] - kPShift;  // no key yet: 2^-inf = 0
+      const float ref = m[nt][e] == -INFINITY ? 0.0f : __fsub_ru(m[nt][e], kPShift);  // no key yet: 2^-inf = 0
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x[i] = ex2(x[i] - ref);
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
         const int p = PACK ? __shfl_sync(0xffffffffu, pos, col >> a.lgG) : pos;
         return PACK || col < G ? p : -1;
       };
-      q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, at, a.rope, a.kscale, lane);
+      q.load(static_cast<const TIO*>(a.q) + n * a.q_stride + h * G * kD, a.q_stride, a.lgG, at, a.rope, a.qmul, a.qexp, lane);
       for (int j0 = 32 * mine; j0 < most; j0 += 32 * (KIND == kCluster ? kClusterCtas * kGatherWarps : warps)) {
         // lane i: key i of two tiles, its code row (in 32 bytes from the cache's begin) and its scales
         int j = j0 + lane, kr = 0;
@@ -641,7 +643,7 @@ __device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& 
 #pragma unroll
       for (int i = 1; i < GB; ++i) x = fmaxf(x, fmaxf(s[i][nt][e], s[i][nt][2 + e]));
       top[nt][e] = x * q.c[nt][e];
-      passes |= top[nt][e] > acc.m[nt][e] + kLag;
+      passes |= top[nt][e] > __fadd_rd(acc.m[nt][e], kLag);
     }
   if (__any_sync(0xffffffffu, passes))
 #pragma unroll
@@ -667,7 +669,7 @@ __device__ __forceinline__ void stream_keys(const Kv4Args& a, const StreamArgs& 
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float off = acc.m[nt][e] == -INFINITY ? 0.0f : kPShift - acc.m[nt][e];
+      const float off = acc.m[nt][e] == -INFINITY ? 0.0f : __fsub_rd(kPShift, acc.m[nt][e]);
 #pragma unroll
       for (int i = 0; i < GB; ++i) {
         s[i][nt][e] = ex2(fmaf(s[i][nt][e], q.c[nt][e], off));
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kS
       if constexpr (NT == 4) {  // a column tile a warp
         static_assert(NT == kStreamWarps && TEAMS == 1, "a column tile a warp; one team at the barrier");
         uint32_t hi[8], lo[8];
-        const float back = load_queries(base, a.q_stride, a.lgG, at(8 * warp + g), a.rope, a.kscale, warp, lane, hi, lo);
+        const float back = load_queries(base, a.q_stride, a.lgG, at(8 * warp + g), a.rope, a.qmul, a.qexp, warp, lane, hi, lo);
         bar_sync(1, 32 * kStreamWarps);  // the last item's queries have been used
         if (t == 0) qc[8 * warp + g] = back;
 #pragma unroll
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(32 * (kStreamWarps + 1) * kStreamTeams<NT>, kS
 #pragma unroll
           for (int e = 0; e < 2; ++e) q.c[nt][e] = qc[8 * nt + 2 * t + e];
       } else {
-        q.load(base, a.q_stride, a.lgG, at, a.rope, a.kscale, lane);
+        q.load(base, a.q_stride, a.lgG, at, a.rope, a.qmul, a.qexp, lane);
       }
       qx = cur.x;
       qh = cur.h;

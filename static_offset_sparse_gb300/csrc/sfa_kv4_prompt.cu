@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
           }
         }
         const int ex = min(max((int)(__float_as_uint(big) >> 23), 9), 253);
-        const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f;
-        cs = logit_factor(ex, a.kscale);
+        const float f = __uint_as_float((uint32_t)(254 - ex) << 23) * 256.0f * a.qmul;
+        cs = logit_factor(ex, a.qexp);
 #pragma unroll 2
         for (int c = 0; c < 4; ++c) {
           float x[2][8] = {{0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0, 0, 0}};
@@ -551,13 +551,13 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
         // a column that had no key so far has some, are the logits looked at, the maximum moved and P taken
         // anew.  (fp32 outputs look first: their P takes the logits' place.)
         const bool look = kExact || t == cur.tb;
-        float sum = 0.0f, off = m == -INFINITY ? 0.0f : kPromptShift<kExact> - m;
+        float sum = 0.0f, off = m == -INFINITY ? 0.0f : __fsub_rd(kPromptShift<kExact>, m);
         if (!look) sum = full ? column_exp<kExact, false>(tl, keys, cs, off) : column_exp<kExact, true>(tl, keys, cs, off);
         const bool again = look || __any_sync(0xffffffffu, sum > kSumLimit || (m == -INFINITY && k_lo <= k_hi));
         if (again) {
           const float top = cs * (full ? column_top<false>(tl + kColS, keys) : column_top<true>(tl + kColS, keys));
           float corr = 1.0f;
-          if (top > m + kLag) {
+          if (top > __fadd_rd(m, kLag)) {
             corr = ex2(m - top);  // 0 on the first keys
             m = top;
             l *= corr;
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
               for (int e = 0; e < 16; ++e) o[e] *= corr;
               tmem_st16(tl + kColO + c, o);
             }
-          off = m == -INFINITY ? 0.0f : kPromptShift<kExact> - m;
+          off = m == -INFINITY ? 0.0f : __fsub_rd(kPromptShift<kExact>, m);
           sum = full ? column_exp<kExact, false>(tl, keys, cs, off) : column_exp<kExact, true>(tl, keys, cs, off);
         }
         l += sum;

@@ -11,7 +11,8 @@ namespace sfa {
 // Probabilities are kept times 2^kPShift, relative to a maximum that may lag
 // the true one by 2^kLag (the statistics move only when a logit passes it by
 // more): at most 2^15 in f16, whose smallest steps then lie 2^-35 below the
-// largest probability of a column.
+// largest probability of a column.  (Sums with a maximum are rounded downwards: to
+// nearest, one of 2^26 would let 2^19 through.)
 constexpr float kPShift = 11.0f, kLag = 4.0f;
 
 // One head's output row (dims 8g .. 8g + 7 of lane (g, t)) and log-sum-exp.

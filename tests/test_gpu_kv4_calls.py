@@ -228,3 +228,49 @@ def test_attend_small_kscale(sfa, dtype, new, width, dist, kscale):
                             kscale=kscale)
     assert sfa.get_device_status() == 0
     check_rows(o, lse, q, cache, table, lens, cu, page, dist, None, float(np.float32(kscale)), 1.0, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,width,dist", [(1, 30, [0, 1, 7, 200]), (1, 80, None), (1, 200, None), (3, 200, None), (6, 200, None),
+                                            (40, 60, None), (40, 60, list(range(70)))])
+@pytest.mark.parametrize("kscale", [1.0, 1e-7])
+def test_attend_large_queries(sfa, dtype, new, width, dist, kscale):
+    """Logits of any size, far beyond those that fp32 can tell apart by less than 1: finite results, and where one key
+    stands out by more than the logits' error, its value alone, whichever kernel the call goes to."""
+    import torch
+
+    rng = np.random.default_rng(52)
+    lens, page, Hq = [500, 130, 41], 32, 8
+    cache, table = make_cache(rng, lens, page, 2)
+    padded = np.pad(table, ((0, 0), (0, width - table.shape[1])), constant_values=-1)
+    cu = np.arange(len(lens) + 1) * new
+    q = torch.from_numpy(rng.standard_normal((cu[-1], Hq, 64)))
+    q *= torch.tensor([2.0 ** e for e in (16, 21, 23, 24, 25, 27, 60, 100)])[None, :, None]
+    q = q.to(_dt(dtype))
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(padded), _i32(lens), cu_q=_i32(cu) if new > 1 else None, dist=dist, rope_theta=0,
+                            kscale=kscale)
+    assert sfa.get_device_status() == 0
+    ks, alone, bf16 = float(np.float32(kscale)), 0, dtype == "bf16"
+    # Probabilities are whole f16 steps of 2^-24 at least (fp32 outputs: their second part is), while the largest of a
+    # column is 2^8 or more (bf16 prompts; 2^11 else), and so is the sum: half a step of each key's is 2^-33 (2^-36 for
+    # fp32 outputs) of its value.  It counts where the key that stands out has a zero and the others all but no weight.
+    floor = 2.0 ** (-33 if bf16 else -36)
+    on, ln, qn = o.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    for r, n in enumerate(lens):
+        k, v = stored(cache, table, r, n, page)
+        a, b = cu[r], cu[r + 1]
+        pos = np.arange(n - (b - a), n)
+        wo, wl, av, sz = ref.attend(qn[a:b], k, v, pos, dist, ks, 1.0, None)
+        bo, bl = ref.bounds(wo, wl, av, sz, bf16)
+        for i, p in enumerate(pos):
+            js = np.arange(p + 1) if dist is None else np.array([p - s for s in dist if s <= p])
+            limit = bo[i] + floor * np.repeat(np.abs(v[js]).sum(0), 4, 0)
+            assert (np.abs(on[a + i] - wo[i]) <= limit).all(), (r, i, float((np.abs(on[a + i] - wo[i]) / limit).max()))
+            assert (np.abs(ln[a + i] - wl[i]) <= bl[i]).all(), (r, i)
+            for h in range(Hq):
+                t = k[js, h // 4] * ks @ qn[a + i, h] / 8
+                two = np.sort(t)[-2:]
+                if len(t) > 1 and two[1] - two[0] > 4 * 2.0 ** -18.5 * sz[i, h] + 40:  # the others' weights: below 2^-57
+                    alone += 1
+                    assert np.array_equal(on[a + i, h], v[js[t.argmax()], h // 4])
+    assert alone > 2 * new
