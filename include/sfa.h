@@ -284,8 +284,8 @@ int sfa_decode_int(const sfa_desc* d, const void* q, const void* k_cache, const 
  * stack of unused page ids (its top last).  Index errors found on the device
  * (a page id outside the pool, a length outside the block table, a position
  * outside the RoPE table) are recorded as SFA_ERR_DEVICE_BOUNDS; the row in
- * question is then skipped, or the key in question left out, never read or
- * written out of range.  All entry points only enqueue work, keep no state
+ * question is then skipped (a query row becomes a zero row with lse = -inf), or
+ * the key in question left out, never read or written out of range.  All entry points only enqueue work, keep no state
  * between calls, and may be captured into a graph. */
 typedef struct {
   int32_t n_pages, page, Hkv, D; /* the pool; page: 16, 32, 64 or 128 rows; D = 64; n_pages * page < 2^31,

@@ -983,6 +983,7 @@ static StreamShape stream_shape(const Kv4Args& a, const Plan& p, bool ragged) {
   z.s.lg_rows = ragged ? __builtin_ctz((unsigned)(8 * z.nt / std::min(G, 8 * z.nt))) : 0;
   z.s.items = ragged ? (a.N >> z.s.lg_rows) + a.R : a.R;
   z.s.W = p.W;
+  z.s.limit = (int)(a.rope ? std::min<int64_t>(cap, a.rope_T) : cap);
   z.teams = kSMs * (z.nt == 1 ? kStreamTeams<1> * kStreamCtas<1> : kStreamTeams<4> * kStreamCtas<4>);
   const int64_t units = (int64_t)z.s.items * a.Hkv;
   if (z.nt == kPromptColumns / 8) {  // cuts its work otherwise
@@ -1057,6 +1058,7 @@ int launch_kv4_attend(const Kv4Args& a, const Plan& p, int dtype, void* ws, void
   cudaError_t e;
   StreamShape z = stream_shape(a, p, a.cu_q != nullptr);
   if (z.s.items > 0) {
+    z.s.row_bytes = a.Hq * kD * (dtype == SFA_BF16 ? 2 : 4);
     z.s.part_o = static_cast<float*>(ws);
     z.s.part_ml = reinterpret_cast<float2*>(z.s.part_o + ((size_t)z.slots * kD << (a.lgG + z.s.lg_rows)));
     e = z.nt == kPromptColumns / 8 ? launch_kv4_prompt(a, z.s, dtype, ws, s)

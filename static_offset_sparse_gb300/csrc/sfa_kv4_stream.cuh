@@ -32,6 +32,7 @@ constexpr int kSMs = 152;
 
 struct StreamArgs {
   int32_t items, lg_rows, chunk_tiles, lg_chunk, max_chunks, W;
+  int32_t limit, row_bytes;  // positions that the block table and the RoPE table have room for; bytes of a row of o
   float* part_o;   // [item][KV head][chunk][column][64]
   float2* part_ml; // [item][KV head][chunk][column] (m, l)
 };
@@ -41,17 +42,40 @@ struct Item {
   __device__ __forceinline__ int plast() const { return pfirst + nrows - 1; }
 };
 
+// What is wrong with an item: rows behind the tables' end, which are not among
+// the item's, or before the request's first position.
+struct Bad {
+  int row = 0, rows = 0;  // those behind the end
+  bool any = false;
+  // The status, and the rows behind the end written as rows without keys: by
+  // thread i of n, where `write` says so.
+  __device__ __forceinline__ void settle(const Kv4Args& a, const StreamArgs& s, bool write, int i, int n) const {
+    if (!any) return;
+    record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+    if (!write) return;
+    uint4* const o = reinterpret_cast<uint4*>(static_cast<char*>(a.o) + (int64_t)row * s.row_bytes);
+#pragma unroll 1
+    for (int j = i; j < rows * (s.row_bytes / 16); j += n) o[j] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int j = i; a.lse && j < rows * a.Hq; j += n) a.lse[(int64_t)row * a.Hq + j] = -INFINITY;
+  }
+};
+
 // Item x.  Requests start at item cu_q[r] / rows + r: room for each one's last,
-// shorter item without a scan over the requests.  A request whose positions
-// leave the tables counts as empty: zero rows, and the status says so.
-__device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, int x) {
+// shorter item without a scan over the requests.  Rows whose positions leave the
+// tables are zero rows, and the status says so: those before a request's first
+// position attend nothing, and a request's items end before those behind the
+// tables' end.  CHECK: what is wrong with it goes to bad, for who looks every item
+// over (each CTA as it finds its share, the prompts' join).
+template <bool CHECK>
+__device__ __forceinline__ Item item_check(const Kv4Args& a, const StreamArgs& s, int x, Bad& bad) {
   Item it;
-  int len;
   if (!a.cu_q) {
+    const int len = max(a.seq_lens[x], -1);
     it.r = it.row0 = x;
     it.nrows = 1;
-    len = a.seq_lens[x];
     it.pfirst = len - 1;
+    if (CHECK) bad.any = len < 0 || len > s.limit;
   } else {
     int lo = 0, n = a.R;  // largest r with cu_q[r] / rows + r <= x
     while (n > 1) {
@@ -60,20 +84,24 @@ __device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, i
       lo += le ? half : 0;
       n = le ? n - half : half;
     }
-    const int c = a.cu_q[lo], end = min(a.cu_q[lo + 1], a.N);
+    const int c = a.cu_q[lo], end = min(a.cu_q[lo + 1], a.N), len = max(a.seq_lens[lo], -1);
+    const int past = end - max(len - s.limit, 0);  // the first row behind the tables' end
     it.r = lo;
     it.row0 = c + ((x - lo - (c >> s.lg_rows)) << s.lg_rows);
-    it.nrows = min(1 << s.lg_rows, end - it.row0);
-    if (c < 0 || it.row0 < c || it.nrows <= 0) {
+    it.nrows = min(1 << s.lg_rows, past - it.row0);
+    it.pfirst = len - (end - it.row0);
+    const bool none = c < 0 || it.row0 < c;
+    if (CHECK && !none) {
+      bad.row = max(it.row0, past);
+      bad.rows = max(min(it.row0 + (1 << s.lg_rows), end) - bad.row, 0);
+      bad.any = bad.rows > 0 || (it.nrows > 0 && it.pfirst < 0);
+    }
+    if (none || it.nrows <= 0) {
       it.nrows = it.nch = it.pfirst = it.c0 = 0;
       return it;
     }
-    len = a.seq_lens[lo];
-    it.pfirst = len - (end - it.row0);
   }
-  const bool empty = !a.cu_q && len == 0;
-  if (empty || it.pfirst < 0 || it.pfirst > (a.max_pages << a.lgS) - it.nrows || (a.rope && it.pfirst > a.rope_T - it.nrows)) {
-    if (!empty) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+  if (it.plast() < 0 || it.pfirst >= s.limit) {  // no row has a position
     it.pfirst = -it.nrows;
     it.c0 = 0;
     it.nch = 1;
@@ -83,6 +111,10 @@ __device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, i
   it.c0 = max(0, it.pfirst - s.W) >> lg;
   it.nch = (it.plast() >> lg) - it.c0 + 1;
   return it;
+}
+__device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, int x) {
+  Bad bad;
+  return item_check<false>(a, s, x, bad);
 }
 
 // What a chunk costs a team besides its tiles (its last ones' odd share among four
@@ -170,7 +202,9 @@ __device__ __forceinline__ bool find_run(const Kv4Args& a, const StreamArgs& sa,
     int at = before;
 #pragma unroll 1
     for (int x = x0; x < x1; ++x) {
-      const Item it = item_at(a, sa, x);
+      Bad bad;
+      const Item it = item_check<true>(a, sa, x, bad);
+      bad.settle(a, sa, blockIdx.x == 0, 0, 1);
       const int wt = run_weight(sa, it), end = at + wt * a.Hkv;
       if (pass > 0 && end > begin(b0) && at < begin(b0 + TEAMS)) {
 #pragma unroll 1

@@ -274,3 +274,47 @@ def test_attend_large_queries(sfa, dtype, new, width, dist, kscale):
                     alone += 1
                     assert np.array_equal(on[a + i, h], v[js[t.argmax()], h // 4])
     assert alone > 2 * new
+
+
+# ------------------------------------------------------------------ rows out of range among rows in range
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,new,width,dist", [(8, 2, 3, 90, [0, 1, 7, 200]), (8, 2, 9, 40, None), (8, 2, 2, 300, None), (8, 2, 4, 300, None),
+                                                   (8, 2, 7, 300, None), (32, 1, 2, 300, list(range(600))), (8, 2, 70, 40, None),
+                                                   (8, 2, 70, 90, list(range(70))), (2, 2, 600, 300, [0, 3])])
+@pytest.mark.parametrize("kind", ["rope", "table", "short"])
+def test_attend_skips_only_the_bad_rows(sfa, dtype, Hq, Hkv, new, width, dist, kind):
+    """Rows behind the RoPE table's or the block table's end, or before the request's first: zero rows and the
+    status; the others of the request, and of other requests, as ever (gather, cluster, stream with one to four
+    column tiles, prompts)."""
+    import torch
+
+    rng = np.random.default_rng(61)
+    page, cap = 32, 32 * width
+    lens = [cap, 900, 40]
+    cache, table = make_cache(rng, lens, page, Hkv)
+    table = np.ascontiguousarray(table[:, :width])
+    cu = np.array([0, new, 2 * new, 2 * new + min(new, 40)])
+    told, lost = list(lens), {0: 0, 1: 0, 2: 0}  # what the call is told; rows that are lost at a request's end (or begin)
+    cs = ref.rope(cap)
+    if kind == "rope":
+        cs, lost[0] = cs[:cap - 1], 1
+    elif kind == "table":
+        told[0], lost[0] = cap + new - 1, new - 1
+    else:
+        told[1], lost[1] = new - 1, -1
+    q = torch.from_numpy(rng.standard_normal((cu[-1], Hq, 64))).to(_dt(dtype))
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(told), cu_q=_i32(cu), dist=dist, rope=_cuda(cs))
+    assert sfa.get_device_status() == 6
+    o, lse, qn = o.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    for r in range(3):
+        k, v = stored(cache, table, r, lens[r], page)
+        rows = np.arange(cu[r], cu[r + 1])
+        pos = told[r] - len(rows) + np.arange(len(rows))
+        fine = (pos >= 0) & (pos < len(cs))
+        assert (~fine).sum() == abs(lost[r]) and fine.any()
+        assert not o[rows[~fine]].any() and np.isneginf(lse[rows[~fine]]).all()
+        wo, wl, av, sz = ref.attend(qn[rows[fine]], k, v, pos[fine], dist, 1.0, 1.0, cs)
+        bo, bl = ref.bounds(wo, wl, av, sz, dtype == "bf16")
+        assert (np.abs(o[rows[fine]] - wo) <= bo).all() and (np.abs(lse[rows[fine]] - wl) <= bl).all(), r
