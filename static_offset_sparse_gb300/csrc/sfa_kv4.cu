@@ -508,6 +508,7 @@ static int check_attend(const sfa_kv4_desc* d, Plan* p, Kv4Args* a) {
   if (rc != SFA_OK) return rc;
   if (d->R < 0 || (d->R == 0 && d->N > 0) || d->max_pages <= 0 || d->Hq <= 0) return SFA_ERR_INVALID_ARG;
   if ((int64_t)d->max_pages * d->page > (1 << 24) || d->Hq % d->Hkv) return SFA_ERR_UNSUPPORTED;
+  if ((int64_t)d->N + d->R > INT32_MAX) return SFA_ERR_UNSUPPORTED;  // (their items are counted in 32 bits)
   const int G = d->Hq / d->Hkv;
   if (G > 32 || (G & (G - 1)) || (int64_t)d->N * d->Hq > (1LL << 31) - 1) return SFA_ERR_UNSUPPORTED;
   if (d->dist) {

@@ -190,3 +190,11 @@ def test_only_rope_tables_are_read_as_read_only_data():
     assert len(reads) >= 5
     for name, text in reads:
         assert "rope" in text, (name, text)
+
+
+@pytest.mark.parametrize("R,N", [(2 ** 31 - 1, 3), (2 ** 31 - 1, 1 << 20), (2 ** 31 - 100, 101)])
+def test_requests_beyond_32_bits(sfa_lib, R, N):
+    """Rows and requests whose number passes 32 bits are refused, not counted from below zero."""
+    n = C.c_size_t(0)
+    assert sfa_lib.sfa_kv4_workspace_size(_desc(R=R, N=N, max_pages=4096), C.byref(n)) == 2
+    assert sfa_lib.sfa_kv4_attend(_desc(R=R, N=N, max_pages=4096), P, P, P, P, P, P, P, None, 0, None) == 2
