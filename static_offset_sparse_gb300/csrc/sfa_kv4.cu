@@ -487,6 +487,11 @@ static int check_pool(const sfa_kv4_desc* d) {
   return SFA_OK;
 }
 
+// Below 128 GiB: rows of 32 bytes are counted in 32 bits.
+static bool cache_fits(const sfa_kv4_desc* d, int Hkv) {
+  return (int64_t)d->n_pages * d->page <= ((1LL << 37) - 1) / kKv4Row / Hkv;
+}
+
 // What append, read and attend share.
 static int check_rows(const sfa_kv4_desc* d) {
   const int rc = check_pool(d);
@@ -494,7 +499,7 @@ static int check_rows(const sfa_kv4_desc* d) {
   if (d->Hkv <= 0 || (d->dtype != SFA_F32 && d->dtype != SFA_BF16)) return SFA_ERR_INVALID_ARG;
   if (!(d->kscale > 0.0f && d->kscale <= 3.4e38f && d->vscale > 0.0f && d->vscale <= 3.4e38f)) return SFA_ERR_INVALID_ARG;
   if (d->D != kD || (int64_t)d->N * d->Hkv > (1 << 27)) return SFA_ERR_UNSUPPORTED;
-  if ((int64_t)d->n_pages * d->page > ((1LL << 37) - 1) / kKv4Row / d->Hkv) return SFA_ERR_UNSUPPORTED;  // rows of 32 bytes in 32 bits
+  if (!cache_fits(d, d->Hkv)) return SFA_ERR_UNSUPPORTED;
   if (d->rope && (d->rope_T <= 0 || !at16(d->rope))) return SFA_ERR_INVALID_ARG;
   return SFA_OK;
 }
@@ -553,8 +558,10 @@ int sfa_kv4_cache_bytes(int32_t n_pages, int32_t page, int32_t Hkv, size_t* byte
   d.page = page;
   if (!bytes || Hkv <= 0) return SFA_ERR_INVALID_ARG;
   const int rc = check_pool(&d);
-  if (rc == SFA_OK) *bytes = (size_t)n_pages * Hkv * page * kKv4Row;
-  return rc;
+  if (rc != SFA_OK) return rc;
+  if (!cache_fits(&d, Hkv)) return SFA_ERR_UNSUPPORTED;
+  *bytes = (size_t)n_pages * Hkv * page * kKv4Row;
+  return SFA_OK;
 }
 
 int sfa_kv4_plan(const sfa_kv4_desc* d, const int32_t* n_new, const int32_t* seq_lens,

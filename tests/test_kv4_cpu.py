@@ -198,3 +198,13 @@ def test_requests_beyond_32_bits(sfa_lib, R, N):
     n = C.c_size_t(0)
     assert sfa_lib.sfa_kv4_workspace_size(_desc(R=R, N=N, max_pages=4096), C.byref(n)) == 2
     assert sfa_lib.sfa_kv4_attend(_desc(R=R, N=N, max_pages=4096), P, P, P, P, P, P, P, None, 0, None) == 2
+
+
+@pytest.mark.parametrize("n_pages,page,Hkv,rc", [(1 << 20, 128, 14, 0), (1 << 20, 128, 15, 2), (1 << 24, 16, 8, 2), (3, 16, 1 << 24, 0), (3, 16, 1 << 30, 2)])
+def test_cache_bytes_of_caches_that_are_too_large(sfa_lib, n_pages, page, Hkv, rc):
+    """A cache that every other call would refuse has no size (128 GiB and more)."""
+    n = C.c_size_t(0)
+    assert sfa_lib.sfa_kv4_cache_bytes(n_pages, page, Hkv, C.byref(n)) == rc
+    assert sfa_lib.sfa_kv4_append(_desc(n_pages=n_pages, page=page, Hkv=Hkv, N=0, k_stride=64 * Hkv % 2 ** 31, v_stride=64 * Hkv % 2 ** 31), P, P, P, P, P, None) == rc
+    if rc == 0:
+        assert n.value == 72 * n_pages * page * Hkv < 2 ** 37
