@@ -32,6 +32,7 @@ _U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 _MAX = 3.4e38  # of the stored numbers' scales
 # the bytes of _lib.Kv4Desc (0.2 us; filling in the structure takes 0.8)
 _desc = struct.Struct("9i4x3q2fPi4xPi4x").pack
+_OFFSETS: dict = {}
 _current_device = torch.cuda.current_device
 # the current stream's handle: the direct getter takes 0.1 us, the Stream object 2
 _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -131,10 +132,17 @@ def _made_rope(rope_theta, cache, t, axis):
     return page and _ROPE_CACHE.get((t.shape[axis] * page, float(rope_theta), cache.get_device()))
 
 
-@functools.lru_cache(maxsize=64)
 def _offsets(dist: tuple):
-    arr, n = i32_array(dist)
-    return C.addressof(arr), n, arr
+    """Address, number and array of host offsets, kept by the values of Python ints."""
+    found = _OFFSETS.get(dist)
+    if found is None:
+        arr, n = i32_array(dist)
+        found = C.addressof(arr), n, arr
+        if all(type(s) is int for s in dist):  # (a tensor's element is found by its identity, whatever it holds now)
+            if len(_OFFSETS) >= 64:
+                _OFFSETS.clear()
+            _OFFSETS[dist] = found
+    return found
 
 
 @functools.cache

@@ -208,3 +208,19 @@ def test_cache_bytes_of_caches_that_are_too_large(sfa_lib, n_pages, page, Hkv, r
     assert sfa_lib.sfa_kv4_append(_desc(n_pages=n_pages, page=page, Hkv=Hkv, N=0, k_stride=64 * Hkv % 2 ** 31, v_stride=64 * Hkv % 2 ** 31), P, P, P, P, P, None) == rc
     if rc == 0:
         assert n.value == 72 * n_pages * page * Hkv < 2 ** 37
+
+
+def test_offset_lists_are_kept_by_value():
+    """Offsets in tensors may change between calls; lists of Python ints are converted once."""
+    torch = pytest.importorskip("torch")
+    from static_offset_sparse_gb300 import kv4
+
+    dist = [torch.tensor(0), torch.tensor(3)]
+    assert list(kv4._offsets(tuple(dist))[2]) == [0, 3]
+    dist[1].fill_(5)
+    assert list(kv4._offsets(tuple(dist))[2]) == [0, 5]
+    assert kv4._offsets((0, 1, 7)) is kv4._offsets((0, 1, 7)) and list(kv4._offsets((0, 1, 7))[2]) == [0, 1, 7]
+    assert list(kv4._offsets(tuple(np.array([0, 1, 7])))[2]) == [0, 1, 7]
+    for i in range(200):  # a bounded number of them
+        assert kv4._offsets((0, i + 1))[1] == 2
+    assert len(kv4._OFFSETS) <= 64
