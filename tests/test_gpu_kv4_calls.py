@@ -318,3 +318,90 @@ def test_attend_skips_only_the_bad_rows(sfa, dtype, Hq, Hkv, new, width, dist, k
         wo, wl, av, sz = ref.attend(qn[rows[fine]], k, v, pos[fine], dist, 1.0, 1.0, cs)
         bo, bl = ref.bounds(wo, wl, av, sz, dtype == "bf16")
         assert (np.abs(o[rows[fine]] - wo) <= bo).all() and (np.abs(lse[rows[fine]] - wl) <= bl).all(), r
+
+
+# ------------------------------------------------------------------ batches that keep every team busy for several chunks
+
+
+def _shared_pages(rng, lens, page, H, width, P=61):
+    """A small pool whose pages many requests share, rows quantised normal numbers; block tables of `width` pages."""
+    x = (rng.standard_normal((2, P, page, H, 64)) * np.exp(0.5 * rng.standard_normal((2, 1, 1, H, 64)))).astype(np.float32)
+    parts = []
+    for codes, scales in (ref.quantise(x[0]), ref.quantise(x[1])):
+        parts.append(((codes[..., 0::2] | codes[..., 1::2] << 4), scales))
+    flat = lambda a: a.transpose(0, 2, 1, 3).reshape(P, H, -1)  # noqa: E731
+    cache = np.concatenate([flat(parts[0][0]), flat(parts[1][0]), flat(np.concatenate([parts[0][1], parts[1][1]], -1))], -1)
+    table = rng.integers(0, P, (len(lens), width)).astype(np.int32)
+    for r, n in enumerate(lens):
+        table[r, -(-n // page):] = -1
+    return np.ascontiguousarray(cache.astype(np.uint8)), table
+
+
+BATCHES = [  # R, most rows, block table rows, Hq, Hkv, page, new rows of a request (None: one), what it reaches
+    (300, 6000, 6000, 8, 2, 64, None),  # eight columns: several chunks a team, their sums in both buffers, join of many columns
+    (700, 3000, 6016, 4, 4, 32, None),  # more requests than threads, chunks of 1024 and more
+    (150, 2000, 2048, 8, 2, 16, None),  # one chunk a request
+    (200, 4000, 5000, 16, 1, 64, None),  # two column tiles
+    (100, 3000, 4000, 8, 2, 32, (2, 4)),  # the same from rows
+    (90, 3000, 4000, 8, 2, 64, (4, 8)),  # four column tiles, queries in shared memory for two KV heads
+    (90, 3000, 4000, 32, 1, 128, None),  # the same from heads
+    (300, 2000, 2048, 16, 2, 64, (2, 4)),  # the same in one chunk
+    (500, 300, 512, 8, 2, 16, (20, 40)),  # prompts: more items than threads, units that end inside a CTA's share
+    (40, 3000, 4096, 8, 2, 64, (9, 130)),  # prompts: units over several CTAs
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", range(len(BATCHES)))
+@pytest.mark.parametrize("window", [None, 700])
+def test_attend_large_batches(sfa, dtype, case, window):
+    """Enough requests that the teams walk over several chunks, requests and heads each."""
+    import torch
+
+    R, most, rows, Hq, Hkv, page, new = BATCHES[case]
+    rng = np.random.default_rng(70 + case)
+    least = new[1] if new else 1
+    lens = [int(x) for x in np.exp(rng.uniform(np.log(least), np.log(most + 1), R))]
+    lens[3], lens[R // 2], lens[-1] = most, 0 if new is None else least, most
+    news = [int(x) for x in rng.integers(new[0], new[1] + 1, R)] if new else [1] * R
+    cache, table = _shared_pages(rng, lens, page, Hkv, -(-rows // page))
+    cu = np.concatenate([[0], np.cumsum(news)])
+    q = torch.from_numpy(1.5 * rng.standard_normal((cu[-1], Hq, 64))).to(_dt(dtype))
+    cs = ref.rope(rows)
+    dist = None if window is None else list(range(window))
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), cu_q=_i32(cu) if new else None, dist=dist, rope=_cuda(cs))
+    assert sfa.get_device_status() == 0
+    o, lse, qn = o.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    picked = set(rng.choice(R, min(R, max(8, 1500 // (Hq * max(news)))), replace=False)) | {3, R // 2, R - 1}
+    for r in sorted(picked):
+        a, b, n = cu[r], cu[r + 1], lens[r]
+        if n == 0:
+            assert not o[a:b].any() and np.isneginf(lse[a:b]).all()
+            continue
+        k, v = stored(cache, table, r, n, page)
+        wo, wl, av, sz = ref.attend(qn[a:b], k, v, np.arange(n - (b - a), n), dist, 1.0, 1.0, cs)
+        bo, bl = ref.bounds(wo, wl, av, sz, dtype == "bf16")
+        assert (np.abs(o[a:b] - wo) <= bo).all() and (np.abs(lse[a:b] - wl) <= bl).all(), (r, float((np.abs(o[a:b] - wo) / bo).max()))
+    assert np.isfinite(o).all() and not np.isnan(lse).any()
+
+
+@pytest.mark.parametrize("Hq,Hkv,dtype", [(8, 2, "f32"), (8, 2, "bf16"), (16, 1, "bf16"), (32, 1, "f32")])
+def test_rows_of_a_large_batch_are_their_own(sfa, Hq, Hkv, dtype):
+    """One row a request, hundreds of them: a row's bits stay whatever the other requests' lengths make of the
+    shares of work, over calls and runs."""
+    import torch
+
+    rng = np.random.default_rng(81)
+    R, page, rows = 300, 64, 6016
+    lens = [int(x) for x in rng.integers(1, rows, R)]
+    cache, table = _shared_pages(rng, [rows] * R, page, Hkv, rows // page)
+    q = torch.from_numpy(rng.standard_normal((R, Hq, 64))).to(_dt(dtype)).cuda()
+    args, rope = (_cuda(cache), _cuda(table)), _cuda(ref.rope(rows))
+    o, lse = sfa.kv4_attend(q, *args, _i32(lens), rope=rope)
+    for turn in range(4):
+        kept = rng.random(R) < (1.0, 0.5, 0.1, 0.02)[turn]
+        other = [n if keep else int(rng.integers(0, rows)) for n, keep in zip(lens, kept)]
+        o2, l2 = sfa.kv4_attend(q, *args, _i32(other), rope=rope)
+        same = torch.from_numpy(np.array(other) == np.array(lens)).cuda()
+        assert same.any() and torch.equal(o[same], o2[same]) and torch.equal(lse[same], l2[same])
+    assert sfa.get_device_status() == 0
