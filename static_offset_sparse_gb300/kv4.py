@@ -193,8 +193,10 @@ def kv4_plan(n_new, seq_lens, block_table, free_pages, n_free, *, page: int, row
     ids) are updated in place.  rows: the capacity of the row maps.  Returns
     cu_q [R + 1], slots [rows], pos [rows], and the lengths and the number of
     free pages after the step (seq_lens_out=seq_lens and n_free_out=n_free
-    update those in place, as a captured step wants).  A step that does not fit
-    changes nothing and sets the device status."""
+    update those in place, as a captured step wants).  What is not given is made
+    as slices of one allocation: keeping or saving one of them keeps or saves
+    all (clone what should live on alone).  A step that does not fit changes
+    nothing and sets the device status."""
     fast = _native()
     if fast is not None:
         r = fast.plan(n_new, seq_lens, block_table, free_pages, n_free, page, rows, seq_lens_out, n_free_out)
