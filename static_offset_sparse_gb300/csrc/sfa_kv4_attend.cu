@@ -254,8 +254,8 @@ constexpr uint32_t kNone = 0xffffffffu;
 // PACK: 8 / G consecutive rows share a warp's columns.  Their keys follow one
 // another in the tiles, and a key of another row counts as absent: what a row
 // costs besides its keys (its query, its outputs) is paid once for all of them,
-// and tiles fill up (7807 rows of 19 keys, 8 / 2 heads: 29 us a row a warp, 25
-// so; 12800 rows, 4 / 4 heads: 82 and 43).
+// and tiles fill up (7807 rows of 19 keys, 8 / 2 heads: 28 us a row a warp, 24
+// so; 12800 rows, 4 / 4 heads: 84 and 49).
 //
 // CLUSTER: a (row, KV head) is a cluster of 8 CTAs, 32 warps, whose results meet
 // through distributed shared memory: a few rows over some thousands of keys in
@@ -555,8 +555,13 @@ static cudaError_t gather_any(const Kv4Args& a, const Plan& p, cudaStream_t s) {
   GatherRows gr = {1, (int)keys, 0};
   if (clustered(a, keys)) return gather_nt<TIO, kCluster>(a, p, kGatherWarps, gr, s);
   // up to a wave of warps: a row's keys go round several, for its latency; beyond, what counts is work
-  const bool many = units > kSMs * 5 * kGatherWarps;
-  if (G < 8 && many && keys <= 4096) {
+  const int64_t wave = kSMs * 5 * kGatherWarps;
+  const bool many = units > wave;
+  // Rows side by side while that leaves more than a wave of warps' work, up to 128 keys (16000 rows of 19, 97,
+  // 193 keys, 8 / 2 heads: 46 us and 59 a row a warp, 118 and 125, 206 and 201; 2 / 2 heads 33 and 56, 111 and
+  // 121, 215 and 196); below it, where few warps end the call, up to 16 (3200 rows of 9, 33, 129 keys: 12.0 and
+  // 13.1, 18.6 and 18.4, 43 and 36; 2 / 2 heads 11.6 and 12.4, 23 and 18, 68 and 35)
+  if (G < 8 && many && keys <= (units * G / 8 * 4 > 5 * wave ? 128 : 16)) {
     gr.rows = 8 / G;
     gr.keys = std::max(2, gr.keys);  // (2^32 / 1 would not fit)
     gr.magic = (uint32_t)(((1ull << 32) + gr.keys - 1) / gr.keys);  // exact up to 8 * 4096 keys

@@ -405,3 +405,50 @@ def test_rows_of_a_large_batch_are_their_own(sfa, Hq, Hkv, dtype):
         same = torch.from_numpy(np.array(other) == np.array(lens)).cuda()
         assert same.any() and torch.equal(o[same], o2[same]) and torch.equal(lse[same], l2[same])
     assert sfa.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,rows,dist", [(16, 4, 2000, FIB), (8, 8, 3900, list(range(0, 80, 2))), (8, 4, 3900, list(range(50)) + list(range(60, 216, 2))),
+                                              (16, 4, 2000, list(range(0, 260, 2)))])
+def test_attend_many_rows_side_by_side(sfa, dtype, Hq, Hkv, rows, dist):
+    """Rows enough that several share a warp's columns over some tiles of keys each (and, with 130 keys, that they do
+    not): requests of one row and of hundreds, a stored NaN value among them, rows behind the last."""
+    import torch
+
+    rng = np.random.default_rng(91)
+    page, G = 16, Hq // Hkv
+    news = [1, 700, 2, 1, 333, 5]
+    news.append(rows - sum(news))
+    lens = [int(n + x) for n, x in zip(news, rng.integers(0, 400, len(news)))]
+    cache, table = _shared_pages(rng, lens, page, Hkv, -(-max(lens) // page), P=300)
+    table[1] = np.where(table[1] >= 0, rng.permutation(300)[:1].repeat(table.shape[1]) % 7 + 290, -1)  # pages of its own
+    for r in range(len(lens)):
+        if r != 1:
+            table[r] = np.where(table[r] >= 290, table[r] - 290, table[r])
+    own = int(table[1, 0])
+    cache[own, 0, 64 * page + 8 * 3 + 5] = 127  # row 3 of the page that request 1 repeats: KV head 0, dims 16 .. 31
+    cu = np.concatenate([[0], np.cumsum(news)])
+    q = torch.from_numpy(rng.standard_normal((rows + 9, Hq, 64))).to(_dt(dtype))
+    cs = ref.rope(table.shape[1] * page)
+    o = torch.full(tuple(q.shape), 3.0, dtype=_dt(dtype), device="cuda")
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), cu_q=_i32(cu), dist=dist, rope=_cuda(cs), o=o)
+    assert sfa.get_device_status() == 0 and (o[rows:] == 3).all()
+    o, lse, qn = o.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    clean = cache.copy()
+    clean[own, 0, 64 * page + 8 * 3 + 5] = 0
+    for r, n in enumerate(lens):
+        a, b = cu[r], cu[r + 1]
+        if b - a > 700:  # a part of the longest
+            a = b - 400
+        k, v = stored(clean, table, r, n, page)
+        pos = np.arange(n - (b - a), n)
+        wo, wl, av, sz = ref.attend(qn[a:b], k, v, pos, dist, 1.0, 1.0, cs)
+        bo, bl = ref.bounds(wo, wl, av, sz, dtype == "bf16")
+        if r == 1:
+            hit = np.array([any((p - s) % page == 3 for s in dist if s <= p) for p in pos])
+            nan = np.zeros(wo.shape, bool)
+            nan[hit, :G, 16:32] = True
+            assert np.array_equal(np.isnan(o[a:b]), nan)
+            wo[nan] = 0
+            o[a:b][nan] = 0
+        assert (np.abs(o[a:b] - wo) <= bo).all() and (np.abs(lse[a:b] - wl) <= bl).all(), r
