@@ -85,8 +85,11 @@ __device__ __forceinline__ int item_steps(const StreamArgs& s, const Item& it) {
 
 // What a piece costs besides its steps (its queries, its first logits, its
 // outputs), in steps: the CTA where a unit begins has it in its share.  Without
-// it the CTAs with more pieces ran a quarter longer than the average (8 prompts
-// over 2048 to 16384 rows: 110 us with 0, 98 with 3, 95 with 6).
+// it the CTAs with more pieces ran a quarter longer than the average.  0, 3, 6,
+// 10, 16: 8 prompts of 300 to 700 rows over 2048 to 16384 141, 125, 119, 123, 130
+// us; 30 of 50 to 200 over up to 4000 89, 58, 57.5, 61, 62; 500 of 20 to 40 over
+// up to 1500 201, 164, 161, 162, 171; 64 of 12 over up to 20000 139, 131, 128,
+// 133, 139.
 constexpr int kUnitCost = 6;
 __device__ __forceinline__ int item_weight(const StreamArgs& s, const Item& it) {
   const int n = item_steps(s, it);

@@ -117,10 +117,14 @@ __device__ __forceinline__ Item item_at(const Kv4Args& a, const StreamArgs& s, i
   return item_check<false>(a, s, x, bad);
 }
 
-// What a chunk costs a team besides its tiles (its last ones' odd share among four
-// warps, their meeting), in tiles.  Without it the teams with more and shorter
-// chunks ended last (128 requests of 1024 to 32768 rows: 53 us with 0, 50 with 8,
-// 49 with 24 and 32; 20 of 5000 to 9000: 16.3, 16.5, 15.0).
+// What a chunk counts for besides its tiles, in tiles, when the shares are made:
+// its four warps' odd tiles, their meeting, and that shares end at whole chunks.
+// Not one of these measured by itself: with 0 the teams with more and shorter
+// chunks ended last, and any number from 8 to 48 evens the shares out about as
+// well.  0, 8, 16, 24, 48: 128 requests of 1024 to 32768 rows 86.4, 86.1, 84.5,
+// 84.5, 84.3 us; 300 of 100 to 6000 48.5, 46.1, 46.3, 46.1, 46.0; 700 of up to
+// 3000 62.7, 57.6, 58.0, 57.7, 59.8; 64 of 4 to 8 rows over up to 20000 97.7,
+// 94.8, 93.3, 93.2, 93.0; one of 400001 27.1, 26.7, 26.8, 26.7, 26.8.
 constexpr int kChunkCost = 24;
 
 // A place in a team's run of chunks: chunk c of (item x, KV head h), its tiles
