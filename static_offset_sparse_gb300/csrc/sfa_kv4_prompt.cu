@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(kPThreads, 1) kv4_prompt_kernel(const Kv4Args 
           for (int e = 0; e < 16; ++e) o[e] = __int_as_float(0x7fffffff);
         if (!mine) {
         } else if (whole) {
-          write_head<TIO>(a, out_row, head, c / 8, o, m + (kPShift - kPromptShift<sizeof(TIO) == 4>), l);
-          write_head<TIO>(a, out_row, head, c / 8 + 1, o + 8, m + (kPShift - kPromptShift<sizeof(TIO) == 4>), l);
+          write_head<TIO>(a, out_row, head, c / 8, o, m, l, kPromptShift<kExact>);
+          write_head<TIO>(a, out_row, head, c / 8 + 1, o + 8, m, l, kPromptShift<kExact>);
         } else {
           store8(parts.o + at * kD + c, o);
           store8(parts.o + at * kD + c + 8, o + 8);
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(256) kv4_prompt_join_kernel(const Kv4Args a, c
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], f, y[e]);
   }
-  write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M + (kPShift - kPromptShift<sizeof(TIO) == 4>), l);
+  write_head<TIO>(a, it.row0 + (col >> a.lgG), h * G + (col & (G - 1)), d, y, M, l, kPromptShift<sizeof(TIO) == 4>);
 }
 
 static constexpr size_t kPartBytes = (size_t)2 * kSMs * kPromptColumns * (kD + 2) * sizeof(float);

@@ -15,16 +15,18 @@ namespace sfa {
 // nearest, one of 2^26 would let 2^19 through.)
 constexpr float kPShift = 11.0f, kLag = 4.0f;
 
-// One head's output row (dims 8g .. 8g + 7 of lane (g, t)) and log-sum-exp.
-// l = 0: no keys, a zero row and -inf.
+// One head's output row (dims 8g .. 8g + 7 of lane (g, t)) and log-sum-exp, of
+// sums of 2^(logit + (shift - m)), the difference rounded downwards as it was
+// there.  l = 0: no keys, a zero row and -inf.
 template <typename TIO>
-__device__ __forceinline__ void write_head(const Kv4Args& a, int64_t n, int head, int g, const float* x, float m, float l) {
+__device__ __forceinline__ void write_head(const Kv4Args& a, int64_t n, int head, int g, const float* x, float m, float l,
+                                           float shift = kPShift) {
   float y[8];
   const float inv = l == 0.0f ? 0.0f : a.vscale / l;
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = l == 0.0f ? 0.0f : x[e] * inv;
   store8(static_cast<TIO*>(a.o) + (n * a.Hq + head) * kD + 8 * g, y);
-  if (a.lse && g == 0) a.lse[n * a.Hq + head] = l == 0.0f ? -INFINITY : (m - kPShift) * kLn2 + logf(l);
+  if (a.lse && g == 0) a.lse[n * a.Hq + head] = l == 0.0f ? -INFINITY : __fsub_ru(m, shift) * kLn2 + logf(l);
 }
 
 constexpr int kTile = 64, kTileBytes = kTile * kKv4Row;

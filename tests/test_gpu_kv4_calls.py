@@ -276,6 +276,34 @@ def test_attend_large_queries(sfa, dtype, new, width, dist, kscale):
     assert alone > 2 * new
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,width,dist", [(1, 4, [0, 1]), (1, 300, None), (3, 300, None), (40, 30, None)])
+def test_lse_of_few_small_logits(sfa, dtype, new, width, dist):
+    """Thousands of log-sum-exps of a few logits near zero, where the largest terms cancel: within the bound, and
+    without a bias (an eighth of it)."""
+    import torch
+
+    rng = np.random.default_rng(53)
+    R, page = 400, 16
+    lens = [int(x) for x in rng.integers(new, new + 4, R)]
+    cache, table = _shared_pages(rng, lens, page, 2, width)
+    cu = np.arange(R + 1) * new
+    q = torch.from_numpy(0.3 * rng.standard_normal((R * new, 8, 64))).to(_dt(dtype))
+    o, lse = sfa.kv4_attend(q.cuda(), _cuda(cache), _cuda(table), _i32(lens), cu_q=_i32(cu) if new > 1 else None, dist=dist, rope_theta=0,
+                            kscale=0.01)
+    assert sfa.get_device_status() == 0
+    ln, qn, off = lse.double().cpu().numpy(), q.double().numpy(), []
+    for r, n in enumerate(lens):
+        k, v = stored(cache, table, r, n, page)
+        a, b = cu[r], cu[r + 1]
+        wo, wl, av, sz = ref.attend(qn[a:b], k, v, np.arange(n - new, n), dist, float(np.float32(0.01)), 1.0, None)
+        bl = ref.bounds(wo, wl, av, sz, dtype == "bf16")[1]
+        off.append(((ln[a:b] - wl) / bl).ravel())
+    off = np.concatenate(off)
+    assert np.abs(off).max() <= 1, float(np.abs(off).max())
+    assert abs(off.mean()) <= 1 / 8, float(off.mean())
+
+
 # ------------------------------------------------------------------ rows out of range among rows in range
 
 
