@@ -348,15 +348,18 @@ int sfa_kv4_read(const sfa_kv4_desc* d, const void* cache, const int32_t* slots,
 /* Attention of N query rows over their requests' cached rows.
  *   q        N rows of [Hq, 64], unrotated
  *   seq_lens [R]      stored rows of each request, the queries' own included
- *   cu_q     [R + 1]  request r's queries are rows cu_q[r] .. cu_q[r + 1] - 1 and stand at its
- *                     last positions, in order; rows from cu_q[R] on are left untouched.  NULL
+ *   cu_q     [R + 1]  0 first, not decreasing, N at most: request r's queries are rows
+ *                     cu_q[r] .. cu_q[r + 1] - 1 and stand at its last positions, in order;
+ *                     rows from cu_q[R] on are left untouched.  NULL
  *                     (N = R): row r is request r's last position; a request of length 0 gives
  *                     a zero row and lse = -inf
  *   o        [N, Hq, 64]  d->dtype
  *   lse      fp32 [N, Hq], natural log of the softmax denominator, or NULL
  * A query at position p attends the rows j <= p (d->dist NULL), or p - s for
  * every s <= p of d->dist (which holds 0 and nothing negative); logits are
- * q . k / 8 after the rotation of q at p by d->rope.  A NaN that is stored
+ * q . k / 8 after the rotation of q at p by d->rope.  For bf16 outputs the
+ * probabilities enter the values' product in f16 (2^-12 of each, and nothing
+ * below 2^-33 of the largest), for fp32 outputs in two such parts.  A NaN that is stored
  * reaches the rows that attend it and no others; rows of a page behind
  * seq_lens may hold anything.  o and lse overlap no input.  What is added in
  * which order depends on the shapes and the row's own request; from 33 query
