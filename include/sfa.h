@@ -372,6 +372,81 @@ int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
                    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, void* o,
                    float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- attention to states of another length ---------------------------
+ *
+ * Cross attention: the queries of one sequence (a decoder's) over the keys and
+ * values of another (an encoder's states), every key for every query, no
+ * rotation.  For query head h, its KV head g = h / (Hq / Hkv):
+ *   s_ij = q_i . k_j / 8 for j < kv_len[b];  o_i = sum_j softmax(s_i)_j v_j
+ *   q, o, dO, dq  [B, Hq, Tq, 64]    k, v, dk, dv  [B, Hkv, Tk, 64]
+ *   lse           fp32 [B, Hq, Tq], natural log of the softmax denominator
+ * q, k and v may be strided (the 64 numbers of a row are dense); all other
+ * tensors are contiguous.  A query at or behind q_len[b], and every query of a
+ * sequence with kv_len[b] = 0, gives a zero row with lse = -inf and has no part in
+ * any gradient; gradients behind the lengths are zeros.  What stands in q, k, v,
+ * o, lse and dO behind the lengths may be anything, NaN too.  A length outside
+ * [0, Tq] or [0, Tk] counts as 0 and is recorded as SFA_ERR_DEVICE_BOUNDS.
+ * Hq / Hkv <= 32 (any whole number); Tq, Tk <= 2^24; B Hq Tq and B Hkv Tk below
+ * 2^30.  Calls only enqueue work, keep no state, and may be captured. */
+typedef struct {
+  int32_t B, Tq, Tk, Hq, Hkv, D; /* D = 64 */
+  int32_t dtype;                 /* sfa_dtype of all tensors but lse */
+  /* elements between sequences, heads and rows: multiples of 16 bytes, 64 at
+   * least, below 2^38 (one whose dimension is 1 is not looked at) */
+  int64_t q_stride[3], k_stride[3], v_stride[3];
+  const int32_t* q_len;  /* device [B], or NULL: Tq each */
+  const int32_t* kv_len; /* device [B], or NULL: Tk each */
+} sfa_cross_desc;
+
+/* Bytes of ws for a call with this description (forward: 0 if it needs none). */
+int sfa_cross_workspace_size(const sfa_cross_desc* d, int backward, size_t* bytes);
+
+/* Writes o and, if not NULL, lse. */
+int sfa_cross_forward(const sfa_cross_desc* d, const void* q, const void* k, const void* v, void* o,
+                      float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Writes dq, dk and dv from the forward's o and lse and the upstream gradient dO.
+ * dk and dv are summed over the query heads of their KV head.  Sums are taken in a
+ * fixed order: equal inputs give equal bits. */
+int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, const void* v,
+                       const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* ---- a decode step of a batch that shares a prefix --------------------
+ *
+ * All B sequences begin with the same P rows (a system prompt, a document, the
+ * prompt of many samples); each has a cache of its own for what follows.  The
+ * prefix is held once and read once for all queries of the batch.
+ *   q             [B, Hq, 64]      unrotated, rows q_stride elements apart
+ *   k_new, v_new  [B, Hkv, 64]     the step's new rows, unrotated (both NULL: none)
+ *   prefix_k/v    [Hkv, P, 64]     rows 0..P-1, keys rotated at them (sfa_rope_keys);
+ *                                  heads prefix_k_stride / prefix_v_stride elements apart
+ *   k_cache/v_cache [B, Hkv, T, 64] contiguous; row r of a sequence stands at position P + r,
+ *                                  its key rotated there
+ *   pos           device int32 [B], 0 <= pos[b] < T
+ *   o             [B, Hq, 64]      d->dtype;  lse fp32 [B, Hq] or NULL
+ * The new key, rotated at P + pos[b] by d->rope (fp32, one rounding), and the new
+ * value are written to row pos[b] of sequence b's caches; then the query, rotated
+ * there too, attends the P rows of the prefix and rows 0..pos[b] of its cache.
+ * What stands behind pos[b] may be anything.  A position out of range writes
+ * nothing, gives a zero row with lse = -inf and is recorded as
+ * SFA_ERR_DEVICE_BOUNDS.  rope: sfa_rope_table for rope_T >= P + T positions, or
+ * NULL for no rotation.  Hq / Hkv <= 32; P, T <= 2^24; B Hq below 2^24, Hkv P and
+ * B Hkv T below 2^30. */
+typedef struct {
+  int32_t B, P, T, Hq, Hkv, D; /* P >= 0; D = 64 */
+  int32_t dtype;
+  int64_t q_stride, k_stride, v_stride;     /* elements between rows of q, k_new, v_new (looked at without new rows too) */
+  int64_t prefix_k_stride, prefix_v_stride; /* elements between heads */
+  const float* rope;
+  int32_t rope_T;
+} sfa_prefix_desc;
+
+int sfa_prefix_workspace_size(const sfa_prefix_desc* d, size_t* bytes);
+int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new, const void* v_new,
+                      const void* prefix_k, const void* prefix_v, void* k_cache, void* v_cache,
+                      const int32_t* pos, void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Allocation-free variant of sfa_forward (no counterpart on the pages; it
  * exists for callers that cannot allocate device memory: programs whose
  * allocator owns all device memory and bars raw cudaMalloc from libraries,
@@ -411,7 +486,12 @@ typedef enum {
   SFA_KERNEL_KV4_APPEND = 8,
   SFA_KERNEL_KV4_READ = 9,
   SFA_KERNEL_KV4_ATTEND = 10,
-  SFA_KERNEL_KINDS = 11
+  SFA_KERNEL_CROSS_FWD = 11,
+  SFA_KERNEL_CROSS_JOIN = 12, /* parts of split sums put together */
+  SFA_KERNEL_CROSS_STAT = 13, /* what comes before: delta, a step's rotations */
+  SFA_KERNEL_CROSS_BWD_Q = 14,
+  SFA_KERNEL_CROSS_BWD_KV = 15,
+  SFA_KERNEL_KINDS = 16
 } sfa_kernel_kind;
 int sfa_timing_enable(int on);
 int sfa_timing_read(double* ms, int64_t* launches, int n);

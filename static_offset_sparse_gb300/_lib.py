@@ -49,6 +49,25 @@ class Kv4Desc(C.Structure):
     ]
 
 
+class CrossDesc(C.Structure):
+    _fields_ = [
+        ("B", C.c_int32), ("Tq", C.c_int32), ("Tk", C.c_int32), ("Hq", C.c_int32), ("Hkv", C.c_int32),
+        ("D", C.c_int32), ("dtype", C.c_int32),
+        ("q_stride", C.c_int64 * 3), ("k_stride", C.c_int64 * 3), ("v_stride", C.c_int64 * 3),
+        ("q_len", C.c_void_p), ("kv_len", C.c_void_p),
+    ]
+
+
+class PrefixDesc(C.Structure):
+    _fields_ = [
+        ("B", C.c_int32), ("P", C.c_int32), ("T", C.c_int32), ("Hq", C.c_int32), ("Hkv", C.c_int32),
+        ("D", C.c_int32), ("dtype", C.c_int32),
+        ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+        ("prefix_k_stride", C.c_int64), ("prefix_v_stride", C.c_int64),
+        ("rope", C.c_void_p), ("rope_T", C.c_int32),
+    ]
+
+
 _LIB = None
 _LOCK = threading.Lock()
 _P = C.c_void_p
@@ -83,6 +102,11 @@ SIGNATURES = {
     "sfa_kv4_read": [C.POINTER(Kv4Desc)] + [_P] * 5,
     "sfa_kv4_workspace_size": [C.POINTER(Kv4Desc), C.POINTER(C.c_size_t)],
     "sfa_kv4_attend": [C.POINTER(Kv4Desc)] + [_P] * 8 + [C.c_size_t, _P],
+    "sfa_cross_workspace_size": [C.POINTER(CrossDesc), C.c_int, C.POINTER(C.c_size_t)],
+    "sfa_cross_forward": [C.POINTER(CrossDesc)] + [_P] * 6 + [C.c_size_t, _P],
+    "sfa_cross_backward": [C.POINTER(CrossDesc)] + [_P] * 10 + [C.c_size_t, _P],
+    "sfa_prefix_workspace_size": [C.POINTER(PrefixDesc), C.POINTER(C.c_size_t)],
+    "sfa_prefix_decode": [C.POINTER(PrefixDesc)] + [_P] * 11 + [C.c_size_t, _P],
     "sfa_rope_keys": [C.POINTER(Desc), _P, _P, _P],
     "sfa_reach": [_I32P, _I32P, C.c_int32, C.c_int32, _I32P, C.POINTER(C.c_int64)],
     "sfa_residue_classes": [_I32P, C.c_int32, C.c_int32, C.POINTER(C.c_int64)],

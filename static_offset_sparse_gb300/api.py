@@ -350,7 +350,8 @@ def get_device_status() -> int:
 
 
 KERNEL_KINDS = ("fwd", "bwd_q", "bwd_kv", "dalpha_reduce", "rope_table", "prep", "decode",
-                "kv4_plan", "kv4_append", "kv4_read", "kv4_attend")
+                "kv4_plan", "kv4_append", "kv4_read", "kv4_attend",
+                "cross_fwd", "cross_join", "cross_stat", "cross_bwd_q", "cross_bwd_kv")
 
 
 def timing_enable(on: bool = True) -> None:

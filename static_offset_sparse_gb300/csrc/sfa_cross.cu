@@ -1,0 +1,409 @@
+// Attention to states of another length (sfa_cross_forward, sfa_cross_backward)
+// and a decode step of a batch that shares a prefix (sfa_prefix_decode): checks
+// of arguments, which kernels a call runs, its workspace, and the small kernels
+// around them.
+#include "sfa_cross.cuh"
+
+namespace sfa {
+
+static bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// ---- small kernels
+
+// lse * log2(e) and delta = sum(o * dO) of each row, eight lanes a row; rows
+// that count for nothing get +inf, which makes their probabilities 0.
+template <typename TIO>
+__global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, float2* stat) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t row = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int d8 = (threadIdx.x & 7) * 8;
+  float sum = 0.0f;
+  bool valid = false;
+  if (row < a.rows) {
+    const int64_t bh = row / a.Tq;
+    const int b = (int)(bh / a.Hq);
+    valid = row - bh * a.Tq < a.queries(b) && a.keys(b) > 0;
+  }
+  if (valid) {
+    float o[8], g[8];
+    load8(static_cast<const TIO*>(a.out) + row * kD + d8, o);
+    load8(static_cast<const TIO*>(a.dO) + row * kD + d8, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(o[e], g[e], sum);
+  }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (row < a.rows && d8 == 0) stat[row] = valid ? make_float2(a.lse[row] * kLog2e, sum) : make_float2(INFINITY, 0.0f);
+}
+
+// out = the sum of n-number parts, in order.
+template <typename TIO>
+__global__ void __launch_bounds__(256) cross_sum_kernel(const float* parts, int splits, int64_t n, void* out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  float x[8], y[8];
+  load8(parts + i, x);
+  for (int s = 1; s < splits; ++s) {
+    load8(parts + s * n + i, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += y[e];
+  }
+  store8(static_cast<TIO*>(out) + i, x);
+}
+
+struct PrefixArgs {
+  const void *q, *k_new, *v_new;
+  int64_t q_stride, k_stride, v_stride;
+  void *k_cache, *v_cache;
+  const int32_t* pos;
+  const float2* rope;
+  float* q32;  // [B, Hq, 64] rotated queries
+  int B, P, T, Hq, Hkv;
+  int* status;
+};
+
+// Rotates a step's queries, and its key rows into the caches next to the
+// values: a warp a head's row, a pair (j, j + 32) a lane.
+template <typename TIO>
+__global__ void __launch_bounds__(128) prefix_prep_kernel(const PrefixArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, heads = a.Hq + (a.k_new ? 2 * a.Hkv : 0);
+  const int64_t x = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (x >= (int64_t)a.B * heads) return;
+  const int b = (int)(x / heads), h = (int)(x - (int64_t)b * heads);
+  const int t = a.pos[b];
+  const bool there = t >= 0 && t < a.T;
+  if (!there && lane == 0) record_status(a.status, SFA_ERR_DEVICE_BOUNDS);
+  float lo = 0.0f, hi = 0.0f;
+  if (there) {
+    const TIO* in = h < a.Hq ? static_cast<const TIO*>(a.q) + b * a.q_stride + h * kD
+                  : h < a.Hq + a.Hkv ? static_cast<const TIO*>(a.k_new) + b * a.k_stride + (h - a.Hq) * kD
+                                     : static_cast<const TIO*>(a.v_new) + b * a.v_stride + (h - a.Hq - a.Hkv) * kD;
+    lo = (float)in[lane];
+    hi = (float)in[lane + 32];
+    if (a.rope && h < a.Hq + a.Hkv) {
+      const float2 cs = __ldg(a.rope + ((int64_t)a.P + t) * 32 + lane);
+      const float x0 = lo, x1 = hi;
+      lo = x0 * cs.x - x1 * cs.y;
+      hi = x0 * cs.y + x1 * cs.x;
+    }
+  }
+  if (h < a.Hq) {
+    float* out = a.q32 + ((int64_t)b * a.Hq + h) * kD;
+    out[lane] = lo;
+    out[lane + 32] = hi;
+  } else if (there) {
+    const bool key = h < a.Hq + a.Hkv;
+    TIO* out = static_cast<TIO*>(key ? a.k_cache : a.v_cache) + (((int64_t)b * a.Hkv + (h - a.Hq) % a.Hkv) * a.T + t) * kD;
+    out[lane] = (TIO)lo;
+    out[lane + 32] = (TIO)hi;
+  }
+}
+
+// ---- which kernels a call runs
+
+// Parts of a forward call, 0: o and lse are written at once.
+static bool few_rows(int rows) { return rows <= kStreamRows; }
+
+static int forward_splits(int64_t units, int rows, int Tk) {  // units: sequences x KV heads
+  if (few_rows(rows)) return wave_splits(units, 4 * kSMs, Tk, 256);
+  return wave_splits(units * ((rows + kSimtTile - 1) / kSimtTile), 3 * kSMs, (Tk + kSimtTile - 1) / kSimtTile, 2);
+}
+
+static size_t part_bytes(int splits, int64_t rows) {
+  return align256((size_t)splits * rows * kD * sizeof(float)) + align256((size_t)splits * rows * sizeof(float2));
+}
+
+static void set_parts(CrossArgs* a, char* ws, int splits, int64_t rows, int first) {
+  a->part_o = reinterpret_cast<float*>(ws) + first * rows * kD;
+  a->part_ml = reinterpret_cast<float2*>(ws + align256((size_t)splits * rows * kD * sizeof(float))) + first * rows;
+}
+
+static int run_forward(const CrossArgs& a, bool q32, int dtype, void* stream) {
+  if (few_rows(a.G * a.Tq) || q32) return launch_cross_stream(a, q32, dtype, stream);
+  return launch_cross_fwd_simt(a, dtype, stream);
+}
+
+// ---- attention to states of another length
+
+// Strides of a [B, H, T, 64] tensor: 16-byte steps that do not overlap, where
+// there is more than one.
+static bool strides_ok(const int64_t* s, int B, int H, int T, int dtype) {
+  const int n[3] = {B, H, T};
+  const int64_t step = dtype == SFA_BF16 ? 8 : 4;
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] < kD || s[i] % step || s[i] >= ((int64_t)1 << 38))) return false;
+  return true;
+}
+
+static int check_cross(const sfa_cross_desc* d) {
+  if (!d) return SFA_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->Tq <= 0 || d->Tk <= 0 || d->Hq <= 0 || d->Hkv <= 0) return SFA_ERR_INVALID_ARG;
+  if (d->dtype != SFA_F32 && d->dtype != SFA_BF16) return SFA_ERR_INVALID_ARG;
+  if (d->D != kD || d->Hq % d->Hkv) return SFA_ERR_UNSUPPORTED;
+  if (d->Hq / d->Hkv > 32) return SFA_ERR_UNSUPPORTED;
+  if (d->Tq > (1 << 24) || d->Tk > (1 << 24)) return SFA_ERR_UNSUPPORTED;
+  if ((__int128)d->B * d->Hq * d->Tq >= ((__int128)1 << 30) || (__int128)d->B * d->Hkv * d->Tk >= ((__int128)1 << 30))
+    return SFA_ERR_UNSUPPORTED;
+  if (!strides_ok(d->q_stride, d->B, d->Hq, d->Tq, d->dtype) || !strides_ok(d->k_stride, d->B, d->Hkv, d->Tk, d->dtype) ||
+      !strides_ok(d->v_stride, d->B, d->Hkv, d->Tk, d->dtype) || !aligned(d->q_len, 4) || !aligned(d->kv_len, 4))
+    return SFA_ERR_INVALID_ARG;
+  return SFA_OK;
+}
+
+static int cross_args(const sfa_cross_desc* d, CrossArgs* a) {
+  *a = CrossArgs{};
+  a->qs = {d->q_stride[0], d->q_stride[1], d->q_stride[2]};
+  a->ks = {d->k_stride[0], d->k_stride[1], d->k_stride[2]};
+  a->vs = {d->v_stride[0], d->v_stride[1], d->v_stride[2]};
+  a->rs = {(int64_t)d->Hq * d->Tq, d->Tq, 1};
+  a->rows = (int64_t)d->B * d->Hq * d->Tq;
+  a->q_len = d->q_len;
+  a->kv_len = d->kv_len;
+  a->B = d->B;
+  a->Tq = d->Tq;
+  a->Tk = d->Tk;
+  a->Hq = d->Hq;
+  a->Hkv = d->Hkv;
+  a->G = d->Hq / d->Hkv;
+  int32_t skip;
+  wait_injection(&a->wait_cycles, &skip);
+  return device_status(&a->status);
+}
+
+static int cross_splits(const sfa_cross_desc* d) {
+  return forward_splits((int64_t)d->B * d->Hkv, d->Hq / d->Hkv * d->Tq, d->Tk);
+}
+
+struct BackwardPlan {
+  int dq_splits, dkv_splits;
+  int64_t rows, keys;
+  size_t stat, bytes;  // bytes of the rows' numbers, of the workspace
+};
+
+static BackwardPlan backward_plan(const sfa_cross_desc* d) {
+  BackwardPlan p;
+  const int64_t units = (int64_t)d->B * d->Hkv;
+  const int rt = (d->Hq / d->Hkv * d->Tq + kSimtTile - 1) / kSimtTile, kt = (d->Tk + kSimtTile - 1) / kSimtTile;
+  p.dq_splits = wave_splits(units * rt, 2 * kSMs, kt, 2);
+  p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
+  p.rows = (int64_t)d->B * d->Hq * d->Tq;
+  p.keys = units * d->Tk;
+  p.stat = align256((size_t)p.rows * sizeof(float2));
+  const size_t q = p.dq_splits > 1 ? (size_t)p.dq_splits * p.rows * kD * sizeof(float) : 0;
+  const size_t kv = p.dkv_splits > 1 ? 2 * (size_t)p.dkv_splits * p.keys * kD * sizeof(float) : 0;
+  p.bytes = p.stat + (q > kv ? q : kv);
+  return p;
+}
+
+static int launch_sum(const float* parts, int splits, int64_t n, void* out, int dtype, void* stream) {
+  const dim3 grid((unsigned)((n / 8 + 255) / 256));
+  LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
+  const cudaError_t e = dtype == SFA_BF16 ? launch_pdl(cross_sum_kernel<bf16>, grid, dim3(256), 0, (cudaStream_t)stream, parts, splits, n, out)
+                                          : launch_pdl(cross_sum_kernel<float>, grid, dim3(256), 0, (cudaStream_t)stream, parts, splits, n, out);
+  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+}
+
+// ---- a decode step behind a shared prefix
+
+static int check_prefix(const sfa_prefix_desc* d) {
+  if (!d) return SFA_ERR_INVALID_ARG;
+  if (d->B <= 0 || d->P < 0 || d->T <= 0 || d->Hq <= 0 || d->Hkv <= 0) return SFA_ERR_INVALID_ARG;
+  if (d->dtype != SFA_F32 && d->dtype != SFA_BF16) return SFA_ERR_INVALID_ARG;
+  if (d->D != kD || d->Hq % d->Hkv) return SFA_ERR_UNSUPPORTED;
+  if (d->Hq / d->Hkv > 32) return SFA_ERR_UNSUPPORTED;
+  if (d->P > (1 << 24) || d->T > (1 << 24) || (__int128)d->B * d->Hq >= (1 << 24) || (__int128)d->Hkv * d->P >= ((__int128)1 << 30) ||
+      (__int128)d->B * d->Hkv * d->T >= ((__int128)1 << 30))
+    return SFA_ERR_UNSUPPORTED;
+  const int64_t step = d->dtype == SFA_BF16 ? 8 : 4;
+  const int64_t s[5] = {d->q_stride, d->k_stride, d->v_stride, d->prefix_k_stride, d->prefix_v_stride};
+  const int64_t least[5] = {(int64_t)d->Hq * kD, (int64_t)d->Hkv * kD, (int64_t)d->Hkv * kD, (int64_t)d->P * kD, (int64_t)d->P * kD};
+  for (int i = 0; i < 5; ++i)
+    if ((i < 3 ? d->B : d->P ? d->Hkv : 1) > 1 && (s[i] < least[i] || s[i] % step || s[i] >= ((int64_t)1 << 38))) return SFA_ERR_INVALID_ARG;
+  if (d->rope && (!aligned(d->rope, 16) || (int64_t)d->rope_T < (int64_t)d->P + d->T)) return SFA_ERR_INVALID_ARG;
+  return SFA_OK;
+}
+
+struct PrefixPlan {
+  int shared, own;  // parts of the prefix and of the sequences' own rows
+  int64_t rows;
+  size_t q32, bytes;
+};
+
+static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
+  PrefixPlan p;
+  const int G = d->Hq / d->Hkv;
+  p.rows = (int64_t)d->B * d->Hq;
+  p.shared = d->P ? forward_splits((int64_t)d->Hkv, G * d->B, d->P) : 0;
+  p.own = wave_splits((int64_t)d->B * d->Hkv * ((G + kStreamRows - 1) / kStreamRows), 4 * kSMs, d->T, 256);
+  p.q32 = align256((size_t)p.rows * kD * sizeof(float));
+  p.bytes = p.q32 + part_bytes(p.shared + p.own, p.rows);
+  return p;
+}
+
+}  // namespace sfa
+
+using namespace sfa;
+
+extern "C" {
+
+int sfa_cross_workspace_size(const sfa_cross_desc* d, int backward, size_t* bytes) {
+  if (!bytes) return SFA_ERR_INVALID_ARG;
+  const int rc = check_cross(d);
+  if (rc != SFA_OK) return rc;
+  if (backward) {
+    *bytes = backward_plan(d).bytes;
+  } else {
+    const int s = cross_splits(d);
+    *bytes = s > 1 ? part_bytes(s, (int64_t)d->B * d->Hq * d->Tq) : 0;
+  }
+  return SFA_OK;
+}
+
+int sfa_cross_forward(const sfa_cross_desc* d, const void* q, const void* k, const void* v, void* o, float* lse, void* ws, size_t ws_bytes,
+                      void* stream) {
+  size_t need = 0;
+  int rc = sfa_cross_workspace_size(d, 0, &need);
+  if (rc != SFA_OK) return rc;
+  if (!q || !k || !v || !o || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4))
+    return SFA_ERR_INVALID_ARG;
+  if (need && (!ws || !aligned(ws, 16))) return SFA_ERR_INVALID_ARG;
+  if (ws_bytes < need) return SFA_ERR_CAPACITY;
+  CrossArgs a;
+  if ((rc = cross_args(d, &a)) != SFA_OK) return rc;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  a.splits = cross_splits(d);
+  a.parts = a.splits > 1;
+  if (a.parts) set_parts(&a, static_cast<char*>(ws), a.splits, a.rows, 0);
+  if ((rc = run_forward(a, false, d->dtype, stream)) != SFA_OK || !a.parts) return rc;
+  return launch_cross_join(a, d->dtype, nullptr, 0, stream);
+}
+
+int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                       void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_cross(d);
+  if (rc != SFA_OK) return rc;
+  const void* ptrs[] = {q, k, v, o, dO, dq, dk, dv, ws};
+  for (const void* x : ptrs)
+    if (!x || !aligned(x, 16)) return SFA_ERR_INVALID_ARG;
+  if (!lse || !aligned(lse, 4)) return SFA_ERR_INVALID_ARG;
+  const BackwardPlan p = backward_plan(d);
+  if (ws_bytes < p.bytes) return SFA_ERR_CAPACITY;
+  CrossArgs a;
+  if ((rc = cross_args(d, &a)) != SFA_OK) return rc;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = o;
+  a.lse = const_cast<float*>(lse);  // read only
+  a.dO = dO;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  float2* const stat = static_cast<float2*>(ws);
+  float* const parts = reinterpret_cast<float*>(static_cast<char*>(ws) + p.stat);
+  {
+    LaunchTimer tm(SFA_KERNEL_CROSS_STAT, stream);
+    const dim3 grid((unsigned)((p.rows + 31) / 32));
+    const cudaError_t e = d->dtype == SFA_BF16 ? launch_pdl(cross_stat_kernel<bf16>, grid, dim3(256), 0, (cudaStream_t)stream, a, stat)
+                                               : launch_pdl(cross_stat_kernel<float>, grid, dim3(256), 0, (cudaStream_t)stream, a, stat);
+    if (e != cudaSuccess) return SFA_ERR_CUDA;
+  }
+  a.stat = stat;
+  a.splits = p.dq_splits;
+  a.parts = a.splits > 1;
+  a.part_a = parts;
+  if ((rc = launch_cross_dq_simt(a, d->dtype, stream)) != SFA_OK) return rc;
+  if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, d->dtype, stream)) != SFA_OK) return rc;
+  a.splits = p.dkv_splits;
+  a.parts = a.splits > 1;
+  a.part_b = parts + (size_t)a.splits * p.keys * kD;
+  if ((rc = launch_cross_dkv_simt(a, d->dtype, stream)) != SFA_OK || !a.parts) return rc;
+  if ((rc = launch_sum(a.part_a, a.splits, p.keys * kD, dk, d->dtype, stream)) != SFA_OK) return rc;
+  return launch_sum(a.part_b, a.splits, p.keys * kD, dv, d->dtype, stream);
+}
+
+int sfa_prefix_workspace_size(const sfa_prefix_desc* d, size_t* bytes) {
+  if (!bytes) return SFA_ERR_INVALID_ARG;
+  const int rc = check_prefix(d);
+  if (rc != SFA_OK) return rc;
+  *bytes = prefix_plan(d).bytes;
+  return SFA_OK;
+}
+
+int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new, const void* v_new, const void* prefix_k,
+                      const void* prefix_v, void* k_cache, void* v_cache, const int32_t* pos, void* o, float* lse, void* ws, size_t ws_bytes,
+                      void* stream) {
+  int rc = check_prefix(d);
+  if (rc != SFA_OK) return rc;
+  if (!q || !k_cache || !v_cache || !pos || !o || !ws || !k_new != !v_new || (d->P && (!prefix_k || !prefix_v))) return SFA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k_new, v_new, prefix_k, prefix_v, k_cache, v_cache, o, ws};
+  for (const void* x : ptrs)
+    if (!aligned(x, 16)) return SFA_ERR_INVALID_ARG;
+  if (!aligned(pos, 4) || !aligned(lse, 4)) return SFA_ERR_INVALID_ARG;
+  const PrefixPlan p = prefix_plan(d);
+  if (ws_bytes < p.bytes) return SFA_ERR_CAPACITY;
+  CrossArgs a = {};
+  int32_t skip;
+  wait_injection(&a.wait_cycles, &skip);
+  if ((rc = device_status(&a.status)) != SFA_OK) return rc;
+  char* const w = static_cast<char*>(ws);
+  PrefixArgs x = {q, k_new, v_new, d->q_stride, d->k_stride, d->v_stride, k_cache, v_cache, pos, reinterpret_cast<const float2*>(d->rope),
+                  reinterpret_cast<float*>(w), d->B, d->P, d->T, d->Hq, d->Hkv, a.status};
+  {
+    LaunchTimer tm(SFA_KERNEL_CROSS_STAT, stream);
+    const int64_t heads = (int64_t)d->B * (d->Hq + (k_new ? 2 * d->Hkv : 0));
+    const dim3 grid((unsigned)((heads + 3) / 4));
+    const cudaError_t e = d->dtype == SFA_BF16 ? launch_pdl(prefix_prep_kernel<bf16>, grid, dim3(128), 0, (cudaStream_t)stream, x)
+                                               : launch_pdl(prefix_prep_kernel<float>, grid, dim3(128), 0, (cudaStream_t)stream, x);
+    if (e != cudaSuccess) return SFA_ERR_CUDA;
+  }
+  a.rows = p.rows;
+  a.q = x.q32;
+  a.Hq = d->Hq;
+  a.Hkv = d->Hkv;
+  a.G = d->Hq / d->Hkv;
+  a.parts = true;
+  if (d->P) {  // the batch as one sequence of B queries
+    a.B = 1;
+    a.Tq = d->B;
+    a.Tk = d->P;
+    a.qs = {0, kD, (int64_t)d->Hq * kD};
+    a.ks = {0, d->prefix_k_stride, kD};
+    a.vs = {0, d->prefix_v_stride, kD};
+    a.rs = {0, 1, d->Hq};
+    a.k = prefix_k;
+    a.v = prefix_v;
+    a.splits = p.shared;
+    set_parts(&a, w + p.q32, p.shared + p.own, p.rows, 0);
+    if ((rc = run_forward(a, true, d->dtype, stream)) != SFA_OK) return rc;
+  }
+  a.B = d->B;
+  a.Tq = 1;
+  a.Tk = d->T;
+  a.qs = {(int64_t)d->Hq * kD, kD, kD};
+  a.ks = a.vs = {(int64_t)d->Hkv * d->T * kD, (int64_t)d->T * kD, kD};
+  a.rs = {d->Hq, 1, 1};
+  a.k = k_cache;
+  a.v = v_cache;
+  a.kv_len = pos;
+  a.kv_add = 1;
+  a.splits = p.own;
+  set_parts(&a, w + p.q32, p.shared + p.own, p.rows, p.shared);
+  if ((rc = launch_cross_stream(a, true, d->dtype, stream)) != SFA_OK) return rc;
+  a.o = o;
+  a.lse = lse;
+  a.splits = p.shared + p.own;
+  set_parts(&a, w + p.q32, a.splits, p.rows, 0);
+  return launch_cross_join(a, d->dtype, pos, d->T, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,381 @@
+"""Attention to states of another length, its gradients, and decode steps behind a shared prefix, against the
+64-bit definitions of cross_ref.py."""
+import math
+
+import pytest
+import torch
+
+import cross_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def sfa(sfa_lib):
+    import static_offset_sparse_gb300 as s
+
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    s.get_device_status()
+    return s
+
+
+def _i32(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _inputs(seed, B, Tq, Tk, Hq, Hkv, dtype, scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    normal = lambda *s: torch.randn(s, generator=gen).to(dtype)  # noqa: E731
+    return normal(B, Hq, Tq, 64) * scale, normal(B, Hkv, Tk, 64), normal(B, Hkv, Tk, 64), normal(B, Hq, Tq, 64)
+
+
+def _spoil(x, lens, what=NAN):
+    """x [B, H, T, ...] with `what` behind the lengths."""
+    if lens is not None:
+        x = x.clone()
+        for b, n in enumerate(lens):
+            x[b, :, n:] = what
+    return x
+
+
+def _forward(sfa, q, k, v, nq, nk, **kw):
+    got = sfa.cross_forward(q.cuda(), k.cuda(), v.cuda(), q_len=_i32(nq), kv_len=_i32(nk), **kw)
+    assert sfa.get_device_status() == 0
+    return got
+
+
+def _check_forward(sfa, q, k, v, nq, nk):
+    o, lse = _forward(sfa, q, k, v, nq, nk)
+    wo, wl, bo, bl = ref.forward(q, k, v, nq, nk)
+    ref.check("o", o, wo, bo)
+    ref.check("lse", lse, wl, bl)
+    return o, lse
+
+
+def _check_backward(sfa, q, k, v, do, nq, nk):
+    """Gradients from o and lse as the forward's exact values round to them, all spoiled behind the lengths."""
+    o, lse, _, _ = ref.forward(_spoil(q, nq, 0.0), _spoil(k, nk, 0.0), _spoil(v, nk, 0.0), nq, nk)
+    o, lse = o.to(q.dtype), lse.float()
+    clean = ref.backward(_spoil(q, nq, 0.0), _spoil(k, nk, 0.0), _spoil(v, nk, 0.0), o, lse, _spoil(do, nq, 0.0), nq, nk)
+    o, lse, do = _spoil(o, nq), _spoil(lse, nq), _spoil(do, nq)
+    got = sfa.cross_backward(*(x.cuda() for x in (q, k, v, o, lse, do)), q_len=_i32(nq), kv_len=_i32(nk))
+    assert sfa.get_device_status() == 0
+    for name, g, w, b in zip(("dq", "dk", "dv"), got, *clean):
+        ref.check(name, g, w, b)
+    return got
+
+
+# (B, Tq, Tk, Hq, Hkv, lengths of queries, lengths of keys)
+SIZES = [
+    (1, 1, 1, 1, 1, None, None),
+    (1, 1, 300, 8, 2, None, None),
+    (3, 1, 777, 8, 2, None, [777, 0, 130]),
+    (2, 3, 5, 4, 2, None, None),
+    (2, 2, 64, 12, 4, [2, 1], [64, 63]),
+    (1, 7, 1000, 32, 1, None, None),
+    (1, 1, 4100, 3, 3, None, None),
+    (2, 17, 65, 8, 8, [17, 0], [65, 1]),
+    (1, 64, 64, 4, 1, None, None),
+    (1, 63, 129, 6, 2, None, None),
+    (1, 130, 127, 2, 2, None, None),
+    (2, 33, 500, 24, 2, [33, 20], [257, 500]),
+    (1, 200, 1000, 5, 1, None, None),
+    (1, 129, 3000, 8, 2, [129], [2999]),
+    (2, 300, 128, 8, 2, [299, 1], [128, 77]),
+    (4, 257, 256, 2, 1, [257, 128, 0, 3], [256, 129, 5, 0]),
+    (1, 1025, 70, 4, 4, None, None),
+    (1, 40, 9000, 8, 8, None, None),
+]
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv,nq,nk", SIZES)
+def test_forward(sfa, B, Tq, Tk, Hq, Hkv, nq, nk, dtype):
+    q, k, v, _ = _inputs(B * 1000 + Tq + Tk, B, Tq, Tk, Hq, Hkv, dtype)
+    _check_forward(sfa, _spoil(q, nq), _spoil(k, nk), _spoil(v, nk), nq, nk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv,nq,nk", SIZES)
+def test_backward(sfa, B, Tq, Tk, Hq, Hkv, nq, nk, dtype):
+    q, k, v, do = _inputs(B * 1000 + Tq + Tk + 1, B, Tq, Tk, Hq, Hkv, dtype)
+    _check_backward(sfa, _spoil(q, nq), _spoil(k, nk), _spoil(v, nk), do, nq, nk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq", [2, 70])
+def test_infinite_padding(sfa, Tq, dtype):
+    q, k, v, do = _inputs(5, 2, Tq, 200, 4, 2, dtype)
+    nq, nk = [Tq, Tq - 1], [133, 200]
+    q, k, v = _spoil(q, nq, INF), _spoil(k, nk, -INF), _spoil(v, nk, INF)
+    _check_forward(sfa, q, k, v, nq, nk)
+    _check_backward(sfa, q, k, v, do, nq, nk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq", [1, 90])
+def test_strided_views(sfa, Tq, dtype):
+    """Queries of a [B, T, H, 64] projection, keys and values of a joint one with heads before rows."""
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(2, Tq, 3 * 8, 64, generator=gen).to(dtype).cuda()
+    kv = torch.randn(2, 150, 2, 2, 64, generator=gen).to(dtype).cuda()
+    q, k, v = x[:, :, 8:16].transpose(1, 2), kv[:, :, 0].transpose(1, 2), kv[:, :, 1].transpose(1, 2)
+    assert not q.is_contiguous() or Tq == 1
+    o, lse = sfa.cross_forward(q, k, v)
+    o2, lse2 = sfa.cross_forward(q.contiguous(), k.contiguous(), v.contiguous())
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    do = torch.randn(2, 8, Tq, 64, generator=gen).to(dtype).cuda()
+    for a, b in zip(sfa.cross_backward(q, k, v, o, lse, do), sfa.cross_backward(q.contiguous(), k.contiguous(), v.contiguous(), o, lse, do)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", [(1, 700), (100, 300)])
+def test_far_logits(sfa, Tq, Tk, dtype):
+    """Logits of 2^30 and more, all of a row below -2^30, and queries of zeros: no NaN, one key takes all."""
+    q, k, v, _ = _inputs(7, 1, Tq, Tk, 4, 2, dtype)
+    k = k.abs()
+    q = q.sign() * 2.0 ** 30
+    q[:, 1] = -q[:, 1].abs()
+    q[:, 3] = 0
+    o, lse = _forward(sfa, q, k, v, None, None)
+    s = q.double() @ k.double().repeat_interleave(2, 1).transpose(-1, -2) / 8
+    top = s.amax(-1)
+    # fp32 products of 2^30: off by 66 u of the terms' sizes
+    size = (q.double().abs() @ k.double().repeat_interleave(2, 1).abs().transpose(-1, -2) / 8).amax(-1)
+    assert bool(((lse.cpu().double() - torch.logsumexp(s, -1)).abs() <= 70 * ref.U * size + 1e-3)[:, :3].all())
+    assert bool(o.isfinite().all()) and bool(lse.isfinite().all()) and bool(top.isfinite().all())
+    near = s >= top[..., None] - 140 * ref.U * size[..., None]  # keys that may take all
+    vv = v.double().repeat_interleave(2, 1)
+    alone = near.sum(-1) == 1
+    r = ref.half_step(dtype)
+    pick = torch.gather(vv, 2, s.argmax(-1)[..., None].expand(-1, -1, -1, 64))
+    off = ((o.cpu().double() - pick).abs() - 2 * r * pick.abs() - 1e-6)[:, :3][alone[:, :3]]
+    assert off.numel() == 0 or float(off.max()) <= 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq", [1, 100])
+def test_nan_stays_in_its_rows(sfa, Tq, dtype):
+    q, k, v, do = _inputs(8, 2, Tq, 200, 8, 2, dtype)
+    q[0, 3, Tq // 2] = NAN
+    k[1, 1, 150] = NAN
+    o, lse = _forward(sfa, q, k, v, None, None)
+    bad = torch.zeros(2, 8, Tq, dtype=torch.bool)
+    bad[0, 3, Tq // 2] = True
+    bad[1, 4:] = True
+    assert torch.equal(lse.isnan().cpu(), bad) and torch.equal(o.isnan().any(-1).cpu(), bad)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_lengths_out_of_range(sfa, dtype):
+    q, k, v, do = (x.cuda() for x in _inputs(9, 3, 20, 40, 4, 2, dtype))
+    o, lse = sfa.cross_forward(q, k, v, q_len=_i32([20, 21, 20]), kv_len=_i32([-1, 40, 41]))
+    assert sfa.get_device_status() == 6
+    assert not o.any() and bool((lse == -INF).all())
+    grads = sfa.cross_backward(q, k, v, o, lse, do, q_len=_i32([20, 21, 20]), kv_len=_i32([-1, 40, 41]))
+    assert sfa.get_device_status() == 6
+    assert not any(g.any() for g in grads)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", [(1, 5000), (200, 2000), (3000, 40)])
+def test_same_bits_again_and_in_a_graph(sfa, Tq, Tk, dtype):
+    q, k, v, do = (x.cuda() for x in _inputs(10, 1, Tq, Tk, 8, 2, dtype))
+    lens = dict(q_len=_i32([Tq]), kv_len=_i32([Tk - 3]))
+
+    def step():
+        o, lse = sfa.cross_forward(q, k, v, **lens)
+        return (o, lse, *sfa.cross_backward(q, k, v, o, lse, do, **lens))
+
+    first = [x.clone() for x in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = [x.clone() for x in step()]
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for x in out:
+        x.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(first, second, out):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    # other contents and lengths in the same graph
+    q.copy_(torch.randn_like(q))
+    lens["kv_len"].fill_(max(1, Tk // 3))
+    want = [x.clone() for x in step()]
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, c in zip(want, out):
+        assert torch.equal(a, c)
+
+
+def test_python_refusals(sfa):
+    q, k, v, do = (x.cuda() for x in _inputs(11, 2, 5, 9, 4, 2, torch.bfloat16))
+    o, lse = sfa.cross_forward(q, k, v)
+    bad = [((q, k.float(), v), {}), ((q, k, v[:, :, :8]), {}), ((q, k[:1], v[:1]), {}), ((q[0], k, v), {}),
+           ((q[..., :32], k, v), {}), ((q, k, v.expand(2, 2, 9, 64)[:, :1].expand(2, 2, 9, 64)), {}),
+           ((q, k, v), dict(q_len=_i32([1]))), ((q, k, v), dict(kv_len=_i32([1, 2]).long())), ((q, k, v), dict(o=o.float())),
+           ((q, k, v), dict(lse=lse[:, :, :4])), ((q, k, v), dict(o=o.transpose(1, 2).contiguous().transpose(1, 2)))]
+    for args, kw in bad:
+        with pytest.raises((ValueError, TypeError)):
+            sfa.cross_forward(*args, **kw)
+    with pytest.raises(TypeError):
+        sfa.cross_forward(q.half(), k.half(), v.half())
+    with pytest.raises(ValueError):
+        sfa.cross_backward(q, k, v, o, lse, do.transpose(1, 2).contiguous().transpose(1, 2))
+    with pytest.raises(ValueError):
+        sfa.cross_backward(q, k, v, o, lse.double(), do)
+    with pytest.raises(sfa.SfaError):
+        sfa.cross_forward(q[:, :3], k, v)
+
+
+def test_outputs_and_workspace_of_the_caller(sfa):
+    q, k, v, do = (x.cuda() for x in _inputs(12, 1, 5, 3001, 8, 2, torch.bfloat16))
+    want = sfa.cross_forward(q, k, v)
+    o, lse = torch.empty_like(q), torch.empty(1, 8, 5, device="cuda")
+    ws = torch.full((sfa.cross_workspace_size(q, k, v) + 64,), 255, dtype=torch.uint8, device="cuda")
+    got = sfa.cross_forward(q, k, v, o=o, lse=lse, ws=ws)
+    assert got[0] is o and got[1] is lse and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert bool((ws[-64:] == 255).all())
+    grads = sfa.cross_backward(q, k, v, o, lse, do)
+    ws = torch.full((sfa.cross_workspace_size(q, k, v, backward=True) + 64,), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.full_like(x, NAN) for x in (q, k, v)]
+    sfa.cross_backward(q, k, v, o, lse, do, dq=outs[0], dk=outs[1], dv=outs[2], ws=ws)
+    assert all(torch.equal(a, b) for a, b in zip(grads, outs)) and bool((ws[-64:] == 255).all())
+
+
+# ------------------------------------------------------------------ decode steps behind a shared prefix
+
+
+def _prefix_inputs(seed, B, P, T, Hq, Hkv, dtype):
+    gen = torch.Generator().manual_seed(seed)
+    normal = lambda *s: torch.randn(s, generator=gen).to(dtype)  # noqa: E731
+    return normal(B, Hq + 2 * Hkv, 64), normal(Hkv, P, 64), normal(Hkv, P, 64), normal(B, Hkv, T, 64), normal(B, Hkv, T, 64)
+
+
+def _step(sfa, qkv, pk, pv, kc, vc, pos, Hq, **kw):
+    Hkv = pk.shape[0]
+    return sfa.prefix_decode(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], pk, pv, kc, vc, _i32(pos), **kw)
+
+
+PREFIXES = [
+    (1, 1, 1, 1, 1, [0]),
+    (1, 0, 40, 8, 2, [39]),
+    (2, 3, 5, 8, 2, [4, 0]),
+    (3, 100, 30, 4, 4, [29, 0, 7]),
+    (5, 1000, 600, 6, 2, [0, 599, 300, 256, 255]),
+    (17, 129, 64, 32, 1, [(7 * i) % 64 for i in range(17)]),
+    (33, 2000, 300, 8, 1, [(37 * i) % 300 for i in range(33)]),
+    (130, 257, 33, 8, 2, [(5 * i) % 33 for i in range(130)]),
+    (40, 5000, 20, 24, 2, [i % 20 for i in range(40)]),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,P,T,Hq,Hkv,pos", PREFIXES)
+def test_prefix(sfa, B, P, T, Hq, Hkv, pos, dtype):
+    qkv, pk, pv, kc, vc = _prefix_inputs(B + P + T, B, P, T, Hq, Hkv, dtype)
+    for b, t in enumerate(pos):  # what stands behind, and at, the step's row is not read
+        kc[b, :, t:] = NAN
+        vc[b, :, t:] = NAN
+    rope = sfa.rope_table(P + T).cpu()
+    dev = [x.cuda() for x in (qkv, pk, pv, kc, vc)]
+    o, lse = _step(sfa, *dev, pos, Hq)
+    assert sfa.get_device_status() == 0
+    r = ref.half_step(dtype)
+    for b, t in enumerate(pos):
+        kc[b, :, t], vc[b, :, t] = dev[3][b, :, t].cpu(), qkv[b, Hq + Hkv:]
+        x = qkv[b, Hq:Hq + Hkv]
+        want = ref.rotated(x, rope[P + t])
+        pair = x.double().abs() + x.double().roll(32, -1).abs()
+        ref.check("new key", dev[3][b, :, t], want, r * want.abs() + 3 * (1 + r) * ref.U * pair + 1e-37)
+    assert torch.equal(dev[3].cpu().nan_to_num(99.0), kc.nan_to_num(99.0)) and torch.equal(dev[4].cpu().nan_to_num(99.0), vc.nan_to_num(99.0))
+    wo, wl, bo, bl = ref.prefix(qkv[:, :Hq], pk, pv, kc, vc, pos, rope)
+    ref.check("o", o, wo, bo)
+    ref.check("lse", lse, wl, bl)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_prefix_rows_out_of_range(sfa, dtype):
+    qkv, pk, pv, kc, vc = (x.cuda() for x in _prefix_inputs(3, 4, 70, 20, 8, 2, dtype))
+    before = kc.clone(), vc.clone()
+    whole = _step(sfa, qkv, pk, pv, kc.clone(), vc.clone(), [3, 4, 19, 5], 8)
+    o, lse = _step(sfa, qkv, pk, pv, kc, vc, [3, -1, 19, 20], 8)
+    assert sfa.get_device_status() == 6
+    for b in (1, 3):
+        assert not o[b].any() and bool((lse[b] == -INF).all())
+        assert torch.equal(kc[b], before[0][b]) and torch.equal(vc[b], before[1][b])
+    for b in (0, 2):
+        assert torch.equal(o[b], whole[0][b]) and torch.equal(lse[b], whole[1][b])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_prefix_without_new_rows_and_rotation(sfa, dtype):
+    """Caches that hold the step's rows, rows of the caller's own strides, no rotation."""
+    B, P, T, Hq, Hkv = 6, 300, 50, 8, 2
+    qkv, pk, pv, kc, vc = _prefix_inputs(4, B, P, T, Hq, Hkv, dtype)
+    pos = [49, 0, 3, 17, 22, 31]
+    wide = torch.zeros(Hkv, P + 24, 64, dtype=dtype)
+    wide[:, :P] = pk
+    for rope in (None, sfa.rope_table(P + T)):
+        o, lse = sfa.prefix_decode(qkv.cuda()[:, :Hq], None, None, wide.cuda()[:, :P], pv.cuda(), kc.cuda(), vc.cuda(), _i32(pos),
+                                   rope=rope, rope_theta=0 if rope is None else 1e4)
+        wo, wl, bo, bl = ref.prefix(qkv[:, :Hq], pk, pv, kc, vc, pos, None if rope is None else rope.cpu())
+        ref.check("o", o, wo, bo)
+        ref.check("lse", lse, wl, bl)
+
+
+def test_prefix_steps_as_a_user_makes_them(sfa):
+    """A prefix laid out by rope_keys, then steps captured once and replayed while pos counts up: the same as
+    decode_int over caches that hold everything, key by key unrotated."""
+    B, P, T, Hq, Hkv = 3, 90, 6, 8, 2
+    gen = torch.Generator().manual_seed(6)
+    normal = lambda *s: torch.randn(s, generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    raw_k, raw_v = normal(1, Hkv, P, 64), normal(1, Hkv, P, 64)
+    pk, pv = sfa.rope_keys(raw_k)[0], raw_v[0]
+    kc, vc = torch.full((B, Hkv, T, 64), NAN, dtype=torch.bfloat16, device="cuda"), torch.full((B, Hkv, T, 64), NAN, dtype=torch.bfloat16, device="cuda")
+    rope, pos, qkv = sfa.rope_table(P + T), _i32([0] * B), normal(B, Hq + 2 * Hkv, 64)
+
+    def step():
+        return sfa.prefix_decode(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], pk, pv, kc, vc, pos, rope=rope)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step()
+    dense_k, dense_v = (torch.cat([x.expand(B, -1, -1, -1), torch.zeros(B, Hkv, T, 64, dtype=x.dtype, device="cuda")], 2).contiguous() for x in (raw_k, raw_v))
+    for t in range(T):
+        qkv.copy_(normal(B, Hq + 2 * Hkv, 64))
+        pos.fill_(t)
+        graph.replay()
+        dense_k[:, :, P + t], dense_v[:, :, P + t] = qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        want, wlse = sfa.decode_int(qkv[:, :Hq].contiguous(), dense_k, dense_v, pos + P, dist=list(range(P + T)))
+        # keys here are rounded once more after the rotation, probabilities and outputs to bf16: logits of up to
+        # 2^-8 sum |q k| / 8 (24 is beyond the largest here) and values of 4 at most
+        assert float((lse - wlse).abs().max()) < 2.0 ** -8 * 24
+        assert float((o.float() - want.float()).abs().max()) < 4 * (2 * 2.0 ** -8 * 24 + 3 * 2.0 ** -8)
+    assert sfa.get_device_status() == 0
+
+
+def test_prefix_python_refusals(sfa):
+    B, P, T, Hq, Hkv = 2, 10, 4, 8, 2
+    qkv, pk, pv, kc, vc = (x.cuda() for x in _prefix_inputs(7, B, P, T, Hq, Hkv, torch.bfloat16))
+    q, kn, vn, pos = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], _i32([0, 1])
+    good = dict(q=q, k_new=kn, v_new=vn, prefix_k=pk, prefix_v=pv, k_cache=kc, v_cache=vc, pos=pos)
+    sfa.prefix_decode(**good)
+    bad = [dict(q=q[:1]), dict(q=q.float()), dict(k_new=None), dict(v_new=vn[:, :1]), dict(prefix_k=pk[:1]), dict(prefix_v=pv[:, :9]),
+           dict(prefix_k=pk.transpose(0, 1).contiguous().transpose(0, 1)), dict(k_cache=kc.transpose(1, 2)), dict(v_cache=vc[:, :, :3]),
+           dict(pos=pos.long()), dict(pos=pos[:1]), dict(rope=torch.zeros(5, 32, device="cuda")), dict(o=torch.zeros(B, Hq, 64, device="cuda"))]
+    for kw in bad:
+        with pytest.raises((ValueError, TypeError)):
+            sfa.prefix_decode(**{**good, **kw})
+    with pytest.raises(sfa.SfaError):
+        sfa.prefix_decode(**good, rope=sfa.rope_table(P + T - 1))
