@@ -57,6 +57,21 @@ int make_band_map(CUtensorMap* m, const void* base, int64_t planes, int T, int d
              : SFA_ERR_CUDA;
 }
 
+// Four-dimensional view of rows of 64 bf16: H heads of T rows of B sequences,
+// whose steps in elements are s_b, s_h, s_t (not looked at where there is one).
+int make_rows4_map(CUtensorMap* m, const void* base, int T, int H, int B, int64_t s_t, int64_t s_h, int64_t s_b, int box_rows, int box_heads) {
+  auto fn = encode_fn();
+  if (!fn) return SFA_ERR_CUDA;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {T > 1 ? (cuuint64_t)s_t * 2 : 128, H > 1 ? (cuuint64_t)s_h * 2 : 128, B > 1 ? (cuuint64_t)s_b * 2 : 128};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_heads, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SFA_OK
+             : SFA_ERR_CUDA;
+}
+
 int make_coef_map(CUtensorMap* m, const void* base, int64_t planes, int T, int NS, int words,
                   int box_slots, int box_q) {
   auto fn = encode_fn();

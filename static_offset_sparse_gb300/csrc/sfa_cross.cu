@@ -61,6 +61,7 @@ struct PrefixArgs {
   const int32_t* pos;
   const float2* rope;
   float* q32;  // [B, Hq, 64] rotated queries
+  bf16* q16;   // or nullptr: the same as two bf16 parts, [2][B, Hq, 64]
   int B, P, T, Hq, Hkv;
   int* status;
 };
@@ -96,6 +97,14 @@ __global__ void __launch_bounds__(128) prefix_prep_kernel(const PrefixArgs a) {
     float* out = a.q32 + ((int64_t)b * a.Hq + h) * kD;
     out[lane] = lo;
     out[lane + 32] = hi;
+    if (a.q16) {
+      bf16* const first = a.q16 + ((int64_t)b * a.Hq + h) * kD;
+      bf16* const second = first + (int64_t)a.B * a.Hq * kD;
+      first[lane] = (bf16)lo;
+      first[lane + 32] = (bf16)hi;
+      second[lane] = (bf16)(lo - (float)(bf16)lo);
+      second[lane + 32] = (bf16)(hi - (float)(bf16)hi);
+    }
   } else if (there) {
     const bool key = h < a.Hq + a.Hkv;
     TIO* out = static_cast<TIO*>(key ? a.k_cache : a.v_cache) + (((int64_t)b * a.Hkv + (h - a.Hq) % a.Hkv) * a.T + t) * kD;
@@ -106,12 +115,16 @@ __global__ void __launch_bounds__(128) prefix_prep_kernel(const PrefixArgs a) {
 
 // ---- which kernels a call runs
 
-// Parts of a forward call, 0: o and lse are written at once.
-static bool few_rows(int rows) { return rows <= kStreamRows; }
+enum Kind { kFewRows, kTensor, kFp32 };
+static Kind forward_kind(int rows, int dtype) { return rows <= kStreamRows ? kFewRows : dtype == SFA_BF16 ? kTensor : kFp32; }
 
-static int forward_splits(int64_t units, int rows, int Tk) {  // units: sequences x KV heads
-  if (few_rows(rows)) return wave_splits(units, 4 * kSMs, Tk, 256);
-  return wave_splits(units * ((rows + kSimtTile - 1) / kSimtTile), 3 * kSMs, (Tk + kSimtTile - 1) / kSimtTile, 2);
+// Parts of a forward call over `units` (sequence, KV head) pairs of Tq queries of G heads.
+static int forward_splits(int64_t units, int G, int Tq, int Tk, int dtype) {
+  switch (forward_kind(G * Tq, dtype)) {
+    case kFewRows: return wave_splits(units, 4 * kSMs, Tk, 256);
+    case kTensor: return wave_splits(units * ((row_tiles(G, Tq).tiles + 1) / 2), kSMs, (Tk + 127) / 128, 2);
+    default: return wave_splits(units * ((G * Tq + kSimtTile - 1) / kSimtTile), 3 * kSMs, (Tk + kSimtTile - 1) / kSimtTile, 2);
+  }
 }
 
 static size_t part_bytes(int splits, int64_t rows) {
@@ -123,9 +136,12 @@ static void set_parts(CrossArgs* a, char* ws, int splits, int64_t rows, int firs
   a->part_ml = reinterpret_cast<float2*>(ws + align256((size_t)splits * rows * kD * sizeof(float))) + first * rows;
 }
 
-static int run_forward(const CrossArgs& a, bool q32, int dtype, void* stream) {
-  if (few_rows(a.G * a.Tq) || q32) return launch_cross_stream(a, q32, dtype, stream);
-  return launch_cross_fwd_simt(a, dtype, stream);
+static int run_forward(const CrossArgs& a, bool prefix, int dtype, void* stream) {
+  switch (forward_kind(a.G * a.Tq, dtype)) {
+    case kFewRows: return launch_cross_stream(a, prefix, dtype, stream);
+    case kTensor: return launch_cross_fwd_tc(a, prefix, stream);
+    default: return launch_cross_fwd_simt(a, stream);
+  }
 }
 
 // ---- attention to states of another length
@@ -176,7 +192,7 @@ static int cross_args(const sfa_cross_desc* d, CrossArgs* a) {
 }
 
 static int cross_splits(const sfa_cross_desc* d) {
-  return forward_splits((int64_t)d->B * d->Hkv, d->Hq / d->Hkv * d->Tq, d->Tk);
+  return forward_splits((int64_t)d->B * d->Hkv, d->Hq / d->Hkv, d->Tq, d->Tk, d->dtype);
 }
 
 struct BackwardPlan {
@@ -231,17 +247,20 @@ static int check_prefix(const sfa_prefix_desc* d) {
 struct PrefixPlan {
   int shared, own;  // parts of the prefix and of the sequences' own rows
   int64_t rows;
-  size_t q32, bytes;
+  bool two;  // whether the queries are wanted as two bf16 parts
+  size_t q32, q16, bytes;
 };
 
 static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
   PrefixPlan p;
   const int G = d->Hq / d->Hkv;
   p.rows = (int64_t)d->B * d->Hq;
-  p.shared = d->P ? forward_splits((int64_t)d->Hkv, G * d->B, d->P) : 0;
+  p.shared = d->P ? forward_splits(d->Hkv, G, d->B, d->P, d->dtype) : 0;
+  p.two = d->P && forward_kind(G * d->B, d->dtype) == kTensor;
   p.own = wave_splits((int64_t)d->B * d->Hkv * ((G + kStreamRows - 1) / kStreamRows), 4 * kSMs, d->T, 256);
   p.q32 = align256((size_t)p.rows * kD * sizeof(float));
-  p.bytes = p.q32 + part_bytes(p.shared + p.own, p.rows);
+  p.q16 = p.two ? align256((size_t)p.rows * kD * 2 * sizeof(bf16)) : 0;
+  p.bytes = p.q32 + p.q16 + part_bytes(p.shared + p.own, p.rows);
   return p;
 }
 
@@ -356,8 +375,9 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
   wait_injection(&a.wait_cycles, &skip);
   if ((rc = device_status(&a.status)) != SFA_OK) return rc;
   char* const w = static_cast<char*>(ws);
+  char* const parts = w + p.q32 + p.q16;
   PrefixArgs x = {q, k_new, v_new, d->q_stride, d->k_stride, d->v_stride, k_cache, v_cache, pos, reinterpret_cast<const float2*>(d->rope),
-                  reinterpret_cast<float*>(w), d->B, d->P, d->T, d->Hq, d->Hkv, a.status};
+                  reinterpret_cast<float*>(w), p.two ? reinterpret_cast<bf16*>(w + p.q32) : nullptr, d->B, d->P, d->T, d->Hq, d->Hkv, a.status};
   {
     LaunchTimer tm(SFA_KERNEL_CROSS_STAT, stream);
     const int64_t heads = (int64_t)d->B * (d->Hq + (k_new ? 2 * d->Hkv : 0));
@@ -376,16 +396,18 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
     a.B = 1;
     a.Tq = d->B;
     a.Tk = d->P;
-    a.qs = {0, kD, (int64_t)d->Hq * kD};
+    a.qs = {p.rows * kD, kD, (int64_t)d->Hq * kD};
+    if (p.two) a.q = x.q16;
     a.ks = {0, d->prefix_k_stride, kD};
     a.vs = {0, d->prefix_v_stride, kD};
     a.rs = {0, 1, d->Hq};
     a.k = prefix_k;
     a.v = prefix_v;
     a.splits = p.shared;
-    set_parts(&a, w + p.q32, p.shared + p.own, p.rows, 0);
+    set_parts(&a, parts, p.shared + p.own, p.rows, 0);
     if ((rc = run_forward(a, true, d->dtype, stream)) != SFA_OK) return rc;
   }
+  a.q = x.q32;
   a.B = d->B;
   a.Tq = 1;
   a.Tk = d->T;
@@ -397,12 +419,12 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
   a.kv_len = pos;
   a.kv_add = 1;
   a.splits = p.own;
-  set_parts(&a, w + p.q32, p.shared + p.own, p.rows, p.shared);
+  set_parts(&a, parts, p.shared + p.own, p.rows, p.shared);
   if ((rc = launch_cross_stream(a, true, d->dtype, stream)) != SFA_OK) return rc;
   a.o = o;
   a.lse = lse;
   a.splits = p.shared + p.own;
-  set_parts(&a, w + p.q32, a.splits, p.rows, 0);
+  set_parts(&a, parts, a.splits, p.rows, 0);
   return launch_cross_join(a, d->dtype, pos, d->T, stream);
 }
 

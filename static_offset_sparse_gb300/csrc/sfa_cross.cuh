@@ -77,6 +77,33 @@ __device__ __forceinline__ void split_keys(int n, int tile, int splits, int s, i
   end = min(n, hi * tile);
 }
 
+// Two fp32 numbers at once.
+__device__ __forceinline__ float2 pair_fma(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+
 // What 2^(x - m) is taken against: 0 for a maximum of -inf (no key, or logits
 // that are all -inf), so that -inf - m stays -inf.
 __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
@@ -84,7 +111,21 @@ __device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0
 // host side
 int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream);
 int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos_T, void* stream);
-int launch_cross_fwd_simt(const CrossArgs& a, int dtype, void* stream);
+int launch_cross_fwd_simt(const CrossArgs& a, void* stream);
+// Tiles of 128 rows of the tensor-core kernels: 2^lgR queries of 128 / 2^lgR
+// heads of a KV head each, so that short sequences share tiles; tile i holds
+// head group i mod groups of query block i / groups (queries behind a length come last).
+struct RowTiles {
+  int lgR, groups, blocks, tiles;
+};
+RowTiles row_tiles(int G, int Tq);
+// A tensor map of bf16 rows: boxes of `heads` x `rows` rows, 128-byte swizzle (sfa_api.cu).
+int make_rows4_map(CUtensorMap* m, const void* base, int T, int H, int B, int64_t s_t, int64_t s_h, int64_t s_b, int box_rows, int box_heads);
+inline int make_view_map(CUtensorMap* m, const void* base, int T, int H, int B, const Strides& s, int rows, int heads) {
+  return make_rows4_map(m, base, T, H, B, s.t, s.h, s.b, rows, heads);
+}
+// bf16; two: queries as two bf16 parts, the second a sequence's stride behind the first
+int launch_cross_fwd_tc(const CrossArgs& a, bool two, void* stream);
 int launch_cross_dq_simt(const CrossArgs& a, int dtype, void* stream);
 int launch_cross_dkv_simt(const CrossArgs& a, int dtype, void* stream);
 constexpr int kStreamRows = 8;  // rows that cross_stream_kernel takes at once

@@ -317,12 +317,10 @@ static cudaError_t simt_launch(void (*f)(const CrossArgs), const CrossArgs& a, i
   return e != cudaSuccess ? e : launch_pdl(f, dim3((unsigned)grid), dim3(threads), smem, st, a);
 }
 
-int launch_cross_fwd_simt(const CrossArgs& a, int dtype, void* stream) {
+int launch_cross_fwd_simt(const CrossArgs& a, void* stream) {
   const int64_t grid = (int64_t)a.B * a.Hkv * simt_row_tiles(a.G * a.Tq) * a.splits;
   LaunchTimer tm(SFA_KERNEL_CROSS_FWD, stream);
-  const cudaError_t e = dtype == SFA_BF16
-                            ? simt_launch<bf16>(cross_fwd_kernel<bf16>, a, grid, kFwdThreads, kFwdSmemBytes, (cudaStream_t)stream)
-                            : simt_launch<float>(cross_fwd_kernel<float>, a, grid, kFwdThreads, kFwdSmemBytes, (cudaStream_t)stream);
+  const cudaError_t e = simt_launch<float>(cross_fwd_kernel<float>, a, grid, kFwdThreads, kFwdSmemBytes, (cudaStream_t)stream);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
