@@ -204,9 +204,16 @@ struct BackwardPlan {
 static BackwardPlan backward_plan(const sfa_cross_desc* d) {
   BackwardPlan p;
   const int64_t units = (int64_t)d->B * d->Hkv;
-  const int rt = (d->Hq / d->Hkv * d->Tq + kSimtTile - 1) / kSimtTile, kt = (d->Tk + kSimtTile - 1) / kSimtTile;
-  p.dq_splits = wave_splits(units * rt, 2 * kSMs, kt, 2);
-  p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
+  const int G = d->Hq / d->Hkv;
+  if (d->dtype == SFA_BF16) {
+    const int rt = row_tiles(G, d->Tq).tiles, kt = (d->Tk + 127) / 128;
+    p.dq_splits = wave_splits(units * rt, kSMs, kt, 2);
+    p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
+  } else {
+    const int rt = (G * d->Tq + kSimtTile - 1) / kSimtTile, kt = (d->Tk + kSimtTile - 1) / kSimtTile;
+    p.dq_splits = wave_splits(units * rt, 2 * kSMs, kt, 2);
+    p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
+  }
   p.rows = (int64_t)d->B * d->Hq * d->Tq;
   p.keys = units * d->Tk;
   p.stat = align256((size_t)p.rows * sizeof(float2));
@@ -340,12 +347,12 @@ int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, co
   a.splits = p.dq_splits;
   a.parts = a.splits > 1;
   a.part_a = parts;
-  if ((rc = launch_cross_dq_simt(a, d->dtype, stream)) != SFA_OK) return rc;
+  if ((rc = d->dtype == SFA_BF16 ? launch_cross_bwd_tc(a, false, stream) : launch_cross_dq_simt(a, stream)) != SFA_OK) return rc;
   if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, d->dtype, stream)) != SFA_OK) return rc;
   a.splits = p.dkv_splits;
   a.parts = a.splits > 1;
   a.part_b = parts + (size_t)a.splits * p.keys * kD;
-  if ((rc = launch_cross_dkv_simt(a, d->dtype, stream)) != SFA_OK || !a.parts) return rc;
+  if ((rc = d->dtype == SFA_BF16 ? launch_cross_bwd_tc(a, true, stream) : launch_cross_dkv_simt(a, stream)) != SFA_OK || !a.parts) return rc;
   if ((rc = launch_sum(a.part_a, a.splits, p.keys * kD, dk, d->dtype, stream)) != SFA_OK) return rc;
   return launch_sum(a.part_b, a.splits, p.keys * kD, dv, d->dtype, stream);
 }

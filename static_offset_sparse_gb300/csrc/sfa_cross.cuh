@@ -126,8 +126,9 @@ inline int make_view_map(CUtensorMap* m, const void* base, int T, int H, int B, 
 }
 // bf16; two: queries as two bf16 parts, the second a sequence's stride behind the first
 int launch_cross_fwd_tc(const CrossArgs& a, bool two, void* stream);
-int launch_cross_dq_simt(const CrossArgs& a, int dtype, void* stream);
-int launch_cross_dkv_simt(const CrossArgs& a, int dtype, void* stream);
+int launch_cross_bwd_tc(const CrossArgs& a, bool dkv, void* stream);  // bf16
+int launch_cross_dq_simt(const CrossArgs& a, void* stream);           // fp32
+int launch_cross_dkv_simt(const CrossArgs& a, void* stream);
 constexpr int kStreamRows = 8;  // rows that cross_stream_kernel takes at once
 constexpr int kSimtTile = 64;   // rows and keys of the fp32 kernels' tiles
 

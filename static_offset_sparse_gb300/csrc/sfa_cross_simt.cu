@@ -39,8 +39,7 @@ __device__ __forceinline__ void tile_product(float (*acc)[4], const float* A, co
 
 // n8 chunks of 8 dims of one row (nullptr: zeros) from chunk c0 on: transposed
 // into line c of tr, and as they are into row r of pl (either may be nullptr).
-template <typename TIO>
-__device__ __forceinline__ void load_row(const TIO* row, int r, int c0, int n8, float mul, float* tr, float* pl) {
+__device__ __forceinline__ void load_row(const float* row, int r, int c0, int n8, float mul, float* tr, float* pl) {
 #pragma unroll
   for (int c = c0; c < c0 + n8; ++c) {
     float x[8];
@@ -63,7 +62,6 @@ __device__ __forceinline__ void load_row(const TIO* row, int r, int c0, int n8, 
 constexpr int kFwdThreads = 128;
 constexpr size_t kFwdSmemBytes = 4 * kLine * sizeof(float);
 
-template <typename TIO>
 __global__ void __launch_bounds__(kFwdThreads) cross_fwd_kernel(const CrossArgs a) {
   extern __shared__ __align__(16) float sm[];
   float *const Qt = sm, *const Kt = sm + kLine, *const Vs = sm + 2 * kLine, *const Pt = sm + 3 * kLine;
@@ -83,7 +81,7 @@ __global__ void __launch_bounds__(kFwdThreads) cross_fwd_kernel(const CrossArgs 
   if (r0 >= (int64_t)nq * a.G) k1 = k0;  // no query in the tile
   {
     const int r = r0 + (tid & 63), t = r / a.G, h = kvh * a.G + (r - t * a.G);
-    const TIO* row = r < rows && t < nq ? static_cast<const TIO*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t : nullptr;
+    const float* row = r < rows && t < nq ? static_cast<const float*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t : nullptr;
     load_row(row, tid & 63, 4 * (tid >> 6), 4, kLogitScale, Qt, (float*)nullptr);
   }
   float o[8][4], m[8], l[8];
@@ -98,8 +96,8 @@ __global__ void __launch_bounds__(kFwdThreads) cross_fwd_kernel(const CrossArgs 
     {
       const int j = j0 + (tid & 63);
       const bool in = j < k1;
-      load_row(in ? static_cast<const TIO*>(a.k) + b * a.ks.b + kvh * a.ks.h + j * a.ks.t : nullptr, tid & 63, 4 * (tid >> 6), 4, 1.0f, Kt, (float*)nullptr);
-      load_row(in ? static_cast<const TIO*>(a.v) + b * a.vs.b + kvh * a.vs.h + j * a.vs.t : nullptr, tid & 63, 4 * (tid >> 6), 4, 1.0f, (float*)nullptr, Vs);
+      load_row(in ? static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h + j * a.ks.t : nullptr, tid & 63, 4 * (tid >> 6), 4, 1.0f, Kt, (float*)nullptr);
+      load_row(in ? static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h + j * a.vs.t : nullptr, tid & 63, 4 * (tid >> 6), 4, 1.0f, (float*)nullptr, Vs);
     }
     __syncthreads();
     float p[8][4];
@@ -151,7 +149,7 @@ __global__ void __launch_bounds__(kFwdThreads) cross_fwd_kernel(const CrossArgs 
       if (tx == 0) a.part_ml[at] = none ? make_float2(-INFINITY, -1.0f) : make_float2(m[i], l[i]);
     } else {
       const float inv = 1.0f / l[i];
-      TIO* out = static_cast<TIO*>(a.o) + row * kD + 4 * tx;
+      float* out = static_cast<float*>(a.o) + row * kD + 4 * tx;
       store2(out, none ? 0.0f : o[i][0] * inv, none ? 0.0f : o[i][1] * inv);
       store2(out + 2, none ? 0.0f : o[i][2] * inv, none ? 0.0f : o[i][3] * inv);
       if (a.lse && tx == 0) a.lse[row] = none ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
@@ -165,7 +163,6 @@ constexpr size_t kDqSmemBytes = 6 * kLine * sizeof(float), kDkvSmemBytes = 8 * k
 
 // dq: a CTA has 64 rows and a split of their keys.
 //   ds = p (dO v - delta), dq = sum ds k / 8
-template <typename TIO>
 __global__ void __launch_bounds__(kBwdThreads) cross_dq_kernel(const CrossArgs a) {
   extern __shared__ __align__(16) float sm[];
   float *const Qt = sm, *const Dt = sm + kLine, *const Kt = sm + 2 * kLine, *const Vt = sm + 3 * kLine, *const Ks = sm + 4 * kLine,
@@ -187,8 +184,8 @@ __global__ void __launch_bounds__(kBwdThreads) cross_dq_kernel(const CrossArgs a
   {
     const int r = r0 + lr, t = r / a.G, h = kvh * a.G + (r - t * a.G);
     const bool in = r < rows && t < nq;
-    load_row(in ? static_cast<const TIO*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t : nullptr, lr, lc, 2, kLogitScale, Qt, (float*)nullptr);
-    load_row(in ? static_cast<const TIO*>(a.dO) + a.row(b, kvh, r) * kD : nullptr, lr, lc, 2, 1.0f, Dt, (float*)nullptr);
+    load_row(in ? static_cast<const float*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t : nullptr, lr, lc, 2, kLogitScale, Qt, (float*)nullptr);
+    load_row(in ? static_cast<const float*>(a.dO) + a.row(b, kvh, r) * kD : nullptr, lr, lc, 2, 1.0f, Dt, (float*)nullptr);
   }
   float2 st[4];
 #pragma unroll
@@ -200,8 +197,8 @@ __global__ void __launch_bounds__(kBwdThreads) cross_dq_kernel(const CrossArgs a
   for (int j0 = k0; j0 < k1; j0 += kTileN) {
     const int j = j0 + lr;
     const bool in = j < k1;
-    load_row(in ? static_cast<const TIO*>(a.k) + b * a.ks.b + kvh * a.ks.h + j * a.ks.t : nullptr, lr, lc, 2, 1.0f, Kt, Ks);
-    load_row(in ? static_cast<const TIO*>(a.v) + b * a.vs.b + kvh * a.vs.h + j * a.vs.t : nullptr, lr, lc, 2, 1.0f, Vt, (float*)nullptr);
+    load_row(in ? static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h + j * a.ks.t : nullptr, lr, lc, 2, 1.0f, Kt, Ks);
+    load_row(in ? static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h + j * a.vs.t : nullptr, lr, lc, 2, 1.0f, Vt, (float*)nullptr);
     __syncthreads();
     float p[4][4] = {}, dp[4][4] = {};
     tile_product<4>(p, Qt, Kt, 4 * ty, 4 * tx);
@@ -229,7 +226,7 @@ __global__ void __launch_bounds__(kBwdThreads) cross_dq_kernel(const CrossArgs a
       float* out = a.part_a + (s * a.rows + row) * kD + 4 * tx;
       *reinterpret_cast<float4*>(out) = make_float4(0.125f * dq[i][0], 0.125f * dq[i][1], 0.125f * dq[i][2], 0.125f * dq[i][3]);
     } else {
-      TIO* out = static_cast<TIO*>(a.dq) + row * kD + 4 * tx;
+      float* out = static_cast<float*>(a.dq) + row * kD + 4 * tx;
       store2(out, 0.125f * dq[i][0], 0.125f * dq[i][1]);
       store2(out + 2, 0.125f * dq[i][2], 0.125f * dq[i][3]);
     }
@@ -238,7 +235,6 @@ __global__ void __launch_bounds__(kBwdThreads) cross_dq_kernel(const CrossArgs a
 
 // dk, dv: a CTA has 64 keys and a split of the rows that attend them.
 //   dv = sum p dO, dk = sum ds q / 8
-template <typename TIO>
 __global__ void __launch_bounds__(kBwdThreads) cross_dkv_kernel(const CrossArgs a) {
   extern __shared__ __align__(16) float sm[];
   float *const Kt = sm, *const Vt = sm + kLine, *const Qt = sm + 2 * kLine, *const Dt = sm + 3 * kLine, *const Qs = sm + 4 * kLine,
@@ -259,15 +255,15 @@ __global__ void __launch_bounds__(kBwdThreads) cross_dkv_kernel(const CrossArgs 
   split_keys(j0 < nk ? rows : 0, kTileN, a.splits, s, b0, b1);
   {
     const int j = j0 + lr;
-    load_row(j < nk ? static_cast<const TIO*>(a.k) + b * a.ks.b + kvh * a.ks.h + j * a.ks.t : nullptr, lr, lc, 2, 1.0f, Kt, (float*)nullptr);
-    load_row(j < nk ? static_cast<const TIO*>(a.v) + b * a.vs.b + kvh * a.vs.h + j * a.vs.t : nullptr, lr, lc, 2, 1.0f, Vt, (float*)nullptr);
+    load_row(j < nk ? static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h + j * a.ks.t : nullptr, lr, lc, 2, 1.0f, Kt, (float*)nullptr);
+    load_row(j < nk ? static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h + j * a.vs.t : nullptr, lr, lc, 2, 1.0f, Vt, (float*)nullptr);
   }
   float dk[4][4] = {}, dv[4][4] = {};
   for (int r0 = b0; r0 < b1; r0 += kTileN) {
     const int r = r0 + lr, t = r / a.G, h = kvh * a.G + (r - t * a.G);
     const bool in = r < b1;
-    load_row(in ? static_cast<const TIO*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t : nullptr, lr, lc, 2, 1.0f, Qt, Qs);
-    load_row(in ? static_cast<const TIO*>(a.dO) + a.row(b, kvh, r) * kD : nullptr, lr, lc, 2, 1.0f, Dt, Ds);
+    load_row(in ? static_cast<const float*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t : nullptr, lr, lc, 2, 1.0f, Qt, Qs);
+    load_row(in ? static_cast<const float*>(a.dO) + a.row(b, kvh, r) * kD : nullptr, lr, lc, 2, 1.0f, Dt, Ds);
     if (tid < kTileN) stat[tid] = in ? a.stat[a.row(b, kvh, r)] : make_float2(INFINITY, 0.0f);
     __syncthreads();
     float p[4][4] = {}, dp[4][4] = {};  // [key][row]
@@ -300,7 +296,7 @@ __global__ void __launch_bounds__(kBwdThreads) cross_dkv_kernel(const CrossArgs 
       *reinterpret_cast<float4*>(a.part_a + at) = make_float4(0.125f * dk[i][0], 0.125f * dk[i][1], 0.125f * dk[i][2], 0.125f * dk[i][3]);
       *reinterpret_cast<float4*>(a.part_b + at) = make_float4(dv[i][0], dv[i][1], dv[i][2], dv[i][3]);
     } else {
-      TIO *ok = static_cast<TIO*>(a.dk) + row * kD + 4 * tx, *ov = static_cast<TIO*>(a.dv) + row * kD + 4 * tx;
+      float *ok = static_cast<float*>(a.dk) + row * kD + 4 * tx, *ov = static_cast<float*>(a.dv) + row * kD + 4 * tx;
       store2(ok, 0.125f * dk[i][0], 0.125f * dk[i][1]);
       store2(ok + 2, 0.125f * dk[i][2], 0.125f * dk[i][3]);
       store2(ov, dv[i][0], dv[i][1]);
@@ -309,37 +305,24 @@ __global__ void __launch_bounds__(kBwdThreads) cross_dkv_kernel(const CrossArgs 
   }
 }
 
-int simt_row_tiles(int rows) { return (rows + kTileN - 1) / kTileN; }
-
-template <typename TIO>
-static cudaError_t simt_launch(void (*f)(const CrossArgs), const CrossArgs& a, int64_t grid, int threads, size_t smem, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  return e != cudaSuccess ? e : launch_pdl(f, dim3((unsigned)grid), dim3(threads), smem, st, a);
+static int launch_tiles(int kind, void (*f)(const CrossArgs), const CrossArgs& a, int tiles, int threads, size_t smem, void* stream) {
+  const int64_t grid = (int64_t)a.B * a.Hkv * tiles * a.splits;
+  LaunchTimer tm(kind, stream);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = launch_pdl(f, dim3((unsigned)grid), dim3(threads), smem, (cudaStream_t)stream, a);
+  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
+
+static int tiles_of(int rows) { return (rows + kTileN - 1) / kTileN; }
 
 int launch_cross_fwd_simt(const CrossArgs& a, void* stream) {
-  const int64_t grid = (int64_t)a.B * a.Hkv * simt_row_tiles(a.G * a.Tq) * a.splits;
-  LaunchTimer tm(SFA_KERNEL_CROSS_FWD, stream);
-  const cudaError_t e = simt_launch<float>(cross_fwd_kernel<float>, a, grid, kFwdThreads, kFwdSmemBytes, (cudaStream_t)stream);
-  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+  return launch_tiles(SFA_KERNEL_CROSS_FWD, cross_fwd_kernel, a, tiles_of(a.G * a.Tq), kFwdThreads, kFwdSmemBytes, stream);
 }
-
-int launch_cross_dq_simt(const CrossArgs& a, int dtype, void* stream) {
-  const int64_t grid = (int64_t)a.B * a.Hkv * simt_row_tiles(a.G * a.Tq) * a.splits;
-  LaunchTimer tm(SFA_KERNEL_CROSS_BWD_Q, stream);
-  const cudaError_t e = dtype == SFA_BF16
-                            ? simt_launch<bf16>(cross_dq_kernel<bf16>, a, grid, kBwdThreads, kDqSmemBytes, (cudaStream_t)stream)
-                            : simt_launch<float>(cross_dq_kernel<float>, a, grid, kBwdThreads, kDqSmemBytes, (cudaStream_t)stream);
-  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+int launch_cross_dq_simt(const CrossArgs& a, void* stream) {
+  return launch_tiles(SFA_KERNEL_CROSS_BWD_Q, cross_dq_kernel, a, tiles_of(a.G * a.Tq), kBwdThreads, kDqSmemBytes, stream);
 }
-
-int launch_cross_dkv_simt(const CrossArgs& a, int dtype, void* stream) {
-  const int64_t grid = (int64_t)a.B * a.Hkv * simt_row_tiles(a.Tk) * a.splits;
-  LaunchTimer tm(SFA_KERNEL_CROSS_BWD_KV, stream);
-  const cudaError_t e = dtype == SFA_BF16
-                            ? simt_launch<bf16>(cross_dkv_kernel<bf16>, a, grid, kBwdThreads, kDkvSmemBytes, (cudaStream_t)stream)
-                            : simt_launch<float>(cross_dkv_kernel<float>, a, grid, kBwdThreads, kDkvSmemBytes, (cudaStream_t)stream);
-  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+int launch_cross_dkv_simt(const CrossArgs& a, void* stream) {
+  return launch_tiles(SFA_KERNEL_CROSS_BWD_KV, cross_dkv_kernel, a, tiles_of(a.Tk), kBwdThreads, kDkvSmemBytes, stream);
 }
 
 }  // namespace sfa
