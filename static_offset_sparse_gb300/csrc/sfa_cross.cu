@@ -118,13 +118,10 @@ __global__ void __launch_bounds__(128) prefix_prep_kernel(const PrefixArgs a) {
 enum Kind { kFewRows, kTensor, kFp32 };
 static Kind forward_kind(int rows, int dtype) { return rows <= kStreamRows ? kFewRows : dtype == SFA_BF16 ? kTensor : kFp32; }
 
-// Parts of a forward call over `units` (sequence, KV head) pairs of Tq queries of G heads.
-static int forward_splits(int64_t units, int G, int Tq, int Tk, int dtype) {
-  switch (forward_kind(G * Tq, dtype)) {
-    case kFewRows: return wave_splits(units, 4 * kSMs, Tk, 256);
-    case kTensor: return wave_splits(units * ((row_tiles(G, Tq).tiles + 1) / 2), kSMs, (Tk + 127) / 128, 2);
-    default: return wave_splits(units * ((G * Tq + kSimtTile - 1) / kSimtTile), 3 * kSMs, (Tk + kSimtTile - 1) / kSimtTile, 2);
-  }
+// Parts of a call over `units` (sequence, KV head) pairs of Tq queries of G heads (not the tensor cores').
+static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind) {
+  if (kind == kFewRows) return wave_splits(units, 4 * kSMs, Tk, 256);
+  return wave_splits(units * ((G * Tq + kSimtTile - 1) / kSimtTile), 3 * kSMs, (Tk + kSimtTile - 1) / kSimtTile, 2);
 }
 
 static size_t part_bytes(int splits, int64_t rows) {
@@ -134,14 +131,6 @@ static size_t part_bytes(int splits, int64_t rows) {
 static void set_parts(CrossArgs* a, char* ws, int splits, int64_t rows, int first) {
   a->part_o = reinterpret_cast<float*>(ws) + first * rows * kD;
   a->part_ml = reinterpret_cast<float2*>(ws + align256((size_t)splits * rows * kD * sizeof(float))) + first * rows;
-}
-
-static int run_forward(const CrossArgs& a, bool prefix, int dtype, void* stream) {
-  switch (forward_kind(a.G * a.Tq, dtype)) {
-    case kFewRows: return launch_cross_stream(a, prefix, dtype, stream);
-    case kTensor: return launch_cross_fwd_tc(a, prefix, stream);
-    default: return launch_cross_fwd_simt(a, stream);
-  }
 }
 
 // ---- attention to states of another length
@@ -191,8 +180,22 @@ static int cross_args(const sfa_cross_desc* d, CrossArgs* a) {
   return device_status(&a->status);
 }
 
-static int cross_splits(const sfa_cross_desc* d) {
-  return forward_splits((int64_t)d->B * d->Hkv, d->Hq / d->Hkv, d->Tq, d->Tk, d->dtype);
+struct ForwardPlan {
+  Kind kind;
+  int splits;
+  size_t bytes;
+};
+
+static ForwardPlan forward_plan(const sfa_cross_desc* d) {
+  const int G = d->Hq / d->Hkv;
+  ForwardPlan p = {forward_kind(G * d->Tq, d->dtype), 1, 0};
+  if (p.kind == kTensor) {
+    p.bytes = cross_tc_bytes(d->B, d->Hkv, G, d->Tq, d->Tk);
+  } else {
+    p.splits = forward_splits((int64_t)d->B * d->Hkv, G, d->Tq, d->Tk, p.kind);
+    if (p.splits > 1) p.bytes = part_bytes(p.splits, (int64_t)d->B * d->Hq * d->Tq);
+  }
+  return p;
 }
 
 struct BackwardPlan {
@@ -252,22 +255,25 @@ static int check_prefix(const sfa_prefix_desc* d) {
 }
 
 struct PrefixPlan {
+  Kind kind;        // of the prefix's part
   int shared, own;  // parts of the prefix and of the sequences' own rows
   int64_t rows;
-  bool two;  // whether the queries are wanted as two bf16 parts
-  size_t q32, q16, bytes;
+  bool two;  // on the tensor cores: the queries are wanted as two bf16 parts
+  size_t q32, q16, parts, bytes;
 };
 
 static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
   PrefixPlan p;
   const int G = d->Hq / d->Hkv;
   p.rows = (int64_t)d->B * d->Hq;
-  p.shared = d->P ? forward_splits(d->Hkv, G, d->B, d->P, d->dtype) : 0;
-  p.two = d->P && forward_kind(G * d->B, d->dtype) == kTensor;
+  p.kind = forward_kind(G * d->B, d->dtype);
+  p.two = d->P && p.kind == kTensor;
+  p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind);
   p.own = wave_splits((int64_t)d->B * d->Hkv * ((G + kStreamRows - 1) / kStreamRows), 4 * kSMs, d->T, 256);
   p.q32 = align256((size_t)p.rows * kD * sizeof(float));
   p.q16 = p.two ? align256((size_t)p.rows * kD * 2 * sizeof(bf16)) : 0;
-  p.bytes = p.q32 + p.q16 + part_bytes(p.shared + p.own, p.rows);
+  p.parts = part_bytes(p.shared + p.own, p.rows);
+  p.bytes = p.q32 + p.q16 + p.parts + (p.two ? cross_tc_bytes(1, d->Hkv, G, d->B, d->P) : 0);
   return p;
 }
 
@@ -284,21 +290,20 @@ int sfa_cross_workspace_size(const sfa_cross_desc* d, int backward, size_t* byte
   if (backward) {
     *bytes = backward_plan(d).bytes;
   } else {
-    const int s = cross_splits(d);
-    *bytes = s > 1 ? part_bytes(s, (int64_t)d->B * d->Hq * d->Tq) : 0;
+    *bytes = forward_plan(d).bytes;
   }
   return SFA_OK;
 }
 
 int sfa_cross_forward(const sfa_cross_desc* d, const void* q, const void* k, const void* v, void* o, float* lse, void* ws, size_t ws_bytes,
                       void* stream) {
-  size_t need = 0;
-  int rc = sfa_cross_workspace_size(d, 0, &need);
+  int rc = check_cross(d);
   if (rc != SFA_OK) return rc;
   if (!q || !k || !v || !o || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4))
     return SFA_ERR_INVALID_ARG;
-  if (need && (!ws || !aligned(ws, 16))) return SFA_ERR_INVALID_ARG;
-  if (ws_bytes < need) return SFA_ERR_CAPACITY;
+  const ForwardPlan p = forward_plan(d);
+  if (p.bytes && (!ws || !aligned(ws, 16))) return SFA_ERR_INVALID_ARG;
+  if (ws_bytes < p.bytes) return SFA_ERR_CAPACITY;
   CrossArgs a;
   if ((rc = cross_args(d, &a)) != SFA_OK) return rc;
   a.q = q;
@@ -306,11 +311,12 @@ int sfa_cross_forward(const sfa_cross_desc* d, const void* q, const void* k, con
   a.v = v;
   a.o = o;
   a.lse = lse;
-  a.splits = cross_splits(d);
+  if (p.kind == kTensor) return launch_cross_fwd_tc(a, ws, stream);
+  a.splits = p.splits;
   a.parts = a.splits > 1;
   if (a.parts) set_parts(&a, static_cast<char*>(ws), a.splits, a.rows, 0);
-  if ((rc = run_forward(a, false, d->dtype, stream)) != SFA_OK || !a.parts) return rc;
-  return launch_cross_join(a, d->dtype, nullptr, 0, stream);
+  rc = p.kind == kFewRows ? launch_cross_stream(a, false, d->dtype, stream) : launch_cross_fwd_simt(a, stream);
+  return rc != SFA_OK || !a.parts ? rc : launch_cross_join(a, d->dtype, nullptr, 0, stream);
 }
 
 int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
@@ -412,8 +418,12 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
     a.v = prefix_v;
     a.splits = p.shared;
     set_parts(&a, parts, p.shared + p.own, p.rows, 0);
-    if ((rc = run_forward(a, true, d->dtype, stream)) != SFA_OK) return rc;
+    rc = p.two ? launch_prefix_tc(a, parts + p.parts, stream)
+         : p.kind == kFewRows ? launch_cross_stream(a, true, d->dtype, stream)
+                              : launch_cross_fwd_simt(a, stream);
+    if (rc != SFA_OK) return rc;
   }
+  const CrossArgs prefix = a;
   a.q = x.q32;
   a.B = d->B;
   a.Tq = 1;
@@ -430,8 +440,9 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
   if ((rc = launch_cross_stream(a, true, d->dtype, stream)) != SFA_OK) return rc;
   a.o = o;
   a.lse = lse;
+  set_parts(&a, parts, p.shared + p.own, p.rows, 0);
+  if (p.two) return launch_prefix_join(prefix, a, parts + p.parts, pos, d->T, stream);
   a.splits = p.shared + p.own;
-  set_parts(&a, parts, a.splits, p.rows, 0);
   return launch_cross_join(a, d->dtype, pos, d->T, stream);
 }
 

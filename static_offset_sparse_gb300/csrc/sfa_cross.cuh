@@ -17,11 +17,16 @@
 #include "sfa_launch.cuh"
 #include "sfa_mma.cuh"
 #include "sfa_tma.cuh"
+#include "sfa_umma.cuh"
 
 namespace sfa {
 
 constexpr int kSMs = 152;
 constexpr float kLogitScale = 0.125f * kLog2e;  // logits in log2 units: 1/sqrt(64) * log2(e)
+
+// What 2^(x - m) is taken against: 0 for a maximum of -inf (no key, or logits
+// that are all -inf), so that -inf - m stays -inf.
+__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 struct Strides {
   int64_t b, h, t;  // elements between sequences, heads, rows
@@ -45,7 +50,7 @@ struct CrossArgs {
   const void *out, *dO;
   const float2* stat;  // [B * Hq * Tq]: lse * log2(e) (+inf for rows that count for nothing), delta
   void *dq, *dk, *dv;
-  float *part_a, *part_b;  // [splits][dq's] or [splits][dk's], [splits][dv's]
+  float *part_a, *part_b;  // fp32 kernels: [splits][dq's] or [splits][dk's], [splits][dv's]
   int* status;
   long long wait_cycles;
 
@@ -69,12 +74,208 @@ struct CrossArgs {
   }
 };
 
+// Tiles of 128 rows of the tensor-core kernels: 2^lgR queries of 128 / 2^lgR
+// heads of a KV head each, so that short sequences share tiles; tile i holds
+// head group i mod groups of query block i / groups (queries behind a length come last).
+struct RowTiles {
+  int lgR, groups, blocks, tiles;
+  // tiles with one of a sequence's nq queries: the first of them
+  __host__ __device__ __forceinline__ int used(int nq) const { return groups * ((nq + (1 << lgR) - 1) >> lgR); }
+};
+RowTiles row_tiles(int G, int Tq);
+
+// Query and head (of its group) of row r of a row tile.
+struct RowOf {
+  int t, g;
+  bool mine;
+};
+__device__ __forceinline__ RowOf row_of(const CrossArgs& a, const RowTiles& rt, int tile, int r) {
+  const int tb = tile / rt.groups, hb = tile - tb * rt.groups;
+  RowOf o;
+  o.t = (tb << rt.lgR) + (r & ((1 << rt.lgR) - 1));
+  o.g = (hb << (7 - rt.lgR)) + (r >> rt.lgR);
+  o.mine = tile < rt.tiles && o.t < a.Tq && o.g < a.G;
+  return o;
+}
+
+// How the tensor-core kernels share out their work: sequence b has units(b)
+// units (tiles that stay on an SM) of steps(b) steps each; all steps of all units,
+// in order, are dealt out evenly over the CTAs, to the step.  Lengths are known
+// on the device only, and whole units are too uneven: with a unit a CTA in turn, 32
+// ragged sequences of up to 1024 x 2048 gave one CTA 70 steps where the mean is 40.
+// A unit that spans CTAs leaves a part from each.  A CTA's share has one unit at
+// most that began before it and one that ends behind it, so two places for parts a
+// CTA are enough: 2 c for a part that does not begin its unit, 2 c + 1 for one that
+// does.  What a unit costs besides its steps counts as kUnitCost steps, with the CTA
+// that begins it.  A CTA has kLeastShare steps at least, or a unit.
+constexpr int kUnitCost = 2, kLeastShare = 6;
+
+struct Shares {
+  int64_t share, rest;
+  int ctas;
+  __host__ __device__ __forceinline__ void set(int64_t total, int64_t units, int most) {
+    const int64_t n = units > total / kLeastShare ? units : total / kLeastShare;
+    ctas = n < 1 ? 1 : n < most ? (int)n : most;
+    share = total / ctas;
+    rest = total - share * ctas;
+  }
+  __host__ __device__ __forceinline__ int64_t begin(int c) const { return share * c + (c < rest ? c : rest); }
+  __host__ __device__ __forceinline__ int owner(int64_t w) const {
+    const int64_t big = (share + 1) * rest;
+    return (int)(w < big ? w / (share + 1) : rest + (w - big) / share);
+  }
+};
+
+// The CTA's pieces of units, one after another.
+struct Walk {
+  int64_t begin, end;      // weight before the unit, where the share ends
+  int b, u, units, steps;  // the unit: number u of sequence b's
+  int s0, s1;              // the piece: its steps s0 .. s1 - 1
+  __device__ __forceinline__ bool whole() const { return s0 == 0 && s1 == steps; }
+  // from weight `off` of the unit on; false if no step of it lies in the share
+  __device__ __forceinline__ bool set(int64_t off) {
+    s0 = off > kUnitCost ? (int)off - kUnitCost : 0;
+    const int64_t left = end - begin - kUnitCost;
+    s1 = left < steps ? (int)left : steps;
+    // the same in all lanes, and known to be
+    s0 = __shfl_sync(0xffffffffu, s0, 0);
+    s1 = __shfl_sync(0xffffffffu, s1, 0);
+    return s0 < s1;
+  }
+  template <typename F>
+  __device__ __forceinline__ bool next(int B, const F& counts) {
+    begin += steps + kUnitCost;
+    if (begin >= end) return false;
+    if (++u == units) {
+      u = 0;
+      do {
+        if (++b >= B) return false;
+        counts(b, units, steps);
+      } while (units == 0);
+    }
+    return set(0);  // (without a step it is the share's last unit)
+  }
+};
+
+struct WalkShared {
+  long long sums[32], units;
+  Walk first;
+  Shares shares;
+  int any;
+};
+
+// The CTA's first piece, by all THREADS threads; false if it has none.
+template <int THREADS, typename F>
+__device__ __forceinline__ bool find_walk(int B, const F& counts, WalkShared& sh, Walk& wk) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (B + THREADS - 1) / THREADS;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  if (tid == 0) {
+    sh.any = 0;
+    sh.units = 0;
+  }
+  __syncthreads();
+  int64_t mine = 0, n = 0;
+  int units, steps;
+  for (int b = b0; b < b1; ++b) {
+    counts(b, units, steps);
+    mine += (int64_t)units * (steps + kUnitCost);
+    n += units;
+  }
+  if (n > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.units), (unsigned long long)n);
+  int64_t upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += x;
+  }
+  if (lane == 31) sh.sums[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i = 0; i < THREADS / 32; ++i) {
+    if (i == warp) upto += total;
+    total += sh.sums[i];
+  }
+  Shares s;
+  s.set(total, sh.units, gridDim.x);
+  const int c = blockIdx.x;
+  const int64_t from = s.begin(c), to = s.begin(c + 1);
+  int64_t at = upto - mine;
+  if (c < s.ctas && from < to && from >= at && from < upto)
+    for (int b = b0; b < b1; ++b) {
+      counts(b, units, steps);
+      const int64_t w = steps + kUnitCost, here = (int64_t)units * w;
+      if (from < at + here) {
+        wk.u = (int)((from - at) / w);
+        wk.begin = at + wk.u * w;
+        wk.end = to;
+        wk.b = b;
+        wk.units = units;
+        wk.steps = steps;
+        sh.first = wk;
+        sh.shares = s;
+        sh.any = 1;
+        break;
+      }
+      at += here;
+    }
+  __syncthreads();
+  if (!sh.any) return false;
+  wk = sh.first;
+  return wk.set(from - wk.begin) || wk.next(B, counts);
+}
+
 // Keys of split s of n, in whole tiles of `tile`: begin and end.
 __device__ __forceinline__ void split_keys(int n, int tile, int splits, int s, int& begin, int& end) {
   const int tiles = (n + tile - 1) / tile;
   const int lo = (int)((int64_t)tiles * s / splits), hi = (int)((int64_t)tiles * (s + 1) / splits);
   begin = lo * tile;
   end = min(n, hi * tile);
+}
+
+// n parts of a row (ml(i): its maximum and sum, a sum below 0 for a part without
+// a key, which has no o; o(i): its 64 sums) to o and lse, by a warp: a part's sums by
+// eight lanes, four parts at a time, always in the same order.  No key at all: zeros,
+// lse = -inf.
+template <typename TIO, typename ML, typename O>
+__device__ __forceinline__ void join_row(const CrossArgs& a, int64_t row, int n, int lane, const ML& ml, const O& o) {
+  float m = -INFINITY, l = 0.0f, y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  bool any = false;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float2 v = i0 + lane < n ? ml(i0 + lane) : make_float2(-INFINITY, -1.0f);
+    const unsigned there = __ballot_sync(0xffffffffu, !(v.y < 0.0f));
+    any |= there != 0;
+    float top = v.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float to = fmaxf(m, top), corr = exp2f(m - shift_of(to));  // (0 on the first)
+    m = to;
+    l *= corr;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= corr;
+    const float f = exp2f(v.x - shift_of(m));
+    if (there >> lane & 1) l = fmaf(f, v.y, l);
+    const int k = min(32, n - i0);
+#pragma unroll 2
+    for (int i = lane >> 3; i < k + 3 - (k + 3) % 4; i += 4) {
+      const float fi = __shfl_sync(0xffffffffu, f, i & 31);
+      if (i < k && (there >> i & 1)) {
+        float z[8];
+        load8(o(i0 + i) + 8 * (lane & 7), z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(fi, z[e], y[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y[e] += __shfl_xor_sync(0xffffffffu, y[e], 8);
+    y[e] += __shfl_xor_sync(0xffffffffu, y[e], 16);
+    y[e] = any ? y[e] / l : 0.0f;
+  }
+  if (lane < 8) store8(static_cast<TIO*>(a.o) + row * kD + 8 * lane, y);
+  if (a.lse && lane == 0) a.lse[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Two fp32 numbers at once.
@@ -100,32 +301,82 @@ __device__ __forceinline__ float2 pair_mul(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// The largest of three (NaN counts as nothing).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+// This warpgroup's registers a thread, of those the block was launched with.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+// 8 columns of this thread's lane, as tmem_ld16 and tmem_st16.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld8(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+// One K = 16 step of a product, as umma_ss_lo and umma_ts_lo, with the choice
+// between setting and adding known to the compiler: from a register it costs
+// more to bring to the tensor core than the rest of the step's operands.
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+template <bool ADD>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t hi, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(hi), "r"(idesc), "n"(ADD ? 1 : 0)
+      : "memory");
+}
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-
-// What 2^(x - m) is taken against: 0 for a maximum of -inf (no key, or logits
-// that are all -inf), so that -inf - m stays -inf.
-__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // host side
 int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream);
 int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos_T, void* stream);
 int launch_cross_fwd_simt(const CrossArgs& a, void* stream);
-// Tiles of 128 rows of the tensor-core kernels: 2^lgR queries of 128 / 2^lgR
-// heads of a KV head each, so that short sequences share tiles; tile i holds
-// head group i mod groups of query block i / groups (queries behind a length come last).
-struct RowTiles {
-  int lgR, groups, blocks, tiles;
-};
-RowTiles row_tiles(int G, int Tq);
 // A tensor map of bf16 rows: boxes of `heads` x `rows` rows, 128-byte swizzle (sfa_api.cu).
 int make_rows4_map(CUtensorMap* m, const void* base, int T, int H, int B, int64_t s_t, int64_t s_h, int64_t s_b, int box_rows, int box_heads);
 inline int make_view_map(CUtensorMap* m, const void* base, int T, int H, int B, const Strides& s, int rows, int heads) {
   return make_rows4_map(m, base, T, H, B, s.t, s.h, s.b, rows, heads);
 }
-// bf16; two: queries as two bf16 parts, the second a sequence's stride behind the first
-int launch_cross_fwd_tc(const CrossArgs& a, bool two, void* stream);
+// Forward pass, bf16; ws: cross_tc_bytes.
+size_t cross_tc_bytes(int B, int Hkv, int G, int Tq, int Tk);
+int launch_cross_fwd_tc(const CrossArgs& a, void* ws, void* stream);
+// The same into parts, the batch as one sequence of queries, those as two bf16
+// parts, a sequence's stride apart; and the join with the sequences' own rows'
+// a.splits parts, which stand behind the prefix's in out.part_o and out.part_ml.
+int launch_prefix_tc(const CrossArgs& a, void* ws, void* stream);
+int launch_prefix_join(const CrossArgs& prefix, const CrossArgs& out, void* ws, const int32_t* pos, int T, void* stream);
 int launch_cross_bwd_tc(const CrossArgs& a, bool dkv, void* stream);  // bf16
 int launch_cross_dq_simt(const CrossArgs& a, void* stream);           // fp32
 int launch_cross_dkv_simt(const CrossArgs& a, void* stream);

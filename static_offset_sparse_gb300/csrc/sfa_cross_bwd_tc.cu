@@ -17,7 +17,6 @@
 // accumulations when P and dS are back.  P and dS are rounded to bf16 for
 // their products; everything else is fp32.
 #include "sfa_cross.cuh"
-#include "sfa_umma.cuh"
 
 namespace sfa {
 
@@ -66,20 +65,6 @@ __device__ __forceinline__ BtItem bt_item(const CrossArgs& a, const BtWork& w, i
   return it;
 }
 
-// Query and head of row r of a row tile.
-struct RowOf {
-  int t, g;
-  bool mine;
-};
-__device__ __forceinline__ RowOf row_of(const CrossArgs& a, const RowTiles& rt, int tile, int r) {
-  const int tb = tile / rt.groups, hb = tile - tb * rt.groups;
-  RowOf o;
-  o.t = (tb << rt.lgR) + (r & ((1 << rt.lgR) - 1));
-  o.g = (hb << (7 - rt.lgR)) + (r >> rt.lgR);
-  o.mine = tile < rt.tiles && o.t < a.Tq && o.g < a.G;
-  return o;
-}
-
 template <bool DKV>
 __global__ void __launch_bounds__(kBtThreads, 1)
     cross_bwd_tc_kernel(const CrossArgs a, const BtWork w, const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
@@ -88,7 +73,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
   __shared__ BtShared sh;
   const uint32_t smem = smem_u32(smem_raw) + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem + 2 * 2 * kBtTile;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform, and known to be)
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < kBtStages; ++i) {

@@ -183,37 +183,12 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, cons
   const int lane = threadIdx.x & 31;
   const int64_t rows = a.rows, row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
-  bool none = false;
+  int n = a.splits;
   if (pos) {
     const int p = pos[row / a.Hq];
-    none = p < 0 || p >= T;
+    if (p < 0 || p >= T) n = 0;
   }
-  float m = -INFINITY;
-  if (!none) {
-    for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, a.part_ml[s * rows + row].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  }
-  const float sh = shift_of(m);
-  float l = 0.0f, y0 = 0.0f, y1 = 0.0f;
-  bool any = false;
-  for (int s0 = 0; s0 < a.splits && !none; s0 += 32) {
-    const float2 ml = s0 + lane < a.splits ? a.part_ml[(s0 + lane) * rows + row] : make_float2(-INFINITY, -1.0f);
-    const float f = exp2f(ml.x - sh);
-    const unsigned there = __ballot_sync(0xffffffffu, !(ml.y < 0.0f));  // (a part without a key has no o)
-    any |= there != 0;
-    for (unsigned left = there; left; left &= left - 1) {
-      const int i = __ffs(left) - 1;
-      const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, ml.y, i);
-      float2 v = *reinterpret_cast<const float2*>(a.part_o + ((s0 + i) * rows + row) * kD + 2 * lane);
-      l = fmaf(fi, li, l);
-      y0 = fmaf(fi, v.x, y0);
-      y1 = fmaf(fi, v.y, y1);
-    }
-  }
-  const float inv = 1.0f / l;
-  store2(static_cast<TIO*>(a.o) + row * kD + 2 * lane, any ? y0 * inv : 0.0f, any ? y1 * inv : 0.0f);
-  if (a.lse && lane == 0) a.lse[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+  join_row<TIO>(a, row, n, lane, [&](int i) { return a.part_ml[i * rows + row]; }, [&](int i) { return a.part_o + (i * rows + row) * kD; });
 }
 
 int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos_T, void* stream) {
