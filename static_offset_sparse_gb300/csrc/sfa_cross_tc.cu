@@ -1,17 +1,23 @@
 // Forward pass of attention to states of another length on the fifth-generation
 // tensor cores (bf16).
 //
-// A unit is two tiles of 128 rows of one (sequence, KV head), a step 128 of their
+// A unit is two tiles of 128 rows of one (sequence, KV head), a step 96 of their
 // keys; both tiles use the same keys and values.  Per step and tile
-//   one thread issues S = Q K^T (128 x 128 sums in tensor memory);
-//   four warps, a thread a row (a lane of tensor memory), take the row's 128
-//     logits into registers at once, which frees S for the next step's product
-//     while they work: the maximum, 2^x, the sum, and P in bf16 back into tensor
-//     memory;
+//   one thread issues S = Q K^T (128 x 96 sums in tensor memory);
+//   four warps, a thread a row (a lane of tensor memory), take 2^x of the row's 96
+//     logits and their sum, and put P in bf16 over them;
 //   the issuing thread takes P as the left operand of O += P V, O in tensor memory.
-// A row's sums are moved to a new maximum only where that grew by more than 2^8
-// (P and O are then at most 2^8 times too large, which fp32 and bf16 hold as well
-// as 1).  The sums are taken in fp32 from probabilities before their rounding to
+// 96 keys, because two such S for each of two tiles fit tensor memory beside O: the
+// next S is there when a step's exponentials end.  (With 128, one S and P beside it,
+// a step took the chain of both, 2300 to 3000 clocks where the tensor cores need
+// 1024 and the exponentials as many.)
+//
+// The shift of 2^x is the maximum of a row's first 96 logits.  Later steps do not look
+// for theirs: a row whose sum over a step passes kSumLimit (or is no number) takes the
+// step again, with its maximum, and moves its sums; P, O and the sum are thus at most
+// kSumLimit times too large, which fp32 and bf16 hold as well as 1.  Maxima cost a
+// fifth of the instructions, and the step's first 200 clocks.  The sums are taken in
+// fp32 from probabilities before their rounding to
 // bf16.  A unit's first products start under the last unit's outputs: one warp walks
 // the CTA's share of the steps and writes down each piece a little ahead, the
 // others read it there (each for itself, they waited 1000 clocks a piece for lengths
@@ -26,19 +32,20 @@ constexpr int kTcThreads = 384;  // 2 x 4 warps of softmax, a copying warp, two 
 // Registers: 168 a thread at launch, 3 x 128 x 168 = 2 x 128 x 216 + 128 x 72.
 constexpr int kTcMoreRegs = 216, kTcFewerRegs = 72;
 constexpr int kTcTile = 128 * 128;  // bytes of 128 rows of 64 bf16
-constexpr int kTcCols = 512, kTcTileCols = 256, kTcP = 128, kTcO = 192;  // tensor memory columns of a tile: S, P, O
-constexpr float kGrow = 8.0f;  // log2 of how far P and O may be too large
+constexpr int kKeys = 96, kKeyTile = kKeys * 128;  // keys of a step, bytes of that many rows
+constexpr int kTcCols = 512, kTcTileCols = 256, kTcO = 2 * kKeys;  // tensor memory columns of a tile: S or P of even steps, of odd ones, O
+constexpr float kSumLimit = 16384.0f;
 // Maxima beyond this are taken from x before the multiplication: a fused
 // 2^(x c - m c) would keep what rounding m c dropped, a factor of 2^(2^-5) and more.
 constexpr float kFar = 1048576.0f;
 
 template <int PARTS>
 struct TcShape {
-  static constexpr int kSlots = 6;                   // key and value tiles in flight
+  static constexpr int kSlots = 8;                   // key and value tiles in flight
   static constexpr int kQBufs = PARTS == 1 ? 2 : 1;  // units whose queries are there
   static constexpr int kQBytes = 2 * PARTS * kTcTile;
   static constexpr int kOut = 8 * 4096;              // outputs on their way: 32 rows of 128 bytes a warp
-  static constexpr int kSmem = kQBufs * kQBytes + kSlots * kTcTile + kOut + 1024;
+  static constexpr int kSmem = kQBufs * kQBytes + kSlots * kKeyTile + kOut + 1024;
 };
 
 constexpr int kPlans = 4;  // pieces written down ahead
@@ -53,7 +60,7 @@ struct TcPiece {
 
 struct TcShared {
   uint64_t full[8], empty[8], q_full[2], q_empty[2];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];  // by tile
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by tile and step's parity
   uint64_t v_ready[4];  // by value slot: what stands behind the last key is zeros
   uint64_t plan_full[kPlans], plan_empty[kPlans];
   TcPiece plan[kPlans];
@@ -68,6 +75,62 @@ struct TcWork {
   float2* place_ml;  // [2 CTAs][256]
   int4* split;       // [CTAs]: the unit that a CTA begins and does not end: sequence, KV head, pair of tiles, parts (0: none)
 };
+
+// A row's logits of a step, -inf from the `left`th on.
+__device__ __forceinline__ void row_logits(uint32_t s, int left, float* x) {
+  tmem_take96(s, x);
+  if (left < kKeys) {
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e)
+      if (e >= left) x[e] = -INFINITY;
+  }
+}
+
+__device__ __forceinline__ float row_top(const float* v) {
+  float tops[4] = {fmaxf(v[0], v[1]), fmaxf(v[2], v[3]), fmaxf(v[4], v[5]), fmaxf(v[6], v[7])};
+#pragma unroll
+  for (int e = 8; e < kKeys; e += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], v[e + 2 * i], v[e + 2 * i + 1]);
+  return max3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
+}
+
+// x to P = 2^(x c - m c) in bf16, two a word; returns their sum.
+__device__ __forceinline__ float row_exp(float* x, float mc) {
+  const float2 c2 = make_float2(kLogitScale, kLogitScale), off2 = make_float2(-mc, -mc);
+  float2 sum[4] = {};
+#pragma unroll
+  for (int e = 0; e < kKeys; e += 2) {
+    const float2 y = pair_fma(make_float2(x[e], x[e + 1]), c2, off2);
+    const float2 p = make_float2(ex2(y.x), ex2(y.y));
+    sum[(e >> 1) & 3] = pair_add(sum[(e >> 1) & 3], p);
+    x[e >> 1] = __uint_as_float(pack_bf16(p.x, p.y));
+  }
+  const float2 both = pair_add(pair_add(sum[0], sum[1]), pair_add(sum[2], sum[3]));
+  return both.x + both.y;
+}
+
+// The same for any m, in a loop, P over the logits that have been read.
+__device__ __forceinline__ float row_exp_any(uint32_t s, int left, float m) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < kKeys; c += 16) {
+    float v[16];
+    tmem_ld8(s + c, v);
+    tmem_ld8(s + c + 8, v + 8);
+    tmem_wait_ld8(v);
+    tmem_wait_ld8(v + 8);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      v[e] = c + e < left ? ex2((v[e] - m) * kLogitScale) : 0.0f;
+      sum += v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(pack_bf16(v[2 * e], v[2 * e + 1]));
+    tmem_st8(s + c / 2, v);
+  }
+  return sum;
+}
 
 __device__ __forceinline__ void st_stage(uint32_t at, float a, float b, float c, float d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)),
@@ -94,10 +157,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.q_full[i]), 1);
       mbar_init(smem_u32(&sh.q_empty[i]), 2);
-      mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.s_free[i]), 4);
-      mbar_init(smem_u32(&sh.p_full[i]), 4);
-      mbar_init(smem_u32(&sh.pv_done[i]), 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(smem_u32(&sh.s_full[i][j]), 1);
+        mbar_init(smem_u32(&sh.p_full[i][j]), 4);
+        mbar_init(smem_u32(&sh.pv_done[i][j]), 1);
+      }
     }
     for (int i = 0; i < Shape::kSlots / 2; ++i) mbar_init(smem_u32(&sh.v_ready[i]), 1);
     for (int i = 0; i < kPlans; ++i) {
@@ -114,7 +178,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   auto counts = [&](int b, int& units, int& steps) {
     const int nk = a.keys(b);
-    steps = (nk + 127) >> 7;
+    steps = (nk + kKeys - 1) / kKeys;
     units = nk > 0 ? a.Hkv * ((w.rt.used(a.queries(b)) + 1) >> 1) : 0;
   };
   Walk wk;
@@ -149,19 +213,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     more_registers<kTcMoreRegs>();
     const int T = warp >> 2, r = tid & 127;
     const uint32_t tl = tm + kTcTileCols * T + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
-    // rows of tiles without work: zeros (a split step's parts have no such rows)
+    // rows of tiles without work: zeros (parts have no such rows)
     if (!a.parts)
-      for (int x = blockIdx.x; x < a.B * a.Hkv; x += gridDim.x) {
-        const int b = x / a.Hkv, kvh = x - b * a.Hkv;
-#pragma unroll 1
-        for (int tile = (a.keys(b) > 0 ? (w.rt.used(a.queries(b)) + 1) & ~1 : 0) + T; tile < w.rt.tiles; tile += 2) {
-          const RowOf ro = row_of(a, w.rt, tile, r);
-          if (!ro.mine) continue;
-          const int64_t row = a.row(b, kvh, ro.t * a.G + ro.g);
+      for (int64_t x = blockIdx.x; x < (int64_t)a.B * a.Hkv * w.rt.tiles; x += gridDim.x) {
+        const int bh = (int)(x / w.rt.tiles), tile = (int)(x - (int64_t)bh * w.rt.tiles), b = bh / a.Hkv;
+        if (tile < (a.keys(b) > 0 ? (w.rt.used(a.queries(b)) + 1) & ~1 : 0)) continue;
+        const RowOf ro = row_of(a, w.rt, tile, r);
+        if (!ro.mine) continue;
+        const int64_t row = a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g);
 #pragma unroll
-          for (int c = 0; c < 64; c += 8) *reinterpret_cast<uint4*>(static_cast<bf16*>(a.o) + row * kD + c) = make_uint4(0, 0, 0, 0);
-          if (a.lse) a.lse[row] = -INFINITY;
-        }
+        for (int c = 32 * T; c < 32 * T + 32; c += 8) *reinterpret_cast<uint4*>(static_cast<bf16*>(a.o) + row * kD + c) = make_uint4(0, 0, 0, 0);
+        if (a.lse && T == 0) a.lse[row] = -INFINITY;
       }
     int np = 0;  // steps of this tile
     for (;;) {
@@ -172,44 +234,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         steps = T == 0 || p.two ? p.steps : 0;
         keys = p.k1 - p.k0;
       }
-      float m = -INFINITY, mc = 0.0f, l = 0.0f;  // what the shift of 2^x was set by, the shift
+      float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < steps; ++j, ++np) {
-        wait(&sh.s_full[T], np);
+        wait(&sh.s_full[T][np & 1], np >> 1);
         if (dead) break;
         tc05_fence_after();
-        float v[128];
+        const uint32_t ts = tl + kKeys * (np & 1);
+        const int left = keys - kKeys * j;
+        float sum = INFINITY;
+        {
+          float v[kKeys];
+          row_logits(ts, left, v);
+          if (j == 0) m = row_top(v);
+          if (__all_sync(0xffffffffu, fabsf(m) <= kFar)) {
+            sum = row_exp(v, m * kLogitScale);
+            if (__all_sync(0xffffffffu, sum <= kSumLimit)) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld32(tl + c, v + c);
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_wait_ld32(v + c);
-        tc05_fence_before();
-        arrive(&sh.s_free[T]);
-        const int left = keys - 128 * j;
-        if (left < 128) {
-#pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e >= left) v[e] = -INFINITY;
-        }
-        float tops[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int e = 4; e < 124; e += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], v[e + 2 * i], v[e + 2 * i + 1]);
-        const float top = fmaxf(max3(tops[0], tops[1], max3(v[124], v[125], v[126])), max3(tops[2], tops[3], v[127]));
-        const bool grown = j == 0 || top > m + kGrow / kLogitScale;
-        if (__any_sync(0xffffffffu, grown)) {
-          float corr = 1.0f;
-          if (grown) {
-            const float to = fmaxf(m, top);
-            corr = ex2((m - shift_of(to)) * kLogitScale);  // 0 on the first keys
-            m = to;
-            mc = shift_of(m) * kLogitScale;
-            l *= corr;
+              for (int c = 0; c < kKeys / 2; c += 16) tmem_st16(ts + c, v + c);
+            } else {
+              sum = INFINITY;
+            }
           }
-          if (j > 0) {
-            wait(&sh.pv_done[T], np - 1);
-            tc05_fence_after();
+        }
+        if (__any_sync(0xffffffffu, sum == INFINITY)) {  // (of all lanes or none)
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 8) {
+            float v[8];
+            tmem_ld8(ts + c, v);
+            tmem_wait_ld8(v);
 #pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, c + e < left ? v[e] : -INFINITY);
+          }
+          const float to = fmaxf(m, top), corr = ex2((m - shift_of(to)) * kLogitScale);  // 0 on the first keys
+          m = to;
+          l *= corr;
+          if (j > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
+            wait(&sh.pv_done[T][(np - 1) & 1], (np - 1) >> 1);
+            tc05_fence_after();
+#pragma unroll 1
             for (int c = 0; c < 64; c += 8) {
               float o[8];
               tmem_ld8(tl + kTcO + c, o);
@@ -219,39 +282,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tmem_st8(tl + kTcO + c, o);
             }
           }
+          sum = row_exp_any(ts, left, shift_of(m));
         }
-        float off = -mc;
-        if (__any_sync(0xffffffffu, !(fabsf(mc) <= kFar))) {
-          off = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 128; ++e) v[e] -= shift_of(m);
-        }
-        if (j > 0) wait(&sh.pv_done[T], np - 1);  // the last step's P has been read
-        if (dead) break;
-        tc05_fence_after();
-        const float2 c2 = make_float2(kLogitScale, kLogitScale), off2 = make_float2(off, off);
-        float2 sum[4] = {};
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-#pragma unroll
-          for (int e = c; e < c + 32; e += 2) {
-            const float2 y = pair_fma(make_float2(v[e], v[e + 1]), c2, off2);
-            const float2 pr = make_float2(ex2(y.x), ex2(y.y));
-            sum[(e >> 1) & 3] = pair_add(sum[(e >> 1) & 3], pr);
-            v[c + ((e - c) >> 1)] = __uint_as_float(pack_bf16(pr.x, pr.y));
-          }
-          tmem_st16(tl + kTcP + c / 2, v + c);
-        }
-        const float2 both = pair_add(pair_add(sum[0], sum[1]), pair_add(sum[2], sum[3]));
-        l += both.x + both.y;
+        l += sum;
         tmem_wait_st();
         tc05_fence_before();
-        arrive(&sh.p_full[T]);
+        arrive(&sh.p_full[T][np & 1]);
       }
-      if (steps > 0 && !dead) {
-        wait(&sh.pv_done[T], np - 1);
+      if (steps > 0) {
+        wait(&sh.pv_done[T][(np - 1) & 1], (np - 1) >> 1);
         tc05_fence_after();
       }
+      const float mc = shift_of(m) * kLogitScale;
       if (dead) break;
       const int plan = pieces % kPlans, code = sh.rows[plan][tid], place = sh.plan[plan].place;
       const bool mine = code != INT_MIN, none = code < 0, whole = place < 0;
@@ -259,7 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // parts: (o, m, l) as they are; else o / l.  Through shared memory, so that eight
       // lanes write a row's 128 bytes together.  (Loops: this code runs once a piece, and
       // fetching it costs more than running it.)
-      const uint32_t stage = ring + Shape::kSlots * kTcTile + warp * 4096;
+      const uint32_t stage = ring + Shape::kSlots * kKeyTile + warp * 4096;
       const bool part = a.parts || !whole;
       char* const to = part ? reinterpret_cast<char*>(whole ? a.part_o : w.place_o) : static_cast<char*>(a.o);
       const int at = part && !whole ? place + tid : row;
@@ -333,7 +375,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
         ++nq;
-        for (int j = p.k0; j < p.k1 && !dead; j += 128)
+        for (int j = p.k0; j < p.k1 && !dead; j += kKeys)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int slot = n % Shape::kSlots;
@@ -341,8 +383,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (dead) break;
             if (elect_one()) {
               const uint32_t bar = smem_u32(&sh.full[slot]);
-              mbar_expect_tx(bar, kTcTile);
-              tma_load_4d(ring + slot * kTcTile, kv ? &vm : &km, 0, j, p.kvh, p.b, bar);
+              mbar_expect_tx(bar, kKeyTile);
+              tma_load_4d(ring + slot * kKeyTile, kv ? &vm : &km, 0, j, p.kvh, p.b, bar);
             }
             __syncwarp();
             ++n;
@@ -359,8 +401,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ---- products of tile T: a step's logits are issued before the last step's
       // outputs.  A warp a tile: one for both took 2800 clocks a step to issue what the
       // tensor cores do in 1024, two take half each, side by side.
-      constexpr uint32_t idS = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
-      constexpr uint32_t kHi = smem_desc_hi(1024), kTileU = kTcTile / 16;
+      constexpr uint32_t idS = idesc_bf16(128, kKeys, false, false), idO = idesc_bf16(128, 64, false, true);
+      constexpr uint32_t kHi = smem_desc_hi(1024), kTileU = kTcTile / 16, kKeyU = kKeyTile / 16;
       const int T = warp - 9;
       const bool lead = elect_one();
       const uint32_t q0 = smem_desc_lo(smem, 16) + T * PARTS * kTileU, k0 = smem_desc_lo(ring, 16), v0 = smem_desc_lo(ring, 8192);
@@ -370,21 +412,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto outputs = [&]() {  // O (+)= P V of step n - 1
         const int slot = (2 * n - 1) % Shape::kSlots;
         wait(&sh.v_ready[slot >> 1], (n - 1) / (Shape::kSlots / 2));
-        if (had) wait(&sh.p_full[T], ns - 1);
+        if (had) wait(&sh.p_full[T][(ns - 1) & 1], (ns - 1) >> 1);
         if (dead) return;
         if (lead) {
           if (had) {
             tc05_fence_after();
-            const uint32_t v = v0 + slot * kTileU;
+            const uint32_t v = v0 + slot * kKeyU, p = d + kKeys * ((ns - 1) & 1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)  // 16 keys: two groups of 8 rows, 8 columns of P
+            for (int i = 0; i < kKeys / 16; ++i)  // 16 keys: two groups of 8 rows, 8 columns of P
               if (i > 0)
-                mma_ts<true>(d + kTcO, d + kTcP + 8 * i, v + 128 * i, kHi, idO);
+                mma_ts<true>(d + kTcO, p + 8 * i, v + 128 * i, kHi, idO);
               else if (begin)
-                mma_ts<false>(d + kTcO, d + kTcP, v, kHi, idO);
+                mma_ts<false>(d + kTcO, p, v, kHi, idO);
               else
-                mma_ts<true>(d + kTcO, d + kTcP, v, kHi, idO);
-            umma_commit(smem_u32(&sh.pv_done[T]));
+                mma_ts<true>(d + kTcO, p, v, kHi, idO);
+            umma_commit(smem_u32(&sh.pv_done[T][(ns - 1) & 1]));
           }
           umma_commit(smem_u32(&sh.empty[slot]));
         }
@@ -399,19 +441,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int j = 0; j < steps && !dead; ++j) {
           const int at = 2 * n, slot = at % Shape::kSlots;
           wait(&sh.full[slot], at / Shape::kSlots);  // (not only its own: what it frees is there by then)
-          if (mine && ns > 0) wait(&sh.s_free[T], ns - 1);
+          if (mine && ns > 1) wait(&sh.pv_done[T][ns & 1], (ns - 2) >> 1);  // P of the step before the last lies where S goes
           if (dead) break;
           if (lead) {
             if (mine) {
               tc05_fence_after();
-              const uint32_t q = q0 + buf * 2 * PARTS * kTileU, k = k0 + slot * kTileU;
+              const uint32_t q = q0 + buf * 2 * PARTS * kTileU, k = k0 + slot * kKeyU, to = d + kKeys * (ns & 1);
 #pragma unroll
               for (int i = 0; i < 4 * PARTS; ++i)
                 if (i > 0)
-                  mma_ss<true>(d, q + (i >> 2) * kTileU + 2 * (i & 3), k + 2 * (i & 3), kHi, idS);
+                  mma_ss<true>(to, q + (i >> 2) * kTileU + 2 * (i & 3), k + 2 * (i & 3), kHi, idS);
                 else
-                  mma_ss<false>(d, q, k, kHi, idS);
-              umma_commit(smem_u32(&sh.s_full[T]));
+                  mma_ss<false>(to, q, k, kHi, idS);
+              umma_commit(smem_u32(&sh.s_full[T][ns & 1]));
             }
             umma_commit(smem_u32(&sh.empty[slot]));
             if (j == steps - 1) umma_commit(smem_u32(&sh.q_empty[buf]));
@@ -429,8 +471,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (dead) {  // products under way end before their memory goes
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
         for (int i = max(0, ns - 1); i <= ns; ++i) {
-          mbar_wait_bounded(smem_u32(&sh.s_full[T]), i & 1, a.wait_cycles);
-          if (i > 0) mbar_wait_bounded(smem_u32(&sh.pv_done[T]), (i - 1) & 1, a.wait_cycles);
+          mbar_wait_bounded(smem_u32(&sh.s_full[T][i & 1]), (i >> 1) & 1, a.wait_cycles);
+          if (i > 0) mbar_wait_bounded(smem_u32(&sh.pv_done[T][(i - 1) & 1]), ((i - 1) >> 1) & 1, a.wait_cycles);
         }
       }
     } else {
@@ -456,8 +498,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             p.b = wk.b;
             p.kvh = kvh;
             p.tile = tile;
-            p.k0 = 128 * wk.s0;
-            p.k1 = min(128 * wk.s1, nk);
+            p.k0 = kKeys * wk.s0;
+            p.k1 = min(kKeys * wk.s1, nk);
             p.two = two;
             p.place = wk.whole() ? -1 : (2 * blockIdx.x + (wk.s0 == 0)) * 256;
             sh.plan[i] = p;
@@ -479,15 +521,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         while (planned < x + 3 && !ended && !dead) plan();
         if (x == planned - 1 && ended) break;
         const int k0 = sh.plan[x % kPlans].k0, k1 = sh.plan[x % kPlans].k1;
-        for (int j = k0; j < k1 && !dead; j += 128, ++n) {
+        for (int j = k0; j < k1 && !dead; j += kKeys, ++n) {
           const int at = 2 * n + 1, slot = at % Shape::kSlots;
           wait(&sh.full[slot], at / Shape::kSlots);
           if (dead) break;
-          if (k1 - j < 128) {
+          if (k1 - j < kKeys) {
 #pragma unroll 1
-            for (int r = k1 - j + lane; r < 128; r += 32)
+            for (int r = k1 - j + lane; r < kKeys; r += 32)
 #pragma unroll
-              for (int c = 0; c < 8; ++c) st_stage(ring + slot * kTcTile + r * 128 + 16 * c, 0.0f, 0.0f, 0.0f, 0.0f);
+              for (int c = 0; c < 8; ++c) st_stage(ring + slot * kKeyTile + r * 128 + 16 * c, 0.0f, 0.0f, 0.0f, 0.0f);
             fence_async_smem();
           }
           arrive(&sh.v_ready[slot >> 1]);
@@ -612,7 +654,7 @@ RowTiles row_tiles(int G, int Tq) {
 static Shares tc_shares(int B, int Hkv, const RowTiles& rt, int Tk) {
   Shares s;
   const int64_t units = (int64_t)B * Hkv * ((rt.tiles + 1) / 2);
-  s.set(units * ((Tk + 127) / 128 + kUnitCost), units, kSMs);
+  s.set(units * ((Tk + kKeys - 1) / kKeys + kUnitCost), units, kSMs);
   return s;
 }
 
@@ -637,8 +679,8 @@ template <int PARTS>
 static int fwd_tc(const CrossArgs& a, const TcWork& w, int ctas, cudaStream_t st) {
   CUtensorMap qm, km, vm;
   int rc = make_view_map(&qm, a.q, a.Tq, a.Hq, PARTS == 2 ? 2 : a.B, a.qs, 1 << w.rt.lgR, 128 >> w.rt.lgR);
-  if (rc == SFA_OK) rc = make_view_map(&km, a.k, a.Tk, a.Hkv, a.B, a.ks, 128, 1);
-  if (rc == SFA_OK) rc = make_view_map(&vm, a.v, a.Tk, a.Hkv, a.B, a.vs, 128, 1);
+  if (rc == SFA_OK) rc = make_view_map(&km, a.k, a.Tk, a.Hkv, a.B, a.ks, kKeys, 1);
+  if (rc == SFA_OK) rc = make_view_map(&vm, a.v, a.Tk, a.Hkv, a.B, a.vs, kKeys, 1);
   if (rc != SFA_OK) return rc;
   auto* f = cross_fwd_tc_kernel<PARTS>;
   static_assert(TcShape<PARTS>::kSmem + sizeof(TcShared) + 1024 <= 228 * 1024, "shared memory of an SM");
@@ -654,7 +696,7 @@ int launch_cross_fwd_tc(const CrossArgs& a, void* ws, void* stream) {
   const int rc = fwd_tc<1>(a, w, ctas, (cudaStream_t)stream);
   // where all lengths are alike and each CTA has whole units, there is nothing to join
   const Shares s = tc_shares(a.B, a.Hkv, w.rt, a.Tk);
-  if (rc != SFA_OK || ctas == 1 || (!a.q_len && !a.kv_len && s.rest == 0 && s.share % ((a.Tk + 127) / 128 + kUnitCost) == 0)) return rc;
+  if (rc != SFA_OK || ctas == 1 || (!a.q_len && !a.kv_len && s.rest == 0 && s.share % ((a.Tk + kKeys - 1) / kKeys + kUnitCost) == 0)) return rc;
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
   const int64_t units = (int64_t)a.B * a.Hkv * ((w.rt.tiles + 1) / 2);
   const bool few = 4 * units <= ctas;
@@ -675,7 +717,7 @@ int launch_prefix_join(const CrossArgs& prefix, const CrossArgs& out, void* ws, 
   const TcWork w = tc_work(prefix, ws, &ctas);
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
   const cudaError_t e = launch_pdl(prefix_join_kernel, dim3((unsigned)((out.rows + 7) / 8)), dim3(256), 0, (cudaStream_t)stream, out, w,
-                                   tc_shares(1, prefix.Hkv, w.rt, prefix.Tk), (prefix.Tk + 127) / 128, pos, T);
+                                   tc_shares(1, prefix.Hkv, w.rt, prefix.Tk), (prefix.Tk + kKeys - 1) / kKeys, pos, T);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
