@@ -12,7 +12,6 @@ static bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)
 
 // lse * log2(e) and delta = sum(o * dO) of each row, eight lanes a row; rows
 // that count for nothing get +inf, which makes their probabilities 0.
-template <typename TIO>
 __global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, float2* stat) {
   pdl_launch_dependents();
   pdl_wait();
@@ -27,8 +26,8 @@ __global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, floa
   }
   if (valid) {
     float o[8], g[8];
-    load8(static_cast<const TIO*>(a.out) + row * kD + d8, o);
-    load8(static_cast<const TIO*>(a.dO) + row * kD + d8, g);
+    load8(static_cast<const float*>(a.out) + row * kD + d8, o);
+    load8(static_cast<const float*>(a.dO) + row * kD + d8, g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(o[e], g[e], sum);
   }
@@ -38,7 +37,6 @@ __global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, floa
 }
 
 // out = the sum of n-number parts, in order.
-template <typename TIO>
 __global__ void __launch_bounds__(256) cross_sum_kernel(const float* parts, int splits, int64_t n, void* out) {
   pdl_launch_dependents();
   pdl_wait();
@@ -51,7 +49,7 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const float* parts, int 
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] += y[e];
   }
-  store8(static_cast<TIO*>(out) + i, x);
+  store8(static_cast<float*>(out) + i, x);
 }
 
 struct PrefixArgs {
@@ -198,25 +196,23 @@ static ForwardPlan forward_plan(const sfa_cross_desc* d) {
   return p;
 }
 
-struct BackwardPlan {
+struct BackwardPlan {  // (what is not bytes is the fp32 kernels')
   int dq_splits, dkv_splits;
   int64_t rows, keys;
   size_t stat, bytes;  // bytes of the rows' numbers, of the workspace
 };
 
 static BackwardPlan backward_plan(const sfa_cross_desc* d) {
-  BackwardPlan p;
+  BackwardPlan p = {};
   const int64_t units = (int64_t)d->B * d->Hkv;
   const int G = d->Hq / d->Hkv;
   if (d->dtype == SFA_BF16) {
-    const int rt = row_tiles(G, d->Tq).tiles, kt = (d->Tk + 127) / 128;
-    p.dq_splits = wave_splits(units * rt, kSMs, kt, 2);
-    p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
-  } else {
-    const int rt = (G * d->Tq + kSimtTile - 1) / kSimtTile, kt = (d->Tk + kSimtTile - 1) / kSimtTile;
-    p.dq_splits = wave_splits(units * rt, 2 * kSMs, kt, 2);
-    p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
+    p.bytes = cross_bwd_tc_bytes(d->B, d->Hkv, G, d->Tq, d->Tk);
+    return p;
   }
+  const int rt = (G * d->Tq + kSimtTile - 1) / kSimtTile, kt = (d->Tk + kSimtTile - 1) / kSimtTile;
+  p.dq_splits = wave_splits(units * rt, 2 * kSMs, kt, 2);
+  p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
   p.rows = (int64_t)d->B * d->Hq * d->Tq;
   p.keys = units * d->Tk;
   p.stat = align256((size_t)p.rows * sizeof(float2));
@@ -226,11 +222,9 @@ static BackwardPlan backward_plan(const sfa_cross_desc* d) {
   return p;
 }
 
-static int launch_sum(const float* parts, int splits, int64_t n, void* out, int dtype, void* stream) {
-  const dim3 grid((unsigned)((n / 8 + 255) / 256));
+static int launch_sum(const float* parts, int splits, int64_t n, void* out, void* stream) {
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
-  const cudaError_t e = dtype == SFA_BF16 ? launch_pdl(cross_sum_kernel<bf16>, grid, dim3(256), 0, (cudaStream_t)stream, parts, splits, n, out)
-                                          : launch_pdl(cross_sum_kernel<float>, grid, dim3(256), 0, (cudaStream_t)stream, parts, splits, n, out);
+  const cudaError_t e = launch_pdl(cross_sum_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, (cudaStream_t)stream, parts, splits, n, out);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
@@ -340,27 +334,26 @@ int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, co
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
+  if (d->dtype == SFA_BF16) return launch_cross_bwd_tc(a, ws, stream);
   float2* const stat = static_cast<float2*>(ws);
   float* const parts = reinterpret_cast<float*>(static_cast<char*>(ws) + p.stat);
   {
     LaunchTimer tm(SFA_KERNEL_CROSS_STAT, stream);
-    const dim3 grid((unsigned)((p.rows + 31) / 32));
-    const cudaError_t e = d->dtype == SFA_BF16 ? launch_pdl(cross_stat_kernel<bf16>, grid, dim3(256), 0, (cudaStream_t)stream, a, stat)
-                                               : launch_pdl(cross_stat_kernel<float>, grid, dim3(256), 0, (cudaStream_t)stream, a, stat);
-    if (e != cudaSuccess) return SFA_ERR_CUDA;
+    if (launch_pdl(cross_stat_kernel, dim3((unsigned)((p.rows + 31) / 32)), dim3(256), 0, (cudaStream_t)stream, a, stat) != cudaSuccess)
+      return SFA_ERR_CUDA;
   }
   a.stat = stat;
   a.splits = p.dq_splits;
   a.parts = a.splits > 1;
   a.part_a = parts;
-  if ((rc = d->dtype == SFA_BF16 ? launch_cross_bwd_tc(a, false, stream) : launch_cross_dq_simt(a, stream)) != SFA_OK) return rc;
-  if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, d->dtype, stream)) != SFA_OK) return rc;
+  if ((rc = launch_cross_dq_simt(a, stream)) != SFA_OK) return rc;
+  if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, stream)) != SFA_OK) return rc;
   a.splits = p.dkv_splits;
   a.parts = a.splits > 1;
   a.part_b = parts + (size_t)a.splits * p.keys * kD;
-  if ((rc = d->dtype == SFA_BF16 ? launch_cross_bwd_tc(a, true, stream) : launch_cross_dkv_simt(a, stream)) != SFA_OK || !a.parts) return rc;
-  if ((rc = launch_sum(a.part_a, a.splits, p.keys * kD, dk, d->dtype, stream)) != SFA_OK) return rc;
-  return launch_sum(a.part_b, a.splits, p.keys * kD, dv, d->dtype, stream);
+  if ((rc = launch_cross_dkv_simt(a, stream)) != SFA_OK || !a.parts) return rc;
+  if ((rc = launch_sum(a.part_a, a.splits, p.keys * kD, dk, stream)) != SFA_OK) return rc;
+  return launch_sum(a.part_b, a.splits, p.keys * kD, dv, stream);
 }
 
 int sfa_prefix_workspace_size(const sfa_prefix_desc* d, size_t* bytes) {

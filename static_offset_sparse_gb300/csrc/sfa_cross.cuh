@@ -426,8 +426,11 @@ int launch_cross_fwd_tc(const CrossArgs& a, void* ws, void* stream);
 // a.splits parts, which stand behind the prefix's in out.part_o and out.part_ml.
 int launch_prefix_tc(const CrossArgs& a, void* ws, void* stream);
 int launch_prefix_join(const CrossArgs& prefix, const CrossArgs& out, void* ws, const int32_t* pos, int T, void* stream);
-int launch_cross_bwd_tc(const CrossArgs& a, bool dkv, void* stream);  // bf16
-int launch_cross_dq_simt(const CrossArgs& a, void* stream);           // fp32
+// Backward pass, bf16; ws: cross_bwd_tc_bytes.
+size_t cross_bwd_tc_bytes(int B, int Hkv, int G, int Tq, int Tk);
+int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream);
+// Backward pass, fp32.
+int launch_cross_dq_simt(const CrossArgs& a, void* stream);
 int launch_cross_dkv_simt(const CrossArgs& a, void* stream);
 constexpr int kStreamRows = 8;  // rows that cross_stream_kernel takes at once
 constexpr int kSimtTile = 64;   // rows and keys of the fp32 kernels' tiles

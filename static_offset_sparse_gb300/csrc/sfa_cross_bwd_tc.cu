@@ -8,61 +8,65 @@
 //          group) pass by:
 //            S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
 //
-// Each sum has one owner, so nothing is added atomically and equal inputs give
-// equal bits; the price is S and dP twice (7 products instead of 5).  In both
-// the probabilities come out of tensor memory the way they go back in as a left
-// operand: a lane per row of the tile that stays, so P and dS never pass shared
-// memory.  Per step one thread issues the next S and dP as soon as eight warps
-// hold this step's in registers (64 columns of both a thread), and the
-// accumulations when P and dS are back.  P and dS are rounded to bf16 for
-// their products; everything else is fp32.
+// Each sum has one owner, or a fixed order of parts, so nothing is added atomically
+// and equal inputs give equal bits; the price is S and dP twice (7 products instead
+// of 5).  In both the probabilities come out of tensor memory the way they go back in
+// as a left operand: a lane per row of the tile that stays, so P and dS never pass
+// shared memory.  Per step one warp issues the next S and dP as soon as eight warps
+// hold this step's in registers (64 columns of both a thread), another the
+// accumulations when P and dS are back.  P and dS are rounded to bf16 for their
+// products; everything else is fp32.  The steps of all tiles are dealt out evenly
+// over the SMs, and planned ahead by one warp, as in the forward pass.
+#include <limits.h>
+
 #include "sfa_cross.cuh"
 
 namespace sfa {
 
-constexpr int kBtThreads = 384;  // 8 warps of softmax, a copying, an issuing and a preparing warp
+constexpr int kBtThreads = 384;  // 8 warps of softmax, a copying warp, two that issue, one that plans and clears rows
+// Registers: 168 a thread at launch, 3 x 128 x 168 = 2 x 128 x 216 + 128 x 72.
+constexpr int kBtMoreRegs = 216, kBtFewerRegs = 72;
 constexpr int kBtTile = 128 * 128;  // bytes of 128 rows of 64 bf16
-constexpr int kBtStages = 4;
-constexpr int kBtSmem = 2 * 2 * kBtTile + kBtStages * 2 * kBtTile + 1024;
+constexpr int kBtStages = 3;
+constexpr int kBtStat = 1024;  // bytes of a row tile's numbers: 128 of -lse log2(e), 128 of -delta
+constexpr int kBtStays = 0, kBtRing = kBtStays + 2 * 2 * kBtTile, kBtOut = kBtRing + kBtStages * 2 * kBtTile,
+              kBtStatRing = kBtOut + 8 * 4096, kBtStatStays = kBtStatRing + kBtStages * kBtStat, kBtSmem = kBtStatStays + 2 * kBtStat + 1024;
+constexpr int kBtPlans = 4;
 // tensor memory: S, dP, P, dS, sums of dq or dk, of dv
 constexpr int kBtDp = 128, kBtP = 256, kBtDs = 320, kBtSum = 384, kBtSum2 = 448;
 
+// A piece as the roles need it.
+struct BtPiece {
+  int steps;                  // none: there are no more pieces
+  int b, kvh, tile, t0;       // the tile that stays, the first that passes by
+  int nq, nk, place;          // place: of its sums, -1 for a whole unit
+};
+
 struct BtShared {
-  uint64_t full[kBtStages], empty[kBtStages], ready[kBtStages];  // ready: rows that count for nothing are zeros, their numbers are there
+  uint64_t full[kBtStages], empty[kBtStages], ready[kBtStages];  // ready: rows that count for nothing are zeros
   uint64_t a_full[2], a_empty[2], s_full, s_free, p_full, done;
-  float nlse[kBtStages][128], ndelta[kBtStages][128];  // of the rows that pass by: -lse log2(e), -delta
+  uint64_t plan_full[kBtPlans], plan_empty[kBtPlans];
+  BtPiece plan[kBtPlans];
+  int rows[kBtPlans][128];  // dq: where a row is; ~ of it for one behind the last query, INT_MIN for none
+  WalkShared walk;
   uint32_t tmem;
 };
 
 struct BtWork {
   RowTiles rt;
-  int key_tiles, items;
+  int key_tiles;
+  const float* stat;  // [B][Hkv][row tiles][2][128]
+  float* places;      // [2 CTAs][128][64], dk and dv: twice that, dv's behind dk's
+  int4* split;        // [CTAs]: the unit that a CTA begins and does not end: sequence, KV head, tile, parts (0: none)
 };
 
-// An item: a tile that stays, and tiles t0 .. t1 - 1 that pass by.
-struct BtItem {
-  int b, kvh, s, tile, t0, t1, nq, nk;
-};
-
-template <bool DKV>
-__device__ __forceinline__ BtItem bt_item(const CrossArgs& a, const BtWork& w, int x) {
-  BtItem it;
-  it.s = x % a.splits;
-  x /= a.splits;
-  const int own = DKV ? w.key_tiles : w.rt.tiles;
-  it.tile = x % own;
-  x /= own;
-  it.kvh = x % a.Hkv;
-  it.b = x / a.Hkv;
-  it.nq = a.queries(it.b);
-  it.nk = a.keys(it.b);
-  const int rows = it.nk > 0 ? w.rt.groups * ((it.nq + (1 << w.rt.lgR) - 1) >> w.rt.lgR) : 0;
-  const int keys = it.nq > 0 ? (it.nk + 127) >> 7 : 0;
-  const bool some = DKV ? it.tile < keys : it.tile < rows;
-  const int n = !some ? 0 : DKV ? rows : keys;
-  it.t0 = (int)((int64_t)n * it.s / a.splits);
-  it.t1 = (int)((int64_t)n * (it.s + 1) / a.splits);
-  return it;
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_out(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 template <bool DKV>
@@ -72,7 +76,6 @@ __global__ void __launch_bounds__(kBtThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ BtShared sh;
   const uint32_t smem = smem_u32(smem_raw) + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const uint32_t ring = smem + 2 * 2 * kBtTile;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform, and known to be)
   pdl_launch_dependents();
   if (tid == 0) {
@@ -83,7 +86,11 @@ __global__ void __launch_bounds__(kBtThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.a_full[i]), 1);
-      mbar_init(smem_u32(&sh.a_empty[i]), 1);
+      mbar_init(smem_u32(&sh.a_empty[i]), DKV ? 1 : 9);  // (dq: the softmax warps read the staying rows' numbers)
+    }
+    for (int i = 0; i < kBtPlans; ++i) {
+      mbar_init(smem_u32(&sh.plan_full[i]), 1);
+      mbar_init(smem_u32(&sh.plan_empty[i]), 10);  // the softmax warps, the copying and one issuing warp
     }
     mbar_init(smem_u32(&sh.s_full), 1);
     mbar_init(smem_u32(&sh.s_free), 8);
@@ -95,11 +102,18 @@ __global__ void __launch_bounds__(kBtThreads, 1)
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
+  if (warp == 8 && lane < 4) prefetch_map(lane == 0 ? &qm : lane == 1 ? &gm : lane == 2 ? &km : &vm);
+  pdl_wait();
+  auto counts = [&](int b, int& units, int& steps) {
+    const int nk = a.keys(b), nq = a.queries(b), keys = (nk + 127) >> 7, rows = w.rt.used(nq);
+    units = nk > 0 && nq > 0 ? a.Hkv * (DKV ? keys : rows) : 0;
+    steps = DKV ? rows : keys;
+  };
+  Walk wk;
   tc05_fence_before();
-  __syncthreads();
+  const bool some = find_walk<kBtThreads>(a.B, counts, sh.walk, wk);  // (with barriers of the CTA)
   tc05_fence_after();
   const uint32_t tm = sh.tmem;
-  pdl_wait();
   bool dead = false;  // a wait ran out: no more waits, no more work
   auto wait = [&](uint64_t* bar, int phase) {  // by a whole warp
     if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait_bounded(smem_u32(bar), phase & 1, a.wait_cycles));
@@ -108,196 +122,85 @@ __global__ void __launch_bounds__(kBtThreads, 1)
     __syncwarp();
     if (lane == 0) bar_arrive(smem_u32(bar));
   };
+  int pieces = 0;  // taken so far
+  // The next piece; false if there is none.
+  auto take = [&](BtPiece& p) {
+    const int i = pieces % kBtPlans;
+    wait(&sh.plan_full[i], pieces / kBtPlans);
+    if (dead) return false;
+    p = sh.plan[i];
+    p.steps = __shfl_sync(0xffffffffu, p.steps, 0);  // (known to be the same in all lanes)
+    return p.steps > 0;
+  };
+  auto give_back = [&]() { arrive(&sh.plan_empty[pieces++ % kBtPlans]); };
 
-  if (warp == 8) {
-    // ---- copies
-    int n = 0, na = 0;  // steps, items so far
-    auto rows = [&](uint32_t dst, const CUtensorMap* m, const BtItem& it, int tile, uint32_t bar) {
-      const int tb = tile / w.rt.groups, hb = tile - tb * w.rt.groups;
-      tma_load_4d(dst, m, 0, tb << w.rt.lgR, it.kvh * a.G + (hb << (7 - w.rt.lgR)), it.b, bar);
-    };
-    for (int x = blockIdx.x; x < w.items && !dead; x += gridDim.x) {
-      const BtItem it = bt_item<DKV>(a, w, x);
-      if (it.t1 <= it.t0) continue;
-      const int buf = na & 1;
-      if (na >= 2) wait(&sh.a_empty[buf], na / 2 - 1);
-      if (dead) break;
-      if (elect_one()) {
-        const uint32_t bar = smem_u32(&sh.a_full[buf]), dst = smem + buf * 2 * kBtTile;
-        mbar_expect_tx(bar, 2 * kBtTile);
-        if (DKV) {
-          tma_load_4d(dst, &km, 0, it.tile * 128, it.kvh, it.b, bar);
-          tma_load_4d(dst + kBtTile, &vm, 0, it.tile * 128, it.kvh, it.b, bar);
-        } else {
-          rows(dst, &qm, it, it.tile, bar);
-          rows(dst + kBtTile, &gm, it, it.tile, bar);
-        }
-      }
-      __syncwarp();
-      ++na;
-      for (int t = it.t0; t < it.t1 && !dead; ++t, ++n) {
-        const int st = n % kBtStages;
-        if (n >= kBtStages) wait(&sh.empty[st], n / kBtStages - 1);
-        if (dead) break;
-        if (elect_one()) {
-          const uint32_t bar = smem_u32(&sh.full[st]), dst = ring + st * 2 * kBtTile;
-          mbar_expect_tx(bar, 2 * kBtTile);
-          if (DKV) {
-            rows(dst, &qm, it, t, bar);
-            rows(dst + kBtTile, &gm, it, t, bar);
-          } else {
-            tma_load_4d(dst, &km, 0, t * 128, it.kvh, it.b, bar);
-            tma_load_4d(dst + kBtTile, &vm, 0, t * 128, it.kvh, it.b, bar);
-          }
-        }
-        __syncwarp();
-      }
-    }
-    if (dead) {  // copies under way end before their memory goes
-      if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
-      for (int i = max(0, n - kBtStages); i < n; ++i) mbar_wait_bounded(smem_u32(&sh.full[i % kBtStages]), (i / kBtStages) & 1, a.wait_cycles);
-      for (int i = max(0, na - 2); i < na; ++i) mbar_wait_bounded(smem_u32(&sh.a_full[i & 1]), (i / 2) & 1, a.wait_cycles);
-    }
-  } else if (warp == 9) {
-    // ---- products
-    constexpr uint32_t idS = idesc_bf16(128, 128, false, false), idO = idesc_bf16(128, 64, false, true);
-    constexpr uint32_t kHi = smem_desc_hi(1024), kTileU = kBtTile / 16;
-    const uint32_t a0 = smem_desc_lo(smem, 16), b0 = smem_desc_lo(ring, 16), bt0 = smem_desc_lo(ring, 8192);
-    int n = 0, na = 0, np = 0;  // steps, items, accumulations so far
-    auto sums = [&](bool begin) {  // of step np
-      wait(&sh.p_full, np);
-      if (dead) return;
-      const int st = np % kBtStages;
-      if (elect_one()) {
-        tc05_fence_after();
-        const uint32_t b = bt0 + 2 * st * kTileU;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) umma_ts_lo(tm + kBtSum, tm + kBtDs + 8 * i, b + 128 * i, kHi, idO, !begin || i > 0);
-        if (DKV)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) umma_ts_lo(tm + kBtSum2, tm + kBtP + 8 * i, b + kTileU + 128 * i, kHi, idO, !begin || i > 0);
-        umma_commit(smem_u32(&sh.done));
-        umma_commit(smem_u32(&sh.empty[st]));
-      }
-      __syncwarp();
-      ++np;
-    };
-    bool had_begin = false;
-    for (int x = blockIdx.x; x < w.items && !dead; x += gridDim.x) {
-      const BtItem it = bt_item<DKV>(a, w, x);
-      if (it.t1 <= it.t0) continue;
-      const int buf = na & 1;
-      wait(&sh.a_full[buf], na / 2);
-      ++na;
-      for (int t = it.t0; t < it.t1 && !dead; ++t) {
-        const int st = n % kBtStages;
-        wait(&sh.full[st], n / kBtStages);
-        wait(&sh.ready[st], n / kBtStages);
-        if (n > 0) wait(&sh.s_free, n - 1);
-        if (dead) break;
-        if (elect_one()) {
-          tc05_fence_after();
-          const uint32_t aa = a0 + 2 * buf * kTileU, b = b0 + 2 * st * kTileU;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma_ss_lo(tm, aa + 2 * i, b + 2 * i, kHi, idS, i > 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma_ss_lo(tm + kBtDp, aa + kTileU + 2 * i, b + kTileU + 2 * i, kHi, idS, i > 0);
-          umma_commit(smem_u32(&sh.s_full));
-          if (t == it.t1 - 1) umma_commit(smem_u32(&sh.a_empty[buf]));
-        }
-        __syncwarp();
-        if (n > 0) sums(had_begin);
-        had_begin = t == it.t0;
-        ++n;
-      }
-    }
-    if (n > 0 && !dead) sums(had_begin);
-    if (dead) {  // products under way end before their memory goes
-      if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
-      if (n > 0) mbar_wait_bounded(smem_u32(&sh.s_full), (n - 1) & 1, a.wait_cycles);
-      if (np > 0) mbar_wait_bounded(smem_u32(&sh.done), (np - 1) & 1, a.wait_cycles);
-    }
-  } else if (warp == 10) {
-    // ---- what the products need besides the copies: rows that count for nothing
-    // are made zeros (they may hold anything, and 0 * NaN would reach every sum),
-    // and the passing rows' numbers are brought
-    int n = 0;
-    for (int x = blockIdx.x; x < w.items && !dead; x += gridDim.x) {
-      const BtItem it = bt_item<DKV>(a, w, x);
-      for (int t = it.t0; t < it.t1 && !dead; ++t, ++n) {
-        const int st = n % kBtStages;
-        if (n >= kBtStages) wait(&sh.empty[st], n / kBtStages - 1);
-        if (dead) break;
-        uint32_t bad = 0;  // of rows lane + 32 i
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = lane + 32 * i;
-          if (DKV) {
-            const RowOf ro = row_of(a, w.rt, t, r);
-            const bool in = ro.mine && ro.t < it.nq;
-            const float2 v = in ? a.stat[a.row(it.b, it.kvh, ro.t * a.G + ro.g)] : make_float2(INFINITY, 0.0f);
-            sh.nlse[st][r] = -v.x;
-            sh.ndelta[st][r] = -v.y;
-            bad |= (in ? 0u : 1u) << i;
-          } else {
-            bad |= (t * 128 + r < it.nk ? 0u : 1u) << i;
-          }
-        }
-        if (__any_sync(0xffffffffu, bad != 0)) {
-          wait(&sh.full[st], n / kBtStages);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (bad >> i & 1)
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(ring + st * 2 * kBtTile + (c >> 3) * kBtTile +
-                                                                               (lane + 32 * i) * 128 + 16 * (c & 7)),
-                             "r"(0)
-                             : "memory");
-          fence_async_smem();
-        }
-        arrive(&sh.ready[st]);
-      }
-    }
-    if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
-  } else if (warp < 8) {
+  if (warp < 8) {
     // ---- P and dS: a thread a row of the tile that stays, 64 of the 128 that pass by
+    more_registers<kBtMoreRegs>();
     const int half = warp >> 2, r = tid & 127;
     const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
-    int n = 0;
-    for (int x = blockIdx.x; x < w.items && !dead; x += gridDim.x) {
-      const BtItem it = bt_item<DKV>(a, w, x);
-      const RowOf ro = DKV ? RowOf{} : row_of(a, w.rt, it.tile, r);
-      float2 own = make_float2(-INFINITY, 0.0f);
-      if (!DKV && ro.mine) {
-        const float2 v = a.stat[a.row(it.b, it.kvh, ro.t * a.G + ro.g)];
-        own = make_float2(-v.x, -v.y);
+    // tiles without work: zeros
+    {
+      const int own = DKV ? w.key_tiles : w.rt.tiles;
+      for (int64_t x = blockIdx.x; x < (int64_t)a.B * a.Hkv * own; x += gridDim.x) {
+        const int bh = (int)(x / own), tile = (int)(x - (int64_t)bh * own), b = bh / a.Hkv;
+        int units, steps;
+        counts(b, units, steps);
+        if (tile < units / a.Hkv) continue;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if (DKV) {
+          const int j = tile * 128 + r;
+          if (j >= a.Tk) continue;
+          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(half ? a.dv : a.dk) + ((int64_t)bh * a.Tk + j) * kD);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) out[c] = zero;
+        } else {
+          const RowOf ro = row_of(a, w.rt, tile, r);
+          if (!ro.mine) continue;
+          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(a.dq) + a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g) * kD + 32 * half);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) out[c] = zero;
+        }
       }
-      for (int t = it.t0; t < it.t1 && !dead; ++t, ++n) {
+    }
+    int n = 0;
+    for (;;) {
+      int steps, nk, t0;
+      {
+        BtPiece p;
+        if (!take(p)) break;
+        steps = p.steps;
+        nk = p.nk;
+        t0 = p.t0;
+      }
+      float2 own = make_float2(-INFINITY, 0.0f);
+      if (!DKV) {
+        const int buf = pieces & 1;
+        wait(&sh.a_full[buf], pieces >> 1);
+        const uint32_t at = smem + kBtStatStays + buf * kBtStat + 4 * r;
+        asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(own.x) : "r"(at) : "memory");
+        asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(own.y) : "r"(at + 512) : "memory");
+        arrive(&sh.a_empty[buf]);
+      }
+      for (int j = 0; j < steps; ++j, ++n) {
         const int st = n % kBtStages;
-        if (DKV) wait(&sh.ready[st], n / kBtStages);
+        if (DKV) wait(&sh.full[st], n / kBtStages);  // (the rows' numbers)
         wait(&sh.s_full, n);
         if (dead) break;
         tc05_fence_after();
         float s[64], d[64];
-        tmem_ld32(tl + 64 * half, s);
-        tmem_ld32(tl + 64 * half + 32, s + 32);
-        tmem_ld32(tl + kBtDp + 64 * half, d);
-        tmem_ld32(tl + kBtDp + 64 * half + 32, d + 32);
-        tmem_wait_ld32(s);
-        tmem_wait_ld32(s + 32);
-        tmem_wait_ld32(d);
-        tmem_wait_ld32(d + 32);
+        tmem_take64(tl + 64 * half, s);
+        tmem_take64(tl + kBtDp + 64 * half, d);
         tc05_fence_before();
         arrive(&sh.s_free);
         const float2 c2 = make_float2(kLogitScale, kLogitScale);
-        const int left = DKV ? 128 : it.nk - 128 * t - 64 * half;  // keys of this half that are there
+        const uint32_t stat = smem + kBtStatRing + st * kBtStat + 256 * half;
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
           float4 nl, nd;
           if (DKV) {
-            nl = *reinterpret_cast<const float4*>(&sh.nlse[st][64 * half + e]);
-            nd = *reinterpret_cast<const float4*>(&sh.ndelta[st][64 * half + e]);
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(nl.x), "=f"(nl.y), "=f"(nl.z), "=f"(nl.w) : "r"(stat + 4 * e));
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(nd.x), "=f"(nd.y), "=f"(nd.z), "=f"(nd.w) : "r"(stat + 512 + 4 * e));
           } else {
             nl = make_float4(own.x, own.x, own.x, own.x);
             nd = make_float4(own.y, own.y, own.y, own.y);
@@ -314,6 +217,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
           d[e >> 1] = __uint_as_float(pack_bf16(g0.x, g0.y));
           d[(e >> 1) + 1] = __uint_as_float(pack_bf16(g1.x, g1.y));
         }
+        const int left = DKV ? 128 : nk - 128 * (t0 + j) - 64 * half;  // keys of this half that are there
         if (left < 64) {
 #pragma unroll
           for (int e = 0; e < 64; ++e)  // (two a register)
@@ -332,61 +236,294 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         tc05_fence_before();
         arrive(&sh.p_full);
       }
-      const bool any = it.t1 > it.t0;
-      if (any && !dead) {
+      if (!dead) {
         wait(&sh.done, n - 1);
         tc05_fence_after();
       }
-      if (DKV) {  // the first four warps have dk, the others dv
-        const int j = it.tile * 128 + r;
-        const int64_t row = ((int64_t)it.b * a.Hkv + it.kvh) * a.Tk + j;
-        const float f = half ? 1.0f : 0.125f;
-#pragma unroll
-        for (int c = 0; c < 64; c += 16) {
-          float o[16];
-          if (any && !dead) {
-            tmem_ld16(tl + (half ? kBtSum2 : kBtSum) + c, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = any && j < it.nk ? o[e] * f : 0.0f;
-          if (j >= a.Tk) continue;
-          if (a.parts) {
-            float* const out = (half ? a.part_b : a.part_a) + ((int64_t)it.s * a.B * a.Hkv * a.Tk + row) * kD + c;
-            store8(out, o);
-            store8(out + 8, o + 8);
-          } else {
-            bf16* const out = static_cast<bf16*>(half ? a.dv : a.dk) + row * kD + c;
-            store8(out, o);
-            store8(out + 8, o + 8);
-          }
-        }
-      } else {  // half the dims each
-        const int64_t row = ro.mine ? a.row(it.b, it.kvh, ro.t * a.G + ro.g) : 0;
-#pragma unroll
+      if (dead) break;
+      // The first four warps have dk, the others dv; dq: half the dims each.  32 dims at
+      // a time through shared memory, so that lanes write rows together.
+      const int plan = pieces % kBtPlans;
+      const BtPiece p = sh.plan[plan];
+      const bool whole = p.place < 0;
+      int row;  // of this thread, where it is written; INT_MIN: nowhere, ~: as zeros
+      if (DKV) {
+        const int key = p.tile * 128 + r;
+        row = whole ? (p.b * a.Hkv + p.kvh) * a.Tk + key : (p.place + (half ? gridDim.x * 2 : 0)) * 128 + r;
+        row = key >= a.Tk ? INT_MIN : key >= p.nk ? ~row : row;
+      } else {
+        row = sh.rows[plan][r];
+        if (!whole && row != INT_MIN) row = row < 0 ? ~(p.place * 128 + r) : p.place * 128 + r;
+      }
+      const bool none = row < 0;
+      const int at = row == INT_MIN ? -1 : none ? ~row : row;
+      const float f = none ? 0.0f : DKV && half ? 1.0f : 0.125f;
+      char* const to = whole ? static_cast<char*>(DKV ? (half ? a.dv : a.dk) : a.dq) : reinterpret_cast<char*>(w.places);
+      const uint32_t stage = smem + kBtOut + warp * 4096;
+      const int lgc = whole ? 2 : 3;  // 16-byte pieces of 32 dims: 4 of bf16, 8 of fp32
+#pragma unroll 1
+      for (int c0 = 0; c0 < (DKV ? 64 : 32); c0 += 32) {
+        const int dim = DKV ? c0 : 32 * half;
+#pragma unroll 1
         for (int c = 0; c < 32; c += 16) {
           float o[16];
-          if (any && !dead) {
-            tmem_ld16(tl + kBtSum + 32 * half + c, o);
-            tmem_wait_ld();
-          }
+          const uint32_t src = tl + (DKV && half ? kBtSum2 : kBtSum) + dim + c;
+          tmem_ld8(src, o);
+          tmem_ld8(src + 8, o + 8);
+          tmem_wait_ld8(o);
+          tmem_wait_ld8(o + 8);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = any && ro.t < it.nq ? o[e] * 0.125f : 0.0f;
-          if (!ro.mine) continue;
-          if (a.parts) {
-            float* const out = a.part_a + (it.s * a.rows + row) * kD + 32 * half + c;
-            store8(out, o);
-            store8(out + 8, o + 8);
+          for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e] * f;
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              st_out(stage + swz(lane, (c >> 3) + k), pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                     pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
           } else {
-            bf16* const out = static_cast<bf16*>(a.dq) + row * kD + 32 * half + c;
-            store8(out, o);
-            store8(out + 8, o + 8);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              st_out(stage + swz(lane, (c >> 2) + k), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                     __float_as_uint(o[4 * k + 3]));
           }
         }
+        __syncwarp();
+#pragma unroll 2
+        for (int i = 0; i < 32; i += 32 >> lgc) {
+          const int rr = i + (lane >> lgc), k = lane & ((1 << lgc) - 1);
+          const int there = __shfl_sync(0xffffffffu, at, rr);
+          uint4 x;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(stage + swz(rr, k)) : "memory");
+          if (there >= 0) *reinterpret_cast<uint4*>(to + (int64_t)there * (whole ? 128 : 256) + dim * (whole ? 2 : 4) + 16 * k) = x;
+        }
+        __syncwarp();
       }
       tc05_fence_before();
+      give_back();
     }
     if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
+  } else {
+    fewer_registers<kBtFewerRegs>();
+    if (warp == 8) {
+      // ---- copies
+      int n = 0;  // steps so far
+      auto rows = [&](uint32_t dst, const CUtensorMap* m, const BtPiece& p, int tile, uint32_t bar) {
+        const int tb = tile / w.rt.groups, hb = tile - tb * w.rt.groups;
+        tma_load_4d(dst, m, 0, tb << w.rt.lgR, p.kvh * a.G + (hb << (7 - w.rt.lgR)), p.b, bar);
+      };
+      auto stat = [&](uint32_t dst, const BtPiece& p, int tile, uint32_t bar) {
+        bulk_copy(dst, w.stat + (((int64_t)p.b * a.Hkv + p.kvh) * w.rt.tiles + tile) * 256, kBtStat, bar);
+      };
+      BtPiece p;
+      for (; take(p); give_back()) {
+        const int buf = pieces & 1;
+        if (pieces >= 2) wait(&sh.a_empty[buf], (pieces >> 1) - 1);
+        if (dead) break;
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&sh.a_full[buf]), dst = smem + kBtStays + buf * 2 * kBtTile;
+          mbar_expect_tx(bar, 2 * kBtTile + (DKV ? 0 : kBtStat));
+          if (DKV) {
+            tma_load_4d(dst, &km, 0, p.tile * 128, p.kvh, p.b, bar);
+            tma_load_4d(dst + kBtTile, &vm, 0, p.tile * 128, p.kvh, p.b, bar);
+          } else {
+            rows(dst, &qm, p, p.tile, bar);
+            rows(dst + kBtTile, &gm, p, p.tile, bar);
+            stat(smem + kBtStatStays + buf * kBtStat, p, p.tile, bar);
+          }
+        }
+        __syncwarp();
+        for (int t = p.t0; t < p.t0 + p.steps && !dead; ++t, ++n) {
+          const int st = n % kBtStages;
+          if (n >= kBtStages) wait(&sh.empty[st], n / kBtStages - 1);
+          if (dead) break;
+          if (elect_one()) {
+            const uint32_t bar = smem_u32(&sh.full[st]), dst = smem + kBtRing + st * 2 * kBtTile;
+            mbar_expect_tx(bar, 2 * kBtTile + (DKV ? kBtStat : 0));
+            if (DKV) {
+              rows(dst, &qm, p, t, bar);
+              rows(dst + kBtTile, &gm, p, t, bar);
+              stat(smem + kBtStatRing + st * kBtStat, p, t, bar);
+            } else {
+              tma_load_4d(dst, &km, 0, t * 128, p.kvh, p.b, bar);
+              tma_load_4d(dst + kBtTile, &vm, 0, t * 128, p.kvh, p.b, bar);
+            }
+          }
+          __syncwarp();
+        }
+        if (dead) break;
+      }
+      if (dead) {  // copies under way end before their memory goes
+        if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
+        for (int i = max(0, n - kBtStages); i < n; ++i) mbar_wait_bounded(smem_u32(&sh.full[i % kBtStages]), (i / kBtStages) & 1, a.wait_cycles);
+        for (int i = max(0, pieces - 1); i <= pieces; ++i) mbar_wait_bounded(smem_u32(&sh.a_full[i & 1]), (i / 2) & 1, a.wait_cycles);
+      }
+    } else if (warp == 9) {
+      // ---- S and dP
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, false), kHi = smem_desc_hi(1024), kTileU = kBtTile / 16;
+      const uint32_t a0 = smem_desc_lo(smem + kBtStays, 16), b0 = smem_desc_lo(smem + kBtRing, 16);
+      const bool lead = elect_one();
+      int n = 0;
+      BtPiece p;
+      for (; take(p); give_back()) {
+        const int buf = pieces & 1;
+        wait(&sh.a_full[buf], pieces >> 1);
+        for (int j = 0; j < p.steps && !dead; ++j, ++n) {
+          const int st = n % kBtStages;
+          wait(&sh.ready[st], n / kBtStages);
+          if (n > 0) wait(&sh.s_free, n - 1);
+          if (dead) break;
+          if (lead) {
+            tc05_fence_after();
+            const uint32_t aa = a0 + 2 * buf * kTileU, b = b0 + 2 * st * kTileU;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i > 0)
+                mma_ss<true>(tm, aa + 2 * i, b + 2 * i, kHi, idS);
+              else
+                mma_ss<false>(tm, aa, b, kHi, idS);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i > 0)
+                mma_ss<true>(tm + kBtDp, aa + kTileU + 2 * i, b + kTileU + 2 * i, kHi, idS);
+              else
+                mma_ss<false>(tm + kBtDp, aa + kTileU, b + kTileU, kHi, idS);
+            umma_commit(smem_u32(&sh.s_full));
+            if (j == p.steps - 1) umma_commit(smem_u32(&sh.a_empty[buf]));
+          }
+          __syncwarp();
+        }
+        if (dead) break;
+      }
+      if (dead) {  // products under way end before their memory goes
+        if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
+        for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.s_full), i & 1, a.wait_cycles);
+      }
+    } else if (warp == 10) {
+      // ---- the sums
+      constexpr uint32_t idO = idesc_bf16(128, 64, false, true), kHi = smem_desc_hi(1024), kTileU = kBtTile / 16;
+      const uint32_t b0 = smem_desc_lo(smem + kBtRing, 8192);
+      const bool lead = elect_one();
+      int n = 0;
+      for (int x = 0; !dead; ++x) {
+        // (the plan stays until the softmax warps, which need this, give it back)
+        const int i = x % kBtPlans;
+        wait(&sh.plan_full[i], x / kBtPlans);
+        if (dead) break;
+        const int steps = __shfl_sync(0xffffffffu, sh.plan[i].steps, 0);
+        if (steps == 0) break;
+        for (int j = 0; j < steps && !dead; ++j, ++n) {
+          const int st = n % kBtStages;
+          wait(&sh.p_full, n);
+          if (dead) break;
+          if (lead) {
+            tc05_fence_after();
+            const uint32_t b = b0 + 2 * st * kTileU;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i > 0)
+                mma_ts<true>(tm + kBtSum, tm + kBtDs + 8 * i, b + 128 * i, kHi, idO);
+              else if (j == 0)
+                mma_ts<false>(tm + kBtSum, tm + kBtDs, b, kHi, idO);
+              else
+                mma_ts<true>(tm + kBtSum, tm + kBtDs, b, kHi, idO);
+            if (DKV)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i > 0)
+                  mma_ts<true>(tm + kBtSum2, tm + kBtP + 8 * i, b + kTileU + 128 * i, kHi, idO);
+                else if (j == 0)
+                  mma_ts<false>(tm + kBtSum2, tm + kBtP, b + kTileU, kHi, idO);
+                else
+                  mma_ts<true>(tm + kBtSum2, tm + kBtP, b + kTileU, kHi, idO);
+            umma_commit(smem_u32(&sh.done));
+            umma_commit(smem_u32(&sh.empty[st]));
+          }
+          __syncwarp();
+        }
+      }
+      if (dead) {  // products under way end before their memory goes
+        if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
+        for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.done), i & 1, a.wait_cycles);
+      }
+    } else {
+      // ---- the pieces; and rows that pass by and count for nothing are made zeros (they
+      // may hold anything, and 0 * NaN would reach every sum)
+      int4 split = make_int4(0, 0, 0, 0);
+      bool more = some, ended = false;
+      int n = 0, planned = 0;
+      auto plan = [&]() {  // one more piece, or that there is none
+        const int i = planned % kBtPlans;
+        if (planned >= kBtPlans) wait(&sh.plan_empty[i], planned / kBtPlans - 1);
+        if (dead) return;
+        if (!more) {
+          if (lane == 0) sh.plan[i].steps = 0;
+          ended = true;
+        } else {
+          const int own = wk.units / a.Hkv, kvh = wk.u / own, tile = wk.u - kvh * own;
+          const int nq = a.queries(wk.b), nk = a.keys(wk.b);
+          if (lane == 0) {
+            BtPiece p;
+            p.steps = wk.s1 - wk.s0;
+            p.b = wk.b;
+            p.kvh = kvh;
+            p.tile = tile;
+            p.t0 = wk.s0;
+            p.nq = nq;
+            p.nk = nk;
+            p.place = wk.whole() ? -1 : 2 * (int)blockIdx.x + (wk.s0 == 0);
+            sh.plan[i] = p;
+          }
+          if (!wk.whole() && wk.s0 == 0) split = make_int4(wk.b, kvh, tile, sh.walk.shares.owner(wk.begin + wk.steps + kUnitCost - 1) - blockIdx.x + 1);
+          if (!DKV)
+#pragma unroll 1
+            for (int r = lane; r < 128; r += 32) {
+              const RowOf ro = row_of(a, w.rt, tile, r);
+              const int row = (int)a.row(wk.b, kvh, ro.t * a.G + ro.g);
+              sh.rows[i][r] = !ro.mine ? INT_MIN : ro.t >= nq ? ~row : row;
+            }
+          more = wk.next(a.B, counts);
+        }
+        ++planned;
+        arrive(&sh.plan_full[i]);
+      };
+      plan();
+      for (int x = 0; !dead; ++x) {
+        while (planned < x + 3 && !ended && !dead) plan();
+        if (dead || (x == planned - 1 && ended)) break;
+        const BtPiece p = sh.plan[x % kBtPlans];
+        for (int t = p.t0; t < p.t0 + p.steps && !dead; ++t, ++n) {
+          const int st = n % kBtStages;
+          wait(&sh.full[st], n / kBtStages);
+          if (dead) break;
+          bool clean;
+          if (DKV) {
+            const int tb = t / w.rt.groups, hb = t - tb * w.rt.groups;
+            clean = (tb + 1) << w.rt.lgR <= p.nq && (hb + 1) << (7 - w.rt.lgR) <= a.G;
+          } else {
+            clean = (t + 1) * 128 <= p.nk;
+          }
+          if (!clean) {
+#pragma unroll 1
+            for (int r = lane; r < 128; r += 32) {
+              bool in;
+              if (DKV) {
+                const RowOf ro = row_of(a, w.rt, t, r);
+                in = ro.g < a.G && ro.t < p.nq;
+              } else {
+                in = t * 128 + r < p.nk;
+              }
+              if (!in)
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  st_out(smem + kBtRing + st * 2 * kBtTile + (c >> 3) * kBtTile + r * 128 + 16 * (c & 7), 0, 0, 0, 0);
+            }
+            fence_async_smem();
+          }
+          arrive(&sh.ready[st]);
+        }
+      }
+      if (lane == 0) w.split[blockIdx.x] = split;
+      if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
+    }
   }
   tc05_fence_before();
   __syncthreads();
@@ -394,24 +531,140 @@ __global__ void __launch_bounds__(kBtThreads, 1)
   if (warp == 9) tmem_dealloc(tm, 512);
 }
 
-int launch_cross_bwd_tc(const CrossArgs& a, bool dkv, void* stream) {
+// What the kernels need of each row, tile by tile: -lse log2(e) and -delta, eight
+// lanes a row; rows that count for nothing get -inf, which makes their
+// probabilities 0.
+__global__ void __launch_bounds__(256) cross_stat_tc_kernel(const CrossArgs a, const RowTiles rt, float* stat) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t x = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);  // row of a tile of a (sequence, KV head)
+  const int d8 = (threadIdx.x & 7) * 8, r = (int)(x & 127);
+  const int64_t tiles = x >> 7, bh = tiles / rt.tiles;
+  float sum = 0.0f, lse = INFINITY;
+  const int b = (int)(bh / a.Hkv);
+  if (b < a.B) {
+    const RowOf ro = row_of(a, rt, (int)(tiles - bh * rt.tiles), r);
+    if (ro.mine && ro.t < a.queries(b) && a.keys(b) > 0) {
+      const int64_t row = a.row(b, (int)(bh - (int64_t)b * a.Hkv), ro.t * a.G + ro.g);
+      float o[8], g[8];
+      load8(static_cast<const bf16*>(a.out) + row * kD + d8, o);
+      load8(static_cast<const bf16*>(a.dO) + row * kD + d8, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(o[e], g[e], sum);
+      lse = a.lse[row] * kLog2e;
+    }
+  }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (b < a.B && d8 == 0) {
+    stat[tiles * 256 + r] = -lse;
+    stat[tiles * 256 + 128 + r] = -sum;
+  }
+}
+
+// Units that span CTAs: the sums of their parts, in order.  CTA (c, y) has 32 rows of
+// the unit that CTA c of the dq kernel (c < q_ctas) or of the dk, dv kernel began, eight
+// lanes a row.
+__global__ void __launch_bounds__(256) cross_sum_places_kernel(const CrossArgs a, const BtWork q, const BtWork kv, int q_ctas, int kv_ctas) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const bool dkv = (int)blockIdx.x >= q_ctas;
+  const int c = dkv ? blockIdx.x - q_ctas : blockIdx.x, lane = threadIdx.x & 31, d8 = (lane & 7) * 8;
+  const int4 s = dkv ? kv.split[c] : q.split[c];
+  if (s.w <= 1) return;
+  // many parts: four at a time, 8 rows of the CTA's 32 at once; few: a row's one after
+  // another, all rows at once
+  const bool many = s.w >= 8;
+  const int ways = many ? 4 : 1, first = many ? lane >> 3 : 0;
+#pragma unroll 2
+  for (int i = 0; i < (many ? 4 : 1) * (dkv ? 2 : 1); ++i) {
+    const int dv = dkv ? i & 1 : 0, k = dkv ? i >> 1 : i;
+    const int r = blockIdx.y * 32 + (many ? 8 * k + (threadIdx.x >> 5) : threadIdx.x >> 3);
+    int64_t row = -1;
+    if (dkv) {
+      const int key = s.z * 128 + r;
+      if (key < a.Tk) row = ((int64_t)s.x * a.Hkv + s.y) * a.Tk + key;
+    } else {
+      const RowOf ro = row_of(a, q.rt, s.z, r);
+      if (ro.mine) row = a.row(s.x, s.y, ro.t * a.G + ro.g);
+    }
+    const float* const from = (dkv ? kv.places : q.places) + (dv ? (int64_t)kv_ctas * 2 * 128 * kD : 0) + r * kD + d8;
+    float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, z[8];
+    if (row >= 0)
+#pragma unroll 2
+      for (int x = first; x < s.w; x += ways) {
+        load8(from + (int64_t)(x == 0 ? 2 * c + 1 : 2 * (c + x)) * 128 * kD, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += z[e];
+      }
+    if (many)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] += __shfl_xor_sync(0xffffffffu, y[e], 8);
+        y[e] += __shfl_xor_sync(0xffffffffu, y[e], 16);
+      }
+    if (row >= 0 && first == 0) store8(static_cast<bf16*>(dkv ? (dv ? a.dv : a.dk) : a.dq) + row * kD + d8, y);
+  }
+}
+
+struct BtPlan {
+  RowTiles rt;
+  int key_tiles, q_ctas, kv_ctas;
+  size_t stat, q_places, kv_places, bytes;
+};
+
+static BtPlan bt_plan(int B, int Hkv, int G, int Tq, int Tk) {
+  BtPlan p;
+  p.rt = row_tiles(G, Tq);
+  p.key_tiles = (Tk + 127) / 128;
+  const int64_t u = (int64_t)B * Hkv, qu = u * p.rt.tiles, ku = u * p.key_tiles;
+  Shares s;
+  s.set(qu * (p.key_tiles + kUnitCost), qu, kSMs);
+  p.q_ctas = s.ctas;
+  s.set(ku * (p.rt.tiles + kUnitCost), ku, kSMs);
+  p.kv_ctas = s.ctas;
+  p.stat = align256((size_t)qu * kBtStat);
+  p.q_places = (size_t)p.q_ctas * 2 * 128 * kD * sizeof(float);
+  p.kv_places = (size_t)p.kv_ctas * 4 * 128 * kD * sizeof(float);
+  p.bytes = p.stat + p.q_places + p.kv_places + align256((size_t)(p.q_ctas + p.kv_ctas) * sizeof(int4));
+  return p;
+}
+
+size_t cross_bwd_tc_bytes(int B, int Hkv, int G, int Tq, int Tk) { return bt_plan(B, Hkv, G, Tq, Tk).bytes; }
+
+int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream) {
   static_assert(kBtSmem + sizeof(BtShared) + 1024 <= 228 * 1024, "shared memory of an SM");
-  BtWork w;
-  w.rt = row_tiles(a.G, a.Tq);
-  w.key_tiles = (a.Tk + 127) / 128;
-  w.items = (int)((int64_t)a.B * a.Hkv * (dkv ? w.key_tiles : w.rt.tiles) * a.splits);
+  const BtPlan p = bt_plan(a.B, a.Hkv, a.G, a.Tq, a.Tk);
+  char* const at = static_cast<char*>(ws);
+  float* const stat = static_cast<float*>(ws);
+  BtWork q = {p.rt, p.key_tiles, stat, reinterpret_cast<float*>(at + p.stat), reinterpret_cast<int4*>(at + p.stat + p.q_places + p.kv_places)};
+  BtWork kv = {p.rt, p.key_tiles, stat, reinterpret_cast<float*>(at + p.stat + p.q_places), q.split + p.q_ctas};
   CUtensorMap qm, gm, km, vm;
   const Strides dense = {(int64_t)a.Hq * a.Tq * kD, (int64_t)a.Tq * kD, kD};
-  int rc = make_view_map(&qm, a.q, a.Tq, a.Hq, a.B, a.qs, 1 << w.rt.lgR, 128 >> w.rt.lgR);
-  if (rc == SFA_OK) rc = make_view_map(&gm, a.dO, a.Tq, a.Hq, a.B, dense, 1 << w.rt.lgR, 128 >> w.rt.lgR);
+  int rc = make_view_map(&qm, a.q, a.Tq, a.Hq, a.B, a.qs, 1 << p.rt.lgR, 128 >> p.rt.lgR);
+  if (rc == SFA_OK) rc = make_view_map(&gm, a.dO, a.Tq, a.Hq, a.B, dense, 1 << p.rt.lgR, 128 >> p.rt.lgR);
   if (rc == SFA_OK) rc = make_view_map(&km, a.k, a.Tk, a.Hkv, a.B, a.ks, 128, 1);
   if (rc == SFA_OK) rc = make_view_map(&vm, a.v, a.Tk, a.Hkv, a.B, a.vs, 128, 1);
   if (rc != SFA_OK) return rc;
-  LaunchTimer tm(dkv ? SFA_KERNEL_CROSS_BWD_KV : SFA_KERNEL_CROSS_BWD_Q, stream);
-  auto* f = dkv ? cross_bwd_tc_kernel<true> : cross_bwd_tc_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kBtSmem);
-  if (e == cudaSuccess)
-    e = launch_pdl(f, dim3((unsigned)(w.items < kSMs ? w.items : kSMs)), dim3(kBtThreads), kBtSmem, (cudaStream_t)stream, a, w, qm, gm, km, vm);
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaFuncSetAttribute(cross_bwd_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBtSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(cross_bwd_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBtSmem);
+  if (e == cudaSuccess) {
+    LaunchTimer tm(SFA_KERNEL_CROSS_STAT, stream);
+    e = launch_pdl(cross_stat_tc_kernel, dim3((unsigned)((int64_t)a.B * a.Hkv * p.rt.tiles * 4)), dim3(256), 0, st, a, p.rt, stat);
+  }
+  if (e == cudaSuccess) {
+    LaunchTimer tm(SFA_KERNEL_CROSS_BWD_Q, stream);
+    e = launch_pdl(cross_bwd_tc_kernel<false>, dim3((unsigned)p.q_ctas), dim3(kBtThreads), kBtSmem, st, a, q, qm, gm, km, vm);
+  }
+  if (e == cudaSuccess) {
+    LaunchTimer tm(SFA_KERNEL_CROSS_BWD_KV, stream);
+    e = launch_pdl(cross_bwd_tc_kernel<true>, dim3((unsigned)p.kv_ctas), dim3(kBtThreads), kBtSmem, st, a, kv, qm, gm, km, vm);
+  }
+  if (e == cudaSuccess) {
+    LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
+    e = launch_pdl(cross_sum_places_kernel, dim3((unsigned)(p.q_ctas + p.kv_ctas), 4), dim3(256), 0, st, a, q, kv, p.q_ctas, p.kv_ctas);
+  }
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
