@@ -12,8 +12,8 @@
 // and equal inputs give equal bits; the price is S and dP twice (7 products instead
 // of 5).  In both the probabilities come out of tensor memory the way they go back in
 // as a left operand: a lane per row of the tile that stays, so P and dS never pass
-// shared memory.  Per step one warp issues the next S and dP as soon as eight warps
-// hold this step's in registers (64 columns of both a thread), another the
+// shared memory.  Per step one warp issues the next S and dP as soon as 16 warps
+// hold this step's in registers (32 columns of both a thread), another the
 // accumulations when P and dS are back.  P and dS are rounded to bf16 for their
 // products; everything else is fp32.  The steps of all tiles are dealt out evenly
 // over the SMs, and planned ahead by one warp, as in the forward pass.
@@ -23,14 +23,16 @@
 
 namespace sfa {
 
-constexpr int kBtThreads = 384;  // 8 warps of softmax, a copying warp, two that issue, one that plans and clears rows
-// Registers: 168 a thread at launch, 3 x 128 x 168 = 2 x 128 x 216 + 128 x 72.
-constexpr int kBtMoreRegs = 216, kBtFewerRegs = 72;
+// 16 warps of softmax, a copying warp, two that issue, one that clears rows, one that
+// plans (three more make a warpgroup).
+constexpr int kBtSoftmax = 16, kBtThreads = 32 * (kBtSoftmax + 8);
+// Registers: 80 a thread at launch, 768 x 80 = 512 x 96 + 256 x 48.
+constexpr int kBtMoreRegs = 96, kBtFewerRegs = 48;
 constexpr int kBtTile = 128 * 128;  // bytes of 128 rows of 64 bf16
-constexpr int kBtStages = 3;
+constexpr int kBtStages = 4;
 constexpr int kBtStat = 1024;  // bytes of a row tile's numbers: 128 of -lse log2(e), 128 of -delta
 constexpr int kBtStays = 0, kBtRing = kBtStays + 2 * 2 * kBtTile, kBtOut = kBtRing + kBtStages * 2 * kBtTile,
-              kBtStatRing = kBtOut + 8 * 4096, kBtStatStays = kBtStatRing + kBtStages * kBtStat, kBtSmem = kBtStatStays + 2 * kBtStat + 1024;
+              kBtStatRing = kBtOut + kBtSoftmax * 1024, kBtStatStays = kBtStatRing + kBtStages * kBtStat, kBtSmem = kBtStatStays + 2 * kBtStat + 1024;
 constexpr int kBtPlans = 4;
 // tensor memory: S, dP, P, dS, sums of dq or dk, of dv
 constexpr int kBtDp = 128, kBtP = 256, kBtDs = 320, kBtSum = 384, kBtSum2 = 448;
@@ -86,23 +88,23 @@ __global__ void __launch_bounds__(kBtThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.a_full[i]), 1);
-      mbar_init(smem_u32(&sh.a_empty[i]), DKV ? 1 : 9);  // (dq: the softmax warps read the staying rows' numbers)
+      mbar_init(smem_u32(&sh.a_empty[i]), DKV ? 1 : kBtSoftmax + 1);  // (dq: the softmax warps read the staying rows' numbers)
     }
     for (int i = 0; i < kBtPlans; ++i) {
       mbar_init(smem_u32(&sh.plan_full[i]), 1);
-      mbar_init(smem_u32(&sh.plan_empty[i]), 10);  // the softmax warps, the copying and one issuing warp
+      mbar_init(smem_u32(&sh.plan_empty[i]), kBtSoftmax + 3);  // all others that take pieces
     }
     mbar_init(smem_u32(&sh.s_full), 1);
-    mbar_init(smem_u32(&sh.s_free), 8);
-    mbar_init(smem_u32(&sh.p_full), 8);
+    mbar_init(smem_u32(&sh.s_free), kBtSoftmax);
+    mbar_init(smem_u32(&sh.p_full), kBtSoftmax);
     mbar_init(smem_u32(&sh.done), 1);
     mbar_fence_init();
   }
-  if (warp == 9) {
+  if (warp == kBtSoftmax + 1) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
   }
-  if (warp == 8 && lane < 4) prefetch_map(lane == 0 ? &qm : lane == 1 ? &gm : lane == 2 ? &km : &vm);
+  if (warp == kBtSoftmax && lane < 4) prefetch_map(lane == 0 ? &qm : lane == 1 ? &gm : lane == 2 ? &km : &vm);
   pdl_wait();
   auto counts = [&](int b, int& units, int& steps) {
     const int nk = a.keys(b), nq = a.queries(b), keys = (nk + 127) >> 7, rows = w.rt.used(nq);
@@ -134,10 +136,10 @@ __global__ void __launch_bounds__(kBtThreads, 1)
   };
   auto give_back = [&]() { arrive(&sh.plan_empty[pieces++ % kBtPlans]); };
 
-  if (warp < 8) {
-    // ---- P and dS: a thread a row of the tile that stays, 64 of the 128 that pass by
+  if (warp < kBtSoftmax) {
+    // ---- P and dS: a thread a row of the tile that stays, 32 of the 128 that pass by
     more_registers<kBtMoreRegs>();
-    const int half = warp >> 2, r = tid & 127;
+    const int quarter = warp >> 2, r = tid & 127;
     const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
     // tiles without work: zeros
     {
@@ -151,15 +153,15 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         if (DKV) {
           const int j = tile * 128 + r;
           if (j >= a.Tk) continue;
-          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(half ? a.dv : a.dk) + ((int64_t)bh * a.Tk + j) * kD);
+          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(quarter >> 1 ? a.dv : a.dk) + ((int64_t)bh * a.Tk + j) * kD + 32 * (quarter & 1));
 #pragma unroll
-          for (int c = 0; c < 8; ++c) out[c] = zero;
+          for (int c = 0; c < 4; ++c) out[c] = zero;
         } else {
           const RowOf ro = row_of(a, w.rt, tile, r);
           if (!ro.mine) continue;
-          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(a.dq) + a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g) * kD + 32 * half);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) out[c] = zero;
+          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(a.dq) + a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g) * kD + 16 * quarter);
+          out[0] = zero;
+          out[1] = zero;
         }
       }
     }
@@ -188,15 +190,15 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         wait(&sh.s_full, n);
         if (dead) break;
         tc05_fence_after();
-        float s[64], d[64];
-        tmem_take64(tl + 64 * half, s);
-        tmem_take64(tl + kBtDp + 64 * half, d);
+        float s[32], d[32];
+        tmem_take32(tl + 32 * quarter, s);
+        tmem_take32(tl + kBtDp + 32 * quarter, d);
         tc05_fence_before();
         arrive(&sh.s_free);
         const float2 c2 = make_float2(kLogitScale, kLogitScale);
-        const uint32_t stat = smem + kBtStatRing + st * kBtStat + 256 * half;
+        const uint32_t stat = smem + kBtStatRing + st * kBtStat + 128 * quarter;
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
+        for (int e = 0; e < 32; e += 4) {
           float4 nl, nd;
           if (DKV) {
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(nl.x), "=f"(nl.y), "=f"(nl.z), "=f"(nl.w) : "r"(stat + 4 * e));
@@ -217,21 +219,17 @@ __global__ void __launch_bounds__(kBtThreads, 1)
           d[e >> 1] = __uint_as_float(pack_bf16(g0.x, g0.y));
           d[(e >> 1) + 1] = __uint_as_float(pack_bf16(g1.x, g1.y));
         }
-        const int left = DKV ? 128 : nk - 128 * (t0 + j) - 64 * half;  // keys of this half that are there
-        if (left < 64) {
+        const int left = DKV ? 128 : nk - 128 * (t0 + j) - 32 * quarter;  // keys of this quarter that are there
+        if (left < 32) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)  // (two a register)
+          for (int e = 0; e < 32; ++e)  // (two a register)
             if (e >= left) d[e >> 1] = __uint_as_float(__float_as_uint(d[e >> 1]) & (e & 1 ? 0x0000ffffu : 0u));
         }
         if (n > 0) wait(&sh.done, n - 1);  // the last step's P and dS have been read
         if (dead) break;
         tc05_fence_after();
-        if (DKV) {
-          tmem_st16(tl + kBtP + 32 * half, s);
-          tmem_st16(tl + kBtP + 32 * half + 16, s + 16);
-        }
-        tmem_st16(tl + kBtDs + 32 * half, d);
-        tmem_st16(tl + kBtDs + 32 * half + 16, d + 16);
+        if (DKV) tmem_st16(tl + kBtP + 16 * quarter, s);
+        tmem_st16(tl + kBtDs + 16 * quarter, d);
         tmem_wait_st();
         tc05_fence_before();
         arrive(&sh.p_full);
@@ -241,15 +239,16 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         tc05_fence_after();
       }
       if (dead) break;
-      // The first four warps have dk, the others dv; dq: half the dims each.  32 dims at
-      // a time through shared memory, so that lanes write rows together.
-      const int plan = pieces % kBtPlans;
+      // The first eight warps have dk, the others dv, half the dims each; dq: a quarter of
+      // the dims each.  16 dims at a time through shared memory, so that lanes write rows
+      // together.
+      const int plan = pieces % kBtPlans, dv = DKV ? quarter >> 1 : 0;
       const BtPiece p = sh.plan[plan];
       const bool whole = p.place < 0;
       int row;  // of this thread, where it is written; INT_MIN: nowhere, ~: as zeros
       if (DKV) {
         const int key = p.tile * 128 + r;
-        row = whole ? (p.b * a.Hkv + p.kvh) * a.Tk + key : (p.place + (half ? gridDim.x * 2 : 0)) * 128 + r;
+        row = whole ? (p.b * a.Hkv + p.kvh) * a.Tk + key : (p.place + (dv ? gridDim.x * 2 : 0)) * 128 + r;
         row = key >= a.Tk ? INT_MIN : key >= p.nk ? ~row : row;
       } else {
         row = sh.rows[plan][r];
@@ -257,45 +256,47 @@ __global__ void __launch_bounds__(kBtThreads, 1)
       }
       const bool none = row < 0;
       const int at = row == INT_MIN ? -1 : none ? ~row : row;
-      const float f = none ? 0.0f : DKV && half ? 1.0f : 0.125f;
-      char* const to = whole ? static_cast<char*>(DKV ? (half ? a.dv : a.dk) : a.dq) : reinterpret_cast<char*>(w.places);
-      const uint32_t stage = smem + kBtOut + warp * 4096;
-      const int lgc = whole ? 2 : 3;  // 16-byte pieces of 32 dims: 4 of bf16, 8 of fp32
+      const float f = none ? 0.0f : dv ? 1.0f : 0.125f;
+      char* const to = whole ? static_cast<char*>(DKV ? (dv ? a.dv : a.dk) : a.dq) : reinterpret_cast<char*>(w.places);
+      const uint32_t stage = smem + kBtOut + warp * 1024;
+      const int lgc = whole ? 1 : 2;  // 16-byte pieces of 16 dims: 2 of bf16, 4 of fp32
 #pragma unroll 1
-      for (int c0 = 0; c0 < (DKV ? 64 : 32); c0 += 32) {
-        const int dim = DKV ? c0 : 32 * half;
+      for (int c = 0; c < (DKV ? 32 : 16); c += 16) {
+        const int dim = DKV ? 32 * (quarter & 1) + c : 16 * quarter;
+        float o[16];
+        const uint32_t src = tl + (dv ? kBtSum2 : kBtSum) + dim;
+        tmem_ld8(src, o);
+        tmem_ld8(src + 8, o + 8);
+        tmem_wait_ld8(o);
+        tmem_wait_ld8(o + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e] * f;
+        auto spot = [&](int rr, int k) { return stage + (rr & 15) * 64 + ((k ^ ((rr >> 1) & 3)) << 4); };
 #pragma unroll 1
-        for (int c = 0; c < 32; c += 16) {
-          float o[16];
-          const uint32_t src = tl + (DKV && half ? kBtSum2 : kBtSum) + dim + c;
-          tmem_ld8(src, o);
-          tmem_ld8(src + 8, o + 8);
-          tmem_wait_ld8(o);
-          tmem_wait_ld8(o + 8);
+        for (int h = 0; h < 32; h += 16) {  // 16 rows
+          if ((lane & 16) == h) {
+            if (whole) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = none ? 0.0f : o[e] * f;
-          if (whole) {
+              for (int k = 0; k < 2; ++k)
+                st_out(spot(lane, k), pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]), pack_bf16(o[8 * k + 4], o[8 * k + 5]),
+                       pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+            } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              st_out(stage + swz(lane, (c >> 3) + k), pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                     pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              st_out(stage + swz(lane, (c >> 2) + k), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
-                     __float_as_uint(o[4 * k + 3]));
+              for (int k = 0; k < 4; ++k)
+                st_out(spot(lane, k), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                       __float_as_uint(o[4 * k + 3]));
+            }
           }
+          __syncwarp();
+          for (int i = h; i < h + 16; i += 32 >> lgc) {
+            const int rr = i + (lane >> lgc), k = lane & ((1 << lgc) - 1);
+            const int there = __shfl_sync(0xffffffffu, at, rr);
+            uint4 x;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(spot(rr, k)) : "memory");
+            if (there >= 0) *reinterpret_cast<uint4*>(to + (int64_t)there * (whole ? 128 : 256) + dim * (whole ? 2 : 4) + 16 * k) = x;
+          }
+          __syncwarp();
         }
-        __syncwarp();
-#pragma unroll 2
-        for (int i = 0; i < 32; i += 32 >> lgc) {
-          const int rr = i + (lane >> lgc), k = lane & ((1 << lgc) - 1);
-          const int there = __shfl_sync(0xffffffffu, at, rr);
-          uint4 x;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(stage + swz(rr, k)) : "memory");
-          if (there >= 0) *reinterpret_cast<uint4*>(to + (int64_t)there * (whole ? 128 : 256) + dim * (whole ? 2 : 4) + 16 * k) = x;
-        }
-        __syncwarp();
       }
       tc05_fence_before();
       give_back();
@@ -303,31 +304,29 @@ __global__ void __launch_bounds__(kBtThreads, 1)
     if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
   } else {
     fewer_registers<kBtFewerRegs>();
-    if (warp == 8) {
+    if (warp == kBtSoftmax) {
       // ---- copies
       int n = 0;  // steps so far
-      auto rows = [&](uint32_t dst, const CUtensorMap* m, const BtPiece& p, int tile, uint32_t bar) {
-        const int tb = tile / w.rt.groups, hb = tile - tb * w.rt.groups;
-        tma_load_4d(dst, m, 0, tb << w.rt.lgR, p.kvh * a.G + (hb << (7 - w.rt.lgR)), p.b, bar);
-      };
-      auto stat = [&](uint32_t dst, const BtPiece& p, int tile, uint32_t bar) {
-        bulk_copy(dst, w.stat + (((int64_t)p.b * a.Hkv + p.kvh) * w.rt.tiles + tile) * 256, kBtStat, bar);
-      };
+      const bool lead = elect_one();
+      const int heads = 1 << (7 - w.rt.lgR);
       BtPiece p;
       for (; take(p); give_back()) {
         const int buf = pieces & 1;
         if (pieces >= 2) wait(&sh.a_empty[buf], (pieces >> 1) - 1);
         if (dead) break;
-        if (elect_one()) {
+        const int row_tile = DKV ? p.t0 : p.tile;
+        int tb = row_tile / w.rt.groups, hb = row_tile - tb * w.rt.groups;
+        const float* stat = w.stat + (((int64_t)p.b * a.Hkv + p.kvh) * w.rt.tiles + row_tile) * 256;
+        if (lead) {
           const uint32_t bar = smem_u32(&sh.a_full[buf]), dst = smem + kBtStays + buf * 2 * kBtTile;
           mbar_expect_tx(bar, 2 * kBtTile + (DKV ? 0 : kBtStat));
           if (DKV) {
             tma_load_4d(dst, &km, 0, p.tile * 128, p.kvh, p.b, bar);
             tma_load_4d(dst + kBtTile, &vm, 0, p.tile * 128, p.kvh, p.b, bar);
           } else {
-            rows(dst, &qm, p, p.tile, bar);
-            rows(dst + kBtTile, &gm, p, p.tile, bar);
-            stat(smem + kBtStatStays + buf * kBtStat, p, p.tile, bar);
+            tma_load_4d(dst, &qm, 0, tb << w.rt.lgR, p.kvh * a.G + hb * heads, p.b, bar);
+            tma_load_4d(dst + kBtTile, &gm, 0, tb << w.rt.lgR, p.kvh * a.G + hb * heads, p.b, bar);
+            bulk_copy(smem + kBtStatStays + buf * kBtStat, stat, kBtStat, bar);
           }
         }
         __syncwarp();
@@ -335,19 +334,26 @@ __global__ void __launch_bounds__(kBtThreads, 1)
           const int st = n % kBtStages;
           if (n >= kBtStages) wait(&sh.empty[st], n / kBtStages - 1);
           if (dead) break;
-          if (elect_one()) {
+          if (lead) {
             const uint32_t bar = smem_u32(&sh.full[st]), dst = smem + kBtRing + st * 2 * kBtTile;
             mbar_expect_tx(bar, 2 * kBtTile + (DKV ? kBtStat : 0));
             if (DKV) {
-              rows(dst, &qm, p, t, bar);
-              rows(dst + kBtTile, &gm, p, t, bar);
-              stat(smem + kBtStatRing + st * kBtStat, p, t, bar);
+              tma_load_4d(dst, &qm, 0, tb << w.rt.lgR, p.kvh * a.G + hb * heads, p.b, bar);
+              tma_load_4d(dst + kBtTile, &gm, 0, tb << w.rt.lgR, p.kvh * a.G + hb * heads, p.b, bar);
+              bulk_copy(smem + kBtStatRing + st * kBtStat, stat, kBtStat, bar);
             } else {
               tma_load_4d(dst, &km, 0, t * 128, p.kvh, p.b, bar);
               tma_load_4d(dst + kBtTile, &vm, 0, t * 128, p.kvh, p.b, bar);
             }
           }
           __syncwarp();
+          if (DKV) {
+            stat += 256;
+            if (++hb == w.rt.groups) {
+              hb = 0;
+              ++tb;
+            }
+          }
         }
         if (dead) break;
       }
@@ -356,7 +362,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         for (int i = max(0, n - kBtStages); i < n; ++i) mbar_wait_bounded(smem_u32(&sh.full[i % kBtStages]), (i / kBtStages) & 1, a.wait_cycles);
         for (int i = max(0, pieces - 1); i <= pieces; ++i) mbar_wait_bounded(smem_u32(&sh.a_full[i & 1]), (i / 2) & 1, a.wait_cycles);
       }
-    } else if (warp == 9) {
+    } else if (warp == kBtSoftmax + 1) {
       // ---- S and dP
       constexpr uint32_t idS = idesc_bf16(128, 128, false, false), kHi = smem_desc_hi(1024), kTileU = kBtTile / 16;
       const uint32_t a0 = smem_desc_lo(smem + kBtStays, 16), b0 = smem_desc_lo(smem + kBtRing, 16);
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
         for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.s_full), i & 1, a.wait_cycles);
       }
-    } else if (warp == 10) {
+    } else if (warp == kBtSoftmax + 2) {
       // ---- the sums
       constexpr uint32_t idO = idesc_bf16(128, 64, false, true), kHi = smem_desc_hi(1024), kTileU = kBtTile / 16;
       const uint32_t b0 = smem_desc_lo(smem + kBtRing, 8192);
@@ -444,63 +450,18 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
         for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.done), i & 1, a.wait_cycles);
       }
-    } else {
-      // ---- the pieces; and rows that pass by and count for nothing are made zeros (they
-      // may hold anything, and 0 * NaN would reach every sum)
-      int4 split = make_int4(0, 0, 0, 0);
-      bool more = some, ended = false;
-      int n = 0, planned = 0;
-      auto plan = [&]() {  // one more piece, or that there is none
-        const int i = planned % kBtPlans;
-        if (planned >= kBtPlans) wait(&sh.plan_empty[i], planned / kBtPlans - 1);
-        if (dead) return;
-        if (!more) {
-          if (lane == 0) sh.plan[i].steps = 0;
-          ended = true;
-        } else {
-          const int own = wk.units / a.Hkv, kvh = wk.u / own, tile = wk.u - kvh * own;
-          const int nq = a.queries(wk.b), nk = a.keys(wk.b);
-          if (lane == 0) {
-            BtPiece p;
-            p.steps = wk.s1 - wk.s0;
-            p.b = wk.b;
-            p.kvh = kvh;
-            p.tile = tile;
-            p.t0 = wk.s0;
-            p.nq = nq;
-            p.nk = nk;
-            p.place = wk.whole() ? -1 : 2 * (int)blockIdx.x + (wk.s0 == 0);
-            sh.plan[i] = p;
-          }
-          if (!wk.whole() && wk.s0 == 0) split = make_int4(wk.b, kvh, tile, sh.walk.shares.owner(wk.begin + wk.steps + kUnitCost - 1) - blockIdx.x + 1);
-          if (!DKV)
-#pragma unroll 1
-            for (int r = lane; r < 128; r += 32) {
-              const RowOf ro = row_of(a, w.rt, tile, r);
-              const int row = (int)a.row(wk.b, kvh, ro.t * a.G + ro.g);
-              sh.rows[i][r] = !ro.mine ? INT_MIN : ro.t >= nq ? ~row : row;
-            }
-          more = wk.next(a.B, counts);
-        }
-        ++planned;
-        arrive(&sh.plan_full[i]);
-      };
-      plan();
-      for (int x = 0; !dead; ++x) {
-        while (planned < x + 3 && !ended && !dead) plan();
-        if (dead || (x == planned - 1 && ended)) break;
-        const BtPiece p = sh.plan[x % kBtPlans];
+    } else if (warp == kBtSoftmax + 3) {
+      // ---- rows that pass by and count for nothing are made zeros (they may hold
+      // anything, and 0 * NaN would reach every sum)
+      int n = 0;
+      BtPiece p;
+      for (; take(p); give_back()) {
+        int tb = DKV ? p.t0 / w.rt.groups : 0, hb = DKV ? p.t0 - tb * w.rt.groups : 0;
         for (int t = p.t0; t < p.t0 + p.steps && !dead; ++t, ++n) {
           const int st = n % kBtStages;
+          const bool clean = DKV ? (tb + 1) << w.rt.lgR <= p.nq && (hb + 1) << (7 - w.rt.lgR) <= a.G : (t + 1) * 128 <= p.nk;
           wait(&sh.full[st], n / kBtStages);
           if (dead) break;
-          bool clean;
-          if (DKV) {
-            const int tb = t / w.rt.groups, hb = t - tb * w.rt.groups;
-            clean = (tb + 1) << w.rt.lgR <= p.nq && (hb + 1) << (7 - w.rt.lgR) <= a.G;
-          } else {
-            clean = (t + 1) * 128 <= p.nk;
-          }
           if (!clean) {
 #pragma unroll 1
             for (int r = lane; r < 128; r += 32) {
@@ -519,7 +480,51 @@ __global__ void __launch_bounds__(kBtThreads, 1)
             fence_async_smem();
           }
           arrive(&sh.ready[st]);
+          if (DKV && ++hb == w.rt.groups) {
+            hb = 0;
+            ++tb;
+          }
         }
+        if (dead) break;
+      }
+      if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
+    } else if (warp == kBtSoftmax + 4) {
+      // ---- the pieces (a warp of its own: lengths and divisions take 3000 clocks a piece)
+      int4 split = make_int4(0, 0, 0, 0);
+      bool more = some;
+      for (int planned = 0; !dead; ++planned) {
+        const int i = planned % kBtPlans;
+        if (planned >= kBtPlans) wait(&sh.plan_empty[i], planned / kBtPlans - 1);
+        if (dead) break;
+        if (!more) {
+          if (lane == 0) sh.plan[i].steps = 0;
+          arrive(&sh.plan_full[i]);
+          break;
+        }
+        const int own = wk.units / a.Hkv, kvh = wk.u / own, tile = wk.u - kvh * own;
+        const int nq = a.queries(wk.b), nk = a.keys(wk.b);
+        if (lane == 0) {
+          BtPiece p;
+          p.steps = wk.s1 - wk.s0;
+          p.b = wk.b;
+          p.kvh = kvh;
+          p.tile = tile;
+          p.t0 = wk.s0;
+          p.nq = nq;
+          p.nk = nk;
+          p.place = wk.whole() ? -1 : 2 * (int)blockIdx.x + (wk.s0 == 0);
+          sh.plan[i] = p;
+        }
+        if (!wk.whole() && wk.s0 == 0) split = make_int4(wk.b, kvh, tile, sh.walk.shares.owner(wk.begin + wk.steps + kUnitCost - 1) - blockIdx.x + 1);
+        if (!DKV)
+#pragma unroll 1
+          for (int r = lane; r < 128; r += 32) {
+            const RowOf ro = row_of(a, w.rt, tile, r);
+            const int row = (int)a.row(wk.b, kvh, ro.t * a.G + ro.g);
+            sh.rows[i][r] = !ro.mine ? INT_MIN : ro.t >= nq ? ~row : row;
+          }
+        more = wk.next(a.B, counts);
+        arrive(&sh.plan_full[i]);
       }
       if (lane == 0) w.split[blockIdx.x] = split;
       if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
@@ -528,7 +533,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
   tc05_fence_before();
   __syncthreads();
   tc05_fence_after();
-  if (warp == 9) tmem_dealloc(tm, 512);
+  if (warp == kBtSoftmax + 1) tmem_dealloc(tm, 512);
 }
 
 // What the kernels need of each row, tile by tile: -lse log2(e) and -delta, eight
