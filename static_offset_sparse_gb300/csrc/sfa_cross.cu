@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(128) prefix_prep_kernel(const PrefixArgs a) {
 // ---- which kernels a call runs
 
 enum Kind { kFewRows, kTensor, kFp32 };
-static Kind forward_kind(int rows, int dtype) { return rows <= kStreamRows ? kFewRows : dtype == SFA_BF16 ? kTensor : kFp32; }
+static int stream_rows(int dtype) { return dtype == SFA_BF16 ? kStreamRowsBf16 : kStreamRows; }
+static Kind forward_kind(int rows, int dtype) { return rows <= stream_rows(dtype) ? kFewRows : dtype == SFA_BF16 ? kTensor : kFp32; }
 
 // Parts of a call over `units` (sequence, KV head) pairs of Tq queries of G heads (not the tensor cores').
 static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind) {
@@ -263,7 +264,7 @@ static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
   p.kind = forward_kind(G * d->B, d->dtype);
   p.two = d->P && p.kind == kTensor;
   p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind);
-  p.own = wave_splits((int64_t)d->B * d->Hkv * ((G + kStreamRows - 1) / kStreamRows), 4 * kSMs, d->T, 256);
+  p.own = wave_splits((int64_t)d->B * d->Hkv * ((G + stream_rows(d->dtype) - 1) / stream_rows(d->dtype)), 4 * kSMs, d->T, 256);
   p.q32 = align256((size_t)p.rows * kD * sizeof(float));
   p.q16 = p.two ? align256((size_t)p.rows * kD * 2 * sizeof(bf16)) : 0;
   p.parts = part_bytes(p.shared + p.own, p.rows);

@@ -424,7 +424,7 @@ int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream);
 // Backward pass, fp32.
 int launch_cross_dq_simt(const CrossArgs& a, void* stream);
 int launch_cross_dkv_simt(const CrossArgs& a, void* stream);
-constexpr int kStreamRows = 8;  // rows that cross_stream_kernel takes at once
+constexpr int kStreamRows = 8, kStreamRowsBf16 = 16;  // rows that the kernels for few rows take at once
 constexpr int kSimtTile = 64;   // rows and keys of the fp32 kernels' tiles
 
 // Splits of `units` units of work a CTA where there are `ctas` CTAs and room for

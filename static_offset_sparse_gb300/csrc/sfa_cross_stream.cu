@@ -1,12 +1,21 @@
 // Few rows over many keys: the step of a decoder over an encoder's states, and
 // the own rows of the sequences behind a shared prefix.
 //
-// Every key and value is read once for the (up to 8) rows of its KV head and
-// used for a few multiplications a row: memory bounds it.  Eight lanes hold a
-// key, 8 dims each, so a warp reads four whole rows at a time straight into
-// registers; a row's products are summed over the eight lanes by halving
+// Every key and value is read once for the rows of its KV head and used for a few
+// multiplications a row: memory bounds it.  All sums are fp32; no shared memory but
+// for the join of a CTA's four warps.
+//
+// fp32: eight lanes hold a key, 8 dims each, so a warp reads four whole rows at a time
+// straight into registers; a row's products are summed over the eight lanes by halving
 // exchanges that leave row r's logit in lane r (7 shuffles for 8 rows, not 24).
-// fp32 throughout.
+//
+// bf16: up to 16 rows are the left operand of mma.sync, keys and then values the right
+// one, in the order in which lanes read whole 16-byte pieces: which dims a k index of
+// the logits' product stands for, and which dim a column of the outputs' is, is free as
+// long as both operands agree.  Logits come out of the product as probabilities go into
+// the next, values need one byte permutation a register (two keys' numbers of a dim
+// side by side).  Probabilities are rounded to bf16 for their product.  (The fp32
+// kernel on bf16 rows took 62 us for 500 sequences of up to 700 rows of 16 / 2 heads.)
 #include "sfa_cross.cuh"
 
 namespace sfa {
@@ -36,22 +45,213 @@ __device__ __forceinline__ float sum_rows(float* acc, int lane) {
   return acc[0];
 }
 
-template <typename TQ, typename TIO, int NR>
+// The warps' sums of a CTA's rows, R of them, [warp][row][64] and (m, l), to parts
+// or to o and lse.
+template <typename TIO, int R>
+__device__ __forceinline__ void stream_out(const CrossArgs& a, const float (*so)[R][kD], const float2 (*sml)[R], int b, int kvh, int r0, int s, int nq,
+                                           bool keys) {
+  const int rows = a.G * a.Tq;
+  for (int i = threadIdx.x; i < R * 32; i += 32 * kStreamWarps) {
+    const int r = i >> 5, d = (i & 31) * 2;
+    if (r0 + r >= rows) break;
+    const int t = (r0 + r) / a.G;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kStreamWarps; ++w) mm = fmaxf(mm, sml[w][r].x);
+    const float sh = shift_of(mm);
+    float ll = 0.0f, y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kStreamWarps; ++w) {
+      const float f = exp2f(sml[w][r].x - sh);
+      ll = fmaf(f, sml[w][r].y, ll);
+      y0 = fmaf(f, so[w][r][d], y0);
+      y1 = fmaf(f, so[w][r][d + 1], y1);
+    }
+    const int64_t row = a.row(b, kvh, r0 + r);
+    const bool none = t >= nq || !keys;
+    if (a.parts) {
+      const int64_t at = s * a.rows + row;
+      if (!none) store2(a.part_o + at * kD + d, y0, y1);
+      if (d == 0) a.part_ml[at] = none ? make_float2(-INFINITY, -1.0f) : make_float2(mm, ll);
+    } else {
+      const float inv = 1.0f / ll;
+      store2(static_cast<TIO*>(a.o) + row * kD + d, none ? 0.0f : y0 * inv, none ? 0.0f : y1 * inv);
+      if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    }
+  }
+}
+
+// The CTA's sequence, KV head, first row and split.
+struct StreamUnit {
+  int b, kvh, r0, s;
+};
+__device__ __forceinline__ StreamUnit stream_unit(const CrossArgs& a, int R) {
+  const int groups = (a.G * a.Tq + R - 1) / R;
+  StreamUnit u;
+  uint32_t x = blockIdx.x;
+  u.s = x % a.splits;
+  x /= a.splits;
+  u.r0 = (int)(x % groups) * R;
+  x /= groups;
+  u.kvh = x % a.Hkv;
+  u.b = x / a.Hkv;
+  return u;
+}
+
+constexpr int kMmaStep = 32;  // keys a warp takes at a time
+
+template <typename TQ>
+__global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(const CrossArgs a) {
+  constexpr int PARTS = sizeof(TQ) == 4 ? 2 : 1;  // of a query: fp32 ones as two bf16 numbers
+  __shared__ float so[kStreamWarps][16][kD];
+  __shared__ float2 sml[kStreamWarps][16];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+  const StreamUnit u = stream_unit(a, 16);
+  const int nq = a.queries(u.b), nk = a.keys(u.b);
+  int k0, k1;
+  split_keys(nk, kMmaStep, a.splits, u.s, k0, k1);
+
+  // queries: rows gid and gid + 8, dims 16 tig .. 16 tig + 15; k indexes 2 tig, 2 tig + 1,
+  // 2 tig + 8, 2 tig + 9 of step s are dims 16 tig + 4 s .. 4 s + 3
+  uint32_t q[PARTS][4][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = u.r0 + gid + 8 * h, t = r / a.G, head = u.kvh * a.G + (r - t * a.G);
+    float x[16];
+    if (r < a.G * a.Tq && t < nq) {
+      const TQ* row = static_cast<const TQ*>(a.q) + u.b * a.qs.b + head * a.qs.h + t * a.qs.t + 16 * tig;
+      load8(row, x);
+      load8(row + 8, x + 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float x0 = x[4 * s + 2 * c], x1 = x[4 * s + 2 * c + 1];
+        const uint32_t hi = pack_bf16(x0, x1);
+        q[0][s][2 * c + h] = hi;
+        if (PARTS == 2) {
+          const float2 f = unpack_bf16(hi);
+          q[PARTS - 1][s][2 * c + h] = pack_bf16(x0 - f.x, x1 - f.y);
+        }
+      }
+  }
+  const bf16* const kp = static_cast<const bf16*>(a.k) + u.b * a.ks.b + u.kvh * a.ks.h + 16 * tig;
+  const bf16* const vp = static_cast<const bf16*>(a.v) + u.b * a.vs.b + u.kvh * a.vs.h + 8 * gid;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of rows gid, gid + 8 (l: this lane's keys)
+  float o[8][4];  // [j]: row gid dims 16 tig + j, 16 tig + 8 + j, the same of row gid + 8
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+
+  for (int base = k0 + warp * kMmaStep; base < k1; base += kMmaStep * kStreamWarps) {
+    uint4 kf[4][2], vf[4][2];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {  // key 8 n + gid
+      const int j = base + 8 * n + gid;
+      const uint4* row = reinterpret_cast<const uint4*>(kp + (int64_t)j * a.ks.t);
+      kf[n][0] = j < k1 ? row[0] : make_uint4(0, 0, 0, 0);
+      kf[n][1] = j < k1 ? row[1] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // key 8 n + 2 tig + h
+        const int j = base + 8 * n + 2 * tig + h;
+        vf[n][h] = j < k1 ? *reinterpret_cast<const uint4*>(vp + (int64_t)j * a.vs.t) : make_uint4(0, 0, 0, 0);
+      }
+    float c[4][4];  // [n]: rows gid (0, 1) and gid + 8 (2, 3), keys 8 n + 2 tig, + 1
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
+      const uint32_t kr[8] = {kf[n][0].x, kf[n][0].y, kf[n][0].z, kf[n][0].w, kf[n][1].x, kf[n][1].y, kf[n][1].z, kf[n][1].w};
+#pragma unroll
+      for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) mma_bf16(c[n], q[p][s], kr[2 * s], kr[2 * s + 1]);
+    }
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (base + 8 * n + 2 * tig + (e & 1) >= k1) c[n][e] = -INFINITY;
+        top[e >> 1] = fmaxf(top[e >> 1], c[n][e]);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+    }
+    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float to = fmaxf(m[h], top[h]), corr = ex2((m[h] - shift_of(to)) * kLogitScale);
+        m[h] = to;
+        l[h] *= corr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j][2 * h] *= corr;
+          o[j][2 * h + 1] *= corr;
+        }
+      }
+    }
+    const float sh[2] = {shift_of(m[0]), shift_of(m[1])};
+    uint32_t p[4][2];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = ex2((c[n][2 * h] - sh[h]) * kLogitScale), p1 = ex2((c[n][2 * h + 1] - sh[h]) * kLogitScale);
+        l[h] += p0 + p1;
+        p[n][h] = pack_bf16(p0, p1);
+      }
+#pragma unroll
+    for (int n = 0; n < 4; n += 2) {  // 16 keys
+      const uint32_t pa[4] = {p[n][0], p[n][1], p[n + 1][0], p[n + 1][1]};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+        auto word = [&](const uint4& x) { return (j >> 1) == 0 ? x.x : (j >> 1) == 1 ? x.y : (j >> 1) == 2 ? x.z : x.w; };
+        mma_bf16(o[j], pa, __byte_perm(word(vf[n][0]), word(vf[n][1]), sel), __byte_perm(word(vf[n + 1][0]), word(vf[n + 1][1]), sel));
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    float* const row = &so[warp][gid + 8 * h][16 * tig];
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      *reinterpret_cast<float4*>(row + j) = make_float4(o[j][2 * h], o[j + 1][2 * h], o[j + 2][2 * h], o[j + 3][2 * h]);
+      *reinterpret_cast<float4*>(row + 8 + j) = make_float4(o[j][2 * h + 1], o[j + 1][2 * h + 1], o[j + 2][2 * h + 1], o[j + 3][2 * h + 1]);
+    }
+    if (tig == 0) sml[warp][gid + 8 * h] = make_float2(m[h] == -INFINITY ? m[h] : m[h] * kLogitScale, l[h]);
+  }
+  __syncthreads();
+  stream_out<bf16, 16>(a, so, sml, u.b, u.kvh, u.r0, u.s, nq, k1 > k0);
+}
+
+template <int NR>
 __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const CrossArgs a) {
-  constexpr int U = sizeof(TIO) == 2 ? 4 : 2;  // keys a lane takes at a time
-  constexpr int kStep = 4 * U;                  // keys a warp takes at a time
+  constexpr int U = 2;          // keys a lane takes at a time
+  constexpr int kStep = 4 * U;  // keys a warp takes at a time
   __shared__ float so[kStreamWarps][NR][kD];
   __shared__ float2 sml[kStreamWarps][NR];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kg = lane >> 3, d8 = (lane & 7) * 8;
-  const int rows = a.G * a.Tq, groups = (rows + NR - 1) / NR;
-  int64_t x = blockIdx.x;
-  const int s = (int)(x % a.splits);
-  x /= a.splits;
-  const int r0 = (int)(x % groups) * NR;
-  x /= groups;
-  const int kvh = (int)(x % a.Hkv), b = (int)(x / a.Hkv);
+  const int rows = a.G * a.Tq;
+  const StreamUnit unit = stream_unit(a, NR);
+  const int s = unit.s, r0 = unit.r0, kvh = unit.kvh, b = unit.b;
   const int nq = a.queries(b), nk = a.keys(b);
   int k0, k1;
   split_keys(nk, kStep, a.splits, s, k0, k1);
@@ -61,7 +261,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const C
   for (int r = 0; r < NR; ++r) {
     const int t = (r0 + r) / a.G, h = kvh * a.G + (r0 + r - t * a.G);
     if (r0 + r < rows && t < nq) {
-      load8(static_cast<const TQ*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t + d8, q[r]);
+      load8(static_cast<const float*>(a.q) + b * a.qs.b + h * a.qs.h + t * a.qs.t + d8, q[r]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) q[r][e] = 0.0f;
@@ -69,8 +269,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const C
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[r][e] *= kLogitScale;
   }
-  const TIO* kp = static_cast<const TIO*>(a.k) + b * a.ks.b + kvh * a.ks.h + d8;
-  const TIO* vp = static_cast<const TIO*>(a.v) + b * a.vs.b + kvh * a.vs.h + d8;
+  const float* kp = static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h + d8;
+  const float* vp = static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h + d8;
   float m = -INFINITY, l = 0.0f;  // of row lane mod NR
   float o[NR][8];
 #pragma unroll
@@ -144,34 +344,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const C
 #pragma unroll
     for (int r = 0; r < NR; ++r) st_smem8(&so[warp][r][d8], o[r]);
   __syncthreads();
-  for (int i = threadIdx.x; i < NR * 32; i += 32 * kStreamWarps) {
-    const int r = i >> 5, d = (i & 31) * 2;
-    if (r0 + r >= rows) break;
-    const int t = (r0 + r) / a.G;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kStreamWarps; ++w) mm = fmaxf(mm, sml[w][r].x);
-    const float sh = shift_of(mm);
-    float ll = 0.0f, y0 = 0.0f, y1 = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kStreamWarps; ++w) {
-      const float f = exp2f(sml[w][r].x - sh);
-      ll = fmaf(f, sml[w][r].y, ll);
-      y0 = fmaf(f, so[w][r][d], y0);
-      y1 = fmaf(f, so[w][r][d + 1], y1);
-    }
-    const int64_t row = a.row(b, kvh, r0 + r);
-    const bool none = t >= nq || k1 <= k0;
-    if (a.parts) {
-      const int64_t at = s * a.rows + row;
-      if (!none) store2(a.part_o + at * kD + d, y0, y1);
-      if (d == 0) a.part_ml[at] = none ? make_float2(-INFINITY, -1.0f) : make_float2(mm, ll);
-    } else {
-      const float inv = none ? 0.0f : 1.0f / ll;
-      store2(static_cast<TIO*>(a.o) + row * kD + d, none ? 0.0f : y0 * inv, none ? 0.0f : y1 * inv);
-      if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
-    }
-  }
+  stream_out<float, NR>(a, so, sml, b, kvh, r0, s, nq, k1 > k0);
 }
 
 // Parts of each row to o and lse, a warp a row.  pos (of sequences whose rows
@@ -201,21 +374,19 @@ int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
-template <typename TQ, typename TIO>
-static cudaError_t stream_rows(const CrossArgs& a, cudaStream_t st) {
-  const int rows = a.G * a.Tq, nr = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
-  const int64_t grid = (int64_t)a.B * a.Hkv * ((rows + nr - 1) / nr) * a.splits;
-  auto* f = nr == 1 ? cross_stream_kernel<TQ, TIO, 1> : nr == 2 ? cross_stream_kernel<TQ, TIO, 2>
-          : nr == 4 ? cross_stream_kernel<TQ, TIO, 4> : cross_stream_kernel<TQ, TIO, 8>;
-  return launch_pdl(f, dim3((unsigned)grid), dim3(32 * kStreamWarps), 0, st, a);
-}
+static unsigned stream_grid(const CrossArgs& a, int R) { return (unsigned)((int64_t)a.B * a.Hkv * ((a.G * a.Tq + R - 1) / R) * a.splits); }
 
 int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream) {
   cudaStream_t st = (cudaStream_t)stream;
+  const dim3 block(32 * kStreamWarps);
+  const int rows = a.G * a.Tq, nr = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
   LaunchTimer tm(SFA_KERNEL_CROSS_FWD, stream);
-  const cudaError_t e = dtype == SFA_F32 ? stream_rows<float, float>(a, st)
-                        : q32            ? stream_rows<float, bf16>(a, st)
-                                         : stream_rows<bf16, bf16>(a, st);
+  cudaError_t e;
+  if (dtype == SFA_BF16)
+    e = launch_pdl(q32 ? cross_stream_mma_kernel<float> : cross_stream_mma_kernel<bf16>, dim3(stream_grid(a, 16)), block, 0, st, a);
+  else
+    e = launch_pdl(nr == 1 ? cross_stream_kernel<1> : nr == 2 ? cross_stream_kernel<2> : nr == 4 ? cross_stream_kernel<4> : cross_stream_kernel<8>,
+                   dim3(stream_grid(a, nr)), block, 0, st, a);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
