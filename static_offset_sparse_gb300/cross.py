@@ -3,19 +3,38 @@ decode step behind a shared prefix (sfa_prefix_decode).
 
 Calls take the current stream of their tensors' device, only enqueue work, keep
 nothing, and may be captured into a CUDA graph (prefix_decode with a RoPE table
-made before).  include/sfa.h says what each computes."""
+made before).  include/sfa.h says what each computes.
+
+As with the paged cache, a call whose arguments are in order and that gives no
+outputs or workspace is made by csrc/cross_py.cpp; any other, or all if that could not
+be built, here."""
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import struct
 
 import torch
 
-from ._lib import check
+from ._lib import _lib, check
+from .api import _ROPE_CACHE
 from .kv4 import _F32, _I32, _U8, _call, _code, _dense, _entry, _ints, _refuse, _rope, _rows
 
 _cross_desc = struct.Struct("7i4x9q2P").pack  # the bytes of _lib.CrossDesc
 _prefix_desc = struct.Struct("7i4x5qPi4x").pack  # and of _lib.PrefixDesc
+
+
+@functools.cache
+def _native():
+    """The native calls, or None where they could not be built."""
+    try:
+        from . import _cross
+    except ImportError:
+        return None
+    L = _lib()
+    _cross.bind(*(C.cast(L[name], C.c_void_p).value for name in ("sfa_cross_workspace_size", "sfa_cross_forward", "sfa_cross_backward",
+                                                                  "sfa_prefix_workspace_size", "sfa_prefix_decode")))
+    return _cross
 
 
 def _view(t, name, like=None, shape=None):
@@ -89,6 +108,13 @@ def cross_forward(q, k, v, *, q_len=None, kv_len=None, o=None, lse=None, ws=None
     and kv_len: int32 [B], how many rows of each sequence count (None: all); a
     query behind its length or without a key gives zeros and lse = -inf.  A single
     token a sequence is Tq = 1.  Returns o [B, Hq, Tq, 64] and lse fp32 [B, Hq, Tq]."""
+    fast = _native()
+    if fast is not None and o is None and lse is None and ws is None:
+        r = fast.forward(q, k, v, q_len, kv_len)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            check(r, "sfa_cross_forward")
     at, qshape, _, d = _describe(q, k, v, q_len, kv_len)
     o, op = _output(o, "o", at, qshape, q.dtype)
     lse, lp = _output(lse, "lse", at, qshape[:3], _F32)
@@ -101,6 +127,13 @@ def cross_backward(q, k, v, o, lse, do, *, q_len=None, kv_len=None, dq=None, dk=
     """Gradients of sum(o * do) for cross_forward's q, k, v, from its o and lse
     (sfa_cross_backward): dq [B, Hq, Tq, 64], dk and dv [B, Hkv, Tk, 64], contiguous,
     zeros behind the lengths.  The same inputs give the same bits."""
+    fast = _native()
+    if fast is not None and dq is None and dk is None and dv is None and ws is None:
+        r = fast.backward(q, k, v, o, lse, do, q_len, kv_len)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            check(r, "sfa_cross_backward")
     at, qshape, kshape, d = _describe(q, k, v, q_len, kv_len)
     inputs = _dense(at, qshape, q.dtype, o, "o"), _dense(at, qshape[:3], _F32, lse, "lse"), _dense(at, qshape, q.dtype, do, "do")
     dq, qp = _output(dq, "dq", at, qshape, q.dtype)
@@ -134,6 +167,17 @@ def prefix_decode(q, k_new, v_new, prefix_k, prefix_v, k_cache, v_cache, pos, *,
     its cache.  rope: a table of rope_table for P + T positions or more, else that of
     rope_theta (0: no rotation; prefix and caches then hold unrotated keys).  Returns o
     [B, Hq, 64] and lse fp32 [B, Hq]."""
+    fast = _native()
+    if fast is not None and o is None and lse is None and ws is None:
+        made = rope
+        if made is None and rope_theta and prefix_k.dim() == 3 and k_cache.dim() == 4:
+            made = _ROPE_CACHE.get((prefix_k.shape[1] + k_cache.shape[2], float(rope_theta), k_cache.get_device()))
+        if made is not None or not rope_theta:
+            r = fast.prefix(q, k_new, v_new, prefix_k, prefix_v, k_cache, v_cache, pos, made)
+            if type(r) is tuple:
+                return r
+            if r is not None:
+                check(r, "sfa_prefix_decode")
     at = k_cache.get_device() if k_cache.is_cuda else -1
     if at < 0 or k_cache.dim() != 4 or not k_cache.is_contiguous():
         _refuse("k_cache", k_cache, k_cache.dtype, (None, None, None, 64))

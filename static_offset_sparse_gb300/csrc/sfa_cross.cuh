@@ -122,6 +122,10 @@ struct Shares {
   __host__ __device__ __forceinline__ int64_t begin(int c) const { return share * c + (c < rest ? c : rest); }
   __host__ __device__ __forceinline__ int owner(int64_t w) const {
     const int64_t big = (share + 1) * rest;
+    if (((w | share) >> 31) == 0 && (big >> 31) == 0) {  // (64-bit division is slow)
+      const uint32_t x = (uint32_t)w, n = (uint32_t)share, b = (uint32_t)big;
+      return (int)(x < b ? x / (n + 1) : (uint32_t)rest + (x - b) / n);
+    }
     return (int)(w < big ? w / (share + 1) : rest + (w - big) / share);
   }
 };

@@ -98,7 +98,7 @@ __device__ __forceinline__ StreamUnit stream_unit(const CrossArgs& a, int R) {
   return u;
 }
 
-constexpr int kMmaStep = 32;  // keys a warp takes at a time
+constexpr int kMmaStep = 16;  // keys a warp takes at a time; the next ones are under way meanwhile
 
 template <typename TQ>
 __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(const CrossArgs a) {
@@ -150,28 +150,32 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(con
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
 
-  for (int base = k0 + warp * kMmaStep; base < k1; base += kMmaStep * kStreamWarps) {
-    uint4 kf[4][2], vf[4][2];
+  struct Rows {
+    uint4 k[2][2], v[2][2];  // key 8 n + gid: both halves of its 32 bytes; keys 8 n + 2 tig, + 1
+  };
+  auto load = [&](Rows& x, int base) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {  // key 8 n + gid
+    for (int n = 0; n < 2; ++n) {
       const int j = base + 8 * n + gid;
       const uint4* row = reinterpret_cast<const uint4*>(kp + (int64_t)j * a.ks.t);
-      kf[n][0] = j < k1 ? row[0] : make_uint4(0, 0, 0, 0);
-      kf[n][1] = j < k1 ? row[1] : make_uint4(0, 0, 0, 0);
+      x.k[n][0] = j < k1 ? row[0] : make_uint4(0, 0, 0, 0);
+      x.k[n][1] = j < k1 ? row[1] : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // key 8 n + 2 tig + h
+      for (int h = 0; h < 2; ++h) {
         const int j = base + 8 * n + 2 * tig + h;
-        vf[n][h] = j < k1 ? *reinterpret_cast<const uint4*>(vp + (int64_t)j * a.vs.t) : make_uint4(0, 0, 0, 0);
+        x.v[n][h] = j < k1 ? *reinterpret_cast<const uint4*>(vp + (int64_t)j * a.vs.t) : make_uint4(0, 0, 0, 0);
       }
-    float c[4][4];  // [n]: rows gid (0, 1) and gid + 8 (2, 3), keys 8 n + 2 tig, + 1
+  };
+  auto take = [&](const Rows& x, int base) {
+    float c[2][4];  // [n]: rows gid (0, 1) and gid + 8 (2, 3), keys 8 n + 2 tig, + 1
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < 2; ++n) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
-      const uint32_t kr[8] = {kf[n][0].x, kf[n][0].y, kf[n][0].z, kf[n][0].w, kf[n][1].x, kf[n][1].y, kf[n][1].z, kf[n][1].w};
+      const uint32_t kr[8] = {x.k[n][0].x, x.k[n][0].y, x.k[n][0].z, x.k[n][0].w, x.k[n][1].x, x.k[n][1].y, x.k[n][1].z, x.k[n][1].w};
 #pragma unroll
       for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
@@ -179,20 +183,18 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(con
     }
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (base + 8 * n + 2 * tig + (e & 1) >= k1) c[n][e] = -INFINITY;
         top[e >> 1] = fmaxf(top[e >> 1], c[n][e]);
       }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-    }
+    // (a lane's own maxima: a row's four lanes exchange theirs only where one has grown)
     if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
         const float to = fmaxf(m[h], top[h]), corr = ex2((m[h] - shift_of(to)) * kLogitScale);
         m[h] = to;
         l[h] *= corr;
@@ -204,25 +206,33 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(con
       }
     }
     const float sh[2] = {shift_of(m[0]), shift_of(m[1])};
-    uint32_t p[4][2];
+    uint32_t p[2][2];
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float p0 = ex2((c[n][2 * h] - sh[h]) * kLogitScale), p1 = ex2((c[n][2 * h + 1] - sh[h]) * kLogitScale);
         l[h] += p0 + p1;
         p[n][h] = pack_bf16(p0, p1);
       }
+    const uint32_t pa[4] = {p[0][0], p[0][1], p[1][0], p[1][1]};
 #pragma unroll
-    for (int n = 0; n < 4; n += 2) {  // 16 keys
-      const uint32_t pa[4] = {p[n][0], p[n][1], p[n + 1][0], p[n + 1][1]};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
-        auto word = [&](const uint4& x) { return (j >> 1) == 0 ? x.x : (j >> 1) == 1 ? x.y : (j >> 1) == 2 ? x.z : x.w; };
-        mma_bf16(o[j], pa, __byte_perm(word(vf[n][0]), word(vf[n][1]), sel), __byte_perm(word(vf[n + 1][0]), word(vf[n + 1][1]), sel));
-      }
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t sel = j & 1 ? 0x7632 : 0x5410;
+      auto word = [&](const uint4& w) { return (j >> 1) == 0 ? w.x : (j >> 1) == 1 ? w.y : (j >> 1) == 2 ? w.z : w.w; };
+      mma_bf16(o[j], pa, __byte_perm(word(x.v[0][0]), word(x.v[0][1]), sel), __byte_perm(word(x.v[1][0]), word(x.v[1][1]), sel));
     }
+  };
+  constexpr int kNext = kMmaStep * kStreamWarps;
+  Rows r0, r1;
+  int base = k0 + warp * kMmaStep;
+  if (base < k1) load(r0, base);
+  for (; base < k1; base += 2 * kNext) {
+    if (base + kNext < k1) load(r1, base + kNext);
+    take(r0, base);
+    if (base + kNext >= k1) break;
+    if (base + 2 * kNext < k1) load(r0, base + 2 * kNext);
+    take(r1, base + kNext);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
