@@ -26,7 +26,7 @@ NATIVE = {"_kv4.so": "kv4_py.cpp", "_cross.so": "cross_py.cpp"}  # native Python
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["sfa_host.cpp", "sfa_api.cu", "sfa_fwd.cu", "sfa_bwd.cu", "sfa_fwd_tc.cu", "sfa_bwd_tc.cu",
            "sfa_noalloc.cu", "sfa_decode.cu", "sfa_schedule.cpp", "sfa_band.cu", "sfa_kv4.cu", "sfa_kv4_attend.cu", "sfa_kv4_prompt.cu",
-           "sfa_cross.cu", "sfa_cross_stream.cu", "sfa_cross_simt.cu", "sfa_cross_tc.cu",
+           "sfa_cross.cu", "sfa_cross_stream.cu", "sfa_cross_f32.cu", "sfa_cross_tc.cu",
            "sfa_cross_bwd_tc.cu"]
 # The bounds-checked build (libsfa_debug.so) recompiles the SIMT kernels with
 # SFA_DEBUG_BOUNDS: every row index they form is range-checked, a bad one is

@@ -120,7 +120,7 @@ static Kind forward_kind(int rows, int dtype) { return rows <= stream_rows(dtype
 // Parts of a call over `units` (sequence, KV head) pairs of Tq queries of G heads (not the tensor cores').
 static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind) {
   if (kind == kFewRows) return wave_splits(units, 4 * kSMs, Tk, 256);
-  return wave_splits(units * ((G * Tq + kSimtTile - 1) / kSimtTile), 3 * kSMs, (Tk + kSimtTile - 1) / kSimtTile, 2);
+  return wave_splits(units * ((G * Tq + kF32Tile - 1) / kF32Tile), 3 * kSMs, (Tk + kF32Tile - 1) / kF32Tile, 1);
 }
 
 static size_t part_bytes(int splits, int64_t rows) {
@@ -211,9 +211,9 @@ static BackwardPlan backward_plan(const sfa_cross_desc* d) {
     p.bytes = cross_bwd_tc_bytes(d->B, d->Hkv, G, d->Tq, d->Tk);
     return p;
   }
-  const int rt = (G * d->Tq + kSimtTile - 1) / kSimtTile, kt = (d->Tk + kSimtTile - 1) / kSimtTile;
-  p.dq_splits = wave_splits(units * rt, 2 * kSMs, kt, 2);
-  p.dkv_splits = wave_splits(units * kt, kSMs, rt, 2);
+  const int rt = (G * d->Tq + kF32Tile - 1) / kF32Tile, kt = (d->Tk + kF32Tile - 1) / kF32Tile;
+  p.dq_splits = wave_splits(units * rt, 8 * kSMs, kt, 1);
+  p.dkv_splits = wave_splits(units * kt, 8 * kSMs, rt, 1);
   p.rows = (int64_t)d->B * d->Hq * d->Tq;
   p.keys = units * d->Tk;
   p.stat = align256((size_t)p.rows * sizeof(float2));
@@ -310,7 +310,7 @@ int sfa_cross_forward(const sfa_cross_desc* d, const void* q, const void* k, con
   a.splits = p.splits;
   a.parts = a.splits > 1;
   if (a.parts) set_parts(&a, static_cast<char*>(ws), a.splits, a.rows, 0);
-  rc = p.kind == kFewRows ? launch_cross_stream(a, false, d->dtype, stream) : launch_cross_fwd_simt(a, stream);
+  rc = p.kind == kFewRows ? launch_cross_stream(a, false, d->dtype, stream) : launch_cross_fwd_f32(a, stream);
   return rc != SFA_OK || !a.parts ? rc : launch_cross_join(a, d->dtype, nullptr, 0, stream);
 }
 
@@ -347,12 +347,12 @@ int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, co
   a.splits = p.dq_splits;
   a.parts = a.splits > 1;
   a.part_a = parts;
-  if ((rc = launch_cross_dq_simt(a, stream)) != SFA_OK) return rc;
+  if ((rc = launch_cross_dq_f32(a, stream)) != SFA_OK) return rc;
   if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, stream)) != SFA_OK) return rc;
   a.splits = p.dkv_splits;
   a.parts = a.splits > 1;
   a.part_b = parts + (size_t)a.splits * p.keys * kD;
-  if ((rc = launch_cross_dkv_simt(a, stream)) != SFA_OK || !a.parts) return rc;
+  if ((rc = launch_cross_dkv_f32(a, stream)) != SFA_OK || !a.parts) return rc;
   if ((rc = launch_sum(a.part_a, a.splits, p.keys * kD, dk, stream)) != SFA_OK) return rc;
   return launch_sum(a.part_b, a.splits, p.keys * kD, dv, stream);
 }
@@ -414,7 +414,7 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
     set_parts(&a, parts, p.shared + p.own, p.rows, 0);
     rc = p.two ? launch_prefix_tc(a, parts + p.parts, stream)
          : p.kind == kFewRows ? launch_cross_stream(a, true, d->dtype, stream)
-                              : launch_cross_fwd_simt(a, stream);
+                              : launch_cross_fwd_f32(a, stream);
     if (rc != SFA_OK) return rc;
   }
   const CrossArgs prefix = a;

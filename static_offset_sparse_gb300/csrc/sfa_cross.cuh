@@ -408,7 +408,7 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 // host side
 int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream);
 int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos_T, void* stream);
-int launch_cross_fwd_simt(const CrossArgs& a, void* stream);
+int launch_cross_fwd_f32(const CrossArgs& a, void* stream);
 // A tensor map of bf16 rows: boxes of `heads` x `rows` rows, 128-byte swizzle (sfa_api.cu).
 int make_rows4_map(CUtensorMap* m, const void* base, int T, int H, int B, int64_t s_t, int64_t s_h, int64_t s_b, int box_rows, int box_heads);
 inline int make_view_map(CUtensorMap* m, const void* base, int T, int H, int B, const Strides& s, int rows, int heads) {
@@ -426,10 +426,10 @@ int launch_prefix_join(const CrossArgs& prefix, const CrossArgs& out, void* ws, 
 size_t cross_bwd_tc_bytes(int B, int Hkv, int G, int Tq, int Tk);
 int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream);
 // Backward pass, fp32.
-int launch_cross_dq_simt(const CrossArgs& a, void* stream);
-int launch_cross_dkv_simt(const CrossArgs& a, void* stream);
+int launch_cross_dq_f32(const CrossArgs& a, void* stream);
+int launch_cross_dkv_f32(const CrossArgs& a, void* stream);
 constexpr int kStreamRows = 8, kStreamRowsBf16 = 16;  // rows that the kernels for few rows take at once
-constexpr int kSimtTile = 64;   // rows and keys of the fp32 kernels' tiles
+constexpr int kF32Tile = 64;   // rows and keys of the fp32 kernels' tiles
 
 // Splits of `units` units of work a CTA where there are `ctas` CTAs and room for
 // `slots`: one wave of them, `least` units each.
