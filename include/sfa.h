@@ -386,6 +386,7 @@ int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
  * any gradient; gradients behind the lengths are zeros.  What stands in q, k, v,
  * o, lse and dO behind the lengths may be anything, NaN too.  A length outside
  * [0, Tq] or [0, Tk] counts as 0 and is recorded as SFA_ERR_DEVICE_BOUNDS.
+ * Outputs overlap neither inputs nor each other.
  * Hq / Hkv <= 32 (any whole number); Tq, Tk <= 2^24; B Hq Tq and B Hkv Tk below
  * 2^30.  Calls only enqueue work, keep no state, and may be captured. */
 typedef struct {
@@ -428,10 +429,12 @@ int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, co
  * The new key, rotated at P + pos[b] by d->rope (fp32, one rounding), and the new
  * value are written to row pos[b] of sequence b's caches; then the query, rotated
  * there too, attends the P rows of the prefix and rows 0..pos[b] of its cache.
- * What stands behind pos[b] may be anything.  A position out of range writes
- * nothing, gives a zero row with lse = -inf and is recorded as
- * SFA_ERR_DEVICE_BOUNDS.  rope: sfa_rope_table for rope_T >= P + T positions, or
- * NULL for no rotation.  Hq / Hkv <= 32; P, T <= 2^24; B Hq below 2^24, Hkv P and
+ * What stands behind pos[b] may be anything; an infinity in a bf16 key that counts
+ * makes its logits NaN (the rotated query is multiplied as the sum of two bf16
+ * numbers).  A position out of range writes nothing, gives a zero row with
+ * lse = -inf and is recorded as SFA_ERR_DEVICE_BOUNDS.  rope: sfa_rope_table for
+ * rope_T >= P + T positions, or NULL for no rotation.  o, lse and the caches
+ * overlap nothing else.  Hq / Hkv <= 32; P, T <= 2^24; B Hq below 2^24, Hkv P and
  * B Hkv T below 2^30. */
 typedef struct {
   int32_t B, P, T, Hq, Hkv, D; /* P >= 0; D = 64 */
@@ -522,7 +525,9 @@ int sfa_set_option(int32_t option, int32_t value);
  * nor the loads of that staged group (window chunks first, then rung pairs),
  * so its consumers' wait runs out with nothing in flight, and the first warp
  * that streams sfa_kv4_attend's first keys start no copies for that tile of its
- * ring; -1 turns this off.
+ * ring; CTA 0 of the tensor-core kernels of sfa_cross_forward, sfa_cross_backward
+ * and sfa_prefix_decode leaves out that copy (forward: keys and values in turn;
+ * backward: steps); -1 turns this off.
  * The setting is process-wide and read by every later call until changed;
  * the outputs of a call that timed out are undefined.  Returns
  * SFA_ERR_INVALID_ARG for wait_cycles < 0 or skip_group < -1. */

@@ -174,8 +174,7 @@ static int cross_args(const sfa_cross_desc* d, CrossArgs* a) {
   a->Hq = d->Hq;
   a->Hkv = d->Hkv;
   a->G = d->Hq / d->Hkv;
-  int32_t skip;
-  wait_injection(&a->wait_cycles, &skip);
+  wait_injection(&a->wait_cycles, &a->debug_skip);
   return device_status(&a->status);
 }
 
@@ -378,8 +377,7 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
   const PrefixPlan p = prefix_plan(d);
   if (ws_bytes < p.bytes) return SFA_ERR_CAPACITY;
   CrossArgs a = {};
-  int32_t skip;
-  wait_injection(&a.wait_cycles, &skip);
+  wait_injection(&a.wait_cycles, &a.debug_skip);
   if ((rc = device_status(&a.status)) != SFA_OK) return rc;
   char* const w = static_cast<char*>(ws);
   char* const parts = w + p.q32 + p.q16;

@@ -53,6 +53,7 @@ struct CrossArgs {
   float *part_a, *part_b;  // fp32 kernels: [splits][dq's] or [splits][dk's], [splits][dv's]
   int* status;
   long long wait_cycles;
+  int debug_skip;  // test injection: the copy that CTA 0 of a tensor-core kernel leaves out, or -1
 
   // Valid queries and keys of sequence b; a length out of range counts as none
   // and is recorded.
@@ -226,6 +227,19 @@ __device__ __forceinline__ bool find_walk(int B, const F& counts, WalkShared& sh
   if (!sh.any) return false;
   wk = sh.first;
   return wk.set(from - wk.begin) || wk.next(B, counts);
+}
+
+// For each x = blockIdx.x, blockIdx.x + gridDim.x, .. below n with empty(x), do(x), by
+// whole warps; a lane looks at an x, so that the lengths of 32 are asked for at once.
+template <typename E, typename D>
+__device__ __forceinline__ void each_empty(int64_t n, int lane, const E& empty, const D& todo) {
+#pragma unroll 1
+  for (int64_t from = blockIdx.x; from < n; from += 32 * (int64_t)gridDim.x) {
+    const int64_t x = from + (int64_t)lane * gridDim.x;
+#pragma unroll 1
+    for (unsigned left = __ballot_sync(0xffffffffu, x < n && empty(x)); left; left &= left - 1)
+      todo(from + (int64_t)(__ffs(left) - 1) * gridDim.x);
+  }
 }
 
 // Keys of split s of n, in whole tiles of `tile`: begin and end.

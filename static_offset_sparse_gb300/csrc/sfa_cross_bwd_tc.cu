@@ -142,28 +142,33 @@ __global__ void __launch_bounds__(kBtThreads, 1)
     const int quarter = warp >> 2, r = tid & 127;
     const uint32_t tl = tm + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
     // tiles without work: zeros
-    {
+    if (a.q_len || a.kv_len) {
       const int own = DKV ? w.key_tiles : w.rt.tiles;
-      for (int64_t x = blockIdx.x; x < (int64_t)a.B * a.Hkv * own; x += gridDim.x) {
-        const int bh = (int)(x / own), tile = (int)(x - (int64_t)bh * own), b = bh / a.Hkv;
-        int units, steps;
-        counts(b, units, steps);
-        if (tile < units / a.Hkv) continue;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        if (DKV) {
-          const int j = tile * 128 + r;
-          if (j >= a.Tk) continue;
-          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(quarter >> 1 ? a.dv : a.dk) + ((int64_t)bh * a.Tk + j) * kD + 32 * (quarter & 1));
+      each_empty(
+          (int64_t)a.B * a.Hkv * own, lane,
+          [&](int64_t x) {
+            const int bh = (int)(x / own);
+            int units, steps;
+            counts(bh / a.Hkv, units, steps);
+            return x - (int64_t)bh * own >= units / a.Hkv;
+          },
+          [&](int64_t x) {
+            const int bh = (int)(x / own), tile = (int)(x - (int64_t)bh * own), b = bh / a.Hkv;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            if (DKV) {
+              const int j = tile * 128 + r;
+              if (j >= a.Tk) return;
+              uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(quarter >> 1 ? a.dv : a.dk) + ((int64_t)bh * a.Tk + j) * kD + 32 * (quarter & 1));
 #pragma unroll
-          for (int c = 0; c < 4; ++c) out[c] = zero;
-        } else {
-          const RowOf ro = row_of(a, w.rt, tile, r);
-          if (!ro.mine) continue;
-          uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(a.dq) + a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g) * kD + 16 * quarter);
-          out[0] = zero;
-          out[1] = zero;
-        }
-      }
+              for (int c = 0; c < 4; ++c) out[c] = zero;
+            } else {
+              const RowOf ro = row_of(a, w.rt, tile, r);
+              if (!ro.mine) return;
+              uint4* const out = reinterpret_cast<uint4*>(static_cast<bf16*>(a.dq) + a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g) * kD + 16 * quarter);
+              out[0] = zero;
+              out[1] = zero;
+            }
+          });
     }
     int n = 0;
     for (;;) {
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
           const int st = n % kBtStages;
           if (n >= kBtStages) wait(&sh.empty[st], n / kBtStages - 1);
           if (dead) break;
-          if (lead) {
+          if (lead && (n != a.debug_skip || blockIdx.x > 0)) {
             const uint32_t bar = smem_u32(&sh.full[st]), dst = smem + kBtRing + st * 2 * kBtTile;
             mbar_expect_tx(bar, 2 * kBtTile + (DKV ? kBtStat : 0));
             if (DKV) {
@@ -359,8 +364,8 @@ __global__ void __launch_bounds__(kBtThreads, 1)
       }
       if (dead) {  // copies under way end before their memory goes
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
-        for (int i = max(0, n - kBtStages); i < n; ++i) mbar_wait_bounded(smem_u32(&sh.full[i % kBtStages]), (i / kBtStages) & 1, a.wait_cycles);
-        for (int i = max(0, pieces - 1); i <= pieces; ++i) mbar_wait_bounded(smem_u32(&sh.a_full[i & 1]), (i / 2) & 1, a.wait_cycles);
+        for (int i = max(0, n - kBtStages); i < n; ++i) mbar_wait_bounded(smem_u32(&sh.full[i % kBtStages]), (i / kBtStages) & 1, kDefaultWaitCycles);
+        for (int i = max(0, pieces - 1); i <= pieces; ++i) mbar_wait_bounded(smem_u32(&sh.a_full[i & 1]), (i / 2) & 1, kDefaultWaitCycles);
       }
     } else if (warp == kBtSoftmax + 1) {
       // ---- S and dP
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
       }
       if (dead) {  // products under way end before their memory goes
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
-        for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.s_full), i & 1, a.wait_cycles);
+        for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.s_full), i & 1, kDefaultWaitCycles);
       }
     } else if (warp == kBtSoftmax + 2) {
       // ---- the sums
@@ -448,7 +453,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
       }
       if (dead) {  // products under way end before their memory goes
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
-        for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.done), i & 1, a.wait_cycles);
+        for (int i = max(0, n - 1); i <= n; ++i) mbar_wait_bounded(smem_u32(&sh.done), i & 1, kDefaultWaitCycles);
       }
     } else if (warp == kBtSoftmax + 3) {
       // ---- rows that pass by and count for nothing are made zeros (they may hold

@@ -19,6 +19,10 @@ constexpr int kTileN = kF32Tile;
 constexpr int kPitch = 68;  // floats a line: lines 4 banks apart, so both reads of right operands are free of conflicts
 constexpr int kThreads32 = 128;
 
+// A number of infinite or overflowing products: split, its parts' products are
+// infinities of either sign.  Below it sums of 64 products stay finite.
+__device__ __forceinline__ bool huge(float x) { return fabsf(x) >= 0x1p60f; }
+
 struct Split {
   uint32_t hi, lo;
 };
@@ -45,6 +49,12 @@ struct Left {
       x[0][i] = lo ? lo[tig + 4 * i] : 0.0f;
       x[1][i] = hi ? hi[tig + 4 * i] : 0.0f;
     }
+  }
+  __device__ __forceinline__ bool plain() const {
+    bool y = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y |= huge(x[0][i]) || huge(x[1][i]);
+    return y;
   }
   // step s: rows gid, gid + 8 of k tig, then of k tig + 4
   __device__ __forceinline__ void step(int s, Split* a) const {
@@ -127,16 +137,48 @@ __device__ __forceinline__ void dims_product(float (*o)[4], const float* p, cons
   }
 }
 
+// Tiles that hold huge numbers are multiplied as they are, by the following two.
+// c[n] as rows_product's, of left(h, d): this lane's row gid (h = 0) or gid + 8, dim d.
+template <int N, typename F>
+__device__ __forceinline__ void rows_plain(float (*c)[4], const F& left, const float* tile, int n0, int tig) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float* const row = tile + (8 * (n0 + n) + 2 * tig + (e & 1)) * kPitch;
+      float y = 0.0f;
+#pragma unroll 1
+      for (int d = 0; d < kD; ++d) y = fmaf(left(e >> 1, d), row[d], y);
+      c[n][e] = y;
+    }
+}
+// o += as dims_product's.
+__device__ __forceinline__ void dims_plain(float (*o)[4], const float* p, const float* tile, int n, int gid, int tig) {
+#pragma unroll 1
+  for (int key = 0; key < 8; ++key) {
+    const int from = 4 * gid + (key >> 1);
+    const float lo = __shfl_sync(0xffffffffu, key & 1 ? p[1] : p[0], from), hi = __shfl_sync(0xffffffffu, key & 1 ? p[3] : p[2], from);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = fmaf(e < 2 ? lo : hi, tile[(8 * n + key) * kPitch + 8 * c + 2 * tig + (e & 1)], o[c][e]);
+  }
+}
+
 // 64 rows into a tile: row(r) gives row r's address, or nullptr for zeros.  Sixteen
-// lanes a row.
+// lanes a row.  Whether this thread met a huge number.
 template <typename F>
-__device__ __forceinline__ void load_tile(float* tile, const F& row) {
+__device__ __forceinline__ bool load_tile(float* tile, const F& row) {
   const int c = (threadIdx.x & 15) * 4;
+  bool plain = false;
 #pragma unroll
   for (int r = threadIdx.x >> 4; r < kTileN; r += kThreads32 / 16) {
     const float* const p = row(r);
-    *reinterpret_cast<float4*>(tile + r * kPitch + c) = p ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 x = p ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    plain |= huge(x.x) || huge(x.y) || huge(x.z) || huge(x.w);
+    *reinterpret_cast<float4*>(tile + r * kPitch + c) = x;
   }
+  return plain;
 }
 
 // ---- forward: a CTA has 64 rows of a (sequence, KV head) and a split of its keys
@@ -157,16 +199,17 @@ __global__ void __launch_bounds__(kThreads32) cross_fwd_kernel(const CrossArgs a
   int k0, k1;
   split_keys(nk, kTileN, a.splits, s, k0, k1);
   if (r0 >= (int64_t)nq * a.G) k1 = k0;  // no query in the tile
+  auto query = [&](int h) {
+    const int r = r0 + 16 * warp + gid + 8 * h, t = r / a.G, head = kvh * a.G + (r - t * a.G);
+    return r < rows && t < nq ? static_cast<const float*>(a.q) + b * a.qs.b + head * a.qs.h + t * a.qs.t : nullptr;
+  };
+  auto query_dim = [&](int h, int d) {
+    const float* const row = query(h);
+    return row ? row[d] : 0.0f;
+  };
   Left q;
-  {
-    const float* row[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = r0 + 16 * warp + gid + 8 * h, t = r / a.G, head = kvh * a.G + (r - t * a.G);
-      row[h] = r < rows && t < nq ? static_cast<const float*>(a.q) + b * a.qs.b + head * a.qs.h + t * a.qs.t : nullptr;
-    }
-    q.load(row[0], row[1], tig);
-  }
+  q.load(query(0), query(1), tig);
+  const bool q_plain = q.plain();
   const float* const kp = static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h;
   const float* const vp = static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h;
   float o[8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // of rows gid, gid + 8 (l: this lane's keys)
@@ -176,12 +219,16 @@ __global__ void __launch_bounds__(kThreads32) cross_fwd_kernel(const CrossArgs a
     for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
   for (int j0 = k0; j0 < k1; j0 += kTileN) {
     __syncthreads();  // the last tile has been read
-    load_tile(Ks, [&](int r) { return j0 + r < k1 ? kp + (int64_t)(j0 + r) * a.ks.t : nullptr; });
-    load_tile(Vs, [&](int r) { return j0 + r < k1 ? vp + (int64_t)(j0 + r) * a.vs.t : nullptr; });
-    __syncthreads();
+    bool plain = load_tile(Ks, [&](int r) { return j0 + r < k1 ? kp + (int64_t)(j0 + r) * a.ks.t : nullptr; });
+    plain |= load_tile(Vs, [&](int r) { return j0 + r < k1 ? vp + (int64_t)(j0 + r) * a.vs.t : nullptr; });
+    plain = __syncthreads_or(plain || q_plain);
     float p[8][4];
-    rows_product<4>(p, q, Ks, 0, gid, tig);
-    rows_product<4>(p + 4, q, Ks, 4, gid, tig);
+    if (plain) {
+      rows_plain<8>(p, query_dim, Ks, 0, tig);
+    } else {
+      rows_product<4>(p, q, Ks, 0, gid, tig);
+      rows_product<4>(p + 4, q, Ks, 4, gid, tig);
+    }
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int n = 0; n < 8; ++n)
@@ -213,7 +260,10 @@ __global__ void __launch_bounds__(kThreads32) cross_fwd_kernel(const CrossArgs a
         p[n][e] = exp2f(p[n][e] - sh[e >> 1]);
         l[e >> 1] += p[n][e];
       }
-      dims_product(o, p[n], Vs, n, gid, tig);
+      if (plain)
+        dims_plain(o, p[n], Vs, n, gid, tig);
+      else
+        dims_product(o, p[n], Vs, n, gid, tig);
     }
   }
 #pragma unroll
@@ -260,20 +310,31 @@ __global__ void __launch_bounds__(kThreads32) cross_dq_kernel(const CrossArgs a)
   int k0, k1;
   split_keys(nk, kTileN, a.splits, s, k0, k1);
   if (r0 >= (int64_t)nq * a.G) k1 = k0;
+  auto query = [&](int h) {
+    const int r = r0 + 16 * warp + gid + 8 * h, t = r / a.G, head = kvh * a.G + (r - t * a.G);
+    return r < rows && t < nq ? static_cast<const float*>(a.q) + b * a.qs.b + head * a.qs.h + t * a.qs.t : nullptr;
+  };
+  auto grad = [&](int h) {
+    const int r = r0 + 16 * warp + gid + 8 * h;
+    return r < rows && r / a.G < nq ? static_cast<const float*>(a.dO) + a.row(b, kvh, r) * kD : nullptr;
+  };
+  auto query_dim = [&](int h, int d) {
+    const float* const row = query(h);
+    return row ? row[d] : 0.0f;
+  };
+  auto grad_dim = [&](int h, int d) {
+    const float* const row = grad(h);
+    return row ? row[d] : 0.0f;
+  };
   Left q, g;
+  q.load(query(0), query(1), tig);
+  g.load(grad(0), grad(1), tig);
+  const bool q_plain = q.plain() || g.plain();
   float2 st[2];
-  {
-    const float *row[2], *grad[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = r0 + 16 * warp + gid + 8 * h, t = r / a.G, head = kvh * a.G + (r - t * a.G);
-      const bool in = r < rows && t < nq;
-      row[h] = in ? static_cast<const float*>(a.q) + b * a.qs.b + head * a.qs.h + t * a.qs.t : nullptr;
-      grad[h] = in ? static_cast<const float*>(a.dO) + a.row(b, kvh, r) * kD : nullptr;
-      st[h] = r < rows ? a.stat[a.row(b, kvh, r)] : make_float2(INFINITY, 0.0f);
-    }
-    q.load(row[0], row[1], tig);
-    g.load(grad[0], grad[1], tig);
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + 16 * warp + gid + 8 * h;
+    st[h] = r < rows ? a.stat[a.row(b, kvh, r)] : make_float2(INFINITY, 0.0f);
   }
   const float* const kp = static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h;
   const float* const vp = static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h;
@@ -284,14 +345,19 @@ __global__ void __launch_bounds__(kThreads32) cross_dq_kernel(const CrossArgs a)
     for (int e = 0; e < 4; ++e) dq[j][e] = 0.0f;
   for (int j0 = k0; j0 < k1; j0 += kTileN) {
     __syncthreads();
-    load_tile(Ks, [&](int r) { return j0 + r < k1 ? kp + (int64_t)(j0 + r) * a.ks.t : nullptr; });
-    load_tile(Vs, [&](int r) { return j0 + r < k1 ? vp + (int64_t)(j0 + r) * a.vs.t : nullptr; });
-    __syncthreads();
+    bool plain = load_tile(Ks, [&](int r) { return j0 + r < k1 ? kp + (int64_t)(j0 + r) * a.ks.t : nullptr; });
+    plain |= load_tile(Vs, [&](int r) { return j0 + r < k1 ? vp + (int64_t)(j0 + r) * a.vs.t : nullptr; });
+    plain = __syncthreads_or(plain || q_plain);
 #pragma unroll 1
     for (int n = 0; n < 8; n += 2) {
       float p[2][4], dp[2][4];
-      rows_product<2>(p, q, Ks, n, gid, tig);
-      rows_product<2>(dp, g, Vs, n, gid, tig);
+      if (plain) {
+        rows_plain<2>(p, query_dim, Ks, n, tig);
+        rows_plain<2>(dp, grad_dim, Vs, n, tig);
+      } else {
+        rows_product<2>(p, q, Ks, n, gid, tig);
+        rows_product<2>(dp, g, Vs, n, gid, tig);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -299,7 +365,10 @@ __global__ void __launch_bounds__(kThreads32) cross_dq_kernel(const CrossArgs a)
           const bool there = j0 + 8 * (n + i) + 2 * tig + (e & 1) < k1 && st[e >> 1].x != INFINITY;
           p[i][e] = there ? exp2f(fmaf(p[i][e], kLogitScale, -st[e >> 1].x)) * (dp[i][e] - st[e >> 1].y) : 0.0f;
         }
-        dims_product(dq, p[i], Ks, n + i, gid, tig);
+        if (plain)
+          dims_plain(dq, p[i], Ks, n + i, gid, tig);
+        else
+          dims_product(dq, p[i], Ks, n + i, gid, tig);
       }
     }
   }
@@ -337,10 +406,13 @@ __global__ void __launch_bounds__(kThreads32, 3) cross_dkv_kernel(const CrossArg
   split_keys(j0 < nk ? rows : 0, kTileN, a.splits, s, b0, b1);
   const float* const kp = static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h;
   const float* const vp = static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h;
+  bool k_plain = false;
   if (b0 < b1) {
-    load_tile(Ks, [&](int r) { return j0 + r < nk ? kp + (int64_t)(j0 + r) * a.ks.t : nullptr; });
-    load_tile(Vs, [&](int r) { return j0 + r < nk ? vp + (int64_t)(j0 + r) * a.vs.t : nullptr; });
+    k_plain |= load_tile(Ks, [&](int r) { return j0 + r < nk ? kp + (int64_t)(j0 + r) * a.ks.t : nullptr; });
+    k_plain |= load_tile(Vs, [&](int r) { return j0 + r < nk ? vp + (int64_t)(j0 + r) * a.vs.t : nullptr; });
   }
+  auto key_dim = [&](int h, int d) { return Ks[(16 * warp + gid + 8 * h) * kPitch + d]; };
+  auto value_dim = [&](int h, int d) { return Vs[(16 * warp + gid + 8 * h) * kPitch + d]; };
   const LeftTile k(Ks, 16 * warp, gid, tig), v(Vs, 16 * warp, gid, tig);
   float dk[8][4], dv[8][4];
 #pragma unroll
@@ -353,18 +425,23 @@ __global__ void __launch_bounds__(kThreads32, 3) cross_dkv_kernel(const CrossArg
       const int r = r0 + i, t = r / a.G, head = kvh * a.G + (r - t * a.G);
       return r < b1 ? static_cast<const float*>(a.q) + b * a.qs.b + head * a.qs.h + t * a.qs.t : nullptr;
     };
-    load_tile(Qs, query);
-    load_tile(Ds, [&](int i) { return r0 + i < b1 ? static_cast<const float*>(a.dO) + a.row(b, kvh, r0 + i) * kD : nullptr; });
+    bool plain = load_tile(Qs, query);
+    plain |= load_tile(Ds, [&](int i) { return r0 + i < b1 ? static_cast<const float*>(a.dO) + a.row(b, kvh, r0 + i) * kD : nullptr; });
     if (threadIdx.x < kTileN) {
       const int r = r0 + threadIdx.x;
       stat[threadIdx.x] = r < b1 ? a.stat[a.row(b, kvh, r)] : make_float2(INFINITY, 0.0f);
     }
-    __syncthreads();
+    plain = __syncthreads_or(plain || k_plain);
 #pragma unroll 1
     for (int n = 0; n < 8; n += 2) {
       float p[2][4], dp[2][4];  // [key][row]
-      rows_product<2>(p, k, Qs, n, gid, tig);
-      rows_product<2>(dp, v, Ds, n, gid, tig);
+      if (plain) {
+        rows_plain<2>(p, key_dim, Qs, n, tig);
+        rows_plain<2>(dp, value_dim, Ds, n, tig);
+      } else {
+        rows_product<2>(p, k, Qs, n, gid, tig);
+        rows_product<2>(dp, v, Ds, n, gid, tig);
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -373,8 +450,13 @@ __global__ void __launch_bounds__(kThreads32, 3) cross_dkv_kernel(const CrossArg
           p[i][e] = st.x != INFINITY ? exp2f(fmaf(p[i][e], kLogitScale, -st.x)) : 0.0f;
           dp[i][e] = st.x != INFINITY ? p[i][e] * (dp[i][e] - st.y) : 0.0f;
         }
-        dims_product(dv, p[i], Ds, n + i, gid, tig);
-        dims_product(dk, dp[i], Qs, n + i, gid, tig);
+        if (plain) {
+          dims_plain(dv, p[i], Ds, n + i, gid, tig);
+          dims_plain(dk, dp[i], Qs, n + i, gid, tig);
+        } else {
+          dims_product(dv, p[i], Ds, n + i, gid, tig);
+          dims_product(dk, dp[i], Qs, n + i, gid, tig);
+        }
       }
     }
   }

@@ -214,17 +214,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int T = warp >> 2, r = tid & 127;
     const uint32_t tl = tm + kTcTileCols * T + ((uint32_t)(warp & 3) << 21);  // this warp's lanes
     // rows of tiles without work: zeros (parts have no such rows)
-    if (!a.parts)
-      for (int64_t x = blockIdx.x; x < (int64_t)a.B * a.Hkv * w.rt.tiles; x += gridDim.x) {
-        const int bh = (int)(x / w.rt.tiles), tile = (int)(x - (int64_t)bh * w.rt.tiles), b = bh / a.Hkv;
-        if (tile < (a.keys(b) > 0 ? (w.rt.used(a.queries(b)) + 1) & ~1 : 0)) continue;
-        const RowOf ro = row_of(a, w.rt, tile, r);
-        if (!ro.mine) continue;
-        const int64_t row = a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g);
+    if (!a.parts && (a.q_len || a.kv_len))
+      each_empty(
+          (int64_t)a.B * a.Hkv * w.rt.tiles, lane,
+          [&](int64_t x) {
+            const int bh = (int)(x / w.rt.tiles), b = bh / a.Hkv;
+            return x - (int64_t)bh * w.rt.tiles >= (a.keys(b) > 0 ? (w.rt.used(a.queries(b)) + 1) & ~1 : 0);
+          },
+          [&](int64_t x) {
+            const int bh = (int)(x / w.rt.tiles), b = bh / a.Hkv;
+            const RowOf ro = row_of(a, w.rt, (int)(x - (int64_t)bh * w.rt.tiles), r);
+            if (!ro.mine) return;
+            const int64_t row = a.row(b, bh - b * a.Hkv, ro.t * a.G + ro.g);
 #pragma unroll
-        for (int c = 32 * T; c < 32 * T + 32; c += 8) *reinterpret_cast<uint4*>(static_cast<bf16*>(a.o) + row * kD + c) = make_uint4(0, 0, 0, 0);
-        if (a.lse && T == 0) a.lse[row] = -INFINITY;
-      }
+            for (int c = 32 * T; c < 32 * T + 32; c += 8) *reinterpret_cast<uint4*>(static_cast<bf16*>(a.o) + row * kD + c) = make_uint4(0, 0, 0, 0);
+            if (a.lse && T == 0) a.lse[row] = -INFINITY;
+          });
     int np = 0;  // steps of this tile
     for (;;) {
       int steps, keys;
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int slot = n % Shape::kSlots;
             if (n >= Shape::kSlots) wait(&sh.empty[slot], n / Shape::kSlots - 1);
             if (dead) break;
-            if (elect_one()) {
+            if (elect_one() && (n != a.debug_skip || blockIdx.x > 0)) {
               const uint32_t bar = smem_u32(&sh.full[slot]);
               mbar_expect_tx(bar, kKeyTile);
               tma_load_4d(ring + slot * kKeyTile, kv ? &vm : &km, 0, j, p.kvh, p.b, bar);
@@ -390,12 +395,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++n;
           }
       }
-      if (dead) {  // copies under way end before their memory goes
+      if (dead) {  // copies under way end before their memory goes (whatever the limit of the others)
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
         for (int i = max(0, n - Shape::kSlots); i < n; ++i)
-          mbar_wait_bounded(smem_u32(&sh.full[i % Shape::kSlots]), (i / Shape::kSlots) & 1, a.wait_cycles);
+          mbar_wait_bounded(smem_u32(&sh.full[i % Shape::kSlots]), (i / Shape::kSlots) & 1, kDefaultWaitCycles);
         for (int i = max(0, nq - Shape::kQBufs); i < nq; ++i)
-          mbar_wait_bounded(smem_u32(&sh.q_full[i % Shape::kQBufs]), (i / Shape::kQBufs) & 1, a.wait_cycles);
+          mbar_wait_bounded(smem_u32(&sh.q_full[i % Shape::kQBufs]), (i / Shape::kQBufs) & 1, kDefaultWaitCycles);
       }
     } else if (warp < 11) {
       // ---- products of tile T: a step's logits are issued before the last step's
@@ -471,8 +476,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (dead) {  // products under way end before their memory goes
         if (lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
         for (int i = max(0, ns - 1); i <= ns; ++i) {
-          mbar_wait_bounded(smem_u32(&sh.s_full[T][i & 1]), (i >> 1) & 1, a.wait_cycles);
-          if (i > 0) mbar_wait_bounded(smem_u32(&sh.pv_done[T][(i - 1) & 1]), ((i - 1) >> 1) & 1, a.wait_cycles);
+          mbar_wait_bounded(smem_u32(&sh.s_full[T][i & 1]), (i >> 1) & 1, kDefaultWaitCycles);
+          if (i > 0) mbar_wait_bounded(smem_u32(&sh.pv_done[T][(i - 1) & 1]), ((i - 1) >> 1) & 1, kDefaultWaitCycles);
         }
       }
     } else {

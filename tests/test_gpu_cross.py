@@ -1,5 +1,6 @@
 """Attention to states of another length, its gradients, and decode steps behind a shared prefix, against the
 64-bit definitions of cross_ref.py."""
+import ctypes
 import math
 
 import pytest
@@ -379,3 +380,229 @@ def test_prefix_python_refusals(sfa):
             sfa.prefix_decode(**{**good, **kw})
     with pytest.raises(sfa.SfaError):
         sfa.prefix_decode(**good, rope=sfa.rope_table(P + T - 1))
+
+
+# ------------------------------------------------------------------ where it can go wrong
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", [(1, 900), (5, 900), (130, 900)])
+def test_logits_that_rise_along_the_keys(sfa, Tq, Tk, dtype):
+    """Each key's logits are far above the ones before it, in steps and by single keys: sums are moved many times."""
+    q, k, v, do = _inputs(20, 1, Tq, Tk, 4, 2, dtype)
+    q = q.abs()
+    rise = torch.arange(Tk, dtype=torch.float32)[:, None] // 50 * 0.7 + (torch.arange(Tk)[:, None] == 600) * 40.0
+    k = (k.abs() * 0.3 + rise).to(dtype)
+    _check_forward(sfa, q, k, v, None, None)
+    _check_backward(sfa, q, k, v, do, None, None)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq", [1, 5, 70])
+@pytest.mark.parametrize("dead", [10, 96, 300])
+def test_keys_of_minus_infinity(sfa, Tq, dead, dtype):
+    """The first keys' logits are -inf: as if they were not there; all of them: NaN, as a softmax has it."""
+    q, k, v, _ = _inputs(21, 1, Tq, 333, 4, 2, dtype)
+    q = q.abs() + 0.1
+    k[:, :, :dead] = -INF
+    k[:, :, dead:] -= 40  # logits of -100 and less: nothing of them may be lost against the dead ones
+    o, lse = _forward(sfa, q, k, v, None, None)
+    wo, wl, bo, bl = ref.forward(q, k[:, :, dead:], v[:, :, dead:])
+    ref.check("o", o, wo, bo)
+    ref.check("lse", lse, wl, bl)
+    o, lse = _forward(sfa, q, torch.full_like(k, -INF), v, None, None)
+    assert bool(o.isnan().all()) and not bool(lse.isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq", [1, 5, 140])
+def test_huge_numbers(sfa, Tq, dtype):
+    """2^100 in a dim of the queries where keys are zero, and in one of the values where gradients are."""
+    q, k, v, do = _inputs(22, 1, Tq, 333, 4, 2, dtype)
+    q[..., 0], k[..., 0] = 2.0 ** 100, 0.0
+    v[..., 3], do[..., 3] = v[..., 3] * 2.0 ** 100, 0.0
+    _check_forward(sfa, q, k, v, None, None)
+    _check_backward(sfa, q, k, v, do, None, None)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv", [(3, 50, 4, 2), (40, 150, 4, 1), (1, 200, 3, 1)])
+def test_many_ragged_sequences(sfa, Tq, Tk, Hq, Hkv, dtype):
+    """More sequences than SMs, lengths from none to all."""
+    B = 413
+    q, k, v, do = _inputs(22, B, Tq, Tk, Hq, Hkv, dtype)
+    gen = torch.Generator().manual_seed(23)
+    nq, nk = (torch.randint(0, n + 1, (B,), generator=gen).tolist() for n in (Tq, Tk))
+    _check_forward(sfa, _spoil(q, nq), _spoil(k, nk), _spoil(v, nk), nq, nk)
+    _check_backward(sfa, _spoil(q, nq), _spoil(k, nk), _spoil(v, nk), do, nq, nk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_one_long_sequence_among_empty_ones(sfa, dtype):
+    B, Tq, Tk = 9, 200, 5000
+    q, k, v, do = _inputs(24, B, Tq, Tk, 2, 1, dtype)
+    nq, nk = [0, 0, 5, 0, 200, 0, 0, 200, 0], [5000, 0, 0, 3, 4999, 0, 1, 0, 9]
+    _check_forward(sfa, q, k, v, nq, nk)
+    _check_backward(sfa, q, k, v, do, nq, nk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq", [1, 40])
+def test_offsets_past_32_bits(sfa, Tq, dtype):
+    """Keys and values whose sequences, heads and rows lie more than 2^31 numbers apart."""
+    B, Tk, Hkv = 2, 130, 2
+    q, k, v, do = _inputs(25, B, Tq, Tk, 4, Hkv, dtype)
+    want = sfa.cross_forward(q.cuda(), k.cuda(), v.cuda())
+    grads = sfa.cross_backward(q.cuda(), k.cuda(), v.cuda(), *want, do.cuda())
+    n = (1 << 31) + 64 * 1024
+    buf = torch.empty(n + 64 * 1024 * 64, dtype=dtype, device="cuda")
+    for strides in ((n, 64 * Tk, 64), (64 * Tk, n, 64), (64 * Hkv * 8, 64 * 8, (1 << 31) // (Tk - 1) // 64 * 64 + 64 * 32)):
+        assert sum((m - 1) * s for m, s in zip((B, Hkv, Tk), strides)) + 64 <= buf.numel()
+        views = []
+        for x in (k, v):
+            view = torch.as_strided(buf, (B, Hkv, Tk, 64), (*strides, 1))
+            view.copy_(x)
+            got = (view, v.cuda()) if x is k else (k.cuda(), view)
+            o, lse = sfa.cross_forward(q.cuda(), *got)
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+            assert all(torch.equal(a, b) for a, b in zip(sfa.cross_backward(q.cuda(), *got, o, lse, do.cuda()), grads))
+            views.append(view)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", [(1, 700), (3, 65), (100, 300), (257, 1)])
+def test_nothing_is_written_beside_the_outputs(sfa, Tq, Tk, dtype):
+    q, k, v, do = (x.cuda() for x in _inputs(26, 2, Tq, Tk, 6, 2, dtype))
+    nk = _i32([Tk, max(1, Tk // 2)])
+
+    def guarded(shape, dt):
+        n = math.prod(shape)
+        whole = torch.full((n + 512,), 3.0, dtype=dt, device="cuda")
+        return whole, whole[256:256 + n].view(shape)
+
+    held = [guarded(q.shape, dtype), guarded(q.shape[:3], torch.float32), guarded(q.shape, dtype), guarded(k.shape, dtype), guarded(k.shape, dtype)]
+    o, lse, dq, dk, dv = (x for _, x in held)
+    sfa.cross_forward(q, k, v, kv_len=nk, o=o, lse=lse)
+    sfa.cross_backward(q, k, v, o, lse, do, kv_len=nk, dq=dq, dk=dk, dv=dv)
+    plain = sfa.cross_forward(q, k, v, kv_len=nk)
+    for a, b in zip((o, lse, dq, dk, dv), (*plain, *sfa.cross_backward(q, k, v, *plain, do, kv_len=nk))):
+        assert torch.equal(a, b)  # (the calls with outputs of the caller go the ctypes way, the others the native one)
+    for whole, _ in held:
+        assert bool((whole[:256] == 3).all()) and bool((whole[-256:] == 3).all())
+
+
+def test_broadcast_keys_are_refused(sfa):
+    """One source for a batch is expanded by the caller's copy (its gradient is a sum the caller takes)."""
+    q, k = torch.zeros(3, 2, 4, 64, device="cuda"), torch.zeros(1, 2, 9, 64, device="cuda")
+    with pytest.raises(ValueError):
+        sfa.cross_forward(q, k.expand(3, 2, 9, 64), k.expand(3, 2, 9, 64))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_calls_at_once_on_two_streams(sfa, dtype):
+    """Two streams' calls overlap: each has a workspace of its own."""
+    q, k, v, do = (x.cuda() for x in _inputs(27, 1, 300, 4000, 8, 2, dtype))
+    q2, k2, v2, do2 = (x.cuda() for x in _inputs(28, 2, 1, 7000, 8, 2, dtype))
+    o, lse = sfa.cross_forward(q, k, v)
+    o2, lse2 = sfa.cross_forward(q2, k2, v2)
+    want, want2 = sfa.cross_backward(q, k, v, o, lse, do), sfa.cross_backward(q2, k2, v2, o2, lse2, do2)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, got2 = [], []
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            got.append((*sfa.cross_forward(q, k, v), *sfa.cross_backward(q, k, v, o, lse, do)))
+        with torch.cuda.stream(b):
+            got2.append((*sfa.cross_forward(q2, k2, v2), *sfa.cross_backward(q2, k2, v2, o2, lse2, do2)))
+    torch.cuda.synchronize()
+    for x in got:
+        assert all(torch.equal(s, t) for s, t in zip(x, (o, lse, *want)))
+    for x in got2:
+        assert all(torch.equal(s, t) for s, t in zip(x, (o2, lse2, *want2)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_prefix_both_ways_and_again(sfa, dtype):
+    """The native call, the ctypes call (outputs of the caller), a second one: the same bits, caches as after one."""
+    B, P, T, Hq, Hkv = 37, 1500, 90, 8, 2
+    qkv, pk, pv, kc, vc = (x.cuda() for x in _prefix_inputs(30, B, P, T, Hq, Hkv, dtype))
+    pos = [(11 * i) % T for i in range(B)]
+    sfa.rope_table(P + T)
+    o, lse = _step(sfa, qkv, pk, pv, kc, vc, pos, Hq)
+    after = kc.clone(), vc.clone()
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    _step(sfa, qkv, pk, pv, kc, vc, pos, Hq, o=o2, lse=lse2)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(kc, after[0]) and torch.equal(vc, after[1])
+
+
+def test_a_training_step_and_steps_after_it(sfa):
+    """An encoder with a signed set, a decoder's cross attention over it trained by one gradient step against
+    differences, then single tokens over the same states: each as a program would call it."""
+    gen = torch.Generator().manual_seed(31)
+    normal = lambda *s: torch.randn(s, generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    B, Tk, Tq = 2, 128, 48
+    x, kv, v0 = normal(B, 4, Tk, 64), normal(B, 2, Tk, 64), normal(B, 2, Tk, 64)
+    states, _ = sfa.forward_int(x, kv, v0, dist=[-3, -2, -1, 0, 1, 2, 3])
+    k = states[:, :2].float().mul(2).bfloat16()
+    v = states[:, 2:].contiguous()
+    q, do = normal(B, 8, Tq, 64), normal(B, 8, Tq, 64)
+    lens = _i32([Tk, 77])
+    o, lse = sfa.cross_forward(q, k, v, kv_len=lens)
+    dq, dk, dv = sfa.cross_backward(q, k, v, o, lse, do, kv_len=lens)
+    # the change of sum(o dO) along a direction against the gradients' product with it, in 64 bits; the quotient's
+    # own error is h^2 times a third derivative (h = 2^-8: below 1e-3 of it), the gradients' 2^-7 of their terms
+    u = [torch.randn(t.shape, generator=gen).double() for t in (q, k, v)]
+    h = 2.0 ** -8
+
+    def value(sign):
+        moved = [t.cpu().double() + sign * h * w for t, w in zip((q, k, v), u)]
+        return float((ref.forward(*moved, None, [Tk, 77])[0] * do.cpu().double()).sum())
+
+    slope = (value(1) - value(-1)) / (2 * h)
+    terms = [(g.cpu().double() * w) for g, w in zip((dq, dk, dv), u)]
+    scale = math.sqrt(sum(float((t * t).sum()) for t in terms))
+    assert abs(slope - sum(float(t.sum()) for t in terms)) <= 2.0 ** -7 * scale * 4 + 1e-3 * abs(slope)
+    for t in range(3):
+        one, one_lse = sfa.cross_forward(q[:, :, t:t + 1], k, v, kv_len=lens)
+        # another order of sums, probabilities and outputs rounded to bf16 in both
+        wo, wl, bo, bl = ref.forward(q[:, :, t:t + 1].cpu(), k.cpu(), v.cpu(), None, [Tk, 77])
+        ref.check("o", one, wo, bo)
+        assert float((one.float() - o[:, :, t:t + 1].float()).abs().max()) <= 2 * float(bo.max())
+        assert float((one_lse - lse[:, :, t:t + 1]).abs().max()) <= 2 * float(bl.max())
+
+
+# bf16 on the tensor cores: CTA 0 leaves out a tile of keys or values (forward), a step (backward)
+@pytest.mark.parametrize("call,skip", [("forward", 0), ("forward", 5), ("backward", 0), ("backward", 3), ("prefix", 2)])
+def test_cross_wait_times_out_and_context_recovers(sfa, sfa_lib, call, skip):
+    gen = torch.Generator().manual_seed(516)
+    q, k, v, do = (torch.randn(1, h, t, 64, generator=gen).bfloat16() for h, t in ((4, 600), (2, 800), (2, 800), (4, 600)))
+    dev = [x.cuda() for x in (q, k, v)]
+    o, lse = sfa.cross_forward(*dev)
+    rows = torch.randn(40, 8, 64, generator=gen).bfloat16().cuda()
+    cache = torch.randn(2, 40, 2, 30, 64, generator=gen).bfloat16().cuda()
+    pos = torch.arange(40, dtype=torch.int32, device="cuda") % 30
+
+    def run():
+        if call == "forward":
+            return sfa.cross_forward(*dev)
+        if call == "backward":
+            return sfa.cross_backward(*dev, o, lse, do.cuda())
+        return sfa.prefix_decode(rows[:, :4], rows[:, 4:6], rows[:, 6:], dev[1][0], dev[2][0], cache[0], cache[1], pos)
+
+    want = [x.clone() for x in run()]
+    torch.cuda.synchronize()
+    assert sfa.get_device_status() == 0
+    try:
+        assert sfa_lib.sfa_debug_inject(ctypes.c_int64(2000000), ctypes.c_int32(skip)) == 0  # about 1 ms
+        run()
+        torch.cuda.synchronize()
+    finally:
+        assert sfa_lib.sfa_debug_inject(ctypes.c_int64(0), ctypes.c_int32(-1)) == 0
+    assert sfa.get_device_status() == 5  # SFA_ERR_TIMEOUT
+    assert sfa.get_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, run()))
+    assert sfa.get_device_status() == 0
+    if call == "forward":
+        wo, wl, bo, bl = ref.forward(q, k, v)
+        ref.check("o", want[0], wo, bo)
+        ref.check("lse", want[1], wl, bl)
