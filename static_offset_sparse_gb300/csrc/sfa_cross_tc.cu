@@ -233,11 +233,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int np = 0;  // steps of this tile
     for (;;) {
       int steps, keys;
+      bool none;  // the row counts for nothing: whatever its sums become, no step is taken again for it
       {
         TcPiece p;
         if (!take(p)) break;
         steps = T == 0 || p.two ? p.steps : 0;
         keys = p.k1 - p.k0;
+        none = sh.rows[pieces % kPlans][tid] < 0;
       }
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < steps; ++j, ++np) {
@@ -246,22 +248,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc05_fence_after();
         const uint32_t ts = tl + kKeys * (np & 1);
         const int left = keys - kKeys * j;
-        float sum = INFINITY;
+        float sum = 0.0f;
+        bool again = true;  // of all lanes or none
         {
           float v[kKeys];
           row_logits(ts, left, v);
           if (j == 0) m = row_top(v);
-          if (__all_sync(0xffffffffu, fabsf(m) <= kFar)) {
+          if (__all_sync(0xffffffffu, none || fabsf(m) <= kFar)) {
             sum = row_exp(v, m * kLogitScale);
-            if (__all_sync(0xffffffffu, sum <= kSumLimit)) {
+            again = !__all_sync(0xffffffffu, none || sum <= kSumLimit);
+            if (!again)
 #pragma unroll
               for (int c = 0; c < kKeys / 2; c += 16) tmem_st16(ts + c, v + c);
-            } else {
-              sum = INFINITY;
-            }
           }
         }
-        if (__any_sync(0xffffffffu, sum == INFINITY)) {  // (of all lanes or none)
+        if (again) {
           float top = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < kKeys; c += 8) {
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float mc = shift_of(m) * kLogitScale;
       if (dead) break;
       const int plan = pieces % kPlans, code = sh.rows[plan][tid], place = sh.plan[plan].place;
-      const bool mine = code != INT_MIN, none = code < 0, whole = place < 0;
+      const bool mine = code != INT_MIN, whole = place < 0;
       const int row = none ? ~code : code;
       // parts: (o, m, l) as they are; else o / l.  Through shared memory, so that eight
       // lanes write a row's 128 bytes together.  (Loops: this code runs once a piece, and
