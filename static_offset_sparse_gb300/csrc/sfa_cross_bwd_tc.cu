@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         const uint32_t at = smem + kBtStatStays + buf * kBtStat + 4 * r;
         asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(own.x) : "r"(at) : "memory");
         asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(own.y) : "r"(at + 512) : "memory");
-        arrive(&sh.a_empty[buf]);
       }
       for (int j = 0; j < steps; ++j, ++n) {
         const int st = n % kBtStages;
@@ -239,6 +238,9 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         tc05_fence_before();
         arrive(&sh.p_full);
       }
+      // (Not before the last use: given back right after the reads above, the buffer was now
+      // and then filled with the piece after next's numbers before `own` had been read.)
+      if (!DKV) arrive(&sh.a_empty[pieces & 1]);
       if (!dead) {
         wait(&sh.done, n - 1);
         tc05_fence_after();

@@ -438,6 +438,23 @@ def test_many_ragged_sequences(sfa, Tq, Tk, Hq, Hkv, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv", [(100, 300, 300, 8, 2), (413, 40, 150, 4, 1)])
+def test_many_ragged_sequences_again_and_again(sfa, B, Tq, Tk, Hq, Hkv, dtype):
+    """Many short units an SM, one behind the other: every call gives the same bits."""
+    gen = torch.Generator().manual_seed(7)
+    q, k, v, do = (x.cuda() for x in _inputs(5, B, Tq, Tk, Hq, Hkv, dtype))
+    nq, nk = (_i32(torch.randint(0, n + 1, (B,), generator=gen).tolist()) for n in (Tq, Tk))
+    first = sfa.cross_forward(q, k, v, q_len=nq, kv_len=nk)
+    grads = sfa.cross_backward(q, k, v, *first, do, q_len=nq, kv_len=nk)
+    for _ in range(60):
+        again = sfa.cross_forward(q, k, v, q_len=nq, kv_len=nk)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+        again = sfa.cross_backward(q, k, v, *first, do, q_len=nq, kv_len=nk)
+        assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    assert sfa.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
 def test_one_long_sequence_among_empty_ones(sfa, dtype):
     B, Tq, Tk = 9, 200, 5000
     q, k, v, do = _inputs(24, B, Tq, Tk, 2, 1, dtype)
