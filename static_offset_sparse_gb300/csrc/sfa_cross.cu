@@ -36,20 +36,23 @@ __global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, floa
   if (row < a.rows && d8 == 0) stat[row] = valid ? make_float2(a.lse[row] * kLog2e, sum) : make_float2(INFINITY, 0.0f);
 }
 
-// out = the sum of n-number parts, in order.
-__global__ void __launch_bounds__(256) cross_sum_kernel(const float* parts, int splits, int64_t n, void* out) {
+// out = the sum of n-number parts, in order; blockIdx.y = 1: the parts behind them, to out1.
+__global__ void __launch_bounds__(256) cross_sum_kernel(const float* parts, int splits, int64_t n, float* out, float* out1) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;
-  float x[8], y[8];
-  load8(parts + i, x);
-  for (int s = 1; s < splits; ++s) {
-    load8(parts + s * n + i, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += y[e];
+  parts += blockIdx.y * splits * n + i;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float4 y = *reinterpret_cast<const float4*>(parts + s * n);
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
   }
-  store8(static_cast<float*>(out) + i, x);
+  *reinterpret_cast<float4*>((blockIdx.y ? out1 : out) + i) = x;
 }
 
 struct PrefixArgs {
@@ -113,14 +116,31 @@ __global__ void __launch_bounds__(128) prefix_prep_kernel(const PrefixArgs a) {
 
 // ---- which kernels a call runs
 
+// Few rows go to the kernels that stream keys.  bf16: as many as one CTA of them takes (16).
+// fp32: up to four CTAs' of 8, each of which reads the keys (from L2), because the other kernel
+// has tiles of 64 rows, however few there are (8 x 8 / 2 heads, 8 queries over 2000: 30.4 us in
+// a tile, 24.8 so; with 64 rows both take the same).
 enum Kind { kFewRows, kTensor, kFp32 };
 static int stream_rows(int dtype) { return dtype == SFA_BF16 ? kStreamRowsBf16 : kStreamRows; }
-static Kind forward_kind(int rows, int dtype) { return rows <= stream_rows(dtype) ? kFewRows : dtype == SFA_BF16 ? kTensor : kFp32; }
+static Kind forward_kind(int rows, int dtype) {
+  if (dtype == SFA_BF16) return rows <= kStreamRowsBf16 ? kFewRows : kTensor;
+  return rows <= 4 * kStreamRows ? kFewRows : kFp32;
+}
 
-// Parts of a call over `units` (sequence, KV head) pairs of Tq queries of G heads (not the tensor cores').
-static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind) {
-  if (kind == kFewRows) return wave_splits(units, 4 * kSMs, Tk, 256);
-  return wave_splits(units * ((G * Tq + kF32Tile - 1) / kF32Tile), 3 * kSMs, (Tk + kF32Tile - 1) / kF32Tile, 1);
+// Parts of a call over `units` (sequence, KV head) pairs of Tq queries of G heads (not the
+// tensor cores').  Few rows, bf16: 256 keys a part at least (with 128, 32 x 8 / 2 heads over
+// 1500 took 12.1 us, so 10.3).  fp32: a part's keys take longer and its join as long, so
+// fewer, and sqrt(Tk / 12) parts at most (8 / 2 heads over 1000: 10.0 us for 13.5; over 10000
+// 18.5 us, and 31 without the limit).
+static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind, int dtype) {
+  if (kind == kFewRows) {
+    const int64_t ctas = units * ((G * Tq + stream_rows(dtype) - 1) / stream_rows(dtype));
+    int s = wave_splits(ctas, 4 * kSMs, Tk, dtype == SFA_BF16 ? 256 : 64);
+    if (dtype == SFA_F32)
+      while (s > 1 && 12 * s * s > Tk) --s;
+    return s;
+  }
+  return wave_splits(units * ((G * Tq + kF32Tile - 1) / kF32Tile), 3 * kSMs, (Tk + kF32Keys - 1) / kF32Keys, 1);
 }
 
 static size_t part_bytes(int splits, int64_t rows) {
@@ -190,7 +210,7 @@ static ForwardPlan forward_plan(const sfa_cross_desc* d) {
   if (p.kind == kTensor) {
     p.bytes = cross_tc_bytes(d->B, d->Hkv, G, d->Tq, d->Tk);
   } else {
-    p.splits = forward_splits((int64_t)d->B * d->Hkv, G, d->Tq, d->Tk, p.kind);
+    p.splits = forward_splits((int64_t)d->B * d->Hkv, G, d->Tq, d->Tk, p.kind, d->dtype);
     if (p.splits > 1) p.bytes = part_bytes(p.splits, (int64_t)d->B * d->Hq * d->Tq);
   }
   return p;
@@ -222,9 +242,12 @@ static BackwardPlan backward_plan(const sfa_cross_desc* d) {
   return p;
 }
 
-static int launch_sum(const float* parts, int splits, int64_t n, void* out, void* stream) {
+// out (and out1 where there is one) = the sums of their parts.
+static int launch_sum(const float* parts, int splits, int64_t n, void* out, void* out1, void* stream) {
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
-  const cudaError_t e = launch_pdl(cross_sum_kernel, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), 0, (cudaStream_t)stream, parts, splits, n, out);
+  const dim3 grid((unsigned)((n / 4 + 255) / 256), out1 ? 2 : 1);
+  const cudaError_t e = launch_pdl(cross_sum_kernel, grid, dim3(256), 0, (cudaStream_t)stream, parts, splits, n, static_cast<float*>(out),
+                                   static_cast<float*>(out1));
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
@@ -262,8 +285,8 @@ static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
   p.rows = (int64_t)d->B * d->Hq;
   p.kind = forward_kind(G * d->B, d->dtype);
   p.two = d->P && p.kind == kTensor;
-  p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind);
-  p.own = wave_splits((int64_t)d->B * d->Hkv * ((G + stream_rows(d->dtype) - 1) / stream_rows(d->dtype)), 4 * kSMs, d->T, 256);
+  p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind, d->dtype);
+  p.own = forward_splits((int64_t)d->B * d->Hkv, G, 1, d->T, kFewRows, d->dtype);
   p.q32 = align256((size_t)p.rows * kD * sizeof(float));
   p.q16 = p.two ? align256((size_t)p.rows * kD * 2 * sizeof(bf16)) : 0;
   p.parts = part_bytes(p.shared + p.own, p.rows);
@@ -347,13 +370,12 @@ int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, co
   a.parts = a.splits > 1;
   a.part_a = parts;
   if ((rc = launch_cross_dq_f32(a, stream)) != SFA_OK) return rc;
-  if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, stream)) != SFA_OK) return rc;
+  if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, nullptr, stream)) != SFA_OK) return rc;
   a.splits = p.dkv_splits;
   a.parts = a.splits > 1;
   a.part_b = parts + (size_t)a.splits * p.keys * kD;
   if ((rc = launch_cross_dkv_f32(a, stream)) != SFA_OK || !a.parts) return rc;
-  if ((rc = launch_sum(a.part_a, a.splits, p.keys * kD, dk, stream)) != SFA_OK) return rc;
-  return launch_sum(a.part_b, a.splits, p.keys * kD, dv, stream);
+  return launch_sum(a.part_a, a.splits, p.keys * kD, dk, dv, stream);
 }
 
 int sfa_prefix_workspace_size(const sfa_prefix_desc* d, size_t* bytes) {

@@ -442,8 +442,9 @@ int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream);
 // Backward pass, fp32.
 int launch_cross_dq_f32(const CrossArgs& a, void* stream);
 int launch_cross_dkv_f32(const CrossArgs& a, void* stream);
-constexpr int kStreamRows = 8, kStreamRowsBf16 = 16;  // rows that the kernels for few rows take at once
-constexpr int kF32Tile = 64;   // rows and keys of the fp32 kernels' tiles
+constexpr int kStreamRows = 8, kStreamRowsBf16 = 16;  // rows that a CTA of the kernels for few rows takes
+constexpr int kF32Tile = 64;  // rows and keys of the fp32 kernels' tiles
+constexpr int kF32Keys = 32;  // keys the fp32 forward kernel takes at a time
 
 // Splits of `units` units of work a CTA where there are `ctas` CTAs and room for
 // `slots`: one wave of them, `least` units each.

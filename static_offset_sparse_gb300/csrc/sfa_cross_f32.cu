@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads32) cross_fwd_kernel(const CrossArgs a
   const int kvh = x % a.Hkv, b = x / a.Hkv;
   const int nq = a.queries(b), nk = a.keys(b);
   int k0, k1;
-  split_keys(nk, kTileN, a.splits, s, k0, k1);
+  split_keys(nk, kF32Keys, a.splits, s, k0, k1);
   if (r0 >= (int64_t)nq * a.G) k1 = k0;  // no query in the tile
   auto query = [&](int h) {
     const int r = r0 + 16 * warp + gid + 8 * h, t = r / a.G, head = kvh * a.G + (r - t * a.G);
@@ -222,48 +222,51 @@ __global__ void __launch_bounds__(kThreads32) cross_fwd_kernel(const CrossArgs a
     bool plain = load_tile(Ks, [&](int r) { return j0 + r < k1 ? kp + (int64_t)(j0 + r) * a.ks.t : nullptr; });
     plain |= load_tile(Vs, [&](int r) { return j0 + r < k1 ? vp + (int64_t)(j0 + r) * a.vs.t : nullptr; });
     plain = __syncthreads_or(plain || q_plain);
-    float p[8][4];
-    if (plain) {
-      rows_plain<8>(p, query_dim, Ks, 0, tig);
-    } else {
-      rows_product<4>(p, q, Ks, 0, gid, tig);
-      rows_product<4>(p + 4, q, Ks, 4, gid, tig);
-    }
-    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[n][e] = j0 + 8 * n + 2 * tig + (e & 1) < k1 ? p[n][e] * kLogitScale : -INFINITY;
-        top[e >> 1] = fmaxf(top[e >> 1], p[n][e]);
-      }
-    float sh[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-      const float to = fmaxf(m[h], top[h]);
-      sh[h] = shift_of(to);
-      const float corr = exp2f(m[h] - sh[h]);  // 0 on the first keys
-      m[h] = to;
-      l[h] *= corr;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        o[j][2 * h] *= corr;
-        o[j][2 * h + 1] *= corr;
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[n][e] = exp2f(p[n][e] - sh[e >> 1]);
-        l[e >> 1] += p[n][e];
-      }
+    // 32 keys at a time, in a loop: where there are few tiles, fetching this code costs as
+    // much as running it
+#pragma unroll 1
+    for (int n0 = 0; n0 < kTileN / 8 && j0 + 8 * n0 < k1; n0 += kF32Keys / 8) {
+      float p[4][4];
       if (plain)
-        dims_plain(o, p[n], Vs, n, gid, tig);
+        rows_plain<4>(p, query_dim, Ks, n0, tig);
       else
-        dims_product(o, p[n], Vs, n, gid, tig);
+        rows_product<4>(p, q, Ks, n0, gid, tig);
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[n][e] = j0 + 8 * (n0 + n) + 2 * tig + (e & 1) < k1 ? p[n][e] * kLogitScale : -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], p[n][e]);
+        }
+      float sh[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+        const float to = fmaxf(m[h], top[h]);
+        sh[h] = shift_of(to);
+        const float corr = exp2f(m[h] - sh[h]);  // 0 on the first keys
+        m[h] = to;
+        l[h] *= corr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j][2 * h] *= corr;
+          o[j][2 * h + 1] *= corr;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[n][e] = exp2f(p[n][e] - sh[e >> 1]);
+          l[e >> 1] += p[n][e];
+        }
+        if (plain)
+          dims_plain(o, p[n], Vs, n0 + n, gid, tig);
+        else
+          dims_product(o, p[n], Vs, n0 + n, gid, tig);
+      }
     }
   }
 #pragma unroll
