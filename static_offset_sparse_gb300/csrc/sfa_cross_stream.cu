@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const C
 
 // Parts of each row to o and lse, a warp a row.  pos (of sequences whose rows
 // are queries' heads, Tq = 1): a position outside [0, T) leaves a zero row.
-template <typename TIO>
+template <int S, typename TIO>
 __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, const int32_t* pos, int T) {
   pdl_launch_dependents();
   pdl_wait();
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, cons
     const int p = pos[row / a.Hq];
     if (p < 0 || p >= T) n = 0;
   }
-  join_row<TIO>(a, row, n, lane, [&](int i) { return a.part_ml[i * rows + row]; }, [&](int i) { return a.part_o + (i * rows + row) * kD; });
+  join_row<S, TIO>(a, row, n, lane, [&](int i) { return a.part_ml[i * rows + row]; }, [&](int i) { return a.part_o + (i * rows + row) * kD; });
 }
 
 int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos_T, void* stream) {
@@ -379,8 +379,11 @@ int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos
   const dim3 grid((unsigned)((rows + 7) / 8));
   cudaStream_t st = (cudaStream_t)stream;
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
-  const cudaError_t e = dtype == SFA_BF16 ? launch_pdl(cross_join_kernel<bf16>, grid, dim3(256), 0, st, a, pos, pos_T)
-                                          : launch_pdl(cross_join_kernel<float>, grid, dim3(256), 0, st, a, pos, pos_T);
+  constexpr int F = kFewParts / 4;
+  const bool few = a.splits <= kFewParts;
+  auto* f = dtype == SFA_BF16 ? (few ? cross_join_kernel<F, bf16> : cross_join_kernel<8, bf16>)
+                              : (few ? cross_join_kernel<F, float> : cross_join_kernel<8, float>);
+  const cudaError_t e = launch_pdl(f, grid, dim3(256), 0, st, a, pos, pos_T);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 

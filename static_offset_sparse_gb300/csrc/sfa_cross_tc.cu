@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(256) cross_join_places_kernel(const CrossArgs 
     const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
     const RowOf ro = row_of(a, w.rt, s.z + (i >> 7), i & 127);
     if (ro.mine)
-      join_row<bf16>(a, s.x * a.rs.b + (s.y * a.G + ro.g) * a.rs.h + ro.t * a.rs.t, s.w, lane, [&](int x) { return w.place_ml[place(x, i)]; },
+      join_row<8, bf16>(a, s.x * a.rs.b + (s.y * a.G + ro.g) * a.rs.h + ro.t * a.rs.t, s.w, lane, [&](int x) { return w.place_ml[place(x, i)]; },
                      [&](int x) { return w.place_o + place(x, i) * kD; });
     return;
   }
@@ -622,6 +622,7 @@ __global__ void __launch_bounds__(256) cross_join_places_kernel(const CrossArgs 
 
 // A decode step behind a prefix: the prefix's parts, whole units' in the rows' own
 // places, and those of the sequences' own rows behind them (a.part_o + rows * 64 on).
+template <int S>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const CrossArgs a, const TcWork w, const Shares shares, int steps, const int32_t* pos, int T) {
   pdl_launch_dependents();
   pdl_wait();
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const CrossArgs a, con
   const int64_t begin = ((int64_t)kvh * ((w.rt.tiles + 1) >> 1) + (tile >> 1)) * (steps + kUnitCost);
   const int c0 = shares.owner(begin + kUnitCost), c1 = shares.owner(begin + kUnitCost + steps - 1), n = c1 - c0 + 1;
   auto place = [&](int x) { return (int64_t)(x == 0 ? 2 * c0 + 1 : 2 * (c0 + x)) * 256 + i; };
-  join_row<bf16>(a, row, there ? n + a.splits : 0, lane,
+  join_row<S, bf16>(a, row, there ? n + a.splits : 0, lane,
                  [&](int x) { return x >= n ? a.part_ml[(1 + x - n) * a.rows + row] : n == 1 ? a.part_ml[row] : w.place_ml[place(x)]; },
                  [&](int x) {
                    return x >= n ? a.part_o + ((1 + x - n) * a.rows + row) * kD : n == 1 ? a.part_o + row * kD : w.place_o + place(x) * kD;
@@ -721,9 +722,12 @@ int launch_prefix_tc(const CrossArgs& a, void* ws, void* stream) {
 int launch_prefix_join(const CrossArgs& prefix, const CrossArgs& out, void* ws, const int32_t* pos, int T, void* stream) {
   int ctas;
   const TcWork w = tc_work(prefix, ws, &ctas);
+  const Shares s = tc_shares(1, prefix.Hkv, w.rt, prefix.Tk);
+  const int steps = (prefix.Tk + kKeys - 1) / kKeys;
+  const bool few = steps / s.share + 2 + out.splits <= kFewParts;
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
-  const cudaError_t e = launch_pdl(prefix_join_kernel, dim3((unsigned)((out.rows + 7) / 8)), dim3(256), 0, (cudaStream_t)stream, out, w,
-                                   tc_shares(1, prefix.Hkv, w.rt, prefix.Tk), (prefix.Tk + kKeys - 1) / kKeys, pos, T);
+  const cudaError_t e = launch_pdl(few ? prefix_join_kernel<kFewParts / 4> : prefix_join_kernel<8>, dim3((unsigned)((out.rows + 7) / 8)), dim3(256), 0,
+                                   (cudaStream_t)stream, out, w, s, steps, pos, T);
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
