@@ -432,9 +432,10 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
     a.v = prefix_v;
     a.splits = p.shared;
     set_parts(&a, parts, p.shared + p.own, p.rows, 0);
-    rc = p.two ? launch_prefix_tc(a, parts + p.parts, stream)
-         : p.kind == kFewRows ? launch_cross_stream(a, true, d->dtype, stream)
-                              : launch_cross_fwd_f32(a, stream);
+    if (p.two)
+      rc = launch_prefix_tc(a, parts + p.parts, stream);
+    else if (p.kind == kFp32)
+      rc = launch_cross_fwd_f32(a, stream);
     if (rc != SFA_OK) return rc;
   }
   const CrossArgs prefix = a;
@@ -451,7 +452,8 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
   a.kv_add = 1;
   a.splits = p.own;
   set_parts(&a, parts, p.shared + p.own, p.rows, p.shared);
-  if ((rc = launch_cross_stream(a, true, d->dtype, stream)) != SFA_OK) return rc;
+  rc = d->P && p.kind == kFewRows ? launch_cross_stream_two(prefix, a, d->dtype, stream) : launch_cross_stream(a, true, d->dtype, stream);
+  if (rc != SFA_OK) return rc;
   a.o = o;
   a.lse = lse;
   set_parts(&a, parts, p.shared + p.own, p.rows, 0);

@@ -427,6 +427,8 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 
 // host side
 int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream);
+// Two in one launch, of fp32 queries; a's rows are as many as b's or more.
+int launch_cross_stream_two(const CrossArgs& a, const CrossArgs& b, int dtype, void* stream);
 int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos_T, void* stream);
 int launch_cross_fwd_f32(const CrossArgs& a, void* stream);
 // A tensor map of bf16 rows: boxes of `heads` x `rows` rows, 128-byte swizzle (sfa_api.cu).

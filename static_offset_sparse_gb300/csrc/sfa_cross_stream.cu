@@ -16,6 +16,8 @@
 // the next, values need one byte permutation a register (two keys' numbers of a dim
 // side by side).  Probabilities are rounded to bf16 for their product.  (The fp32
 // kernel on bf16 rows took 62 us for 500 sequences of up to 700 rows of 16 / 2 heads.)
+#include <type_traits>
+
 #include "sfa_cross.cuh"
 
 namespace sfa {
@@ -85,10 +87,9 @@ __device__ __forceinline__ void stream_out(const CrossArgs& a, const float (*so)
 struct StreamUnit {
   int b, kvh, r0, s;
 };
-__device__ __forceinline__ StreamUnit stream_unit(const CrossArgs& a, int R) {
+__device__ __forceinline__ StreamUnit stream_unit(const CrossArgs& a, int R, uint32_t x) {
   const int groups = (a.G * a.Tq + R - 1) / R;
   StreamUnit u;
-  uint32_t x = blockIdx.x;
   u.s = x % a.splits;
   x /= a.splits;
   u.r0 = (int)(x % groups) * R;
@@ -98,17 +99,31 @@ __device__ __forceinline__ StreamUnit stream_unit(const CrossArgs& a, int R) {
   return u;
 }
 
+// TWO calls in one launch, which wait for nothing of one another: the first n0 CTAs are
+// a0's, the others a1's.  (A decode step of 4 sequences behind 1000 rows: 16.1 us in two
+// launches, so 11.8.)
+template <bool TWO>
+struct StreamCall {
+  const bool second;
+  const CrossArgs a;
+  const uint32_t x;
+  __device__ __forceinline__ StreamCall(const CrossArgs& a0, const CrossArgs& a1, uint32_t n0)
+      : second(TWO && blockIdx.x >= n0), a(second ? a1 : a0), x(second ? blockIdx.x - n0 : blockIdx.x) {}
+};
+
 constexpr int kMmaStep = 16;  // keys a warp takes at a time; the next ones are under way meanwhile
 
-template <typename TQ>
-__global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(const CrossArgs a) {
+template <typename TQ, bool TWO>
+__global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(const CrossArgs a0, const CrossArgs a1, uint32_t n0) {
   constexpr int PARTS = sizeof(TQ) == 4 ? 2 : 1;  // of a query: fp32 ones as two bf16 numbers
   __shared__ float so[kStreamWarps][16][kD];
   __shared__ float2 sml[kStreamWarps][16];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
-  const StreamUnit u = stream_unit(a, 16);
+  const StreamCall<TWO> call(a0, a1, n0);
+  const CrossArgs& a = call.a;
+  const StreamUnit u = stream_unit(a, 16, call.x);
   const int nq = a.queries(u.b), nk = a.keys(u.b);
   int k0, k1;
   split_keys(nk, kMmaStep, a.splits, u.s, k0, k1);
@@ -250,8 +265,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_mma_kernel(con
   stream_out<bf16, 16>(a, so, sml, u.b, u.kvh, u.r0, u.s, nq, k1 > k0);
 }
 
-template <int NR>
-__global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const CrossArgs a) {
+template <int NR, bool TWO>
+__global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const CrossArgs a0, const CrossArgs a1, uint32_t n0) {
   constexpr int U = 2;          // keys a lane takes at a time
   constexpr int kStep = 4 * U;  // keys a warp takes at a time
   __shared__ float so[kStreamWarps][NR][kD];
@@ -259,8 +274,10 @@ __global__ void __launch_bounds__(32 * kStreamWarps) cross_stream_kernel(const C
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kg = lane >> 3, d8 = (lane & 7) * 8;
+  const StreamCall<TWO> call(a0, a1, n0);
+  const CrossArgs& a = call.a;
   const int rows = a.G * a.Tq;
-  const StreamUnit unit = stream_unit(a, NR);
+  const StreamUnit unit = stream_unit(a, NR, call.x);
   const int s = unit.s, r0 = unit.r0, kvh = unit.kvh, b = unit.b;
   const int nq = a.queries(b), nk = a.keys(b);
   int k0, k1;
@@ -389,18 +406,23 @@ int launch_cross_join(const CrossArgs& a, int dtype, const int32_t* pos, int pos
 
 static unsigned stream_grid(const CrossArgs& a, int R) { return (unsigned)((int64_t)a.B * a.Hkv * ((a.G * a.Tq + R - 1) / R) * a.splits); }
 
-int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream) {
+template <bool TWO>
+static int launch_stream(const CrossArgs& a0, const CrossArgs& a1, bool q32, int dtype, void* stream) {
   cudaStream_t st = (cudaStream_t)stream;
-  const dim3 block(32 * kStreamWarps);
-  const int rows = a.G * a.Tq, nr = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8;
+  const int rows = a0.G * a0.Tq, nr = rows == 1 ? 1 : rows == 2 ? 2 : rows <= 4 ? 4 : 8, R = dtype == SFA_BF16 ? 16 : nr;
+  const unsigned n0 = stream_grid(a0, R);
+  const dim3 grid(n0 + (TWO ? stream_grid(a1, R) : 0)), block(32 * kStreamWarps);
+  using Q16 = std::conditional_t<TWO, float, bf16>;  // (two: of fp32 queries always)
+  auto* f = dtype == SFA_BF16 ? (q32 ? cross_stream_mma_kernel<float, TWO> : cross_stream_mma_kernel<Q16, TWO>)
+            : nr == 1         ? cross_stream_kernel<1, TWO>
+            : nr == 2         ? cross_stream_kernel<2, TWO>
+            : nr == 4         ? cross_stream_kernel<4, TWO>
+                              : cross_stream_kernel<8, TWO>;
   LaunchTimer tm(SFA_KERNEL_CROSS_FWD, stream);
-  cudaError_t e;
-  if (dtype == SFA_BF16)
-    e = launch_pdl(q32 ? cross_stream_mma_kernel<float> : cross_stream_mma_kernel<bf16>, dim3(stream_grid(a, 16)), block, 0, st, a);
-  else
-    e = launch_pdl(nr == 1 ? cross_stream_kernel<1> : nr == 2 ? cross_stream_kernel<2> : nr == 4 ? cross_stream_kernel<4> : cross_stream_kernel<8>,
-                   dim3(stream_grid(a, nr)), block, 0, st, a);
-  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+  return launch_pdl(f, grid, block, 0, st, a0, a1, n0) == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
+
+int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream) { return launch_stream<false>(a, a, q32, dtype, stream); }
+int launch_cross_stream_two(const CrossArgs& a, const CrossArgs& b, int dtype, void* stream) { return launch_stream<true>(a, b, true, dtype, stream); }
 
 }  // namespace sfa
