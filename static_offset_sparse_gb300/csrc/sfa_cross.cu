@@ -128,16 +128,18 @@ static Kind forward_kind(int rows, int dtype) {
 }
 
 // Parts of a call over `units` (sequence, KV head) pairs of Tq queries of G heads (not the
-// tensor cores').  Few rows, bf16: 256 keys a part at least (with 128, 32 x 8 / 2 heads over
-// 1500 took 12.1 us, so 10.3).  fp32: a part's keys take longer and its join as long, so
-// fewer, and sqrt(Tk / 12) parts at most (8 / 2 heads over 1000: 10.0 us for 13.5; over 10000
-// 18.5 us, and 31 without the limit).
+// tensor cores').  Few rows, bf16: two waves of the three CTAs that fit an SM (128 x 8 / 2
+// heads over 2048: 31.1 us, one wave of four 37.2), 256 keys a part at least (with 128,
+// 32 x 8 / 2 heads over 1500 took 11.4 us, so 9.9), 128 where all parts are an SM's each
+// and there is a join anyway (4 heads over 1000: 5.8 us for 7.1).  fp32: a part's keys take
+// longer and its join as long, so fewer, and sqrt(Tk / 12) parts at most (8 / 2 heads over
+// 1000: 9.4 us for 13.5; over 10000 16.8 us, and 31 without the limit).
 static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind, int dtype) {
   if (kind == kFewRows) {
     const int64_t ctas = units * ((G * Tq + stream_rows(dtype) - 1) / stream_rows(dtype));
-    int s = wave_splits(ctas, 4 * kSMs, Tk, dtype == SFA_BF16 ? 256 : 64);
-    if (dtype == SFA_F32)
-      while (s > 1 && 12 * s * s > Tk) --s;
+    if (dtype == SFA_BF16) return wave_splits(ctas, 6 * kSMs, Tk, Tk >= 512 && ctas * (Tk / 128) <= kSMs ? 128 : 256);
+    int s = wave_splits(ctas, 4 * kSMs, Tk, 64);
+    while (s > 1 && 12 * s * s > Tk) --s;
     return s;
   }
   return wave_splits(units * ((G * Tq + kF32Tile - 1) / kF32Tile), 3 * kSMs, (Tk + kF32Keys - 1) / kF32Keys, 1);
