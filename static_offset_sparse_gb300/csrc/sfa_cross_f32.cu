@@ -9,8 +9,8 @@
 // the issue of the splits and of the reads of right operands (about 2.5
 // instructions beside each matrix instruction) and, where there is one tile an SM, the
 // chain from one to the next.  (On the fp32 units, with 16 sums a thread, a backward pass
-// of 2 x 8 / 2 heads, 333 x 1000 ragged rows, took 158 us, so 108; a forward pass of
-// 4 x 4 heads, 37 x 777, 19.7 and 16.7.)
+// of 2 x 8 / 2 heads, 333 x 1000 ragged rows, took 158 us, so 97; a forward pass of
+// 4 x 4 heads, 37 x 777, 19.7 and 14.8.)
 #include "sfa_cross.cuh"
 
 namespace sfa {
