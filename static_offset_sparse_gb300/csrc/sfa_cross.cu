@@ -36,13 +36,20 @@ __global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, floa
   if (row < a.rows && d8 == 0) stat[row] = valid ? make_float2(a.lse[row] * kLog2e, sum) : make_float2(INFINITY, 0.0f);
 }
 
-// out = the sum of n-number parts, in order; blockIdx.y = 1: the parts behind them, to out1.
-__global__ void __launch_bounds__(256) cross_sum_kernel(const float* parts, int splits, int64_t n, float* out, float* out1) {
+// blockIdx.y-th: out = the sum of n-number parts, in order (n = 0: nothing).
+struct SumArgs {
+  const float* parts[3];
+  float* out[3];
+  int64_t n[3];
+  int splits[3];
+};
+__global__ void __launch_bounds__(256) cross_sum_kernel(const __grid_constant__ SumArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = a.n[blockIdx.y];
   if (i >= n) return;
-  parts += blockIdx.y * splits * n + i;
+  const float* const parts = a.parts[blockIdx.y] + i;
+  const int splits = a.splits[blockIdx.y];
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
   for (int s = 0; s < splits; ++s) {
@@ -52,7 +59,7 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const float* parts, int 
     x.z += y.z;
     x.w += y.w;
   }
-  *reinterpret_cast<float4*>((blockIdx.y ? out1 : out) + i) = x;
+  *reinterpret_cast<float4*>(a.out[blockIdx.y] + i) = x;
 }
 
 struct PrefixArgs {
@@ -221,7 +228,8 @@ static ForwardPlan forward_plan(const sfa_cross_desc* d) {
 struct BackwardPlan {  // (what is not bytes is the fp32 kernels')
   int dq_splits, dkv_splits;
   int64_t rows, keys;
-  size_t stat, bytes;  // bytes of the rows' numbers, of the workspace
+  size_t stat, bytes;   // bytes of the rows' numbers, of the workspace
+  size_t dq_parts;      // numbers of dq's parts, before those of dk and dv
 };
 
 static BackwardPlan backward_plan(const sfa_cross_desc* d) {
@@ -233,24 +241,16 @@ static BackwardPlan backward_plan(const sfa_cross_desc* d) {
     return p;
   }
   const int rt = (G * d->Tq + kF32Tile - 1) / kF32Tile, kt = (d->Tk + kF32Tile - 1) / kF32Tile;
-  p.dq_splits = wave_splits(units * rt, 8 * kSMs, kt, 1);
-  p.dkv_splits = wave_splits(units * kt, 8 * kSMs, rt, 1);
+  // (three CTAs fit an SM: two waves of dq's, fewer of the heavier others; with 8 and 8,
+  // 2 x 8 / 2 heads, 333 x 1000 ragged rows took 94 us, so 78)
+  p.dq_splits = wave_splits(units * rt, 6 * kSMs, kt, 1);
+  p.dkv_splits = wave_splits(units * kt, 4 * kSMs, rt, 1);
   p.rows = (int64_t)d->B * d->Hq * d->Tq;
   p.keys = units * d->Tk;
   p.stat = align256((size_t)p.rows * sizeof(float2));
-  const size_t q = p.dq_splits > 1 ? (size_t)p.dq_splits * p.rows * kD * sizeof(float) : 0;
-  const size_t kv = p.dkv_splits > 1 ? 2 * (size_t)p.dkv_splits * p.keys * kD * sizeof(float) : 0;
-  p.bytes = p.stat + (q > kv ? q : kv);
+  p.dq_parts = p.dq_splits > 1 ? (size_t)p.dq_splits * p.rows * kD : 0;
+  p.bytes = p.stat + (p.dq_parts + (p.dkv_splits > 1 ? 2 * (size_t)p.dkv_splits * p.keys * kD : 0)) * sizeof(float);
   return p;
-}
-
-// out (and out1 where there is one) = the sums of their parts.
-static int launch_sum(const float* parts, int splits, int64_t n, void* out, void* out1, void* stream) {
-  LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
-  const dim3 grid((unsigned)((n / 4 + 255) / 256), out1 ? 2 : 1);
-  const cudaError_t e = launch_pdl(cross_sum_kernel, grid, dim3(256), 0, (cudaStream_t)stream, parts, splits, n, static_cast<float*>(out),
-                                   static_cast<float*>(out1));
-  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
 // ---- a decode step behind a shared prefix
@@ -368,16 +368,23 @@ int sfa_cross_backward(const sfa_cross_desc* d, const void* q, const void* k, co
       return SFA_ERR_CUDA;
   }
   a.stat = stat;
+  CrossArgs kv = a;
   a.splits = p.dq_splits;
   a.parts = a.splits > 1;
   a.part_a = parts;
-  if ((rc = launch_cross_dq_f32(a, stream)) != SFA_OK) return rc;
-  if (a.parts && (rc = launch_sum(parts, a.splits, p.rows * kD, dq, nullptr, stream)) != SFA_OK) return rc;
-  a.splits = p.dkv_splits;
-  a.parts = a.splits > 1;
-  a.part_b = parts + (size_t)a.splits * p.keys * kD;
-  if ((rc = launch_cross_dkv_f32(a, stream)) != SFA_OK || !a.parts) return rc;
-  return launch_sum(a.part_a, a.splits, p.keys * kD, dk, dv, stream);
+  kv.splits = p.dkv_splits;
+  kv.parts = kv.splits > 1;
+  kv.part_a = parts + p.dq_parts;
+  kv.part_b = kv.part_a + (size_t)kv.splits * p.keys * kD;
+  if ((rc = launch_cross_bwd_f32(a, kv, stream)) != SFA_OK || (!a.parts && !kv.parts)) return rc;
+  const int64_t n = a.parts ? p.rows * kD : 0, m = kv.parts ? p.keys * kD : 0;
+  const SumArgs sums = {{a.part_a, kv.part_a, kv.part_b},
+                        {static_cast<float*>(dq), static_cast<float*>(dk), static_cast<float*>(dv)},
+                        {n, m, m},
+                        {a.splits, kv.splits, kv.splits}};
+  LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
+  const dim3 grid((unsigned)(((n > m ? n : m) / 4 + 255) / 256), 3);
+  return launch_pdl(cross_sum_kernel, grid, dim3(256), 0, (cudaStream_t)stream, sums) == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
 int sfa_prefix_workspace_size(const sfa_prefix_desc* d, size_t* bytes) {

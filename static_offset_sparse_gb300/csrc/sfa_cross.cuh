@@ -447,9 +447,8 @@ int launch_prefix_join(const CrossArgs& prefix, const CrossArgs& out, void* ws, 
 // Backward pass, bf16; ws: cross_bwd_tc_bytes.
 size_t cross_bwd_tc_bytes(int B, int Hkv, int G, int Tq, int Tk);
 int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream);
-// Backward pass, fp32.
-int launch_cross_dq_f32(const CrossArgs& a, void* stream);
-int launch_cross_dkv_f32(const CrossArgs& a, void* stream);
+// Backward pass, fp32: dq, and dk and dv.
+int launch_cross_bwd_f32(const CrossArgs& q, const CrossArgs& kv, void* stream);
 constexpr int kStreamRows = 8, kStreamRowsBf16 = 16;  // rows that a CTA of the kernels for few rows takes
 constexpr int kF32Tile = 64;  // rows and keys of the fp32 kernels' tiles
 constexpr int kF32Keys = 32;  // keys the fp32 forward kernel takes at a time

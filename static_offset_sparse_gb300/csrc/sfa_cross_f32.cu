@@ -9,7 +9,7 @@
 // the issue of the splits and of the reads of right operands (about 2.5
 // instructions beside each matrix instruction) and, where there is one tile an SM, the
 // chain from one to the next.  (On the fp32 units, with 16 sums a thread, a backward pass
-// of 2 x 8 / 2 heads, 333 x 1000 ragged rows, took 158 us, so 97; a forward pass of
+// of 2 x 8 / 2 heads, 333 x 1000 ragged rows, took 158 us, so 78; a forward pass of
 // 4 x 4 heads, 37 x 777, 19.7 and 14.8.)
 #include "sfa_cross.cuh"
 
@@ -296,14 +296,10 @@ __global__ void __launch_bounds__(kThreads32) cross_fwd_kernel(const CrossArgs a
 // ---- backward
 // dq: a CTA has 64 rows and a split of their keys.
 //   ds = p (dO v - delta), dq = sum ds k / 8
-__global__ void __launch_bounds__(kThreads32) cross_dq_kernel(const CrossArgs a) {
-  __shared__ __align__(16) float Ks[kTileN * kPitch];
-  __shared__ __align__(16) float Vs[kTileN * kPitch];
-  pdl_launch_dependents();
-  pdl_wait();
+__device__ __forceinline__ void cross_dq(const CrossArgs& a, float* sm, uint32_t x) {
+  float *const Ks = sm, *const Vs = sm + kTileN * kPitch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
   const int rows = a.G * a.Tq, tiles = (rows + kTileN - 1) / kTileN;
-  uint32_t x = blockIdx.x;
   const int s = x % a.splits;
   x /= a.splits;
   const int r0 = (int)(x % tiles) * kTileN;
@@ -388,17 +384,11 @@ __global__ void __launch_bounds__(kThreads32) cross_dq_kernel(const CrossArgs a)
 
 // dk, dv: a CTA has 64 keys and a split of the rows that attend them.
 //   dv = sum p dO, dk = sum ds q / 8
-constexpr size_t kDkvSmemBytes = 4 * kTileN * kPitch * sizeof(float);
-
-__global__ void __launch_bounds__(kThreads32, 3) cross_dkv_kernel(const CrossArgs a) {
-  extern __shared__ __align__(16) float sm[];
+__device__ __forceinline__ void cross_dkv(const CrossArgs& a, float* sm, uint32_t x) {
   float *const Qs = sm, *const Ds = sm + kTileN * kPitch, *const Ks = sm + 2 * kTileN * kPitch, *const Vs = sm + 3 * kTileN * kPitch;
   __shared__ float2 stat[kTileN];
-  pdl_launch_dependents();
-  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
   const int tiles = (a.Tk + kTileN - 1) / kTileN;
-  uint32_t x = blockIdx.x;
   const int s = x % a.splits;
   x /= a.splits;
   const int j0 = (int)(x % tiles) * kTileN;
@@ -478,18 +468,34 @@ __global__ void __launch_bounds__(kThreads32, 3) cross_dkv_kernel(const CrossArg
   }
 }
 
-static int launch_tiles(int kind, void (*f)(const CrossArgs), const CrossArgs& a, int rows, size_t smem, void* stream) {
-  const int64_t grid = (int64_t)a.B * a.Hkv * ((rows + kTileN - 1) / kTileN) * a.splits;
-  LaunchTimer tm(kind, stream);
-  cudaError_t e = smem ? cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
-  if (e == cudaSuccess) e = launch_pdl(f, dim3((unsigned)grid), dim3(kThreads32), smem, (cudaStream_t)stream, a);
-  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+// Both, which wait for nothing of one another, in one launch, so that their last CTAs fill
+// the SMs together (2 x 8 / 2 heads, 333 x 1000 ragged rows: 78 us, 97 one behind the other):
+// the first n0 CTAs are kv's.
+constexpr size_t kBwdSmemBytes = 4 * kTileN * kPitch * sizeof(float);
+__global__ void __launch_bounds__(kThreads32, 3) cross_bwd_kernel(const CrossArgs q, const CrossArgs kv, uint32_t n0) {
+  extern __shared__ __align__(16) float sm[];
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x < n0)
+    cross_dkv(kv, sm, blockIdx.x);
+  else
+    cross_dq(q, sm, blockIdx.x - n0);
 }
 
-int launch_cross_fwd_f32(const CrossArgs& a, void* stream) { return launch_tiles(SFA_KERNEL_CROSS_FWD, cross_fwd_kernel, a, a.G * a.Tq, 0, stream); }
-int launch_cross_dq_f32(const CrossArgs& a, void* stream) { return launch_tiles(SFA_KERNEL_CROSS_BWD_Q, cross_dq_kernel, a, a.G * a.Tq, 0, stream); }
-int launch_cross_dkv_f32(const CrossArgs& a, void* stream) {
-  return launch_tiles(SFA_KERNEL_CROSS_BWD_KV, cross_dkv_kernel, a, a.Tk, kDkvSmemBytes, stream);
+static unsigned tiles_grid(const CrossArgs& a, int rows) { return (unsigned)((int64_t)a.B * a.Hkv * ((rows + kTileN - 1) / kTileN) * a.splits); }
+
+int launch_cross_fwd_f32(const CrossArgs& a, void* stream) {
+  LaunchTimer tm(SFA_KERNEL_CROSS_FWD, stream);
+  const cudaError_t e = launch_pdl(cross_fwd_kernel, dim3(tiles_grid(a, a.G * a.Tq)), dim3(kThreads32), 0, (cudaStream_t)stream, a);
+  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+}
+int launch_cross_bwd_f32(const CrossArgs& q, const CrossArgs& kv, void* stream) {
+  const unsigned n0 = tiles_grid(kv, kv.Tk);
+  LaunchTimer tm(SFA_KERNEL_CROSS_BWD_KV, stream);
+  cudaError_t e = cudaFuncSetAttribute(cross_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmemBytes);
+  if (e == cudaSuccess)
+    e = launch_pdl(cross_bwd_kernel, dim3(n0 + tiles_grid(q, q.G * q.Tq)), dim3(kThreads32), kBwdSmemBytes, (cudaStream_t)stream, q, kv, n0);
+  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
 }  // namespace sfa
