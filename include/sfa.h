@@ -493,7 +493,7 @@ typedef enum {
   SFA_KERNEL_CROSS_JOIN = 12, /* parts of split sums put together */
   SFA_KERNEL_CROSS_STAT = 13, /* what comes before: delta, a step's rotations */
   SFA_KERNEL_CROSS_BWD_Q = 14,
-  SFA_KERNEL_CROSS_BWD_KV = 15, /* fp32: dq's too, in one launch */
+  SFA_KERNEL_CROSS_BWD_KV = 15, /* dq's too where one launch does both: in fp32, of small calls */
   SFA_KERNEL_KINDS = 16
 } sfa_kernel_kind;
 int sfa_timing_enable(int on);

@@ -169,9 +169,9 @@ struct WalkShared {
   int any;
 };
 
-// The CTA's first piece, by all THREADS threads; false if it has none.
+// The first piece of CTA c of ctas, by all its THREADS threads; false if it has none.
 template <int THREADS, typename F>
-__device__ __forceinline__ bool find_walk(int B, const F& counts, WalkShared& sh, Walk& wk) {
+__device__ __forceinline__ bool find_walk(int B, const F& counts, int c, int ctas, WalkShared& sh, Walk& wk) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (B + THREADS - 1) / THREADS;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   if (tid == 0) {
@@ -201,8 +201,7 @@ __device__ __forceinline__ bool find_walk(int B, const F& counts, WalkShared& sh
     total += sh.sums[i];
   }
   Shares s;
-  s.set(total, sh.units, gridDim.x);
-  const int c = blockIdx.x;
+  s.set(total, sh.units, ctas);
   const int64_t from = s.begin(c), to = s.begin(c + 1);
   int64_t at = upto - mine;
   if (c < s.ctas && from < to && from >= at && from < upto)
@@ -229,16 +228,16 @@ __device__ __forceinline__ bool find_walk(int B, const F& counts, WalkShared& sh
   return wk.set(from - wk.begin) || wk.next(B, counts);
 }
 
-// For each x = blockIdx.x, blockIdx.x + gridDim.x, .. below n with empty(x), do(x), by
-// whole warps; a lane looks at an x, so that the lengths of 32 are asked for at once.
+// For each x = c, c + ctas, .. below n with empty(x), todo(x), by whole warps; a lane
+// looks at an x, so that the lengths of 32 are asked for at once.
 template <typename E, typename D>
-__device__ __forceinline__ void each_empty(int64_t n, int lane, const E& empty, const D& todo) {
+__device__ __forceinline__ void each_empty(int64_t n, int c, int ctas, int lane, const E& empty, const D& todo) {
 #pragma unroll 1
-  for (int64_t from = blockIdx.x; from < n; from += 32 * (int64_t)gridDim.x) {
-    const int64_t x = from + (int64_t)lane * gridDim.x;
+  for (int64_t from = c; from < n; from += 32 * (int64_t)ctas) {
+    const int64_t x = from + (int64_t)lane * ctas;
 #pragma unroll 1
     for (unsigned left = __ballot_sync(0xffffffffu, x < n && empty(x)); left; left &= left - 1)
-      todo(from + (int64_t)(__ffs(left) - 1) * gridDim.x);
+      todo(from + (int64_t)(__ffs(left) - 1) * ctas);
   }
 }
 

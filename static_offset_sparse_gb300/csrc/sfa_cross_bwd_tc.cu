@@ -1,6 +1,6 @@
 // Backward pass of attention to states of another length on the
-// fifth-generation tensor cores (bf16): one kernel for dq, one for dk and dv,
-// which are the same walk with the roles of queries and keys exchanged.
+// fifth-generation tensor cores (bf16): dq, and dk and dv, which are the same walk
+// with the roles of queries and keys exchanged.
 //
 //   dq     a tile of 128 rows stays, their keys and values pass by:
 //            S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K
@@ -59,6 +59,7 @@ struct BtWork {
   int key_tiles;
   const float* stat;  // [B][Hkv][row tiles][2][128]
   float* places;      // [2 CTAs][128][64], dk and dv: twice that, dv's behind dk's
+  int ctas;
   int4* split;        // [CTAs]: the unit that a CTA begins and does not end: sequence, KV head, tile, parts (0: none)
 };
 
@@ -71,12 +72,10 @@ __device__ __forceinline__ void st_out(uint32_t at, uint32_t a, uint32_t b, uint
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// CTA cta of ctas.
 template <bool DKV>
-__global__ void __launch_bounds__(kBtThreads, 1)
-    cross_bwd_tc_kernel(const CrossArgs a, const BtWork w, const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
-                        const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ BtShared sh;
+__device__ __forceinline__ void cross_bwd_tc(const CrossArgs& a, const BtWork& w, const CUtensorMap& qm, const CUtensorMap& gm, const CUtensorMap& km,
+                                             const CUtensorMap& vm, uint8_t* smem_raw, BtShared& sh, int cta, int ctas) {
   const uint32_t smem = smem_u32(smem_raw) + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform, and known to be)
   pdl_launch_dependents();
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
   };
   Walk wk;
   tc05_fence_before();
-  const bool some = find_walk<kBtThreads>(a.B, counts, sh.walk, wk);  // (with barriers of the CTA)
+  const bool some = find_walk<kBtThreads>(a.B, counts, cta, ctas, sh.walk, wk);  // (with barriers of the CTA)
   tc05_fence_after();
   const uint32_t tm = sh.tmem;
   bool dead = false;  // a wait ran out: no more waits, no more work
@@ -145,7 +144,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
     if (a.q_len || a.kv_len) {
       const int own = DKV ? w.key_tiles : w.rt.tiles;
       each_empty(
-          (int64_t)a.B * a.Hkv * own, lane,
+          (int64_t)a.B * a.Hkv * own, cta, ctas, lane,
           [&](int64_t x) {
             const int bh = (int)(x / own);
             int units, steps;
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
       int row;  // of this thread, where it is written; INT_MIN: nowhere, ~: as zeros
       if (DKV) {
         const int key = p.tile * 128 + r;
-        row = whole ? (p.b * a.Hkv + p.kvh) * a.Tk + key : (p.place + (dv ? gridDim.x * 2 : 0)) * 128 + r;
+        row = whole ? (p.b * a.Hkv + p.kvh) * a.Tk + key : (p.place + (dv ? ctas * 2 : 0)) * 128 + r;
         row = key >= a.Tk ? INT_MIN : key >= p.nk ? ~row : row;
       } else {
         row = sh.rows[plan][r];
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
           const int st = n % kBtStages;
           if (n >= kBtStages) wait(&sh.empty[st], n / kBtStages - 1);
           if (dead) break;
-          if (lead && (n != a.debug_skip || blockIdx.x > 0)) {
+          if (lead && (n != a.debug_skip || cta > 0)) {
             const uint32_t bar = smem_u32(&sh.full[st]), dst = smem + kBtRing + st * 2 * kBtTile;
             mbar_expect_tx(bar, 2 * kBtTile + (DKV ? kBtStat : 0));
             if (DKV) {
@@ -519,10 +518,10 @@ __global__ void __launch_bounds__(kBtThreads, 1)
           p.t0 = wk.s0;
           p.nq = nq;
           p.nk = nk;
-          p.place = wk.whole() ? -1 : 2 * (int)blockIdx.x + (wk.s0 == 0);
+          p.place = wk.whole() ? -1 : 2 * cta + (wk.s0 == 0);
           sh.plan[i] = p;
         }
-        if (!wk.whole() && wk.s0 == 0) split = make_int4(wk.b, kvh, tile, sh.walk.shares.owner(wk.begin + wk.steps + kUnitCost - 1) - blockIdx.x + 1);
+        if (!wk.whole() && wk.s0 == 0) split = make_int4(wk.b, kvh, tile, sh.walk.shares.owner(wk.begin + wk.steps + kUnitCost - 1) - cta + 1);
         if (!DKV)
 #pragma unroll 1
           for (int r = lane; r < 128; r += 32) {
@@ -533,7 +532,7 @@ __global__ void __launch_bounds__(kBtThreads, 1)
         more = wk.next(a.B, counts);
         arrive(&sh.plan_full[i]);
       }
-      if (lane == 0) w.split[blockIdx.x] = split;
+      if (lane == 0) w.split[cta] = split;
       if (dead && lane == 0) record_status(a.status, SFA_ERR_TIMEOUT);
     }
   }
@@ -541,6 +540,23 @@ __global__ void __launch_bounds__(kBtThreads, 1)
   __syncthreads();
   tc05_fence_after();
   if (warp == kBtSoftmax + 1) tmem_dealloc(tm, 512);
+}
+
+// dq's CTAs, dk's and dv's, or both in one launch, kv's first (BtPlan says which).  Each
+// in a kernel of its own, because with both in one the registers of a thread do not reach
+// (32 x 8 / 2 heads, 1024 x 2048 ragged rows through it in two launches: 251 us, so 239).
+enum BtPart { kBtDq, kBtDkv, kBtBoth };
+template <BtPart PART>
+__global__ void __launch_bounds__(kBtThreads, 1)
+    cross_bwd_tc_kernel(const CrossArgs a, const BtWork q, const BtWork kv, const __grid_constant__ CUtensorMap qm,
+                        const __grid_constant__ CUtensorMap gm, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ BtShared sh;
+  const int first = PART == kBtBoth ? kv.ctas : 0, cta = blockIdx.x;  // dq's first
+  if (PART == kBtDkv || (PART == kBtBoth && cta < first))
+    cross_bwd_tc<true>(a, kv, qm, gm, km, vm, smem_raw, sh, cta, PART == kBtDkv ? gridDim.x : kv.ctas);
+  else
+    cross_bwd_tc<false>(a, q, qm, gm, km, vm, smem_raw, sh, cta - first, PART == kBtDq ? gridDim.x : q.ctas);
 }
 
 // What the kernels need of each row, tile by tile: -lse log2(e) and -delta, eight
@@ -590,11 +606,11 @@ __global__ void __launch_bounds__(256) cross_stat_tc_kernel(const CrossArgs a, c
 // Units that span CTAs: the sums of their parts, in order.  CTA (c, y) has 32 rows of
 // the unit that CTA c of the dq kernel (c < q_ctas) or of the dk, dv kernel began, eight
 // lanes a row.
-__global__ void __launch_bounds__(256) cross_sum_places_kernel(const CrossArgs a, const BtWork q, const BtWork kv, int q_ctas, int kv_ctas) {
+__global__ void __launch_bounds__(256) cross_sum_places_kernel(const CrossArgs a, const BtWork q, const BtWork kv) {
   pdl_launch_dependents();
   pdl_wait();
-  const bool dkv = (int)blockIdx.x >= q_ctas;
-  const int c = dkv ? blockIdx.x - q_ctas : blockIdx.x, lane = threadIdx.x & 31, d8 = (lane & 7) * 8;
+  const bool dkv = (int)blockIdx.x >= q.ctas;
+  const int c = dkv ? blockIdx.x - q.ctas : blockIdx.x, lane = threadIdx.x & 31, d8 = (lane & 7) * 8;
   const int4 s = dkv ? kv.split[c] : q.split[c];
   if (s.w <= 1) return;
   // many parts: four at a time, 8 rows of the CTA's 32 at once; few: a row's one after
@@ -613,7 +629,7 @@ __global__ void __launch_bounds__(256) cross_sum_places_kernel(const CrossArgs a
       const RowOf ro = row_of(a, q.rt, s.z, r);
       if (ro.mine) row = a.row(s.x, s.y, ro.t * a.G + ro.g);
     }
-    const float* const from = (dkv ? kv.places : q.places) + (dv ? (int64_t)kv_ctas * 2 * 128 * kD : 0) + r * kD + d8;
+    const float* const from = (dkv ? kv.places : q.places) + (dv ? (int64_t)kv.ctas * 2 * 128 * kD : 0) + r * kD + d8;
     float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, z[8];
     if (row >= 0)
 #pragma unroll 2
@@ -634,6 +650,7 @@ __global__ void __launch_bounds__(256) cross_sum_places_kernel(const CrossArgs a
 
 struct BtPlan {
   RowTiles rt;
+  bool one;  // whether dq, and dk and dv, are one launch
   int key_tiles, q_ctas, kv_ctas;
   size_t stat, q_places, kv_places, bytes;
 };
@@ -643,11 +660,23 @@ static BtPlan bt_plan(int B, int Hkv, int G, int Tq, int Tk) {
   p.rt = row_tiles(G, Tq);
   p.key_tiles = (Tk + 127) / 128;
   const int64_t u = (int64_t)B * Hkv, qu = u * p.rt.tiles, ku = u * p.key_tiles;
-  Shares s;
-  s.set(qu * (p.key_tiles + kUnitCost), qu, kSMs);
-  p.q_ctas = s.ctas;
-  s.set(ku * (p.rt.tiles + kUnitCost), ku, kSMs);
-  p.kv_ctas = s.ctas;
+  // Both in one launch, the SMs shared out by weights (and 15 : 14, a step of dk and dv
+  // against one of dq): a start and an uneven end less (4 x 8 / 2 heads, 64 x 64: 22.8 us in
+  // two, so 14.3; 4 x 8 / 8, 4096 x 77: 56.7 and 50.2).  From 128 steps an SM on what the
+  // weights do not know costs more than that (32 x 8 / 2 heads, 1024 x 2048: 425 us in two
+  // launches, 436 in one; 200 x 8 / 2, 33 x 1500: 267 and 290).
+  const int64_t qw = qu * (p.key_tiles + kUnitCost), kw = ku * (p.rt.tiles + kUnitCost);
+  p.one = qw + kw <= 128 * kSMs;
+  Shares q, kv;
+  q.set(qw, qu, kSMs);
+  kv.set(kw, ku, kSMs);
+  if (p.one && q.ctas + kv.ctas > kSMs) {
+    const int n = (int)((kSMs * 15 * kw + (15 * kw + 14 * qw) / 2) / (15 * kw + 14 * qw));
+    kv.set(kw, ku, n < 1 ? 1 : n < kSMs ? n : kSMs - 1);
+    q.set(qw, qu, kSMs - kv.ctas);
+  }
+  p.q_ctas = q.ctas;
+  p.kv_ctas = kv.ctas;
   p.stat = align256((size_t)qu * kBtStat);
   p.q_places = (size_t)p.q_ctas * 2 * 128 * kD * sizeof(float);
   p.kv_places = (size_t)p.kv_ctas * 4 * 128 * kD * sizeof(float);
@@ -662,8 +691,8 @@ int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream) {
   const BtPlan p = bt_plan(a.B, a.Hkv, a.G, a.Tq, a.Tk);
   char* const at = static_cast<char*>(ws);
   float* const stat = static_cast<float*>(ws);
-  BtWork q = {p.rt, p.key_tiles, stat, reinterpret_cast<float*>(at + p.stat), reinterpret_cast<int4*>(at + p.stat + p.q_places + p.kv_places)};
-  BtWork kv = {p.rt, p.key_tiles, stat, reinterpret_cast<float*>(at + p.stat + p.q_places), q.split + p.q_ctas};
+  BtWork q = {p.rt, p.key_tiles, stat, reinterpret_cast<float*>(at + p.stat), p.q_ctas, reinterpret_cast<int4*>(at + p.stat + p.q_places + p.kv_places)};
+  BtWork kv = {p.rt, p.key_tiles, stat, reinterpret_cast<float*>(at + p.stat + p.q_places), p.kv_ctas, q.split + p.q_ctas};
   CUtensorMap qm, gm, km, vm;
   const Strides dense = {(int64_t)a.Hq * a.Tq * kD, (int64_t)a.Tq * kD, kD};
   int rc = make_view_map(&qm, a.q, a.Tq, a.Hq, a.B, a.qs, 1 << p.rt.lgR, 128 >> p.rt.lgR);
@@ -672,23 +701,25 @@ int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream) {
   if (rc == SFA_OK) rc = make_view_map(&vm, a.v, a.Tk, a.Hkv, a.B, a.vs, 128, 1);
   if (rc != SFA_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaFuncSetAttribute(cross_bwd_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBtSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(cross_bwd_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBtSmem);
+  cudaError_t e = cudaSuccess;
   if (e == cudaSuccess) {
     LaunchTimer tm(SFA_KERNEL_CROSS_STAT, stream);
     e = launch_pdl(cross_stat_tc_kernel, dim3((unsigned)((int64_t)a.B * a.Hkv * p.rt.tiles)), dim3(256), 0, st, a, p.rt, stat);
   }
-  if (e == cudaSuccess) {
-    LaunchTimer tm(SFA_KERNEL_CROSS_BWD_Q, stream);
-    e = launch_pdl(cross_bwd_tc_kernel<false>, dim3((unsigned)p.q_ctas), dim3(kBtThreads), kBtSmem, st, a, q, qm, gm, km, vm);
-  }
-  if (e == cudaSuccess) {
-    LaunchTimer tm(SFA_KERNEL_CROSS_BWD_KV, stream);
-    e = launch_pdl(cross_bwd_tc_kernel<true>, dim3((unsigned)p.kv_ctas), dim3(kBtThreads), kBtSmem, st, a, kv, qm, gm, km, vm);
+  auto launch = [&](int kind, auto* f, int ctas) {
+    LaunchTimer tm(kind, stream);
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kBtSmem);
+    return e != cudaSuccess ? e : launch_pdl(f, dim3((unsigned)ctas), dim3(kBtThreads), kBtSmem, st, a, q, kv, qm, gm, km, vm);
+  };
+  if (p.one) {
+    if (e == cudaSuccess) e = launch(SFA_KERNEL_CROSS_BWD_KV, cross_bwd_tc_kernel<kBtBoth>, p.q_ctas + p.kv_ctas);
+  } else {
+    if (e == cudaSuccess) e = launch(SFA_KERNEL_CROSS_BWD_Q, cross_bwd_tc_kernel<kBtDq>, p.q_ctas);
+    if (e == cudaSuccess) e = launch(SFA_KERNEL_CROSS_BWD_KV, cross_bwd_tc_kernel<kBtDkv>, p.kv_ctas);
   }
   if (e == cudaSuccess) {
     LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
-    e = launch_pdl(cross_sum_places_kernel, dim3((unsigned)(p.q_ctas + p.kv_ctas), 4), dim3(256), 0, st, a, q, kv, p.q_ctas, p.kv_ctas);
+    e = launch_pdl(cross_sum_places_kernel, dim3((unsigned)(p.q_ctas + p.kv_ctas), 4), dim3(256), 0, st, a, q, kv);
   }
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   Walk wk;
   tc05_fence_before();
-  const bool some = find_walk<kTcThreads>(a.B, counts, sh.walk, wk);  // (with barriers of the CTA)
+  const bool some = find_walk<kTcThreads>(a.B, counts, blockIdx.x, gridDim.x, sh.walk, wk);  // (with barriers of the CTA)
   tc05_fence_after();
   const uint32_t tm = sh.tmem;
   bool dead = false;  // a wait ran out: no more waits, no more work
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // rows of tiles without work: zeros (parts have no such rows)
     if (!a.parts && (a.q_len || a.kv_len))
       each_empty(
-          (int64_t)a.B * a.Hkv * w.rt.tiles, lane,
+          (int64_t)a.B * a.Hkv * w.rt.tiles, blockIdx.x, gridDim.x, lane,
           [&](int64_t x) {
             const int bh = (int)(x / w.rt.tiles), b = bh / a.Hkv;
             return x - (int64_t)bh * w.rt.tiles >= (a.keys(b) > 0 ? (w.rt.used(a.queries(b)) + 1) & ~1 : 0);

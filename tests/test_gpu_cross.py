@@ -438,7 +438,7 @@ def test_many_ragged_sequences(sfa, Tq, Tk, Hq, Hkv, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
-@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv", [(100, 300, 300, 8, 2), (413, 40, 150, 4, 1)])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv", [(100, 300, 300, 8, 2), (413, 40, 150, 4, 1), (130, 400, 500, 8, 2)])
 def test_many_ragged_sequences_again_and_again(sfa, B, Tq, Tk, Hq, Hkv, dtype):
     """Many short units an SM, one behind the other: every call gives the same bits."""
     gen = torch.Generator().manual_seed(7)
@@ -452,6 +452,16 @@ def test_many_ragged_sequences_again_and_again(sfa, B, Tq, Tk, Hq, Hkv, dtype):
         again = sfa.cross_backward(q, k, v, *first, do, q_len=nq, kv_len=nk)
         assert all(torch.equal(a, b) for a, b in zip(grads, again))
     assert sfa.get_device_status() == 0
+
+
+def test_backward_of_a_large_batch(sfa):
+    """Enough steps an SM for dq, and dk and dv, to be launches of their own."""
+    B, Tq, Tk = 17, 1000, 2040
+    q, k, v, do = _inputs(25, B, Tq, Tk, 4, 2, torch.bfloat16)
+    gen = torch.Generator().manual_seed(26)
+    nq, nk = (torch.randint(n // 2, n + 1, (B,), generator=gen).tolist() for n in (Tq, Tk))
+    nq[3], nk[5] = 0, 0
+    _check_backward(sfa, _spoil(q, nq), _spoil(k, nk), _spoil(v, nk), do, nq, nk)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
