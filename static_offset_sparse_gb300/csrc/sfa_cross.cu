@@ -134,20 +134,29 @@ static Kind forward_kind(int rows, int dtype) {
   return rows <= 4 * kStreamRows ? kFewRows : kFp32;
 }
 
+// Whether a row's splits are a cluster, without workspace and join (32 x 8 / 2 heads over
+// 1500 10.0 -> 8.3 us): where all CTAs are on the card at once (64 x 8 / 2 heads, 4 queries
+// over 2000, bf16, 7 splits: 18.5 us with a join, 26.3 in clusters), three an SM in bf16, two
+// in fp32, four of up to 4 rows.
+static bool clustered(int rows, int64_t units, int splits, int dtype) {
+  const int64_t ctas = units * ((rows + stream_rows(dtype) - 1) / stream_rows(dtype)) * splits;
+  return splits > 1 && splits <= kClusterSplits && ctas <= (dtype == SFA_BF16 ? 3 : rows > 4 ? 2 : 4) * kSMs;
+}
+
 // Parts of a call over `units` (sequence, KV head) pairs of Tq queries of G heads (not the
 // tensor cores').  Few rows, bf16: two waves of the three CTAs that fit an SM (128 x 8 / 2
 // heads over 2048: 31.1 us, one wave of four 37.2), 256 keys a part at least (with 128,
 // 32 x 8 / 2 heads over 1500 took 11.4 us, so 9.9), 128 where all parts are an SM's each
 // and there is a join anyway (4 heads over 1000: 5.8 us for 7.1).  fp32: a part's keys take
 // longer and its join as long, so fewer, and sqrt(Tk / 12) parts at most (8 / 2 heads over
-// 1000: 9.4 us for 13.5; over 10000 16.8 us, and 31 without the limit).
+// 1000: 9.1 us for 13.5; over 10000 16.8 us, and 31 without the limit).
 static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind, int dtype) {
   if (kind == kFewRows) {
     const int64_t ctas = units * ((G * Tq + stream_rows(dtype) - 1) / stream_rows(dtype));
     if (dtype == SFA_BF16) return wave_splits(ctas, 6 * kSMs, Tk, Tk >= 512 && ctas * (Tk / 128) <= kSMs ? 128 : 256);
     int s = wave_splits(ctas, 4 * kSMs, Tk, 64);
     while (s > 1 && 12 * s * s > Tk) --s;
-    return s;
+    return (s == 9 || s == 10) && clustered(G * Tq, units, kClusterSplits, dtype) ? kClusterSplits : s;
   }
   return wave_splits(units * ((G * Tq + kF32Tile - 1) / kF32Tile), 3 * kSMs, (Tk + kF32Keys - 1) / kF32Keys, 1);
 }
@@ -210,17 +219,19 @@ static int cross_args(const sfa_cross_desc* d, CrossArgs* a) {
 struct ForwardPlan {
   Kind kind;
   int splits;
+  bool cluster;
   size_t bytes;
 };
 
 static ForwardPlan forward_plan(const sfa_cross_desc* d) {
   const int G = d->Hq / d->Hkv;
-  ForwardPlan p = {forward_kind(G * d->Tq, d->dtype), 1, 0};
+  ForwardPlan p = {forward_kind(G * d->Tq, d->dtype), 1, false, 0};
   if (p.kind == kTensor) {
     p.bytes = cross_tc_bytes(d->B, d->Hkv, G, d->Tq, d->Tk);
   } else {
     p.splits = forward_splits((int64_t)d->B * d->Hkv, G, d->Tq, d->Tk, p.kind, d->dtype);
-    if (p.splits > 1) p.bytes = part_bytes(p.splits, (int64_t)d->B * d->Hq * d->Tq);
+    p.cluster = p.kind == kFewRows && clustered(G * d->Tq, (int64_t)d->B * d->Hkv, p.splits, d->dtype);
+    if (p.splits > 1 && !p.cluster) p.bytes = part_bytes(p.splits, (int64_t)d->B * d->Hq * d->Tq);
   }
   return p;
 }
@@ -332,7 +343,8 @@ int sfa_cross_forward(const sfa_cross_desc* d, const void* q, const void* k, con
   a.lse = lse;
   if (p.kind == kTensor) return launch_cross_fwd_tc(a, ws, stream);
   a.splits = p.splits;
-  a.parts = a.splits > 1;
+  a.cluster = p.cluster;
+  a.parts = a.splits > 1 && !a.cluster;
   if (a.parts) set_parts(&a, static_cast<char*>(ws), a.splits, a.rows, 0);
   rc = p.kind == kFewRows ? launch_cross_stream(a, false, d->dtype, stream) : launch_cross_fwd_f32(a, stream);
   return rc != SFA_OK || !a.parts ? rc : launch_cross_join(a, d->dtype, nullptr, 0, stream);

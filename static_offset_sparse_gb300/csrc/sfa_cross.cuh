@@ -43,7 +43,8 @@ struct CrossArgs {
   int kv_add;  // added to kv_len (1 where it holds the position of the last key)
   int B, Tq, Tk, Hq, Hkv, G;
   int splits;       // parts that the keys of a row (dk, dv: the rows of a key) are split into
-  bool parts;       // whether parts are written (always with more than one split), or o and lse
+  bool parts;       // whether parts are written, or o and lse
+  bool cluster;     // few rows: a cluster's CTAs are a row's splits, which meet in shared memory
   float* part_o;    // [splits][rows][64]
   float2* part_ml;  // [splits][rows] (m, l); l < 0: no key, and no sum in part_o
   // backward
@@ -449,6 +450,7 @@ int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream);
 // Backward pass, fp32: dq, and dk and dv.
 int launch_cross_bwd_f32(const CrossArgs& q, const CrossArgs& kv, void* stream);
 constexpr int kStreamRows = 8, kStreamRowsBf16 = 16;  // rows that a CTA of the kernels for few rows takes
+constexpr int kClusterSplits = 8;  // splits whose CTAs may be a cluster
 constexpr int kF32Tile = 64;  // rows and keys of the fp32 kernels' tiles
 constexpr int kF32Keys = 32;  // keys the fp32 forward kernel takes at a time
 

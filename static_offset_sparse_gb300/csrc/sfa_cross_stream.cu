@@ -3,7 +3,7 @@
 //
 // Every key and value is read once for the rows of its KV head and used for a few
 // multiplications a row: memory bounds it.  All sums are fp32; no shared memory but
-// for the join of a CTA's four warps.
+// for the join of a CTA's four warps and of a cluster's CTAs.
 //
 // fp32: eight lanes hold a key, 8 dims each, so a warp reads four whole rows at a time
 // straight into registers; a row's products are summed over the eight lanes by halving
@@ -48,13 +48,11 @@ __device__ __forceinline__ float sum_rows(float* acc, int lane) {
 }
 
 // The warps' sums of a CTA's rows, R of them, [warp][row][64] and (m, l), to parts
-// or to o and lse.
+// or to o and lse; in a cluster, whose CTAs have a split each, rank by rank a row.
 template <typename TIO, int R>
-__device__ __forceinline__ void stream_out(const CrossArgs& a, const float (*so)[R][kD], const float2 (*sml)[R], int b, int kvh, int r0, int s, int nq,
-                                           bool keys) {
-  const int rows = a.G * a.Tq;
-  for (int i = threadIdx.x; i < R * 32; i += 32 * kStreamWarps) {
-    const int r = i >> 5, d = (i & 31) * 2;
+__device__ __forceinline__ void stream_out(const CrossArgs& a, float (*so)[R][kD], float2 (*sml)[R], int b, int kvh, int r0, int s, int nq, bool keys) {
+  const int rows = a.G * a.Tq, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = 2 * lane;
+  for (int r = warp; r < R; r += kStreamWarps) {
     if (r0 + r >= rows) break;
     const int t = (r0 + r) / a.G;
     float mm = -INFINITY;
@@ -75,12 +73,51 @@ __device__ __forceinline__ void stream_out(const CrossArgs& a, const float (*so)
       const int64_t at = s * a.rows + row;
       if (!none) store2(a.part_o + at * kD + d, y0, y1);
       if (d == 0) a.part_ml[at] = none ? make_float2(-INFINITY, -1.0f) : make_float2(mm, ll);
+    } else if (a.cluster) {
+      __syncwarp();  // (the row is this warp's alone)
+      so[0][r][d] = y0;
+      so[0][r][d + 1] = y1;
+      if (d == 0) sml[0][r] = none ? make_float2(-INFINITY, -1.0f) : make_float2(mm, ll);
     } else {
       const float inv = 1.0f / ll;
       store2(static_cast<TIO*>(a.o) + row * kD + d, none ? 0.0f : y0 * inv, none ? 0.0f : y1 * inv);
       if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
     }
   }
+  if (!a.cluster) return;
+  cluster_sync();
+  for (int r = s + a.splits * warp; r < R; r += a.splits * kStreamWarps) {
+    if (r0 + r >= rows) break;
+    float m[kClusterSplits], l[kClusterSplits], y0[kClusterSplits], y1[kClusterSplits], mm = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kClusterSplits; ++c) {
+      const bool there = c < a.splits;  // (else this CTA's own, for nothing)
+      const int rank = there ? c : s;
+      m[c] = cluster_read(&sml[0][r].x, rank);
+      l[c] = cluster_read(&sml[0][r].y, rank);
+      y0[c] = cluster_read(&so[0][r][d], rank);
+      y1[c] = cluster_read(&so[0][r][d + 1], rank);
+      if (!there) l[c] = -1.0f;
+      if (there) mm = fmaxf(mm, m[c]);
+    }
+    const float sh = shift_of(mm);
+    float ll = 0.0f, z0 = 0.0f, z1 = 0.0f;
+    bool any = false;
+#pragma unroll
+    for (int c = 0; c < kClusterSplits; ++c)
+      if (!(l[c] < 0.0f)) {
+        const float f = exp2f(m[c] - sh);
+        any = true;
+        ll = fmaf(f, l[c], ll);
+        z0 = fmaf(f, y0[c], z0);
+        z1 = fmaf(f, y1[c], z1);
+      }
+    const int64_t row = a.row(b, kvh, r0 + r);
+    const float inv = 1.0f / ll;
+    store2(static_cast<TIO*>(a.o) + row * kD + d, any ? z0 * inv : 0.0f, any ? z1 * inv : 0.0f);
+    if (a.lse && d == 0) a.lse[row] = any ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+  }
+  cluster_sync();  // until all have read
 }
 
 // The CTA's sequence, KV head, first row and split.
@@ -419,7 +456,9 @@ static int launch_stream(const CrossArgs& a0, const CrossArgs& a1, bool q32, int
             : nr == 4         ? cross_stream_kernel<4, TWO>
                               : cross_stream_kernel<8, TWO>;
   LaunchTimer tm(SFA_KERNEL_CROSS_FWD, stream);
-  return launch_pdl(f, grid, block, 0, st, a0, a1, n0) == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
+  const cudaError_t e = !TWO && a0.cluster ? launch_pdl_cluster(f, grid, block, (unsigned)a0.splits, 0, st, a0, a1, n0)
+                                           : launch_pdl(f, grid, block, 0, st, a0, a1, n0);
+  return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
 
 int launch_cross_stream(const CrossArgs& a, bool q32, int dtype, void* stream) { return launch_stream<false>(a, a, q32, dtype, stream); }

@@ -279,18 +279,6 @@ struct GatherRows {
   uint32_t magic;  // 2^32 / keys, rounded up: a key's row without a division
 };
 
-// A float of another CTA of the cluster, at the place that `mine` has in this one.
-__device__ __forceinline__ float cluster_read(const float* mine, int rank) {
-  uint32_t addr;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-
 template <typename TIO, int NT, GatherKind KIND>
 __global__ void __launch_bounds__(32 * kGatherWarps, NT == 1 ? 5 : 1)
     kv4_gather_kernel(const Kv4Args a, const __grid_constant__ Plan P, int warps, const GatherRows gr) {
