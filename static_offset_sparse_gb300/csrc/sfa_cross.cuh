@@ -109,14 +109,14 @@ __device__ __forceinline__ RowOf row_of(const CrossArgs& a, const RowTiles& rt, 
 // most that began before it and one that ends behind it, so two places for parts a
 // CTA are enough: 2 c for a part that does not begin its unit, 2 c + 1 for one that
 // does.  What a unit costs besides its steps counts as kUnitCost steps, with the CTA
-// that begins it.  A CTA has kLeastShare steps at least, or a unit.
-constexpr int kUnitCost = 2, kLeastShare = 6;
+// that begins it.  A CTA has `least` steps at least, or a unit.
+constexpr int kUnitCost = 2;
 
 struct Shares {
   int64_t share, rest;
   int ctas;
-  __host__ __device__ __forceinline__ void set(int64_t total, int64_t units, int most) {
-    const int64_t n = units > total / kLeastShare ? units : total / kLeastShare;
+  __host__ __device__ __forceinline__ void set(int64_t total, int64_t units, int most, int least) {
+    const int64_t n = units > total / least ? units : total / least;
     ctas = n < 1 ? 1 : n < most ? (int)n : most;
     share = total / ctas;
     rest = total - share * ctas;
@@ -131,6 +131,17 @@ struct Shares {
     return (int)(w < big ? w / (share + 1) : rest + (w - big) / share);
   }
 };
+
+// Shares of `units` units of weight w among `most` CTAs.  Where all are alike and whole
+// units take at most `extra` steps longer than a division to the step, they stay whole:
+// parts are written, read and joined for less than that.
+inline Shares deal(int64_t units, int64_t w, int most, int least, bool alike, int extra) {
+  Shares s;
+  s.set(units * w, units, most, least);
+  const int64_t per = (units + most - 1) / most;
+  if (alike && units % per == 0 && per * w <= s.share + extra) s.set(units * w, units, (int)(units / per), least);
+  return s;
+}
 
 // The CTA's pieces of units, one after another.
 struct Walk {
@@ -172,7 +183,7 @@ struct WalkShared {
 
 // The first piece of CTA c of ctas, by all its THREADS threads; false if it has none.
 template <int THREADS, typename F>
-__device__ __forceinline__ bool find_walk(int B, const F& counts, int c, int ctas, WalkShared& sh, Walk& wk) {
+__device__ __forceinline__ bool find_walk(int B, const F& counts, int c, int ctas, int least, WalkShared& sh, Walk& wk) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = (B + THREADS - 1) / THREADS;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   if (tid == 0) {
@@ -202,7 +213,7 @@ __device__ __forceinline__ bool find_walk(int B, const F& counts, int c, int cta
     total += sh.sums[i];
   }
   Shares s;
-  s.set(total, sh.units, ctas);
+  s.set(total, sh.units, ctas, least);
   const int64_t from = s.begin(c), to = s.begin(c + 1);
   int64_t at = upto - mine;
   if (c < s.ctas && from < to && from >= at && from < upto)

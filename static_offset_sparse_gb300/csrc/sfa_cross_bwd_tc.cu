@@ -19,6 +19,8 @@
 // over the SMs, and planned ahead by one warp, as in the forward pass.
 #include <limits.h>
 
+#include <algorithm>
+
 #include "sfa_cross.cuh"
 
 namespace sfa {
@@ -34,6 +36,7 @@ constexpr int kBtStat = 1024;  // bytes of a row tile's numbers: 128 of -lse log
 constexpr int kBtStays = 0, kBtRing = kBtStays + 2 * 2 * kBtTile, kBtOut = kBtRing + kBtStages * 2 * kBtTile,
               kBtStatRing = kBtOut + kBtSoftmax * 1024, kBtStatStays = kBtStatRing + kBtStages * kBtStat, kBtSmem = kBtStatStays + 2 * kBtStat + 1024;
 constexpr int kBtPlans = 4;
+constexpr int kBtLeast = 6;  // steps a CTA has at least (with 3, 4 x 8 / 2 heads, 64 x 64 took 15.7 us, so 14.1)
 // tensor memory: S, dP, P, dS, sums of dq or dk, of dv
 constexpr int kBtDp = 128, kBtP = 256, kBtDs = 320, kBtSum = 384, kBtSum2 = 448;
 
@@ -112,7 +115,7 @@ __device__ __forceinline__ void cross_bwd_tc(const CrossArgs& a, const BtWork& w
   };
   Walk wk;
   tc05_fence_before();
-  const bool some = find_walk<kBtThreads>(a.B, counts, cta, ctas, sh.walk, wk);  // (with barriers of the CTA)
+  const bool some = find_walk<kBtThreads>(a.B, counts, cta, ctas, kBtLeast, sh.walk, wk);  // (with barriers of the CTA)
   tc05_fence_after();
   const uint32_t tm = sh.tmem;
   bool dead = false;  // a wait ran out: no more waits, no more work
@@ -655,7 +658,9 @@ struct BtPlan {
   size_t stat, q_places, kv_places, bytes;
 };
 
-static BtPlan bt_plan(int B, int Hkv, int G, int Tq, int Tk) {
+// Steps that whole units may take longer (8 x 8 / 2 heads, 512 x 512: 34.7 us in parts, so 30.9).
+constexpr int kBtExtra = 4;
+static BtPlan bt_plan(int B, int Hkv, int G, int Tq, int Tk, bool alike) {
   BtPlan p;
   p.rt = row_tiles(G, Tq);
   p.key_tiles = (Tk + 127) / 128;
@@ -667,13 +672,11 @@ static BtPlan bt_plan(int B, int Hkv, int G, int Tq, int Tk) {
   // launches, 436 in one; 200 x 8 / 2, 33 x 1500: 267 and 290).
   const int64_t qw = qu * (p.key_tiles + kUnitCost), kw = ku * (p.rt.tiles + kUnitCost);
   p.one = qw + kw <= 128 * kSMs;
-  Shares q, kv;
-  q.set(qw, qu, kSMs);
-  kv.set(kw, ku, kSMs);
+  Shares q = deal(qu, p.key_tiles + kUnitCost, kSMs, kBtLeast, alike, kBtExtra), kv = deal(ku, p.rt.tiles + kUnitCost, kSMs, kBtLeast, alike, kBtExtra);
   if (p.one && q.ctas + kv.ctas > kSMs) {
     const int n = (int)((kSMs * 15 * kw + (15 * kw + 14 * qw) / 2) / (15 * kw + 14 * qw));
-    kv.set(kw, ku, n < 1 ? 1 : n < kSMs ? n : kSMs - 1);
-    q.set(qw, qu, kSMs - kv.ctas);
+    kv = deal(ku, p.rt.tiles + kUnitCost, n < 1 ? 1 : n < kSMs ? n : kSMs - 1, kBtLeast, alike, kBtExtra);
+    q = deal(qu, p.key_tiles + kUnitCost, kSMs - kv.ctas, kBtLeast, alike, kBtExtra);
   }
   p.q_ctas = q.ctas;
   p.kv_ctas = kv.ctas;
@@ -684,11 +687,13 @@ static BtPlan bt_plan(int B, int Hkv, int G, int Tq, int Tk) {
   return p;
 }
 
-size_t cross_bwd_tc_bytes(int B, int Hkv, int G, int Tq, int Tk) { return bt_plan(B, Hkv, G, Tq, Tk).bytes; }
+size_t cross_bwd_tc_bytes(int B, int Hkv, int G, int Tq, int Tk) {
+  return std::max(bt_plan(B, Hkv, G, Tq, Tk, false).bytes, bt_plan(B, Hkv, G, Tq, Tk, true).bytes);
+}
 
 int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream) {
   static_assert(kBtSmem + sizeof(BtShared) + 1024 <= 228 * 1024, "shared memory of an SM");
-  const BtPlan p = bt_plan(a.B, a.Hkv, a.G, a.Tq, a.Tk);
+  const BtPlan p = bt_plan(a.B, a.Hkv, a.G, a.Tq, a.Tk, !a.q_len && !a.kv_len);
   char* const at = static_cast<char*>(ws);
   float* const stat = static_cast<float*>(ws);
   BtWork q = {p.rt, p.key_tiles, stat, reinterpret_cast<float*>(at + p.stat), p.q_ctas, reinterpret_cast<int4*>(at + p.stat + p.q_places + p.kv_places)};

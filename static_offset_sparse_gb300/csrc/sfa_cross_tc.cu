@@ -34,6 +34,9 @@ constexpr int kTcMoreRegs = 216, kTcFewerRegs = 72;
 constexpr int kTcTile = 128 * 128;  // bytes of 128 rows of 64 bf16
 constexpr int kKeys = 96, kKeyTile = kKeys * 128;  // keys of a step, bytes of that many rows
 constexpr int kTcCols = 512, kTcTileCols = 256, kTcO = 2 * kKeys;  // tensor memory columns of a tile: S or P of even steps, of odd ones, O
+// Steps a CTA has at least (8 / 2 heads, 17 queries over 1000: 12.4 us, with 6 14.9; 4 x 8 / 2,
+// 128 over 2000: 17.7 and 20.8).
+constexpr int kTcLeast = 3;
 constexpr float kSumLimit = 16384.0f;
 // Maxima beyond this are taken from x before the multiplication: a fused
 // 2^(x c - m c) would keep what rounding m c dropped, a factor of 2^(2^-5) and more.
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   Walk wk;
   tc05_fence_before();
-  const bool some = find_walk<kTcThreads>(a.B, counts, blockIdx.x, gridDim.x, sh.walk, wk);  // (with barriers of the CTA)
+  const bool some = find_walk<kTcThreads>(a.B, counts, blockIdx.x, gridDim.x, kTcLeast, sh.walk, wk);  // (with barriers of the CTA)
   tc05_fence_after();
   const uint32_t tm = sh.tmem;
   bool dead = false;  // a wait ran out: no more waits, no more work
@@ -657,25 +660,28 @@ RowTiles row_tiles(int G, int Tq) {
   return best;
 }
 
-// CTAs for the most that the lengths may come to, and the shares of a step behind a prefix.
-static Shares tc_shares(int B, int Hkv, const RowTiles& rt, int Tk) {
-  Shares s;
-  const int64_t units = (int64_t)B * Hkv * ((rt.tiles + 1) / 2);
-  s.set(units * ((Tk + kKeys - 1) / kKeys + kUnitCost), units, kSMs);
-  return s;
+// Shares, of the most that the lengths may come to.  (A unit in parts costs a launch and
+// their writing: 8 x 8 / 2 heads, 512 x 512 22.3 us in 152 shares of 6.7 steps, 14.0 in 128
+// whole units of 8; 2 x 16 / 2, 2048 x 300 27.1 and 18.2; with 12 steps for 8, 17 x 1000 took
+// 14.1 us for 12.3.  A prefix's are written and joined with the own rows' anyway.)
+static Shares tc_shares(int B, int Hkv, const RowTiles& rt, int Tk, bool alike, int extra) {
+  return deal((int64_t)B * Hkv * ((rt.tiles + 1) / 2), (Tk + kKeys - 1) / kKeys + kUnitCost, kSMs, kTcLeast, alike, extra);
+}
+static Shares call_shares(const CrossArgs& a, const RowTiles& rt) {
+  return tc_shares(a.B, a.Hkv, rt, a.Tk, !a.q_len && !a.kv_len, a.parts ? 0 : 8);
 }
 
 static size_t places_o(int ctas) { return (size_t)2 * ctas * 256 * kD * sizeof(float); }
 
 size_t cross_tc_bytes(int B, int Hkv, int G, int Tq, int Tk) {
-  const int ctas = tc_shares(B, Hkv, row_tiles(G, Tq), Tk).ctas;
+  const int ctas = tc_shares(B, Hkv, row_tiles(G, Tq), Tk, false, 0).ctas;  // (lengths may differ)
   return align256(places_o(ctas) + (size_t)2 * ctas * 256 * sizeof(float2) + ctas * sizeof(int4));
 }
 
 static TcWork tc_work(const CrossArgs& a, void* ws, int* ctas) {
   TcWork w;
   w.rt = row_tiles(a.G, a.Tq);
-  *ctas = tc_shares(a.B, a.Hkv, w.rt, a.Tk).ctas;
+  *ctas = call_shares(a, w.rt).ctas;
   w.place_o = static_cast<float*>(ws);
   w.place_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + places_o(*ctas));
   w.split = reinterpret_cast<int4*>(w.place_ml + (size_t)2 * *ctas * 256);
@@ -702,7 +708,7 @@ int launch_cross_fwd_tc(const CrossArgs& a, void* ws, void* stream) {
   const TcWork w = tc_work(a, ws, &ctas);
   const int rc = fwd_tc<1>(a, w, ctas, (cudaStream_t)stream);
   // where all lengths are alike and each CTA has whole units, there is nothing to join
-  const Shares s = tc_shares(a.B, a.Hkv, w.rt, a.Tk);
+  const Shares s = call_shares(a, w.rt);
   if (rc != SFA_OK || ctas == 1 || (!a.q_len && !a.kv_len && s.rest == 0 && s.share % ((a.Tk + kKeys - 1) / kKeys + kUnitCost) == 0)) return rc;
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
   const int64_t units = (int64_t)a.B * a.Hkv * ((w.rt.tiles + 1) / 2);
@@ -722,7 +728,7 @@ int launch_prefix_tc(const CrossArgs& a, void* ws, void* stream) {
 int launch_prefix_join(const CrossArgs& prefix, const CrossArgs& out, void* ws, const int32_t* pos, int T, void* stream) {
   int ctas;
   const TcWork w = tc_work(prefix, ws, &ctas);
-  const Shares s = tc_shares(1, prefix.Hkv, w.rt, prefix.Tk);
+  const Shares s = call_shares(prefix, w.rt);
   const int steps = (prefix.Tk + kKeys - 1) / kKeys;
   const bool few = steps / s.share + 2 + out.splits <= kFewParts;
   LaunchTimer tm(SFA_KERNEL_CROSS_JOIN, stream);
