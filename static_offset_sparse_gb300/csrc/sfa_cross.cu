@@ -288,7 +288,8 @@ struct PrefixPlan {
   Kind kind;        // of the prefix's part
   int shared, own;  // parts of the prefix and of the sequences' own rows
   int64_t rows;
-  bool two;  // on the tensor cores: the queries are wanted as two bf16 parts
+  bool two;   // on the tensor cores: the queries are wanted as two bf16 parts
+  bool both;  // few rows: the prefix's and the sequences' own rows in one launch
   size_t q32, q16, parts, bytes;
 };
 
@@ -298,6 +299,10 @@ static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
   p.rows = (int64_t)d->B * d->Hq;
   p.kind = forward_kind(G * d->B, d->dtype);
   p.two = d->P && p.kind == kTensor;
+  // (in fp32 one kernel for both has the prefix's rows a CTA, which over many own rows of
+  // fewer heads costs more than a launch: 32 x 8 / 8 heads behind 1000, own rows up to 2000,
+  // 66.5 us and 59.8 apart)
+  p.both = d->P && p.kind == kFewRows && (d->dtype == SFA_BF16 || G > 4 || (int64_t)d->B * d->Hkv * d->T <= 1 << 18);
   p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind, d->dtype);
   p.own = forward_splits((int64_t)d->B * d->Hkv, G, 1, d->T, kFewRows, d->dtype);
   p.q32 = align256((size_t)p.rows * kD * sizeof(float));
@@ -457,6 +462,8 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
       rc = launch_prefix_tc(a, parts + p.parts, stream);
     else if (p.kind == kFp32)
       rc = launch_cross_fwd_f32(a, stream);
+    else if (!p.both)
+      rc = launch_cross_stream(a, true, d->dtype, stream);
     if (rc != SFA_OK) return rc;
   }
   const CrossArgs prefix = a;
@@ -473,7 +480,7 @@ int sfa_prefix_decode(const sfa_prefix_desc* d, const void* q, const void* k_new
   a.kv_add = 1;
   a.splits = p.own;
   set_parts(&a, parts, p.shared + p.own, p.rows, p.shared);
-  rc = d->P && p.kind == kFewRows ? launch_cross_stream_two(prefix, a, d->dtype, stream) : launch_cross_stream(a, true, d->dtype, stream);
+  rc = p.both ? launch_cross_stream_two(prefix, a, d->dtype, stream) : launch_cross_stream(a, true, d->dtype, stream);
   if (rc != SFA_OK) return rc;
   a.o = o;
   a.lse = lse;

@@ -277,6 +277,7 @@ PREFIXES = [
     (33, 2000, 300, 8, 1, [(37 * i) % 300 for i in range(33)]),
     (130, 257, 33, 8, 2, [(5 * i) % 33 for i in range(130)]),
     (40, 5000, 20, 24, 2, [i % 20 for i in range(40)]),
+    (16, 50, 2100, 8, 8, [(523 * i) % 2100 for i in range(16)]),
 ]
 
 
