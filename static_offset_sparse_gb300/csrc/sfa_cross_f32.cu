@@ -375,10 +375,11 @@ __device__ __forceinline__ void cross_dq(const CrossArgs& a, float* sm, uint32_t
   for (int h = 0; h < 2; ++h) {
     const int r = r0 + 16 * warp + gid + 8 * h;
     if (r >= rows) continue;
+    const bool none = r / a.G >= nq;  // (its sums were of zeros times keys, NaN where a key is no number)
     const int64_t row = a.row(b, kvh, r);
     float* const out = a.parts ? a.part_a + (s * a.rows + row) * kD : static_cast<float*>(a.dq) + row * kD;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) store2(out + 8 * j + 2 * tig, 0.125f * dq[j][2 * h], 0.125f * dq[j][2 * h + 1]);
+    for (int j = 0; j < 8; ++j) store2(out + 8 * j + 2 * tig, none ? 0.0f : 0.125f * dq[j][2 * h], none ? 0.0f : 0.125f * dq[j][2 * h + 1]);
   }
 }
 

@@ -634,3 +634,29 @@ def test_cross_wait_times_out_and_context_recovers(sfa, sfa_lib, call, skip):
         wo, wl, bo, bl = ref.forward(q, k, v)
         ref.check("o", want[0], wo, bo)
         ref.check("lse", want[1], wl, bl)
+
+
+# ------------------------------------------------------------------ infinities and NaN in keys that count
+
+
+def _odd_key(seed, Tq, Tk, dtype, what):
+    """Inputs of two ragged sequences, queries above 0, and one key of KV head 1 of the first that is `what`."""
+    q, k, v, do = _inputs(seed, 2, Tq, Tk, 4, 2, dtype)
+    nq, nk = [Tq - (Tq + 2) // 3, Tq], [Tk, Tk - 3]
+    k[0, 1, Tk // 2] = what
+    return _spoil(q.abs() + 0.1, nq), _spoil(k, nk), _spoil(v, nk), do, nq, nk
+
+
+ODD_SIZES = [(5, 40), (70, 40), (70, 900), (300, 200)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", ODD_SIZES)
+@pytest.mark.parametrize("what", [NAN, INF, -INF])
+def test_dq_behind_the_queries_is_zero_whatever_a_key_holds(sfa, what, Tq, Tk, dtype):
+    q, k, v, do, nq, nk = _odd_key(40, Tq, Tk, dtype, what)
+    o, lse, _, _ = ref.forward(*(_spoil(x, n, 0.0) for x, n in ((q, nq), (k, nk), (v, nk))), nq, nk)
+    dq, dk, dv = sfa.cross_backward(*(x.cuda() for x in (q, k, v, o.to(dtype), lse.float(), do)), q_len=_i32(nq), kv_len=_i32(nk))
+    assert sfa.get_device_status() == 0
+    assert bool((dq[0, :, nq[0]:] == 0).all())
+    assert bool((dk[1, :, nk[1]:] == 0).all()) and bool((dv[1, :, nk[1]:] == 0).all())
