@@ -660,3 +660,18 @@ def test_dq_behind_the_queries_is_zero_whatever_a_key_holds(sfa, what, Tq, Tk, d
     assert sfa.get_device_status() == 0
     assert bool((dq[0, :, nq[0]:] == 0).all())
     assert bool((dk[1, :, nk[1]:] == 0).all()) and bool((dv[1, :, nk[1]:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", ODD_SIZES)
+@pytest.mark.parametrize("what", [NAN, -INF])
+def test_gradients_of_a_key_of_minus_infinity(sfa, what, Tq, Tk, dtype):
+    """Its probabilities are 0, and so are its dk and dv, whatever rows a tile holds besides those that count (dq:
+    0 times -inf, NaN).  A key of NaN makes all of its head's gradients NaN, and none of another's."""
+    q, k, v, do, nq, nk = _odd_key(41, Tq, Tk, dtype, what)
+    dq, dk, dv = _check_backward(sfa, q, k, v, do, nq, nk)
+    if what == -INF:
+        assert bool((dk[0, 1, Tk // 2] == 0).all()) and bool((dv[0, 1, Tk // 2] == 0).all())
+        assert bool(dk[0].isfinite().all()) and bool(dv[0].isfinite().all())
+    assert bool(dq[0, :2].isfinite().all()) and bool(dq[1].isfinite().all())
+    assert bool(dq[0, 2:, :nq[0]].isnan().all())
