@@ -10,8 +10,8 @@ static bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)
 
 // ---- small kernels
 
-// lse * log2(e) and delta = sum(o * dO) of each row, eight lanes a row; rows
-// that count for nothing get +inf, which makes their probabilities 0.
+// lse * log2(e) and delta = sum(o * dO) of each row, eight lanes a row (of rows that
+// count for nothing: zeros, which nothing reads).
 __global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, float2* stat) {
   pdl_launch_dependents();
   pdl_wait();
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) cross_stat_kernel(const CrossArgs a, floa
   }
 #pragma unroll
   for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (row < a.rows && d8 == 0) stat[row] = valid ? make_float2(a.lse[row] * kLog2e, sum) : make_float2(INFINITY, 0.0f);
+  if (row < a.rows && d8 == 0) stat[row] = valid ? make_float2(a.lse[row] * kLog2e, sum) : make_float2(0.0f, 0.0f);
 }
 
 // blockIdx.y-th: out = the sum of n-number parts, in order (n = 0: nothing).

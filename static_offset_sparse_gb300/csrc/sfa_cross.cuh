@@ -49,7 +49,7 @@ struct CrossArgs {
   float2* part_ml;  // [splits][rows] (m, l); l < 0: no key, and no sum in part_o
   // backward
   const void *out, *dO;
-  const float2* stat;  // [B * Hq * Tq]: lse * log2(e) (+inf for rows that count for nothing), delta
+  const float2* stat;  // [B * Hq * Tq]: lse * log2(e), delta, of rows that count
   void *dq, *dk, *dv;
   float *part_a, *part_b;  // fp32 kernels: [splits][dq's] or [splits][dk's], [splits][dv's]
   int* status;

@@ -330,10 +330,12 @@ __device__ __forceinline__ void cross_dq(const CrossArgs& a, float* sm, uint32_t
   g.load(grad(0), grad(1), tig);
   const bool q_plain = q.plain() || g.plain();
   float2 st[2];
+  bool counts[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = r0 + 16 * warp + gid + 8 * h;
-    st[h] = r < rows ? a.stat[a.row(b, kvh, r)] : make_float2(INFINITY, 0.0f);
+    counts[h] = r < rows && r / a.G < nq;
+    st[h] = counts[h] ? a.stat[a.row(b, kvh, r)] : make_float2(0.0f, 0.0f);
   }
   const float* const kp = static_cast<const float*>(a.k) + b * a.ks.b + kvh * a.ks.h;
   const float* const vp = static_cast<const float*>(a.v) + b * a.vs.b + kvh * a.vs.h;
@@ -361,7 +363,7 @@ __device__ __forceinline__ void cross_dq(const CrossArgs& a, float* sm, uint32_t
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool there = j0 + 8 * (n + i) + 2 * tig + (e & 1) < k1 && st[e >> 1].x != INFINITY;
+          const bool there = j0 + 8 * (n + i) + 2 * tig + (e & 1) < k1 && counts[e >> 1];
           p[i][e] = there ? exp2f(fmaf(p[i][e], kLogitScale, -st[e >> 1].x)) * (dp[i][e] - st[e >> 1].y) : 0.0f;
         }
         if (plain)
@@ -375,7 +377,7 @@ __device__ __forceinline__ void cross_dq(const CrossArgs& a, float* sm, uint32_t
   for (int h = 0; h < 2; ++h) {
     const int r = r0 + 16 * warp + gid + 8 * h;
     if (r >= rows) continue;
-    const bool none = r / a.G >= nq;  // (its sums were of zeros times keys, NaN where a key is no number)
+    const bool none = !counts[h];  // (its sums were of zeros times keys, NaN where a key is no number)
     const int64_t row = a.row(b, kvh, r);
     float* const out = a.parts ? a.part_a + (s * a.rows + row) * kD : static_cast<float*>(a.dq) + row * kD;
 #pragma unroll
@@ -423,7 +425,7 @@ __device__ __forceinline__ void cross_dkv(const CrossArgs& a, float* sm, uint32_
     plain |= load_tile(Ds, [&](int i) { return r0 + i < b1 ? static_cast<const float*>(a.dO) + a.row(b, kvh, r0 + i) * kD : nullptr; });
     if (threadIdx.x < kTileN) {
       const int r = r0 + threadIdx.x;
-      stat[threadIdx.x] = r < b1 ? a.stat[a.row(b, kvh, r)] : make_float2(INFINITY, 0.0f);
+      stat[threadIdx.x] = r < b1 ? a.stat[a.row(b, kvh, r)] : make_float2(0.0f, 0.0f);
     }
     plain = __syncthreads_or(plain || k_plain);
 #pragma unroll 1
@@ -440,9 +442,11 @@ __device__ __forceinline__ void cross_dkv(const CrossArgs& a, float* sm, uint32_
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 st = stat[8 * (n + i) + 2 * tig + (e & 1)];
-          p[i][e] = st.x != INFINITY ? exp2f(fmaf(p[i][e], kLogitScale, -st.x)) : 0.0f;
-          dp[i][e] = st.x != INFINITY ? p[i][e] * (dp[i][e] - st.y) : 0.0f;
+          const int r = 8 * (n + i) + 2 * tig + (e & 1);
+          const float2 st = stat[r];
+          const bool there = r0 + r < b1;
+          p[i][e] = there ? exp2f(fmaf(p[i][e], kLogitScale, -st.x)) : 0.0f;
+          dp[i][e] = there ? p[i][e] * (dp[i][e] - st.y) : 0.0f;
         }
         if (plain) {
           dims_plain(dv, p[i], Ds, n + i, gid, tig);

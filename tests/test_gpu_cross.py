@@ -675,3 +675,15 @@ def test_gradients_of_a_key_of_minus_infinity(sfa, what, Tq, Tk, dtype):
         assert bool(dk[0].isfinite().all()) and bool(dv[0].isfinite().all())
     assert bool(dq[0, :2].isfinite().all()) and bool(dq[1].isfinite().all())
     assert bool(dq[0, 2:, :nq[0]].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("Tq,Tk", ODD_SIZES)
+def test_gradients_of_rows_whose_lse_is_infinite(sfa, Tq, Tk, dtype):
+    """A logit of +inf: its row's softmax is not defined, and neither is what its probabilities enter.  (Other keys'
+    probabilities are 0, so their dv is too.)"""
+    q, k, v, do, nq, nk = _odd_key(42, Tq, Tk, dtype, INF)
+    dq, dk, dv = _check_backward(sfa, q, k, v, do, nq, nk)
+    assert bool(dq[0, 2:, :nq[0]].isnan().all()) and bool(dk[0, 1].isnan().all()) and bool(dv[0, 1, Tk // 2].isnan().all())
+    assert bool((dv[0, 1, :Tk // 2] == 0).all()) and bool((dv[0, 1, Tk // 2 + 1:] == 0).all())
+    assert bool(dq[0, :2].isfinite().all()) and bool(dk[0, 0].isfinite().all()) and bool(dq[1].isfinite().all())
