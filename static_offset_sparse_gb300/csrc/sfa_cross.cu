@@ -149,14 +149,18 @@ static bool clustered(int rows, int64_t units, int splits, int dtype) {
 // 32 x 8 / 2 heads over 1500 took 11.4 us, so 9.9), 128 where all parts are an SM's each
 // and there is a join anyway (4 heads over 1000: 5.8 us for 7.1).  fp32: a part's keys take
 // longer and its join as long, so fewer, and sqrt(Tk / 12) parts at most (8 / 2 heads over
-// 1000: 9.1 us for 13.5; over 10000 16.8 us, and 31 without the limit).
-static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind, int dtype) {
+// 1000: 9.1 us for 13.5; over 10000 16.8 us, and 31 without the limit).  A call whose parts
+// are joined by themselves takes kClusterSplits for up to two more, if they can be a cluster
+// then (8 / 2 heads over 1300 7.8 us in 10 parts, 7.3 so; over 2200 8.6 in 13, 8.9 in 8).  A
+// prefix's and the own rows' parts are joined together, never in a cluster (`joined`: 4
+// sequences behind 1300, 8 / 2 heads, 12.1 us in 10 parts, 12.7 in 8).
+static int forward_splits(int64_t units, int G, int Tq, int Tk, Kind kind, int dtype, bool joined) {
   if (kind == kFewRows) {
     const int64_t ctas = units * ((G * Tq + stream_rows(dtype) - 1) / stream_rows(dtype));
     if (dtype == SFA_BF16) return wave_splits(ctas, 6 * kSMs, Tk, Tk >= 512 && ctas * (Tk / 128) <= kSMs ? 128 : 256);
     int s = wave_splits(ctas, 4 * kSMs, Tk, 64);
     while (s > 1 && 12 * s * s > Tk) --s;
-    return (s == 9 || s == 10) && clustered(G * Tq, units, kClusterSplits, dtype) ? kClusterSplits : s;
+    return !joined && s > kClusterSplits && s <= kClusterSplits + 2 && clustered(G * Tq, units, kClusterSplits, dtype) ? kClusterSplits : s;
   }
   return wave_splits(units * ((G * Tq + kF32Tile - 1) / kF32Tile), 3 * kSMs, (Tk + kF32Keys - 1) / kF32Keys, 1);
 }
@@ -229,7 +233,7 @@ static ForwardPlan forward_plan(const sfa_cross_desc* d) {
   if (p.kind == kTensor) {
     p.bytes = cross_tc_bytes(d->B, d->Hkv, G, d->Tq, d->Tk);
   } else {
-    p.splits = forward_splits((int64_t)d->B * d->Hkv, G, d->Tq, d->Tk, p.kind, d->dtype);
+    p.splits = forward_splits((int64_t)d->B * d->Hkv, G, d->Tq, d->Tk, p.kind, d->dtype, false);
     p.cluster = p.kind == kFewRows && clustered(G * d->Tq, (int64_t)d->B * d->Hkv, p.splits, d->dtype);
     if (p.splits > 1 && !p.cluster) p.bytes = part_bytes(p.splits, (int64_t)d->B * d->Hq * d->Tq);
   }
@@ -303,8 +307,8 @@ static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
   // fewer heads costs more than a launch: 32 x 8 / 8 heads behind 1000, own rows up to 2000,
   // 66.5 us and 59.8 apart)
   p.both = d->P && p.kind == kFewRows && (d->dtype == SFA_BF16 || G > 4 || (int64_t)d->B * d->Hkv * d->T <= 1 << 18);
-  p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind, d->dtype);
-  p.own = forward_splits((int64_t)d->B * d->Hkv, G, 1, d->T, kFewRows, d->dtype);
+  p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind, d->dtype, true);
+  p.own = forward_splits((int64_t)d->B * d->Hkv, G, 1, d->T, kFewRows, d->dtype, true);
   p.q32 = align256((size_t)p.rows * kD * sizeof(float));
   p.q16 = p.two ? align256((size_t)p.rows * kD * 2 * sizeof(bf16)) : 0;
   p.parts = part_bytes(p.shared + p.own, p.rows);

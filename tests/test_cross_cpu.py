@@ -101,6 +101,20 @@ def test_prefix_pointer_and_workspace_refusals(sfa_lib):
             assert sfa_lib.sfa_prefix_decode(d, *args, 1 << 40, None) == 1, i
 
 
+def _aligned(n):
+    return (n + 255) // 256 * 256
+
+
+@pytest.mark.parametrize("P,T,parts", [(1000, 64, 9 + 1), (1300, 1000, 10 + 9), (300, 1200, 4 + 10)])
+def test_parts_behind_a_prefix_are_not_cut_to_what_a_cluster_takes(sfa_lib, P, T, parts):
+    """A prefix's and the own rows' parts, sqrt(rows / 12) each and one for 64 rows at most, are joined through the
+    workspace: 32 rows of queries in fp32, then (64 sums, maximum and sum) of each part and row."""
+    n = C.c_size_t(0)
+    d = _prefix(B=4, P=P, T=T, dtype=0, prefix_k_stride=64 * P, prefix_v_stride=64 * P)
+    assert sfa_lib.sfa_prefix_workspace_size(d, C.byref(n)) == 0
+    assert n.value == _aligned(32 * 256) + _aligned(parts * 32 * 256) + _aligned(parts * 32 * 8)
+
+
 def test_python_refusals():
     import static_offset_sparse_gb300 as sfa
 
