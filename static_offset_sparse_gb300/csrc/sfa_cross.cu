@@ -303,10 +303,14 @@ static PrefixPlan prefix_plan(const sfa_prefix_desc* d) {
   p.rows = (int64_t)d->B * d->Hq;
   p.kind = forward_kind(G * d->B, d->dtype);
   p.two = d->P && p.kind == kTensor;
-  // (in fp32 one kernel for both has the prefix's rows a CTA, which over many own rows of
-  // fewer heads costs more than a launch: 32 x 8 / 8 heads behind 1000, own rows up to 2000,
-  // 66.5 us and 59.8 apart)
-  p.both = d->P && p.kind == kFewRows && (d->dtype == SFA_BF16 || G > 4 || (int64_t)d->B * d->Hkv * d->T <= 1 << 18);
+  // In fp32 one kernel for both has the prefix's rows a CTA, 8 of more than 4, which costs more
+  // than a launch over many own rows of fewer heads.  In one launch and apart: 8 x 16 / 4 heads
+  // behind 1000, own rows of 100 12.4 and 18.7 us, of 1000 17.6 and 20.1, of 4000 30.3 and 24.3;
+  // 8 x 8 / 2, 4000 20.3 and 23.1, 16000 52.4 and 41.0; 32 x 8 / 8, 100 18.1 and 19.5, 1000 53.7
+  // and 42.9; up to 4 rows (4 x 8 / 8), 4000 20.1 and 21.8, 16000 59.7 and 60.0; more than 4 heads
+  // (4 x 64 / 8), 16000 85.7 and 88.8.
+  p.both = d->P && p.kind == kFewRows &&
+           (d->dtype == SFA_BF16 || G > 4 || G * d->B <= 4 || (int64_t)d->B * d->Hkv * d->T <= 1 << 16);
   p.shared = !d->P ? 0 : p.two ? 1 : forward_splits(d->Hkv, G, d->B, d->P, p.kind, d->dtype, true);
   p.own = forward_splits((int64_t)d->B * d->Hkv, G, 1, d->T, kFewRows, d->dtype, true);
   p.q32 = align256((size_t)p.rows * kD * sizeof(float));

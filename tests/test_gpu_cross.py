@@ -687,3 +687,16 @@ def test_gradients_of_rows_whose_lse_is_infinite(sfa, Tq, Tk, dtype):
     assert bool(dq[0, 2:, :nq[0]].isnan().all()) and bool(dk[0, 1].isnan().all()) and bool(dv[0, 1, Tk // 2].isnan().all())
     assert bool((dv[0, 1, :Tk // 2] == 0).all()) and bool((dv[0, 1, Tk // 2 + 1:] == 0).all())
     assert bool(dq[0, :2].isfinite().all()) and bool(dk[0, 0].isfinite().all()) and bool(dq[1].isfinite().all())
+
+
+# fp32: own rows up to 2^16 and, with more of them, up to four rows a KV head and call share a launch with the prefix
+@pytest.mark.parametrize("B,P,T,Hq,Hkv", [(8, 300, 2000, 16, 4), (8, 300, 2100, 16, 4), (4, 300, 5000, 8, 8), (5, 300, 5000, 8, 8)])
+def test_prefix_in_one_launch_and_apart(sfa, B, P, T, Hq, Hkv):
+    qkv, pk, pv, kc, vc = _prefix_inputs(43, B, P, T, Hq, Hkv, torch.float32)
+    pos = [(T - 1) * (i + 1) // B for i in range(B)]
+    dev = [x.cuda() for x in (qkv, pk, pv, kc, vc)]
+    o, lse = _step(sfa, *dev, pos, Hq)
+    assert sfa.get_device_status() == 0
+    wo, wl, bo, bl = ref.prefix(qkv[:, :Hq], pk, pv, dev[3].cpu(), dev[4].cpu(), pos, sfa.rope_table(P + T).cpu())
+    ref.check("o", o, wo, bo)
+    ref.check("lse", lse, wl, bl)
