@@ -15,7 +15,7 @@ __all__ = [
     "LIB_PATH", "MAX_RUNGS", "SCHED_COPRIME", "SCHED_FIXED", "SCHED_LINEAR", "SFA_BF16",
     "SFA_F32", "SfaError", "alpha_schedule", "backward", "backward_int", "band_plan",
     "kv4_append", "kv4_attend", "kv4_cache", "kv4_plan", "kv4_read", "kv4_workspace_size",
-    "cross_backward", "cross_forward", "cross_workspace_size", "prefix_decode",
+    "cross_backward", "cross_forward", "cross_workspace_size", "prefix_decode", "prefix_workspace_size",
     "decode_int", "forward", "forward_int", "get_device_status", "int_distances", "make_desc", "offsets_christoffel",
     "offset_histogram", "offsets_fib", "offsets_pow2", "offsets_powerlaw", "reach",
     "residue_classes", "rope_keys", "rope_table", "rung_table", "status_string",
@@ -23,7 +23,7 @@ __all__ = [
 ]
 
 _KV4 = ("kv4_append", "kv4_attend", "kv4_cache", "kv4_plan", "kv4_read", "kv4_workspace_size")
-_CROSS = ("cross_backward", "cross_forward", "cross_workspace_size", "prefix_decode")
+_CROSS = ("cross_backward", "cross_forward", "cross_workspace_size", "prefix_decode", "prefix_workspace_size")
 
 
 def __getattr__(name):

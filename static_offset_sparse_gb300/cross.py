@@ -95,7 +95,7 @@ def _output(t, name, at, shape, dtype):
 
 
 def cross_workspace_size(q, k, v, *, backward: bool = False) -> int:
-    """Scratch bytes of cross_forward or cross_backward for these shapes."""
+    """Scratch bytes of cross_forward or cross_backward for these shapes (of any lengths)."""
     d = _describe(q, k, v, None, None)[3]
     n = C.c_size_t(0)
     check(_entry("sfa_cross_workspace_size")(d, int(backward), C.byref(n)), "sfa_cross_workspace_size")
@@ -107,7 +107,8 @@ def cross_forward(q, k, v, *, q_len=None, kv_len=None, o=None, lse=None, ws=None
     (sfa_cross_forward; bf16 or fp32, strided views of other layouts too).  q_len
     and kv_len: int32 [B], how many rows of each sequence count (None: all); a
     query behind its length or without a key gives zeros and lse = -inf.  A single
-    token a sequence is Tq = 1.  Returns o [B, Hq, Tq, 64] and lse fp32 [B, Hq, Tq]."""
+    token a sequence is Tq = 1.  ws: scratch of cross_workspace_size bytes or more (one
+    that is smaller is not used).  Returns o [B, Hq, Tq, 64] and lse fp32 [B, Hq, Tq]."""
     fast = _native()
     if fast is not None and o is None and lse is None and ws is None:
         r = fast.forward(q, k, v, q_len, kv_len)
@@ -126,7 +127,8 @@ def cross_forward(q, k, v, *, q_len=None, kv_len=None, o=None, lse=None, ws=None
 def cross_backward(q, k, v, o, lse, do, *, q_len=None, kv_len=None, dq=None, dk=None, dv=None, ws=None):
     """Gradients of sum(o * do) for cross_forward's q, k, v, from its o and lse
     (sfa_cross_backward): dq [B, Hq, Tq, 64], dk and dv [B, Hkv, Tk, 64], contiguous,
-    zeros behind the lengths.  The same inputs give the same bits."""
+    zeros behind the lengths.  The same inputs give the same bits.  ws: scratch of
+    cross_workspace_size(q, k, v, backward=True) bytes or more."""
     fast = _native()
     if fast is not None and dq is None and dk is None and dv is None and ws is None:
         r = fast.backward(q, k, v, o, lse, do, q_len, kv_len)
@@ -155,6 +157,22 @@ def _heads(t, name, index, dtype, Hkv):
     return P, s[0]
 
 
+def prefix_workspace_size(q, prefix_k, k_cache) -> int:
+    """Scratch bytes of prefix_decode for these shapes."""
+    if not k_cache.is_cuda or k_cache.dim() != 4 or not k_cache.is_contiguous() or k_cache.shape[3] != 64:
+        _refuse("k_cache", k_cache, k_cache.dtype, (None, None, None, 64))
+    B, Hkv, T, _ = k_cache.shape
+    dtype, at = k_cache.dtype, k_cache.get_device()
+    n, Hq, qs = _rows(q, "q", 0, at)
+    if n != B or q.dtype is not dtype:
+        raise ValueError(f"q must have the caches' {B} rows and type {dtype}, got {n} and {q.dtype}")
+    P, ps = _heads(prefix_k, "prefix_k", at, dtype, Hkv)
+    n = C.c_size_t(0)
+    d = _prefix_desc(B, P, T, Hq, Hkv, 64, _code(dtype), qs, 64 * Hkv, 64 * Hkv, ps, ps, 0, 0)
+    check(_entry("sfa_prefix_workspace_size")(d, C.byref(n)), "sfa_prefix_workspace_size")
+    return n.value
+
+
 def prefix_decode(q, k_new, v_new, prefix_k, prefix_v, k_cache, v_cache, pos, *, rope_theta: float = 1e4, rope=None,
                   o=None, lse=None, ws=None):
     """One decode step of a batch whose sequences all begin with the same P rows
@@ -165,8 +183,8 @@ def prefix_decode(q, k_new, v_new, prefix_k, prefix_v, k_cache, v_cache, pos, *,
     position P + pos.  The new key is rotated there and written with the value; then
     the query attends the prefix, read once for the whole batch, and rows 0..pos of
     its cache.  rope: a table of rope_table for P + T positions or more, else that of
-    rope_theta (0: no rotation; prefix and caches then hold unrotated keys).  Returns o
-    [B, Hq, 64] and lse fp32 [B, Hq]."""
+    rope_theta (0: no rotation; prefix and caches then hold unrotated keys).  ws: scratch
+    of prefix_workspace_size bytes or more.  Returns o [B, Hq, 64] and lse fp32 [B, Hq]."""
     fast = _native()
     if fast is not None and o is None and lse is None and ws is None:
         made = rope

@@ -163,3 +163,11 @@ def test_gradients_against_differences():
             flat[i] = old
             # third-order remainder h^2 and the differences' own rounding, 1e-16 |loss| / h
             assert abs((up - down) / (2 * h) - float(g.view(-1)[i])) < 1e-7
+
+
+def test_prefix_workspace_size_refuses_cpu_tensors():
+    import static_offset_sparse_gb300 as sfa
+
+    cache = torch.zeros(1, 2, 5, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        sfa.prefix_workspace_size(torch.zeros(1, 4, 64), torch.zeros(2, 7, 64), cache)

@@ -700,3 +700,47 @@ def test_prefix_in_one_launch_and_apart(sfa, B, P, T, Hq, Hkv):
     wo, wl, bo, bl = ref.prefix(qkv[:, :Hq], pk, pv, dev[3].cpu(), dev[4].cpu(), pos, sfa.rope_table(P + T).cpu())
     ref.check("o", o, wo, bo)
     ref.check("lse", lse, wl, bl)
+
+
+def _guarded_ws(n):
+    """n bytes with 256 guarded ones before and behind."""
+    buf = torch.full((n + 512,), 255, dtype=torch.uint8, device="cuda")
+    return buf, buf[256:256 + n]
+
+
+def _guards_hold(buf):
+    return bool((buf[:256] == 255).all()) and bool((buf[-256:] == 255).all())
+
+
+# few rows in parts, few rows in a cluster, tiles in parts; the tensor cores' one and two launches
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv,ragged", [(1, 1, 20000, 8, 2, False), (8, 1, 1500, 8, 2, True), (2, 37, 777, 4, 4, True),
+                                                   (1, 333, 1000, 8, 2, False), (1, 130, 9000, 8, 2, True), (17, 1000, 2040, 4, 2, True)])
+def test_workspaces_of_exact_size(sfa, B, Tq, Tk, Hq, Hkv, ragged, dtype):
+    q, k, v, do = (x.cuda() for x in _inputs(61, B, Tq, Tk, Hq, Hkv, dtype))
+    lens = dict(q_len=_i32([Tq - i % Tq for i in range(B)]), kv_len=_i32([Tk - 7 * i for i in range(B)])) if ragged else {}
+    want = sfa.cross_forward(q, k, v, **lens)
+    buf, ws = _guarded_ws(sfa.cross_workspace_size(q, k, v))
+    got = sfa.cross_forward(q, k, v, ws=ws, **lens)
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and _guards_hold(buf)
+    grads = sfa.cross_backward(q, k, v, *want, do, **lens)
+    buf, ws = _guarded_ws(sfa.cross_workspace_size(q, k, v, backward=True))
+    got = sfa.cross_backward(q, k, v, *want, do, ws=ws, **lens)
+    assert all(torch.equal(a, b) for a, b in zip(grads, got)) and _guards_hold(buf)
+    assert bool((ws != 255).any())
+
+
+# no prefix, prefix and own rows in one launch, apart (tiles; streams), the tensor cores
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,P,T,Hq,Hkv", [(5, 0, 700, 8, 2), (3, 1000, 300, 8, 2), (40, 1000, 90, 8, 2), (32, 100, 1025, 8, 8), (130, 9000, 40, 8, 2)])
+def test_prefix_workspaces_of_exact_size(sfa, B, P, T, Hq, Hkv, dtype):
+    qkv, pk, pv, kc, vc = (x.cuda() for x in _prefix_inputs(62, B, P, T, Hq, Hkv, dtype))
+    pos = [(37 * i) % T for i in range(B)]
+    want = _step(sfa, qkv, pk, pv, kc, vc, pos, Hq)
+    buf, ws = _guarded_ws(sfa.prefix_workspace_size(qkv[:, :Hq], pk, kc))
+    got = _step(sfa, qkv, pk, pv, kc, vc, pos, Hq, ws=ws)
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and _guards_hold(buf) and bool((ws != 255).any())
+    with pytest.raises(ValueError):
+        sfa.prefix_workspace_size(qkv[:, :Hq], pk[:, :, :32], kc)
+    with pytest.raises(ValueError):
+        sfa.prefix_workspace_size(qkv[:, :Hq].cpu(), pk, kc)
