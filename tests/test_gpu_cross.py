@@ -744,3 +744,50 @@ def test_prefix_workspaces_of_exact_size(sfa, B, P, T, Hq, Hkv, dtype):
         sfa.prefix_workspace_size(qkv[:, :Hq], pk[:, :, :32], kc)
     with pytest.raises(ValueError):
         sfa.prefix_workspace_size(qkv[:, :Hq].cpu(), pk, kc)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B", [3, 40])
+def test_captured_prefix_steps_against_the_definition(sfa, B, dtype):
+    """A step captured once and replayed while pos counts up, each replay against the 64-bit definition over the
+    caches as it left them; zeros, the plain mean of the values and o without the own rows are far outside the bound."""
+    P, T, Hq, Hkv = 90, 6, 8, 2
+    gen = torch.Generator().manual_seed(60)
+    normal = lambda *s: torch.randn(s, generator=gen).to(dtype)  # noqa: E731
+    pk, pv = normal(Hkv, P, 64), normal(Hkv, P, 64)
+    kc, vc = (torch.full((B, Hkv, T, 64), NAN, dtype=dtype, device="cuda") for _ in range(2))
+    rope, pos, qkv = sfa.rope_table(P + T), _i32([0] * B), normal(B, Hq + 2 * Hkv, 64).cuda()
+    dk, dv = pk.cuda(), pv.cuda()
+
+    def step():
+        return sfa.prefix_decode(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], dk, dv, kc, vc, pos, rope=rope)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step()
+    tab = rope.cpu()
+    for t in range(T):
+        new = normal(B, Hq + 2 * Hkv, 64)
+        qkv.copy_(new)
+        pos.fill_(t)
+        o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        keys, values = kc.cpu(), vc.cpu()
+        want = ref.rotated(new[:, Hq:Hq + Hkv], tab[P + t])
+        pair = new[:, Hq:Hq + Hkv].double().abs() + new[:, Hq:Hq + Hkv].double().roll(32, -1).abs()
+        r = ref.half_step(dtype)
+        ref.check("new key", keys[:, :, t], want, r * want.abs() + 3 * (1 + r) * ref.U * pair + 1e-37)
+        assert torch.equal(values[:, :, t], new[:, Hq + Hkv:]) and bool(keys[:, :, t + 1:].isnan().all())
+        wo, wl, bo, bl = ref.prefix(new[:, :Hq], pk, pv, keys, values, [t] * B, tab)
+        ref.check("o", o, wo, bo)
+        ref.check("lse", lse, wl, bl)
+        every = torch.cat([pv.expand(B, -1, -1, -1), values[:, :, :t + 1]], 2).double().mean(2).repeat_interleave(Hq // Hkv, 1)
+        alone, alone_lse, _, _ = ref.forward(ref.rotated(new[:, :Hq], tab[P + t]).transpose(0, 1)[None], pk[None], pv[None])
+        for wrong in (torch.zeros_like(wo), every, alone[0].transpose(0, 1)):
+            with pytest.raises(AssertionError):
+                ref.check("wrong o", wrong, wo, bo)
+        with pytest.raises(AssertionError):
+            ref.check("wrong lse", alone_lse[0].transpose(0, 1), wl, bl)
+    assert sfa.get_device_status() == 0
