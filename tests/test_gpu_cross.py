@@ -791,3 +791,45 @@ def test_captured_prefix_steps_against_the_definition(sfa, B, dtype):
         with pytest.raises(AssertionError):
             ref.check("wrong lse", alone_lse[0].transpose(0, 1), wl, bl)
     assert sfa.get_device_status() == 0
+
+
+# ------------------------------------------------------------------ plans that the sizes above do not reach
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv", [(50, 33, 300, 16, 4), (76, 33, 200, 8, 4), (51, 33, 200, 24, 6), (77, 20, 100, 8, 2)])
+def test_several_whole_units_an_sm(sfa, B, Tq, Tk, Hq, Hkv, dtype):
+    """Batches of equal lengths and more units than SMs: each CTA has whole ones, so that nothing is joined."""
+    q, k, v, do = _inputs(50, B, Tq, Tk, Hq, Hkv, dtype)
+    _check_forward(sfa, q, k, v, None, None)
+    _check_backward(sfa, q, k, v, do, None, None)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+def test_more_sequences_than_threads(sfa, dtype):
+    """A CTA's threads share out the sequences: several each, most of them short or empty."""
+    B, Tq, Tk, Hq, Hkv = 1601, 9, 40, 4, 1
+    q, k, v, do = _inputs(51, B, Tq, Tk, Hq, Hkv, dtype)
+    gen = torch.Generator().manual_seed(52)
+    nq, nk = (torch.randint(-n, n + 1, (B,), generator=gen).clamp(min=0).tolist() for n in (Tq, Tk))
+    q, k, v = _spoil(q, nq), _spoil(k, nk), _spoil(v, nk)
+    _check_forward(sfa, q, k, v, nq, nk)
+    _check_backward(sfa, q, k, v, do, nq, nk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hkv", [(3, 1, 1500, 8, 2), (3, 200, 1500, 8, 2), (1, 150, 9000, 6, 2)])
+def test_strided_views_with_lengths(sfa, B, Tq, Tk, Hq, Hkv, dtype):
+    """[B, T, H, 64] projections as they are, rows behind the lengths NaN, calls of many parts: as dense ones."""
+    q, k, v, do = _inputs(53, B, Tq, Tk, Hq, Hkv, dtype)
+    nq, nk = [Tq, Tq - Tq // 3, Tq // 2][:B], [Tk - 1, Tk // 3, Tk][:B]
+    q, k, v = _spoil(q, nq), _spoil(k, nk), _spoil(v, nk)
+    lens = dict(q_len=_i32(nq), kv_len=_i32(nk))
+    kv = torch.stack([k, v]).permute(1, 3, 0, 2, 4).contiguous().cuda()  # [B, T, (k, v), H, 64]
+    views = q.transpose(1, 2).contiguous().cuda().transpose(1, 2), kv[:, :, 0].transpose(1, 2), kv[:, :, 1].transpose(1, 2)
+    assert not views[1].is_contiguous()
+    o, lse = _check_forward(sfa, q, k, v, nq, nk)
+    assert all(torch.equal(a, b) for a, b in zip(sfa.cross_forward(*views, **lens), (o, lse)))
+    dense = sfa.cross_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, do.cuda(), **lens)
+    assert all(torch.equal(a, b) for a, b in zip(sfa.cross_backward(*views, o, lse, do.cuda(), **lens), dense))
+    _check_backward(sfa, *(x.cpu() for x in views), do, nq, nk)
