@@ -722,8 +722,8 @@ int launch_cross_bwd_tc(const CrossArgs& a, void* ws, void* stream) {
   if (rc == SFA_OK) rc = make_view_map(&vm, a.v, a.Tk, a.Hkv, a.B, a.vs, 128, 1);
   if (rc != SFA_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaSuccess;
-  if (e == cudaSuccess) {
+  cudaError_t e;
+  {
     LaunchTimer tm(SFA_KERNEL_CROSS_STAT, stream);
     e = launch_pdl(cross_stat_tc_kernel, dim3((unsigned)((int64_t)a.B * a.Hkv * p.rt.tiles)), dim3(256), 0, st, a, p.rt, stat);
   }
