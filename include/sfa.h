@@ -386,7 +386,10 @@ int sfa_kv4_attend(const sfa_kv4_desc* d, const void* q, const void* cache,
  * any gradient; gradients behind the lengths are zeros.  What stands in q, k, v,
  * o, lse and dO behind the lengths may be anything, NaN too.  A length outside
  * [0, Tq] or [0, Tk] counts as 0 and is recorded as SFA_ERR_DEVICE_BOUNDS.
- * Outputs overlap neither inputs nor each other.
+ * Outputs overlap neither inputs nor each other.  A logit that is +inf or NaN makes
+ * its row's o and lse NaN.  For bf16 probabilities, and dS, are rounded to bf16 once
+ * for their products; fp32 products of more than 32 rows a KV head, and all of
+ * gradients, are three tf32 products each (2^-22 of a term), sums fp32.
  * Hq / Hkv <= 32 (any whole number); Tq, Tk <= 2^24; B Hq Tq and B Hkv Tk below
  * 2^30.  Calls only enqueue work, keep no state, and may be captured. */
 typedef struct {

@@ -833,3 +833,13 @@ def test_strided_views_with_lengths(sfa, B, Tq, Tk, Hq, Hkv, dtype):
     dense = sfa.cross_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, do.cuda(), **lens)
     assert all(torch.equal(a, b) for a, b in zip(sfa.cross_backward(*views, o, lse, do.cuda(), **lens), dense))
     _check_backward(sfa, *(x.cpu() for x in views), do, nq, nk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk", [(2, 1, 333), (1, 1, 20000), (2, 5, 333), (2, 70, 333), (1, 140, 9000)])
+def test_a_logit_of_infinity_makes_its_rows_nan(sfa, B, Tq, Tk, dtype):
+    q, k, v, _ = _inputs(44, B, Tq, Tk, 4, 2, dtype)
+    k[0, 1, Tk // 3] = INF
+    o, lse = _forward(sfa, q.abs() + 0.1, k, v, None, None)
+    assert bool(o[0, 2:].isnan().all()) and bool(lse[0, 2:].isnan().all())
+    assert bool(o[0, :2].isfinite().all()) and bool(lse[0, :2].isfinite().all()) and bool(o[1:].isfinite().all())
