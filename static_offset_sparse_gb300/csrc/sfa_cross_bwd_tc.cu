@@ -227,9 +227,8 @@ __device__ __forceinline__ void cross_bwd_tc(const CrossArgs& a, const BtWork& w
         }
         // Rows that count for nothing are zeros, whose products with a key or value that is not finite
         // are NaN: their P and dS are made zeros too.  If one of the 32 counts for nothing, the last
-        // does, so its dS says whether to look (asking for rows behind a length first, and making
-        // zeros in each tile that has some, took 248 us in place of 240 for 32 x 8 / 2 heads,
-        // 1024 x 2048 ragged rows).
+        // does, so its dS says whether to look (32 x 8 / 2 heads, 1024 x 2048 ragged rows: 242 us, and
+        // 248 with zeros made in each tile that has such rows, whatever their products).
         if (DKV && __any_sync(0xffffffffu, (__float_as_uint(d[15]) & 0x7fffffffu) > 0x7f80ffffu)) {
           const RowOf ro = row_of(a, w.rt, t0 + j, 32 * quarter + lane);
           const unsigned in = __ballot_sync(0xffffffffu, ro.mine && ro.t < sh.plan[pieces % kBtPlans].nq);
@@ -563,7 +562,7 @@ __device__ __forceinline__ void cross_bwd_tc(const CrossArgs& a, const BtWork& w
 
 // dq's CTAs, dk's and dv's, or both in one launch, kv's first (BtPlan says which).  Each
 // in a kernel of its own, because with both in one the registers of a thread do not reach
-// (32 x 8 / 2 heads, 1024 x 2048 ragged rows through it in two launches: 251 us, so 239).
+// (32 x 8 / 2 heads, 1024 x 2048 ragged rows through it in two launches: 251 us, so 240).
 enum BtPart { kBtDq, kBtDkv, kBtBoth };
 template <BtPart PART>
 __global__ void __launch_bounds__(kBtThreads, 1)
