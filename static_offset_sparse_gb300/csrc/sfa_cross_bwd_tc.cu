@@ -175,12 +175,14 @@ __device__ __forceinline__ void cross_bwd_tc(const CrossArgs& a, const BtWork& w
     int n = 0;
     for (;;) {
       int steps, nk, t0;
+      unsigned counted;  // dk, dv: which of this warp's keys count
       {
         BtPiece p;
         if (!take(p)) break;
         steps = p.steps;
         nk = p.nk;
         t0 = p.t0;
+        counted = DKV ? __ballot_sync(0xffffffffu, r < p.nk - 128 * p.tile) : 0;
       }
       float2 own = make_float2(-INFINITY, 0.0f);
       if (!DKV) {
@@ -227,9 +229,9 @@ __device__ __forceinline__ void cross_bwd_tc(const CrossArgs& a, const BtWork& w
         }
         // Rows that count for nothing are zeros, whose products with a key or value that is not finite
         // are NaN: their P and dS are made zeros too.  If one of the 32 counts for nothing, the last
-        // does, so its dS says whether to look (32 x 8 / 2 heads, 1024 x 2048 ragged rows: 242 us, and
-        // 248 with zeros made in each tile that has such rows, whatever their products).
-        if (DKV && __any_sync(0xffffffffu, (__float_as_uint(d[15]) & 0x7fffffffu) > 0x7f80ffffu)) {
+        // does, so its dS says whether to look, of keys that count (32 x 8 / 2 heads, 1024 x 2048 ragged
+        // rows: 238 us, and 248 with zeros made in each tile that has such rows, whatever their products).
+        if (DKV && (__ballot_sync(0xffffffffu, (__float_as_uint(d[15]) & 0x7fffffffu) > 0x7f80ffffu) & counted) != 0) {
           const RowOf ro = row_of(a, w.rt, t0 + j, 32 * quarter + lane);
           const unsigned in = __ballot_sync(0xffffffffu, ro.mine && ro.t < sh.plan[pieces % kBtPlans].nq);
 #pragma unroll
@@ -562,7 +564,7 @@ __device__ __forceinline__ void cross_bwd_tc(const CrossArgs& a, const BtWork& w
 
 // dq's CTAs, dk's and dv's, or both in one launch, kv's first (BtPlan says which).  Each
 // in a kernel of its own, because with both in one the registers of a thread do not reach
-// (32 x 8 / 2 heads, 1024 x 2048 ragged rows through it in two launches: 251 us, so 240).
+// (32 x 8 / 2 heads, 1024 x 2048 ragged rows through it in two launches: 251 us, so 238).
 enum BtPart { kBtDq, kBtDkv, kBtBoth };
 template <BtPart PART>
 __global__ void __launch_bounds__(kBtThreads, 1)
